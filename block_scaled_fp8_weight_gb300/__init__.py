@@ -24,6 +24,8 @@ __all__ = [
     "set_option", "get_option", "OPT_PDL", "OPT_WAIT_TIMEOUT_NS", "OPT_DEBUG_SKIP_LOADS",
     "OPT_GEMM_PATH", "gemm_kernel", "KERNELS", "sm_clock_sample", "prefetch_l2",
     "MAX_M", "STATUS",
+    "KVCache", "qkv_append", "kv_read", "tree_attention", "tree_attention_workspace_bytes", "verify_tree",
+    "kv_commit", "MAX_NODES",
 ]
 
 MAX_M = 16384
@@ -31,7 +33,7 @@ OPT_PDL, OPT_WAIT_TIMEOUT_NS, OPT_DEBUG_SKIP_LOADS, OPT_GEMM_PATH = 1, 2, 3, 4
 # bsf8_gemm's kernels (BSF8_KERNEL_*), the values gemm_kernel() returns and OPT_GEMM_PATH forces
 KERNELS = {2: "stream", 4: "decode_ahead", 5: "tensor_core", 6: "wide", 7: "decode_ahead_tc"}
 STATUS = {0: "OK", 1: "ERR_SHAPE", 2: "ERR_ALIGN", 3: "ERR_STRIDE", 4: "ERR_WORKSPACE",
-          5: "ERR_NULL", 6: "ERR_CUDA", 7: "ERR_TIMEOUT", 8: "ERR_DEVICE", 9: "ERR_VALUE"}
+          5: "ERR_NULL", 6: "ERR_CUDA", 7: "ERR_TIMEOUT", 8: "ERR_DEVICE", 9: "ERR_VALUE", 10: "ERR_INDEX"}
 
 _lock = threading.Lock()
 _lib = None
@@ -86,6 +88,13 @@ def load(build_if_missing: bool = True):
             "bsf8_splitk_reduce_f32": (I, [P, P, I, I64, P]),
             "bsf8_pad_k": (I, [P, P, P, P, I, I, I, I, I, P]),
             "bsf8_pad_x": (I, [P, I64, P, I, I, I, I, P]),
+            "bsf8_qkv_append": (I, [P, P, P, I64, I64, I64, P, P, P, I, I, P, P, P, P, I, I, I, P, P,
+                                    ctypes.c_float, I, I, P]),
+            "bsf8_kv_read": (I, [P, P, I, I, P, P, P, P, I, P]),
+            "bsf8_tree_attention_workspace_bytes": (SZ, [I, I, I, I, I]),
+            "bsf8_tree_attention": (I, [P, I64, P, P, I, P, P, P, ctypes.c_float, I, P, P, I, I, I, P, SZ, P]),
+            "bsf8_verify_tree": (I, [P, P, I64, P, P, P, P, P, P, P, I, I, I, P]),
+            "bsf8_kv_commit": (I, [P, P, I, P, P, P, I, I, P]),
             "bsf8_device_status": (I, [P, P]),
             "bsf8_set_option": (I, [I, I64]),
             "bsf8_get_option": (I64, [I]),
@@ -412,3 +421,10 @@ def set_option(option: int, value: int):
 
 def get_option(option: int) -> int:
     return int(load().bsf8_get_option(option))
+
+
+# ----------------------------------------------------------------------- decode operators
+
+from .decode import (  # noqa: E402
+    MAX_NODES, KVCache, kv_commit, kv_read, qkv_append, tree_attention, tree_attention_workspace_bytes, verify_tree,
+)

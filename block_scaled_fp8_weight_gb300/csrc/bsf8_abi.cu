@@ -261,6 +261,31 @@ inline RowsCall plan_rows(int M, int N, int K, int G, int S) {
     return c;
 }
 
+// ----------------------------------------------------------------- decode operators
+
+
+// A cache descriptor's own rules, and the block table's.
+inline int check_cache(const bsf8_kv_cache *c, const int32_t *table, int requests, int table_pages) {
+    if (!c || !c->k8 || !c->kexp || !c->v8 || !c->vexp || !table) return BSF8_ERR_NULL;
+    if (c->pages < 1 || c->heads < 1 || requests < 1 || table_pages < 1) return BSF8_ERR_SHAPE;
+    if (c->page_size < 16 || c->page_size > 1024 || c->page_size % 16 != 0) return BSF8_ERR_SHAPE;
+    if (c->dim != 64 && c->dim != 128 && c->dim != 256) return BSF8_ERR_SHAPE;
+    if ((long long)c->heads * c->page_size >= (1LL << 31) ||
+        (long long)c->pages * c->heads * c->page_size >= (1LL << 31) ||
+        (long long)table_pages * c->page_size >= (1LL << 31))
+        return BSF8_ERR_SHAPE;
+    if (!aligned16(c->k8) || !aligned16(c->kexp) || !aligned16(c->v8) || !aligned16(c->vexp))
+        return BSF8_ERR_ALIGN;
+    return BSF8_OK;
+}
+
+inline CacheView cache_view(const bsf8_kv_cache *c, const int32_t *table, int requests, int table_pages) {
+    return CacheView{c->k8, c->kexp, c->v8, c->vexp, table, c->pages, c->page_size, c->heads, c->dim,
+                     requests, table_pages};
+}
+
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -277,6 +302,7 @@ const char *bsf8_strerror(int status) {
         case BSF8_ERR_TIMEOUT: return "a kernel gave up a bounded wait (outputs undefined)";
         case BSF8_ERR_DEVICE: return "device cannot run the sm_103a kernels";
         case BSF8_ERR_VALUE: return "option or scalar argument out of range";
+        case BSF8_ERR_INDEX: return "a kernel met an index outside its table and skipped it";
         default: return "unknown status";
     }
 }
@@ -446,6 +472,137 @@ int bsf8_pad_x(const void *x, int64_t ldx, void *x_out, int M, int G, int K, int
     if (!aligned16(x) || (ldx % 8) != 0 || !aligned16(x_out)) return BSF8_ERR_ALIGN;
     return from_cuda(launch_pad_x(x, (long long)ldx, x_out, M, G, K, Kp,
                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_qkv_append(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
+                    int64_t ldv, void *q_out, const bsf8_kv_cache *cache, const int32_t *table,
+                    int requests, int table_pages, const int32_t *req, const int32_t *slot,
+                    const int32_t *pos, const float *cos_sin, int positions, int rot,
+                    int interleaved, const void *q_norm, const void *k_norm, float eps, int N,
+                    int Hq, bsf8_stream_t stream) {
+    int st = check_cache(cache, table, requests, table_pages);
+    if (st) return st;
+    if (N == 0) return BSF8_OK;  // nothing to do; empty tensors may have no address
+    if (!k || !v || !req || !slot || (Hq > 0 && (!q || !q_out))) return BSF8_ERR_NULL;
+    if (rot != 0 && (!pos || !cos_sin)) return BSF8_ERR_NULL;
+    const int D = cache->dim;
+    if (N < 0 || Hq < 0 || (long long)(Hq + 2LL * cache->heads) * D >= (1LL << 24)) return BSF8_ERR_SHAPE;
+    if (rot < 0 || rot > D || rot % 16 != 0 || (rot > 0 && positions < 1)) return BSF8_ERR_SHAPE;
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return BSF8_ERR_VALUE;
+    const int64_t kvw = (int64_t)cache->heads * D;
+    if (ldk < kvw || ldv < kvw || (Hq > 0 && ldq < (int64_t)Hq * D)) return BSF8_ERR_STRIDE;
+    if (!aligned16(k) || !aligned16(v) || ldk % 8 != 0 || ldv % 8 != 0) return BSF8_ERR_ALIGN;
+    if (Hq > 0 && (!aligned16(q) || !aligned16(q_out) || ldq % 8 != 0)) return BSF8_ERR_ALIGN;
+    if ((rot > 0 && !aligned16(cos_sin)) || !aligned16(q_norm) || !aligned16(k_norm)) return BSF8_ERR_ALIGN;
+    if (!aligned4(req) || !aligned4(slot) || !aligned4(pos) || !aligned4(table)) return BSF8_ERR_ALIGN;
+    AppendArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.ldq = ldq;
+    a.ldk = ldk;
+    a.ldv = ldv;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.req = req;
+    a.slot = slot;
+    a.pos = pos;
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.rot = rot;
+    a.interleaved = interleaved ? 1 : 0;
+    a.q_norm = static_cast<const uint16_t *>(q_norm);
+    a.k_norm = static_cast<const uint16_t *>(k_norm);
+    a.eps = eps;
+    a.N = N;
+    a.Hq = Hq;
+    return from_cuda(launch_append(cache_view(cache, table, requests, table_pages), a,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests, int table_pages,
+                 const int32_t *req, const int32_t *slot, void *k_out, void *v_out, int N,
+                 bsf8_stream_t stream) {
+    int st = check_cache(cache, table, requests, table_pages);
+    if (st) return st;
+    if (N == 0) return BSF8_OK;
+    if (!req || !slot || (!k_out && !v_out)) return BSF8_ERR_NULL;
+    if (N < 0) return BSF8_ERR_SHAPE;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(req) || !aligned4(slot) || !aligned4(table))
+        return BSF8_ERR_ALIGN;
+    return from_cuda(launch_kv_read(cache_view(cache, table, requests, table_pages), req, slot, k_out, v_out, N,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t bsf8_tree_attention_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
+    if (B < 1 || B > 4096 || T < 1 || T > BSF8_MAX_NODES || heads < 1 || Hq < 1 || Hq % heads != 0 ||
+        (dim != 64 && dim != 128 && dim != 256))
+        return 0;
+    return attend_workspace_bytes(B, T, Hq, heads, dim);
+}
+
+int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
+                        const int32_t *table, int table_pages, const int32_t *ctx,
+                        const int32_t *nodes, const int32_t *mask, float scale, int max_len,
+                        void *out, float *lse, int B, int T, int Hq, void *workspace,
+                        size_t workspace_bytes, bsf8_stream_t stream) {
+    int st = check_cache(cache, table, B, table_pages);
+    if (st) return st;
+    if (!q || !ctx || !out) return BSF8_ERR_NULL;
+    if (B > 4096 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
+        return BSF8_ERR_SHAPE;
+    if (max_len < 1 || (long long)max_len > (long long)table_pages * cache->page_size) return BSF8_ERR_SHAPE;
+    if (!(scale > 0.0f) || scale > 3.0e38f) return BSF8_ERR_VALUE;
+    if (ldq < (int64_t)Hq * cache->dim) return BSF8_ERR_STRIDE;
+    if (!aligned16(q) || !aligned16(out) || ldq % 8 != 0) return BSF8_ERR_ALIGN;
+    if (!aligned4(ctx) || !aligned4(nodes) || !aligned4(mask) || !aligned4(lse) || !aligned4(table))
+        return BSF8_ERR_ALIGN;
+    const size_t need = attend_workspace_bytes(B, T, Hq, cache->heads, cache->dim);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return BSF8_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return BSF8_ERR_ALIGN;
+    }
+    AttendArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.ldq = ldq;
+    a.ctx = ctx;
+    a.nodes = nodes;
+    a.mask = mask;
+    a.scale = scale;
+    a.max_len = max_len;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.workspace = workspace;
+    return from_cuda(launch_attend(cache_view(cache, table, B, table_pages), a,
+                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_verify_tree(const float *p, const float *q, int64_t ld, const int32_t *tokens,
+                     const int32_t *parent, const float *u, const int32_t *nodes, int32_t *path,
+                     int32_t *count, int32_t *token, int B, int T, int V, bsf8_stream_t stream) {
+    if (!p || !tokens || !parent || !u || !path || !count || !token) return BSF8_ERR_NULL;
+    if (B < 1 || B > 65535 || T < 1 || T > BSF8_MAX_NODES || V < 1 || V > (1 << 20)) return BSF8_ERR_SHAPE;
+    if (ld < V) return BSF8_ERR_STRIDE;
+    if (!aligned16(p) || !aligned16(q)) return BSF8_ERR_ALIGN;
+    if (!aligned4(tokens) || !aligned4(parent) || !aligned4(u) || !aligned4(nodes) || !aligned4(path) ||
+        !aligned4(count) || !aligned4(token))
+        return BSF8_ERR_ALIGN;
+    VerifyArgs a{p, q, ld, tokens, parent, u, nodes, path, count, token, B, T, V};
+    return from_cuda(launch_verify(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_pages,
+                   const int32_t *ctx, const int32_t *path, const int32_t *count, int B, int T,
+                   bsf8_stream_t stream) {
+    int st = check_cache(cache, table, B, table_pages);
+    if (st) return st;
+    if (!ctx || !path || !count) return BSF8_ERR_NULL;
+    if (B > 65535 || T < 1 || T > BSF8_MAX_NODES) return BSF8_ERR_SHAPE;
+    if (!aligned4(ctx) || !aligned4(path) || !aligned4(count) || !aligned4(table)) return BSF8_ERR_ALIGN;
+    return from_cuda(launch_kv_commit(cache_view(cache, table, B, table_pages), ctx, path, count, B, T,
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int bsf8_device_status(int *status, bsf8_stream_t stream) {

@@ -1,0 +1,355 @@
+// bsf8_cache.cu -- the paged key/value cache: append (with the per-head norm and the
+// rotation in the same pass), read back, and the commit of a token tree's kept nodes.
+//
+// A cached row (token, head) is dim e4m3 codes and dim / 32 exponent bytes, one per 32
+// channels, chosen as make_twin_rows chooses them.  All three move each byte once and are
+// bound by HBM at prompt sizes, by launch and load latency at decode sizes.
+#include "bsf8_device.cuh"
+#include "bsf8_internal.h"
+
+#include <algorithm>
+
+namespace bsf8 {
+
+// Loads here are plain ones, not the read-only path (__ldg, __restrict__): the compiler may
+// move those above the dependency wait, and everything these kernels read may have been
+// written by the kernel before.
+
+namespace {
+
+template <typename... Params, typename... Args>
+cudaError_t launch_cache(void (*kernel)(Params...), long long blocks, int threads, cudaStream_t stream,
+                         Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min(blocks, 1LL << 30), 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = options().pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
+// Row (page, head, offset) of a token in the cache's arrays, for head 0; negative where an
+// index leaves its table.  Heads are page_size rows apart.
+__device__ __forceinline__ long long cache_row(const CacheView &c, int req, int slot) {
+    if ((unsigned)req >= (unsigned)c.requests || slot < 0) return -1;
+    const int pi = slot / c.page_size;
+    if (pi >= c.table_pages) return -1;
+    const int page = *(c.table + (size_t)req * c.table_pages + pi);
+    if ((unsigned)page >= (unsigned)c.pages) return -1;
+    return ((long long)page * c.heads) * c.page_size + (slot - pi * c.page_size);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&y)[8]) {
+    y[0] = bf16_lo(w.x); y[1] = bf16_hi(w.x);
+    y[2] = bf16_lo(w.y); y[3] = bf16_hi(w.y);
+    y[4] = bf16_lo(w.z); y[5] = bf16_hi(w.z);
+    y[6] = bf16_lo(w.w); y[7] = bf16_hi(w.w);
+}
+
+}  // namespace
+
+// -------------------------------------------------------------------- append
+//
+// D / 8 lanes hold a row, 8 channels a lane (one 16-byte load): the norm's sum is a shuffle
+// tree over them, a rotation partner of the split form sits rot / 16 lanes away, and the
+// four lanes of a 32-channel block share its exponent.  A group of lanes takes up to H heads
+// of one token and kind (q, k or v), whose loads are in flight together and whose cosines
+// and sines are loaded once.
+template <int D, int H>
+__global__ void __launch_bounds__(256) append_kernel(const CacheView c, const AppendArgs a, int *status) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int LPR = D / 8;
+    const int sub = threadIdx.x % LPR;
+    const int lane = threadIdx.x & 31;
+    const uint32_t gmask = LPR == 32 ? 0xFFFFFFFFu : ((1u << LPR) - 1u) << (lane - sub);
+    const int c0 = sub * 8;  // this lane's first channel
+    const int qc = (a.Hq + H - 1) / H, kc = (c.heads + H - 1) / H;
+    const int chunks = qc + 2 * kc;
+    const long long items = (long long)a.N * chunks;
+    const long long step = (long long)gridDim.x * (256 / LPR);
+    for (long long it = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR; it < items; it += step) {
+        const int n = (int)(it / chunks);
+        int ch = (int)(it - (long long)n * chunks);
+        const int kind = ch < qc ? 0 : ch < qc + kc ? 1 : 2;
+        ch -= kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
+        const int h0 = ch * H;
+        const int heads = kind == 0 ? a.Hq : c.heads;
+        const uint16_t *src = kind == 0   ? a.q + (size_t)n * a.ldq
+                              : kind == 1 ? a.k + (size_t)n * a.ldk
+                                          : a.v + (size_t)n * a.ldv;
+        uint4 w[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            w[j] = h0 + j < heads ? *reinterpret_cast<const uint4 *>(src + (size_t)(h0 + j) * D + c0)
+                                  : make_uint4(0, 0, 0, 0);
+        int pos = 0;
+        if (a.rot > 0) {
+            pos = *(a.pos + n);
+            if ((unsigned)pos >= (unsigned)a.positions) {
+                if (sub == 0) report_index(status);
+                continue;  // uniform over the group
+            }
+        }
+        long long row = 0;
+        if (kind > 0) {
+            const int slot = *(a.slot + n);
+            if (slot < 0) continue;
+            row = cache_row(c, *(a.req + n), slot);
+            if (row < 0) {
+                if (sub == 0) report_index(status);
+                continue;
+            }
+        }
+        const uint16_t *nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+        float g[8];
+        if (nw) unpack8(*reinterpret_cast<const uint4 *>(nw + c0), g);
+        const bool turned = kind < 2 && a.rot > 0 && c0 < a.rot;
+        float cs[8], sn[8];  // split form: per channel; interleaved: per pair (4)
+        const int half = a.rot / 2;
+        if (turned) {
+            const float *t = a.cos_sin + (size_t)pos * a.rot;
+            const int i0 = a.interleaved ? c0 / 2 : (c0 < half ? c0 : c0 - half);
+            const float4 x0 = *reinterpret_cast<const float4 *>(t + i0);
+            const float4 y0 = *reinterpret_cast<const float4 *>(t + half + i0);
+            cs[0] = x0.x; cs[1] = x0.y; cs[2] = x0.z; cs[3] = x0.w;
+            sn[0] = y0.x; sn[1] = y0.y; sn[2] = y0.z; sn[3] = y0.w;
+            if (!a.interleaved) {
+                const float4 x1 = *reinterpret_cast<const float4 *>(t + i0 + 4);
+                const float4 y1 = *reinterpret_cast<const float4 *>(t + half + i0 + 4);
+                cs[4] = x1.x; cs[5] = x1.y; cs[6] = x1.z; cs[7] = x1.w;
+                sn[4] = y1.x; sn[5] = y1.y; sn[6] = y1.z; sn[7] = y1.w;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            if (h0 + j >= heads) break;
+            float y[8];
+            unpack8(w[j], y);
+            if (nw) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+                for (int m = LPR / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(gmask, ss, m);
+                const float r = __frsqrt_rn(ss * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = y[i] * r * g[i];
+            }
+            if (kind < 2 && a.rot > 0) {
+                if (a.interleaved) {
+                    if (turned) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = y[2 * i], v = y[2 * i + 1];
+                            y[2 * i] = u * cs[i] - v * sn[i];
+                            y[2 * i + 1] = v * cs[i] + u * sn[i];
+                        }
+                    }
+                } else {  // the partner channel is rot / 2 away: half / 8 lanes up or down
+                    const int from = !turned ? lane : c0 < half ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float o = __shfl_sync(gmask, y[i], from);
+                        if (turned) y[i] = c0 < half ? y[i] * cs[i] - o * sn[i] : y[i] * cs[i] + o * sn[i];
+                    }
+                }
+            }
+            if (kind == 0) {
+                *reinterpret_cast<uint4 *>(a.q_out + ((size_t)n * a.Hq + h0 + j) * D + c0) =
+                    make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                               pack_bf16(y[6], y[7]));
+                continue;
+            }
+            uint32_t am = 0;  // magnitude bits order as magnitudes do, NaN above infinity
+#pragma unroll
+            for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+            am = max(am, __shfl_xor_sync(gmask, am, 1));
+            am = max(am, __shfl_xor_sync(gmask, am, 2));
+            // 448 = 1.75 * 2^8: adding 0x1FFFFF carries into the exponent past mantissa 0.75
+            int e = max(0, (int)((am + 0x1FFFFFu) >> 23) - 8);
+            uint2 codes;
+            if (am >= 0x7F800000u) {
+                e = 255;
+                codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            } else {
+                const float inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e), exact products
+                codes = make_uint2(pack_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                   pack_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+            }
+            const size_t r = (size_t)row + (size_t)(h0 + j) * c.page_size;
+            uint8_t *d8 = kind == 1 ? c.k8 : c.v8, *de = kind == 1 ? c.kexp : c.vexp;
+            *reinterpret_cast<uint2 *>(d8 + r * D + c0) = codes;
+            if ((sub & 3) == 0) de[r * (D / 32) + c0 / 32] = (uint8_t)e;
+        }
+    }
+}
+
+template <int D>
+cudaError_t append_dim(const CacheView &c, const AppendArgs &a, cudaStream_t stream, int *status) {
+    constexpr int per = 256 / (D / 8);
+    // one head a group while the groups of all heads leave SMs idle, else four
+    const long long rows = (long long)a.N * (a.Hq + 2LL * c.heads);
+    if (rows <= 152LL * 8 * per) return launch_cache(append_kernel<D, 1>, (rows + per - 1) / per, 256, stream, c, a, status);
+    const long long items = (long long)a.N * ((a.Hq + 3) / 4 + 2 * ((c.heads + 3) / 4));
+    return launch_cache(append_kernel<D, 4>, (items + per - 1) / per, 256, stream, c, a, status);
+}
+
+cudaError_t launch_append(const CacheView &c, const AppendArgs &a, cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    switch (c.dim) {
+        case 64: return append_dim<64>(c, a, stream, status);
+        case 128: return append_dim<128>(c, a, stream, status);
+        case 256: return append_dim<256>(c, a, stream, status);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// ---------------------------------------------------------------------- read
+// A thread per 16 codes of a row (one 16-byte load, two 16-byte stores), the rebuild of
+// bsf8_dequant.
+__global__ void __launch_bounds__(256) kv_read_kernel(const CacheView c, const int32_t *req,
+                                                      const int32_t *slot,
+                                                      uint16_t *k_out, uint16_t *v_out,
+                                                      int cpt, long long items, int *status) {
+    pdl_trigger();
+    pdl_wait();
+    const int cpr = c.dim / 16;  // pieces a row; cpt: pieces a token of one side
+    const long long step = (long long)gridDim.x * blockDim.x;
+    const bool both = k_out && v_out;
+    for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < items; it += step) {
+        const long long ns = it / cpt;
+        const int piece = (int)(it - ns * cpt);
+        const int n = (int)(both ? ns >> 1 : ns);
+        const bool key = both ? (ns & 1) == 0 : k_out != nullptr;
+        const int h = piece / cpr, p = piece - h * cpr;
+        const int sl = *(slot + n);
+        const long long row0 = cache_row(c, *(req + n), sl);
+        uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
+        if (row0 >= 0) {
+            const size_t r = (size_t)row0 + (size_t)h * c.page_size;
+            const uint4 q = *reinterpret_cast<const uint4 *>((key ? c.k8 : c.v8) + r * c.dim + 16 * p);
+            const uint32_t e = (key ? c.kexp : c.vexp)[r * (c.dim / 32) + p / 2];
+            const Scale sc = make_scale(e);
+            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                rebuild4(qw[i], sc, o[2 * i], o[2 * i + 1]);
+                if (nan_code_mask(qw[i])) patch_nan_codes(qw[i], o[2 * i], o[2 * i + 1]);
+            }
+            o0 = make_uint4(o[0], o[1], o[2], o[3]);
+            o1 = make_uint4(o[4], o[5], o[6], o[7]);
+        } else if (sl >= 0) {
+            report_index(status);
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>((key ? k_out : v_out) + ((size_t)n * cpt + piece) * 16);
+        dst[0] = o0;
+        dst[1] = o1;
+    }
+}
+
+cudaError_t launch_kv_read(const CacheView &c, const int32_t *req, const int32_t *slot, void *k_out,
+                           void *v_out, int N, cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    const int cpt = c.heads * (c.dim / 16);
+    const long long items = (long long)N * cpt * (k_out && v_out ? 2 : 1);
+    return launch_cache(kv_read_kernel, (items + 255) / 256, 256, stream, c, req, slot,
+                        static_cast<uint16_t *>(k_out), static_cast<uint16_t *>(v_out), cpt, items, status);
+}
+
+// -------------------------------------------------------------------- commit
+// A block per request; a thread owns a 16-byte column of a head's rows (or a head's exponent
+// bytes) and moves the kept nodes in order, eight loads before their eight stores.  In place
+// without a hazard: path is strictly increasing, so path[i] >= i, and a store to slot i can
+// only hit a source path[j] with j <= i, which its thread has read already.
+constexpr int kCommitBatch = 8;
+
+template <typename U>
+__device__ __forceinline__ void commit_column(uint8_t *base, size_t row_bytes, const long long *rows, int count,
+                                              size_t col, size_t head_off) {
+    for (int i = 1; i < count; i += kCommitBatch) {
+        U v[kCommitBatch];
+#pragma unroll
+        for (int j = 0; j < kCommitBatch; ++j)
+            if (i + j < count && rows[2 * (i + j)] >= 0)
+                v[j] = *reinterpret_cast<const U *>(base + ((size_t)rows[2 * (i + j)] + head_off) * row_bytes + col);
+#pragma unroll
+        for (int j = 0; j < kCommitBatch; ++j)
+            if (i + j < count && rows[2 * (i + j)] >= 0)
+                *reinterpret_cast<U *>(base + ((size_t)rows[2 * (i + j) + 1] + head_off) * row_bytes + col) = v[j];
+    }
+}
+
+__global__ void __launch_bounds__(256) kv_commit_kernel(const CacheView c, const int32_t *ctx,
+                                                        const int32_t *path,
+                                                        const int32_t *count, int T, int *status) {
+    __shared__ long long rows[2 * 256];  // source and target row of each kept node (head 0)
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.x;
+    const int n = min(*(count + b), T), at = *(ctx + b);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+        const int from = *(path + (size_t)b * T + i);
+        long long src = -1, dst = -1;
+        if (from >= i && at >= 0 && from <= 0x7FFFFFFF - at) {
+            src = cache_row(c, b, at + from);
+            dst = cache_row(c, b, at + i);
+        }
+        if (src < 0 || dst < 0) {
+            report_index(status);
+            src = -1;
+        }
+        rows[2 * i] = src;
+        rows[2 * i + 1] = dst;
+    }
+    __syncthreads();
+    const int cpr = c.dim / 16, cols = c.heads * cpr;
+    for (int t = threadIdx.x; t < 2 * cols + 2 * c.heads; t += blockDim.x) {
+        if (t < 2 * cols) {
+            const int k = t % cols, h = k / cpr;
+            commit_column<uint4>(t < cols ? c.k8 : c.v8, c.dim, rows, n, 16 * (size_t)(k - h * cpr),
+                                 (size_t)h * c.page_size);
+        } else {
+            const int k = t - 2 * cols, h = k % c.heads;
+            uint8_t *base = k < c.heads ? c.kexp : c.vexp;
+            const size_t off = (size_t)h * c.page_size;
+            if (c.dim == 64) commit_column<uint16_t>(base, 2, rows, n, 0, off);
+            else if (c.dim == 128) commit_column<uint32_t>(base, 4, rows, n, 0, off);
+            else commit_column<uint2>(base, 8, rows, n, 0, off);
+        }
+    }
+}
+
+cudaError_t launch_kv_commit(const CacheView &c, const int32_t *ctx, const int32_t *path, const int32_t *count,
+                             int B, int T, cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    const int cols = 2 * c.heads * (c.dim / 16 + 1);
+    const int threads = std::min(256, (cols + 31) / 32 * 32);
+    return launch_cache(kv_commit_kernel, B, threads, stream, c, ctx, path, count, T, status);
+}
+
+}  // namespace bsf8

@@ -13,6 +13,7 @@ namespace bsf8 {
 // Kernels record a bounded wait that ran out in the library's device status word
 // (defined in bsf8_abi.cu; its address reaches the kernels as a parameter).
 constexpr int kStatusTimeout = 7;  // == BSF8_ERR_TIMEOUT
+constexpr int kStatusIndex = 10;   // == BSF8_ERR_INDEX
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -87,6 +88,9 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
 }
 
 __device__ __forceinline__ void report_timeout(int *status) { atomicExch(status, kStatusTimeout); }
+
+// A device-side index outside its table; does not hide a timeout recorded before.
+__device__ __forceinline__ void report_index(int *status) { atomicCAS(status, 0, kStatusIndex); }
 
 // ------------------------------------------------------------- bulk copies (TMA)
 

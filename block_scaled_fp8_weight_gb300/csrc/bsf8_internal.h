@@ -123,4 +123,57 @@ cudaError_t launch_pad_k(const uint8_t *w8, const uint8_t *ex, uint8_t *w8_out, 
 cudaError_t launch_pad_x(const void *x, long long ldx, void *x_out, int M, int G, int K, int Kp,
                          cudaStream_t stream);
 
+// ---- decode operators.  A cache descriptor and its block table as the kernels take them.
+struct CacheView {
+    uint8_t *k8, *kexp, *v8, *vexp;
+    const int32_t *table;
+    int pages, page_size, heads, dim;
+    int requests, table_pages;
+};
+
+// bsf8_cache.cu
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    long long ldq, ldk, ldv;
+    uint16_t *q_out;
+    const int32_t *req, *slot, *pos;
+    const float *cos_sin;
+    int positions, rot, interleaved;
+    const uint16_t *q_norm, *k_norm;
+    float eps;
+    int N, Hq;
+};
+cudaError_t launch_append(const CacheView &c, const AppendArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_read(const CacheView &c, const int32_t *req, const int32_t *slot, void *k_out,
+                           void *v_out, int N, cudaStream_t stream);
+cudaError_t launch_kv_commit(const CacheView &c, const int32_t *ctx, const int32_t *path, const int32_t *count,
+                             int B, int T, cudaStream_t stream);
+
+// bsf8_verify.cu
+struct VerifyArgs {
+    const float *p, *q;
+    long long ld;
+    const int32_t *tokens, *parent;
+    const float *u;
+    const int32_t *nodes;
+    int32_t *path, *count, *token;
+    int B, T, V;
+};
+cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream);
+
+// bsf8_attend.cu
+struct AttendArgs {
+    const uint16_t *q;
+    long long ldq;
+    const int32_t *ctx, *nodes, *mask;
+    float scale;
+    int max_len;
+    uint16_t *out;
+    float *lse;
+    int B, T, Hq;
+    void *workspace;
+};
+size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim);
+cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream);
+
 }  // namespace bsf8

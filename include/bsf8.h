@@ -54,7 +54,9 @@ enum {
     BSF8_ERR_CUDA = 6,      /* a CUDA runtime call failed (launch, attribute, copy)     */
     BSF8_ERR_TIMEOUT = 7,   /* a kernel gave up a bounded wait (device status only)     */
     BSF8_ERR_DEVICE = 8,    /* the current device is not sm_103 / cannot run the kernels */
-    BSF8_ERR_VALUE = 9      /* an option or scalar argument is out of range             */
+    BSF8_ERR_VALUE = 9,     /* an option or scalar argument is out of range             */
+    BSF8_ERR_INDEX = 10     /* a kernel met an index outside its table and skipped it   */
+                            /* (device status only)                                     */
 };
 
 /* Largest row count a single bsf8_gemm call accepts.  The pages serve 2..8 and 9..192
@@ -287,6 +289,147 @@ int bsf8_pad_k(const uint8_t *w8, const uint8_t *exp, uint8_t *w8_out, uint8_t *
  * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_CUDA. */
 int bsf8_pad_x(const void *x, int64_t ldx, void *x_out, int M, int G, int K, int Kp,
                bsf8_stream_t stream);
+
+/* ================================================================ decode operators
+ * What a decode, verify or draft pass runs beside its linear layers: queries and keys are
+ * normed and rotated, keys and values go into a paged cache in the twin's number format with
+ * one exponent per (row, 32 channels), a tree of drafted tokens attends to that cache, the
+ * drafts are verified against the target's probabilities, and the kept ones move together.
+ * The pages serve these passes (decode, verify, draft rows) but show none of these operators;
+ * the format is bsf8_make_twin_rows' (e4m3 codes, exponent byte e + 127, the smallest
+ * e >= -127 with 448 * 2^e >= amax; a block with an infinity or a NaN gets byte 255 and codes
+ * 0x7F, and reads back as NaN).
+ *
+ * The cache: token `slot` of request b lies in page table[b][slot / page_size], row
+ * slot % page_size.  A page holds [heads][page_size][dim] codes and
+ * [heads][page_size][dim / 32] exponent bytes, for keys and for values.
+ *   k8, v8      device, uint8 [pages][heads][page_size][dim], 16-byte aligned
+ *   kexp, vexp  device, uint8 [pages][heads][page_size][dim / 32], 16-byte aligned
+ *   page_size   a multiple of 16, 16 .. 1024;  dim  64, 128 or 256
+ *   pages * heads * page_size < 2^31
+ * The struct itself is host memory, read before the call returns.  table is a device array
+ * int32 [requests][table_pages]; only entries of slots that a call touches are read.
+ *
+ * Indices that live on the device (table entries, slots, requests, positions, lengths)
+ * cannot be checked on the host.  The kernels check them: an index outside its table makes
+ * the kernel skip that row and record BSF8_ERR_INDEX in the device status word
+ * (bsf8_device_status), and nothing outside the given buffers is read or written. */
+typedef struct {
+    uint8_t *k8, *kexp, *v8, *vexp;
+    int pages, page_size, heads, dim;
+} bsf8_kv_cache;
+
+/* Most nodes of a token tree (its root, the last kept token, counts). */
+#define BSF8_MAX_NODES 256
+
+/* Norms, rotates and appends the projections of N tokens in one pass.  Per head row x of
+ * dim channels, in fp32:
+ *   y = x * w / sqrt(mean(x^2) + eps)            where the norm's weight w is given
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for the first `rot` channels, the
+ *   pairs (a, b) = (i, i + rot/2), or (2i, 2i + 1) when `interleaved`, with
+ *   cos = cos_sin[pos][i] and sin = cos_sin[pos][rot/2 + i], i < rot/2
+ * for queries and keys; queries are rounded once to bf16, keys and values (values neither
+ * normed nor rotated) once to cache codes.
+ *   q, k, v    device, bf16; head h of token n at q[n * ldq + h * dim] (ldk, ldv likewise);
+ *              q may be NULL with Hq = 0: only keys and values are appended
+ *   q_out      device, out, bf16 [N][Hq][dim]
+ *   req, slot  device, int32 [N]: where token n goes; slot < 0: its k and v are not kept
+ *              (a padded row), its q is written all the same
+ *   pos        device, int32 [N] (0 .. positions - 1), needed where rot > 0; may differ from
+ *              the slot: the siblings of a token tree share a position
+ *   cos_sin    device, fp32 [positions][rot], 16-byte aligned
+ *   rot        0 (no rotation) .. dim, a multiple of 16
+ *   q_norm, k_norm  device, bf16 [dim], or NULL (no norm);  eps >= 0, finite
+ * Pointers of bf16 rows 16-byte aligned, ld* multiples of 8.  Two tokens of a call must not
+ * name the same (req, slot).  A token with a bad position is skipped whole (its q rows are
+ * not written), one with a bad req, slot or page keeps its q rows.
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_VALUE,
+ *         BSF8_ERR_CUDA. */
+int bsf8_qkv_append(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
+                    int64_t ldv, void *q_out, const bsf8_kv_cache *cache, const int32_t *table,
+                    int requests, int table_pages, const int32_t *req, const int32_t *slot,
+                    const int32_t *pos, const float *cos_sin, int positions, int rot,
+                    int interleaved, const void *q_norm, const void *k_norm, float eps, int N,
+                    int Hq, bsf8_stream_t stream);
+
+/* Reads N cached tokens back: k_out and v_out (device, out, bf16 [N][heads][dim], 16-byte
+ * aligned; either may be NULL) get bf16(e4m3(code) * 2^(byte - 127)) of token slot[n] of
+ * request req[n]; rows with slot < 0 become zeros, and so do rows with a bad index.
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_CUDA. */
+int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests, int table_pages,
+                 const int32_t *req, const int32_t *slot, void *k_out, void *v_out, int N,
+                 bsf8_stream_t stream);
+
+/* Attention of a token tree over the cache.  Request b has ctx[b] cached tokens (slots 0 ..
+ * ctx[b] - 1) that every node sees, and nodes[b] tree nodes, already appended at slots
+ * ctx[b] + j; query row t of the request is node t:
+ *   out[b][t][h] = sum_l p_l v_l / sum_l p_l,   p_l = exp(scale * q[b][t][h] . k_l),
+ * over the ctx[b] tokens and the nodes j < nodes[b] with bit j of mask[b][t] set (mask NULL:
+ * j <= t, a chain; T = 1 is the single-token step).  Query head h reads cache head
+ * h / (Hq / heads).  Sums and softmax statistics are fp32; see bsf8_attend.cu for how the
+ * products are formed.  A row that sees nothing, and rows t >= nodes[b], give zeros and an
+ * lse of -inf.  A key or a value block that holds NaN reaches exactly the rows that see it.
+ *   q      device, bf16, 16-byte aligned; node t of request b at q + (b * T + t) * ldq, its
+ *          heads one after another; ldq >= Hq * dim, a multiple of 8
+ *   ctx    device, int32 [B];  nodes  device, int32 [B], or NULL (all T)
+ *   mask   device, int32 [B][T][ceil(T / 32)], bit j % 32 of word j / 32, or NULL
+ *   max_len  host: no request has more than max_len cached tokens, its nodes included
+ *          (1 .. table_pages * page_size); it sizes the launch, and longer requests count as
+ *          BSF8_ERR_INDEX and are cut there
+ *   out    device, out, bf16 [B][T][Hq][dim], 16-byte aligned
+ *   lse    device, out, fp32 [B][T][Hq]: log of the sum of p_l, or NULL
+ *   workspace  device, 16-byte aligned, of at least bsf8_tree_attention_workspace_bytes(...);
+ *          no zeroing needed; not to be shared by calls that can overlap
+ *   T      1 .. BSF8_MAX_NODES;  B  1 .. 4096;  Hq a multiple of heads;  scale finite, > 0
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_VALUE,
+ *         BSF8_ERR_WORKSPACE, BSF8_ERR_CUDA. */
+int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
+                        const int32_t *table, int table_pages, const int32_t *ctx,
+                        const int32_t *nodes, const int32_t *mask, float scale, int max_len,
+                        void *out, float *lse, int B, int T, int Hq, void *workspace,
+                        size_t workspace_bytes, bsf8_stream_t stream);
+
+/* Workspace bsf8_tree_attention needs (0 for invalid sizes). */
+size_t bsf8_tree_attention_workspace_bytes(int B, int T, int Hq, int heads, int dim);
+
+/* Verifies drafted token trees against the target's probabilities by recursive rejection, so
+ * that the kept tokens and the next one are distributed as the target's own.  Request b's
+ * tree has nodes[b] nodes; node 0 is the last token kept before, parent[b][i] < i.  p[b][i] is
+ * the target's distribution after node i, q[b][i] the draft's, from which the children of i
+ * were drawn independently; q NULL: the children were not drawn at random (a draft's top
+ * tokens), each then counts as drawn from a distribution that has only its token.
+ * The walk starts at node 0.  At node c, with R = P(c) and Z = 2^40, its children are asked in
+ * order of their index; child i with token x and number u = u[b][i]:
+ *   Q' = floor(Q(c) * Z / 2^40);   kept if floor(floor(u * 2^24) * Q'(x) / 2^24) < R(x):
+ *   the walk goes on at node i; else R = max(R - Q', 0), Z = sum of R, next child,
+ * where P(x) = floor(p(x) * 2^40), Q likewise (p and q clamped to [0, 1], a NaN counts as 0).
+ * When no child is kept, the next token is drawn from R (from P(c) where R is all 0): the
+ * lowest x with  R(0) + .. + R(x) > floor(floor(u[b][0] * 2^24) * sum of R / 2^24),  V - 1
+ * where there is none.  All of it in integers: the result does not depend on any order.
+ *   p, q    device, fp32, node i of request b at p + (b * T + i) * ld, 16-byte aligned
+ *   tokens  device, int32 [B][T] (0 .. V - 1; [b][0] is not read)
+ *   parent  device, int32 [B][T] ([b][0] is not read)
+ *   u       device, fp32 [B][T], uniform in [0, 1), multiples of 2^-24 used whole
+ *   nodes   device, int32 [B], or NULL (all T)
+ *   path    device, out, int32 [B][T]: the kept nodes in order, node 0 first, then -1
+ *   count   device, out, int32 [B]: how many are kept (node 0 counts)
+ *   token   device, out, int32 [B]: the next token
+ *   T  1 .. BSF8_MAX_NODES;  V  1 .. 2^20;  ld >= V
+ * A child with a bad token or parent is never kept (BSF8_ERR_INDEX).
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_CUDA. */
+int bsf8_verify_tree(const float *p, const float *q, int64_t ld, const int32_t *tokens,
+                     const int32_t *parent, const float *u, const int32_t *nodes, int32_t *path,
+                     int32_t *count, int32_t *token, int B, int T, int V, bsf8_stream_t stream);
+
+/* Moves the kept nodes of each request's tree together: for i < count[b], slot
+ * ctx[b] + path[b][i] -> ctx[b] + i, keys and values, codes and exponents, bit for bit.
+ * path[b] is strictly increasing over the first count[b] (as bsf8_verify_tree gives it); the
+ * slots behind keep what they held.
+ *   ctx, count  device, int32 [B];  path  device, int32 [B][T];  T  1 .. BSF8_MAX_NODES
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_CUDA. */
+int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_pages,
+                   const int32_t *ctx, const int32_t *path, const int32_t *count, int B, int T,
+                   bsf8_stream_t stream);
 
 /* ------------------------------------------------------------------ diagnostics
  * Not part of the method: a measurement aid.  Launches 2*nsm one-warp blocks on `stream`;
