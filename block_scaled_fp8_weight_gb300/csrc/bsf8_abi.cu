@@ -551,7 +551,8 @@ int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
     if (B > 4096 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
         return BSF8_ERR_SHAPE;
     if (max_len < 1 || (long long)max_len > (long long)table_pages * cache->page_size) return BSF8_ERR_SHAPE;
-    if (!(scale > 0.0f) || scale > 3.0e38f) return BSF8_ERR_VALUE;
+    if (!attend_fits(cache_view(cache, table, B, table_pages), B, T, Hq, max_len)) return BSF8_ERR_SHAPE;
+    if (!(scale > 0.0f) || scale > 2.0e38f) return BSF8_ERR_VALUE;
     if (ldq < (int64_t)Hq * cache->dim) return BSF8_ERR_STRIDE;
     if (!aligned16(q) || !aligned16(out) || ldq % 8 != 0) return BSF8_ERR_ALIGN;
     if (!aligned4(ctx) || !aligned4(nodes) || !aligned4(mask) || !aligned4(lse) || !aligned4(table))

@@ -174,6 +174,7 @@ struct AttendArgs {
     void *workspace;
 };
 size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim);
+bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len);
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream);
 
 }  // namespace bsf8
