@@ -534,7 +534,7 @@ int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests,
 }
 
 size_t bsf8_tree_attention_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
-    if (B < 1 || B > 4096 || T < 1 || T > BSF8_MAX_NODES || heads < 1 || Hq < 1 || Hq % heads != 0 ||
+    if (B < 1 || B > 1024 || T < 1 || T > BSF8_MAX_NODES || heads < 1 || Hq < 1 || Hq % heads != 0 ||
         (dim != 64 && dim != 128 && dim != 256))
         return 0;
     return attend_workspace_bytes(B, T, Hq, heads, dim);
@@ -548,7 +548,7 @@ int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
     int st = check_cache(cache, table, B, table_pages);
     if (st) return st;
     if (!q || !ctx || !out) return BSF8_ERR_NULL;
-    if (B > 4096 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
+    if (B > 1024 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
         return BSF8_ERR_SHAPE;
     if (max_len < 1 || (long long)max_len > (long long)table_pages * cache->page_size) return BSF8_ERR_SHAPE;
     if (!attend_fits(cache_view(cache, table, B, table_pages), B, T, Hq, max_len)) return BSF8_ERR_SHAPE;

@@ -43,18 +43,24 @@
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
+#include <cuda.h>
+
 #include <algorithm>
+#include <mutex>
 
 namespace bsf8 {
 
 namespace {
 
 constexpr int kAttendBlocks = 152;   // one an SM of a GB300 (no block waits for another)
-constexpr int kMaxBatch = 4096;
-constexpr int kSoftWarps = 4, kDeqWarps = 8;
-constexpr int kProducerWarp = kSoftWarps + kDeqWarps, kMmaWarp = kProducerWarp + 1;
-constexpr int kThreadsA = (kMmaWarp + 1) * 32;
-constexpr int kInfo = 4;             // tiles whose exponents and flags are kept
+constexpr int kMaxBatch = 1024;
+constexpr int kSoftWarps = 8;        // two sets of four, a set every other tile
+constexpr int kDeqWarps = 8;
+constexpr int kProducerWarp = kSoftWarps + kDeqWarps, kScoutWarp = kProducerWarp + 1;
+constexpr int kMmaWarp = kScoutWarp + 1;  // two: S, O
+constexpr int kThreadsA = (kMmaWarp + 2) * 32;
+constexpr int kExps = 4;             // tiles whose exponents are in shared memory
+constexpr int kInfo = 8;             // tiles whose exponents and flags are kept
 constexpr float kBias = 13.0f;       // p = 2^(x - m + kBias)
 constexpr float kSlack = 2.0f;       // m lags the maximum by at most this
 constexpr int kShift = 6;            // f16 values are code * 2^(e - E + kShift)
@@ -62,15 +68,18 @@ constexpr int kShift = 6;            // f16 values are code * 2^(e - E + kShift)
 template <int D>
 struct Shape {
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
-    static constexpr int NS = D == 256 ? 1 : 2;      // S buffers
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
-    static constexpr int NSLOT = D == 64 ? 8 : 5;
-    static constexpr int F16 = TN * D * 2;           // bytes of an f16 tile
-    // tensor memory columns: Q (f16 pairs), P (f16 pairs), O, S
-    static constexpr int CQ = 0, CP = D / 2, CO = D == 256 ? 256 : CP + TN / 2, CS = D == 256 ? 192 : CO + D;
-    static constexpr int oK = 0, oV = F16, oRing = 3 * F16, oExp = oRing + NSLOT * SLOT;
-    static constexpr int oStage = oExp + NSLOT * 512, oPrefix = oStage + 4 * 32 * 33 * 4;
+    static constexpr int NSLOT = D == 256 ? 2 : 4;   // ring slots of keys, and of values
+    static constexpr int F16 = TN * D * 2;           // bytes of an f16 tile of values
+    // tensor memory columns: two S (a tile's P, f16 pairs, takes its S's place), O, the scales of Q
+    // and of two tiles' keys, and up to dim 128 Q (two e4m3 parts, four to a column)
+    static constexpr int CS = 0, CO = 2 * TN, CA = CO + D, CB = CA + 4,
+                         CQ = D == 256 ? 0 : CA + 32;
+    static constexpr bool QS = D == 256;             // Q in shared memory
+    static constexpr int oV = 0, oK = 2 * F16, oRing = oK + NSLOT * SLOT, oQ = oRing + NSLOT * SLOT;
+    static constexpr int oExp = oQ + (QS ? 2 * 128 * D : 0), oStage = oExp + 2 * kExps * 512;
+    static constexpr int oPrefix = oStage + 2 * 128 * 17 * 4;
 };
 
 // At least 176 KB, so that no block of another kernel that holds tensor memory (84 KB of shared
@@ -82,6 +91,8 @@ constexpr int attend_smem(int B) {
 }
 
 struct AttendParams {
+    CUtensorMap kmap;  // the key codes as rows of D bytes, box min(D, 128) x box_rows, swizzled
+    int box_rows;
     CacheView c;
     const uint16_t *q;
     long long ldq;
@@ -172,6 +183,46 @@ __device__ __forceinline__ void umma_a(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// kind::mxf8f6f4, e4m3 A and B with a power-of-two scale (ue8m0) per row and 32 channels, fp32
+// accumulator, M = 128; sa, sb: which byte of the scales' words.
+__device__ __forceinline__ constexpr uint32_t idesc_mx(int n, int sa, int sb) {
+    return ((uint32_t)sb << 4) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(128 >> 4) << 24) |
+           ((uint32_t)sa << 29);
+}
+
+__device__ __forceinline__ void umma_mx_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], [%1], %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_mx_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+}
+
+// Codes of K (or Q): rows of RB = 128 or 64 bytes with the swizzle of that width, 8-row atoms.
+template <int RB>
+__device__ __forceinline__ uint64_t desc_codes(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(8 * RB >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)(RB == 128 ? 2 : 4) << 61);
+}
+
+__device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int col, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(col), "r"(row), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ void commit_a(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
@@ -203,6 +254,12 @@ __device__ __forceinline__ void ld_cols(uint32_t t, uint32_t (&r)[32]) {
         : "memory");
 }
 
+__device__ __forceinline__ void st_cols(uint32_t t, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3])
+                 : "memory");
+}
+
 __device__ __forceinline__ void st_cols(uint32_t t, const uint32_t (&r)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]),
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -232,8 +289,40 @@ __device__ __forceinline__ void st_cols(uint32_t t, const uint32_t (&r)[32]) {
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error at most 2^-22
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // relative error about 2^-22
     return y;
+}
+
+// (x0, x1) * c + off and a + b, two fp32 at a time.
+__device__ __forceinline__ void fma2(float &y0, float &y1, uint32_t x0, uint32_t x1, uint64_t c, uint64_t off) {
+    uint64_t x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(x0), "r"(x1));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(x), "l"(c), "l"(off));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y0), "=f"(y1) : "l"(y));
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
+__device__ __forceinline__ float sum_pair(uint64_t a) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+    return x + y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -245,6 +334,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// f16 pair -> e4m3 pair, nearest even.
+__device__ __forceinline__ uint32_t f16_to_e4m3(uint32_t two) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(two));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
 
@@ -288,54 +390,56 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     return r;
 }
 
-// N registers of P (f16 pairs) into columns [t, t + N) of the thread's lane.
-template <int N>
-__device__ __forceinline__ void st_part(uint32_t t, const uint32_t (&r)[N]) {
-    constexpr int C = N < 32 ? N : 32;
-#pragma unroll
-    for (int k = 0; k < N; k += C) {
-        uint32_t x[C];
-#pragma unroll
-        for (int j = 0; j < C; ++j) x[j] = r[k + j];
-        st_cols(t + k, x);
-    }
-}
-
-// 32 channels of a row's output: bf16 where the segment is the whole row, else a partial.
-template <int RT, int D>
+// N channels (from k) of a row's output: bf16 where the segment is the whole row, else a partial.
+template <int RT, int D, int N>
 __device__ __forceinline__ void store_row(const AttendParams &p, const Segment &g, bool whole, int slotw, int row,
-                                          int t, int hq, int k, const float (&y)[32]) {
+                                          int t, int hq, int k, const float (&y)[N]) {
     if (whole) {
         uint16_t *dst = p.out + (((size_t)g.b * p.T + t) * p.Hq + hq) * D + k;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
-            *reinterpret_cast<uint4 *>(dst + j) = make_uint4(pack_bf(y[j], y[j + 1]), pack_bf(y[j + 2], y[j + 3]),
-                                                             pack_bf(y[j + 4], y[j + 5]), pack_bf(y[j + 6], y[j + 7]));
+        for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<uint2 *>(dst + j) = make_uint2(pack_bf(y[j], y[j + 1]), pack_bf(y[j + 2], y[j + 3]));
     } else {
         float *dst = p.part + ((size_t)slotw * RT + row) * D + k;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
+        for (int j = 0; j < N; j += 4)
             *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
     }
 }
 
+// Slow path of a wait, out of line: every role has several waits.
+__device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, unsigned long long timeout_ns, int *err,
+                                         int *status) {
+    const bool ok = mbar_wait_bounded(bar, parity, timeout_ns);
+    if (!ok) {
+        *(volatile int *)err = 1;
+        report_timeout(status);
+    }
+    return ok && !*(volatile int *)err;
+}
+
 struct AttendShared {
-    uint64_t full8[8], empty8[8];   // ring slots: codes and exponents landed; read by all dequant warps
-    uint64_t k_full;                // the f16 keys of a tile are written
-    uint64_t v_full[2];
-    uint64_t s_full[2], s_empty[2]; // S written (and the f16 keys read); read by all softmax warps
-    uint64_t p_full;                // P written, O rescaled
+    uint64_t k_code[4], k_free[4];  // ring slots of key codes: landed; multiplied
+    uint64_t v_code[4], v_free[4];  // of value codes: landed; read by all dequant warps
+    uint64_t x_full[kExps], x_free[kExps];  // a tile's exponents (keys and values); read
+    uint64_t sf_full[2];            // a tile's key scales are in tensor memory
+    uint64_t v_full[2];             // the f16 values of a tile are written
+    uint64_t s_full[2];             // S written
+    uint64_t p_full[2];             // P written, O rescaled
     uint64_t pv_done[2];            // O updated, P and the f16 values read
-    uint64_t q_full;                // the segment's Q is in tensor memory
-    uint64_t soft;                  // the softmax warps' own barrier (bounded, unlike bar.sync)
+    uint64_t m_full[2][4];          // a softmax warp's rows have their maximum of the tile
+    uint64_t q_full;                // a segment's Q is in place
+    uint64_t soft, set[2];          // the softmax warps' own barriers (bounded, unlike bar.sync)
     uint32_t tmem;
     int err;
-    int vbits[8];                   // a slot's 16-key groups that exist (bit i)
-    int ek[kInfo], valid[kInfo];    // a tile's key exponent, its groups
+    int valid[kInfo];               // a tile's 16-key groups that exist (bit i)
     int ev[kInfo], vnan[kInfo];     // the segment's value exponent at the tile; a value block holds NaN
+    int care[kInfo];                // the tile's values need care: missing keys, NaN
     uint8_t nanblk[kInfo][128];     // then: each key's NaN blocks
-    float2 stat[4][32];
-    int scan[16];
+    float mrow[2][128];             // the rows' maxima, handed from set to set
+    float2 stat[kSoftWarps][32];
+    uint32_t nan[kSoftWarps][32];
+    int scan[32];
 };
 
 }  // namespace
@@ -343,8 +447,8 @@ struct AttendShared {
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     using S = Shape<D>;
-    constexpr int TN = S::TN, NS = S::NS, REP = 128 / RT, CPT = TN / REP;  // CPT: key columns a thread
-    constexpr int CH = CPT < 32 ? CPT : 32;                                // taken CH at a time
+    constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP;  // CPT: key columns a thread
+    constexpr int CH = CPT < 32 ? CPT : 32;                    // taken CH at a time
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
     __shared__ AttendShared s;
@@ -352,18 +456,24 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 8; ++i) {
-            mbar_init(&s.full8[i], 33);  // 32 lanes' exponent copies and lane 0's byte count
-            mbar_init(&s.empty8[i], kDeqWarps);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s.k_code[i], 1);
+            mbar_init(&s.k_free[i], 1);
+            mbar_init(&s.v_code[i], 1);
+            mbar_init(&s.v_free[i], kDeqWarps);
+            mbar_init(&s.x_full[i], 1);
+            mbar_init(&s.x_free[i], kDeqWarps);
+            mbar_init(&s.m_full[0][i], 1);
+            mbar_init(&s.m_full[1][i], 1);
         }
-        mbar_init(&s.k_full, kDeqWarps);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.sf_full[i], 4);
             mbar_init(&s.v_full[i], kDeqWarps);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.s_empty[i], kSoftWarps);
+            mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
+            mbar_init(&s.set[i], 4);
         }
-        mbar_init(&s.p_full, kSoftWarps);
         mbar_init(&s.q_full, kSoftWarps);
         mbar_init(&s.soft, kSoftWarps);
         s.err = 0;
@@ -410,332 +520,425 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const uint32_t tmem = s.tmem;
     const long long total = prefix[p.B];
     const int w0 = range_start(total, blockIdx.x), w1 = range_start(total, blockIdx.x + 1);
-    volatile int *const err = &s.err;
-    // A bounded wait by every lane; false when it ran out or another warp's did.
+    // A bounded wait of one thread; false when it ran out.
+    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        return wait_longer(bar, parity, p.timeout_ns, &s.err, p.status);
+    };
+    // The same by every lane of a warp.
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity);
-        if (!ok) ok = mbar_wait_bounded(bar, parity, p.timeout_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) {
-            *err = 1;
-            report_timeout(p.status);
+        return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
+    };
+
+    // A batch of BT tiles' 16-key groups, one a lane: the page of the lane's group (a load that stays
+    // in flight until the batch is used), then its cache row (head h), -1 if there is none.
+    constexpr int NSB = TN / 16, BT = 32 / NSB;
+    auto page_of = [&](const Segment &g, int tile) -> int {
+        const int tok = (tile + lane / NSB) * TN + 16 * (lane % NSB);
+        return tok < g.ctx + g.nodes ? p.c.table[(size_t)g.b * p.c.table_pages + tok / p.c.page_size] : -1;
+    };
+    auto row_of = [&](const Segment &g, int tile, int page) -> int {
+        const int tok = (tile + lane / NSB) * TN + 16 * (lane % NSB);
+        if (tok >= g.ctx + g.nodes) return -1;
+        if ((unsigned)page >= (unsigned)p.c.pages) {
+            report_index(p.status);
+            return -1;
         }
-        return ok && !*err;
+        return (page * p.c.heads + g.h) * p.c.page_size + tok % p.c.page_size;
     };
 
     if (warp == kProducerWarp) {
-        // ------------------------------------------------------------ producer
-        constexpr int NSB = TN / 16;             // 16-key groups a tile
-        constexpr int KPL = 16 / S::EB;          // keys of a lane's 16 exponent bytes
-        int slot = 0, n = 0;
-        uint32_t ph = 0;
+        // ------------------------------------------------------------ producer: codes
+        const int gpb = p.box_rows / 16;  // groups a box: boxes never cross a page's end
+        const bool lead = lane < NSB && lane % gpb == 0;
+        int tile = 0;
         bool ok = true;
-        // lane i < NSB: the cache row (head h) of the tile's 16-key group i, -1 if there is none
-        auto group_row = [&](const Segment &g, int tile) -> long long {
-            long long row = -1;
-            const int tok = tile * TN + 16 * lane;
-            if (lane < NSB && tok < g.ctx + g.nodes) {
-                const int pi = tok / p.c.page_size;
-                const int page = p.c.table[(size_t)g.b * p.c.table_pages + pi];
-                if ((unsigned)page < (unsigned)p.c.pages)
-                    row = ((long long)page * p.c.heads + g.h) * p.c.page_size + (tok - pi * p.c.page_size);
-                else
-                    report_index(p.status);
-            }
-            return row;
-        };
-        auto copy = [&](const uint8_t *codes, const uint8_t *exps, long long row) -> bool {
-            if (n >= S::NSLOT && !wait(&s.empty8[slot], ph ^ 1u)) return false;
-            const uint32_t there = __ballot_sync(0xFFFFFFFFu, row >= 0);
-            const long long prev = __shfl_up_sync(0xFFFFFFFFu, row, 1);
-            const bool follows = lane > 0 && row >= 0 && prev >= 0 && prev + 16 == row;
-            const uint32_t fol = __ballot_sync(0xFFFFFFFFu, follows);
-            uint64_t *const bar = &s.full8[slot];
-            if (lane == 0) {
-                s.vbits[slot] = (int)there;
-                mbar_arrive_expect_tx(bar, (uint32_t)__popc(there) * 16u * D);
-            }
-            __syncwarp();
-            if (!p.skip_loads && row >= 0 && !follows) {  // the first group of a contiguous run
-                const int run = 1 + __ffs(~(fol >> (lane + 1))) - 1;
-                bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, codes + (size_t)row * D,
-                         (uint32_t)(run * 16 * D), bar);
-            }
-            const int key = lane * KPL;
-            const long long erow = __shfl_sync(0xFFFFFFFFu, row, min(key / 16, 31));
-            if (key < TN && erow >= 0) {
-                const uint8_t *src = exps + ((size_t)erow + (key & 15)) * S::EB;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                 smem_u32(base + S::oExp + slot * 512 + lane * 16)),
-                             "l"(src)
-                             : "memory");
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-            ++n;
-            if (++slot == S::NSLOT) {
-                slot = 0;
-                ph ^= 1u;
-            }
-            return true;
-        };
         for (int pos = w0; pos < w1 && ok;) {
             const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
             const int tiles = g.kv1 - g.kv0;
-            long long row = group_row(g, g.kv0), next = -1;
-            ok = copy(p.c.k8, p.c.kexp, row);
-            for (int i = 0; i < tiles && ok; ++i) {
-                if (i + 1 < tiles) {
-                    next = group_row(g, g.kv0 + i + 1);
-                    ok = copy(p.c.k8, p.c.kexp, next);
+            int page = page_of(g, g.kv0), rows = -1;
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                const int j = i % BT;
+                if (j == 0) {
+                    rows = row_of(g, g.kv0 + i, page);
+                    page = page_of(g, g.kv0 + i + BT);
                 }
-                ok = ok && copy(p.c.v8, p.c.vexp, row);
-                row = next;
+                const int row = __shfl_sync(0xFFFFFFFFu, rows, (j * NSB + lane) & 31);
+                const bool go = lead && row >= 0;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, go)) * (uint32_t)(p.box_rows * D);
+                const int slot = tile % S::NSLOT;
+                const uint32_t fph = (uint32_t)((tile / S::NSLOT) & 1) ^ 1u;
+                ok = tile < S::NSLOT || wait(&s.k_free[slot], fph);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&s.k_code[slot], bytes);
+                __syncwarp();
+                if (go && !p.skip_loads)
+#pragma unroll
+                    for (int c = 0; c < D; c += 128)  // 128-byte columns of the tile, one after another
+                        tma_rows(base + S::oK + slot * S::SLOT + c * TN + lane * 16 * (D < 128 ? D : 128), &p.kmap, c, row,
+                                 &s.k_code[slot]);
+                ok = tile < S::NSLOT || wait(&s.v_free[slot], fph);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&s.v_code[slot], bytes);
+                __syncwarp();
+                if (go && !p.skip_loads)
+                    bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
+                             (uint32_t)(p.box_rows * D), &s.v_code[slot]);
             }
             pos += tiles;
         }
         // every copy must have landed before the block's memory goes away (bounded)
-        asm volatile("cp.async.wait_all;" ::: "memory");
         if (!p.skip_loads)
-            for (int i = max(0, n - S::NSLOT); i < n; ++i)
-                (void)mbar_wait_bounded(&s.full8[i % S::NSLOT], (uint32_t)((i / S::NSLOT) & 1), p.timeout_ns);
-    } else if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMA issue
-        constexpr uint32_t idS = idesc_a(TN, false), idO = idesc_a(D, true);
-        const uint32_t sK = smem_u32(base + S::oK), sV = smem_u32(base + S::oV);
-        int ik = 0, iv = 0, seg = 0;  // tiles of the block so far
-        bool ok = true;
-        auto issue_s = [&]() -> bool {
-            if (!wait(&s.k_full, (uint32_t)(ik & 1))) return false;
-            const int sb = ik % NS;
-            if (ik >= NS && !wait(&s.s_empty[sb], (uint32_t)(((ik / NS) & 1) ^ 1))) return false;
-            fence_after();
-            if (lane == 0) {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)  // channels: 64-channel column ks / 4, then 32 bytes a step
-                    umma_a(tmem + S::CS + sb * TN, tmem + S::CQ + 8 * ks,
-                           desc_a(sK + (ks >> 2) * (TN * 128), 16) + 2 * (ks & 3), idS, ks > 0);
-                commit_a(&s.s_full[sb]);
+            for (int i = max(0, tile - S::NSLOT); i < tile + (ok ? 0 : 1); ++i) {
+                const int slot = i % S::NSLOT;
+                const uint32_t iph = (uint32_t)((i / S::NSLOT) & 1);
+                (void)mbar_wait_bounded(&s.k_code[slot], iph, ok ? p.timeout_ns : 100000000ull);
+                (void)mbar_wait_bounded(&s.v_code[slot], iph, ok ? p.timeout_ns : 100000000ull);
             }
-            __syncwarp();
-            ++ik;
-            return true;
-        };
-        for (int pos = w0; pos < w1 && ok; ++seg) {
+    } else if (warp == kScoutWarp) {
+        // ------------------------------------------------------------ scout: exponents and flags
+        constexpr int KPL = 16 / S::EB;  // keys of a lane's 16 exponent bytes
+        const int key0 = lane * KPL;
+        int tile = 0;
+        bool ok = true;
+        for (int pos = w0; pos < w1 && ok;) {
             const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
             const int tiles = g.kv1 - g.kv0;
-            ok = wait(&s.q_full, (uint32_t)(seg & 1)) && issue_s();
-            for (int i = 0; i < tiles && ok; ++i) {
-                if (i + 1 < tiles) ok = issue_s();
-                ok = ok && wait(&s.v_full[iv & 1], (uint32_t)((iv >> 1) & 1)) && wait(&s.p_full, (uint32_t)(iv & 1));
+            int E = 0;  // the largest value exponent of the segment so far
+            int page = page_of(g, g.kv0), rows = -1;
+            uint4 kx = make_uint4(0, 0, 0, 0), vx = kx, kn = kx, vn = kx;
+            uint32_t vb = 0, vbn = 0;
+            // starts the loads of tile i's exponents
+            auto load = [&](int i) {
+                const int j = i % BT;
+                if (j == 0) {
+                    rows = row_of(g, g.kv0 + i, page);
+                    page = page_of(g, g.kv0 + i + BT);
+                }
+                const int row = __shfl_sync(0xFFFFFFFFu, rows, (j * NSB + lane) & 31);
+                vbn = __ballot_sync(0xFFFFFFFFu, lane < NSB && row >= 0);
+                const int krow = __shfl_sync(0xFFFFFFFFu, rows, (j * NSB + (key0 >> 4)) & 31);
+                kn = vn = make_uint4(0, 0, 0, 0);
+                if (key0 < TN && krow >= 0) {
+                    const size_t at = ((size_t)krow + (key0 & 15)) * S::EB;
+                    kn = *reinterpret_cast<const uint4 *>(p.c.kexp + at);
+                    vn = *reinterpret_cast<const uint4 *>(p.c.vexp + at);
+                }
+            };
+            load(0);
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                kx = kn;
+                vx = vn;
+                vb = vbn;
+                if (i + 1 < tiles) load(i + 1);
+                const int xs = tile % kExps, info = tile % kInfo;
+                ok = tile < kExps || wait(&s.x_free[xs], (uint32_t)((tile / kExps) & 1) ^ 1u);
                 if (!ok) break;
-                fence_after();
+                uint8_t *const ex = base + S::oExp + xs * 1024;  // keys', then values'
+                if (key0 < TN) {
+                    *reinterpret_cast<uint4 *>(ex + lane * 16) = kx;
+                    *reinterpret_cast<uint4 *>(ex + 512 + lane * 16) = vx;
+                }
+                // the largest value exponent of the keys that exist, 255 (NaN) left out
+                const int keys = min(TN, g.ctx + g.nodes - (g.kv0 + i) * TN);
+                const bool part = keys < TN || vb != (1u << NSB) - 1u;
+                uint4 v = vx;
+                if (part) {
+                    const int bytes = (vb >> (key0 >> 4)) & 1 ? (keys - key0) * S::EB : 0;
+                    v.x &= low_bits(8 * bytes);
+                    v.y &= low_bits(8 * bytes - 32);
+                    v.z &= low_bits(8 * bytes - 64);
+                    v.w &= low_bits(8 * bytes - 96);
+                }
+                uint32_t mx = __vmaxu4(__vmaxu4(v.x, v.y), __vmaxu4(v.z, v.w));
+                const bool nan = __any_sync(0xFFFFFFFFu, __vcmpeq4(mx, 0xFFFFFFFFu) != 0);
+                if (nan) {
+                    auto drop = [](uint32_t x) { return x & ~__vcmpeq4(x, 0xFFFFFFFFu); };
+                    mx = __vmaxu4(__vmaxu4(drop(v.x), drop(v.y)), __vmaxu4(drop(v.z), drop(v.w)));
+                }
+                mx = __vmaxu4(mx, mx >> 16);
+                E = max(E, (int)__reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu)));
+                __syncwarp();
+                if (nan)
+                    for (int key = lane; key < TN; key += 32) {
+                        uint32_t m = 0;
+                        for (int j = 0; j < S::EB; ++j) m |= (ex[512 + key * S::EB + j] == 255 ? 1u : 0u) << j;
+                        s.nanblk[info][key] = (uint8_t)m;
+                    }
                 if (lane == 0) {
-#pragma unroll
-                    for (int ks = 0; ks < TN / 16; ++ks)  // 16 keys a step: two 8-key atoms
-                        umma_a(tmem + S::CO, tmem + S::CP + 8 * ks,
-                               desc_a(sV + (iv & 1) * S::F16 + ks * 2048, TN * 128), idO, i > 0 || ks > 0);
-                    commit_a(&s.pv_done[iv & 1]);
+                    s.valid[info] = (int)vb;
+                    s.ev[info] = E;
+                    s.vnan[info] = nan;
+                    s.care[info] = nan || part;
                 }
                 __syncwarp();
-                ++iv;
+                if (lane == 0) mbar_arrive(&s.x_full[xs]);
             }
             pos += tiles;
         }
-        // the last products must be done before tensor memory goes back (bounded)
-        if (iv > 0) (void)wait(&s.pv_done[(iv - 1) & 1], (uint32_t)(((iv - 1) >> 1) & 1));
-        if (ik > 0) (void)wait(&s.s_full[(ik - 1) % NS], (uint32_t)(((ik - 1) / NS) & 1));
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue: a thread a product
+        // One thread issues an MMA about every 100 cycles whatever its size (to N = 128); two with
+        // an accumulator each, one every 64.
+        const bool value = warp > kMmaWarp;
+        int tile = 0, seg = 0;  // of the block so far
+        bool ok = true;
+        if (lane == 0) {
+            for (int pos = w0; pos < w1 && ok; ++seg) {
+                const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
+                const int tiles = g.kv1 - g.kv0;
+                if (!value) ok = wait1(&s.q_full, (uint32_t)(seg & 1));
+                for (int i = 0; i < tiles && ok; ++i, ++tile) {
+                    const int buf = tile & 1;
+                    const uint32_t bph = (uint32_t)((tile >> 1) & 1);
+                    const uint32_t sp = tmem + S::CS + buf * TN;
+                    if (value) {
+                        ok = wait1(&s.v_full[buf], bph) && wait1(&s.p_full[buf], bph);
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t src = smem_u32(base + S::oV) + buf * S::F16;
+#pragma unroll
+                        for (int ks = 0; ks < TN / 16; ++ks)  // 16 keys a step: two 8-key atoms
+                            umma_a(tmem + S::CO, sp + 8 * ks, desc_a(src + ks * 2048, TN * 128), idesc_a(D, true),
+                                   i > 0 || ks > 0);
+                        commit_a(&s.pv_done[buf]);
+                    } else {
+                        const int slot = tile % S::NSLOT;
+                        // S takes the place of the P of two tiles before
+                        ok = wait1(&s.k_code[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait1(&s.sf_full[buf], bph) &&
+                             (tile < 2 || wait1(&s.pv_done[buf], bph ^ 1u));
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t src = smem_u32(base + S::oK) + slot * S::SLOT;
+                        const uint32_t sfb = tmem + S::CB + 4 * buf;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)  // Q's upper and lower parts
+#pragma unroll
+                            for (int ks = 0; ks < D / 32; ++ks) {  // 32 channels a step
+                                const uint64_t bd = desc_codes<(D < 128 ? 64 : 128)>(src + (ks >> 2) * (TN * 128)) + 2 * (ks & 3);
+                                const uint32_t id = idesc_mx(TN, part, ks & 3), fb = sfb + 2 * (ks >> 2);
+                                if constexpr (S::QS)
+                                    umma_mx_ss(sp,
+                                               desc_codes<128>(smem_u32(base + S::oQ) + part * (128 * D) + (ks >> 2) * (128 * 128)) +
+                                                   2 * (ks & 3),
+                                               bd, id, tmem + S::CA, fb, part + ks > 0);
+                                else
+                                    umma_mx_ts(sp, tmem + S::CQ + part * (D / 4) + 8 * ks, bd, id, tmem + S::CA, fb,
+                                               part + ks > 0);
+                            }
+                        commit_a(&s.s_full[buf]);
+                        commit_a(&s.k_free[slot]);
+                    }
+                }
+                pos += tiles;
+            }
+            // the last products must be done before tensor memory goes back (bounded)
+            if (tile > 0)
+                (void)wait1(value ? &s.pv_done[(tile - 1) & 1] : &s.s_full[(tile - 1) & 1],
+                            (uint32_t)(((tile - 1) >> 1) & 1));
+        }
     } else if (warp >= kSoftWarps) {
-        // ------------------------------------------------------------ dequant
+        // ------------------------------------------------------------ values to f16; key scales
         const int dw = warp - kSoftWarps;
         constexpr int NQ = D / 64, RPW = TN / kDeqWarps, PASSES = RPW / 8 * NQ;
-        int slot = 0, ik = 0, iv = 0;
-        uint32_t ph = 0;
+        int kt = 0, vt = 0;  // tiles of the block so far: key scales, values
         bool ok = true;
         // Conflict-free on both sides: in a quarter-warp, four 16-code chunks of an even row and
         // four of the next row from another 64-channel column (other banks in the codes; odd
         // against even 16-byte units in the swizzled f16 rows).
-        const int ci = lane & 3, cj = (lane >> 2) & 1, cr = 2 * (lane >> 3) + cj;
-        auto turn = [&](uint8_t *dst, int E, bool check, int keys, uint32_t vbits, bool value) {
-            const uint8_t *src = base + S::oRing + slot * S::SLOT;
-            const uint8_t *ex = base + S::oExp + slot * 512;
-#pragma unroll
-            for (int ps = 0; ps < PASSES; ++ps) {
-                const int row = dw * RPW + (ps / NQ) * 8 + cr, ch = ci + 4 * ((cj + ps) % NQ);
-                uint4 w = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
-                const int e = ex[row * S::EB + (ch >> 1)];
-                if (check && value && (row >= keys || !((vbits >> (row >> 4)) & 1) || e == 255)) w = make_uint4(0, 0, 0, 0);
-                const uint32_t sc = f16_pow2(e - E + kShift);
-                uint4 lo, hi;
-                widen16(w, check && value && w.x == 0 && w.y == 0 && w.z == 0 && w.w == 0 ? 0u : sc, lo, hi);
-                uint8_t *d = dst + (ch >> 2) * (TN * 128) + row * 128;
-                const int u = 2 * (ch & 3), x = row & 7;
-                *reinterpret_cast<uint4 *>(d + ((u ^ x) << 4)) = lo;
-                *reinterpret_cast<uint4 *>(d + (((u + 1) ^ x) << 4)) = hi;
-            }
-        };
-        // The largest exponent byte of the tile's keys that exist, 255 (NaN) left out; bit 8: a 255
-        // was among them.
-        auto tile_exponent = [&](int keys, uint32_t vbits) -> int {
-            constexpr int KPL = 16 / S::EB;
-            const int key0 = lane * KPL;
-            uint32_t mx = 0, nan = 0;
-            if (key0 < TN) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(base + S::oExp + slot * 512 + lane * 16);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t x = w[j];
-                    uint32_t keep = 0;  // byte mask of keys that exist
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0 + (4 * j + i) / S::EB;
-                        if (key < keys && ((vbits >> (key >> 4)) & 1)) keep |= 0xFFu << (8 * i);
-                    }
-                    x &= keep;
-                    const uint32_t is = __vcmpeq4(x, 0xFFFFFFFFu);
-                    nan |= is;
-                    mx = __vmaxu4(mx, x & ~is);
-                }
-            }
-            mx = __vmaxu4(mx, mx >> 16);
-            mx = max(mx & 0xFFu, (mx >> 8) & 0xFFu);
-            mx = __reduce_max_sync(0xFFFFFFFFu, mx);
-            return (int)mx | (__any_sync(0xFFFFFFFFu, nan != 0) ? 256 : 0);
-        };
-        auto release = [&]() {  // the slot is read; the f16 tile is on its way to the async proxy
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.empty8[slot]);
-            if (++slot == S::NSLOT) {
-                slot = 0;
-                ph ^= 1u;
-            }
-        };
-        auto keys_tile = [&](const Segment &g, int tile) -> bool {
-            if (!wait(&s.full8[slot], ph)) return false;
-            if (ik > 0 && !wait(&s.s_full[(ik - 1) % NS], (uint32_t)(((ik - 1) / NS) & 1))) return false;
-            const int keys = min(TN, g.ctx + g.nodes - tile * TN);
-            const uint32_t vb = (uint32_t)s.vbits[slot];
-            const int E = tile_exponent(keys, vb) & 255;
-            turn(base + S::oK, E, false, keys, vb, false);
-            if (dw == 0 && lane == 0) {
-                s.ek[ik % kInfo] = E;
-                s.valid[ik % kInfo] = (int)vb;
-            }
-            release();
-            if (lane == 0) mbar_arrive(&s.k_full);
-            ++ik;
-            return true;
-        };
+        const int ci = lane & 3, cj = (lane >> 2) & 1, cr = dw * RPW + 2 * (lane >> 3) + cj;
         for (int pos = w0; pos < w1 && ok;) {
             const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
             const int tiles = g.kv1 - g.kv0;
-            int EV = 0;  // the segment's running value exponent
-            ok = keys_tile(g, g.kv0);
-            for (int i = 0; i < tiles && ok; ++i) {
-                if (i + 1 < tiles) ok = keys_tile(g, g.kv0 + i + 1);
-                ok = ok && wait(&s.full8[slot], ph);
-                if (ok && iv >= 2) ok = wait(&s.pv_done[iv & 1], (uint32_t)(((iv >> 1) & 1) ^ 1));
-                if (!ok) break;
-                const int keys = min(TN, g.ctx + g.nodes - (g.kv0 + i) * TN);
-                const uint32_t vb = (uint32_t)s.vbits[slot];
-                const int te = tile_exponent(keys, vb);
-                const bool nan = te >= 256;
-                EV = max(EV, te & 255);
-                const bool check = nan || keys < TN || vb != (1u << (TN / 16)) - 1u;
-                uint8_t *dst = base + S::oV + (iv & 1) * S::F16;
-                if (check) turn(dst, EV, true, keys, vb, true);
-                else turn(dst, EV, false, keys, vb, true);
-                if (nan && dw == 0) {
-                    const uint8_t *ex = base + S::oExp + slot * 512;
-                    for (int key = lane; key < TN; key += 32) {
-                        uint32_t m = 0;
-                        for (int j = 0; j < S::EB; ++j) m |= (ex[key * S::EB + j] == 255 ? 1u : 0u) << j;
-                        s.nanblk[iv % kInfo][key] = (uint8_t)m;
+            for (int i = -1; i < tiles; ++i) {
+                if (i + 1 < tiles) {
+                    if (dw < 4) {  // a warp a quarter of tensor memory's lanes: each holds all scales
+                        const int xs = kt % kExps;
+                        ok = wait(&s.x_full[xs], (uint32_t)((kt / kExps) & 1)) &&
+                             (kt < 2 || wait(&s.s_full[kt & 1], (uint32_t)((kt >> 1) & 1) ^ 1u));
+                        if (!ok) break;
+                        fence_after();
+                        const uint8_t *ex = base + S::oExp + xs * 1024;
+                        uint32_t f[4];  // column c: keys 32 c + lane (dim 256: keys 32 (c % 2) + lane, word c / 2)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            f[c] = D == 64    ? *reinterpret_cast<const uint16_t *>(ex + (32 * c + lane) * 2)
+                                   : D == 128 ? *reinterpret_cast<const uint32_t *>(ex + (32 * c + lane) * 4)
+                                              : *reinterpret_cast<const uint32_t *>(ex + (32 * (c & 1) + lane) * 8 + 4 * (c >> 1));
+                        st_cols(tmem + ((uint32_t)(32 * dw) << 16) + S::CB + 4 * (kt & 1), f);
+                        wait_st();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.sf_full[kt & 1]);
                     }
-                    __syncwarp();
+                    ++kt;
                 }
-                if (dw == 0 && lane == 0) {
-                    s.ev[iv % kInfo] = EV;
-                    s.vnan[iv % kInfo] = nan ? 1 : 0;
+                if (i < 0) continue;
+                const int slot = vt % S::NSLOT, xs = vt % kExps, buf = vt & 1, info = vt % kInfo;
+                ok = wait(&s.x_full[xs], (uint32_t)((vt / kExps) & 1)) &&
+                     wait(&s.v_code[slot], (uint32_t)((vt / S::NSLOT) & 1)) &&
+                     (vt < 2 || wait(&s.pv_done[buf], (uint32_t)((vt >> 1) & 1) ^ 1u));
+                if (!ok) break;
+                const uint8_t *src = base + S::oRing + slot * S::SLOT, *ex = base + S::oExp + xs * 1024 + 512;
+                uint8_t *dst = base + S::oV + buf * S::F16;
+                const int E = s.ev[info] - kShift;
+                uint4 w[PASSES];
+                int e[PASSES];
+#pragma unroll
+                for (int ps = 0; ps < PASSES; ++ps) {  // every load before the first store
+                    const int row = cr + (ps / NQ) * 8, ch = ci + 4 * ((cj + ps) % NQ);
+                    w[ps] = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
+                    e[ps] = ex[row * S::EB + (ch >> 1)];
                 }
-                release();
-                if (lane == 0) mbar_arrive(&s.v_full[iv & 1]);
-                ++iv;
+                if (s.care[info]) {  // missing keys and NaN blocks count as zeros
+                    const int keys = g.ctx + g.nodes - (g.kv0 + i) * TN;
+                    const uint32_t vb = (uint32_t)s.valid[info];
+#pragma unroll
+                    for (int ps = 0; ps < PASSES; ++ps) {
+                        const int row = cr + (ps / NQ) * 8;
+                        if (row >= keys || !((vb >> (row >> 4)) & 1) || e[ps] == 255) {
+                            w[ps] = make_uint4(0, 0, 0, 0);
+                            e[ps] = 0;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int ps = 0; ps < PASSES; ++ps) {
+                    const int row = cr + (ps / NQ) * 8, ch = ci + 4 * ((cj + ps) % NQ);
+                    uint4 lo, hi;
+                    widen16(w[ps], f16_pow2(e[ps] - E), lo, hi);
+                    uint8_t *d = dst + (ch >> 2) * (TN * 128) + row * 128;
+                    const int u = 2 * (ch & 3), x = row & 7;
+                    *reinterpret_cast<uint4 *>(d + ((u ^ x) << 4)) = lo;
+                    *reinterpret_cast<uint4 *>(d + (((u + 1) ^ x) << 4)) = hi;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // f16 for the MMA's reads
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&s.v_full[buf]);
+                    mbar_arrive(&s.v_free[slot]);
+                    mbar_arrive(&s.x_free[xs]);
+                }
+                ++vt;
             }
             pos += tiles;
         }
     } else {
         // ------------------------------------------------------------ softmax and output
-        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);  // this warp's tensor memory lanes
-        const int row = (32 * warp + lane) % RT;                   // row of the tile
-        const int col0 = (32 * warp / RT) * CPT;                   // this copy's key columns
+        const int set = warp >> 2, quad = warp & 3;                // tiles of one parity; tensor memory lanes
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+        const int row = (32 * quad + lane) % RT;                   // row of the tile
+        const int copy = 32 * quad / RT, col0 = copy * CPT;        // this copy's key columns
         int it = 0;
-        uint32_t soft_ph = 0;
+        uint32_t soft_ph = 0, set_ph = 0;
         bool ok = true;
-        auto soft_sync = [&]() -> bool {
+        auto soft_sync = [&]() -> bool {  // all softmax warps
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.soft);
             soft_ph ^= 1u;
             return wait(&s.soft, soft_ph ^ 1u);
         };
-        {   // P is zero outside each copy's columns, once and for all
-            const uint32_t z[16] = {};
-            if (REP > 1) {
-#pragma unroll
-                for (int c = 0; c < TN / 2; c += 16) st_cols(tl + S::CP + c, z);
-                wait_st();
-            }
-        }
-        for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
-            const int tiles = g.kv1 - g.kv0;
-            const int r = g.rt * RT + row;         // row of the request and head
+        auto set_sync = [&]() -> bool {   // the set's four
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.set[set]);
+            set_ph ^= 1u;
+            return wait(&s.set[set], set_ph ^ 1u);
+        };
+        // A segment's Q: each row scaled by a power of two 2^-eq so that its largest lies in
+        // [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4 (its scale is 2^-4).  Exact
+        // for bf16 values within 2^14 of the row's largest, else off by at most 2^-22 of that.  The
+        // sets take half of the channels each.
+        auto put_q = [&](const Segment &g) -> int {
+            const int r = g.rt * RT + row;
             const bool real = r < g.nodes * p.g;
             const int t = real ? r / p.g : 0, hq = g.h * p.g + (real ? r - t * p.g : 0);
-            // ---- Q: the row scaled by a power of two so that its largest lies in [2^13, 2^14)
             const uint16_t *qr = p.q + ((size_t)g.b * p.T + t) * p.ldq + (size_t)hq * D;
             uint32_t am = 0;
             if (real)
+#pragma unroll 8
                 for (int c = 0; c < D; c += 8) {
                     const uint4 v = *reinterpret_cast<const uint4 *>(qr + c);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
                 }
-            const int eq = max((int)(am >> 7) - 127 - 13, -100);
-            const float qs = pow2i(-eq);  // eq <= 115
+            const int eq = max((int)(am >> 7) - 127 - 7, -100);
+            const float qs = pow2i(-eq);  // eq <= 121
 #pragma unroll 1
-            for (int c = 0; c < D; c += 64) {
-                uint32_t o[32];
+            for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 32) {
+                uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (real) v = *reinterpret_cast<const uint4 *>(qr + c + 8 * j);
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t h2[4], l2[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[4 * j + k] = pack_f16(__uint_as_float(w[k] << 16) * qs, __uint_as_float(w[k] & 0xFFFF0000u) * qs);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t x = pack_f16(__uint_as_float(w[k] << 16) * qs, __uint_as_float(w[k] & 0xFFFF0000u) * qs);
+                        h2[k] = f16_to_e4m3(x);
+                        l2[k] = f16_to_e4m3(f16x2_mul(f16x2_sub(x, e4m3_to_f16((uint16_t)h2[k])), 0x4C004C00u));  // * 16
+                    }
+                    hi[2 * j] = h2[0] | (h2[1] << 16);
+                    hi[2 * j + 1] = h2[2] | (h2[3] << 16);
+                    lo[2 * j] = l2[0] | (l2[1] << 16);
+                    lo[2 * j + 1] = l2[2] | (l2[3] << 16);
                 }
-                st_cols(tl + S::CQ + c / 2, o);
+                if constexpr (S::QS) {
+                    const int lr = 32 * quad + lane;  // rows of 128 channels, 128-byte swizzle
+                    uint8_t *d = base + S::oQ + (c >> 7) * (128 * 128) + lr * 128;
+                    const int u = (c & 127) >> 4, x = lr & 7;
+                    *reinterpret_cast<uint4 *>(d + ((u ^ x) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(d + (((u + 1) ^ x) << 4)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    *reinterpret_cast<uint4 *>(d + 128 * D + ((u ^ x) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    *reinterpret_cast<uint4 *>(d + 128 * D + (((u + 1) ^ x) << 4)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                } else {
+                    st_cols(tl + S::CQ + c / 4, hi);
+                    st_cols(tl + S::CQ + D / 4 + c / 4, lo);
+                }
             }
-            wait_st();
+            if constexpr (S::QS)
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            else
+                wait_st();
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.q_full);
-            const float crow = p.scale_log2 * pow2i(eq);
+            return eq;
+        };
+        {   // Q's scales: byte 0 (2^0) for the upper part, byte 1 (2^-4) for the lower
+            const uint32_t f[4] = {0x7B7Fu, 0x7B7Fu, 0x7B7Fu, 0x7B7Fu};
+            st_cols(tl + S::CA, f);  // both sets write the same
+            wait_st();
+        }
+        Segment next{};
+        int eq_next = 0;
+        for (int pos = w0; pos < w1 && ok;) {
+            if (pos == w0) {
+                next = segment_at<D, RT>(p, prefix, pos, w1);
+                eq_next = put_q(next);
+            }
+            const Segment g = next;
+            const int tiles = g.kv1 - g.kv0;
+            const int r = g.rt * RT + row;         // row of the request and head
+            const bool real = r < g.nodes * p.g;
+            const int t = real ? r / p.g : 0, hq = g.h * p.g + (real ? r - t * p.g : 0);
+            const float c = p.scale_log2 * pow2i(eq_next);  // S -> x
+            pos += tiles;
 
-            float m = -INFINITY, l = 0.0f;
-            int ev = 0;
+            float m = -INFINITY, l = 0.0f;  // of the set's tiles; l in units of 2^(m - bias)
             uint32_t nanblk = 0;
             const int32_t *mrow = p.mask ? p.mask + ((size_t)g.b * p.T + t) * p.W : nullptr;
             for (int i = 0; i < tiles && ok; ++i, ++it) {
-                const int sb = it % NS, info = it % kInfo;
-                ok = wait(&s.s_full[sb], (uint32_t)((it / NS) & 1));
+                if ((it & 1) != set) continue;
+                const int info = it % kInfo;
+                const uint32_t tph = (uint32_t)((it >> 1) & 1);
+                ok = wait(&s.s_full[set], tph);
                 if (!ok) break;
                 fence_after();
-                const uint32_t ts = tl + S::CS + sb * TN + col0;
-                const float c = crow * pow2i(s.ek[info] - 127 - kShift);  // S -> x
+                const uint32_t tb = tl + S::CS + set * TN, ts = tb + col0;
                 const int slot0 = (g.kv0 + i) * TN + col0;                // cache slot of the thread's first column
                 const uint32_t vb = (uint32_t)s.valid[info];
                 const bool masked = (g.kv0 + i + 1) * TN > g.ctx || vb != (1u << (TN / 16)) - 1u;
@@ -759,11 +962,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     w &= ((gb & 1u) ? 0x0000FFFFu : 0u) | ((gb & 2u) ? 0xFFFF0000u : 0u);
                     return CH < 32 ? w & ((1u << (CH & 31)) - 1u) : w;
                 };
-                // ---- the maximum
-                float mt = -INFINITY;
                 uint32_t x[CH];
-#pragma unroll
-                for (int k = 0; k < CPT; k += CH) {
+                auto load = [&](int k) {  // S of columns [k, k + CH), -inf where not seen
                     ld_cols(ts + k, x);
                     wait_ld();
                     if (masked) {
@@ -771,160 +971,196 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
 #pragma unroll
                         for (int j = 0; j < CH; ++j) x[j] = (w >> j) & 1u ? x[j] : 0xFF800000u;
                     }
+                };
+                // ---- the maximum, joined with that of the tiles before (the other set's last)
+                float mt = -INFINITY;
+#pragma unroll 1
+                for (int k = 0; k < CPT; k += CH) {
+                    load(k);
+                    float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) mt = fmaxf(mt, __uint_as_float(x[j]));
+                    for (int j = 0; j < CH; j += 4) {
+                        m0 = max3(m0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                        m1 = max3(m1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                    }
+                    mt = max3(mt, m0, m1);
                 }
                 mt = mt == -INFINITY ? mt : mt * c;
-                const bool grow = mt > m + kSlack;  // also out of m = -inf
-                const float mn = grow ? mt : m;
+                float mp = -INFINITY;
+                if (i > 0) {
+                    ok = wait(&s.m_full[set ^ 1][quad], (uint32_t)(((it - 1) >> 1) & 1));
+                    if (!ok) break;
+                    mp = s.mrow[set ^ 1][32 * quad + lane];
+                }
+                const bool grow = mt > mp + kSlack;  // also out of -inf
+                const float mn = grow ? mt : mp;
+                s.mrow[set][32 * quad + lane] = mn;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.m_full[set][quad]);
                 const float off = mn == -INFINITY ? 0.0f : kBias - mn;
-                // ---- p, its sum, and P for the second product
-                uint32_t pk[CPT / 2];
-                float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
+                const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                // ---- p, its sum, and P (over S; a chunk's P lands on columns already read)
+                uint64_t sum = pair(0.0f, 0.0f);
+#pragma unroll 1
                 for (int k = 0; k < CPT; k += CH) {
-                    if (CPT > CH) {
-                        ld_cols(ts + k, x);
-                        wait_ld();
-                        if (masked) {
-                            const uint32_t w = seen(k);
-#pragma unroll
-                            for (int j = 0; j < CH; ++j) x[j] = (w >> j) & 1u ? x[j] : 0xFF800000u;
-                        }
-                    }
+                    if (CPT > CH) load(k);
+                    uint32_t pk[CH / 2];
 #pragma unroll
                     for (int j = 0; j < CH; j += 2) {
-                        const float a = ex2(fmaf(__uint_as_float(x[j]), c, off));
-                        const float b = ex2(fmaf(__uint_as_float(x[j + 1]), c, off));
-                        sum0 += a;
-                        sum1 += b;
-                        pk[(k + j) / 2] = pack_f16(a, b);
+                        float a, b;
+                        fma2(a, b, x[j], x[j + 1], c2, off2);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum = add2(sum, pair(a, b));
+                        pk[j / 2] = pack_f16(a, b);
                     }
+                    st_cols(tb + (col0 + k) / 2, pk);
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.s_empty[sb]);
-                // ---- the values' exponent; the product before this one must be done with P and O
-                ok = wait(&s.v_full[it & 1], (uint32_t)((it >> 1) & 1));
-                if (ok && it > 0) ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
-                if (!ok) break;
-                fence_after();
-                const int evn = s.ev[info];
-                const float fm = grow ? (m == -INFINITY ? 0.0f : ex2(m - mn)) : 1.0f;
-                if (i > 0 && __any_sync(0xFFFFFFFFu, grow || evn != ev)) {
-                    const float f = fm * pow2i(max(ev - evn, -149));
-#pragma unroll 1
-                    for (int k = 0; k < D; k += 32) {
-                        uint32_t o[32];
-                        ld_cols(tl + S::CO + k, o);
-                        wait_ld();
+                if constexpr (REP > 1) {  // the copy's P is zero at the other copies' keys
+                    const uint32_t z[CPT / 2] = {};
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        st_cols(tl + S::CO + k, o);
+                    for (int q = 0; q < REP; ++q)
+                        if (q != copy) st_cols(tb + q * (CPT / 2), z);
+                }
+                // ---- O in the units of the new maximum and value exponent
+                ok = wait(&s.v_full[set], tph);
+                if (!ok) break;
+                if (i > 0) {
+                    const int evp = s.ev[(it - 1) % kInfo], evn = s.ev[info];
+                    if (__any_sync(0xFFFFFFFFu, grow || evn != evp)) {
+                        ok = wait(&s.pv_done[set ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
+                        if (!ok) break;
+                        fence_after();
+                        const float f = (grow ? (mp == -INFINITY ? 0.0f : ex2(mp - mn)) : 1.0f) * pow2i(max(evp - evn, -149));
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            ld_cols(tl + S::CO + k, o);
+                            wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            st_cols(tl + S::CO + k, o);
+                        }
                     }
                 }
-                ev = evn;
-                l = l * fm + (sum0 + sum1);
+                l = l * (mn == m ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn)) + sum_pair(sum);
                 m = mn;
                 if (s.vnan[info]) {
 #pragma unroll 1
                     for (int k = 0; k < CPT; k += CH) {
-                        uint32_t w = real ? (masked ? seen(k) : 0xFFFFFFFFu) : 0u;
+                        const uint32_t w = real ? (masked ? seen(k) : 0xFFFFFFFFu) : 0u;
                         for (int j = 0; j < CH; ++j)
                             if ((w >> j) & 1u) nanblk |= s.nanblk[info][col0 + k + j];
                     }
                 }
-                st_part(tl + S::CP + col0 / 2, pk);
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full);
+                if (lane == 0) mbar_arrive(&s.p_full[set]);
             }
-            pos += tiles;
             if (!ok) break;
-            // ---- the segment's output
+            if (pos < w1) {  // the next segment's Q, once this one's last S is there
+                next = segment_at<D, RT>(p, prefix, pos, w1);
+                ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                eq_next = put_q(next);
+            }
+            // ---- the segment's output; the sets take half of the channels each
             ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
             if (!ok) break;
             fence_after();
+            const int ev = s.ev[(it - 1) % kInfo];
+            s.stat[warp][lane] = make_float2(m, l);
+            s.nan[warp][lane] = nanblk;
+            ok = soft_sync();
+            if (!ok) break;
+            // a copy's maximum is the later of its two sets'; copies and sets are added in order
+            float M = -INFINITY, mc = -INFINITY, L = 0.0f;
+#pragma unroll
+            for (int q = 0; q < REP; ++q) {
+                const int w = q * (RT / 32) + quad % (RT / 32);
+                M = max3(M, s.stat[w][lane].x, s.stat[w + 4][lane].x);
+            }
+#pragma unroll
+            for (int q = 0; q < 2 * REP; ++q) {
+                const float2 st = s.stat[(q >> 1) * (RT / 32) + quad % (RT / 32) + 4 * (q & 1)][lane];
+                L += st.y == 0.0f ? 0.0f : st.y * ex2(st.x == -INFINITY ? 0.0f : st.x - M);
+            }
+            mc = fmaxf(s.stat[quad][lane].x, s.stat[quad + 4][lane].x);
+            nanblk = s.nan[quad][lane] | s.nan[quad + 4][lane];
+            const bool any = s.stat[quad][lane].y != 0.0f || s.stat[quad + 4][lane].y != 0.0f;
             const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
             const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
-            float M = m, L = l;
-            if (REP > 1) {  // the copies' maxima and sums
-                s.stat[warp][lane] = make_float2(m, l);
-                ok = soft_sync();
-                if (!ok) break;
-                M = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < REP; ++q) M = fmaxf(M, s.stat[(warp + q * (RT / 32)) & 3][lane].x);
-                L = 0.0f;
-#pragma unroll
-                for (int q = 0; q < REP; ++q) {  // in the order of the copies
-                    const float2 st = s.stat[(q * (RT / 32) + warp % (RT / 32)) & 3][lane];
-                    L += st.y == 0.0f ? 0.0f : st.y * ex2(st.x == -INFINITY ? 0.0f : st.x - M);
-                }
-            }
-            // O (this copy) * f = its share of the normalised output
-            const float f = L == 0.0f ? 0.0f : (l == 0.0f ? 0.0f : ex2(m == -INFINITY ? 0.0f : m - M)) / L;
+            // O (this copy) * f * fv = its share of the normalised output
+            const float f = any ? ex2(mc == -INFINITY ? 0.0f : mc - M) / L : 0.0f;
             const float fv = pow2i(ev - 127 - kShift);
-            const float Lt = L * pow2i(-(int)kBias);  // the sum in units of 2^M
-            if (real && row < RT && 32 * warp < RT) {
-                if (whole) {
-                    if (p.lse)
-                        p.lse[((size_t)g.b * p.T + t) * p.Hq + hq] =
-                            L == 0.0f ? -INFINITY : (M + log2f(Lt)) * 0.69314718055994531f;
-                } else {
-                    p.stat[(size_t)slotw * RT + row] = make_float2(M, Lt);
-                }
-            }
-            float *const stage = reinterpret_cast<float *>(base + S::oStage);
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-                uint32_t o[32];
+            auto share = [&](int k, float (&y)[16]) {  // of channels [k, k + 16)
+                uint32_t o[16];
                 ld_cols(tl + S::CO + k, o);
                 wait_ld();
                 const bool bad = (nanblk >> (k / 32)) & 1u;
-                float y[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    y[j] = bad ? __uint_as_float(0x7FC00000u) : L == 0.0f ? 0.0f : __uint_as_float(o[j]) * f * fv;
-                if (REP == 1) {
+                for (int j = 0; j < 16; ++j)
+                    y[j] = bad ? __uint_as_float(0x7FC00000u) : any ? __uint_as_float(o[j]) * f * fv : 0.0f;
+            };
+            const float Lt = L * pow2i(-(int)kBias);  // the sum in units of 2^M
+            if (set == 0 && copy == 0 && real) {
+                if (!whole)
+                    p.stat[(size_t)slotw * RT + row] = make_float2(M, Lt);
+                else if (p.lse)
+                    p.lse[((size_t)g.b * p.T + t) * p.Hq + hq] =
+                        L == 0.0f ? -INFINITY : (M + log2f(Lt)) * 0.69314718055994531f;
+            }
+            if constexpr (REP == 1) {
+#pragma unroll 1
+                for (int k = set * (D / 2); k < (set + 1) * (D / 2); k += 16) {
+                    float y[16];
+                    share(k, y);
                     if (real) store_row<RT, D>(p, g, whole, slotw, row, t, hq, k, y);
-                } else {
+                }
+            } else {
+                // through shared memory, W channels of the real rows of every copy at a time (padded to
+                // W + 1 floats a row); then a thread takes four channels of a row, the copies in order
+                float *const stage = reinterpret_cast<float *>(base + S::oStage) + set * (128 * 17);
+                const int rows = min(RT, g.nodes * p.g - g.rt * RT);
+                const int W = rows * REP <= 32 ? 64 : rows * REP <= 64 ? 32 : 16;
+                const int W1 = W + 1, W4 = W / 4, own = 32 * quad + lane;
+                const int c1 = (set + 1) * (D / 2);
+                for (int k0 = set * (D / 2); k0 < c1; k0 += W) {
+                    const int wd = min(W, c1 - k0);
+#pragma unroll 1
+                    for (int k = 0; k < wd; k += 16) {
+                        float y[16];
+                        share(k0 + k, y);
+                        if (row < rows)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) stage[(warp * 32 + lane) * 33 + j] = y[j];
-                    ok = soft_sync();
+                            for (int j = 0; j < 16; ++j) stage[(copy * rows + row) * W1 + k + j] = y[j];
+                    }
+                    ok = set_sync();
                     if (!ok) break;
-                    // thread -> a row's part of 32 / REP channels: the copies added in their order
-                    constexpr int CW = 32 / REP;
-                    const int rr = threadIdx.x / REP, j0 = (threadIdx.x % REP) * CW;
-                    float z[CW];
+                    for (int u = own; u < rows * W4; u += 128) {
+                        const int rr = u / W4, j0 = 4 * (u - rr * W4);
+                        if (j0 >= wd) continue;
+                        float z[4];
 #pragma unroll
-                    for (int j = 0; j < CW; ++j) {
-                        z[j] = stage[rr * 33 + j0 + j];
+                        for (int j = 0; j < 4; ++j) {
+                            z[j] = stage[rr * W1 + j0 + j];
 #pragma unroll
-                        for (int q = 1; q < REP; ++q) z[j] += stage[(rr + q * RT) * 33 + j0 + j];
-                    }
-                    const int r2 = g.rt * RT + rr;
-                    if (r2 < g.nodes * p.g) {
-                        const int t2 = r2 / p.g, h2 = g.h * p.g + (r2 - t2 * p.g);
-                        if (whole) {
-                            uint16_t *dst = p.out + (((size_t)g.b * p.T + t2) * p.Hq + h2) * D + k + j0;
-#pragma unroll
-                            for (int j = 0; j < CW; j += 8)
-                                *reinterpret_cast<uint4 *>(dst + j) =
-                                    make_uint4(pack_bf(z[j], z[j + 1]), pack_bf(z[j + 2], z[j + 3]),
-                                               pack_bf(z[j + 4], z[j + 5]), pack_bf(z[j + 6], z[j + 7]));
-                        } else {
-                            float *dst = p.part + ((size_t)slotw * RT + rr) * D + k + j0;
-#pragma unroll
-                            for (int j = 0; j < CW; j += 4)
-                                *reinterpret_cast<float4 *>(dst + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+                            for (int q = 1; q < REP; ++q) z[j] += stage[(rr + q * rows) * W1 + j0 + j];
                         }
+                        const int r2 = g.rt * RT + rr;
+                        const int t2 = r2 / p.g, h2 = g.h * p.g + (r2 - t2 * p.g);
+                        store_row<RT, D>(p, g, whole, slotw, rr, t2, h2, k0 + j0, z);
                     }
-                    ok = soft_sync();
+                    ok = set_sync();
                     if (!ok) break;
                 }
             }
+            // the statistics are read before the next segment writes them: its Q comes after both
+            // sets' outputs, its first statistics after its first product
+            if (!ok) break;
+            ok = soft_sync();
         }
     }
 
@@ -1025,6 +1261,38 @@ cudaError_t launch_attend_grid(F *fn, long long blocks, int threads, size_t smem
     return cudaLaunchKernelEx(&cfg, fn, prm);
 }
 
+using EncodeTiledFnA = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFnA encode_fn_a() {
+    static EncodeTiledFnA fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFnA>(f);
+    });
+    return fn;
+}
+
+// The key codes as [rows][dim] bytes; a box is box_rows rows (inside a page and a tile) of at most
+// 128 bytes, swizzled by its width.
+cudaError_t key_map(const CacheView &c, int box_rows, CUtensorMap *out) {
+    EncodeTiledFnA fn = encode_fn_a();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint32_t w = (cuuint32_t)std::min(c.dim, 128);
+    const cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.pages * c.heads * c.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.dim};
+    const cuuint32_t box[2] = {w, (cuuint32_t)box_rows}, es[2] = {1u, 1u};
+    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.k8, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int D, int RT>
 cudaError_t launch_attend_as(const AttendParams &prm, cudaStream_t stream) {
     static int configured[64] = {0};
@@ -1071,6 +1339,11 @@ bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream) {
     AttendParams prm{};
     prm.c = c;
+    const int tn = c.dim == 256 ? 64 : 128;
+    prm.box_rows = 16;  // the largest power of two that divides a page, up to a tile
+    while (prm.box_rows < tn && c.page_size % (2 * prm.box_rows) == 0) prm.box_rows *= 2;
+    const cudaError_t e = key_map(c, prm.box_rows, &prm.kmap);
+    if (e != cudaSuccess) return e;
     prm.q = a.q;
     prm.ldq = a.ldq;
     prm.ctx = a.ctx;

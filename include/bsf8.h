@@ -380,7 +380,7 @@ int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests,
  *   lse    device, out, fp32 [B][T][Hq]: log of the sum of p_l, or NULL
  *   workspace  device, 16-byte aligned, of at least bsf8_tree_attention_workspace_bytes(...);
  *          no zeroing needed; not to be shared by calls that can overlap
- *   T      1 .. BSF8_MAX_NODES;  B  1 .. 4096;  Hq a multiple of heads;  scale finite, > 0
+ *   T      1 .. BSF8_MAX_NODES;  B  1 .. 1024;  Hq a multiple of heads;  scale finite, > 0
  * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_VALUE,
  *         BSF8_ERR_WORKSPACE, BSF8_ERR_CUDA. */
 int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,

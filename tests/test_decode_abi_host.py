@@ -81,7 +81,7 @@ def test_attention_refusals(lib):
         assert attention(lib, cache(**bad)) == status, bad
     for name in ("q", "table", "ctx", "out"):
         assert attention(lib, **{name: 0}) == NULL, name
-    for kw in (dict(B=0), dict(B=4097), dict(T=0), dict(T=257), dict(Hq=0), dict(Hq=3), dict(max_len=0), dict(max_len=65),
+    for kw in (dict(B=0), dict(B=1025), dict(T=0), dict(T=257), dict(Hq=0), dict(Hq=3), dict(max_len=0), dict(max_len=65),
                dict(table_pages=0)):
         assert attention(lib, **kw) == SHAPE, kw
     for s in (0.0, -1.0, float("nan"), float("inf")):
