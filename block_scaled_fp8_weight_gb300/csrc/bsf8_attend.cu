@@ -91,6 +91,7 @@ constexpr int attend_smem(int B) {
 }
 
 struct AttendParams {
+    unsigned long long page_magic;  // floor(2^32 / (page_size / 16)) + 1: divides 16-key groups by a page's
     CUtensorMap kmap;  // the key codes as rows of D bytes, box min(D, 128) x box_rows, swizzled
     int box_rows;
     CacheView c;
@@ -105,6 +106,7 @@ struct AttendParams {
     float *part;         // [blocks][2][RT][D] normalised outputs
     float2 *stat;        // [blocks][2][RT] (m, sum)
     int *prefix;         // [B + 1] the requests' items, for the join
+    uint32_t tries;      // suspensions of a wait
     unsigned long long timeout_ns;
     int skip_loads;
     int *status;
@@ -136,9 +138,10 @@ struct Segment {
     int b, h, rt, kv0, kv1, nt, ctx, nodes;
 };
 
-// The segment at item pos of a block whose range ends at end.
+// The segment at item pos of a block whose range ends at end, by a whole warp into *out (shared
+// memory).  Out of line: all roles call it.
 template <int D, int RT>
-__device__ __forceinline__ Segment segment_at(const AttendParams &p, const int *prefix, int pos, int end) {
+__device__ __noinline__ void find_segment(const AttendParams &p, const int *prefix, int pos, int end, Segment *out) {
     Segment s;
     int lo = 0, hi = p.B;  // prefix[lo] <= pos < prefix[hi]
     while (hi - lo > 1) {
@@ -156,7 +159,9 @@ __device__ __forceinline__ Segment segment_at(const AttendParams &p, const int *
     s.kv1 = min(s.nt, s.kv0 + (end - pos));
     s.h = seg / rts;
     s.rt = seg - s.h * rts;
-    return s;
+    __syncwarp();  // the segment before is no longer read
+    if ((threadIdx.x & 31) == 0) *out = s;
+    __syncwarp();
 }
 
 // ------------------------------------------------------------------ tcgen05 wrappers
@@ -226,6 +231,12 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
 __device__ __forceinline__ void commit_a(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -407,15 +418,27 @@ __device__ __forceinline__ void store_row(const AttendParams &p, const Segment &
     }
 }
 
-// Slow path of a wait, out of line: every role has several waits.
-__device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, unsigned long long timeout_ns, int *err,
-                                         int *status) {
-    const bool ok = mbar_wait_bounded(bar, parity, timeout_ns);
-    if (!ok) {
-        *(volatile int *)err = 1;
-        report_timeout(status);
-    }
-    return ok && !*(volatile int *)err;
+// Waits for a phase of `bar`, at most `tries` suspensions of kSuspendNs each; false when they ran out.
+// A few instructions: every role has several waits, and the block's roles share an SM's instruction
+// caches.
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint32_t tries) {
+    uint32_t left;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %4;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra AGAIN;\n"
+        "DONE:\n\t"
+        "mov.u32 %0, n;\n\t}"
+        : "=r"(left)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(tries), "r"(kSuspendNs)
+        : "memory");
+    return left != 0;
 }
 
 struct AttendShared {
@@ -431,12 +454,12 @@ struct AttendShared {
     uint64_t q_full;                // a segment's Q is in place
     uint64_t soft, set[2];          // the softmax warps' own barriers (bounded, unlike bar.sync)
     uint32_t tmem;
-    int err;
     int valid[kInfo];               // a tile's 16-key groups that exist (bit i)
     int ev[kInfo], vnan[kInfo];     // the segment's value exponent at the tile; a value block holds NaN
     int care[kInfo];                // the tile's values need care: missing keys, NaN
     uint8_t nanblk[kInfo][128];     // then: each key's NaN blocks
     float mrow[2][128];             // the rows' maxima, handed from set to set
+    Segment seg[kThreadsA / 32];    // each warp's current segment
     float2 stat[kSoftWarps][32];
     uint32_t nan[kSoftWarps][32];
     int scan[32];
@@ -476,7 +499,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         }
         mbar_init(&s.q_full, kSoftWarps);
         mbar_init(&s.soft, kSoftWarps);
-        s.err = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -517,36 +539,38 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     __syncthreads();
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b <= p.B; b += kThreadsA) p.prefix[b] = prefix[b];
-    const uint32_t tmem = s.tmem;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0);
     const long long total = prefix[p.B];
     const int w0 = range_start(total, blockIdx.x), w1 = range_start(total, blockIdx.x + 1);
-    // A bounded wait of one thread; false when it ran out.
-    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
-#pragma unroll 1
-        for (int i = 0; i < 256; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        return wait_longer(bar, parity, p.timeout_ns, &s.err, p.status);
-    };
-    // The same by every lane of a warp.
+    // A bounded wait of one thread, or of a warp; false when it ran out (the thread reports it at its
+    // role's end).
+    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool { return wait_phase(bar, parity, p.tries); };
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
+        return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, p.tries));
+    };
+    bool ok = true;  // no wait of this thread ran out
+    auto segment = [&](int pos) -> Segment {
+        find_segment<D, RT>(p, prefix, pos, w1, &s.seg[warp]);
+        return s.seg[warp];
     };
 
     // A batch of BT tiles' 16-key groups, one a lane: the page of the lane's group (a load that stays
     // in flight until the batch is used), then its cache row (head h), -1 if there is none.
     constexpr int NSB = TN / 16, BT = 32 / NSB;
+    // exact: group * (magic * d - 2^32) < 2^32 for groups below 2^26 and d <= 64
+    auto in_page = [&](int grp) -> int { return (int)(((unsigned long long)(unsigned)grp * p.page_magic) >> 32); };
     auto page_of = [&](const Segment &g, int tile) -> int {
-        const int tok = (tile + lane / NSB) * TN + 16 * (lane % NSB);
-        return tok < g.ctx + g.nodes ? p.c.table[(size_t)g.b * p.c.table_pages + tok / p.c.page_size] : -1;
+        const int grp = (tile + lane / NSB) * NSB + lane % NSB;
+        return 16 * grp < g.ctx + g.nodes ? p.c.table[(size_t)g.b * p.c.table_pages + in_page(grp)] : -1;
     };
     auto row_of = [&](const Segment &g, int tile, int page) -> int {
-        const int tok = (tile + lane / NSB) * TN + 16 * (lane % NSB);
-        if (tok >= g.ctx + g.nodes) return -1;
+        const int grp = (tile + lane / NSB) * NSB + lane % NSB;
+        if (16 * grp >= g.ctx + g.nodes) return -1;
         if ((unsigned)page >= (unsigned)p.c.pages) {
             report_index(p.status);
             return -1;
         }
-        return (page * p.c.heads + g.h) * p.c.page_size + tok % p.c.page_size;
+        return (page * p.c.heads + g.h - in_page(grp)) * p.c.page_size + 16 * grp;
     };
 
     if (warp == kProducerWarp) {
@@ -554,9 +578,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         const int gpb = p.box_rows / 16;  // groups a box: boxes never cross a page's end
         const bool lead = lane < NSB && lane % gpb == 0;
         int tile = 0;
-        bool ok = true;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
+            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
             int page = page_of(g, g.kv0), rows = -1;
             for (int i = 0; i < tiles; ++i, ++tile) {
@@ -602,9 +625,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         constexpr int KPL = 16 / S::EB;  // keys of a lane's 16 exponent bytes
         const int key0 = lane * KPL;
         int tile = 0;
-        bool ok = true;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
+            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
             int E = 0;  // the largest value exponent of the segment so far
             int page = page_of(g, g.kv0), rows = -1;
@@ -682,75 +704,77 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         // ------------------------------------------------------------ MMA issue: a thread a product
         // One thread issues an MMA about every 100 cycles whatever its size (to N = 128); two with
         // an accumulator each, one every 64.
-        const bool value = warp > kMmaWarp;
-        int tile = 0, seg = 0;  // of the block so far
-        bool ok = true;
-        if (lane == 0) {
-            for (int pos = w0; pos < w1 && ok; ++seg) {
-                const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
-                const int tiles = g.kv1 - g.kv0;
-                if (!value) ok = wait1(&s.q_full, (uint32_t)(seg & 1));
-                for (int i = 0; i < tiles && ok; ++i, ++tile) {
-                    const int buf = tile & 1;
-                    const uint32_t bph = (uint32_t)((tile >> 1) & 1);
-                    const uint32_t sp = tmem + S::CS + buf * TN;
-                    if (value) {
-                        ok = wait1(&s.v_full[buf], bph) && wait1(&s.p_full[buf], bph);
-                        if (!ok) break;
-                        fence_after();
-                        const uint32_t src = smem_u32(base + S::oV) + buf * S::F16;
+        // The whole warp walks along, so that addresses and descriptors stay in uniform registers.
+        const bool value = __shfl_sync(0xFFFFFFFFu, warp, 0) > kMmaWarp;
+        const bool one = elect_one();
+        int tile = 0;  // of the block so far
+        uint32_t qph = 0;
+        for (int pos = w0; pos < w1 && ok; qph ^= 1u) {
+            const Segment g = segment(pos);
+            const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0);
+            if (!value) ok = wait(&s.q_full, qph);
+            for (int i = 0; i < tiles && ok; ++i, ++tile) {
+                const int buf = tile & 1;
+                const uint32_t bph = (uint32_t)((tile >> 1) & 1);
+                const uint32_t sp = tmem + S::CS + buf * TN;
+                if (value) {
+                    ok = wait(&s.v_full[buf], bph) && wait(&s.p_full[buf], bph);
+                    if (!ok) break;
+                    fence_after();
+                    const uint64_t bd = desc_a(smem_u32(base + S::oV) + buf * S::F16, TN * 128);
+                    if (one) {
 #pragma unroll
                         for (int ks = 0; ks < TN / 16; ++ks)  // 16 keys a step: two 8-key atoms
-                            umma_a(tmem + S::CO, sp + 8 * ks, desc_a(src + ks * 2048, TN * 128), idesc_a(D, true),
-                                   i > 0 || ks > 0);
+                            umma_a(tmem + S::CO, sp + 8 * ks, bd + ks * (2048 >> 4), idesc_a(D, true), i > 0 || ks > 0);
                         commit_a(&s.pv_done[buf]);
-                    } else {
-                        const int slot = tile % S::NSLOT;
-                        // S takes the place of the P of two tiles before
-                        ok = wait1(&s.k_code[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait1(&s.sf_full[buf], bph) &&
-                             (tile < 2 || wait1(&s.pv_done[buf], bph ^ 1u));
-                        if (!ok) break;
-                        fence_after();
-                        const uint32_t src = smem_u32(base + S::oK) + slot * S::SLOT;
-                        const uint32_t sfb = tmem + S::CB + 4 * buf;
+                    }
+                } else {
+                    const int slot = tile % S::NSLOT;
+                    // S takes the place of the P of two tiles before
+                    ok = wait(&s.k_code[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait(&s.sf_full[buf], bph) &&
+                         (tile < 2 || wait(&s.pv_done[buf], bph ^ 1u));
+                    if (!ok) break;
+                    fence_after();
+                    constexpr int RB = D < 128 ? 64 : 128;
+                    const uint64_t bd = desc_codes<RB>(smem_u32(base + S::oK) + slot * S::SLOT);
+                    const uint64_t ad = desc_codes<128>(smem_u32(base + S::oQ));
+                    const uint32_t sfb = tmem + S::CB + 4 * buf;
+                    if (one) {
 #pragma unroll
                         for (int part = 0; part < 2; ++part)  // Q's upper and lower parts
 #pragma unroll
                             for (int ks = 0; ks < D / 32; ++ks) {  // 32 channels a step
-                                const uint64_t bd = desc_codes<(D < 128 ? 64 : 128)>(src + (ks >> 2) * (TN * 128)) + 2 * (ks & 3);
+                                const uint64_t bk = bd + (ks >> 2) * (TN * 128 >> 4) + 2 * (ks & 3);
                                 const uint32_t id = idesc_mx(TN, part, ks & 3), fb = sfb + 2 * (ks >> 2);
                                 if constexpr (S::QS)
-                                    umma_mx_ss(sp,
-                                               desc_codes<128>(smem_u32(base + S::oQ) + part * (128 * D) + (ks >> 2) * (128 * 128)) +
-                                                   2 * (ks & 3),
-                                               bd, id, tmem + S::CA, fb, part + ks > 0);
+                                    umma_mx_ss(sp, ad + part * (128 * D >> 4) + (ks >> 2) * (128 * 128 >> 4) + 2 * (ks & 3), bk,
+                                               id, tmem + S::CA, fb, part + ks > 0);
                                 else
-                                    umma_mx_ts(sp, tmem + S::CQ + part * (D / 4) + 8 * ks, bd, id, tmem + S::CA, fb,
+                                    umma_mx_ts(sp, tmem + S::CQ + part * (D / 4) + 8 * ks, bk, id, tmem + S::CA, fb,
                                                part + ks > 0);
                             }
                         commit_a(&s.s_full[buf]);
                         commit_a(&s.k_free[slot]);
                     }
                 }
-                pos += tiles;
+                __syncwarp();
             }
-            // the last products must be done before tensor memory goes back (bounded)
-            if (tile > 0)
-                (void)wait1(value ? &s.pv_done[(tile - 1) & 1] : &s.s_full[(tile - 1) & 1],
-                            (uint32_t)(((tile - 1) >> 1) & 1));
+            pos += tiles;
         }
+        // the last products must be done before tensor memory goes back (bounded)
+        if (tile > 0)
+            (void)wait(value ? &s.pv_done[(tile - 1) & 1] : &s.s_full[(tile - 1) & 1], (uint32_t)(((tile - 1) >> 1) & 1));
     } else if (warp >= kSoftWarps) {
         // ------------------------------------------------------------ values to f16; key scales
         const int dw = warp - kSoftWarps;
         constexpr int NQ = D / 64, RPW = TN / kDeqWarps, PASSES = RPW / 8 * NQ;
         int kt = 0, vt = 0;  // tiles of the block so far: key scales, values
-        bool ok = true;
         // Conflict-free on both sides: in a quarter-warp, four 16-code chunks of an even row and
         // four of the next row from another 64-channel column (other banks in the codes; odd
         // against even 16-byte units in the swizzled f16 rows).
         const int ci = lane & 3, cj = (lane >> 2) & 1, cr = dw * RPW + 2 * (lane >> 3) + cj;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment_at<D, RT>(p, prefix, pos, w1);
+            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
             for (int i = -1; i < tiles; ++i) {
                 if (i + 1 < tiles) {
@@ -833,7 +857,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         const int copy = 32 * quad / RT, col0 = copy * CPT;        // this copy's key columns
         int it = 0;
         uint32_t soft_ph = 0, set_ph = 0;
-        bool ok = true;
         auto soft_sync = [&]() -> bool {  // all softmax warps
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.soft);
@@ -913,23 +936,134 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             st_cols(tl + S::CA, f);  // both sets write the same
             wait_st();
         }
-        Segment next{};
-        int eq_next = 0;
-        for (int pos = w0; pos < w1 && ok;) {
-            if (pos == w0) {
-                next = segment_at<D, RT>(p, prefix, pos, w1);
-                eq_next = put_q(next);
+        // Per turn: the next segment's Q (once the last S of the one before is there), then the output
+        // of the one before, then the segment's tiles.
+        Segment g{};
+        int r = 0, t = 0, hq = 0;          // row of the request and head; its node and query head
+        bool real = false;
+        float m = 0.0f, l = 0.0f;          // of the set's tiles; l in units of 2^(m - bias)
+        uint32_t nanblk = 0;
+        for (int pos = w0; ok;) {
+            const bool more = pos < w1;
+            Segment next{};
+            int eq = 0;
+            if (more) {
+                next = segment(pos);
+                if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                eq = put_q(next);
             }
-            const Segment g = next;
+            if (it > 0) {
+                // ---- the segment's output; the sets take half of the channels each
+                ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                const int ev = s.ev[(it - 1) % kInfo];
+                s.stat[warp][lane] = make_float2(m, l);
+                s.nan[warp][lane] = nanblk;
+                ok = soft_sync();
+                if (!ok) break;
+                // a copy's maximum is the later of its two sets'; copies and sets are added in order
+                float M = -INFINITY, mc = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int q = 0; q < REP; ++q) {
+                    const int w = q * (RT / 32) + quad % (RT / 32);
+                    M = max3(M, s.stat[w][lane].x, s.stat[w + 4][lane].x);
+                }
+#pragma unroll
+                for (int q = 0; q < 2 * REP; ++q) {
+                    const float2 st = s.stat[(q >> 1) * (RT / 32) + quad % (RT / 32) + 4 * (q & 1)][lane];
+                    L += st.y == 0.0f ? 0.0f : st.y * ex2(st.x == -INFINITY ? 0.0f : st.x - M);
+                }
+                mc = fmaxf(s.stat[quad][lane].x, s.stat[quad + 4][lane].x);
+                nanblk = s.nan[quad][lane] | s.nan[quad + 4][lane];
+                const bool any = s.stat[quad][lane].y != 0.0f || s.stat[quad + 4][lane].y != 0.0f;
+                const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
+                const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
+                // O (this copy) * f * fv = its share of the normalised output
+                const float f = any ? ex2(mc == -INFINITY ? 0.0f : mc - M) / L : 0.0f;
+                const float fv = pow2i(ev - 127 - kShift);
+                auto share = [&](int k, float (&y)[16]) {  // of channels [k, k + 16)
+                    uint32_t o[16];
+                    ld_cols(tl + S::CO + k, o);
+                    wait_ld();
+                    const bool bad = (nanblk >> (k / 32)) & 1u;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        y[j] = bad ? __uint_as_float(0x7FC00000u) : any ? __uint_as_float(o[j]) * f * fv : 0.0f;
+                };
+                const float Lt = L * pow2i(-(int)kBias);  // the sum in units of 2^M
+                if (set == 0 && copy == 0 && real) {
+                    if (!whole)
+                        p.stat[(size_t)slotw * RT + row] = make_float2(M, Lt);
+                    else if (p.lse)
+                        p.lse[((size_t)g.b * p.T + t) * p.Hq + hq] =
+                            L == 0.0f ? -INFINITY : (M + log2f(Lt)) * 0.69314718055994531f;
+                }
+                if constexpr (REP == 1) {
+#pragma unroll 1
+                    for (int k = set * (D / 2); k < (set + 1) * (D / 2); k += 16) {
+                        float y[16];
+                        share(k, y);
+                        if (real) store_row<RT, D>(p, g, whole, slotw, row, t, hq, k, y);
+                    }
+                } else {
+                    // through shared memory, W channels of the real rows of every copy at a time (padded to
+                    // W + 1 floats a row); then a thread takes four channels of a row, the copies in order
+                    float *const stage = reinterpret_cast<float *>(base + S::oStage) + set * (128 * 17);
+                    const int rows = min(RT, g.nodes * p.g - g.rt * RT);
+                    const int W = rows * REP <= 32 ? 64 : rows * REP <= 64 ? 32 : 16;
+                    const int W1 = W + 1, W4 = W / 4, own = 32 * quad + lane;
+                    const int c1 = (set + 1) * (D / 2);
+                    for (int k0 = set * (D / 2); k0 < c1; k0 += W) {
+                        const int wd = min(W, c1 - k0);
+#pragma unroll 1
+                        for (int k = 0; k < wd; k += 16) {
+                            float y[16];
+                            share(k0 + k, y);
+                            if (row < rows)
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) stage[(copy * rows + row) * W1 + k + j] = y[j];
+                        }
+                        ok = set_sync();
+                        if (!ok) break;
+                        for (int u = own; u < rows * W4; u += 128) {
+                            const int rr = u / W4, j0 = 4 * (u - rr * W4);
+                            if (j0 >= wd) continue;
+                            float z[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                z[j] = stage[rr * W1 + j0 + j];
+#pragma unroll
+                                for (int q = 1; q < REP; ++q) z[j] += stage[(rr + q * rows) * W1 + j0 + j];
+                            }
+                            const int r2 = g.rt * RT + rr;
+                            const int t2 = r2 / p.g, h2 = g.h * p.g + (r2 - t2 * p.g);
+                            store_row<RT, D>(p, g, whole, slotw, rr, t2, h2, k0 + j0, z);
+                        }
+                        ok = set_sync();
+                        if (!ok) break;
+                    }
+                }
+                // the statistics are read, and O is, before the next tile's writes
+                if (!ok) break;
+                ok = soft_sync();
+                if (!ok) break;
+            }
+            if (!more) break;
+            g = next;
             const int tiles = g.kv1 - g.kv0;
-            const int r = g.rt * RT + row;         // row of the request and head
-            const bool real = r < g.nodes * p.g;
-            const int t = real ? r / p.g : 0, hq = g.h * p.g + (real ? r - t * p.g : 0);
-            const float c = p.scale_log2 * pow2i(eq_next);  // S -> x
+            r = g.rt * RT + row;
+            real = r < g.nodes * p.g;
+            t = real ? r / p.g : 0;
+            hq = g.h * p.g + (real ? r - t * p.g : 0);
+            const float c = p.scale_log2 * pow2i(eq);  // S -> x
             pos += tiles;
 
-            float m = -INFINITY, l = 0.0f;  // of the set's tiles; l in units of 2^(m - bias)
-            uint32_t nanblk = 0;
+            m = -INFINITY;
+            l = 0.0f;
+            nanblk = 0;
             const int32_t *mrow = p.mask ? p.mask + ((size_t)g.b * p.T + t) * p.W : nullptr;
             for (int i = 0; i < tiles && ok; ++i, ++it) {
                 if ((it & 1) != set) continue;
@@ -1059,111 +1193,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 if (lane == 0) mbar_arrive(&s.p_full[set]);
             }
             if (!ok) break;
-            if (pos < w1) {  // the next segment's Q, once this one's last S is there
-                next = segment_at<D, RT>(p, prefix, pos, w1);
-                ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
-                if (!ok) break;
-                fence_after();
-                eq_next = put_q(next);
-            }
-            // ---- the segment's output; the sets take half of the channels each
-            ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
-            if (!ok) break;
-            fence_after();
-            const int ev = s.ev[(it - 1) % kInfo];
-            s.stat[warp][lane] = make_float2(m, l);
-            s.nan[warp][lane] = nanblk;
-            ok = soft_sync();
-            if (!ok) break;
-            // a copy's maximum is the later of its two sets'; copies and sets are added in order
-            float M = -INFINITY, mc = -INFINITY, L = 0.0f;
-#pragma unroll
-            for (int q = 0; q < REP; ++q) {
-                const int w = q * (RT / 32) + quad % (RT / 32);
-                M = max3(M, s.stat[w][lane].x, s.stat[w + 4][lane].x);
-            }
-#pragma unroll
-            for (int q = 0; q < 2 * REP; ++q) {
-                const float2 st = s.stat[(q >> 1) * (RT / 32) + quad % (RT / 32) + 4 * (q & 1)][lane];
-                L += st.y == 0.0f ? 0.0f : st.y * ex2(st.x == -INFINITY ? 0.0f : st.x - M);
-            }
-            mc = fmaxf(s.stat[quad][lane].x, s.stat[quad + 4][lane].x);
-            nanblk = s.nan[quad][lane] | s.nan[quad + 4][lane];
-            const bool any = s.stat[quad][lane].y != 0.0f || s.stat[quad + 4][lane].y != 0.0f;
-            const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
-            const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
-            // O (this copy) * f * fv = its share of the normalised output
-            const float f = any ? ex2(mc == -INFINITY ? 0.0f : mc - M) / L : 0.0f;
-            const float fv = pow2i(ev - 127 - kShift);
-            auto share = [&](int k, float (&y)[16]) {  // of channels [k, k + 16)
-                uint32_t o[16];
-                ld_cols(tl + S::CO + k, o);
-                wait_ld();
-                const bool bad = (nanblk >> (k / 32)) & 1u;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    y[j] = bad ? __uint_as_float(0x7FC00000u) : any ? __uint_as_float(o[j]) * f * fv : 0.0f;
-            };
-            const float Lt = L * pow2i(-(int)kBias);  // the sum in units of 2^M
-            if (set == 0 && copy == 0 && real) {
-                if (!whole)
-                    p.stat[(size_t)slotw * RT + row] = make_float2(M, Lt);
-                else if (p.lse)
-                    p.lse[((size_t)g.b * p.T + t) * p.Hq + hq] =
-                        L == 0.0f ? -INFINITY : (M + log2f(Lt)) * 0.69314718055994531f;
-            }
-            if constexpr (REP == 1) {
-#pragma unroll 1
-                for (int k = set * (D / 2); k < (set + 1) * (D / 2); k += 16) {
-                    float y[16];
-                    share(k, y);
-                    if (real) store_row<RT, D>(p, g, whole, slotw, row, t, hq, k, y);
-                }
-            } else {
-                // through shared memory, W channels of the real rows of every copy at a time (padded to
-                // W + 1 floats a row); then a thread takes four channels of a row, the copies in order
-                float *const stage = reinterpret_cast<float *>(base + S::oStage) + set * (128 * 17);
-                const int rows = min(RT, g.nodes * p.g - g.rt * RT);
-                const int W = rows * REP <= 32 ? 64 : rows * REP <= 64 ? 32 : 16;
-                const int W1 = W + 1, W4 = W / 4, own = 32 * quad + lane;
-                const int c1 = (set + 1) * (D / 2);
-                for (int k0 = set * (D / 2); k0 < c1; k0 += W) {
-                    const int wd = min(W, c1 - k0);
-#pragma unroll 1
-                    for (int k = 0; k < wd; k += 16) {
-                        float y[16];
-                        share(k0 + k, y);
-                        if (row < rows)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) stage[(copy * rows + row) * W1 + k + j] = y[j];
-                    }
-                    ok = set_sync();
-                    if (!ok) break;
-                    for (int u = own; u < rows * W4; u += 128) {
-                        const int rr = u / W4, j0 = 4 * (u - rr * W4);
-                        if (j0 >= wd) continue;
-                        float z[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            z[j] = stage[rr * W1 + j0 + j];
-#pragma unroll
-                            for (int q = 1; q < REP; ++q) z[j] += stage[(rr + q * rows) * W1 + j0 + j];
-                        }
-                        const int r2 = g.rt * RT + rr;
-                        const int t2 = r2 / p.g, h2 = g.h * p.g + (r2 - t2 * p.g);
-                        store_row<RT, D>(p, g, whole, slotw, rr, t2, h2, k0 + j0, z);
-                    }
-                    ok = set_sync();
-                    if (!ok) break;
-                }
-            }
-            // the statistics are read before the next segment writes them: its Q comes after both
-            // sets' outputs, its first statistics after its first product
-            if (!ok) break;
-            ok = soft_sync();
         }
     }
 
+    if (!ok) report_timeout(p.status);
     __syncwarp();
     fence_before();
     __syncthreads();
@@ -1342,6 +1375,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     const int tn = c.dim == 256 ? 64 : 128;
     prm.box_rows = 16;  // the largest power of two that divides a page, up to a tile
     while (prm.box_rows < tn && c.page_size % (2 * prm.box_rows) == 0) prm.box_rows *= 2;
+    prm.page_magic = (1ull << 32) / (unsigned)(c.page_size / 16) + 1;
     const cudaError_t e = key_map(c, prm.box_rows, &prm.kmap);
     if (e != cudaSuccess) return e;
     prm.q = a.q;
@@ -1364,6 +1398,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.prefix = reinterpret_cast<int *>(prm.stat + rows);
     const Options opt = options();
     prm.timeout_ns = opt.timeout_ns;
+    prm.tries = (uint32_t)std::min<unsigned long long>(std::max<unsigned long long>(opt.timeout_ns / kSuspendNs, 1), 0x7FFFFFFFu);
     prm.skip_loads = opt.skip_loads;
     prm.status = status_word();
     if (!prm.status) return cudaErrorInvalidSymbol;
