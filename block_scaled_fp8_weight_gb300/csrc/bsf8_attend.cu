@@ -54,12 +54,11 @@ namespace {
 
 constexpr int kAttendBlocks = 152;   // one an SM of a GB300 (no block waits for another)
 constexpr int kMaxBatch = 1024;
-constexpr int kSoftWarps = 8;        // two sets of four, a set every other tile
+constexpr int kSoftWarps = 8;        // two sets of four, half of a copy's key columns each
 constexpr int kDeqWarps = 8;
 constexpr int kProducerWarp = kSoftWarps + kDeqWarps, kScoutWarp = kProducerWarp + 1;
 constexpr int kMmaWarp = kScoutWarp + 1;  // two: S, O
 constexpr int kThreadsA = (kMmaWarp + 2) * 32;
-constexpr int kExps = 4;             // tiles whose exponents are in shared memory
 constexpr int kInfo = 8;             // tiles whose exponents and flags are kept
 constexpr float kBias = 13.0f;       // p = 2^(x - m + kBias)
 constexpr float kSlack = 2.0f;       // m lags the maximum by at most this
@@ -78,7 +77,7 @@ struct Shape {
                          CQ = D == 256 ? 0 : CA + 32;
     static constexpr bool QS = D == 256;             // Q in shared memory
     static constexpr int oV = 0, oK = 2 * F16, oRing = oK + NSLOT * SLOT, oQ = oRing + NSLOT * SLOT;
-    static constexpr int oExp = oQ + (QS ? 2 * 128 * D : 0), oStage = oExp + 2 * kExps * 512;
+    static constexpr int oExp = oQ + (QS ? 2 * 128 * D : 0), oStage = oExp + NSLOT * 1024;
     static constexpr int oPrefix = oStage + 2 * 128 * 17 * 4;
 };
 
@@ -138,11 +137,11 @@ struct Segment {
     int b, h, rt, kv0, kv1, nt, ctx, nodes;
 };
 
-// The segment at item pos of a block whose range ends at end, by a whole warp into *out (shared
-// memory).  Out of line: all roles call it.
+// The segment at item pos of a block whose range ends at end.
 template <int D, int RT>
-__device__ __noinline__ void find_segment(const AttendParams &p, const int *prefix, int pos, int end, Segment *out) {
-    Segment s;
+__device__ __forceinline__ Segment segment_at(const AttendParams &p, const int *prefix, int pos, int end) {
+    Segment s{};
+    if (pos >= end) return s;
     int lo = 0, hi = p.B;  // prefix[lo] <= pos < prefix[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -159,9 +158,24 @@ __device__ __noinline__ void find_segment(const AttendParams &p, const int *pref
     s.kv1 = min(s.nt, s.kv0 + (end - pos));
     s.h = seg / rts;
     s.rt = seg - s.h * rts;
-    __syncwarp();  // the segment before is no longer read
-    if ((threadIdx.x & 31) == 0) *out = s;
-    __syncwarp();
+    return s;
+}
+
+// The segment after s, at item pos < end.
+template <int D, int RT>
+__device__ __forceinline__ void next_segment(const AttendParams &p, Segment &s, int pos, int end) {
+    if ((++s.rt) * RT >= s.nodes * p.g) {
+        s.rt = 0;
+        if (++s.h == p.c.heads) {
+            s.h = 0;
+            do {
+                (void)lengths(p, ++s.b, s.ctx, s.nodes);
+            } while (s.nodes == 0);  // ends: there are items left
+            s.nt = (s.ctx + s.nodes + Shape<D>::TN - 1) / Shape<D>::TN;
+        }
+    }
+    s.kv0 = 0;
+    s.kv1 = min(s.nt, end - pos);
 }
 
 // ------------------------------------------------------------------ tcgen05 wrappers
@@ -220,6 +234,16 @@ __device__ __forceinline__ uint64_t desc_codes(uint32_t saddr) {
            ((uint64_t)1 << 46) | ((uint64_t)(RB == 128 ? 2 : 4) << 61);
 }
 
+// 32 rows of 16 bytes, unswizzled (8-row groups of 128 bytes one after another) -> four tensor
+// memory columns of 32 lanes, repeated in all four lane quarters.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t t, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(t), "l"(desc) : "memory");
+}
+
 __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int col, int row, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -243,6 +267,13 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void ld_cols(uint32_t t, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+}
 
 __device__ __forceinline__ void ld_cols(uint32_t t, uint32_t (&r)[16]) {
     asm volatile(
@@ -442,15 +473,13 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint3
 }
 
 struct AttendShared {
-    uint64_t k_code[4], k_free[4];  // ring slots of key codes: landed; multiplied
-    uint64_t v_code[4], v_free[4];  // of value codes: landed; read by all dequant warps
-    uint64_t x_full[kExps], x_free[kExps];  // a tile's exponents (keys and values); read
-    uint64_t sf_full[2];            // a tile's key scales are in tensor memory
+    uint64_t k_full[4], k_free[4];  // ring slots of keys: codes landed and scales written; multiplied
+    uint64_t c_full[4], c_free[4];  // of values: codes landed and exponents written; read by all dequant warps
     uint64_t v_full[2];             // the f16 values of a tile are written
     uint64_t s_full[2];             // S written
     uint64_t p_full[2];             // P written, O rescaled
     uint64_t pv_done[2];            // O updated, P and the f16 values read
-    uint64_t m_full[2][4];          // a softmax warp's rows have their maximum of the tile
+    uint64_t pair[4];               // the two softmax warps of the same rows
     uint64_t q_full;                // a segment's Q is in place
     uint64_t soft, set[2];          // the softmax warps' own barriers (bounded, unlike bar.sync)
     uint32_t tmem;
@@ -458,8 +487,7 @@ struct AttendShared {
     int ev[kInfo], vnan[kInfo];     // the segment's value exponent at the tile; a value block holds NaN
     int care[kInfo];                // the tile's values need care: missing keys, NaN
     uint8_t nanblk[kInfo][128];     // then: each key's NaN blocks
-    float mrow[2][128];             // the rows' maxima, handed from set to set
-    Segment seg[kThreadsA / 32];    // each warp's current segment
+    float mrow[2][2][128];          // a tile's maxima of the rows' halves (tiles in turn)
     float2 stat[kSoftWarps][32];
     uint32_t nan[kSoftWarps][32];
     int scan[32];
@@ -470,8 +498,8 @@ struct AttendShared {
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     using S = Shape<D>;
-    constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP;  // CPT: key columns a thread
-    constexpr int CH = CPT < 32 ? CPT : 32;                    // taken CH at a time
+    constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP / 2;  // CPT: key columns a thread
+    constexpr int CH = CPT <= 32 ? CPT : 16;                       // taken CH at a time
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
     __shared__ AttendShared s;
@@ -480,20 +508,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&s.k_code[i], 1);
+            mbar_init(&s.k_full[i], 2);  // the producer's byte count, the scout
             mbar_init(&s.k_free[i], 1);
-            mbar_init(&s.v_code[i], 1);
-            mbar_init(&s.v_free[i], kDeqWarps);
-            mbar_init(&s.x_full[i], 1);
-            mbar_init(&s.x_free[i], kDeqWarps);
-            mbar_init(&s.m_full[0][i], 1);
-            mbar_init(&s.m_full[1][i], 1);
+            mbar_init(&s.c_full[i], 2);
+            mbar_init(&s.c_free[i], kDeqWarps);
+            mbar_init(&s.pair[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s.sf_full[i], 4);
             mbar_init(&s.v_full[i], kDeqWarps);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.p_full[i], kSoftWarps);
             mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.set[i], 4);
         }
@@ -549,10 +573,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, p.tries));
     };
     bool ok = true;  // no wait of this thread ran out
-    auto segment = [&](int pos) -> Segment {
-        find_segment<D, RT>(p, prefix, pos, w1, &s.seg[warp]);
-        return s.seg[warp];
-    };
+    // The block's first segment; each role walks on from it.
+    const Segment first = segment_at<D, RT>(p, prefix, w0, w1);
 
     // A batch of BT tiles' 16-key groups, one a lane: the page of the lane's group (a load that stays
     // in flight until the batch is used), then its cache row (head h), -1 if there is none.
@@ -578,8 +600,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         const int gpb = p.box_rows / 16;  // groups a box: boxes never cross a page's end
         const bool lead = lane < NSB && lane % gpb == 0;
         int tile = 0;
+        Segment g = first;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
             int page = page_of(g, g.kv0), rows = -1;
             for (int i = 0; i < tiles; ++i, ++tile) {
@@ -595,38 +617,39 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 const uint32_t fph = (uint32_t)((tile / S::NSLOT) & 1) ^ 1u;
                 ok = tile < S::NSLOT || wait(&s.k_free[slot], fph);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&s.k_code[slot], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&s.k_full[slot], bytes);
                 __syncwarp();
                 if (go && !p.skip_loads)
 #pragma unroll
                     for (int c = 0; c < D; c += 128)  // 128-byte columns of the tile, one after another
                         tma_rows(base + S::oK + slot * S::SLOT + c * TN + lane * 16 * (D < 128 ? D : 128), &p.kmap, c, row,
-                                 &s.k_code[slot]);
-                ok = tile < S::NSLOT || wait(&s.v_free[slot], fph);
+                                 &s.k_full[slot]);
+                ok = tile < S::NSLOT || wait(&s.c_free[slot], fph);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&s.v_code[slot], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&s.c_full[slot], bytes);
                 __syncwarp();
                 if (go && !p.skip_loads)
                     bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
-                             (uint32_t)(p.box_rows * D), &s.v_code[slot]);
+                             (uint32_t)(p.box_rows * D), &s.c_full[slot]);
             }
             pos += tiles;
+            if (pos < w1) next_segment<D, RT>(p, g, pos, w1);
         }
         // every copy must have landed before the block's memory goes away (bounded)
         if (!p.skip_loads)
             for (int i = max(0, tile - S::NSLOT); i < tile + (ok ? 0 : 1); ++i) {
                 const int slot = i % S::NSLOT;
                 const uint32_t iph = (uint32_t)((i / S::NSLOT) & 1);
-                (void)mbar_wait_bounded(&s.k_code[slot], iph, ok ? p.timeout_ns : 100000000ull);
-                (void)mbar_wait_bounded(&s.v_code[slot], iph, ok ? p.timeout_ns : 100000000ull);
+                (void)mbar_wait_bounded(&s.k_full[slot], iph, ok ? p.timeout_ns : 100000000ull);
+                (void)mbar_wait_bounded(&s.c_full[slot], iph, ok ? p.timeout_ns : 100000000ull);
             }
     } else if (warp == kScoutWarp) {
         // ------------------------------------------------------------ scout: exponents and flags
         constexpr int KPL = 16 / S::EB;  // keys of a lane's 16 exponent bytes
         const int key0 = lane * KPL;
         int tile = 0;
+        Segment g = first;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
             int E = 0;  // the largest value exponent of the segment so far
             int page = page_of(g, g.kv0), rows = -1;
@@ -649,20 +672,37 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     vn = *reinterpret_cast<const uint4 *>(p.c.vexp + at);
                 }
             };
-            load(0);
-            for (int i = 0; i < tiles; ++i, ++tile) {
+            for (int i = -1; i < tiles; ++i) {
                 kx = kn;
                 vx = vn;
                 vb = vbn;
                 if (i + 1 < tiles) load(i + 1);
-                const int xs = tile % kExps, info = tile % kInfo;
-                ok = tile < kExps || wait(&s.x_free[xs], (uint32_t)((tile / kExps) & 1) ^ 1u);
+                if (i < 0) continue;
+                const int slot = tile % S::NSLOT, info = tile % kInfo;
+                const uint32_t fph = (uint32_t)((tile / S::NSLOT) & 1) ^ 1u;
+                ok = tile < S::NSLOT || (wait(&s.k_free[slot], fph) && wait(&s.c_free[slot], fph));
                 if (!ok) break;
-                uint8_t *const ex = base + S::oExp + xs * 1024;  // keys', then values'
+                // the keys' as tensor memory wants them -- 32 rows (lanes) of four words (columns): column
+                // c of row l is key 32 c + l's word (dim 256: key 32 (c % 2) + l's word c / 2) -- the
+                // values' as they are
+                uint8_t *const ex = base + S::oExp + slot * 1024;
                 if (key0 < TN) {
-                    *reinterpret_cast<uint4 *>(ex + lane * 16) = kx;
+                    uint32_t *const kw = reinterpret_cast<uint32_t *>(ex) + (key0 & 31) * 4 + (key0 >> 5);
+                    const uint32_t w[4] = {kx.x, kx.y, kx.z, kx.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (D == 64) {
+                            kw[8 * j] = w[j] & 0xFFFFu;
+                            kw[8 * j + 4] = w[j] >> 16;
+                        } else if constexpr (D == 128) {
+                            kw[4 * j] = w[j];
+                        } else {
+                            kw[4 * (j >> 1) + 2 * (j & 1)] = w[j];
+                        }
+                    }
                     *reinterpret_cast<uint4 *>(ex + 512 + lane * 16) = vx;
                 }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scales go by tcgen05.cp
                 // the largest value exponent of the keys that exist, 255 (NaN) left out
                 const int keys = min(TN, g.ctx + g.nodes - (g.kv0 + i) * TN);
                 const bool part = keys < TN || vb != (1u << NSB) - 1u;
@@ -696,9 +736,14 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     s.care[info] = nan || part;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.x_full[xs]);
+                if (lane == 0) {
+                    mbar_arrive(&s.k_full[slot]);
+                    mbar_arrive(&s.c_full[slot]);
+                }
+                ++tile;
             }
             pos += tiles;
+            if (pos < w1) next_segment<D, RT>(p, g, pos, w1);
         }
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA issue: a thread a product
@@ -709,8 +754,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         const bool one = elect_one();
         int tile = 0;  // of the block so far
         uint32_t qph = 0;
+        Segment g = first;
         for (int pos = w0; pos < w1 && ok; qph ^= 1u) {
-            const Segment g = segment(pos);
             const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0);
             if (!value) ok = wait(&s.q_full, qph);
             for (int i = 0; i < tiles && ok; ++i, ++tile) {
@@ -731,15 +776,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 } else {
                     const int slot = tile % S::NSLOT;
                     // S takes the place of the P of two tiles before
-                    ok = wait(&s.k_code[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait(&s.sf_full[buf], bph) &&
+                    ok = wait(&s.k_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) &&
                          (tile < 2 || wait(&s.pv_done[buf], bph ^ 1u));
                     if (!ok) break;
                     fence_after();
                     constexpr int RB = D < 128 ? 64 : 128;
                     const uint64_t bd = desc_codes<RB>(smem_u32(base + S::oK) + slot * S::SLOT);
                     const uint64_t ad = desc_codes<128>(smem_u32(base + S::oQ));
+                    const uint64_t xd = desc_scales(smem_u32(base + S::oExp) + slot * 1024);
                     const uint32_t sfb = tmem + S::CB + 4 * buf;
                     if (one) {
+                        copy_scales(sfb, xd);  // in order with the MMAs of this thread
 #pragma unroll
                         for (int part = 0; part < 2; ++part)  // Q's upper and lower parts
 #pragma unroll
@@ -760,108 +807,101 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 __syncwarp();
             }
             pos += tiles;
+            if (pos < w1) next_segment<D, RT>(p, g, pos, w1);
         }
         // the last products must be done before tensor memory goes back (bounded)
         if (tile > 0)
             (void)wait(value ? &s.pv_done[(tile - 1) & 1] : &s.s_full[(tile - 1) & 1], (uint32_t)(((tile - 1) >> 1) & 1));
     } else if (warp >= kSoftWarps) {
-        // ------------------------------------------------------------ values to f16; key scales
+        // ------------------------------------------------------------ values to f16
         const int dw = warp - kSoftWarps;
-        constexpr int NQ = D / 64, RPW = TN / kDeqWarps, PASSES = RPW / 8 * NQ;
-        int kt = 0, vt = 0;  // tiles of the block so far: key scales, values
-        // Conflict-free on both sides: in a quarter-warp, four 16-code chunks of an even row and
-        // four of the next row from another 64-channel column (other banks in the codes; odd
-        // against even 16-byte units in the swizzled f16 rows).
-        const int ci = lane & 3, cj = (lane >> 2) & 1, cr = dw * RPW + 2 * (lane >> 3) + cj;
+        // A lane takes 32-channel blocks: two 16-byte loads of codes, one scale, four 16-byte stores.
+        // Eight lanes of a quarter-warp: four rows (8-row atom rows 4 a .. 4 a + 3), two neighbouring
+        // blocks of a 64-channel column: their stores hit all eight 16-byte units of the swizzled
+        // f16 rows; their loads, of alternating columns, every bank twice.
+        constexpr int NC = D / 64, RPW = TN / kDeqWarps, PASSES = RPW * NC * 2 / 32;
+        const int b2 = lane & 1, rj = (lane >> 1) & 3, rg = lane >> 3;  // block of the column, row of four, group
+        int tile = 0;
+        Segment g = first;
         for (int pos = w0; pos < w1 && ok;) {
-            const Segment g = segment(pos);
             const int tiles = g.kv1 - g.kv0;
-            for (int i = -1; i < tiles; ++i) {
-                if (i + 1 < tiles) {
-                    if (dw < 4) {  // a warp a quarter of tensor memory's lanes: each holds all scales
-                        const int xs = kt % kExps;
-                        ok = wait(&s.x_full[xs], (uint32_t)((kt / kExps) & 1)) &&
-                             (kt < 2 || wait(&s.s_full[kt & 1], (uint32_t)((kt >> 1) & 1) ^ 1u));
-                        if (!ok) break;
-                        fence_after();
-                        const uint8_t *ex = base + S::oExp + xs * 1024;
-                        uint32_t f[4];  // column c: keys 32 c + lane (dim 256: keys 32 (c % 2) + lane, word c / 2)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            f[c] = D == 64    ? *reinterpret_cast<const uint16_t *>(ex + (32 * c + lane) * 2)
-                                   : D == 128 ? *reinterpret_cast<const uint32_t *>(ex + (32 * c + lane) * 4)
-                                              : *reinterpret_cast<const uint32_t *>(ex + (32 * (c & 1) + lane) * 8 + 4 * (c >> 1));
-                        st_cols(tmem + ((uint32_t)(32 * dw) << 16) + S::CB + 4 * (kt & 1), f);
-                        wait_st();
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.sf_full[kt & 1]);
-                    }
-                    ++kt;
-                }
-                if (i < 0) continue;
-                const int slot = vt % S::NSLOT, xs = vt % kExps, buf = vt & 1, info = vt % kInfo;
-                ok = wait(&s.x_full[xs], (uint32_t)((vt / kExps) & 1)) &&
-                     wait(&s.v_code[slot], (uint32_t)((vt / S::NSLOT) & 1)) &&
-                     (vt < 2 || wait(&s.pv_done[buf], (uint32_t)((vt >> 1) & 1) ^ 1u));
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                const int slot = tile % S::NSLOT, buf = tile & 1, info = tile % kInfo;
+                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) &&
+                     (tile < 2 || wait(&s.pv_done[buf], (uint32_t)((tile >> 1) & 1) ^ 1u));
                 if (!ok) break;
-                const uint8_t *src = base + S::oRing + slot * S::SLOT, *ex = base + S::oExp + xs * 1024 + 512;
+                const uint8_t *src = base + S::oRing + slot * S::SLOT, *ex = base + S::oExp + slot * 1024 + 512;
                 uint8_t *dst = base + S::oV + buf * S::F16;
                 const int E = s.ev[info] - kShift;
-                uint4 w[PASSES];
+                const bool care = s.care[info];  // missing keys and NaN blocks count as zeros
+                uint4 w[PASSES][2];
                 int e[PASSES];
 #pragma unroll
                 for (int ps = 0; ps < PASSES; ++ps) {  // every load before the first store
-                    const int row = cr + (ps / NQ) * 8, ch = ci + 4 * ((cj + ps) % NQ);
-                    w[ps] = *reinterpret_cast<const uint4 *>(src + row * D + ch * 16);
-                    e[ps] = ex[row * S::EB + (ch >> 1)];
+                    const int q = ps * 4 + rg;  // four-row group and column of the warp's part
+                    const int row = dw * RPW + (q / NC) * 4 + rj, col = NC == 1 ? 0 : (q + rj) % NC;
+                    const uint8_t *c = src + row * D + col * 64 + b2 * 32;
+                    w[ps][0] = *reinterpret_cast<const uint4 *>(c);
+                    w[ps][1] = *reinterpret_cast<const uint4 *>(c + 16);
+                    e[ps] = ex[row * S::EB + 2 * col + b2];
                 }
-                if (s.care[info]) {  // missing keys and NaN blocks count as zeros
+                if (care) {
                     const int keys = g.ctx + g.nodes - (g.kv0 + i) * TN;
                     const uint32_t vb = (uint32_t)s.valid[info];
 #pragma unroll
                     for (int ps = 0; ps < PASSES; ++ps) {
-                        const int row = cr + (ps / NQ) * 8;
+                        const int row = dw * RPW + ((ps * 4 + rg) / NC) * 4 + rj;
                         if (row >= keys || !((vb >> (row >> 4)) & 1) || e[ps] == 255) {
-                            w[ps] = make_uint4(0, 0, 0, 0);
+                            w[ps][0] = w[ps][1] = make_uint4(0, 0, 0, 0);
                             e[ps] = 0;
                         }
                     }
                 }
 #pragma unroll
                 for (int ps = 0; ps < PASSES; ++ps) {
-                    const int row = cr + (ps / NQ) * 8, ch = ci + 4 * ((cj + ps) % NQ);
-                    uint4 lo, hi;
-                    widen16(w[ps], f16_pow2(e[ps] - E), lo, hi);
-                    uint8_t *d = dst + (ch >> 2) * (TN * 128) + row * 128;
-                    const int u = 2 * (ch & 3), x = row & 7;
-                    *reinterpret_cast<uint4 *>(d + ((u ^ x) << 4)) = lo;
-                    *reinterpret_cast<uint4 *>(d + (((u + 1) ^ x) << 4)) = hi;
+                    const int q = ps * 4 + rg;
+                    const int row = dw * RPW + (q / NC) * 4 + rj, col = NC == 1 ? 0 : (q + rj) % NC;
+                    const uint32_t sc = f16_pow2(e[ps] - E);
+                    uint8_t *d = dst + col * (TN * 128) + row * 128;
+                    const int x = row & 7;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 lo, hi;
+                        widen16(w[ps][h], sc, lo, hi);
+                        const int u = 4 * b2 + 2 * h;
+                        *reinterpret_cast<uint4 *>(d + ((u ^ x) << 4)) = lo;
+                        *reinterpret_cast<uint4 *>(d + (((u + 1) ^ x) << 4)) = hi;
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // f16 for the MMA's reads
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&s.v_full[buf]);
-                    mbar_arrive(&s.v_free[slot]);
-                    mbar_arrive(&s.x_free[xs]);
+                    mbar_arrive(&s.c_free[slot]);
                 }
-                ++vt;
             }
             pos += tiles;
+            if (pos < w1) next_segment<D, RT>(p, g, pos, w1);
         }
     } else {
         // ------------------------------------------------------------ softmax and output
-        const int set = warp >> 2, quad = warp & 3;                // tiles of one parity; tensor memory lanes
+        const int set = warp >> 2, quad = warp & 3;                // half of the columns; tensor memory lanes
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
         const int row = (32 * quad + lane) % RT;                   // row of the tile
-        const int copy = 32 * quad / RT, col0 = copy * CPT;        // this copy's key columns
+        const int copy = 32 * quad / RT, col0 = (2 * copy + set) * CPT;  // this copy's and set's key columns
         int it = 0;
-        uint32_t soft_ph = 0, set_ph = 0;
+        uint32_t soft_ph = 0, set_ph = 0, pair_ph = 0;
         auto soft_sync = [&]() -> bool {  // all softmax warps
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.soft);
             soft_ph ^= 1u;
             return wait(&s.soft, soft_ph ^ 1u);
+        };
+        auto pair_sync = [&]() -> bool {  // the two warps of the same rows
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.pair[quad]);
+            pair_ph ^= 1u;
+            return wait(&s.pair[quad], pair_ph ^ 1u);
         };
         auto set_sync = [&]() -> bool {   // the set's four
             __syncwarp();
@@ -938,17 +978,18 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         }
         // Per turn: the next segment's Q (once the last S of the one before is there), then the output
         // of the one before, then the segment's tiles.
-        Segment g{};
+        Segment g = first;
         int r = 0, t = 0, hq = 0;          // row of the request and head; its node and query head
         bool real = false;
-        float m = 0.0f, l = 0.0f;          // of the set's tiles; l in units of 2^(m - bias)
+        float m = 0.0f, l = 0.0f;          // the copy's maximum; the thread's sum in units of 2^(m - bias)
         uint32_t nanblk = 0;
         for (int pos = w0; ok;) {
             const bool more = pos < w1;
             Segment next{};
             int eq = 0;
             if (more) {
-                next = segment(pos);
+                next = g;
+                if (it > 0) next_segment<D, RT>(p, next, pos, w1);
                 if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
                 if (!ok) break;
                 fence_after();
@@ -964,7 +1005,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 s.nan[warp][lane] = nanblk;
                 ok = soft_sync();
                 if (!ok) break;
-                // a copy's maximum is the later of its two sets'; copies and sets are added in order
+                // a copy's two sets have the same maximum; copies and sets are added in order
                 float M = -INFINITY, mc = -INFINITY, L = 0.0f;
 #pragma unroll
                 for (int q = 0; q < REP; ++q) {
@@ -1066,17 +1107,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             nanblk = 0;
             const int32_t *mrow = p.mask ? p.mask + ((size_t)g.b * p.T + t) * p.W : nullptr;
             for (int i = 0; i < tiles && ok; ++i, ++it) {
-                if ((it & 1) != set) continue;
-                const int info = it % kInfo;
+                const int info = it % kInfo, buf = it & 1;
                 const uint32_t tph = (uint32_t)((it >> 1) & 1);
-                ok = wait(&s.s_full[set], tph);
+                ok = wait(&s.s_full[buf], tph);
                 if (!ok) break;
                 fence_after();
-                const uint32_t tb = tl + S::CS + set * TN, ts = tb + col0;
-                const int slot0 = (g.kv0 + i) * TN + col0;                // cache slot of the thread's first column
+                const uint32_t tb = tl + S::CS + buf * TN, ts = tb + col0;
+                const int slot0 = (g.kv0 + i) * TN + col0;  // cache slot of the thread's first column
                 const uint32_t vb = (uint32_t)s.valid[info];
                 const bool masked = (g.kv0 + i + 1) * TN > g.ctx || vb != (1u << (TN / 16)) - 1u;
-                // visible keys among columns [k, k + CH) of the thread
+                // visible keys among columns [k, k + 32) of the thread
                 auto seen = [&](int k) -> uint32_t {
                     const int s0 = slot0 + k, j0 = s0 - g.ctx;  // node of the first column (negative: context)
                     uint32_t w = low_bits(-j0);
@@ -1094,103 +1134,116 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     }
                     const uint32_t gb = vb >> ((col0 + k) >> 4);
                     w &= ((gb & 1u) ? 0x0000FFFFu : 0u) | ((gb & 2u) ? 0xFFFF0000u : 0u);
-                    return CH < 32 ? w & ((1u << (CH & 31)) - 1u) : w;
+                    return w;
                 };
-                uint32_t x[CH];
-                auto load = [&](int k) {  // S of columns [k, k + CH), -inf where not seen
-                    ld_cols(ts + k, x);
-                    wait_ld();
-                    if (masked) {
+                if (masked) {  // S of what a row does not see becomes -inf, in place
+                    constexpr int MC = CPT < 32 ? CPT : 32;
+#pragma unroll 1
+                    for (int k = 0; k < CPT; k += MC) {
                         const uint32_t w = seen(k);
+                        uint32_t y[MC];
+                        ld_cols(ts + k, y);
+                        wait_ld();
 #pragma unroll
-                        for (int j = 0; j < CH; ++j) x[j] = (w >> j) & 1u ? x[j] : 0xFF800000u;
+                        for (int j = 0; j < MC; ++j) y[j] = (w >> j) & 1u ? y[j] : 0xFF800000u;
+                        st_cols(ts + k, y);
                     }
-                };
-                // ---- the maximum, joined with that of the tiles before (the other set's last)
-                float mt = -INFINITY;
+                    wait_st();
+                }
+                // ---- p = 2^(x - m + bias) of the thread's columns with the m so far: after a segment's
+                // first tiles the maximum hardly ever passes it by more than the slack, and one pass
+                // does.  Else a second one, with the m that the first found.
+                uint32_t pk[CPT / 2];
+                uint64_t sum;
+                const float mp = m;
+                bool again = false;
 #pragma unroll 1
-                for (int k = 0; k < CPT; k += CH) {
-                    load(k);
+                while (true) {
+                    const float off = m == -INFINITY ? 0.0f : kBias - m;
+                    const uint64_t c2 = pair(c, c), off2 = pair(off, off);
                     float m0 = -INFINITY, m1 = -INFINITY;
+                    sum = pair(0.0f, 0.0f);
+                    uint32_t x[CPT > CH ? 2 : 1][CH];
+                    ld_cols(ts, x[0]);
+                    wait_ld();
 #pragma unroll
-                    for (int j = 0; j < CH; j += 4) {
-                        m0 = max3(m0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
-                        m1 = max3(m1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                    for (int k = 0; k < CPT; k += CH) {
+                        uint32_t(&y)[CH] = x[CPT > CH ? (k / CH) & 1 : 0];
+                        if constexpr (CPT > CH)
+                            if (k + CH < CPT) ld_cols(ts + k + CH, x[(k / CH + 1) & 1]);  // on its way meanwhile
+#pragma unroll
+                        for (int j = 0; j < CH; j += 4) {
+                            m0 = max3(m0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                            m1 = max3(m1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < CH; j += 2) {
+                            float a, b;
+                            fma2(a, b, y[j], y[j + 1], c2, off2);
+                            a = ex2(a);
+                            b = ex2(b);
+                            sum = add2(sum, pair(a, b));
+                            pk[(k + j) / 2] = pack_f16(a, b);
+                        }
+                        if (CPT > CH) wait_ld();
                     }
-                    mt = max3(mt, m0, m1);
-                }
-                mt = mt == -INFINITY ? mt : mt * c;
-                float mp = -INFINITY;
-                if (i > 0) {
-                    ok = wait(&s.m_full[set ^ 1][quad], (uint32_t)(((it - 1) >> 1) & 1));
+                    if (!again) s.mrow[buf][set][32 * quad + lane] = fmaxf(m0, m1);
+                    fence_before();
+                    ok = pair_sync();  // S is read by both before either's P is written over it
                     if (!ok) break;
-                    mp = s.mrow[set ^ 1][32 * quad + lane];
+                    fence_after();
+                    if (again) break;
+                    const float mt = fmaxf(s.mrow[buf][0][32 * quad + lane], s.mrow[buf][1][32 * quad + lane]);
+                    const float me = mt == -INFINITY ? mt : mt * c;
+                    if (me > m + kSlack) m = me;  // also out of -inf
+                    again = __any_sync(0xFFFFFFFFu, m != mp);
+                    if (!again) break;
                 }
-                const bool grow = mt > mp + kSlack;  // also out of -inf
-                const float mn = grow ? mt : mp;
-                s.mrow[set][32 * quad + lane] = mn;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.m_full[set][quad]);
-                const float off = mn == -INFINITY ? 0.0f : kBias - mn;
-                const uint64_t c2 = pair(c, c), off2 = pair(off, off);
-                // ---- p, its sum, and P (over S; a chunk's P lands on columns already read)
-                uint64_t sum = pair(0.0f, 0.0f);
-#pragma unroll 1
-                for (int k = 0; k < CPT; k += CH) {
-                    if (CPT > CH) load(k);
-                    uint32_t pk[CH / 2];
-#pragma unroll
-                    for (int j = 0; j < CH; j += 2) {
-                        float a, b;
-                        fma2(a, b, x[j], x[j + 1], c2, off2);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum = add2(sum, pair(a, b));
-                        pk[j / 2] = pack_f16(a, b);
-                    }
-                    st_cols(tb + (col0 + k) / 2, pk);
-                }
-                if constexpr (REP > 1) {  // the copy's P is zero at the other copies' keys
+                if (!ok) break;
+                const bool grow = m != mp;
+                // ---- P over S, zeros at the other copies' keys (a set every other piece)
+                st_cols(tb + col0 / 2, pk);
+                if constexpr (REP > 1) {
                     const uint32_t z[CPT / 2] = {};
 #pragma unroll
                     for (int q = 0; q < REP; ++q)
-                        if (q != copy) st_cols(tb + q * (CPT / 2), z);
+                        if (q != copy) st_cols(tb + (2 * q + set) * (CPT / 2), z);
                 }
-                // ---- O in the units of the new maximum and value exponent
-                ok = wait(&s.v_full[set], tph);
+                // ---- O in the units of the new maximum and value exponent, half of the channels a set
+                ok = wait(&s.v_full[buf], tph);
                 if (!ok) break;
                 if (i > 0) {
                     const int evp = s.ev[(it - 1) % kInfo], evn = s.ev[info];
                     if (__any_sync(0xFFFFFFFFu, grow || evn != evp)) {
-                        ok = wait(&s.pv_done[set ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
+                        ok = wait(&s.pv_done[buf ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
                         if (!ok) break;
                         fence_after();
-                        const float f = (grow ? (mp == -INFINITY ? 0.0f : ex2(mp - mn)) : 1.0f) * pow2i(max(evp - evn, -149));
+                        const float f = (grow ? (mp == -INFINITY ? 0.0f : ex2(mp - m)) : 1.0f) * pow2i(max(evp - evn, -149));
 #pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            uint32_t o[32];
+                        for (int k = set * (D / 2); k < (set + 1) * (D / 2); k += 16) {
+                            uint32_t o[16];
                             ld_cols(tl + S::CO + k, o);
                             wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                             st_cols(tl + S::CO + k, o);
                         }
                     }
                 }
-                l = l * (mn == m ? 1.0f : m == -INFINITY ? 0.0f : ex2(m - mn)) + sum_pair(sum);
-                m = mn;
+                l = l * (!grow ? 1.0f : mp == -INFINITY ? 0.0f : ex2(mp - m)) + sum_pair(sum);
                 if (s.vnan[info]) {
 #pragma unroll 1
-                    for (int k = 0; k < CPT; k += CH) {
+                    for (int k = 0; k < CPT; k += 32) {
                         const uint32_t w = real ? (masked ? seen(k) : 0xFFFFFFFFu) : 0u;
-                        for (int j = 0; j < CH; ++j)
+#pragma unroll 1
+                        for (int j = 0; j < CPT - k && j < 32; ++j)
                             if ((w >> j) & 1u) nanblk |= s.nanblk[info][col0 + k + j];
                     }
                 }
                 wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[set]);
+                if (lane == 0) mbar_arrive(&s.p_full[buf]);
             }
             if (!ok) break;
         }
