@@ -54,7 +54,7 @@ namespace {
 
 constexpr int kAttendBlocks = 152;   // one an SM of a GB300 (no block waits for another)
 constexpr int kMaxBatch = 1024;
-constexpr int kSoftWarps = 8;        // two sets of four, half of a copy's key columns each
+constexpr int kSoftWarps = 8;        // two sets of four, a set every other tile
 constexpr int kDeqWarps = 8;
 constexpr int kProducerWarp = kSoftWarps + kDeqWarps, kScoutWarp = kProducerWarp + 1;
 constexpr int kMmaWarp = kScoutWarp + 1;  // two: S, O
@@ -479,7 +479,7 @@ struct AttendShared {
     uint64_t s_full[2];             // S written
     uint64_t p_full[2];             // P written, O rescaled
     uint64_t pv_done[2];            // O updated, P and the f16 values read
-    uint64_t pair[4];               // the two softmax warps of the same rows
+    uint64_t m_full[2][4];          // a softmax warp's rows have their maximum of the tile
     uint64_t q_full;                // a segment's Q is in place
     uint64_t soft, set[2];          // the softmax warps' own barriers (bounded, unlike bar.sync)
     uint32_t tmem;
@@ -487,7 +487,7 @@ struct AttendShared {
     int ev[kInfo], vnan[kInfo];     // the segment's value exponent at the tile; a value block holds NaN
     int care[kInfo];                // the tile's values need care: missing keys, NaN
     uint8_t nanblk[kInfo][128];     // then: each key's NaN blocks
-    float mrow[2][2][128];          // a tile's maxima of the rows' halves (tiles in turn)
+    float mrow[2][128];             // the rows' maxima, handed from set to set
     float2 stat[kSoftWarps][32];
     uint32_t nan[kSoftWarps][32];
     int scan[32];
@@ -498,8 +498,8 @@ struct AttendShared {
 template <int D, int RT>
 __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     using S = Shape<D>;
-    constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP / 2;  // CPT: key columns a thread
-    constexpr int CH = CPT <= 32 ? CPT : 16;                       // taken CH at a time
+    constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP;  // CPT: key columns a thread
+    constexpr int CH = CPT <= 32 ? CPT : CPT == 64 ? 16 : 32;  // taken CH at a time
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
     __shared__ AttendShared s;
@@ -512,12 +512,13 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             mbar_init(&s.k_free[i], 1);
             mbar_init(&s.c_full[i], 2);
             mbar_init(&s.c_free[i], kDeqWarps);
-            mbar_init(&s.pair[i], 2);
+            mbar_init(&s.m_full[0][i], 1);
+            mbar_init(&s.m_full[1][i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.v_full[i], kDeqWarps);
             mbar_init(&s.s_full[i], 1);
-            mbar_init(&s.p_full[i], kSoftWarps);
+            mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.set[i], 4);
         }
@@ -885,23 +886,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         }
     } else {
         // ------------------------------------------------------------ softmax and output
-        const int set = warp >> 2, quad = warp & 3;                // half of the columns; tensor memory lanes
+        const int set = warp >> 2, quad = warp & 3;                // tiles of one parity; tensor memory lanes
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
         const int row = (32 * quad + lane) % RT;                   // row of the tile
-        const int copy = 32 * quad / RT, col0 = (2 * copy + set) * CPT;  // this copy's and set's key columns
+        const int copy = 32 * quad / RT, col0 = copy * CPT;        // this copy's key columns
         int it = 0;
-        uint32_t soft_ph = 0, set_ph = 0, pair_ph = 0;
+        uint32_t soft_ph = 0, set_ph = 0;
         auto soft_sync = [&]() -> bool {  // all softmax warps
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.soft);
             soft_ph ^= 1u;
             return wait(&s.soft, soft_ph ^ 1u);
-        };
-        auto pair_sync = [&]() -> bool {  // the two warps of the same rows
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.pair[quad]);
-            pair_ph ^= 1u;
-            return wait(&s.pair[quad], pair_ph ^ 1u);
         };
         auto set_sync = [&]() -> bool {   // the set's four
             __syncwarp();
@@ -981,7 +976,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         Segment g = first;
         int r = 0, t = 0, hq = 0;          // row of the request and head; its node and query head
         bool real = false;
-        float m = 0.0f, l = 0.0f;          // the copy's maximum; the thread's sum in units of 2^(m - bias)
+        float m = 0.0f, l = 0.0f;          // the rows' maximum at the set's last tile; its sum in 2^(m - bias)
         uint32_t nanblk = 0;
         for (int pos = w0; ok;) {
             const bool more = pos < w1;
@@ -1005,7 +1000,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 s.nan[warp][lane] = nanblk;
                 ok = soft_sync();
                 if (!ok) break;
-                // a copy's two sets have the same maximum; copies and sets are added in order
+                // a copy's maximum is the later of its two sets'; copies and sets are added in order
                 float M = -INFINITY, mc = -INFINITY, L = 0.0f;
 #pragma unroll
                 for (int q = 0; q < REP; ++q) {
@@ -1107,7 +1102,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             nanblk = 0;
             const int32_t *mrow = p.mask ? p.mask + ((size_t)g.b * p.T + t) * p.W : nullptr;
             for (int i = 0; i < tiles && ok; ++i, ++it) {
-                const int info = it % kInfo, buf = it & 1;
+                if ((it & 1) != set) continue;
+                const int info = it % kInfo, buf = set;
                 const uint32_t tph = (uint32_t)((it >> 1) & 1);
                 ok = wait(&s.s_full[buf], tph);
                 if (!ok) break;
@@ -1150,66 +1146,103 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     }
                     wait_st();
                 }
-                // ---- p = 2^(x - m + bias) of the thread's columns with the m so far: after a segment's
-                // first tiles the maximum hardly ever passes it by more than the slack, and one pass
-                // does.  Else a second one, with the m that the first found.
-                uint32_t pk[CPT / 2];
+                const float ml = m;    // the rows' m at the set's last tile, and
+                float mp = -INFINITY;  // at the tile before, the other set's
+                // from the thread's largest S: the rows' m at this tile, handed on to the other set
+                auto settle = [&](float mt) -> bool {
+                    if (i > 0) {
+                        if (!wait(&s.m_full[set ^ 1][quad], (uint32_t)(((it - 1) >> 1) & 1))) return false;
+                        mp = s.mrow[set ^ 1][32 * quad + lane];
+                    }
+                    const float me = mt == -INFINITY ? mt : mt * c;
+                    m = me > mp + kSlack ? me : mp;  // also out of -inf
+                    s.mrow[set][32 * quad + lane] = m;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.m_full[set][quad]);
+                    return true;
+                };
                 uint64_t sum;
-                const float mp = m;
-                bool again = false;
+                // p = 2^(x - m + bias) of a chunk, its sum and its f16 pairs
+                auto powers = [&](const uint32_t (&y)[CH], uint64_t c2, uint64_t off2, uint32_t *out) {
+#pragma unroll
+                    for (int j = 0; j < CH; j += 2) {
+                        float a, b;
+                        fma2(a, b, y[j], y[j + 1], c2, off2);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum = add2(sum, pair(a, b));
+                        out[j / 2] = pack_f16(a, b);
+                    }
+                };
+                auto largest = [&](const uint32_t (&y)[CH], float &m0, float &m1) {
+#pragma unroll
+                    for (int j = 0; j < CH; j += 4) {
+                        m0 = max3(m0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                        m1 = max3(m1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
+                    }
+                };
+                float m0 = -INFINITY, m1 = -INFINITY;
+                if constexpr (CPT <= 64) {
+                    // One pass, with the set's last m: after a segment's first tiles the maximum hardly
+                    // ever passes it by more than the slack.  Else a second, with the m that the first
+                    // found.  P waits in registers for that, as it takes S's place.
+                    uint32_t pk[CPT / 2];
+                    bool again = false;
 #pragma unroll 1
-                while (true) {
+                    while (true) {
+                        const float off = m == -INFINITY ? 0.0f : kBias - m;
+                        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                        sum = pair(0.0f, 0.0f);
+                        uint32_t x[CPT > CH ? 2 : 1][CH];
+                        ld_cols(ts, x[0]);
+                        wait_ld();
+#pragma unroll
+                        for (int k = 0; k < CPT; k += CH) {
+                            uint32_t(&y)[CH] = x[CPT > CH ? (k / CH) & 1 : 0];
+                            if constexpr (CPT > CH)
+                                if (k + CH < CPT) ld_cols(ts + k + CH, x[(k / CH + 1) & 1]);  // on its way meanwhile
+                            largest(y, m0, m1);
+                            powers(y, c2, off2, pk + k / 2);
+                            if (CPT > CH) wait_ld();
+                        }
+                        if (again) break;
+                        ok = settle(fmaxf(m0, m1));
+                        again = __any_sync(0xFFFFFFFFu, m != ml);
+                        if (!ok || !again) break;
+                    }
+                    if (!ok) break;
+                    st_cols(tb + col0 / 2, pk);
+                    if constexpr (REP > 1) {  // P is zero at the other copies' keys
+                        const uint32_t z[CPT / 2] = {};
+#pragma unroll
+                        for (int q = 0; q < REP; ++q)
+                            if (q != copy) st_cols(tb + q * (CPT / 2), z);
+                    }
+                } else {
+                    // Two passes: 64 registers of P on top of the rest would spill.
+#pragma unroll 1
+                    for (int k = 0; k < CPT; k += CH) {
+                        uint32_t y[CH];
+                        ld_cols(ts + k, y);
+                        wait_ld();
+                        largest(y, m0, m1);
+                    }
+                    ok = settle(fmaxf(m0, m1));
+                    if (!ok) break;
                     const float off = m == -INFINITY ? 0.0f : kBias - m;
                     const uint64_t c2 = pair(c, c), off2 = pair(off, off);
-                    float m0 = -INFINITY, m1 = -INFINITY;
                     sum = pair(0.0f, 0.0f);
-                    uint32_t x[CPT > CH ? 2 : 1][CH];
-                    ld_cols(ts, x[0]);
-                    wait_ld();
-#pragma unroll
-                    for (int k = 0; k < CPT; k += CH) {
-                        uint32_t(&y)[CH] = x[CPT > CH ? (k / CH) & 1 : 0];
-                        if constexpr (CPT > CH)
-                            if (k + CH < CPT) ld_cols(ts + k + CH, x[(k / CH + 1) & 1]);  // on its way meanwhile
-#pragma unroll
-                        for (int j = 0; j < CH; j += 4) {
-                            m0 = max3(m0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                            m1 = max3(m1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
-                        }
-#pragma unroll
-                        for (int j = 0; j < CH; j += 2) {
-                            float a, b;
-                            fma2(a, b, y[j], y[j + 1], c2, off2);
-                            a = ex2(a);
-                            b = ex2(b);
-                            sum = add2(sum, pair(a, b));
-                            pk[(k + j) / 2] = pack_f16(a, b);
-                        }
-                        if (CPT > CH) wait_ld();
+#pragma unroll 1
+                    for (int k = 0; k < CPT; k += CH) {  // a chunk's P lands on columns already read
+                        uint32_t y[CH], pk[CH / 2];
+                        ld_cols(ts + k, y);
+                        wait_ld();
+                        powers(y, c2, off2, pk);
+                        st_cols(tb + k / 2, pk);
                     }
-                    if (!again) s.mrow[buf][set][32 * quad + lane] = fmaxf(m0, m1);
-                    fence_before();
-                    ok = pair_sync();  // S is read by both before either's P is written over it
-                    if (!ok) break;
-                    fence_after();
-                    if (again) break;
-                    const float mt = fmaxf(s.mrow[buf][0][32 * quad + lane], s.mrow[buf][1][32 * quad + lane]);
-                    const float me = mt == -INFINITY ? mt : mt * c;
-                    if (me > m + kSlack) m = me;  // also out of -inf
-                    again = __any_sync(0xFFFFFFFFu, m != mp);
-                    if (!again) break;
                 }
-                if (!ok) break;
                 const bool grow = m != mp;
-                // ---- P over S, zeros at the other copies' keys (a set every other piece)
-                st_cols(tb + col0 / 2, pk);
-                if constexpr (REP > 1) {
-                    const uint32_t z[CPT / 2] = {};
-#pragma unroll
-                    for (int q = 0; q < REP; ++q)
-                        if (q != copy) st_cols(tb + (2 * q + set) * (CPT / 2), z);
-                }
-                // ---- O in the units of the new maximum and value exponent, half of the channels a set
+                // ---- O in the units of the new maximum and value exponent
                 ok = wait(&s.v_full[buf], tph);
                 if (!ok) break;
                 if (i > 0) {
@@ -1220,17 +1253,17 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                         fence_after();
                         const float f = (grow ? (mp == -INFINITY ? 0.0f : ex2(mp - m)) : 1.0f) * pow2i(max(evp - evn, -149));
 #pragma unroll 1
-                        for (int k = set * (D / 2); k < (set + 1) * (D / 2); k += 16) {
-                            uint32_t o[16];
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
                             ld_cols(tl + S::CO + k, o);
                             wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                             st_cols(tl + S::CO + k, o);
                         }
                     }
                 }
-                l = l * (!grow ? 1.0f : mp == -INFINITY ? 0.0f : ex2(mp - m)) + sum_pair(sum);
+                l = l * (m == ml ? 1.0f : ml == -INFINITY ? 0.0f : ex2(ml - m)) + sum_pair(sum);
                 if (s.vnan[info]) {
 #pragma unroll 1
                     for (int k = 0; k < CPT; k += 32) {
