@@ -56,6 +56,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libbsf8.so (building it first if it is missing and nvcc is available)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -425,6 +427,15 @@ def get_option(option: int) -> int:
 
 # ----------------------------------------------------------------------- decode operators
 
-from .decode import (  # noqa: E402
-    MAX_NODES, KVCache, kv_commit, kv_read, qkv_append, tree_attention, tree_attention_workspace_bytes, verify_tree,
-)
+# decode.py imports torch, which the rest of this module only does when a call needs it.
+_DECODE = ("KVCache", "qkv_append", "kv_read", "tree_attention", "tree_attention_workspace_bytes", "verify_tree",
+           "kv_commit", "MAX_NODES")
+
+
+def __getattr__(name):
+    if name in _DECODE:
+        from . import decode
+        for n in _DECODE:
+            globals()[n] = getattr(decode, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
