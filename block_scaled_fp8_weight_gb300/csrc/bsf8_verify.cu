@@ -28,11 +28,20 @@ constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kNodes = 256;        // BSF8_MAX_NODES
 constexpr int kMaxVCluster = 8;    // the portable cluster size
+constexpr int kBatch = 4;          // 16-byte loads of a row a thread has in flight
 typedef unsigned long long u64;
 constexpr u64 kOne = 1ull << 40;
 
-__device__ __forceinline__ u64 fix(float p) {  // floor(p * 2^40), p clamped to [0, 1], NaN as 0
-    return __float2ull_rz(fminf(fmaxf(p, 0.0f), 1.0f) * 1099511627776.0f);
+// floor(p * 2^40), p clamped to [0, 1], NaN as 0, in two steps of 20 bits: adding 2^23 towards zero
+// leaves floor(x) in the low bits of the sum (0 <= x < 2^23), and the rest is exact in fp32.  The
+// conversion instruction to 64 bits runs at a small part of the rate of these.
+__device__ __forceinline__ u64 fix(float p) {
+    const float x = fminf(fmaxf(p, 0.0f), 1.0f) * 1048576.0f;
+    const float t = __fadd_rz(x, 8388608.0f);
+    const float r = (x - (t - 8388608.0f)) * 1048576.0f;
+    const uint32_t hi = __float_as_uint(t) & 0x7FFFFFu;
+    const uint32_t lo = __float_as_uint(__fadd_rz(r, 8388608.0f)) & 0x7FFFFFu;
+    return (u64)hi * 1048576u + lo;
 }
 
 __device__ __forceinline__ u64 times(u64 q, u64 z) {  // floor(q z / 2^40)
@@ -69,15 +78,24 @@ struct VerifyShared {
     u64 total;                 // the mass Z of R
     int cur, rej, next, count; // the walk's node, rejections there, next child, nodes kept
     int done, summed;          // no child is left to ask; the sums are those of the present R
+    int small;                 // every Z here is below 2^42
+    int stop;                  // both: the draw is next
     u64 at;                    // the draw's threshold inside a warp's part
     int warp;                  // that warp, or -1
 };
 
+// floor(q z / 2^40) for q <= 2^40 and z < 2^42, from parts of 20 bits.
+__device__ __forceinline__ u64 times20(u64 q, uint32_t zh, uint32_t zl) {
+    const uint32_t qh = (uint32_t)(q >> 20), ql = (uint32_t)q & 0xFFFFFu;
+    return (u64)qh * zh + (((u64)qh * zl + (u64)ql * zh + (((u64)ql * zl) >> 20)) >> 20);
+}
+
 // R of element x, whose fixed-point probabilities at the walk's node are P and Q.
 __device__ __forceinline__ u64 left_of(u64 P, u64 Q, int x, const VerifyShared &s, bool drawn) {
     if (drawn) {
-        u64 off = 0;
-        for (int j = 0; j < s.rej; ++j) off += s.Z[j] == kOne ? Q : times(Q, s.Z[j]);
+        u64 off = s.rej > 0 ? Q : 0;  // the first rejection's mass is 2^40
+        for (int j = 1; j < s.rej; ++j)
+            off += s.small ? times20(Q, (uint32_t)(s.Z[j] >> 20), (uint32_t)s.Z[j] & 0xFFFFFu) : times(Q, s.Z[j]);
         return P > off ? P - off : 0;
     }
     for (int j = 0; j < s.rej; ++j)
@@ -109,9 +127,11 @@ __device__ __forceinline__ void walk(VerifyShared &s, int n, bool drawn) {
             s.cur = i;
             s.path[s.count++] = i;
             s.rej = 0;
+            s.small = 1;
             s.total = kOne;
         } else {
             s.Z[s.rej] = z;
+            if (z >= 1ull << 42) s.small = 0;
             s.gone[s.rej] = s.tok[i];
             ++s.rej;
             s.done = 0;
@@ -119,6 +139,19 @@ __device__ __forceinline__ void walk(VerifyShared &s, int n, bool drawn) {
         s.summed = 0;
     }
     s.next = i;
+}
+
+// The next thing after a sum (or the start), by thread 0: on along the walk, or, when R was all 0
+// after the last child, a sum of P instead.
+__device__ __forceinline__ void step(VerifyShared &s, int n, bool drawn) {
+    if (s.done) s.rej = 0;
+    else walk(s, n, drawn);
+    s.stop = s.done && s.summed;
+}
+
+// Cluster barrier whose lanes need not arrive together.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, int cluster, int *status) {
@@ -158,20 +191,19 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
     }
     if (tid == 0) {
         s.cur = s.rej = s.summed = s.done = 0;
+        s.small = 1;
         s.next = s.count = 1;
         s.path[0] = 0;
         s.total = kOne;
     }
     __syncthreads();
+    if (tid == 0) step(s, n, drawn);
+    __syncthreads();
 
     int per_warp = 0, mis = 0, groups = 0;  // of the last pass's row
-    for (uint32_t pass = 0;; ++pass) {
-        if (tid == 0) {
-            if (s.done) s.rej = 0;  // a second sum after the last child: R was all 0, draw from P
-            else walk(s, n, drawn);
-        }
-        __syncthreads();
-        if (s.done && s.summed) break;
+    // Thread 0 changes the walk's state only between the last two barriers of a turn, so that every
+    // thread reads the same state at its top.
+    for (uint32_t pass = 0; !s.stop; ++pass) {
         // -------------------------------------------------------------- a pass: the sums of R
         const float *prow = pb + (size_t)s.cur * a.ld;
         const float *qrow = drawn ? qb + (size_t)s.cur * a.ld : nullptr;
@@ -180,38 +212,51 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
         groups = (V + mis + 3) / 4;
         per_warp = ((groups + cluster * kVWarps - 1) / (cluster * kVWarps) + 31) / 32 * 32;
         const int g0 = (rank * kVWarps + warp) * per_warp, g1 = min(groups, g0 + per_warp);
-        u64 sum = 0;
         const int rej = s.rej;
-        if (rej == 0 || !drawn) {
-#pragma unroll 4
-            for (int g = g0 + lane; g < g1; g += 32) {
-                float pv[4];
-                load4(prow, 4 * g - mis, V, pv);
+        const bool useq = drawn && rej > 0;
+        u64 sum = 0;
+        auto add = [&](const float (&pv)[4], const float (&qv)[4], int x) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum += rej == 0 ? fix(pv[i]) : left_of(fix(pv[i]), 0, 4 * g - mis + i, s, false);
-            }
-        } else if (rej == 1) {  // Z was 2^40, so Q' = Q
-#pragma unroll 4
-            for (int g = g0 + lane; g < g1; g += 32) {
-                float pv[4], qv[4];
-                load4(prow, 4 * g - mis, V, pv);
-                load4(qrow, 4 * g - mis, V, qv);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u64 P = fix(pv[i]), Q = fix(qv[i]);
+            for (int i = 0; i < 4; ++i) {
+                const u64 P = fix(pv[i]);
+                if (rej == 0) {
+                    sum += P;
+                } else if (rej == 1 && drawn) {
+                    const u64 Q = fix(qv[i]);
                     sum += P > Q ? P - Q : 0;
+                } else {
+                    sum += left_of(P, drawn ? fix(qv[i]) : 0, x + i, s, drawn);
                 }
             }
-        } else {
-#pragma unroll 2
-            for (int g = g0 + lane; g < g1; g += 32) {
-                float pv[4], qv[4];
-                load4(prow, 4 * g - mis, V, pv);
-                load4(qrow, 4 * g - mis, V, qv);
+        };
+        // whole groups of four, kBatch loads of each row in flight; then the ragged ones
+        const int gi = max(g0, mis > 0 ? 1 : 0), ge = min(g1, (V + mis) / 4);
+        int g = gi + lane;
+        for (; g + 32 * (kBatch - 1) < ge; g += 32 * kBatch) {
+            float4 pf[kBatch], qf[kBatch];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum += left_of(fix(pv[i]), fix(qv[i]), 0, s, true);
+            for (int j = 0; j < kBatch; ++j) pf[j] = *reinterpret_cast<const float4 *>(prow + 4 * (g + 32 * j) - mis);
+            if (useq)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) qf[j] = *reinterpret_cast<const float4 *>(qrow + 4 * (g + 32 * j) - mis);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const float pv[4] = {pf[j].x, pf[j].y, pf[j].z, pf[j].w};
+                const float qv[4] = {qf[j].x, qf[j].y, qf[j].z, qf[j].w};
+                add(pv, qv, 4 * (g + 32 * j) - mis);
             }
+        }
+        for (; g < g1; g += 32) {
+            float pv[4], qv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            load4(prow, 4 * g - mis, V, pv);
+            if (useq) load4(qrow, 4 * g - mis, V, qv);
+            add(pv, qv, 4 * g - mis);
+        }
+        if (gi > g0 && g0 == 0 && g1 > 0 && lane == 0) {  // the row's first, partial group
+            float pv[4], qv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            load4(prow, -mis, V, pv);
+            if (useq) load4(qrow, -mis, V, qv);
+            add(pv, qv, -mis);
         }
         sum = warp_sum(sum);
         if (lane == 0) s.wsum[warp] = sum;
@@ -226,7 +271,7 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
         // A slot of bsum is written again two passes on: by then its readers have passed the
         // barrier of the pass between.
         if (cluster > 1) {
-            cluster_sync();
+            cluster_barrier();
             if (tid < cluster) s.rsum[tid] = ld_cluster_u64(map_to_rank(&s.bsum[pass & 1], tid));
         }
         __syncthreads();
@@ -235,9 +280,10 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
             for (int r = 0; r < cluster; ++r) t += s.rsum[r];
             s.total = t;
             s.summed = t > 0 || s.rej == 0;  // nothing left after rejections: once more, from P
+            s.stop = s.done && s.summed;
+            if (!s.stop) step(s, n, drawn);
         }
         __syncthreads();
-        if (s.done && s.summed) break;
     }
 
     // ------------------------------------------------------------------ the draw
@@ -303,15 +349,16 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
             a.token[b] = found;
         }
     }
-    if (cluster > 1) cluster_sync();  // no block leaves while another may read its sums
+    if (cluster > 1) cluster_barrier();  // no block leaves while another may read its sums
 }
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
-    // blocks a request: as many as about fill the SMs, and no more than 4096 elements a block need
+    // Blocks a request: 8 unless fewer give each at most 4096 elements.  Also with many requests: the
+    // walks differ in length, and the longest one's passes are the faster the more SMs share them.
     int cluster = 1;
-    while (cluster < kMaxVCluster && (long long)a.B * cluster * 2 <= 304 && a.V > 4096 * cluster) cluster *= 2;
+    while (cluster < kMaxVCluster && a.V > 4096 * cluster) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * cluster), 1, 1);
     cfg.blockDim = dim3(kVThreads, 1, 1);

@@ -64,6 +64,21 @@ def test_many_walks(bsf8_lib, near):
     compare(p, None, tok, parent, u)
 
 
+def test_long_walks_over_large_rows(bsf8_lib):
+    """Several sums a walk, each over the blocks of a cluster: far drafts (rejections in a row), near
+    ones, and every request at another length."""
+    r = np.random.default_rng(12)
+    for near, V in ((0.3, 33001), (2.5, 40000)):
+        p, q, tok, parent, u = problem(r, 12, 10, V, near=near)
+        compare(p, q, tok, parent, u, nodes=r.integers(5, 11, size=12))
+    # many requests at once: the same walks give the same answers
+    P, Q = np.tile(p, (25, 1, 1)), np.tile(q, (25, 1, 1))
+    tile = lambda x: np.tile(x, (25, 1))  # noqa: E731
+    path, count, token = bsf8.verify_tree(dev(P), dev(tile(tok)), dev(tile(parent)), dev(tile(u)), q=dev(Q))
+    for t in (path.view(25, 12, 10), count.view(25, 12), token.view(25, 12)):
+        assert torch.equal(t, t[:1].expand_as(t))
+
+
 def test_edges(bsf8_lib):
     """One-hot rows, rows of zeros and NaN, u = 0 and the largest u, tokens the target excludes."""
     V, T = 11, 4
