@@ -8,13 +8,15 @@
 // sums, so neither the split of a row over threads and blocks nor their order changes a bit.
 //
 // A cluster of blocks per request.  What the walk may ask of single elements -- p and q of each
-// node's token at its parent -- is loaded up front by one thread a node; thread 0 of every
-// block then walks the tree in shared memory (the same steps in each), and the vocabulary is
-// read only where a sum of R is needed: once a rejection, and for the last draw unless the
-// last step was a rejection (its sum is the draw's).  A pass gives each block a contiguous
-// slice of the row and each warp a contiguous part of it, so the draw's element is found by
-// adding up slices, then warps, then one warp's part, which its block reads again (from L2).
-// HBM bound at large batches (one row of p and q a request), latency bound at small ones.
+// node's token at its parent -- is loaded up front by one thread a node, which also settles the
+// node's test for the case that no sibling was asked before it.  Warp 0 of every block then walks
+// the tree in shared memory (the same steps in each), and the vocabulary is read only where a sum of
+// R is needed: once a rejection, and for the last draw unless the last step was a rejection (its sum
+// is the draw's).  A pass gives each block a contiguous slice of the row and each warp a contiguous
+// part of it, so the draw's element is found by adding up slices, then warps, then one warp's part,
+// which its block reads again (from L2).
+// HBM bound at large batches (one row of p and q a request), latency bound at small ones: the chain
+// nodes, their probabilities, a pass, the cluster's barrier, the draw.
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
@@ -24,9 +26,10 @@ namespace bsf8 {
 
 namespace {
 
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kNodes = 256;        // BSF8_MAX_NODES
+static_assert(kNodes <= kVThreads, "a thread a node");
 constexpr int kMaxVCluster = 8;    // the portable cluster size
 constexpr int kBatch = 4;          // 16-byte loads of a row a thread has in flight
 typedef unsigned long long u64;
@@ -70,16 +73,15 @@ struct VerifyShared {
     u64 P[kNodes], Q[kNodes];  // of node i's token, at node i's parent
     uint32_t U[kNodes];
     int parent[kNodes], tok[kNodes], path[kNodes];
+    uint8_t first[kNodes];     // kept if asked before its siblings
     u64 Z[kNodes];             // the mass before each rejection at the walk's node
     int gone[kNodes];          // the token of each rejection there
     u64 wsum[kVWarps];         // a pass: each warp's sum of R
     u64 bsum[2];               // this block's, read by the cluster (slots taken in turn)
     u64 rsum[kMaxVCluster];    // every block's
-    u64 total;                 // the mass Z of R
-    int cur, rej, next, count; // the walk's node, rejections there, next child, nodes kept
-    int done, summed;          // no child is left to ask; the sums are those of the present R
+    int cur, rej;              // the walk's node, rejections there
     int small;                 // every Z here is below 2^42
-    int stop;                  // both: the draw is next
+    int stop;                  // the draw is next: no child is left to ask and R is summed
     u64 at;                    // the draw's threshold inside a warp's part
     int warp;                  // that warp, or -1
 };
@@ -91,7 +93,7 @@ __device__ __forceinline__ u64 times20(u64 q, uint32_t zh, uint32_t zl) {
 }
 
 // R of element x, whose fixed-point probabilities at the walk's node are P and Q.
-__device__ __forceinline__ u64 left_of(u64 P, u64 Q, int x, const VerifyShared &s, bool drawn) {
+__device__ __noinline__ u64 left_of(u64 P, u64 Q, int x, const VerifyShared &s, bool drawn) {
     if (drawn) {
         u64 off = s.rej > 0 ? Q : 0;  // the first rejection's mass is 2^40
         for (int j = 1; j < s.rej; ++j)
@@ -115,38 +117,66 @@ __device__ __forceinline__ void load4(const float *row, int x, int V, float (&v)
     }
 }
 
-// The walk from where it stands until a rejection (whose sum of R is wanted) or the last child.
-__device__ __forceinline__ void walk(VerifyShared &s, int n, bool drawn) {
-    int i = s.next;
-    s.done = 1;
-    for (; i < n && s.done; ++i) {
-        if (s.parent[i] != s.cur) continue;
-        const u64 z = s.total;
-        const u64 q = times(s.Q[i], z);
-        if (part(s.U[i], q) < left_of(s.P[i], s.Q[i], s.tok[i], s, drawn)) {  // kept
+// The walk's own state, the same in every lane of warp 0.
+struct Walk {
+    u64 total;                    // the mass Z of R
+    int cur, rej, next, count;    // node, rejections there, next child to ask, nodes kept
+    bool done, summed;            // no child is left to ask; the sums are those of the present R
+};
+
+// The next thing after a sum (or the start), by warp 0: on along the walk until a rejection (whose
+// sum of R is wanted) or the last child; or, when R was all 0 after that, a sum of P instead.
+__device__ __forceinline__ void step(VerifyShared &s, Walk &w, int n, bool drawn, int lane) {
+    if (w.done) w.rej = 0;
+    while (!w.done) {
+        // the next child of w.cur
+        int i = n;
+        for (int base = w.next & ~31; base < n; base += 32) {
+            const int c = base + lane;
+            const uint32_t m = __ballot_sync(0xFFFFFFFFu, c >= w.next && c < n && s.parent[c] == w.cur);
+            if (m) {
+                i = base + __ffs(m) - 1;
+                break;
+            }
+        }
+        w.next = min(n, i + 1);
+        if (i == n) {
+            w.done = true;
+            break;
+        }
+        bool kept = s.first[i];
+        if (w.rej > 0) kept = part(s.U[i], times(s.Q[i], w.total)) < left_of(s.P[i], s.Q[i], s.tok[i], s, drawn);
+        w.summed = false;
+        if (!kept) {
+            __syncwarp();
+            if (lane == 0) {
+                s.Z[w.rej] = w.total;
+                s.gone[w.rej] = s.tok[i];
+                if (w.total >= 1ull << 42) s.small = 0;
+                s.rej = w.rej + 1;
+            }
+            __syncwarp();
+            ++w.rej;
+            break;
+        }
+        w.cur = i;
+        w.rej = 0;
+        w.total = kOne;
+        __syncwarp();
+        if (lane == 0) {
+            s.path[w.count] = i;
             s.cur = i;
-            s.path[s.count++] = i;
             s.rej = 0;
             s.small = 1;
-            s.total = kOne;
-        } else {
-            s.Z[s.rej] = z;
-            if (z >= 1ull << 42) s.small = 0;
-            s.gone[s.rej] = s.tok[i];
-            ++s.rej;
-            s.done = 0;
         }
-        s.summed = 0;
+        __syncwarp();
+        ++w.count;
     }
-    s.next = i;
-}
-
-// The next thing after a sum (or the start), by thread 0: on along the walk, or, when R was all 0
-// after the last child, a sum of P instead.
-__device__ __forceinline__ void step(VerifyShared &s, int n, bool drawn) {
-    if (s.done) s.rej = 0;
-    else walk(s, n, drawn);
-    s.stop = s.done && s.summed;
+    __syncwarp();
+    if (lane == 0) {
+        s.rej = w.rej;
+        s.stop = w.done && w.summed;
+    }
 }
 
 // Cluster barrier whose lanes need not arrive together.
@@ -154,13 +184,18 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-__global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, int cluster, int *status) {
+__global__ void __launch_bounds__(kVThreads, 4) verify_kernel(const VerifyArgs a, int cluster, int *status) {
     __shared__ VerifyShared s;
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int T = a.T, V = a.V;
+    // every node's words at once with the node count
+    const size_t nb = (size_t)b * T + tid;
+    const bool mine = tid < T;
+    const float u0 = mine ? a.u[nb] : 0.0f;
+    const int par0 = mine ? a.parent[nb] : -1, x0 = mine ? a.tokens[nb] : 0;
     int n = a.nodes ? a.nodes[b] : T;
     if (n < 1 || n > T) {
         if (tid == 0) report_index(status);
@@ -169,16 +204,18 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
     const bool drawn = a.q != nullptr;
     const float *const pb = a.p + (size_t)b * T * a.ld;
     const float *const qb = drawn ? a.q + (size_t)b * T * a.ld : nullptr;
-    for (int i = tid; i < n; i += kVThreads) {
-        s.U[i] = (uint32_t)(fminf(fmaxf(a.u[(size_t)b * T + i], 0.0f), 0.99999994f) * 16777216.0f);
+    if (tid < n) {  // T <= kVThreads
+        const int i = tid;
+        s.U[i] = (uint32_t)(fminf(fmaxf(u0, 0.0f), 0.99999994f) * 16777216.0f);
         int par = -1, x = 0;
         u64 P = 0, Q = 0;
         if (i > 0) {
-            par = a.parent[(size_t)b * T + i];
-            x = a.tokens[(size_t)b * T + i];
+            par = par0;
+            x = x0;
             if ((unsigned)par >= (unsigned)i || (unsigned)x >= (unsigned)V) {
                 report_index(status);
                 par = -1;
+                x = 0;
             } else {
                 P = fix(pb[(size_t)par * a.ld + x]);
                 Q = drawn ? fix(qb[(size_t)par * a.ld + x]) : kOne;
@@ -188,20 +225,19 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
         s.tok[i] = x;
         s.P[i] = P;
         s.Q[i] = Q;
+        s.first[i] = part(s.U[i], Q) < P;
     }
     if (tid == 0) {
-        s.cur = s.rej = s.summed = s.done = 0;
+        s.cur = s.rej = s.path[0] = 0;
         s.small = 1;
-        s.next = s.count = 1;
-        s.path[0] = 0;
-        s.total = kOne;
     }
+    Walk w{kOne, 0, 0, 1, 1, false, false};
     __syncthreads();
-    if (tid == 0) step(s, n, drawn);
+    if (warp == 0) step(s, w, n, drawn, lane);
     __syncthreads();
 
     int per_warp = 0, mis = 0, groups = 0;  // of the last pass's row
-    // Thread 0 changes the walk's state only between the last two barriers of a turn, so that every
+    // Warp 0 changes the walk's state only between the last two barriers of a turn, so that every
     // thread reads the same state at its top.
     for (uint32_t pass = 0; !s.stop; ++pass) {
         // -------------------------------------------------------------- a pass: the sums of R
@@ -215,18 +251,45 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
         const int rej = s.rej;
         const bool useq = drawn && rej > 0;
         u64 sum = 0;
-        auto add = [&](const float (&pv)[4], const float (&qv)[4], int x) {
+        const uint32_t zh1 = rej > 1 ? (uint32_t)(s.Z[1] >> 20) : 0, zl1 = rej > 1 ? (uint32_t)s.Z[1] & 0xFFFFFu : 0;
+        // r less floor(Q z / 2^40), at least 0 (Q < 2^31, z < 2^42 in parts of 22 and 20 bits; the
+        // quotient is below 2^33, and at or above 2^32 it exceeds r)
+        auto less = [](uint32_t r, uint32_t Q, uint32_t zh, uint32_t zl) -> uint32_t {
+            const u64 t = (u64)Q * zh + (u64)__umulhi(Q, zl << 12);
+            const uint32_t off = (uint32_t)(t >> 20);
+            return (uint32_t)(t >> 52) ? 0u : max(r, off) - off;
+        };
+        // Almost all probabilities of a large vocabulary are small: below 2^-9 the fixed point fits 31
+        // bits, one conversion (negative and NaN give 0) and 32-bit differences do.
+        auto add = [&](const float4 &pf, const float4 &qf, int x) {
+            const float top = fmaxf(fmaxf(fmaxf(pf.x, pf.y), fmaxf(pf.z, pf.w)),
+                                    useq ? fmaxf(fmaxf(qf.x, qf.y), fmaxf(qf.z, qf.w)) : 0.0f);
+            const float pv[4] = {pf.x, pf.y, pf.z, pf.w}, qv[4] = {qf.x, qf.y, qf.z, qf.w};
+            if (top < 0.001953125f && (rej == 0 || (useq && s.small))) {
+                uint32_t r[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const u64 P = fix(pv[i]);
-                if (rej == 0) {
-                    sum += P;
-                } else if (rej == 1 && drawn) {
-                    const u64 Q = fix(qv[i]);
-                    sum += P > Q ? P - Q : 0;
-                } else {
-                    sum += left_of(P, drawn ? fix(qv[i]) : 0, x + i, s, drawn);
+                for (int i = 0; i < 4; ++i) r[i] = __float2uint_rz(pv[i] * 1099511627776.0f);
+                if (useq) {
+                    uint32_t Q[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        Q[i] = __float2uint_rz(qv[i] * 1099511627776.0f);
+                        r[i] = max(r[i], Q[i]) - Q[i];
+                    }
+                    uint32_t zh = zh1, zl = zl1;
+#pragma unroll 1
+                    for (int j = 1; j < rej; ++j) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) r[i] = less(r[i], Q[i], zh, zl);
+                        zh = (uint32_t)(s.Z[j + 1 < rej ? j + 1 : j] >> 20);
+                        zl = (uint32_t)s.Z[j + 1 < rej ? j + 1 : j] & 0xFFFFFu;
+                    }
                 }
+                sum += (u64)(r[0] + r[1]) + (r[2] + r[3]);  // each below 2^31
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum += left_of(fix(pv[i]), useq ? fix(qv[i]) : 0, x + i, s, drawn);
             }
         };
         // whole groups of four, kBatch loads of each row in flight; then the ragged ones
@@ -236,28 +299,20 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
             float4 pf[kBatch], qf[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) pf[j] = *reinterpret_cast<const float4 *>(prow + 4 * (g + 32 * j) - mis);
-            if (useq)
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) qf[j] = *reinterpret_cast<const float4 *>(qrow + 4 * (g + 32 * j) - mis);
+            for (int j = 0; j < kBatch; ++j)
+                qf[j] = useq ? *reinterpret_cast<const float4 *>(qrow + 4 * (g + 32 * j) - mis) : make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const float pv[4] = {pf[j].x, pf[j].y, pf[j].z, pf[j].w};
-                const float qv[4] = {qf[j].x, qf[j].y, qf[j].z, qf[j].w};
-                add(pv, qv, 4 * (g + 32 * j) - mis);
-            }
+            for (int j = 0; j < kBatch; ++j) add(pf[j], qf[j], 4 * (g + 32 * j) - mis);
         }
-        for (; g < g1; g += 32) {
+        auto ragged = [&](int k) {
             float pv[4], qv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            load4(prow, 4 * g - mis, V, pv);
-            if (useq) load4(qrow, 4 * g - mis, V, qv);
-            add(pv, qv, 4 * g - mis);
-        }
-        if (gi > g0 && g0 == 0 && g1 > 0 && lane == 0) {  // the row's first, partial group
-            float pv[4], qv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            load4(prow, -mis, V, pv);
-            if (useq) load4(qrow, -mis, V, qv);
-            add(pv, qv, -mis);
-        }
+            load4(prow, 4 * k - mis, V, pv);
+            if (useq) load4(qrow, 4 * k - mis, V, qv);
+            add(make_float4(pv[0], pv[1], pv[2], pv[3]), make_float4(qv[0], qv[1], qv[2], qv[3]), 4 * k - mis);
+        };
+        for (; g < g1; g += 32) ragged(g);
+        if (gi > g0 && g0 == 0 && g1 > 0 && lane == 0) ragged(0);  // the row's first, partial group
         sum = warp_sum(sum);
         if (lane == 0) s.wsum[warp] = sum;
         __syncthreads();
@@ -270,40 +325,47 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
         }
         // A slot of bsum is written again two passes on: by then its readers have passed the
         // barrier of the pass between.
-        if (cluster > 1) {
-            cluster_barrier();
-            if (tid < cluster) s.rsum[tid] = ld_cluster_u64(map_to_rank(&s.bsum[pass & 1], tid));
-        }
-        __syncthreads();
-        if (tid == 0) {
+        if (cluster > 1) cluster_barrier();
+        if (warp == 0) {
             u64 t = 0;
-            for (int r = 0; r < cluster; ++r) t += s.rsum[r];
-            s.total = t;
-            s.summed = t > 0 || s.rej == 0;  // nothing left after rejections: once more, from P
-            s.stop = s.done && s.summed;
-            if (!s.stop) step(s, n, drawn);
+            __syncwarp();
+            if (cluster > 1) {
+                if (lane < cluster) s.rsum[lane] = t = ld_cluster_u64(map_to_rank(&s.bsum[pass & 1], lane));
+            } else if (lane == 0) {
+                t = s.rsum[0];
+            }
+            w.total = warp_sum(t);
+            w.summed = w.total > 0 || w.rej == 0;  // nothing left after rejections: once more, from P
+            if (w.done && w.summed) {
+                if (lane == 0) s.stop = 1;
+            } else {
+                step(s, w, n, drawn, lane);
+            }
         }
         __syncthreads();
     }
 
     // ------------------------------------------------------------------ the draw
-    if (tid == 0) {
-        const u64 thr = part(s.U[0], s.total);
-        u64 before = 0;
-        for (int r = 0; r < rank; ++r) before += s.rsum[r];
-        s.warp = -1;
-        for (int w = 0; w < kVWarps; ++w) {
-            if (thr >= before && thr < before + s.wsum[w]) {
-                s.warp = w;
-                s.at = thr - before;
-            }
-            before += s.wsum[w];
+    if (warp == 0) {
+        const u64 thr = part(s.U[0], w.total);
+        const u64 mine = lane < kVWarps ? s.wsum[lane] : 0;
+        u64 upto = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+            if (lane >= m) upto += o;
         }
-        if (s.total == 0 && rank == 0) a.token[b] = V - 1;
-    }
-    if (rank == 0) {
-        for (int i = tid; i < T; i += kVThreads) a.path[(size_t)b * T + i] = i < s.count ? s.path[i] : -1;
-        if (tid == 0) a.count[b] = s.count;
+        const u64 before = warp_sum(lane < rank ? s.rsum[lane] : 0) + upto - mine;
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, thr >= before && thr < before + mine);
+        if (lane == 0) s.warp = here ? __ffs(here) - 1 : -1;
+        if (thr >= before && thr < before + mine) s.at = thr - before;
+        if (rank == 0) {
+            if (lane == 0) {
+                a.count[b] = w.count;
+                if (w.total == 0) a.token[b] = V - 1;
+            }
+            for (int i = lane; i < T; i += 32) a.path[(size_t)b * T + i] = i < w.count ? s.path[i] : -1;
+        }
     }
     __syncthreads();
     if (s.warp >= 0) {  // one block of the cluster: its warp's part again, in order over the threads
@@ -327,7 +389,7 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(const VerifyArgs a, i
             const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
             if (lane >= m) upto += o;
         }
-        __syncthreads();  // s.wsum is read above by thread 0 only, before its barrier
+        __syncthreads();  // s.wsum was read by warp 0, before the barrier above
         if (lane == 31) s.wsum[warp] = upto;
         __syncthreads();
         u64 before = upto - sum;
