@@ -72,147 +72,161 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&y)[8]) {
 //
 // D / 8 lanes hold a row, 8 channels a lane (one 16-byte load): the norm's sum is a shuffle
 // tree over them, a rotation partner of the split form sits rot / 16 lanes away, and the
-// four lanes of a 32-channel block share its exponent.  A group of lanes takes up to H heads
-// of one token and kind (q, k or v), whose loads are in flight together and whose cosines
-// and sines are loaded once.
-template <int D, int H>
-__global__ void __launch_bounds__(256) append_kernel(const CacheView c, const AppendArgs a, int *status) {
+// four lanes of a 32-channel block share its exponent.  A row is (token, q | k | v, head); a
+// token's rows are numbered q heads, k heads, v heads.
+
+// A block takes up to kTokens consecutive tokens and, by blockIdx.y, 256 / LPR rows of each: a lane
+// group has one row number throughout, so that from token to token only addresses move on.  The
+// tokens' places and positions are looked up once, by a thread a token, while the first rows are on
+// their way; kAhead rows a lane group stay in flight.  (Looking them up in every lane group cost
+// more instructions than the norm, the rotation and the rounding together.)
+constexpr int kTokens = 16, kAhead = 2;
+
+template <int D>
+__global__ void __launch_bounds__(256, 4) append_kernel(const CacheView c, const AppendArgs a, int tokens, int *status) {
+    __shared__ long long s_row[kTokens];  // cache row of head 0; -1: not kept
+    __shared__ int s_pos[kTokens];        // -1: the token is left out
     pdl_trigger();
     pdl_wait();
     constexpr int LPR = D / 8;
-    const int sub = threadIdx.x % LPR;
-    const int lane = threadIdx.x & 31;
+    const int sub = threadIdx.x % LPR, lane = threadIdx.x & 31;
     const uint32_t gmask = LPR == 32 ? 0xFFFFFFFFu : ((1u << LPR) - 1u) << (lane - sub);
     const int c0 = sub * 8;  // this lane's first channel
-    const int qc = (a.Hq + H - 1) / H, kc = (c.heads + H - 1) / H;
-    const int chunks = qc + 2 * kc;
-    const long long items = (long long)a.N * chunks;
-    const long long step = (long long)gridDim.x * (256 / LPR);
-    for (long long it = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR; it < items; it += step) {
-        const int n = (int)(it / chunks);
-        int ch = (int)(it - (long long)n * chunks);
-        const int kind = ch < qc ? 0 : ch < qc + kc ? 1 : 2;
-        ch -= kind == 0 ? 0 : kind == 1 ? qc : qc + kc;
-        const int h0 = ch * H;
-        const int heads = kind == 0 ? a.Hq : c.heads;
-        const uint16_t *src = kind == 0   ? a.q + (size_t)n * a.ldq
-                              : kind == 1 ? a.k + (size_t)n * a.ldk
-                                          : a.v + (size_t)n * a.ldv;
-        uint4 w[H];
+    const int n0 = (int)blockIdx.x * tokens, count = min(tokens, a.N - n0);
+    // the row: query, key or value head
+    int r = (int)blockIdx.y * (256 / LPR) + threadIdx.x / LPR;
+    const bool real = r < a.Hq + 2 * c.heads;
+    const int kind = !real ? 3 : r < a.Hq ? 0 : r < a.Hq + c.heads ? 1 : 2;
+    r -= kind == 0 ? 0 : kind == 1 ? a.Hq : a.Hq + c.heads;
+    const long long ld = kind == 0 ? a.ldq : kind == 1 ? a.ldk : a.ldv;
+    const uint16_t *src = (kind == 0 ? a.q : kind == 1 ? a.k : a.v) + (size_t)r * D + c0 + n0 * ld;
+    uint4 w[kAhead];
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-            w[j] = h0 + j < heads ? *reinterpret_cast<const uint4 *>(src + (size_t)(h0 + j) * D + c0)
-                                  : make_uint4(0, 0, 0, 0);
-        int pos = 0;
-        if (a.rot > 0) {
-            pos = *(a.pos + n);
-            if ((unsigned)pos >= (unsigned)a.positions) {
-                if (sub == 0) report_index(status);
-                continue;  // uniform over the group
-            }
-        }
-        long long row = 0;
-        if (kind > 0) {
-            const int slot = *(a.slot + n);
-            if (slot < 0) continue;
-            row = cache_row(c, *(a.req + n), slot);
-            if (row < 0) {
-                if (sub == 0) report_index(status);
-                continue;
-            }
-        }
-        const uint16_t *nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-        float g[8];
-        if (nw) unpack8(*reinterpret_cast<const uint4 *>(nw + c0), g);
-        const bool turned = kind < 2 && a.rot > 0 && c0 < a.rot;
-        float cs[8], sn[8];  // split form: per channel; interleaved: per pair (4)
-        const int half = a.rot / 2;
-        if (turned) {
-            const float *t = a.cos_sin + (size_t)pos * a.rot;
-            const int i0 = a.interleaved ? c0 / 2 : (c0 < half ? c0 : c0 - half);
-            const float4 x0 = *reinterpret_cast<const float4 *>(t + i0);
-            const float4 y0 = *reinterpret_cast<const float4 *>(t + half + i0);
-            cs[0] = x0.x; cs[1] = x0.y; cs[2] = x0.z; cs[3] = x0.w;
-            sn[0] = y0.x; sn[1] = y0.y; sn[2] = y0.z; sn[3] = y0.w;
-            if (!a.interleaved) {
-                const float4 x1 = *reinterpret_cast<const float4 *>(t + i0 + 4);
-                const float4 y1 = *reinterpret_cast<const float4 *>(t + half + i0 + 4);
-                cs[4] = x1.x; cs[5] = x1.y; cs[6] = x1.z; cs[7] = x1.w;
-                sn[4] = y1.x; sn[5] = y1.y; sn[6] = y1.z; sn[7] = y1.w;
-            }
-        }
+    for (int j = 0; j < kAhead; ++j)
+        if (real && j < count) w[j] = *reinterpret_cast<const uint4 *>(src + j * ld);
+    if (threadIdx.x < count) {
+        const int n = n0 + threadIdx.x;
+        const int slot = a.slot[n], req = a.req[n], pos = a.rot > 0 ? a.pos[n] : 0;
+        const bool good = a.rot == 0 || (unsigned)pos < (unsigned)a.positions;
+        const long long row = slot < 0 ? -1 : cache_row(c, req, slot);
+        if (!good || (row < 0 && slot >= 0)) report_index(status);
+        s_row[threadIdx.x] = row;
+        s_pos[threadIdx.x] = good ? pos : -1;
+    }
+    __syncthreads();
+    if (!real) return;
+    src += kAhead * ld;
+    uint16_t *out = a.q_out + ((size_t)n0 * a.Hq + r) * D + c0;
+    uint8_t *const codes_at = (kind == 1 ? c.k8 : c.v8) + (size_t)r * c.page_size * D + c0;
+    uint8_t *const exps_at = (kind == 1 ? c.kexp : c.vexp) + (size_t)r * c.page_size * (D / 32) + c0 / 32;
+    const uint16_t *const nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+    float g[8];
+    if (nw) unpack8(*reinterpret_cast<const uint4 *>(nw + c0), g);
+    const int half = a.rot / 2;
+    const bool turns = kind < 2 && a.rot > 0, turned = turns && c0 < a.rot;
+    const float *const angles = a.cos_sin + (a.interleaved ? c0 / 2 : (c0 < half ? c0 : c0 - half));
+    const int from = !turned ? lane : c0 < half ? lane + half / 8 : lane - half / 8;  // split form's partner
+
+    for (int t0 = 0; t0 < count; t0 += kAhead) {
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            if (h0 + j >= heads) break;
+        for (int j = 0; j < kAhead; ++j) {
+            const int t = t0 + j;
+            if (t >= count) break;  // uniform over the block
             float y[8];
             unpack8(w[j], y);
-            if (nw) {
-                float ss = 0.0f;
+            if (t + kAhead < count) w[j] = *reinterpret_cast<const uint4 *>(src);
+            src += ld;
+            const int pos = s_pos[t];
+            if (pos >= 0) {
+                if (nw) {
+                    float ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+                    for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
 #pragma unroll
-                for (int m = LPR / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(gmask, ss, m);
-                const float r = __frsqrt_rn(ss * (1.0f / D) + a.eps);
+                    for (int k = LPR / 2; k > 0; k >>= 1) ss += __shfl_xor_sync(gmask, ss, k);
+                    const float s = rsqrtf(fmaf(ss, 1.0f / D, a.eps));
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * r * g[i];
-            }
-            if (kind < 2 && a.rot > 0) {
-                if (a.interleaved) {
-                    if (turned) {
+                    for (int i = 0; i < 8; ++i) y[i] = y[i] * s * g[i];
+                }
+                if (turns) {
+                    const float *const at = angles + (size_t)pos * a.rot;
+                    if (a.interleaved) {
+                        if (turned) {
+                            const float4 x = *reinterpret_cast<const float4 *>(at);
+                            const float4 z = *reinterpret_cast<const float4 *>(at + half);
+                            const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float u = y[2 * i], v = y[2 * i + 1];
-                            y[2 * i] = u * cs[i] - v * sn[i];
-                            y[2 * i + 1] = v * cs[i] + u * sn[i];
+                            for (int i = 0; i < 4; ++i) {
+                                const float u = y[2 * i], v = y[2 * i + 1];
+                                y[2 * i] = u * cs[i] - v * sn[i];
+                                y[2 * i + 1] = v * cs[i] + u * sn[i];
+                            }
+                        }
+                    } else {  // the partner channel is rot / 2 away; its sine counts negative below it
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float4 x = make_float4(1, 1, 1, 1), z = make_float4(0, 0, 0, 0);
+                            if (turned) {
+                                x = *reinterpret_cast<const float4 *>(at + 4 * k);
+                                z = *reinterpret_cast<const float4 *>(at + half + 4 * k);
+                            }
+                            const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float o = __shfl_sync(gmask, y[4 * k + i], from);
+                                y[4 * k + i] = fmaf(y[4 * k + i], cs[i], c0 < half ? -o * sn[i] : o * sn[i]);
+                            }
                         }
                     }
-                } else {  // the partner channel is rot / 2 away: half / 8 lanes up or down
-                    const int from = !turned ? lane : c0 < half ? lane + half / 8 : lane - half / 8;
+                }
+                if (kind == 0) {
+                    *reinterpret_cast<uint4 *>(out) = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]),
+                                                                 pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+                } else {
+                    uint32_t am = 0;  // magnitude bits order as magnitudes do, NaN above infinity
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float o = __shfl_sync(gmask, y[i], from);
-                        if (turned) y[i] = c0 < half ? y[i] * cs[i] - o * sn[i] : y[i] * cs[i] + o * sn[i];
+                    for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    am = max(am, __shfl_xor_sync(gmask, am, 1));
+                    am = max(am, __shfl_xor_sync(gmask, am, 2));
+                    // 448 = 1.75 * 2^8: adding 0x1FFFFF carries into the exponent past mantissa 0.75
+                    int e = max(0, (int)((am + 0x1FFFFFu) >> 23) - 8);
+                    uint2 codes;
+                    if (am >= 0x7F800000u) {
+                        e = 255;
+                        codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                    } else {
+                        const float inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e), exact products
+                        codes = make_uint2(pack_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                                           pack_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+                    }
+                    const long long row = s_row[t];
+                    if (row >= 0) {
+                        *reinterpret_cast<uint2 *>(codes_at + row * D) = codes;
+                        if ((sub & 3) == 0) exps_at[row * (D / 32)] = (uint8_t)e;
                     }
                 }
             }
-            if (kind == 0) {
-                *reinterpret_cast<uint4 *>(a.q_out + ((size_t)n * a.Hq + h0 + j) * D + c0) =
-                    make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                               pack_bf16(y[6], y[7]));
-                continue;
-            }
-            uint32_t am = 0;  // magnitude bits order as magnitudes do, NaN above infinity
-#pragma unroll
-            for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-            am = max(am, __shfl_xor_sync(gmask, am, 1));
-            am = max(am, __shfl_xor_sync(gmask, am, 2));
-            // 448 = 1.75 * 2^8: adding 0x1FFFFF carries into the exponent past mantissa 0.75
-            int e = max(0, (int)((am + 0x1FFFFFu) >> 23) - 8);
-            uint2 codes;
-            if (am >= 0x7F800000u) {
-                e = 255;
-                codes = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            } else {
-                const float inv = __uint_as_float((uint32_t)(254 - e) << 23);  // 2^(127 - e), exact products
-                codes = make_uint2(pack_e4m3(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                                   pack_e4m3(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-            }
-            const size_t r = (size_t)row + (size_t)(h0 + j) * c.page_size;
-            uint8_t *d8 = kind == 1 ? c.k8 : c.v8, *de = kind == 1 ? c.kexp : c.vexp;
-            *reinterpret_cast<uint2 *>(d8 + r * D + c0) = codes;
-            if ((sub & 3) == 0) de[r * (D / 32) + c0 / 32] = (uint8_t)e;
+            out += (size_t)a.Hq * D;
         }
     }
 }
 
 template <int D>
 cudaError_t append_dim(const CacheView &c, const AppendArgs &a, cudaStream_t stream, int *status) {
-    constexpr int per = 256 / (D / 8);
-    // one head a group while the groups of all heads leave SMs idle, else four
-    const long long rows = (long long)a.N * (a.Hq + 2LL * c.heads);
-    if (rows <= 152LL * 8 * per) return launch_cache(append_kernel<D, 1>, (rows + per - 1) / per, 256, stream, c, a, status);
-    const long long items = (long long)a.N * ((a.Hq + 3) / 4 + 2 * ((c.heads + 3) / 4));
-    return launch_cache(append_kernel<D, 4>, (items + per - 1) / per, 256, stream, c, a, status);
+    constexpr int G = 256 / (D / 8);
+    const int chunks = (a.Hq + 2 * c.heads + G - 1) / G;
+    // tokens a block: one while that keeps every block resident (four an SM), up to 16 after that
+    const int tokens = (int)std::min<long long>(kTokens, ((long long)a.N * chunks + 152 * 4 - 1) / (152 * 4));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.N + tokens - 1) / tokens), (unsigned)chunks, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = options().pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, append_kernel<D>, c, a, tokens, status);
 }
 
 cudaError_t launch_append(const CacheView &c, const AppendArgs &a, cudaStream_t stream) {
@@ -227,46 +241,57 @@ cudaError_t launch_append(const CacheView &c, const AppendArgs &a, cudaStream_t 
 }
 
 // ---------------------------------------------------------------------- read
-// A thread per 16 codes of a row (one 16-byte load, two 16-byte stores), the rebuild of
-// bsf8_dequant.
-__global__ void __launch_bounds__(256) kv_read_kernel(const CacheView c, const int32_t *req,
-                                                      const int32_t *slot,
-                                                      uint16_t *k_out, uint16_t *v_out,
-                                                      int cpt, long long items, int *status) {
+// A token's pieces are its rows' runs of 16 codes (one 16-byte load, two 16-byte stores), keys then
+// values; a thread takes kReadPieces of a token's, equally far apart, all of their loads in flight:
+// the chain slot, page, codes is walked once for them.  The rebuild is bsf8_dequant's.
+constexpr int kReadPieces = 4;
+
+__global__ void __launch_bounds__(256) kv_read_kernel(const CacheView c, const int32_t *req, const int32_t *slot,
+                                                      uint16_t *k_out, uint16_t *v_out, int side, long long threads,
+                                                      int per, int *status) {
     pdl_trigger();
     pdl_wait();
-    const int cpr = c.dim / 16;  // pieces a row; cpt: pieces a token of one side
+    const int cpr = c.dim / 16;  // pieces a row; side: a side's; per: threads a token
     const long long step = (long long)gridDim.x * blockDim.x;
-    const bool both = k_out && v_out;
-    for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < items; it += step) {
-        const long long ns = it / cpt;
-        const int piece = (int)(it - ns * cpt);
-        const int n = (int)(both ? ns >> 1 : ns);
-        const bool key = both ? (ns & 1) == 0 : k_out != nullptr;
-        const int h = piece / cpr, p = piece - h * cpr;
-        const int sl = *(slot + n);
-        const long long row0 = cache_row(c, *(req + n), sl);
-        uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
-        if (row0 >= 0) {
-            const size_t r = (size_t)row0 + (size_t)h * c.page_size;
-            const uint4 q = *reinterpret_cast<const uint4 *>((key ? c.k8 : c.v8) + r * c.dim + 16 * p);
-            const uint32_t e = (key ? c.kexp : c.vexp)[r * (c.dim / 32) + p / 2];
-            const Scale sc = make_scale(e);
-            const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+    for (long long it = (long long)blockIdx.x * blockDim.x + threadIdx.x; it < threads; it += step) {
+        const int n = (int)(it / per), t = (int)(it - (long long)n * per);
+        const int sl = slot[n];
+        const long long row0 = cache_row(c, req[n], sl);
+        if (row0 < 0 && sl >= 0) report_index(status);
+        uint4 q[kReadPieces];
+        uint32_t e[kReadPieces];
+#pragma unroll
+        for (int j = 0; j < kReadPieces; ++j) {
+            const int pc = t + j * per;
+            const bool key = k_out && pc < side;
+            const int x = key || !k_out ? pc : pc - side;  // piece of its side
+            q[j] = make_uint4(0, 0, 0, 0);
+            e[j] = 127;
+            if (x < side && row0 >= 0) {
+                const int h = x / cpr, p = x - h * cpr;
+                const size_t r = (size_t)row0 + (size_t)h * c.page_size;
+                q[j] = *reinterpret_cast<const uint4 *>((key ? c.k8 : c.v8) + r * c.dim + 16 * p);
+                e[j] = (key ? c.kexp : c.vexp)[r * (c.dim / 32) + p / 2];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kReadPieces; ++j) {
+            const int pc = t + j * per;
+            const bool key = k_out && pc < side;
+            const int x = key || !k_out ? pc : pc - side;
+            if (x >= side || (!key && !v_out)) continue;
+            const Scale sc = make_scale(e[j]);
+            const uint32_t qw[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
             uint32_t o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 rebuild4(qw[i], sc, o[2 * i], o[2 * i + 1]);
                 if (nan_code_mask(qw[i])) patch_nan_codes(qw[i], o[2 * i], o[2 * i + 1]);
             }
-            o0 = make_uint4(o[0], o[1], o[2], o[3]);
-            o1 = make_uint4(o[4], o[5], o[6], o[7]);
-        } else if (sl >= 0) {
-            report_index(status);
+            uint4 *dst = reinterpret_cast<uint4 *>((key ? k_out : v_out) + ((size_t)n * side + x) * 16);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
         }
-        uint4 *dst = reinterpret_cast<uint4 *>((key ? k_out : v_out) + ((size_t)n * cpt + piece) * 16);
-        dst[0] = o0;
-        dst[1] = o1;
     }
 }
 
@@ -274,10 +299,11 @@ cudaError_t launch_kv_read(const CacheView &c, const int32_t *req, const int32_t
                            void *v_out, int N, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
-    const int cpt = c.heads * (c.dim / 16);
-    const long long items = (long long)N * cpt * (k_out && v_out ? 2 : 1);
-    return launch_cache(kv_read_kernel, (items + 255) / 256, 256, stream, c, req, slot,
-                        static_cast<uint16_t *>(k_out), static_cast<uint16_t *>(v_out), cpt, items, status);
+    const int side = c.heads * (c.dim / 16), both = side * (k_out && v_out ? 2 : 1);
+    const int per = (both + kReadPieces - 1) / kReadPieces;
+    const long long threads = (long long)N * per;
+    return launch_cache(kv_read_kernel, (threads + 255) / 256, 256, stream, c, req, slot,
+                        static_cast<uint16_t *>(k_out), static_cast<uint16_t *>(v_out), side, threads, per, status);
 }
 
 // -------------------------------------------------------------------- commit
