@@ -62,7 +62,7 @@ def load(build_if_missing: bool = True):
         if _lib is not None:
             return _lib
         path = _build.LIB
-        if not os.path.exists(path):
+        if not os.path.exists(path) or not os.path.exists(_build.EXT):
             if not build_if_missing:
                 raise RuntimeError(f"libbsf8 is not built ({path}); run build.build()")
             _build.build()
