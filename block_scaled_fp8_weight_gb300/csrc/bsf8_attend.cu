@@ -50,7 +50,8 @@ namespace {
 
 template <int D, int ROWS>
 struct Shape {
-    static constexpr int DIM = D, RT = ROWS;
+    static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
+    static constexpr bool RAWV = false;
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        init_pipes(s);
+        init_pipes(s, kDeqWarps);
         for (int i = 0; i < 8; ++i) mbar_init(&s.m_full[i >> 2][i & 3], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1);
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         mbar_init(&s.soft, kSoftWarps);
         fence_mbar_init();
     }
-    hold_tmem(s, warp);
+    hold_tmem(s, warp == kMmaWarp);
     pdl_trigger();
     pdl_wait();
     sum_items<S>(p, s, prefix, warp, lane);
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     }
 
     if (!ok) report_timeout(p.status);
-    free_tmem(tmem, warp);
+    free_tmem(tmem, warp == kMmaWarp);
 }
 
 // ------------------------------------------------------------------ host side
@@ -599,7 +600,11 @@ namespace {
 
 // Rows a tile: the smallest that holds all of a request's rows of a head (more copies of a small
 // tile mean less softmax work a thread), 128 past that.
-int row_tile(int T, int g) { return T * g <= 32 ? 32 : T * g <= 64 ? 64 : 128; }
+int row_tile(int T, int g, int dim) {
+    const int rows = T * g;
+    if (dim == 128 && rows <= 16) return rows <= 8 ? 8 : 16;
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+}
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
@@ -620,16 +625,16 @@ EncodeTiledFnA encode_fn_a() {
     return fn;
 }
 
-// The key codes as [rows][dim] bytes; a box is box_rows rows (inside a page and a tile) of at most
+// Codes as [rows][dim] bytes; a box is box_rows rows (inside a page and a tile) of at most
 // 128 bytes, swizzled by its width.
-cudaError_t key_map(const CacheView &c, int box_rows, CUtensorMap *out) {
+cudaError_t code_map(const CacheView &c, void *codes, int box_rows, CUtensorMap *out) {
     EncodeTiledFnA fn = encode_fn_a();
     if (!fn) return cudaErrorNotSupported;
     const cuuint32_t w = (cuuint32_t)std::min(c.dim, 128);
     const cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)c.pages * c.heads * c.page_size};
     const cuuint64_t strides[1] = {(cuuint64_t)c.dim};
     const cuuint32_t box[2] = {w, (cuuint32_t)box_rows}, es[2] = {1u, 1u};
-    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.k8, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, codes, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           w == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -637,7 +642,7 @@ cudaError_t key_map(const CacheView &c, int box_rows, CUtensorMap *out) {
 
 template <int D>
 cudaError_t launch_attend_dim(const AttendParams &prm, cudaStream_t stream) {
-    switch (row_tile(prm.T, prm.g)) {
+    switch (row_tile(prm.T, prm.g, D)) {
         case 32: return launch_attend_shape<Shape<D, 32>>(attend_kernel<D, 32>, prm, stream);
         case 64: return launch_attend_shape<Shape<D, 64>>(attend_kernel<D, 64>, prm, stream);
         default: return launch_attend_shape<Shape<D, 128>>(attend_kernel<D, 128>, prm, stream);
@@ -648,13 +653,13 @@ cudaError_t launch_attend_dim(const AttendParams &prm, cudaStream_t stream) {
 
 // Two partials a block, their statistics, and the prefix sums.
 size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
-    const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(T, Hq / heads);
+    const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(T, Hq / heads, dim);
     return rows * dim * 4 + rows * 8 + round16(((size_t)B + 1) * 4);
 }
 
 // Items of the largest call these arguments allow; they are counted in 31 bits.
 bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
-    const int g = Hq / c.heads, rt = row_tile(T, g), tn = c.dim == 256 ? 64 : 128;
+    const int g = Hq / c.heads, rt = row_tile(T, g, c.dim), tn = c.dim == 256 ? 64 : 128;
     return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn) < 2147483648.0;
 }
 
@@ -665,7 +670,8 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.box_rows = 16;  // the largest power of two that divides a page, up to a tile
     while (prm.box_rows < tn && c.page_size % (2 * prm.box_rows) == 0) prm.box_rows *= 2;
     prm.page_magic = (1ull << 32) / (unsigned)(c.page_size / 16) + 1;
-    const cudaError_t e = key_map(c, prm.box_rows, &prm.kmap);
+    cudaError_t e = code_map(c, c.k8, prm.box_rows, &prm.kmap);
+    if (e == cudaSuccess) e = code_map(c, c.v8, prm.box_rows, &prm.vmap);
     if (e != cudaSuccess) return e;
     prm.q = a.q;
     prm.ldq = a.ldq;
@@ -681,7 +687,8 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.Hq = a.Hq;
     prm.g = a.Hq / c.heads;
     prm.W = (a.T + 31) / 32;
-    const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(a.T, prm.g);
+    const int rt = row_tile(a.T, prm.g, c.dim);
+    const size_t rows = (size_t)kAttendBlocks * 2 * rt;
     prm.part = static_cast<float *>(a.workspace);
     prm.stat = reinterpret_cast<float2 *>(prm.part + rows * c.dim);
     prm.prefix = reinterpret_cast<int *>(prm.stat + rows);
@@ -691,6 +698,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.skip_loads = opt.skip_loads;
     prm.status = status_word();
     if (!prm.status) return cudaErrorInvalidSymbol;
+    if (rt <= 16) return launch_attend_few(prm, rt, stream);
     switch (c.dim) {
         case 64: return launch_attend_dim<64>(prm, stream);
         case 128: return launch_attend_dim<128>(prm, stream);

@@ -26,9 +26,12 @@ constexpr float kBias = 13.0f;       // p = 2^(x - m + kBias)
 constexpr float kSlack = 2.0f;       // m lags the maximum by at most this
 constexpr int kShift = 6;            // f16 values are code * 2^(e - E + kShift)
 
+}  // namespace
+
 struct AttendParams {
     unsigned long long page_magic;  // floor(2^32 / (page_size / 16)) + 1: divides 16-key groups by a page's
     CUtensorMap kmap;  // the key codes as rows of D bytes, box min(D, 128) x box_rows, swizzled
+    CUtensorMap vmap;  // the value codes likewise
     int box_rows;
     CacheView c;
     const uint16_t *q;
@@ -47,6 +50,11 @@ struct AttendParams {
     int skip_loads;
     int *status;
 };
+
+// The kernels for up to 16 rows of a request and head at dim 128 (bsf8_attend_few.cu).
+cudaError_t launch_attend_few(const AttendParams &prm, int rows, cudaStream_t stream);
+
+namespace {
 
 // A request's context and node counts, inside their bounds.
 __device__ __forceinline__ bool lengths(const AttendParams &p, int b, int &ctx, int &nodes) {
@@ -169,6 +177,19 @@ template <int RB>
 __device__ __forceinline__ uint64_t desc_codes(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(8 * RB >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)(RB == 128 ? 2 : 4) << 61);
+}
+
+// kind::f8f6f4, e4m3 A and B without scales, both given by columns (M- and N-major), M = 128.
+__device__ __forceinline__ constexpr uint32_t idesc_8(int n) {
+    return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
 
 // 32 rows of 16 bytes, unswizzled (8-row groups of 128 bytes one after another) -> four tensor
@@ -435,22 +456,22 @@ struct AttendPipes {
     int scan[32];
 };
 
-__device__ __forceinline__ void init_pipes(AttendPipes &s) {
+__device__ __forceinline__ void init_pipes(AttendPipes &s, int value_readers) {
     for (int i = 0; i < 4; ++i) {
         mbar_init(&s.k_full[i], 2);  // the producer's byte count, the scout
         mbar_init(&s.k_free[i], 1);
         mbar_init(&s.c_full[i], 2);
-        mbar_init(&s.c_free[i], kDeqWarps);
+        mbar_init(&s.c_free[i], value_readers);
     }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&s.v_full[i], kDeqWarps);
+        mbar_init(&s.v_full[i], value_readers);
         mbar_init(&s.pv_done[i], 1);
     }
 }
 
 // Tensor memory, all of it: held before the next kernel's blocks may come.
-__device__ __forceinline__ void hold_tmem(AttendPipes &s, int warp) {
-    if (warp == kMmaWarp) {
+__device__ __forceinline__ void hold_tmem(AttendPipes &s, bool one) {
+    if (one) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -460,11 +481,11 @@ __device__ __forceinline__ void hold_tmem(AttendPipes &s, int warp) {
     fence_after();
 }
 
-__device__ __forceinline__ void free_tmem(uint32_t tmem, int warp) {
+__device__ __forceinline__ void free_tmem(uint32_t tmem, bool one) {
     __syncwarp();
     fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (one) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -477,7 +498,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32
 // Prefix sums of the requests' items, by the whole block (ends with a barrier).
 template <class S>
 __device__ __forceinline__ void sum_items(const AttendParams &p, AttendPipes &s, int *prefix, int warp, int lane) {
-    const int per = (p.B + kThreadsA - 1) / kThreadsA;
+    const int per = (p.B + S::THREADS - 1) / S::THREADS;
     {
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
         int sum = 0;
@@ -502,7 +523,7 @@ __device__ __forceinline__ void sum_items(const AttendParams &p, AttendPipes &s,
     }
     __syncthreads();
     if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= p.B; b += kThreadsA) p.prefix[b] = prefix[b];
+        for (int b = threadIdx.x; b <= p.B; b += S::THREADS) p.prefix[b] = prefix[b];
 }
 
 // A batch of BT tiles' 16-key groups, one a lane: the page of the lane's group (a load that stays
@@ -530,7 +551,8 @@ struct Pages {
     }
 };
 
-// The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values as they are.
+// The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values likewise (RAWV) or as
+// they are.
 template <class S>
 __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w0,
                                    int w1, int warp, int lane) {
@@ -570,9 +592,13 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&s.c_full[slot], bytes);
             __syncwarp();
-            if (go && !p.skip_loads)
-                bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
-                         (uint32_t)(p.box_rows * D), &s.c_full[slot]);
+            if (go && !p.skip_loads) {
+                if constexpr (S::RAWV)
+                    tma_rows(base + S::oRing + slot * S::SLOT + lane * 16 * D, &p.vmap, 0, row, &s.c_full[slot]);
+                else
+                    bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
+                             (uint32_t)(p.box_rows * D), &s.c_full[slot]);
+            }
         }
         pos += tiles;
         if (pos < w1) next_segment<S>(p, g, pos, w1);
@@ -885,7 +911,7 @@ cudaError_t launch_attend_shape(F *kernel, const AttendParams &prm, cudaStream_t
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
-    e = launch_attend_grid(kernel, kAttendBlocks, kThreadsA, attend_smem<S>(prm.B), stream, prm);
+    e = launch_attend_grid(kernel, kAttendBlocks, S::THREADS, attend_smem<S>(prm.B), stream, prm);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)prm.B * prm.T * prm.Hq;
     return launch_attend_grid(join_kernel<S>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, prm);

@@ -1,0 +1,540 @@
+// bsf8_attend_few.cu -- attention over the paged block-scaled fp8 cache for up to 16 rows (a row is a
+// (node, query head) of one request and cache head) at dim 128: single tokens, small trees.
+//
+// The formula, the cut of the work into items and the join are those of bsf8_attend.cu.  What differs
+// is that keys and channels, not rows, fill the MMA's 128 lanes, and that the cached codes enter
+// both products as they are:
+//   S^T = K Q^T   A: a tile's 128 keys x 128 channels of codes, with their exponents as the scales
+//                 of a block-scaled MMA.  B: each row of Q as the sum of two e4m3 parts, the parts as
+//                 two columns with scales 2^eq and 2^(eq - 4); softmax adds them (fp32).
+//   O^T += V^T P  A: the tile's codes again, 128 channels x 128 keys.  A value's exponent belongs to
+//                 a key and 32 channels, so it goes into P: for each of the four channel blocks c a
+//                 copy p 2^(e(key, c) - E), E the segment's largest exponent so far.  Lane quarter c
+//                 of O^T is right in the columns of copy c only, and only those are read.  Each copy
+//                 is the sum of three e4m3 parts (12 bits of p where it is above 2^-14 of the largest,
+//                 half of 2^-25 of that below), in columns of their own: 12 columns a row.
+// So nothing is widened, and an SM's shared memory moves about 90 KB a tile (144 KB in bsf8_attend.cu)
+// while HBM moves 33.
+//
+// Warps: producer, scout (bsf8_attend.cuh); Q (a segment's rows, one segment ahead); one for each
+// product; two sets of four for the softmax, alternating tiles, thread = key.  The rows' reference m
+// (p = 2^(x - m + 6)) is common to a tile's keys: a set takes the one of the tile before from the
+// other set, its warps vote whether any x passes it by more than 2, and only then (a segment's first
+// tiles, as a rule) is a new maximum formed and O rescaled.  Sums stay with the thread, in fp32, to
+// the segment's end.  O and Q are double-buffered by segment.
+//
+// Keys that do not exist or hold a NaN block: p is 0 there, and the warp of the second product
+// clears their codes first, as 0 times a NaN code is not 0.
+#include "bsf8_attend.cuh"
+
+namespace bsf8 {
+
+namespace {
+
+constexpr int kFewWarps = 13, kFewProducer = 8, kFewScout = 9, kFewS = 10, kFewO = 11, kFewQ = 12;
+constexpr float kFewBias = 6.0f;      // p <= 2^8, in e4m3's range
+constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing: any x passes it
+
+template <int ROWS>
+struct FewShape {
+    static constexpr int DIM = 128, RT = ROWS, THREADS = kFewWarps * 32, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
+    static constexpr bool RAWV = true;
+    static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
+    static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
+    static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
+    static constexpr int PBUF = PCOLS * TN * 128;
+    // tensor memory columns: two O, S, scales of two tiles' keys and of two segments' rows
+    static constexpr int CO = 0, CS = 2 * NP, CB = CS + NS * NQ, CA = CB + 8;
+    static_assert(CA + 8 <= 512);
+    static constexpr int oK = 0, oRing = NSLOT * SLOT, oP = 2 * NSLOT * SLOT, oQ = oP + 2 * PBUF;
+    static constexpr int QBUF = 4096, oQs = oQ + 2 * QBUF, oExp = oQs + 2 * 512, oPrefix = oExp + NSLOT * 1024;
+};
+
+template <int ROWS>
+struct FewShared : AttendPipes {
+    uint64_t s_full[4], s_free[4];    // S written; read
+    uint64_t p_full[2];               // P written, O rescaled
+    uint64_t m_full[2];               // a set's tile has its references
+    uint64_t vote[2];                 // a set's warps
+    uint64_t q_full[2], q_free[2];    // a segment's Q written; multiplied
+    uint64_t l_full[2], o_free[2];    // a segment's sums written; output read
+    alignas(16) float off[2][ROWS];   // bias - m, by the parity of the tile
+    alignas(16) int grow[2][2][4];    // votes
+    int epoch[2];                     // how often the references have changed in the segment
+    float most[2][4][ROWS];           // a warp's largest S
+    float sum[2][8][ROWS], soff[2][2][ROWS];  // by the parity of the segment: sums, their bias - m
+    int nan[2][4][ROWS];              // rows that see a NaN of a channel block
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A pair of rows' p times the scale pair sc as three e4m3 pairs: y = h + m / 16 + l / 256.
+__device__ __forceinline__ void split3(uint32_t p2, uint32_t sc, uint32_t &h, uint32_t &m, uint32_t &l) {
+    const uint32_t y = f16x2_mul(p2, sc);
+    h = f16_to_e4m3(y);
+    const uint32_t r = f16x2_mul(f16x2_sub(y, e4m3_to_f16((uint16_t)h)), 0x4C004C00u);  // * 16
+    m = f16_to_e4m3(r);
+    l = f16_to_e4m3(f16x2_mul(f16x2_sub(r, e4m3_to_f16((uint16_t)m)), 0x4C004C00u));
+}
+
+}  // namespace
+
+template <int ROWS>
+__global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __grid_constant__ AttendParams p) {
+    using S = FewShape<ROWS>;
+    constexpr int TN = S::TN;
+    extern __shared__ uint8_t dyn_smem[];
+    uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
+    __shared__ FewShared<ROWS> s;
+    int *const prefix = reinterpret_cast<int *>(base + S::oPrefix);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        init_pipes(s, 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s.s_full[i], 1);
+            mbar_init(&s.s_free[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.m_full[i], 1);
+            mbar_init(&s.vote[i], 4);
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_free[i], 1);
+            mbar_init(&s.l_full[i], 8);
+            mbar_init(&s.o_free[i], 4);
+        }
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < 8 * ROWS; i += S::THREADS) (&s.nan[0][0][0])[i] = 0;
+    hold_tmem(s, warp == kFewS);
+    pdl_trigger();
+    pdl_wait();
+    sum_items<S>(p, s, prefix, warp, lane);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s.tmem, 0);
+    const long long total = prefix[p.B];
+    const int w0 = range_start(total, blockIdx.x), w1 = range_start(total, blockIdx.x + 1);
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool { return wait_warp(bar, parity, p.tries); };
+    bool ok = true;  // no wait of this thread ran out
+    const Segment first = segment_at<S>(p, prefix, w0, w1);
+
+    if (warp == kFewProducer) {
+        ok = produce<S>(p, s, base, first, w0, w1, warp, lane);
+    } else if (warp == kFewScout) {
+        ok = scout<S>(p, s, base, first, w0, w1, warp, lane);
+    } else if (warp == kFewQ) {
+        // ------------------------------------------------------------ Q
+        // Eight lanes a row.  Each row scaled by a power of two 2^-eq so that its largest lies in
+        // [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4.  Exact for bf16 values
+        // within 2^14 of the row's largest, else off by at most 2^-22 of that.
+        Segment g = first;
+        int seg = 0;
+        for (int pos = w0; pos < w1; ++seg) {
+            const int par = seg & 1;
+            ok = seg < 2 || wait(&s.q_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
+            if (!ok) break;
+            uint8_t *const qb = base + S::oQ + par * S::QBUF;
+#pragma unroll 1
+            for (int r0 = 0; r0 < ROWS; r0 += 4) {
+                const int row = r0 + (lane >> 3), u = lane & 7;
+                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (row < g.nodes * p.g) {  // one row tile holds all rows
+                    const int t = row / p.g, hq = g.h * p.g + row - t * p.g;
+                    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)g.b * p.T + t) * p.ldq +
+                                                                     (size_t)hq * S::DIM + 16 * u);
+                    v[0] = q[0];
+                    v[1] = q[1];
+                }
+                const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+                uint32_t am = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll
+                for (int k = 1; k < 8; k <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, k));
+                const int eq = max((int)(am >> 7) - 127 - 7, -100);  // at most 121
+                const float qs = pow2i(-eq);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t x = pack_f16(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[j] & 0xFFFF0000u) * qs);
+                    const uint32_t h2 = f16_to_e4m3(x);
+                    const uint32_t l2 = f16_to_e4m3(f16x2_mul(f16x2_sub(x, e4m3_to_f16((uint16_t)h2)), 0x4C004C00u));
+                    hi[j >> 1] = j & 1 ? hi[j >> 1] | (h2 << 16) : h2;
+                    lo[j >> 1] = j & 1 ? lo[j >> 1] | (l2 << 16) : l2;
+                }
+                // rows of 128 bytes, 128-byte swizzle (ROWS is a multiple of 8)
+                uint8_t *const d = qb + row * 128 + ((u ^ (row & 7)) << 4);
+                *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(d + ROWS * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (u == 0) {  // the scales of columns row and ROWS + row, the same for every 32 channels
+                    uint32_t *const sc = reinterpret_cast<uint32_t *>(base + S::oQs + par * 512);
+                    sc[4 * row] = 0x01010101u * (uint32_t)(eq + 127);
+                    sc[4 * (ROWS + row)] = 0x01010101u * (uint32_t)(eq + 123);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.q_full[par]);
+            pos += g.kv1 - g.kv0;
+            if (pos < w1) next_segment<S>(p, g, pos, w1);
+        }
+    } else if (warp == kFewS) {
+        // ------------------------------------------------------------ S^T = K Q^T
+        const bool one = elect_one();
+        int tile = 0, seg = 0;
+        Segment g = first;
+        for (int pos = w0; pos < w1 && ok; ++seg) {
+            const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0), par = seg & 1;
+            ok = wait(&s.q_full[par], (uint32_t)((seg >> 1) & 1));
+            if (!ok) break;
+            fence_after();
+            const uint32_t sfb = tmem + S::CA + 4 * par;
+            if (one) copy_scales(sfb, desc_scales(smem_u32(base + S::oQs) + par * 512));  // in order with the MMAs
+            __syncwarp();
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                const int slot = tile % S::NSLOT, buf = tile % S::NS;
+                ok = wait(&s.k_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) &&
+                     (tile < S::NS || wait(&s.s_free[buf], (uint32_t)((tile / S::NS) & 1) ^ 1u));
+                if (!ok) break;
+                fence_after();
+                const uint32_t sfa = tmem + S::CB + 4 * (tile & 1), d = tmem + S::CS + buf * S::NQ;
+                const uint64_t ad = desc_codes<128>(smem_u32(base + S::oK) + slot * S::SLOT);
+                const uint64_t bd = desc_codes<128>(smem_u32(base + S::oQ) + par * S::QBUF);
+                if (one) {
+                    copy_scales(sfa, desc_scales(smem_u32(base + S::oExp) + slot * 1024));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)  // 32 channels a step
+                        umma_mx_ss(d, ad + 2 * ks, bd + 2 * ks, idesc_mx(S::NQ, ks, 0), sfa, sfb, ks > 0);
+                    commit_a(&s.s_full[buf]);
+                    commit_a(&s.k_free[slot]);
+                    if (i + 1 == tiles) commit_a(&s.q_free[par]);
+                }
+                __syncwarp();
+            }
+            pos += tiles;
+            if (pos < w1) next_segment<S>(p, g, pos, w1);
+        }
+        // the last products must be done before tensor memory goes back (bounded)
+        if (tile > 0) (void)wait(&s.s_full[(tile - 1) % S::NS], (uint32_t)(((tile - 1) / S::NS) & 1));
+    } else if (warp == kFewO) {
+        // ------------------------------------------------------------ O^T += V^T P
+        const bool one = elect_one();
+        int tile = 0, seg = 0;
+        Segment g = first;
+        for (int pos = w0; pos < w1 && ok; ++seg) {
+            const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0), par = seg & 1;
+            ok = seg < 2 || wait(&s.o_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
+            for (int i = 0; i < tiles && ok; ++i, ++tile) {
+                const int slot = tile % S::NSLOT, buf = tile & 1;
+                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1));
+                if (!ok) break;
+                const TileInfo inf = load_info(&s.info[tile % kInfo]);
+                if (inf.flags & 1) {
+                    const int keys = g.ctx + g.nodes - (g.kv0 + i) * TN;
+                    uint8_t *const v = base + S::oRing + slot * S::SLOT;
+                    for (int key = lane; key < TN; key += 32) {
+                        const bool gone = key >= keys || !((inf.valid >> (key >> 4)) & 1);
+                        const uint32_t bad = gone ? 15u : inf.flags & 2 ? s.nanblk[tile % kInfo][key] : 0u;
+                        for (int u = 0; u < 8; ++u)
+                            if ((bad >> (u >> 1)) & 1u)
+                                *reinterpret_cast<uint4 *>(v + key * 128 + ((u ^ (key & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
+                ok = wait(&s.p_full[buf], (uint32_t)((tile >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                const uint32_t d = tmem + S::CO + par * S::NP;
+                const uint64_t ad = desc_a(smem_u32(base + S::oRing) + slot * S::SLOT, TN * 128);
+                const uint64_t bd = desc_a(smem_u32(base + S::oP) + buf * S::PBUF, TN * 128);
+                if (one) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)  // 32 keys a step: four 8-key atoms
+                        umma_8(d, ad + ks * (4096 >> 4), bd + ks * (4096 >> 4), idesc_8(S::NP), i > 0 || ks > 0);
+                    commit_a(&s.pv_done[buf]);
+                    commit_a(&s.c_free[slot]);
+                }
+                __syncwarp();
+            }
+            pos += tiles;
+            if (pos < w1) next_segment<S>(p, g, pos, w1);
+        }
+        if (tile > 0) (void)wait(&s.pv_done[(tile - 1) & 1], (uint32_t)(((tile - 1) >> 1) & 1));
+    } else {
+        // ------------------------------------------------------------ softmax and output
+        const int set = warp >> 2, quad = warp & 3, key = 32 * quad + lane;  // key of a tile, channel of O^T
+        const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
+        const float c = p.scale_log2;
+        uint32_t vote_ph = 0;
+        auto set_sync = [&]() -> bool {  // the set's four warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.vote[set]);
+            vote_ph ^= 1u;
+            return wait(&s.vote[set], vote_ph ^ 1u);
+        };
+        int it = 0, seg = 0;
+        Segment g = first;
+        for (int pos = w0; pos < w1 && ok; ++seg) {
+            const int tiles = g.kv1 - g.kv0, par = seg & 1, rows = g.nodes * p.g;
+            float l[ROWS], off[ROWS], last[ROWS];  // sums, in 2^(m - bias); bias - m now, and at the set's last tile
+            int epoch = 0;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                l[r] = 0.0f;
+                off[r] = last[r] = kUnseen;
+            }
+            for (int i = 0; i < tiles; ++i, ++it) {
+                if ((it & 1) != set) continue;
+                const int info = it % kInfo, buf = it % S::NS;
+                ok = wait(&s.s_full[buf], (uint32_t)((it / S::NS) & 1));
+                if (!ok) break;
+                fence_after();
+                uint32_t x[ROWS], xl[ROWS];
+                ld_cols(tl + S::CS + buf * S::NQ, x);
+                ld_cols(tl + S::CS + buf * S::NQ + ROWS, xl);
+                const TileInfo inf = load_info(&s.info[info]);
+                const uint32_t ex = *reinterpret_cast<const uint32_t *>(base + S::oExp + (it % S::NSLOT) * 1024 + 512 + 4 * key);
+                const int slot = (g.kv0 + i) * TN + key;  // the thread's cache slot
+                // the references of the tile before, from the other set (at a segment's start too its tile is
+                // waited for: it has then read the references that this set is about to replace)
+                int now = 0;
+                if (it > 0) ok = wait(&s.m_full[set ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (i > 0) {
+                    now = s.epoch[(it - 1) & 1];
+#pragma unroll
+                    for (int r = 0; r < ROWS; r += 4) {
+                        const float4 v = *reinterpret_cast<const float4 *>(&s.off[(it - 1) & 1][r]);
+                        off[r] = v.x, off[r + 1] = v.y, off[r + 2] = v.z, off[r + 3] = v.w;
+                    }
+                }
+                wait_ld();
+                if (!ok) break;
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.s_free[buf]);
+                float sv[ROWS];
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) sv[r] = __uint_as_float(x[r]) + __uint_as_float(xl[r]);
+                uint32_t vis = 0xFFFFFFFFu;  // rows that see the key
+                if ((g.kv0 + i + 1) * TN > g.ctx || inf.valid != 0xFF) {
+                    const int j = slot - g.ctx;
+                    if (!((inf.valid >> (key >> 4)) & 1) || j >= g.nodes) vis = 0;
+                    else if (j >= 0) {
+                        vis = 0;
+                        for (int t = 0; t < g.nodes; ++t) {
+                            const bool sees = p.mask ? (p.mask[((size_t)g.b * p.T + t) * p.W + (j >> 5)] >> (j & 31)) & 1 : j <= t;
+                            if (sees) vis |= low_bits(p.g) << (t * p.g);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+                        if (!((vis >> r) & 1u)) sv[r] = -INFINITY;
+                }
+                bool up = false;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) up |= fmaf(sv[r], c, off[r]) > kFewBias + kSlack;
+                const bool any = __any_sync(0xFFFFFFFFu, up);
+                int *const votes = s.grow[set][(it >> 1) & 1];
+                if (lane == 0) votes[quad] = any;
+                ok = set_sync();
+                if (!ok) break;
+                const int4 v4 = *reinterpret_cast<const int4 *>(votes);
+                const bool grow = v4.x | v4.y | v4.z | v4.w;
+                float f[ROWS];
+                if (grow) {
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        const float w = warp_max(sv[r]);
+                        if (lane == 0) s.most[set][quad][r] = w;
+                    }
+                    ok = set_sync();
+                    if (!ok) break;
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        const float mt = fmaxf(fmaxf(s.most[set][0][r], s.most[set][1][r]),
+                                               fmaxf(s.most[set][2][r], s.most[set][3][r]));
+                        const float next = fmaf(mt, c, off[r]) > kFewBias + kSlack ? kFewBias - mt * c : off[r];
+                        f[r] = next == off[r] ? 1.0f : ex2(next - off[r]);
+                        off[r] = next;
+                    }
+                    ++now;
+                }
+                if (quad == 0) {
+                    if (lane == 0) {
+#pragma unroll
+                        for (int r = 0; r < ROWS; r += 4)
+                            *reinterpret_cast<float4 *>(&s.off[it & 1][r]) = make_float4(off[r], off[r + 1], off[r + 2], off[r + 3]);
+                        s.epoch[it & 1] = now;
+                        mbar_arrive(&s.m_full[set]);
+                    }
+                    __syncwarp();
+                }
+                if (now != epoch) {
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        l[r] *= off[r] == last[r] ? 1.0f : ex2(off[r] - last[r]);
+                        last[r] = off[r];
+                    }
+                    epoch = now;
+                }
+                uint32_t p2[ROWS / 2];
+#pragma unroll
+                for (int r = 0; r < ROWS; r += 2) {
+                    const float a = ex2(fmaf(sv[r], c, off[r])), b = ex2(fmaf(sv[r + 1], c, off[r + 1]));
+                    l[r] += a;
+                    l[r + 1] += b;
+                    p2[r / 2] = pack_f16(a, b);
+                }
+                // ---- O in the units of the new references and value exponent
+                if (i > 0 && (grow || inf.rise)) {
+                    ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                    if (!ok) break;
+                    fence_after();
+                    const float fv = pow2i(max(-inf.rise, -149));
+#pragma unroll 1
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t at = tl + S::CO + par * S::NP + (4 * k + quad) * ROWS;
+                        uint32_t o[ROWS];
+                        ld_cols(at, o);
+                        wait_ld();
+#pragma unroll
+                        for (int r = 0; r < ROWS; ++r)
+                            o[r] = __float_as_uint(__uint_as_float(o[r]) * (grow ? f[r] * fv : fv));
+                        st_cols(at, o);
+                    }
+                    wait_st();
+                    fence_before();
+                }
+                // ---- P, once the product before the last has read its place
+                ok = it < 2 || wait(&s.pv_done[it & 1], (uint32_t)((it >> 1) & 1) ^ 1u);
+                if (!ok) break;
+                uint8_t *const pb = base + S::oP + (it & 1) * S::PBUF + key * 128;
+                // column 4 ROWS part + ROWS block + row of the key's 128-byte rows, swizzled
+                constexpr int U = ROWS == 8 ? 2 : 4;  // 16-byte units a part
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    uint32_t w[3][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {  // four rows of a block a word
+                        const int blk = ROWS == 8 ? 2 * u + (j >> 1) : u, r = ROWS == 8 ? 4 * (j & 1) : 4 * j;
+                        const int e = (int)((ex >> (8 * blk)) & 0xFFu);
+                        const uint32_t sc = e == 255 ? 0u : f16_pow2(min(e - inf.ev, 0));
+                        uint32_t a[3], b[3];
+                        split3(p2[r / 2], sc, a[0], a[1], a[2]);
+                        split3(p2[r / 2 + 1], sc, b[0], b[1], b[2]);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) w[k][j] = a[k] | (b[k] << 16);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const int un = k * U + u;
+                        *reinterpret_cast<uint4 *>(pb + (un >> 3) * (TN * 128) + (((un & 7) ^ (key & 7)) << 4)) =
+                            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                    }
+                }
+                if (inf.flags & 2) {
+                    const uint32_t bad = s.nanblk[info][key];
+                    for (int r = 0; r < ROWS && r < rows; ++r)
+                        if ((vis >> r) & 1u)
+                            for (int k = 0; k < 4; ++k)
+                                if ((bad >> k) & 1u) s.nan[par][k][r] = 1;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[it & 1]);
+            }
+            if (!ok) break;
+            // ---- the segment's sums
+            ok = seg < 2 || wait(&s.o_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
+            if (!ok) break;
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                float a = l[r];
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, k);
+                if (lane == 0) {
+                    s.sum[par][warp][r] = a;
+                    if (quad == 0) s.soff[par][set][r] = last[r];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.l_full[par]);
+            if (((it - 1) & 1) == set) {
+                // ---- the output, by the set of the last tile; thread = channel
+                ok = wait(&s.l_full[par], (uint32_t)((seg >> 1) & 1)) &&
+                     wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (!ok) break;
+                fence_after();
+                const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
+                const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
+                const float fv = pow2i(s.info[(it - 1) % kInfo].ev - 127);
+                // lane r: row r's sum, in units of the last reference
+                const int rl = lane % ROWS;
+                const float end = s.soff[par][set][rl];
+                float L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) {
+                    const float q = s.soff[par][w >> 2][rl], a = s.sum[par][w][rl];
+                    L += a == 0.0f ? 0.0f : a * (q == end ? 1.0f : ex2(end - q));
+                }
+                const float inv = L == 0.0f ? 0.0f : fv / L;
+                const bool bad = s.nan[par][quad][rl];
+                __syncwarp();
+                if (lane < ROWS) s.nan[par][quad][lane] = 0;
+                if (quad == 0 && lane < ROWS && lane < rows) {
+                    const float Lt = L * (1.0f / 64.0f);  // bias 6
+                    const float M = end == kUnseen ? -INFINITY : kFewBias - end;
+                    const int t = lane / p.g, hq = g.h * p.g + lane - t * p.g;
+                    if (!whole)
+                        p.stat[(size_t)slotw * ROWS + lane] = make_float2(M, Lt);
+                    else if (p.lse)
+                        p.lse[((size_t)g.b * p.T + t) * p.Hq + hq] =
+                            L == 0.0f ? -INFINITY : (M + log2f(Lt)) * 0.69314718055994531f;
+                }
+                float y[ROWS];
+#pragma unroll
+                for (int k = 2; k >= 0; --k) {
+                    uint32_t o[ROWS];
+                    ld_cols(tl + S::CO + par * S::NP + (4 * k + quad) * ROWS, o);
+                    wait_ld();
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) y[r] = (k == 2 ? 0.0f : y[r] * 0.0625f) + __uint_as_float(o[r]);
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.o_free[par]);
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const float k = __shfl_sync(0xFFFFFFFFu, inv, r);
+                    const bool nan = __shfl_sync(0xFFFFFFFFu, (int)bad, r);
+                    const float z = nan ? __uint_as_float(0x7FC00000u) : k == 0.0f ? 0.0f : y[r] * k;
+                    if (r < rows) {
+                        if (whole) {
+                            const int t = r / p.g, hq = g.h * p.g + r - t * p.g;
+                            p.out[(((size_t)g.b * p.T + t) * p.Hq + hq) * S::DIM + key] = (uint16_t)pack_bf(z, 0.0f);
+                        } else {
+                            p.part[((size_t)slotw * ROWS + r) * S::DIM + key] = z;
+                        }
+                    }
+                }
+            }
+            pos += tiles;
+            if (pos < w1) next_segment<S>(p, g, pos, w1);
+        }
+    }
+
+    if (!ok) report_timeout(p.status);
+    free_tmem(tmem, warp == kFewS);
+}
+
+cudaError_t launch_attend_few(const AttendParams &prm, int rows, cudaStream_t stream) {
+    return rows <= 8 ? launch_attend_shape<FewShape<8>>(attend_few_kernel<8>, prm, stream)
+                     : launch_attend_shape<FewShape<16>>(attend_few_kernel<16>, prm, stream);
+}
+
+}  // namespace bsf8
