@@ -51,7 +51,6 @@ namespace {
 template <int D, int ROWS>
 struct Shape {
     static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
-    static constexpr bool RAWV = false;
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        init_pipes(s, kDeqWarps);
+        init_pipes(s);
         for (int i = 0; i < 8; ++i) mbar_init(&s.m_full[i >> 2][i & 3], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.s_full[i], 1);

@@ -430,6 +430,11 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, uint3
     return left != 0;
 }
 
+struct BlockShared {
+    uint32_t tmem;
+    int scan[32];
+};
+
 // What the scout says of a tile.  An entry is written again eight tiles later, once the dequant
 // warps have read the slot of the tile four later, thus after the softmax of the tile two later.
 struct __align__(16) TileInfo {
@@ -445,32 +450,30 @@ __device__ __forceinline__ TileInfo load_info(const TileInfo *i) {
 }
 
 // What the roles of a block tell each other by, as far as the kernels share it.
-struct AttendPipes {
+struct AttendPipes : BlockShared {
     uint64_t k_full[4], k_free[4];  // ring slots of keys: codes landed and scales written; multiplied
     uint64_t c_full[4], c_free[4];  // of values: codes landed and exponents written; read by all dequant warps
     uint64_t v_full[2];             // the f16 values of a tile are written
     uint64_t pv_done[2];            // O updated, P and the f16 values read
-    uint32_t tmem;
     TileInfo info[kInfo];
     uint8_t nanblk[kInfo][128];     // where a value block holds NaN: each key's NaN blocks
-    int scan[32];
 };
 
-__device__ __forceinline__ void init_pipes(AttendPipes &s, int value_readers) {
+__device__ __forceinline__ void init_pipes(AttendPipes &s) {
     for (int i = 0; i < 4; ++i) {
         mbar_init(&s.k_full[i], 2);  // the producer's byte count, the scout
         mbar_init(&s.k_free[i], 1);
         mbar_init(&s.c_full[i], 2);
-        mbar_init(&s.c_free[i], value_readers);
+        mbar_init(&s.c_free[i], kDeqWarps);
     }
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&s.v_full[i], value_readers);
+        mbar_init(&s.v_full[i], kDeqWarps);
         mbar_init(&s.pv_done[i], 1);
     }
 }
 
 // Tensor memory, all of it: held before the next kernel's blocks may come.
-__device__ __forceinline__ void hold_tmem(AttendPipes &s, bool one) {
+__device__ __forceinline__ void hold_tmem(BlockShared &s, bool one) {
     if (one) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s.tmem))
                      : "memory");
@@ -497,7 +500,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32
 
 // Prefix sums of the requests' items, by the whole block (ends with a barrier).
 template <class S>
-__device__ __forceinline__ void sum_items(const AttendParams &p, AttendPipes &s, int *prefix, int warp, int lane) {
+__device__ __forceinline__ void sum_items(const AttendParams &p, BlockShared &s, int *prefix, int warp, int lane) {
     const int per = (p.B + S::THREADS - 1) / S::THREADS;
     {
         const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
@@ -551,8 +554,7 @@ struct Pages {
     }
 };
 
-// The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values likewise (RAWV) or as
-// they are.
+// The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values as they are.
 template <class S>
 __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w0,
                                    int w1, int warp, int lane) {
@@ -592,13 +594,9 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
             if (!ok) break;
             if (lane == 0) mbar_arrive_expect_tx(&s.c_full[slot], bytes);
             __syncwarp();
-            if (go && !p.skip_loads) {
-                if constexpr (S::RAWV)
-                    tma_rows(base + S::oRing + slot * S::SLOT + lane * 16 * D, &p.vmap, 0, row, &s.c_full[slot]);
-                else
-                    bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
-                             (uint32_t)(p.box_rows * D), &s.c_full[slot]);
-            }
+            if (go && !p.skip_loads)
+                bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
+                         (uint32_t)(p.box_rows * D), &s.c_full[slot]);
         }
         pos += tiles;
         if (pos < w1) next_segment<S>(p, g, pos, w1);

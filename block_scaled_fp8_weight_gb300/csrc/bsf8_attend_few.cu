@@ -16,29 +16,33 @@
 // So nothing is widened, and an SM's shared memory moves about 90 KB a tile (144 KB in bsf8_attend.cu)
 // while HBM moves 33.
 //
-// Warps: producer, scout (bsf8_attend.cuh); Q (a segment's rows, one segment ahead); one for each
-// product; two sets of four for the softmax, alternating tiles, thread = key.  The rows' reference m
-// (p = 2^(x - m + 6)) is common to a tile's keys: a set takes the one of the tile before from the
-// other set, its warps vote whether any x passes it by more than 2, and only then (a segment's first
+// Warps: a producer of keys (codes, both kinds of exponents), one of values (codes, and a segment's Q,
+// which so comes tiles ahead); one for each product; two sets of four for the softmax, alternating
+// tiles, thread = key.  The rows' reference m (p = 2^(x - m + 6)) and the value exponent E are common
+// to a tile's keys: a set takes those of the tile before from the other set, its warps exchange their
+// largest exponents and whether any x passes its m by more than 2, and only then (a segment's first
 // tiles, as a rule) is a new maximum formed and O rescaled.  Sums stay with the thread, in fp32, to
 // the segment's end.  O and Q are double-buffered by segment.
 //
-// Keys that do not exist or hold a NaN block: p is 0 there, and the warp of the second product
-// clears their codes first, as 0 times a NaN code is not 0.
+// Keys that do not exist or hold a NaN block: p is 0 there, and the key's thread clears their value
+// codes first, as 0 times a NaN code is not 0.
 #include "bsf8_attend.cuh"
 
 namespace bsf8 {
 
 namespace {
 
-constexpr int kFewWarps = 13, kFewProducer = 8, kFewScout = 9, kFewS = 10, kFewO = 11, kFewQ = 12;
+constexpr int kFewWarps = 12, kFewK = 8, kFewV = 9, kFewS = 10, kFewO = 11;
+// Tiles whose value exponents and flags are kept: the keys' producer fills an entry again eight tiles
+// later, once the S of the tile four later is done, which takes the place of this tile's or a later one's
+// S, thus after the softmax has read that.
+constexpr int kRing = 8;
 constexpr float kFewBias = 6.0f;      // p <= 2^8, in e4m3's range
 constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing: any x passes it
 
 template <int ROWS>
 struct FewShape {
     static constexpr int DIM = 128, RT = ROWS, THREADS = kFewWarps * 32, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
-    static constexpr bool RAWV = true;
     static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
     static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
@@ -47,24 +51,110 @@ struct FewShape {
     static constexpr int CO = 0, CS = 2 * NP, CB = CS + NS * NQ, CA = CB + 8;
     static_assert(CA + 8 <= 512);
     static constexpr int oK = 0, oRing = NSLOT * SLOT, oP = 2 * NSLOT * SLOT, oQ = oP + 2 * PBUF;
-    static constexpr int QBUF = 4096, oQs = oQ + 2 * QBUF, oExp = oQs + 2 * 512, oPrefix = oExp + NSLOT * 1024;
+    static constexpr int QBUF = 4096, oQs = oQ + 2 * QBUF;
+    // a slot's key exponents, as tensor memory wants them and as they come; the values' as they come
+    static constexpr int oExp = oQs + 2 * 512, oVex = oExp + NSLOT * 1024, oPrefix = oVex + kRing * 512;
 };
 
 template <int ROWS>
-struct FewShared : AttendPipes {
+struct FewShared : BlockShared {
+    uint64_t k_full[4], k_free[4];    // ring slots of keys: codes and exponents landed; multiplied
+    uint64_t c_full[4], c_free[4];    // of values
     uint64_t s_full[4], s_free[4];    // S written; read
     uint64_t p_full[2];               // P written, O rescaled
+    uint64_t pv_done[2];              // O updated, P and the values read
     uint64_t m_full[2];               // a set's tile has its references
     uint64_t vote[2];                 // a set's warps
     uint64_t q_full[2], q_free[2];    // a segment's Q written; multiplied
     uint64_t l_full[2], o_free[2];    // a segment's sums written; output read
     alignas(16) float off[2][ROWS];   // bias - m, by the parity of the tile
     alignas(16) int grow[2][2][4];    // votes
-    int epoch[2];                     // how often the references have changed in the segment
+    int epoch[2], ev[2];              // how often the references have changed in the segment; E
     float most[2][4][ROWS];           // a warp's largest S
     float sum[2][8][ROWS], soff[2][2][ROWS];  // by the parity of the segment: sums, their bias - m
     int nan[2][4][ROWS];              // rows that see a NaN of a channel block
+    int valid[kRing];                 // a tile's 16-key groups that exist (bit i)
+    int pages[2][2][32];              // the producers' block table entries: of a batch, of the next
 };
+
+// A batch of tiles' boxes (box_rows keys, inside a page and a tile), one a lane: 32 / boxes tiles.
+// The table's entries come by cp.async, a batch ahead.
+struct Batch {
+    int *ring;     // [2][32]
+    int gpb, nb;   // 16-key groups a box, boxes a tile
+    int phase;
+
+    // exact: group * (magic * d - 2^32) < 2^32 for groups below 2^26 and d <= 64
+    static __device__ __forceinline__ int in_page(const AttendParams &p, int grp) {
+        return (int)(((unsigned long long)(unsigned)grp * p.page_magic) >> 32);
+    }
+    __device__ __forceinline__ int group(int tile, int lane) const { return (tile + lane / nb) * 8 + lane % nb * gpb; }
+    __device__ __forceinline__ void ask(const AttendParams &p, const Segment &g, int tile, int lane) {
+        const int grp = group(tile, lane);
+        int *const at = ring + 32 * phase + lane;
+        if (16 * grp < g.ctx + g.nodes)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at)),
+                         "l"(p.c.table + (size_t)g.b * p.c.table_pages + in_page(p, grp))
+                         : "memory");
+        phase ^= 1;
+    }
+    // The cache rows (head h) of the batch asked for last, -1 where there are none.
+    __device__ __forceinline__ int rows(const AttendParams &p, const Segment &g, int tile, int lane) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const int grp = group(tile, lane), page = ring[32 * (phase ^ 1) + lane];
+        if (16 * grp >= g.ctx + g.nodes) return -1;
+        if ((unsigned)page >= (unsigned)p.c.pages) {
+            report_index(p.status);
+            return -1;
+        }
+        return (page * p.c.heads + g.h - in_page(p, grp)) * p.c.page_size + 16 * grp;
+    }
+};
+
+// A segment's rows of Q, by a warp, eight lanes a row.  Each row scaled by a power of two 2^-eq so that
+// its largest lies in [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4.  Exact for
+// bf16 values within 2^14 of the row's largest, else off by at most 2^-22 of that.
+template <int ROWS>
+__device__ __forceinline__ void put_q(const AttendParams &p, const Segment &g, uint8_t *qb, uint32_t *sc, int lane) {
+#pragma unroll 1
+    for (int r0 = 0; r0 < ROWS; r0 += 4) {
+        const int row = r0 + (lane >> 3), u = lane & 7;
+        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (row < g.nodes * p.g) {  // one row tile holds all rows
+            const int t = row / p.g, hq = g.h * p.g + row - t * p.g;
+            const uint4 *q =
+                reinterpret_cast<const uint4 *>(p.q + ((size_t)g.b * p.T + t) * p.ldq + (size_t)hq * 128 + 16 * u);
+            v[0] = q[0];
+            v[1] = q[1];
+        }
+        const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        uint32_t am = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+#pragma unroll
+        for (int k = 1; k < 8; k <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, k));
+        const int eq = max((int)(am >> 7) - 127 - 7, -100);  // at most 121
+        const float qs = pow2i(-eq);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t x = pack_f16(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[j] & 0xFFFF0000u) * qs);
+            const uint32_t h2 = f16_to_e4m3(x);
+            const uint32_t l2 = f16_to_e4m3(f16x2_mul(f16x2_sub(x, e4m3_to_f16((uint16_t)h2)), 0x4C004C00u));
+            hi[j >> 1] = j & 1 ? hi[j >> 1] | (h2 << 16) : h2;
+            lo[j >> 1] = j & 1 ? lo[j >> 1] | (l2 << 16) : l2;
+        }
+        // rows of 128 bytes, 128-byte swizzle (ROWS is a multiple of 8)
+        uint8_t *const d = qb + row * 128 + ((u ^ (row & 7)) << 4);
+        *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(d + ROWS * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (u == 0) {  // the scales of columns row and ROWS + row, the same for every 32 channels
+            sc[4 * row] = 0x01010101u * (uint32_t)(eq + 127);
+            sc[4 * (ROWS + row)] = 0x01010101u * (uint32_t)(eq + 123);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
 
 __device__ __forceinline__ float warp_max(float x) {
     float y;
@@ -94,13 +184,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        init_pipes(s, 1);
         for (int i = 0; i < 4; ++i) {
+            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_free[i], 1);
+            mbar_init(&s.c_full[i], 1);
+            mbar_init(&s.c_free[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.s_free[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.p_full[i], 4);
+            mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.m_full[i], 1);
             mbar_init(&s.vote[i], 4);
             mbar_init(&s.q_full[i], 1);
@@ -122,66 +216,68 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
     bool ok = true;  // no wait of this thread ran out
     const Segment first = segment_at<S>(p, prefix, w0, w1);
 
-    if (warp == kFewProducer) {
-        ok = produce<S>(p, s, base, first, w0, w1, warp, lane);
-    } else if (warp == kFewScout) {
-        ok = scout<S>(p, s, base, first, w0, w1, warp, lane);
-    } else if (warp == kFewQ) {
-        // ------------------------------------------------------------ Q
-        // Eight lanes a row.  Each row scaled by a power of two 2^-eq so that its largest lies in
-        // [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4.  Exact for bf16 values
-        // within 2^14 of the row's largest, else off by at most 2^-22 of that.
+    if (warp == kFewK || warp == kFewV) {
+        // ------------------------------------------------------------ producers
+        const bool value = warp == kFewV;
+        uint64_t *const full = value ? s.c_full : s.k_full, *const free = value ? s.c_free : s.k_free;
+        Batch batch{&s.pages[value][0][0], p.box_rows / 16, TN / p.box_rows, 0};
+        const int bt = 32 / batch.nb;
+        const uint32_t box_bytes = (uint32_t)p.box_rows * (value ? 128u : 128u + 2 * S::EB);
+        int tile = 0, seg = 0;
         Segment g = first;
-        int seg = 0;
-        for (int pos = w0; pos < w1; ++seg) {
-            const int par = seg & 1;
-            ok = seg < 2 || wait(&s.q_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
-            if (!ok) break;
-            uint8_t *const qb = base + S::oQ + par * S::QBUF;
-#pragma unroll 1
-            for (int r0 = 0; r0 < ROWS; r0 += 4) {
-                const int row = r0 + (lane >> 3), u = lane & 7;
-                uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (row < g.nodes * p.g) {  // one row tile holds all rows
-                    const int t = row / p.g, hq = g.h * p.g + row - t * p.g;
-                    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + ((size_t)g.b * p.T + t) * p.ldq +
-                                                                     (size_t)hq * S::DIM + 16 * u);
-                    v[0] = q[0];
-                    v[1] = q[1];
+        for (int pos = w0; pos < w1 && ok; ++seg) {
+            const int tiles = g.kv1 - g.kv0, par = seg & 1;
+            batch.ask(p, g, g.kv0, lane);
+            if (value) {
+                ok = seg < 2 || wait(&s.q_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
+                if (!ok) break;
+                put_q<ROWS>(p, g, base + S::oQ + par * S::QBUF, reinterpret_cast<uint32_t *>(base + S::oQs + par * 512), lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.q_full[par]);
+            }
+            int rows = -1;
+            for (int i = 0; i < tiles; ++i, ++tile) {
+                const int j = i & (bt - 1);
+                if (j == 0) {
+                    rows = batch.rows(p, g, g.kv0 + i, lane);
+                    if (i + bt < tiles) batch.ask(p, g, g.kv0 + i + bt, lane);
                 }
-                const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-                uint32_t am = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-#pragma unroll
-                for (int k = 1; k < 8; k <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, k));
-                const int eq = max((int)(am >> 7) - 127 - 7, -100);  // at most 121
-                const float qs = pow2i(-eq);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t x = pack_f16(__uint_as_float(w[j] << 16) * qs, __uint_as_float(w[j] & 0xFFFF0000u) * qs);
-                    const uint32_t h2 = f16_to_e4m3(x);
-                    const uint32_t l2 = f16_to_e4m3(f16x2_mul(f16x2_sub(x, e4m3_to_f16((uint16_t)h2)), 0x4C004C00u));
-                    hi[j >> 1] = j & 1 ? hi[j >> 1] | (h2 << 16) : h2;
-                    lo[j >> 1] = j & 1 ? lo[j >> 1] | (l2 << 16) : l2;
+                const int slot = tile % S::NSLOT;
+                ok = tile < S::NSLOT || wait(&free[slot], (uint32_t)((tile / S::NSLOT) & 1) ^ 1u);
+                if (!ok) break;
+                const int row = __shfl_sync(0xFFFFFFFFu, rows, (j * batch.nb + lane / batch.gpb) & 31);  // of group lane
+                const bool there = lane < 8 && row >= 0;
+                const bool go = there && lane % batch.gpb == 0;
+                const uint32_t groups =
+                    __ballot_sync(0xFFFFFFFFu, there && 16 * ((g.kv0 + i) * 8 + lane) < g.ctx + g.nodes);
+                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, go));
+                if (lane == 0) {
+                    if (!value) s.valid[tile % kRing] = (int)groups;
+                    mbar_arrive_expect_tx(&full[slot], boxes * box_bytes);
                 }
-                // rows of 128 bytes, 128-byte swizzle (ROWS is a multiple of 8)
-                uint8_t *const d = qb + row * 128 + ((u ^ (row & 7)) << 4);
-                *reinterpret_cast<uint4 *>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(d + ROWS * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (u == 0) {  // the scales of columns row and ROWS + row, the same for every 32 channels
-                    uint32_t *const sc = reinterpret_cast<uint32_t *>(base + S::oQs + par * 512);
-                    sc[4 * row] = 0x01010101u * (uint32_t)(eq + 127);
-                    sc[4 * (ROWS + row)] = 0x01010101u * (uint32_t)(eq + 123);
+                __syncwarp();
+                // row is the box's first
+                if (go && !p.skip_loads) {
+                    const int at = slot * S::SLOT + lane * 16 * 128;
+                    if (value) {
+                        tma_rows(base + S::oRing + at, &p.vmap, 0, row, &full[slot]);
+                    } else {
+                        tma_rows(base + S::oK + at, &p.kmap, 0, row, &full[slot]);
+                        bulk_g2s(base + S::oExp + slot * 1024 + 512 + lane * 64, p.c.kexp + (size_t)row * S::EB,
+                                 (uint32_t)p.box_rows * S::EB, &full[slot]);
+                        bulk_g2s(base + S::oVex + tile % kRing * 512 + lane * 64, p.c.vexp + (size_t)row * S::EB,
+                                 (uint32_t)p.box_rows * S::EB, &full[slot]);
+                    }
                 }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.q_full[par]);
-            pos += g.kv1 - g.kv0;
+            pos += tiles;
             if (pos < w1) next_segment<S>(p, g, pos, w1);
         }
+        // every copy must have landed before the block's memory goes away (bounded)
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!p.skip_loads)
+            for (int i = max(0, tile - S::NSLOT); i < tile; ++i)
+                (void)mbar_wait_bounded(&full[i % S::NSLOT], (uint32_t)((i / S::NSLOT) & 1), ok ? p.timeout_ns : 100000000ull);
     } else if (warp == kFewS) {
         // ------------------------------------------------------------ S^T = K Q^T
         const bool one = elect_one();
@@ -204,6 +300,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 const uint32_t sfa = tmem + S::CB + 4 * (tile & 1), d = tmem + S::CS + buf * S::NQ;
                 const uint64_t ad = desc_codes<128>(smem_u32(base + S::oK) + slot * S::SLOT);
                 const uint64_t bd = desc_codes<128>(smem_u32(base + S::oQ) + par * S::QBUF);
+                {   // the exponents as tensor memory wants them: 32 rows (lanes) of four words (columns), column
+                    // c of row l being key 32 c + l's
+                    uint32_t *const sc = reinterpret_cast<uint32_t *>(base + S::oExp + slot * 1024);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(sc + 128 + 4 * lane);  // keys 4 lane .. + 3
+                    uint32_t *const d4 = sc + (4 * lane & 31) * 4 + (lane >> 3);
+                    d4[0] = w.x, d4[4] = w.y, d4[8] = w.z, d4[12] = w.w;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
                 if (one) {
                     copy_scales(sfa, desc_scales(smem_u32(base + S::oExp) + slot * 1024));
 #pragma unroll
@@ -230,23 +335,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
             ok = seg < 2 || wait(&s.o_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
             for (int i = 0; i < tiles && ok; ++i, ++tile) {
                 const int slot = tile % S::NSLOT, buf = tile & 1;
-                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1));
-                if (!ok) break;
-                const TileInfo inf = load_info(&s.info[tile % kInfo]);
-                if (inf.flags & 1) {
-                    const int keys = g.ctx + g.nodes - (g.kv0 + i) * TN;
-                    uint8_t *const v = base + S::oRing + slot * S::SLOT;
-                    for (int key = lane; key < TN; key += 32) {
-                        const bool gone = key >= keys || !((inf.valid >> (key >> 4)) & 1);
-                        const uint32_t bad = gone ? 15u : inf.flags & 2 ? s.nanblk[tile % kInfo][key] : 0u;
-                        for (int u = 0; u < 8; ++u)
-                            if ((bad >> (u >> 1)) & 1u)
-                                *reinterpret_cast<uint4 *>(v + key * 128 + ((u ^ (key & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                ok = wait(&s.p_full[buf], (uint32_t)((tile >> 1) & 1));
+                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait(&s.p_full[buf], (uint32_t)((tile >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint32_t d = tmem + S::CO + par * S::NP;
@@ -282,7 +371,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
         for (int pos = w0; pos < w1 && ok; ++seg) {
             const int tiles = g.kv1 - g.kv0, par = seg & 1, rows = g.nodes * p.g;
             float l[ROWS], off[ROWS], last[ROWS];  // sums, in 2^(m - bias); bias - m now, and at the set's last tile
-            int epoch = 0;
+            int epoch = 0, E = 0;
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
                 l[r] = 0.0f;
@@ -290,22 +379,23 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
             }
             for (int i = 0; i < tiles; ++i, ++it) {
                 if ((it & 1) != set) continue;
-                const int info = it % kInfo, buf = it % S::NS;
+                const int buf = it % S::NS;
                 ok = wait(&s.s_full[buf], (uint32_t)((it / S::NS) & 1));
                 if (!ok) break;
                 fence_after();
                 uint32_t x[ROWS], xl[ROWS];
                 ld_cols(tl + S::CS + buf * S::NQ, x);
                 ld_cols(tl + S::CS + buf * S::NQ + ROWS, xl);
-                const TileInfo inf = load_info(&s.info[info]);
-                const uint32_t ex = *reinterpret_cast<const uint32_t *>(base + S::oExp + (it % S::NSLOT) * 1024 + 512 + 4 * key);
+                const uint32_t valid = (uint32_t)s.valid[it % kRing];  // read before S is given back
+                uint32_t ex = *reinterpret_cast<const uint32_t *>(base + S::oVex + it % kRing * 512 + 4 * key);
                 const int slot = (g.kv0 + i) * TN + key;  // the thread's cache slot
                 // the references of the tile before, from the other set (at a segment's start too its tile is
                 // waited for: it has then read the references that this set is about to replace)
-                int now = 0;
+                int now = 0, before = 0;
                 if (it > 0) ok = wait(&s.m_full[set ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
                 if (i > 0) {
                     now = s.epoch[(it - 1) & 1];
+                    before = s.ev[(it - 1) & 1];
 #pragma unroll
                     for (int r = 0; r < ROWS; r += 4) {
                         const float4 v = *reinterpret_cast<const float4 *>(&s.off[(it - 1) & 1][r]);
@@ -321,10 +411,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) sv[r] = __uint_as_float(x[r]) + __uint_as_float(xl[r]);
                 uint32_t vis = 0xFFFFFFFFu;  // rows that see the key
-                if ((g.kv0 + i + 1) * TN > g.ctx || inf.valid != 0xFF) {
+                uint32_t bad = 0;            // channel blocks (a byte each) whose values count as zeros
+                if ((g.kv0 + i + 1) * TN > g.ctx || valid != 0xFFu) {
                     const int j = slot - g.ctx;
-                    if (!((inf.valid >> (key >> 4)) & 1) || j >= g.nodes) vis = 0;
-                    else if (j >= 0) {
+                    if (!((valid >> (key >> 4)) & 1u) || j >= g.nodes) {
+                        vis = ex = 0;
+                        bad = 0xFFFFFFFFu;
+                    } else if (j >= 0) {
                         vis = 0;
                         for (int t = 0; t < g.nodes; ++t) {
                             const bool sees = p.mask ? (p.mask[((size_t)g.b * p.T + t) * p.W + (j >> 5)] >> (j & 31)) & 1 : j <= t;
@@ -339,12 +432,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) up |= fmaf(sv[r], c, off[r]) > kFewBias + kSlack;
                 const bool any = __any_sync(0xFFFFFFFFu, up);
+                // the largest value exponent, NaN (255) left out
+                const uint32_t nans = __vcmpeq4(ex, 0xFFFFFFFFu);
+                ex &= ~nans;
+                bad |= nans;
+                uint32_t mx = __vmaxu4(ex, ex >> 16);
+                mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu));
                 int *const votes = s.grow[set][(it >> 1) & 1];
-                if (lane == 0) votes[quad] = any;
+                if (lane == 0) votes[quad] = (int)mx | (any ? 256 : 0);
                 ok = set_sync();
                 if (!ok) break;
                 const int4 v4 = *reinterpret_cast<const int4 *>(votes);
-                const bool grow = v4.x | v4.y | v4.z | v4.w;
+                const bool grow = (v4.x | v4.y | v4.z | v4.w) & 256;
+                E = max(max(before, max(v4.x & 255, v4.y & 255)), max(v4.z & 255, v4.w & 255));
+                const int rise = E - before;
                 float f[ROWS];
                 if (grow) {
 #pragma unroll
@@ -370,6 +471,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                         for (int r = 0; r < ROWS; r += 4)
                             *reinterpret_cast<float4 *>(&s.off[it & 1][r]) = make_float4(off[r], off[r + 1], off[r + 2], off[r + 3]);
                         s.epoch[it & 1] = now;
+                        s.ev[it & 1] = E;
                         mbar_arrive(&s.m_full[set]);
                     }
                     __syncwarp();
@@ -391,11 +493,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                     p2[r / 2] = pack_f16(a, b);
                 }
                 // ---- O in the units of the new references and value exponent
-                if (i > 0 && (grow || inf.rise)) {
+                if (i > 0 && (grow || rise)) {
                     ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
                     if (!ok) break;
                     fence_after();
-                    const float fv = pow2i(max(-inf.rise, -149));
+                    const float fv = pow2i(max(-rise, -149));
 #pragma unroll 1
                     for (int k = 0; k < 3; ++k) {
                         const uint32_t at = tl + S::CO + par * S::NP + (4 * k + quad) * ROWS;
@@ -423,7 +525,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                     for (int j = 0; j < 4; ++j) {  // four rows of a block a word
                         const int blk = ROWS == 8 ? 2 * u + (j >> 1) : u, r = ROWS == 8 ? 4 * (j & 1) : 4 * j;
                         const int e = (int)((ex >> (8 * blk)) & 0xFFu);
-                        const uint32_t sc = e == 255 ? 0u : f16_pow2(min(e - inf.ev, 0));
+                        const uint32_t sc = f16_pow2(e - E);
                         uint32_t a[3], b[3];
                         split3(p2[r / 2], sc, a[0], a[1], a[2]);
                         split3(p2[r / 2 + 1], sc, b[0], b[1], b[2]);
@@ -437,12 +539,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                             make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                     }
                 }
-                if (inf.flags & 2) {
-                    const uint32_t bad = s.nanblk[info][key];
+                if (__any_sync(0xFFFFFFFFu, bad)) {
+                    ok = wait(&s.c_full[it % S::NSLOT], (uint32_t)((it / S::NSLOT) & 1));
+                    if (!ok) break;
+                    uint8_t *const v = base + S::oRing + (it % S::NSLOT) * S::SLOT + key * 128;
+                    for (int u = 0; u < 8; ++u)
+                        if ((bad >> (4 * (u & 6))) & 255u)
+                            *reinterpret_cast<uint4 *>(v + ((u ^ (key & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                     for (int r = 0; r < ROWS && r < rows; ++r)
                         if ((vis >> r) & 1u)
                             for (int k = 0; k < 4; ++k)
-                                if ((bad >> k) & 1u) s.nan[par][k][r] = 1;
+                                if ((nans >> (8 * k)) & 255u) s.nan[par][k][r] = 1;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -472,7 +579,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 fence_after();
                 const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
                 const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
-                const float fv = pow2i(s.info[(it - 1) % kInfo].ev - 127);
+                const float fv = pow2i(E - 127);
                 // lane r: row r's sum, in units of the last reference
                 const int rl = lane % ROWS;
                 const float end = s.soff[par][set][rl];
