@@ -17,8 +17,8 @@
 // while HBM moves 33.
 //
 // Warps: a producer of keys (codes, both kinds of exponents), one of values (codes, and a segment's Q,
-// which so comes tiles ahead); one for each product; two sets of four for the softmax, alternating
-// tiles, thread = key.  The rows' reference m (p = 2^(x - m + 6)) and the value exponent E are common
+// which so comes tiles ahead); one for each product; sets of four for the softmax, each every
+// third tile, thread = key.  The rows' reference m (p = 2^(x - m + 6)) and the value exponent E are common
 // to a tile's keys: a set takes those of the tile before from the other set, its warps exchange their
 // largest exponents and whether any x passes its m by more than 2, and only then (a segment's first
 // tiles, as a rule) is a new maximum formed and O rescaled.  Sums stay with the thread, in fp32, to
@@ -32,7 +32,7 @@ namespace bsf8 {
 
 namespace {
 
-constexpr int kFewWarps = 12, kFewK = 8, kFewV = 9, kFewS = 10, kFewO = 11;
+constexpr int kFewK = 0, kFewV = 1, kFewS = 2, kFewO = 3;  // then the sets
 // Tiles whose value exponents and flags are kept: the keys' producer fills an entry again eight tiles
 // later, once the S of the tile four later is done, which takes the place of this tile's or a later one's
 // S, thus after the softmax has read that.
@@ -42,7 +42,7 @@ constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing
 
 template <int ROWS>
 struct FewShape {
-    static constexpr int DIM = 128, RT = ROWS, THREADS = kFewWarps * 32, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
+    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
     static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
     static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
@@ -50,7 +50,7 @@ struct FewShape {
     // tensor memory columns: two O, S, scales of two tiles' keys and of two segments' rows
     static constexpr int CO = 0, CS = 2 * NP, CB = CS + NS * NQ, CA = CB + 8;
     static_assert(CA + 8 <= 512);
-    static constexpr int oK = 0, oRing = NSLOT * SLOT, oP = 2 * NSLOT * SLOT, oQ = oP + 2 * PBUF;
+    static constexpr int oK = 0, oRing = NSLOT * SLOT, oP = 2 * NSLOT * SLOT, oQ = oP + SETS * PBUF;
     static constexpr int QBUF = 4096, oQs = oQ + 2 * QBUF;
     // a slot's key exponents, as tensor memory wants them and as they come; the values' as they come
     static constexpr int oExp = oQs + 2 * 512, oVex = oExp + NSLOT * 1024, oPrefix = oVex + kRing * 512;
@@ -61,18 +61,21 @@ struct FewShared : BlockShared {
     uint64_t k_full[4], k_free[4];    // ring slots of keys: codes and exponents landed; multiplied
     uint64_t c_full[4], c_free[4];    // of values
     uint64_t s_full[4], s_free[4];    // S written; read
-    uint64_t p_full[2];               // P written, O rescaled
-    uint64_t pv_done[2];              // O updated, P and the values read
-    uint64_t m_full[2];               // a set's tile has its references
-    uint64_t vote[2];                 // a set's warps
+    uint64_t p_full[3];               // a set's P written, O rescaled
+    uint64_t pv_done[3];              // O updated, P and the values read
+    uint64_t m_full[3];               // a set's tile has its references
+    uint64_t vote[3];                 // a set's warps
     uint64_t q_full[2], q_free[2];    // a segment's Q written; multiplied
-    uint64_t l_full[2], o_free[2];    // a segment's sums written; output read
+    uint64_t l_full[2], o_full[2];    // a segment's sums written; its last product done
+    uint64_t o_free[2];               // its output read
     alignas(16) float off[2][ROWS];   // bias - m, by the parity of the tile
-    alignas(16) int grow[2][2][4];    // votes
+    alignas(16) int grow[3][2][4];    // votes
     int epoch[2], ev[2];              // how often the references have changed in the segment; E
-    float most[2][4][ROWS];           // a warp's largest S
-    float sum[2][8][ROWS], soff[2][2][ROWS];  // by the parity of the segment: sums, their bias - m
-    int nan[2][4][ROWS];              // rows that see a NaN of a channel block
+    float most[3][4][ROWS];           // a warp's largest S
+    float sum[2][12][ROWS], soff[2][3][ROWS];  // by the parity of the segment: sums, their bias - m
+    // Rows that see a NaN of a channel block, by segment: while a set writes out a segment, the others pass
+    // at most two more tiles, thus segments.
+    int nan[4][4][ROWS];
     int valid[kRing];                 // a tile's 16-key groups that exist (bit i)
     int pages[2][2][32];              // the producers' block table entries: of a batch, of the next
 };
@@ -80,17 +83,16 @@ struct FewShared : BlockShared {
 // A batch of tiles' boxes (box_rows keys, inside a page and a tile), one a lane: 32 / boxes tiles.
 // The table's entries come by cp.async, a batch ahead.
 struct Batch {
-    int *ring;     // [2][32]
-    int gpb, nb;   // 16-key groups a box, boxes a tile
+    int *ring;   // [2][32]
+    int first;   // the lane's first 16-key group in the batch
     int phase;
 
     // exact: group * (magic * d - 2^32) < 2^32 for groups below 2^26 and d <= 64
     static __device__ __forceinline__ int in_page(const AttendParams &p, int grp) {
         return (int)(((unsigned long long)(unsigned)grp * p.page_magic) >> 32);
     }
-    __device__ __forceinline__ int group(int tile, int lane) const { return (tile + lane / nb) * 8 + lane % nb * gpb; }
     __device__ __forceinline__ void ask(const AttendParams &p, const Segment &g, int tile, int lane) {
-        const int grp = group(tile, lane);
+        const int grp = 8 * tile + first;
         int *const at = ring + 32 * phase + lane;
         if (16 * grp < g.ctx + g.nodes)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at)),
@@ -101,7 +103,7 @@ struct Batch {
     // The cache rows (head h) of the batch asked for last, -1 where there are none.
     __device__ __forceinline__ int rows(const AttendParams &p, const Segment &g, int tile, int lane) {
         asm volatile("cp.async.wait_all;" ::: "memory");
-        const int grp = group(tile, lane), page = ring[32 * (phase ^ 1) + lane];
+        const int grp = 8 * tile + first, page = ring[32 * (phase ^ 1) + lane];
         if (16 * grp >= g.ctx + g.nodes) return -1;
         if ((unsigned)page >= (unsigned)p.c.pages) {
             report_index(p.status);
@@ -174,9 +176,9 @@ __device__ __forceinline__ void split3(uint32_t p2, uint32_t sc, uint32_t &h, ui
 }  // namespace
 
 template <int ROWS>
-__global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(const __grid_constant__ AttendParams p) {
     using S = FewShape<ROWS>;
-    constexpr int TN = S::TN;
+    constexpr int TN = S::TN, SETS = S::SETS;
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
     __shared__ FewShared<ROWS> s;
@@ -193,18 +195,21 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
             mbar_init(&s.s_free[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.q_full[i], 1);
+            mbar_init(&s.q_free[i], 1);
+            mbar_init(&s.l_full[i], 4 * SETS);
+            mbar_init(&s.o_full[i], 1);
+            mbar_init(&s.o_free[i], 4);
+        }
+        for (int i = 0; i < SETS; ++i) {
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
             mbar_init(&s.m_full[i], 1);
             mbar_init(&s.vote[i], 4);
-            mbar_init(&s.q_full[i], 1);
-            mbar_init(&s.q_free[i], 1);
-            mbar_init(&s.l_full[i], 8);
-            mbar_init(&s.o_free[i], 4);
         }
         fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < 8 * ROWS; i += S::THREADS) (&s.nan[0][0][0])[i] = 0;
+    for (int i = threadIdx.x; i < 16 * ROWS; i += S::THREADS) (&s.nan[0][0][0])[i] = 0;
     hold_tmem(s, warp == kFewS);
     pdl_trigger();
     pdl_wait();
@@ -220,9 +225,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
         // ------------------------------------------------------------ producers
         const bool value = warp == kFewV;
         uint64_t *const full = value ? s.c_full : s.k_full, *const free = value ? s.c_free : s.k_free;
-        Batch batch{&s.pages[value][0][0], p.box_rows / 16, TN / p.box_rows, 0};
-        const int bt = 32 / batch.nb;
-        const uint32_t box_bytes = (uint32_t)p.box_rows * (value ? 128u : 128u + 2 * S::EB);
+        const int nb = TN / p.box_rows, bt = 32 / nb, gpb = p.box_rows / 16;  // boxes a tile, tiles a batch, groups a box
+        Batch batch{&s.pages[value][0][0], lane * gpb, 0};
+        const uint32_t some = low_bits(nb), box_bytes = (uint32_t)p.box_rows * (value ? 128u : 128u + 2 * S::EB);
+        const int ex_bytes = p.box_rows * S::EB, at = lane * p.box_rows * 128, ex_at = lane * ex_bytes;  // of lane's box
         int tile = 0, seg = 0;
         Segment g = first;
         for (int pos = w0; pos < w1 && ok; ++seg) {
@@ -235,40 +241,42 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.q_full[par]);
             }
-            int rows = -1;
+            int rows = -1, j = 0;
+            uint32_t have = 0;  // the batch's boxes that exist
             for (int i = 0; i < tiles; ++i, ++tile) {
-                const int j = i & (bt - 1);
                 if (j == 0) {
                     rows = batch.rows(p, g, g.kv0 + i, lane);
+                    have = __ballot_sync(0xFFFFFFFFu, rows >= 0);
                     if (i + bt < tiles) batch.ask(p, g, g.kv0 + i + bt, lane);
                 }
                 const int slot = tile % S::NSLOT;
                 ok = tile < S::NSLOT || wait(&free[slot], (uint32_t)((tile / S::NSLOT) & 1) ^ 1u);
                 if (!ok) break;
-                const int row = __shfl_sync(0xFFFFFFFFu, rows, (j * batch.nb + lane / batch.gpb) & 31);  // of group lane
-                const bool there = lane < 8 && row >= 0;
-                const bool go = there && lane % batch.gpb == 0;
-                const uint32_t groups =
-                    __ballot_sync(0xFFFFFFFFu, there && 16 * ((g.kv0 + i) * 8 + lane) < g.ctx + g.nodes);
-                const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, go));
+                const int row = __shfl_sync(0xFFFFFFFFu, rows, (j * nb + lane) & 31);  // the box's first
+                const uint32_t boxes = (have >> (j * nb)) & some;
                 if (lane == 0) {
-                    if (!value) s.valid[tile % kRing] = (int)groups;
-                    mbar_arrive_expect_tx(&full[slot], boxes * box_bytes);
+                    if (!value) {
+                        uint32_t groups = low_bits((g.ctx + g.nodes - (g.kv0 + i) * TN + 15) >> 4) & 0xFFu;
+                        if (boxes != some)
+                            for (int k = 0; k < 8; ++k)
+                                if (!((boxes >> (k / gpb)) & 1u)) groups &= ~(1u << k);
+                        s.valid[tile % kRing] = (int)groups;
+                    }
+                    mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(boxes) * box_bytes);
                 }
                 __syncwarp();
-                // row is the box's first
-                if (go && !p.skip_loads) {
-                    const int at = slot * S::SLOT + lane * 16 * 128;
+                if (lane < nb && row >= 0 && !p.skip_loads) {
                     if (value) {
-                        tma_rows(base + S::oRing + at, &p.vmap, 0, row, &full[slot]);
+                        tma_rows(base + S::oRing + slot * S::SLOT + at, &p.vmap, 0, row, &full[slot]);
                     } else {
-                        tma_rows(base + S::oK + at, &p.kmap, 0, row, &full[slot]);
-                        bulk_g2s(base + S::oExp + slot * 1024 + 512 + lane * 64, p.c.kexp + (size_t)row * S::EB,
-                                 (uint32_t)p.box_rows * S::EB, &full[slot]);
-                        bulk_g2s(base + S::oVex + tile % kRing * 512 + lane * 64, p.c.vexp + (size_t)row * S::EB,
-                                 (uint32_t)p.box_rows * S::EB, &full[slot]);
+                        tma_rows(base + S::oK + slot * S::SLOT + at, &p.kmap, 0, row, &full[slot]);
+                        bulk_g2s(base + S::oExp + slot * 1024 + 512 + ex_at, p.c.kexp + (size_t)row * S::EB, (uint32_t)ex_bytes,
+                                 &full[slot]);
+                        bulk_g2s(base + S::oVex + tile % kRing * 512 + ex_at, p.c.vexp + (size_t)row * S::EB,
+                                 (uint32_t)ex_bytes, &full[slot]);
                     }
                 }
+                j = j + 1 == bt ? 0 : j + 1;
             }
             pos += tiles;
             if (pos < w1) next_segment<S>(p, g, pos, w1);
@@ -334,8 +342,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
             const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0), par = seg & 1;
             ok = seg < 2 || wait(&s.o_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
             for (int i = 0; i < tiles && ok; ++i, ++tile) {
-                const int slot = tile % S::NSLOT, buf = tile & 1;
-                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait(&s.p_full[buf], (uint32_t)((tile >> 1) & 1));
+                const int slot = tile % S::NSLOT, buf = tile % SETS;
+                ok = wait(&s.c_full[slot], (uint32_t)((tile / S::NSLOT) & 1)) && wait(&s.p_full[buf], (uint32_t)((tile / SETS) & 1));
                 if (!ok) break;
                 fence_after();
                 const uint32_t d = tmem + S::CO + par * S::NP;
@@ -347,16 +355,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                         umma_8(d, ad + ks * (4096 >> 4), bd + ks * (4096 >> 4), idesc_8(S::NP), i > 0 || ks > 0);
                     commit_a(&s.pv_done[buf]);
                     commit_a(&s.c_free[slot]);
+                    if (i + 1 == tiles) commit_a(&s.o_full[par]);
                 }
                 __syncwarp();
             }
             pos += tiles;
             if (pos < w1) next_segment<S>(p, g, pos, w1);
         }
-        if (tile > 0) (void)wait(&s.pv_done[(tile - 1) & 1], (uint32_t)(((tile - 1) >> 1) & 1));
+        if (tile > 0) (void)wait(&s.pv_done[(tile - 1) % SETS], (uint32_t)(((tile - 1) / SETS) & 1));
     } else {
         // ------------------------------------------------------------ softmax and output
-        const int set = warp >> 2, quad = warp & 3, key = 32 * quad + lane;  // key of a tile, channel of O^T
+        const int set = (warp >> 2) - 1, quad = warp & 3, key = 32 * quad + lane;  // key of a tile, channel of O^T
         const uint32_t tl = tmem + ((uint32_t)(32 * quad) << 16);
         const float c = p.scale_log2;
         uint32_t vote_ph = 0;
@@ -378,7 +387,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 off[r] = last[r] = kUnseen;
             }
             for (int i = 0; i < tiles; ++i, ++it) {
-                if ((it & 1) != set) continue;
+                if (it % SETS != set) continue;
                 const int buf = it % S::NS;
                 ok = wait(&s.s_full[buf], (uint32_t)((it / S::NS) & 1));
                 if (!ok) break;
@@ -389,10 +398,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 const uint32_t valid = (uint32_t)s.valid[it % kRing];  // read before S is given back
                 uint32_t ex = *reinterpret_cast<const uint32_t *>(base + S::oVex + it % kRing * 512 + 4 * key);
                 const int slot = (g.kv0 + i) * TN + key;  // the thread's cache slot
-                // the references of the tile before, from the other set (at a segment's start too its tile is
-                // waited for: it has then read the references that this set is about to replace)
+                // the references of the tile before, from its set (at a segment's start too its tile is
+                // waited for: it has then read the references that are about to be replaced)
                 int now = 0, before = 0;
-                if (it > 0) ok = wait(&s.m_full[set ^ 1], (uint32_t)(((it - 1) >> 1) & 1));
+                if (it > 0) ok = wait(&s.m_full[(it - 1) % SETS], (uint32_t)(((it - 1) / SETS) & 1));
                 if (i > 0) {
                     now = s.epoch[(it - 1) & 1];
                     before = s.ev[(it - 1) & 1];
@@ -438,7 +447,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 bad |= nans;
                 uint32_t mx = __vmaxu4(ex, ex >> 16);
                 mx = __reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu));
-                int *const votes = s.grow[set][(it >> 1) & 1];
+                int *const votes = s.grow[set][(it / SETS) & 1];
                 if (lane == 0) votes[quad] = (int)mx | (any ? 256 : 0);
                 ok = set_sync();
                 if (!ok) break;
@@ -492,9 +501,13 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                     l[r + 1] += b;
                     p2[r / 2] = pack_f16(a, b);
                 }
+                // P's place is free once the set's last product is done.  Only then may the product of the tile before
+                // be waited for: a phase's parity says which of two it is, not of three.
+                ok = it < SETS || wait(&s.pv_done[set], (uint32_t)((it / SETS) & 1) ^ 1u);
+                if (!ok) break;
                 // ---- O in the units of the new references and value exponent
                 if (i > 0 && (grow || rise)) {
-                    ok = wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                    ok = wait(&s.pv_done[(it - 1) % SETS], (uint32_t)(((it - 1) / SETS) & 1));
                     if (!ok) break;
                     fence_after();
                     const float fv = pow2i(max(-rise, -149));
@@ -512,10 +525,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                     wait_st();
                     fence_before();
                 }
-                // ---- P, once the product before the last has read its place
-                ok = it < 2 || wait(&s.pv_done[it & 1], (uint32_t)((it >> 1) & 1) ^ 1u);
-                if (!ok) break;
-                uint8_t *const pb = base + S::oP + (it & 1) * S::PBUF + key * 128;
+                // ---- P
+                uint8_t *const pb = base + S::oP + set * S::PBUF + key * 128;
                 // column 4 ROWS part + ROWS block + row of the key's 128-byte rows, swizzled
                 constexpr int U = ROWS == 8 ? 2 : 4;  // 16-byte units a part
 #pragma unroll
@@ -549,11 +560,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                     for (int r = 0; r < ROWS && r < rows; ++r)
                         if ((vis >> r) & 1u)
                             for (int k = 0; k < 4; ++k)
-                                if ((nans >> (8 * k)) & 255u) s.nan[par][k][r] = 1;
+                                if ((nans >> (8 * k)) & 255u) s.nan[seg & 3][k][r] = 1;
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[it & 1]);
+                if (lane == 0) mbar_arrive(&s.p_full[set]);
             }
             if (!ok) break;
             // ---- the segment's sums
@@ -565,16 +576,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
 #pragma unroll
                 for (int k = 16; k > 0; k >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, k);
                 if (lane == 0) {
-                    s.sum[par][warp][r] = a;
+                    s.sum[par][warp - 4][r] = a;
                     if (quad == 0) s.soff[par][set][r] = last[r];
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.l_full[par]);
-            if (((it - 1) & 1) == set) {
+            if ((it - 1) % SETS == set) {
                 // ---- the output, by the set of the last tile; thread = channel
-                ok = wait(&s.l_full[par], (uint32_t)((seg >> 1) & 1)) &&
-                     wait(&s.pv_done[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+                ok = wait(&s.l_full[par], (uint32_t)((seg >> 1) & 1)) && wait(&s.o_full[par], (uint32_t)((seg >> 1) & 1));
                 if (!ok) break;
                 fence_after();
                 const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
@@ -585,14 +595,14 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1) attend_few_kernel(const __g
                 const float end = s.soff[par][set][rl];
                 float L = 0.0f;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
+                for (int w = 0; w < 4 * SETS; ++w) {
                     const float q = s.soff[par][w >> 2][rl], a = s.sum[par][w][rl];
                     L += a == 0.0f ? 0.0f : a * (q == end ? 1.0f : ex2(end - q));
                 }
                 const float inv = L == 0.0f ? 0.0f : fv / L;
-                const bool bad = s.nan[par][quad][rl];
+                const bool bad = s.nan[seg & 3][quad][rl];
                 __syncwarp();
-                if (lane < ROWS) s.nan[par][quad][lane] = 0;
+                if (lane < ROWS) s.nan[seg & 3][quad][lane] = 0;
                 if (quad == 0 && lane < ROWS && lane < rows) {
                     const float Lt = L * (1.0f / 64.0f);  // bias 6
                     const float M = end == kUnseen ? -INFINITY : kFewBias - end;
