@@ -51,6 +51,7 @@ namespace {
 template <int D, int ROWS>
 struct Shape {
     static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
+    static constexpr int START = 2;                  // tiles' worth of time that a segment takes besides its own
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
@@ -115,9 +116,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const Segment first = segment_at<S>(p, prefix, w0, w1);
 
     if (warp == kProducerWarp) {
-        ok = produce<S>(p, s, base, first, w0, w1, warp, lane);
+        ok = produce<S>(p, s, base, first, w1, warp, lane);
     } else if (warp == kScoutWarp) {
-        ok = scout<S>(p, s, base, first, w0, w1, warp, lane);
+        ok = scout<S>(p, s, base, first, w1, warp, lane);
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA issue: a thread a product
         // One thread issues an MMA about every 100 cycles whatever its size (to N = 128); two with
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         int tile = 0;  // of the block so far
         uint32_t qph = 0;
         Segment g = first;
-        for (int pos = w0; pos < w1 && ok; qph ^= 1u) {
+        for (; live(g) && ok; qph ^= 1u) {
             const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0);
             if (!value) ok = wait(&s.q_full, qph);
             for (int i = 0; i < tiles && ok; ++i, ++tile) {
@@ -181,14 +182,13 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 }
                 __syncwarp();
             }
-            pos += tiles;
-            if (pos < w1) next_segment<S>(p, g, pos, w1);
+            next_segment<S>(p, g, w1);
         }
         // the last products must be done before tensor memory goes back (bounded)
         if (tile > 0)
             (void)wait(value ? &s.pv_done[(tile - 1) & 1] : &s.s_full[(tile - 1) & 1], (uint32_t)(((tile - 1) >> 1) & 1));
     } else if (warp >= kSoftWarps) {
-        ok = widen_values<S>(p, s, base, first, w0, w1, warp, lane);
+        ok = widen_values<S>(p, s, base, first, w1, warp, lane);
     } else {
         // ------------------------------------------------------------ softmax and output
         const int set = warp >> 2, quad = warp & 3;                // tiles of one parity; tensor memory lanes
@@ -283,13 +283,12 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         bool real = false;
         float m = 0.0f, l = 0.0f;          // the rows' maximum at the set's last tile; its sum in 2^(m - bias)
         uint32_t nanblk = 0;
-        for (int pos = w0; ok;) {
-            const bool more = pos < w1;
-            Segment next{};
+        while (ok) {
+            Segment next = g;
+            if (it > 0) next_segment<S>(p, next, w1);
+            const bool more = live(next);
             int eq = 0;
             if (more) {
-                next = g;
-                if (it > 0) next_segment<S>(p, next, pos, w1);
                 if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
                 if (!ok) break;
                 fence_after();
@@ -400,7 +399,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             t = real ? r / p.g : 0;
             hq = g.h * p.g + (real ? r - t * p.g : 0);
             const float c = p.scale_log2 * pow2i(eq);  // S -> x
-            pos += tiles;
 
             m = -INFINITY;
             l = 0.0f;
@@ -659,7 +657,7 @@ size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
 // Items of the largest call these arguments allow; they are counted in 31 bits.
 bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
     const int g = Hq / c.heads, rt = row_tile(T, g, c.dim), tn = c.dim == 256 ? 64 : 128;
-    return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn) < 2147483648.0;
+    return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn + 4) < 2147483648.0;
 }
 
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream) {

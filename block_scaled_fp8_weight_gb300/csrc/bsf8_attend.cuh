@@ -44,7 +44,7 @@ struct AttendParams {
     int B, T, Hq, g, W;  // g: query heads a cache head, W: mask words a row
     float *part;         // [blocks][2][RT][D] normalised outputs
     float2 *stat;        // [blocks][2][RT] (m, sum)
-    int *prefix;         // [B + 1] the requests' items, for the join
+    int *prefix;         // [B + 1] the requests' work, for the join
     uint32_t tries;      // suspensions of a wait
     unsigned long long timeout_ns;
     int skip_loads;
@@ -66,23 +66,30 @@ __device__ __forceinline__ bool lengths(const AttendParams &p, int b, int &ctx, 
     return false;
 }
 
+// A request's work, in tiles: a segment (a row tile of a head over all keys) counts its tiles of keys
+// and S::START for its start and end.
 template <class S>
-__device__ __forceinline__ int items_of(const AttendParams &p, int ctx, int nodes) {
+__device__ __forceinline__ int work_of(const AttendParams &p, int ctx, int nodes) {
     if (nodes == 0) return 0;
     const int nt = (ctx + nodes + S::TN - 1) / S::TN;
-    return p.c.heads * ((nodes * p.g + S::RT - 1) / S::RT) * nt;
+    return p.c.heads * ((nodes * p.g + S::RT - 1) / S::RT) * (nt + S::START);
 }
 
-// The work of block w: items [w total / W, (w + 1) total / W).
+// The share of block w: [w total / W, (w + 1) total / W).  The tiles whose places lie in it are the
+// block's; a segment's places are START empty ones, then its tiles'.
 __device__ __forceinline__ int range_start(long long total, int w) {
     return (int)(total * w / kAttendBlocks);
 }
 
 struct Segment {
     int b, h, rt, kv0, kv1, nt, ctx, nodes;
+    int next;  // the place after its last
 };
 
-// The segment at item pos of a block whose range ends at end.
+__device__ __forceinline__ bool live(const Segment &s) { return s.kv1 > s.kv0; }
+
+// The segment at place pos of a block whose share ends at end; not live if none of its tiles are the
+// block's (then none of a later segment's are).
 template <class S>
 __device__ __forceinline__ Segment segment_at(const AttendParams &p, const int *prefix, int pos, int end) {
     Segment s{};
@@ -98,29 +105,32 @@ __device__ __forceinline__ Segment segment_at(const AttendParams &p, const int *
     s.nt = (s.ctx + s.nodes + S::TN - 1) / S::TN;
     const int rts = (s.nodes * p.g + S::RT - 1) / S::RT;
     const int rem = pos - prefix[lo];
-    const int seg = rem / s.nt;
-    s.kv0 = rem - seg * s.nt;
-    s.kv1 = min(s.nt, s.kv0 + (end - pos));
+    const int seg = rem / (s.nt + S::START), in = rem - seg * (s.nt + S::START);
+    s.kv0 = max(0, in - S::START);
+    s.kv1 = min(s.nt, in + (end - pos) - S::START);
+    s.next = pos - in + s.nt + S::START;
     s.h = seg / rts;
     s.rt = seg - s.h * rts;
     return s;
 }
 
-// The segment after s, at item pos < end.
+// The segment after s.
 template <class S>
-__device__ __forceinline__ void next_segment(const AttendParams &p, Segment &s, int pos, int end) {
+__device__ __forceinline__ void next_segment(const AttendParams &p, Segment &s, int end) {
+    s.kv0 = s.kv1 = 0;
+    if (s.next + S::START >= end) return;
     if ((++s.rt) * S::RT >= s.nodes * p.g) {
         s.rt = 0;
         if (++s.h == p.c.heads) {
             s.h = 0;
             do {
                 (void)lengths(p, ++s.b, s.ctx, s.nodes);
-            } while (s.nodes == 0);  // ends: there are items left
+            } while (s.nodes == 0);  // ends: there is work left
             s.nt = (s.ctx + s.nodes + S::TN - 1) / S::TN;
         }
     }
-    s.kv0 = 0;
-    s.kv1 = min(s.nt, end - pos);
+    s.kv1 = min(s.nt, end - s.next - S::START);
+    s.next += s.nt + S::START;
 }
 
 // ------------------------------------------------------------------ tcgen05 wrappers
@@ -498,7 +508,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, uint32
     return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, tries));
 }
 
-// Prefix sums of the requests' items, by the whole block (ends with a barrier).
+// Prefix sums of the requests' work, by the whole block (ends with a barrier).
 template <class S>
 __device__ __forceinline__ void sum_items(const AttendParams &p, BlockShared &s, int *prefix, int warp, int lane) {
     const int per = (p.B + S::THREADS - 1) / S::THREADS;
@@ -508,7 +518,7 @@ __device__ __forceinline__ void sum_items(const AttendParams &p, BlockShared &s,
         for (int b = b0; b < b1; ++b) {
             int ctx, nodes;
             if (!lengths(p, b, ctx, nodes) && blockIdx.x == 0) report_index(p.status);
-            sum += items_of<S>(p, ctx, nodes);
+            sum += work_of<S>(p, ctx, nodes);
             prefix[b + 1] = sum;  // within the thread's requests; completed below
         }
         int up = sum;
@@ -556,8 +566,8 @@ struct Pages {
 
 // The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values as they are.
 template <class S>
-__device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w0,
-                                   int w1, int warp, int lane) {
+__device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
+                                   int warp, int lane) {
     constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
     (void)warp;
     (void)BT;
@@ -567,7 +577,7 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
     const bool lead = lane < NSB && lane % gpb == 0;
     int tile = 0;
     Segment g = first;
-    for (int pos = w0; pos < w1 && ok;) {
+    while (live(g) && ok) {
         const int tiles = g.kv1 - g.kv0;
         int page = Pages<S>::page_of(p, g, g.kv0, lane), rows = -1;
         for (int i = 0; i < tiles; ++i, ++tile) {
@@ -598,8 +608,7 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
                 bulk_g2s(base + S::oRing + slot * S::SLOT + lane * 16 * D, p.c.v8 + (size_t)row * D,
                          (uint32_t)(p.box_rows * D), &s.c_full[slot]);
         }
-        pos += tiles;
-        if (pos < w1) next_segment<S>(p, g, pos, w1);
+        next_segment<S>(p, g, w1);
     }
     // every copy must have landed before the block's memory goes away (bounded)
     if (!p.skip_loads)
@@ -614,8 +623,8 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
 
 // The scout warp: exponents and flags.
 template <class S>
-__device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w0,
-                                   int w1, int warp, int lane) {
+__device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
+                                   int warp, int lane) {
     constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
     (void)warp;
     (void)BT;
@@ -625,7 +634,7 @@ __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uin
     const int key0 = lane * KPL;
     int tile = 0;
     Segment g = first;
-    for (int pos = w0; pos < w1 && ok;) {
+    while (live(g) && ok) {
         const int tiles = g.kv1 - g.kv0;
         int E = 0;  // the largest value exponent of the segment so far
         int page = Pages<S>::page_of(p, g, g.kv0, lane), rows = -1;
@@ -716,16 +725,15 @@ __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uin
             }
             ++tile;
         }
-        pos += tiles;
-        if (pos < w1) next_segment<S>(p, g, pos, w1);
+        next_segment<S>(p, g, w1);
     }
     return ok;
 }
 
 // The dequant warps: values to f16.
 template <class S>
-__device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w0,
-                                   int w1, int warp, int lane) {
+__device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
+                                   int warp, int lane) {
     constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
     (void)warp;
     (void)BT;
@@ -740,7 +748,7 @@ __device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes 
     const int b2 = lane & 1, rj = (lane >> 1) & 3, rg = lane >> 3;  // block of the column, row of four, group
     int tile = 0;
     Segment g = first;
-    for (int pos = w0; pos < w1 && ok;) {
+    while (live(g) && ok) {
         const int tiles = g.kv1 - g.kv0;
         for (int i = 0; i < tiles; ++i, ++tile) {
             const int slot = tile % S::NSLOT, buf = tile & 1, info = tile % kInfo;
@@ -798,8 +806,7 @@ __device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes 
                 mbar_arrive(&s.c_free[slot]);
             }
         }
-        pos += tiles;
-        if (pos < w1) next_segment<S>(p, g, pos, w1);
+        next_segment<S>(p, g, w1);
     }
     return ok;
 }
@@ -833,7 +840,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
         const int h = hq / p.g, r = t * p.g + (hq - h * p.g), rt = r / RT, row = r - rt * RT;
         const int nt = (ctx + nodes + S::TN - 1) / S::TN;
         const long long total = p.prefix[p.B];
-        const int first = p.prefix[b] + (h * ((nodes * p.g + RT - 1) / RT) + rt) * nt, last = first + nt - 1;
+        const int first = p.prefix[b] + (h * ((nodes * p.g + RT - 1) / RT) + rt) * (nt + S::START) + S::START;
+        const int last = first + nt - 1;  // the places of its tiles
         auto block_of = [&](int item) {
             int w = (int)((long long)item * kAttendBlocks / total);
             while (range_start(total, w + 1) <= item) ++w;

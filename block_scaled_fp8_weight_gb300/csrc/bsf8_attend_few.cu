@@ -42,7 +42,7 @@ constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing
 
 template <int ROWS>
 struct FewShape {
-    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
+    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, START = 3, SLOT = TN * DIM, NSLOT = 4;
     static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
     static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
@@ -63,14 +63,16 @@ struct FewShared : BlockShared {
     uint64_t s_full[4], s_free[4];    // S written; read
     uint64_t p_full[3];               // a set's P written, O rescaled
     uint64_t pv_done[3];              // O updated, P and the values read
-    uint64_t m_full[3];               // a set's tile has its references
+    uint64_t m_full[4];               // a tile (of four) has its references
     uint64_t vote[3];                 // a set's warps
     uint64_t q_full[2], q_free[2];    // a segment's Q written; multiplied
     uint64_t l_full[2], o_full[2];    // a segment's sums written; its last product done
     uint64_t o_free[2];               // its output read
-    alignas(16) float off[2][ROWS];   // bias - m, by the parity of the tile
+    // The references: bias - m, by their number in the segment, and a tile's number and E.  Four of each: a
+    // set that has not yet read a tile's keeps the third tile after that, its own next, from its vote.
+    alignas(16) float off[4][ROWS];
+    int2 ref[4];
     alignas(16) int grow[3][2][4];    // votes
-    int epoch[2], ev[2];              // how often the references have changed in the segment; E
     float most[3][4][ROWS];           // a warp's largest S
     float sum[2][12][ROWS], soff[2][3][ROWS];  // by the parity of the segment: sums, their bias - m
     // Rows that see a NaN of a channel block, by segment: while a set writes out a segment, the others pass
@@ -193,6 +195,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
             mbar_init(&s.c_free[i], 1);
             mbar_init(&s.s_full[i], 1);
             mbar_init(&s.s_free[i], 4);
+            mbar_init(&s.m_full[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s.q_full[i], 1);
@@ -204,7 +207,6 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         for (int i = 0; i < SETS; ++i) {
             mbar_init(&s.p_full[i], 4);
             mbar_init(&s.pv_done[i], 1);
-            mbar_init(&s.m_full[i], 1);
             mbar_init(&s.vote[i], 4);
         }
         fence_mbar_init();
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         const int ex_bytes = p.box_rows * S::EB, at = lane * p.box_rows * 128, ex_at = lane * ex_bytes;  // of lane's box
         int tile = 0, seg = 0;
         Segment g = first;
-        for (int pos = w0; pos < w1 && ok; ++seg) {
+        for (; live(g) && ok; ++seg) {
             const int tiles = g.kv1 - g.kv0, par = seg & 1;
             batch.ask(p, g, g.kv0, lane);
             if (value) {
@@ -278,8 +280,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 }
                 j = j + 1 == bt ? 0 : j + 1;
             }
-            pos += tiles;
-            if (pos < w1) next_segment<S>(p, g, pos, w1);
+            next_segment<S>(p, g, w1);
         }
         // every copy must have landed before the block's memory goes away (bounded)
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         const bool one = elect_one();
         int tile = 0, seg = 0;
         Segment g = first;
-        for (int pos = w0; pos < w1 && ok; ++seg) {
+        for (; live(g) && ok; ++seg) {
             const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0), par = seg & 1;
             ok = wait(&s.q_full[par], (uint32_t)((seg >> 1) & 1));
             if (!ok) break;
@@ -328,8 +329,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 }
                 __syncwarp();
             }
-            pos += tiles;
-            if (pos < w1) next_segment<S>(p, g, pos, w1);
+            next_segment<S>(p, g, w1);
         }
         // the last products must be done before tensor memory goes back (bounded)
         if (tile > 0) (void)wait(&s.s_full[(tile - 1) % S::NS], (uint32_t)(((tile - 1) / S::NS) & 1));
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         const bool one = elect_one();
         int tile = 0, seg = 0;
         Segment g = first;
-        for (int pos = w0; pos < w1 && ok; ++seg) {
+        for (; live(g) && ok; ++seg) {
             const int tiles = __shfl_sync(0xFFFFFFFFu, g.kv1 - g.kv0, 0), par = seg & 1;
             ok = seg < 2 || wait(&s.o_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
             for (int i = 0; i < tiles && ok; ++i, ++tile) {
@@ -359,8 +359,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 }
                 __syncwarp();
             }
-            pos += tiles;
-            if (pos < w1) next_segment<S>(p, g, pos, w1);
+            next_segment<S>(p, g, w1);
         }
         if (tile > 0) (void)wait(&s.pv_done[(tile - 1) % SETS], (uint32_t)(((tile - 1) / SETS) & 1));
     } else {
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         };
         int it = 0, seg = 0;
         Segment g = first;
-        for (int pos = w0; pos < w1 && ok; ++seg) {
+        for (; live(g) && ok; ++seg) {
             const int tiles = g.kv1 - g.kv0, par = seg & 1, rows = g.nodes * p.g;
             float l[ROWS], off[ROWS], last[ROWS];  // sums, in 2^(m - bias); bias - m now, and at the set's last tile
             int epoch = 0, E = 0;
@@ -398,21 +397,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 const uint32_t valid = (uint32_t)s.valid[it % kRing];  // read before S is given back
                 uint32_t ex = *reinterpret_cast<const uint32_t *>(base + S::oVex + it % kRing * 512 + 4 * key);
                 const int slot = (g.kv0 + i) * TN + key;  // the thread's cache slot
-                // the references of the tile before, from its set (at a segment's start too its tile is
-                // waited for: it has then read the references that are about to be replaced)
-                int now = 0, before = 0;
-                if (it > 0) ok = wait(&s.m_full[(it - 1) % SETS], (uint32_t)(((it - 1) / SETS) & 1));
-                if (i > 0) {
-                    now = s.epoch[(it - 1) & 1];
-                    before = s.ev[(it - 1) & 1];
-#pragma unroll
-                    for (int r = 0; r < ROWS; r += 4) {
-                        const float4 v = *reinterpret_cast<const float4 *>(&s.off[(it - 1) & 1][r]);
-                        off[r] = v.x, off[r + 1] = v.y, off[r + 2] = v.z, off[r + 3] = v.w;
-                    }
-                }
                 wait_ld();
-                if (!ok) break;
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.s_free[buf]);
@@ -437,6 +422,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     for (int r = 0; r < ROWS; ++r)
                         if (!((vis >> r) & 1u)) sv[r] = -INFINITY;
                 }
+                // does any x pass the references that the set knows?
                 bool up = false;
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) up |= fmaf(sv[r], c, off[r]) > kFewBias + kSlack;
@@ -452,11 +438,28 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 ok = set_sync();
                 if (!ok) break;
                 const int4 v4 = *reinterpret_cast<const int4 *>(votes);
-                const bool grow = (v4.x | v4.y | v4.z | v4.w) & 256;
+                // the references of the tile before (at a segment's start too its tile is waited for: the last ones
+                // have then been read)
+                int now = 0, before = 0;
+                if (it > 0) ok = wait(&s.m_full[(it - 1) & 3], (uint32_t)(((it - 1) >> 2) & 1));
+                if (!ok) break;
+                if (i > 0) {
+                    const int2 v = s.ref[(it - 1) & 3];
+                    now = v.x;
+                    before = v.y;
+                }
                 E = max(max(before, max(v4.x & 255, v4.y & 255)), max(v4.z & 255, v4.w & 255));
                 const int rise = E - before;
+                bool grow = false;
                 float f[ROWS];
-                if (grow) {
+                if (((v4.x | v4.y | v4.z | v4.w) & 256) || now != epoch) {
+                    if (now != epoch) {
+#pragma unroll
+                        for (int r = 0; r < ROWS; r += 4) {
+                            const float4 v = *reinterpret_cast<const float4 *>(&s.off[now & 3][r]);
+                            off[r] = v.x, off[r + 1] = v.y, off[r + 2] = v.z, off[r + 3] = v.w;
+                        }
+                    }
 #pragma unroll
                     for (int r = 0; r < ROWS; ++r) {
                         const float w = warp_max(sv[r]);
@@ -470,18 +473,21 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                                                fmaxf(s.most[set][2][r], s.most[set][3][r]));
                         const float next = fmaf(mt, c, off[r]) > kFewBias + kSlack ? kFewBias - mt * c : off[r];
                         f[r] = next == off[r] ? 1.0f : ex2(next - off[r]);
+                        grow |= next != off[r];
                         off[r] = next;
                     }
-                    ++now;
+                    now += grow;
                 }
                 if (quad == 0) {
                     if (lane == 0) {
+                        if (grow) {
 #pragma unroll
-                        for (int r = 0; r < ROWS; r += 4)
-                            *reinterpret_cast<float4 *>(&s.off[it & 1][r]) = make_float4(off[r], off[r + 1], off[r + 2], off[r + 3]);
-                        s.epoch[it & 1] = now;
-                        s.ev[it & 1] = E;
-                        mbar_arrive(&s.m_full[set]);
+                            for (int r = 0; r < ROWS; r += 4)
+                                *reinterpret_cast<float4 *>(&s.off[now & 3][r]) =
+                                    make_float4(off[r], off[r + 1], off[r + 2], off[r + 3]);
+                        }
+                        s.ref[it & 3] = make_int2(now, E);
+                        mbar_arrive(&s.m_full[it & 3]);
                     }
                     __syncwarp();
                 }
@@ -640,8 +646,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     }
                 }
             }
-            pos += tiles;
-            if (pos < w1) next_segment<S>(p, g, pos, w1);
+            next_segment<S>(p, g, w1);
         }
     }
 
