@@ -51,7 +51,7 @@ namespace {
 template <int D, int ROWS>
 struct Shape {
     static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
-    static constexpr int START = 2;                  // tiles' worth of time that a segment takes besides its own
+    static constexpr int START = 5;                  // tiles' worth of time that a segment takes besides its own
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes

@@ -22,8 +22,8 @@ constexpr int kProducerWarp = kSoftWarps + kDeqWarps, kScoutWarp = kProducerWarp
 constexpr int kMmaWarp = kScoutWarp + 1;  // two: S, O
 constexpr int kThreadsA = (kMmaWarp + 2) * 32;
 constexpr int kInfo = 8;             // tiles whose exponents and flags are kept
-constexpr float kBias = 13.0f;       // p = 2^(x - m + kBias)
-constexpr float kSlack = 2.0f;       // m lags the maximum by at most this
+constexpr float kBias = 9.0f;        // p = 2^(x - m + kBias)
+constexpr float kSlack = 6.0f;       // m lags the maximum by at most this
 constexpr int kShift = 6;            // f16 values are code * 2^(e - E + kShift)
 
 }  // namespace

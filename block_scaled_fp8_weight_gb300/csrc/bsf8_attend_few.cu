@@ -37,12 +37,13 @@ constexpr int kFewK = 0, kFewV = 1, kFewS = 2, kFewO = 3;  // then the sets
 // later, once the S of the tile four later is done, which takes the place of this tile's or a later one's
 // S, thus after the softmax has read that.
 constexpr int kRing = 8;
-constexpr float kFewBias = 6.0f;      // p <= 2^8, in e4m3's range
+constexpr float kFewBias = 6.0f;      // p = 2^(x - m + kFewBias)
+constexpr float kFewSlack = 2.8f;     // m lags the maximum by at most this: p <= 2^8.8 < 448, e4m3's largest
 constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing: any x passes it
 
 template <int ROWS>
 struct FewShape {
-    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, START = 3, SLOT = TN * DIM, NSLOT = 4;
+    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, START = 4, SLOT = TN * DIM, NSLOT = 4;
     static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
     static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 // does any x pass the references that the set knows?
                 bool up = false;
 #pragma unroll
-                for (int r = 0; r < ROWS; ++r) up |= fmaf(sv[r], c, off[r]) > kFewBias + kSlack;
+                for (int r = 0; r < ROWS; ++r) up |= fmaf(sv[r], c, off[r]) > kFewBias + kFewSlack;
                 const bool any = __any_sync(0xFFFFFFFFu, up);
                 // the largest value exponent, NaN (255) left out
                 const uint32_t nans = __vcmpeq4(ex, 0xFFFFFFFFu);
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     for (int r = 0; r < ROWS; ++r) {
                         const float mt = fmaxf(fmaxf(s.most[set][0][r], s.most[set][1][r]),
                                                fmaxf(s.most[set][2][r], s.most[set][3][r]));
-                        const float next = fmaf(mt, c, off[r]) > kFewBias + kSlack ? kFewBias - mt * c : off[r];
+                        const float next = fmaf(mt, c, off[r]) > kFewBias + kFewSlack ? kFewBias - mt * c : off[r];
                         f[r] = next == off[r] ? 1.0f : ex2(next - off[r]);
                         grow |= next != off[r];
                         off[r] = next;
