@@ -74,6 +74,7 @@ struct AttendShared : AttendPipes {
     uint64_t q_full;                // a segment's Q is in place
     uint64_t soft, set[2];          // the softmax warps' own barriers (bounded, unlike bar.sync)
     float mrow[2][128];             // the rows' maxima, handed from set to set
+    uint32_t amax[kSoftWarps][32];  // of the halves of Q's rows
     float2 stat[kSoftWarps][32];
     uint32_t nan[kSoftWarps][32];
 };
@@ -212,30 +213,48 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
         // A segment's Q: each row scaled by a power of two 2^-eq so that its largest lies in
         // [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4 (its scale is 2^-4).  Exact
         // for bf16 values within 2^14 of the row's largest, else off by at most 2^-22 of that.  The
-        // sets take half of the channels each.
-        auto put_q = [&](const Segment &g) -> int {
+        // sets take half of the channels each: up to dim 128 from registers (asked for before the last
+        // tile of the segment before is waited for), else 32 channels at a time.
+        constexpr int HELD = D <= 128 ? D / 16 : 1;
+        auto q_row = [&](const Segment &g, bool &real) -> const uint4 * {
             const int r = g.rt * RT + row;
-            const bool real = r < g.nodes * p.g;
+            real = r < g.nodes * p.g;
             const int t = real ? r / p.g : 0, hq = g.h * p.g + (real ? r - t * p.g : 0);
-            const uint16_t *qr = p.q + ((size_t)g.b * p.T + t) * p.ldq + (size_t)hq * D;
-            uint32_t am = 0;
-            if (real)
-#pragma unroll 8
-                for (int c = 0; c < D; c += 8) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(qr + c);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            return reinterpret_cast<const uint4 *>(p.q + ((size_t)g.b * p.T + t) * p.ldq + (size_t)hq * D + set * (D / 2));
+        };
+        auto largest_of = [](uint32_t am, const uint4 &v) -> uint32_t {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
-                }
-            const int eq = max((int)(am >> 7) - 127 - 7, -100);
+            for (int j = 0; j < 4; ++j) am = max(am, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+            return am;
+        };
+        auto put_q = [&](const Segment &g, const uint4 (&held)[HELD], int &eq) -> bool {
+            bool real;
+            const uint4 *const qr = q_row(g, real);
+            uint32_t am = 0;
+            if constexpr (D <= 128) {
+#pragma unroll
+                for (int j = 0; j < HELD; ++j) am = largest_of(am, held[j]);
+            } else if (real) {
+#pragma unroll 8
+                for (int j = 0; j < D / 16; ++j) am = largest_of(am, qr[j]);
+            }
+            s.amax[warp][lane] = am;
+            if (!soft_sync()) return false;
+            am = max(am, s.amax[warp ^ 4][lane]);
+            eq = max((int)(am >> 7) - 127 - 7, -100);
             const float qs = pow2i(-eq);  // eq <= 121
-#pragma unroll 1
-            for (int c = set * (D / 2); c < (set + 1) * (D / 2); c += 32) {
+            constexpr int CHUNK = 32;
+#pragma unroll(D <= 128 ? D / 64 : 1)
+            for (int c0 = 0; c0 < D / 2; c0 += CHUNK) {
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (real) v = *reinterpret_cast<const uint4 *>(qr + c + 8 * j);
+                    if constexpr (D <= 128)
+                        v = held[c0 / 8 + j];
+                    else if (real)
+                        v = qr[c0 / 8 + j];
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                     uint32_t h2[4], l2[4];
 #pragma unroll
@@ -249,6 +268,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     lo[2 * j] = l2[0] | (l2[1] << 16);
                     lo[2 * j + 1] = l2[2] | (l2[3] << 16);
                 }
+                const int c = set * (D / 2) + c0;
                 if constexpr (S::QS) {
                     const int lr = 32 * quad + lane;  // rows of 128 channels, 128-byte swizzle
                     uint8_t *d = base + S::oQ + (c >> 7) * (128 * 128) + lr * 128;
@@ -269,7 +289,7 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.q_full);
-            return eq;
+            return true;
         };
         {   // Q's scales: byte 0 (2^0) for the upper part, byte 1 (2^-4) for the lower
             const uint32_t f[4] = {0x7B7Fu, 0x7B7Fu, 0x7B7Fu, 0x7B7Fu};
@@ -289,10 +309,19 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             const bool more = live(next);
             int eq = 0;
             if (more) {
+                uint4 held[HELD] = {};
+                if constexpr (D <= 128) {
+                    bool there;
+                    const uint4 *const qr = q_row(next, there);
+                    if (there)
+#pragma unroll
+                        for (int j = 0; j < HELD; ++j) held[j] = qr[j];
+                }
                 if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
                 if (!ok) break;
                 fence_after();
-                eq = put_q(next);
+                ok = put_q(next, held, eq);
+                if (!ok) break;
             }
             if (it > 0) {
                 // ---- the segment's output; the sets take half of the channels each
@@ -648,10 +677,10 @@ cudaError_t launch_attend_dim(const AttendParams &prm, cudaStream_t stream) {
 
 }  // namespace
 
-// Two partials a block, their statistics, and the prefix sums.
+// Two partials a block, their statistics, and the prefix sums; 16 bytes to start on a whole sector.
 size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
     const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(T, Hq / heads, dim);
-    return rows * dim * 4 + rows * 8 + round16(((size_t)B + 1) * 4);
+    return 16 + rows * dim * 4 + rows * 8 + round16(((size_t)B + 1) * 4);
 }
 
 // Items of the largest call these arguments allow; they are counted in 31 bits.
@@ -686,7 +715,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.W = (a.T + 31) / 32;
     const int rt = row_tile(a.T, prm.g, c.dim);
     const size_t rows = (size_t)kAttendBlocks * 2 * rt;
-    prm.part = static_cast<float *>(a.workspace);
+    prm.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(a.workspace) + 31) / 32 * 32);
     prm.stat = reinterpret_cast<float2 *>(prm.part + rows * c.dim);
     prm.prefix = reinterpret_cast<int *>(prm.stat + rows);
     const Options opt = options();

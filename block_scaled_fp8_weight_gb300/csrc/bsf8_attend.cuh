@@ -42,7 +42,7 @@ struct AttendParams {
     uint16_t *out;
     float *lse;
     int B, T, Hq, g, W;  // g: query heads a cache head, W: mask words a row
-    float *part;         // [blocks][2][RT][D] normalised outputs
+    float *part;         // [blocks][2][RT][D] normalised outputs (32-byte aligned)
     float2 *stat;        // [blocks][2][RT] (m, sum)
     int *prefix;         // [B + 1] the requests' work, for the join
     uint32_t tries;      // suspensions of a wait
@@ -400,20 +400,44 @@ __device__ __forceinline__ uint32_t pack_bf(float lo, float hi) {
     return r;
 }
 
+// 32 bytes, a whole sector, by a thread (32-byte aligned).
+__device__ __forceinline__ void st_global8(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // N channels (from k) of a row's output: bf16 where the segment is the whole row, else a partial.
 template <int RT, int D, int N>
 __device__ __forceinline__ void store_row(const AttendParams &p, const Segment &g, bool whole, int slotw, int row,
                                           int t, int hq, int k, const float (&y)[N]) {
     if (whole) {
         uint16_t *dst = p.out + (((size_t)g.b * p.T + t) * p.Hq + hq) * D + k;
+        if constexpr (N == 16) {
 #pragma unroll
-        for (int j = 0; j < N; j += 4)
-            *reinterpret_cast<uint2 *>(dst + j) = make_uint2(pack_bf(y[j], y[j + 1]), pack_bf(y[j + 2], y[j + 3]));
+            for (int j = 0; j < N; j += 8)
+                *reinterpret_cast<uint4 *>(dst + j) = make_uint4(pack_bf(y[j], y[j + 1]), pack_bf(y[j + 2], y[j + 3]),
+                                                                 pack_bf(y[j + 4], y[j + 5]), pack_bf(y[j + 6], y[j + 7]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j += 4)
+                *reinterpret_cast<uint2 *>(dst + j) = make_uint2(pack_bf(y[j], y[j + 1]), pack_bf(y[j + 2], y[j + 3]));
+        }
     } else {
         float *dst = p.part + ((size_t)slotw * RT + row) * D + k;
+        if constexpr (N == 16) {
 #pragma unroll
-        for (int j = 0; j < N; j += 4)
-            *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            for (int k = 0; k < 16; k += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(y[k + j]);
+                st_global8(dst + k, w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j += 4)
+                *reinterpret_cast<float4 *>(dst + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+        }
     }
 }
 
