@@ -83,6 +83,10 @@ struct FewShared : BlockShared {
     int pages[2][2][32];              // the producers' block table entries: of a batch, of the next
 };
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 // A batch of tiles' boxes (box_rows keys, inside a page and a tile), one a lane: 32 / boxes tiles.
 // The table's entries come by cp.async, a batch ahead.
 struct Batch {
@@ -101,11 +105,12 @@ struct Batch {
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at)),
                          "l"(p.c.table + (size_t)g.b * p.c.table_pages + in_page(p, grp))
                          : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");  // exponents asked for later are not waited for in rows()
         phase ^= 1;
     }
     // The cache rows (head h) of the batch asked for last, -1 where there are none.
     __device__ __forceinline__ int rows(const AttendParams &p, const Segment &g, int tile, int lane) {
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         const int grp = 8 * tile + first, page = ring[32 * (phase ^ 1) + lane];
         if (16 * grp >= g.ctx + g.nodes) return -1;
         if ((unsigned)page >= (unsigned)p.c.pages) {
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&s.k_full[i], 1);
+            mbar_init(&s.k_full[i], 33);  // the codes' byte count, the lanes' exponents
             mbar_init(&s.k_free[i], 1);
             mbar_init(&s.c_full[i], 1);
             mbar_init(&s.c_free[i], 1);
@@ -230,8 +235,10 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
         uint64_t *const full = value ? s.c_full : s.k_full, *const free = value ? s.c_free : s.k_free;
         const int nb = TN / p.box_rows, bt = 32 / nb, gpb = p.box_rows / 16;  // boxes a tile, tiles a batch, groups a box
         Batch batch{&s.pages[value][0][0], lane * gpb, 0};
-        const uint32_t some = low_bits(nb), box_bytes = (uint32_t)p.box_rows * (value ? 128u : 128u + 2 * S::EB);
-        const int ex_bytes = p.box_rows * S::EB, at = lane * p.box_rows * 128, ex_at = lane * ex_bytes;  // of lane's box
+        const uint32_t some = low_bits(nb), box_bytes = (uint32_t)p.box_rows * 128u;
+        const int at = lane * p.box_rows * 128;  // of the lane's box
+        // the exponents of keys 4 lane .. + 3: whose box, how far into it
+        const int ex_box = (lane >> 2) / gpb, ex_off = 4 * lane - ex_box * p.box_rows;
         int tile = 0, seg = 0;
         Segment g = first;
         for (; live(g) && ok; ++seg) {
@@ -268,16 +275,17 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(boxes) * box_bytes);
                 }
                 __syncwarp();
-                if (lane < nb && row >= 0 && !p.skip_loads) {
-                    if (value) {
-                        tma_rows(base + S::oRing + slot * S::SLOT + at, &p.vmap, 0, row, &full[slot]);
-                    } else {
-                        tma_rows(base + S::oK + slot * S::SLOT + at, &p.kmap, 0, row, &full[slot]);
-                        bulk_g2s(base + S::oExp + slot * 1024 + 512 + ex_at, p.c.kexp + (size_t)row * S::EB, (uint32_t)ex_bytes,
-                                 &full[slot]);
-                        bulk_g2s(base + S::oVex + tile % kRing * 512 + ex_at, p.c.vexp + (size_t)row * S::EB,
-                                 (uint32_t)ex_bytes, &full[slot]);
+                if (lane < nb && row >= 0 && !p.skip_loads)
+                    tma_rows(base + (value ? S::oRing : S::oK) + slot * S::SLOT + at, value ? &p.vmap : &p.kmap, 0, row,
+                             &full[slot]);
+                if (!value) {  // 16 bytes a lane and kind: one instruction a kind, whatever the pages
+                    const int ex_row = __shfl_sync(0xFFFFFFFFu, rows, (j * nb + ex_box) & 31);
+                    if (ex_row >= 0 && !p.skip_loads) {
+                        const size_t from = ((size_t)ex_row + ex_off) * S::EB;
+                        cp_async16(base + S::oExp + slot * 1024 + 512 + lane * 16, p.c.kexp + from);
+                        cp_async16(base + S::oVex + tile % kRing * 512 + lane * 16, p.c.vexp + from);
                     }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
                 }
                 j = j + 1 == bt ? 0 : j + 1;
             }
