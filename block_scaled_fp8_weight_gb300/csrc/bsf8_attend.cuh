@@ -855,6 +855,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const long long idx = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     if (idx >= (long long)p.B * p.T * p.Hq) return;
     const int hq = (int)(idx % p.Hq), t = (int)(idx / p.Hq % p.T), b = (int)(idx / p.Hq / p.T);
+    const long long total = p.prefix[p.B];  // asked for with the lengths, not after them
+    const int before = p.prefix[b];
     int ctx, nodes;
     (void)lengths(p, b, ctx, nodes);
     uint16_t *const dst = p.out + (size_t)idx * D + lane * PC;
@@ -863,8 +865,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (t < nodes) {
         const int h = hq / p.g, r = t * p.g + (hq - h * p.g), rt = r / RT, row = r - rt * RT;
         const int nt = (ctx + nodes + S::TN - 1) / S::TN;
-        const long long total = p.prefix[p.B];
-        const int first = p.prefix[b] + (h * ((nodes * p.g + RT - 1) / RT) + rt) * (nt + S::START) + S::START;
+        const int first = before + (h * ((nodes * p.g + RT - 1) / RT) + rt) * (nt + S::START) + S::START;
         const int last = first + nt - 1;  // the places of its tiles
         auto block_of = [&](int item) {
             int w = (int)((long long)item * kAttendBlocks / total);
