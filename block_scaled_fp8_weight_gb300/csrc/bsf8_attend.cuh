@@ -838,70 +838,133 @@ __device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes 
 }  // namespace
 
 // ------------------------------------------------------------------ the join
-// A warp per row: rows past the request's nodes become zeros, rows that one block finished are
-// left alone, the others are joined from their blocks' partials in block order:
+// Rows past the request's nodes become zeros, rows that one block finished are left alone, the others
+// are joined from their blocks' partials:
 //   out = sum w_i o_i / sum w_i,  w_i = 2^(m_i - max m) sum_i.
+// WPR warps a row: each takes every WPR-th partial, in order (a lane a partial's maximum and sum, then
+// all lanes the channels, a group of partials in flight), and the warps' results are added in order.
+// Bound by latency: three loads that depend on each other.  A row alone over 50 blocks: 20 us in a
+// warp with a partial after another.
 namespace {
+
 constexpr int kJoinWarps = 8;
+
+template <int PC>
+__device__ __forceinline__ void load_channels(const float *src, float (&o)[PC]) {
+    if constexpr (PC == 2) {
+        const float2 v = *reinterpret_cast<const float2 *>(src);
+        o[0] = v.x, o[1] = v.y;
+    } else {
+#pragma unroll
+        for (int j = 0; j < PC; j += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + j);
+            o[j] = v.x, o[j + 1] = v.y, o[j + 2] = v.z, o[j + 3] = v.w;
+        }
+    }
 }
 
-template <class S>
+}  // namespace
+
+template <class S, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttendParams p) {
     pdl_trigger();
     pdl_wait();
     constexpr int D = S::DIM, RT = S::RT;
-    constexpr int PC = D / 32;  // channels a lane
-    const int lane = threadIdx.x & 31;
-    const long long idx = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    constexpr int PC = D / 32, GROUP = PC == 8 ? 4 : 8;  // channels a lane, partials in flight
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = WPR == 1 ? 0 : warp;
+    const long long idx = WPR == 1 ? (long long)blockIdx.x * kJoinWarps + warp : blockIdx.x;
     if (idx >= (long long)p.B * p.T * p.Hq) return;
     const int hq = (int)(idx % p.Hq), t = (int)(idx / p.Hq % p.T), b = (int)(idx / p.Hq / p.T);
     const long long total = p.prefix[p.B];  // asked for with the lengths, not after them
     const int before = p.prefix[b];
     int ctx, nodes;
     (void)lengths(p, b, ctx, nodes);
-    uint16_t *const dst = p.out + (size_t)idx * D + lane * PC;
     float y[PC] = {};
-    float lse = -INFINITY;
+    float M = -INFINITY, sum = 0.0f;
     if (t < nodes) {
         const int h = hq / p.g, r = t * p.g + (hq - h * p.g), rt = r / RT, row = r - rt * RT;
         const int nt = (ctx + nodes + S::TN - 1) / S::TN;
         const int first = before + (h * ((nodes * p.g + RT - 1) / RT) + rt) * (nt + S::START) + S::START;
         const int last = first + nt - 1;  // the places of its tiles
-        auto block_of = [&](int item) {
-            int w = (int)((long long)item * kAttendBlocks / total);
-            while (range_start(total, w + 1) <= item) ++w;
+        // the block of a place: an estimate that is at most one off, then the exact one
+        const float per = (float)kAttendBlocks / (float)total;
+        auto block_of = [&](int place) {
+            int w = max(0, (int)((float)place * per) - 1);
+            while (range_start(total, w + 1) <= place) ++w;
             return w;
         };
-        const int wa = block_of(first), wz = block_of(last);
-        if (wa == wz) return;
-        float M = -INFINITY;
-        for (int w = wa + lane; w <= wz; w += 32) {
-            const int s = range_start(total, w);
-            if (range_start(total, w + 1) > s) M = fmaxf(M, p.stat[(size_t)(2 * w + (s > first ? 0 : 1)) * RT + row].x);
+        const int wa = block_of(first), n = block_of(last) - wa + 1;
+        if (n == 1) return;
+        for (int base = part; base < n; base += 32 * WPR) {
+            const int k = base + lane * WPR, w = wa + k;
+            int at = -1;
+            if (k < n) {
+                const int s = range_start(total, w);
+                if (range_start(total, w + 1) > s) at = (2 * w + (s > first ? 0 : 1)) * RT + row;
+            }
+            float2 st = make_float2(-INFINITY, 0.0f);
+            if (at >= 0) st = p.stat[at];
+            const int count = min(32, (n - base + WPR - 1) / WPR);
+            float f = 0.0f;
+            for (int j0 = 0; j0 < count; j0 += GROUP) {
+                float o[GROUP][PC];
+                bool in[GROUP];
+#pragma unroll
+                for (int j = 0; j < GROUP; ++j) {
+                    const int a = __shfl_sync(0xFFFFFFFFu, at, (j0 + j) & 31);
+                    in[j] = j0 + j < count && a >= 0;
+                    if (in[j]) load_channels<PC>(p.part + (size_t)a * D + lane * PC, o[j]);
+                }
+                if (j0 == 0) {  // with the first group on its way
+                    float m = st.x;
+#pragma unroll
+                    for (int q = 16; q > 0; q >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, q));
+                    m = fmaxf(m, M);
+                    const float g = M == -INFINITY ? 0.0f : ex2(M - m);
+                    M = m;
+                    sum *= g;
+#pragma unroll
+                    for (int c = 0; c < PC; ++c) y[c] *= g;
+                    f = st.y == 0.0f ? 0.0f : ex2(st.x == -INFINITY ? 0.0f : st.x - M) * st.y;
+                }
+#pragma unroll
+                for (int j = 0; j < GROUP; ++j) {
+                    const float g = __shfl_sync(0xFFFFFFFFu, f, (j0 + j) & 31);
+                    if (!in[j]) continue;
+                    sum += g;
+#pragma unroll
+                    for (int c = 0; c < PC; ++c) y[c] = fmaf(g, o[j][c], y[c]);
+                }
+            }
         }
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, k));
-        float sum = 0.0f;
-#pragma unroll 4
-        for (int w = wa; w <= wz; ++w) {
-            const int s = range_start(total, w);
-            if (range_start(total, w + 1) <= s) continue;
-            const size_t at = (size_t)(2 * w + (s > first ? 0 : 1)) * RT + row;
-            const float2 st = p.stat[at];
-            const float f = st.y == 0.0f ? 0.0f : ex2(st.x == -INFINITY ? 0.0f : st.x - M) * st.y;
-            const float *o = p.part + at * D + lane * PC;
-            sum += f;
-#pragma unroll
-            for (int j = 0; j < PC; ++j) y[j] = fmaf(f, o[j], y[j]);
-        }
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int j = 0; j < PC; ++j) y[j] *= inv;
-        if (sum != 0.0f) lse = (M + log2f(sum)) * 0.69314718055994531f;
     }
+    if constexpr (WPR > 1) {
+        __shared__ float s_m[WPR], s_sum[WPR], s_y[WPR][D];
 #pragma unroll
-    for (int j = 0; j < PC; j += 2) *reinterpret_cast<uint32_t *>(dst + j) = pack_bf(y[j], y[j + 1]);
-    if (p.lse && lane == 0) p.lse[idx] = lse;
+        for (int c = 0; c < PC; ++c) s_y[warp][lane * PC + c] = y[c];
+        if (lane == 0) {
+            s_m[warp] = M;
+            s_sum[warp] = sum;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        M = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) M = fmaxf(M, s_m[w]);
+#pragma unroll
+        for (int c = 0; c < PC; ++c) y[c] = 0.0f;
+        for (int w = 0; w < WPR; ++w) {
+            const float g = s_m[w] == -INFINITY ? (M == -INFINITY ? 1.0f : 0.0f) : ex2(s_m[w] - M);
+            sum = fmaf(g, s_sum[w], sum);
+#pragma unroll
+            for (int c = 0; c < PC; ++c) y[c] = fmaf(g, s_y[w][lane * PC + c], y[c]);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *const dst = p.out + (size_t)idx * D + lane * PC;
+#pragma unroll
+    for (int c = 0; c < PC; c += 2) *reinterpret_cast<uint32_t *>(dst + c) = pack_bf(y[c] * inv, y[c + 1] * inv);
+    if (p.lse && lane == 0) p.lse[idx] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
 }
 
 // Launches the join with the kernel's shape; the kernels' grids.
@@ -944,8 +1007,10 @@ cudaError_t launch_attend_shape(F *kernel, const AttendParams &prm, cudaStream_t
     }
     e = launch_attend_grid(kernel, kAttendBlocks, S::THREADS, attend_smem<S>(prm.B), stream, prm);
     if (e != cudaSuccess) return e;
+    // a block a row while all of them run at once, else a warp
     const long long rows = (long long)prm.B * prm.T * prm.Hq;
-    return launch_attend_grid(join_kernel<S>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, prm);
+    if (rows <= 152 * 8) return launch_attend_grid(join_kernel<S, kJoinWarps>, rows, kJoinWarps * 32, 0, stream, prm);
+    return launch_attend_grid(join_kernel<S, 1>, (rows + kJoinWarps - 1) / kJoinWarps, kJoinWarps * 32, 0, stream, prm);
 }
 
 }  // namespace bsf8
