@@ -80,7 +80,7 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&y)[8]) {
 // tokens' places and positions are looked up once, by a thread a token, while the first rows are on
 // their way; kAhead rows a lane group stay in flight.  (Looking them up in every lane group cost
 // more instructions than the norm, the rotation and the rounding together.)
-constexpr int kTokens = 16, kAhead = 2;
+constexpr int kTokens = 64, kAhead = 2;
 
 template <int D>
 __global__ void __launch_bounds__(256, 4) append_kernel(const CacheView c, const AppendArgs a, int tokens, int *status) {
@@ -215,8 +215,11 @@ template <int D>
 cudaError_t append_dim(const CacheView &c, const AppendArgs &a, cudaStream_t stream, int *status) {
     constexpr int G = 256 / (D / 8);
     const int chunks = (a.Hq + 2 * c.heads + G - 1) / G;
-    // tokens a block: one while that keeps every block resident (four an SM), up to 16 after that
-    const int tokens = (int)std::min<long long>(kTokens, ((long long)a.N * chunks + 152 * 4 - 1) / (152 * 4));
+    // tokens a block: the work in whole waves of resident blocks (four an SM), as few as kTokens allow
+    // (8191 tokens in three waves of 16: 50 us, in one of 41: 45 us; in a full one and a quarter: 64 us)
+    const long long resident = 152 * 4, work = (long long)a.N * chunks;
+    const long long waves = (work + resident * kTokens - 1) / (resident * kTokens);
+    const int tokens = (int)((work + resident * waves - 1) / (resident * waves));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((a.N + tokens - 1) / tokens), (unsigned)chunks, 1);
     cfg.blockDim = dim3(256, 1, 1);
