@@ -2,44 +2,56 @@
 //
 //   out[row] = sum_l 2^(x_l - m) v_l / sum_l 2^(x_l - m),   x_l = scale log2(e) q[row].k_l,
 // over the keys l that the row sees; a row is a (node, query head) of one request and cache
-// head.  One pass over the cache with the running maximum m and sum of a softmax.
+// head.  One pass over the cache with the running maximum m and sum of a softmax.  Up to 16 rows at
+// dim 128 run in bsf8_attend_few.cu, on the same cut of the work and the same join.
 //
 // Work.  An item is a tile of TN keys (128; 64 at dim 256) of one (request, head, tile of RT
-// rows).  The items of all requests, in that order, are cut into one equal contiguous range per
-// block (one block an SM), whatever the requests' lengths: every block computes the same prefix
-// sums of the requests' items.  A block's range is a run of segments (consecutive keys of one
-// row tile).  A segment that holds all keys of its rows writes the output; any other writes a
-// partial (its rows' normalised output, maximum and sum) to one of the block's two workspace
-// slots -- only a block's first and last segment can be incomplete -- and a second kernel
-// joins the partials of each row in block order.  Nothing depends on timing: the same call
-// gives the same bits.
+// rows), a segment all items of one (request, head, row tile).  The segments of all requests, in that
+// order, each as long as its items and START more for its start and end, are cut into one equal
+// contiguous share per block (one block an SM), whatever the requests' lengths: every block computes the
+// same prefix sums.  (Without the START places a block full of short requests held up the others: 64
+// requests of 70 to 16384 tokens took 250 us, with them 184; 16 trees of 23 nodes 80 us, then 50.)
+// A block that has a whole segment writes the output; else it writes a partial (its rows' normalised
+// output, maximum and sum) to one of its two workspace slots -- only a block's first and last segment
+// can be incomplete -- and a second kernel joins each row's partials in block order.  Nothing
+// depends on timing: the same call gives the same bits.
 //
 // A block's warps, each with its own loop over the items:
-//   producer  bulk copies of the codes (page runs of a head are contiguous) and cp.async of the
-//             exponents into a ring of slots, K(0) K(1) V(0) K(2) V(1) ...;
-//   8 dequant a slot's codes -> f16 tiles in shared memory (128-byte swizzle), as
-//             code * 2^(e - E + 6), E the largest exponent of the tile (keys), or of the segment
-//             so far (values): exact for exponents within 2^21 of E, else off by at most 2^-31
-//             of 2^E; e4m3 times a power of two needs no more than f16's 11 bits;
-//   MMA       one thread: S = Q K^T (Q in tensor memory as A, f16 scaled by a power of two a
-//             row; exact products, fp32 sums), then O += P V (P in tensor memory as A, V as an
-//             N-major B);  S(i + 1) is issued before O(i), so it runs under softmax(i);
-//   4 softmax thread = row: maximum, p = 2^(x - m + 13) (fp32, summed in fp32), rounded to f16
-//             for the second product: 11 bits of p at any p above 2^-27 of the largest, half of
-//             2^-37 of it below.  (bf16 would round p to 8 bits: 1.4 times the error of the
-//             output's own rounding.)  m only moves when the maximum has grown by more than
-//             2^2 over it, which keeps p <= 2^15 and rescaling O (a round trip of O through
-//             registers) rare.
+//   producer  the codes, into rings of slots: keys by TMA boxes (swizzled for the MMA), values by
+//             bulk copies (page runs of a head are contiguous);
+//   scout     exponents and flags: the keys' exponents laid out for tensor memory, the largest value
+//             exponent E of the segment so far, which groups of keys exist;
+//   8 dequant a tile's values -> f16 in shared memory (128-byte swizzle), as code * 2^(e - E + 6): exact for
+//             exponents within 2^21 of E, else off by at most 2^-31 of 2^E; e4m3 times a power of
+//             two needs no more than f16's 11 bits;
+//   S         S = Q K^T on the cached codes (block-scaled MMA): the exponents go along as its scales.  Q is the
+//             sum of two e4m3 parts (A, in tensor memory; at dim 256 in shared memory): 8 MMAs a tile;
+//   O         O += P V (P in tensor memory as A, V as an N-major B): 8 MMAs of 16 keys;
+//   8 softmax two sets of four, a set every other tile, thread = row: p = 2^(x - m + 9) (fp32, summed in
+//             fp32), rounded to f16 for the second product: 11 bits of p at any p above 2^-23 of 2^m,
+//             half of 2^-33 of it below.  (bf16 would round p to 8 bits: 1.4 times the error of the
+//             output's own rounding.)  m, handed from set to set, only moves when the maximum has
+//             grown by more than 2^6 over it: p stays below f16's largest, and rescaling O (a round
+//             trip through registers) becomes rare; with 2^2 it took 4 us of 50 at 4096 tokens.
 // RT rows of Q fill the MMA's 128 rows 128 / RT times; each copy handles its own part of the
 // tile's key columns (its P is zero elsewhere), so that with few rows all four softmax warps
-// still work; the copies' maxima, sums and outputs join at the segment's end.
+// still work; the copies' sums and outputs join at the segment's end.
 // Masks are 32-bit words a row and 32 keys; tiles wholly inside the context skip them.  Keys
 // past a request's end (a page's unused slots may hold anything) and keys on bad pages are
 // masked, and their values are zeroed; a value block that holds NaN is zeroed too, and the rows
 // that see it get their NaN at the end, so that it reaches no other row.
 //
-// Bound: the cache is read once, 2 dim (1 + 1/32) bytes a key and head, from HBM; the shared
-// memory of an SM (codes in, codes out, f16 in, the MMA's read of f16) is nearly as busy.
+// Bound.  The cache is read once a row tile, 2 dim (1 + 1/32) bytes a key and head: 1440 cycles of an SM's
+// share of HBM a tile of 128 keys at dim 128; the tensor cores need 1024 for it, the exponentials of
+// 128 rows 512, shared memory (codes in and out, f16 in and out, the MMAs' reads: 144 KB) 1150.  It
+// takes 2350: S of a tile waits for the product with the P two tiles before, whose place it takes
+// (tensor memory has no room for more: two S, O and Q fill 460 of 512 columns, another S does not
+// fit), so the latencies of softmax (2800 cycles) and of the products with their handoffs (1900) add
+// up over two tiles.  P in columns of its own with Q in shared memory ran 20 percent slower, each tile
+// halved between the sets 13 percent slower.
+// Measured: 6 row tiles x 131072 keys x 4 heads at dim 128: 213 us (0.97 PFLOP/s, 0.49 of the measured
+// bf16 rate); 84 to 161 rows, 16 requests of 8192 tokens at most, 4 heads: 47 us, of which a third is
+// segments' starts and ends.
 #include "bsf8_attend.cuh"
 
 #include <mutex>
@@ -51,7 +63,9 @@ namespace {
 template <int D, int ROWS>
 struct Shape {
     static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
-    static constexpr int START = 5;                  // tiles' worth of time that a segment takes besides its own
+    // tiles' worth of time that a segment takes besides its own (trees of 23 nodes over up to 8192 tokens:
+    // 58 us with 2, 53 with 3, 51 with 4 and 6)
+    static constexpr int START = 5;
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
@@ -624,8 +638,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
 
 namespace {
 
-// Rows a tile: the smallest that holds all of a request's rows of a head (more copies of a small
-// tile mean less softmax work a thread), 128 past that.
+// Rows a tile: the smallest that holds all of a request's rows of a head, 128 past that.  4 rows x 8
+// heads x 64 requests of up to 16384 tokens, dim 128: 184 us in the kernel for 8 rows (which
+// has no dims but 128), 244 in the one for 32; fewer rows a tile than needed would read the cache again.
 int row_tile(int T, int g, int dim) {
     const int rows = T * g;
     if (dim == 128 && rows <= 16) return rows <= 8 ? 8 : 16;

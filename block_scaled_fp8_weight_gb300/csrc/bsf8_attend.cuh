@@ -843,8 +843,8 @@ __device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes 
 //   out = sum w_i o_i / sum w_i,  w_i = 2^(m_i - max m) sum_i.
 // WPR warps a row: each takes every WPR-th partial, in order (a lane a partial's maximum and sum, then
 // all lanes the channels, a group of partials in flight), and the warps' results are added in order.
-// Bound by latency: three loads that depend on each other.  A row alone over 50 blocks: 20 us in a
-// warp with a partial after another.
+// Bound by latency: three loads that depend on each other.  A row over 50 blocks: 20 us in a warp with a
+// partial after another, 3 so.
 namespace {
 
 constexpr int kJoinWarps = 8;

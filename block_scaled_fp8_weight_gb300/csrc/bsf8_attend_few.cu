@@ -11,21 +11,29 @@
 //                 a key and 32 channels, so it goes into P: for each of the four channel blocks c a
 //                 copy p 2^(e(key, c) - E), E the segment's largest exponent so far.  Lane quarter c
 //                 of O^T is right in the columns of copy c only, and only those are read.  Each copy
-//                 is the sum of three e4m3 parts (12 bits of p where it is above 2^-14 of the largest,
-//                 half of 2^-25 of that below), in columns of their own: 12 columns a row.
+//                 is the sum of three e4m3 parts (12 bits of p = 2^(x - m) where it is above 2^-12, to
+//                 2^-24 below that), in columns of their own: 12 columns a row.
 // So nothing is widened, and an SM's shared memory moves about 90 KB a tile (144 KB in bsf8_attend.cu)
 // while HBM moves 33.
 //
 // Warps: a producer of keys (codes, both kinds of exponents), one of values (codes, and a segment's Q,
-// which so comes tiles ahead); one for each product; sets of four for the softmax, each every
-// third tile, thread = key.  The rows' reference m (p = 2^(x - m + 6)) and the value exponent E are common
-// to a tile's keys: a set takes those of the tile before from the other set, its warps exchange their
-// largest exponents and whether any x passes its m by more than 2, and only then (a segment's first
-// tiles, as a rule) is a new maximum formed and O rescaled.  Sums stay with the thread, in fp32, to
-// the segment's end.  O and Q are double-buffered by segment.
+// which so comes tiles ahead); one for each product; sets of four for the softmax, three up to 8 rows,
+// two past that, tile about, thread = key.  The rows' references m and the value exponent E are common
+// to a tile's keys.  A set's warps exchange their largest exponents and whether any x passes the m that
+// the set knows by more than 2.8; then the set takes the tile before's number of changes of m and E, and
+// only where that is new, or an x did pass (a segment's first tiles, as a rule), forms new maxima and
+// rescales O.  Sums stay with the thread, in fp32, to the segment's end.  O and Q are double-buffered
+// by segment.
 //
 // Keys that do not exist or hold a NaN block: p is 0 there, and the key's thread clears their value
 // codes first, as 0 times a NaN code is not 0.
+//
+// Bound: HBM at long contexts.  A tile of 128 keys takes an SM 1440 cycles at its share of the measured
+// HBM rate, which is what it takes here; three sets (of the softmax's 3600 cycles a tile, latencies
+// mostly) keep up with that, two did not (265 us below).  64 requests of 70 to 16384 tokens, 4 rows, 8
+// heads: 184 us, 0.89 of the measured HBM rate.  At short contexts latency bounds: one request of 1000
+// tokens, a tile a block, takes 13 us -- prefix sums 2, table, codes and Q 2.5, products and softmax 2,
+// output 1.5, the join 3, launches 2.
 #include "bsf8_attend.cuh"
 
 namespace bsf8 {
@@ -43,7 +51,12 @@ constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing
 
 template <int ROWS>
 struct FewShape {
-    static constexpr int DIM = 128, RT = ROWS, SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32, TN = 128, EB = 4, START = 4, SLOT = TN * DIM, NSLOT = 4;
+    static constexpr int DIM = 128, RT = ROWS, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
+    // three sets' registers do not suffice for 16 rows, nor does shared memory for their P
+    static constexpr int SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32;
+    // tiles' worth of time that a segment takes besides its own (64 requests of 70 to 16384 tokens: 218 us
+    // with 2, 197 with 3, 187 with 4 and 5, 189 with 6)
+    static constexpr int START = 4;
     static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
     static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
