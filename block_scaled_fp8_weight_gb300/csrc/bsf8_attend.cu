@@ -157,9 +157,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     fence_after();
                     const uint64_t bd = desc_a(smem_u32(base + S::oV) + buf * S::F16, TN * 128);
                     if (one) {
+                        // At dim 128 as two accumulators of 64 channels in turn: 205 us where one of 128 takes 212 (long
+                        // trees); at 64 and 256, and for S, no difference.
+                        constexpr int OW = D == 128 ? 64 : D;
 #pragma unroll
                         for (int ks = 0; ks < TN / 16; ++ks)  // 16 keys a step: two 8-key atoms
-                            umma_a(tmem + S::CO, sp + 8 * ks, bd + ks * (2048 >> 4), idesc_a(D, true), i > 0 || ks > 0);
+#pragma unroll
+                            for (int k = 0; k < D; k += OW)
+                                umma_a(tmem + S::CO + k, sp + 8 * ks, bd + ks * (2048 >> 4) + k / 64 * (TN * 128 >> 4),
+                                       idesc_a(OW, true), i > 0 || ks > 0);
                         commit_a(&s.pv_done[buf]);
                     }
                 } else {
