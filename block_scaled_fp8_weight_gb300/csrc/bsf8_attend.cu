@@ -99,7 +99,7 @@ template <int D, int RT>
 __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_constant__ AttendParams p) {
     using S = Shape<D, RT>;
     constexpr int TN = S::TN, REP = 128 / RT, CPT = TN / REP;  // CPT: key columns a thread
-    constexpr int CH = CPT <= 32 ? CPT : CPT == 64 ? 16 : 32;  // taken CH at a time
+    constexpr int CH = CPT <= 32 ? CPT : 16;  // taken CH at a time
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
     __shared__ AttendShared s;
@@ -575,26 +575,28 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                             if (q != copy) st_cols(tb + q * (CPT / 2), z);
                     }
                 } else {
-                    // Two passes: 64 registers of P on top of the rest would spill.
-#pragma unroll 1
-                    for (int k = 0; k < CPT; k += CH) {
-                        uint32_t y[CH];
-                        ld_cols(ts + k, y);
-                        wait_ld();
-                        largest(y, m0, m1);
-                    }
+                    // Two passes: 64 registers of P on top of the rest would spill.  Both unrolled, 16 columns on their
+                    // way while the 16 before are worked on (193 us long trees; 32 at a time in a loop: 205).
                     ok = receive();
                     if (!ok) break;
+                    uint32_t x[2][CH], pk[CH / 2];
+                    ld_cols(ts, x[0]);
+#pragma unroll
+                    for (int k = 0; k < CPT; k += CH) {
+                        wait_ld();
+                        ld_cols(ts + (k + CH) % CPT, x[(k / CH + 1) & 1]);  // the last: the first again
+                        largest(x[(k / CH) & 1], m0, m1);
+                    }
                     settle(fmaxf(m0, m1));
                     const float off = m == -INFINITY ? 0.0f : kBias - m;
                     const uint64_t c2 = pair(c, c), off2 = pair(off, off);
                     sum = pair(0.0f, 0.0f);
-#pragma unroll 1
+                    static_assert(CPT / CH % 2 == 0 || CPT <= 64);
+#pragma unroll
                     for (int k = 0; k < CPT; k += CH) {  // a chunk's P lands on columns already read
-                        uint32_t y[CH], pk[CH / 2];
-                        ld_cols(ts + k, y);
                         wait_ld();
-                        powers(y, c2, off2, pk);
+                        if (k + CH < CPT) ld_cols(ts + k + CH, x[(k / CH + 1) & 1]);
+                        powers(x[(k / CH) & 1], c2, off2, pk);
                         st_cols(tb + k / 2, pk);
                     }
                 }
@@ -617,6 +619,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                         }
                     }
                 }
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.p_full[buf]);
                 l = l * (m == ml ? 1.0f : ml == -INFINITY ? 0.0f : ex2(ml - m)) + sum_pair(sum);
                 if (inf.flags & 2) {
 #pragma unroll 1
@@ -627,10 +633,6 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                             if ((w >> j) & 1u) nanblk |= s.nanblk[info][col0 + k + j];
                     }
                 }
-                wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s.p_full[buf]);
             }
             if (!ok) break;
         }
