@@ -44,13 +44,13 @@
 // Bound.  The cache is read once a row tile, 2 dim (1 + 1/32) bytes a key and head: 1440 cycles of an SM's
 // share of HBM a tile of 128 keys at dim 128; the tensor cores need 1024 for it, the exponentials of
 // 128 rows 512, shared memory (codes in and out, f16 in and out, the MMAs' reads: 144 KB) 1150.  It
-// takes 2350: S of a tile waits for the product with the P two tiles before, whose place it takes
+// takes 2080: S of a tile waits for the product with the P two tiles before, whose place it takes
 // (tensor memory has no room for more: two S, O and Q fill 460 of 512 columns, another S does not
-// fit), so the latencies of softmax (2800 cycles) and of the products with their handoffs (1900) add
+// fit), so the latencies of softmax (2300 cycles) and of the products with their handoffs (1900) add
 // up over two tiles.  P in columns of its own with Q in shared memory ran 20 percent slower, each tile
 // halved between the sets 13 percent slower.
-// Measured: 6 row tiles x 131072 keys x 4 heads at dim 128: 213 us (0.97 PFLOP/s, 0.49 of the measured
-// bf16 rate); 84 to 161 rows, 16 requests of 8192 tokens at most, 4 heads: 47 us, of which a third is
+// Measured: 6 row tiles x 131072 keys x 4 heads at dim 128: 189 us (1.09 PFLOP/s, 0.56 of the measured
+// bf16 rate); 84 to 161 rows, 16 requests of 8192 tokens at most, 4 heads: 44 us, of which a third is
 // segments' starts and ends.
 #include "bsf8_attend.cuh"
 
