@@ -64,7 +64,7 @@ def _torch_flags():
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE]
     cc = ["g++", "-O2", "-std=c++17", "-fPIC", *[f"-I{i}" for i in inc],
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-    ld = [f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-L{HERE}",
+    ld = [f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", f"-L{HERE}",
           "-l:libbsf8.so", "-Wl,-rpath,$ORIGIN"]
     return cc, ld
 
