@@ -2,8 +2,8 @@
 //
 //   out[row] = sum_l 2^(x_l - m) v_l / sum_l 2^(x_l - m),   x_l = scale log2(e) q[row].k_l,
 // over the keys l that the row sees; a row is a (node, query head) of one request and cache
-// head.  One pass over the cache with the running maximum m and sum of a softmax.  Up to 16 rows at
-// dim 128 run in bsf8_attend_few.cu, on the same cut of the work and the same join.
+// head.  One pass over the cache with the running maximum m and sum of a softmax.  Up to 8 rows at
+// dim 128 over long contexts run in bsf8_attend_few.cu, on the same cut of the work and the same join.
 //
 // Work.  An item is a tile of TN keys (128; 64 at dim 256) of one (request, head, tile of RT
 // rows), a segment all items of one (request, head, row tile).  The segments of all requests, in that
@@ -646,14 +646,16 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
 
 namespace {
 
-// Rows a tile: the smallest that holds all of a request's rows of a head, 128 past that.  4 rows x 8
-// heads x 64 requests of up to 16384 tokens, dim 128: 184 us in the kernel for 8 rows (which
-// has no dims but 128), 244 in the one for 32; fewer rows a tile than needed would read the cache again.
-int row_tile(int T, int g, int dim) {
-    const int rows = T * g;
-    if (dim == 128 && rows <= 16) return rows <= 8 ? 8 : 16;
-    return rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-}
+// Rows a tile: the smallest that holds all of a request's rows of a head, 128 past that; fewer would read
+// the cache again.
+int row_tile(int T, int g) { return T * g <= 32 ? 32 : T * g <= 64 ? 64 : 128; }
+
+// Up to 8 rows at dim 128 the kernel with keys in the lanes, where requests may be longer than 2048
+// tokens: 64 requests x 8 heads x 8 rows, contexts of all lengths up to 4000, 16000: 71, 186 us there, 78, 227
+// in the one for 32 rows; up to 200, 2000: 28.6, 56.1 there, 28.3, 53.4 here; one request of 50, 16000: 11.5,
+// 16.2 there, 10.2, 18.2 here.  (For 16 rows it took a third longer than the one for 32 at every length, at
+// dim 64 as long.)
+bool few_rows(int T, int g, int dim, int max_len) { return dim == 128 && T * g <= kFewRows && max_len > 2048; }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
@@ -691,7 +693,7 @@ cudaError_t code_map(const CacheView &c, void *codes, int box_rows, CUtensorMap 
 
 template <int D>
 cudaError_t launch_attend_dim(const AttendParams &prm, cudaStream_t stream) {
-    switch (row_tile(prm.T, prm.g, D)) {
+    switch (row_tile(prm.T, prm.g)) {
         case 32: return launch_attend_shape<Shape<D, 32>>(attend_kernel<D, 32>, prm, stream);
         case 64: return launch_attend_shape<Shape<D, 64>>(attend_kernel<D, 64>, prm, stream);
         default: return launch_attend_shape<Shape<D, 128>>(attend_kernel<D, 128>, prm, stream);
@@ -702,13 +704,13 @@ cudaError_t launch_attend_dim(const AttendParams &prm, cudaStream_t stream) {
 
 // Two partials a block, their statistics, and the prefix sums; 16 bytes to start on a whole sector.
 size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
-    const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(T, Hq / heads, dim);
+    const size_t rows = (size_t)kAttendBlocks * 2 * row_tile(T, Hq / heads);
     return 16 + rows * dim * 4 + rows * 8 + round16(((size_t)B + 1) * 4);
 }
 
 // Items of the largest call these arguments allow; they are counted in 31 bits.
 bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
-    const int g = Hq / c.heads, rt = row_tile(T, g, c.dim), tn = c.dim == 256 ? 64 : 128;
+    const int g = Hq / c.heads, rt = row_tile(T, g), tn = c.dim == 256 ? 64 : 128;
     return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn + 4) < 2147483648.0;
 }
 
@@ -736,7 +738,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.Hq = a.Hq;
     prm.g = a.Hq / c.heads;
     prm.W = (a.T + 31) / 32;
-    const int rt = row_tile(a.T, prm.g, c.dim);
+    const int rt = row_tile(a.T, prm.g);  // the workspace holds 32 rows where 8 are used
     const size_t rows = (size_t)kAttendBlocks * 2 * rt;
     prm.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(a.workspace) + 31) / 32 * 32);
     prm.stat = reinterpret_cast<float2 *>(prm.part + rows * c.dim);
@@ -747,7 +749,7 @@ cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t 
     prm.skip_loads = opt.skip_loads;
     prm.status = status_word();
     if (!prm.status) return cudaErrorInvalidSymbol;
-    if (rt <= 16) return launch_attend_few(prm, rt, stream);
+    if (few_rows(a.T, prm.g, c.dim, a.max_len)) return launch_attend_few(prm, stream);
     switch (c.dim) {
         case 64: return launch_attend_dim<64>(prm, stream);
         case 128: return launch_attend_dim<128>(prm, stream);

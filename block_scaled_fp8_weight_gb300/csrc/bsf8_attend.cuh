@@ -51,8 +51,9 @@ struct AttendParams {
     int *status;
 };
 
-// The kernels for up to 16 rows of a request and head at dim 128 (bsf8_attend_few.cu).
-cudaError_t launch_attend_few(const AttendParams &prm, int rows, cudaStream_t stream);
+// The kernel for up to 8 rows of a request and head at dim 128 (bsf8_attend_few.cu).
+constexpr int kFewRows = 8;
+cudaError_t launch_attend_few(const AttendParams &prm, cudaStream_t stream);
 
 namespace {
 

@@ -1,5 +1,5 @@
-// bsf8_attend_few.cu -- attention over the paged block-scaled fp8 cache for up to 16 rows (a row is a
-// (node, query head) of one request and cache head) at dim 128: single tokens, small trees.
+// bsf8_attend_few.cu -- attention over the paged block-scaled fp8 cache for up to 8 rows (a row is a
+// (node, query head) of one request and cache head) at dim 128 and long contexts: single tokens.
 //
 // The formula, the cut of the work into items and the join are those of bsf8_attend.cu.  What differs
 // is that keys and channels, not rows, fill the MMA's 128 lanes, and that the cached codes enter
@@ -11,14 +11,16 @@
 //                 a key and 32 channels, so it goes into P: for each of the four channel blocks c a
 //                 copy p 2^(e(key, c) - E), E the segment's largest exponent so far.  Lane quarter c
 //                 of O^T is right in the columns of copy c only, and only those are read.  Each copy
-//                 is the sum of three e4m3 parts (12 bits of p = 2^(x - m) where it is above 2^-12, to
-//                 2^-24 below that), in columns of their own: 12 columns a row.
+//                 is the sum of four e4m3 parts (p = 2^(x - m), rounded to f16's 11 bits first, whole
+//                 where it is above 2^-12, to 2^-35 below that), in columns of their own: 16 columns a row.
+//                 (Three parts, to 2^-24 of p, lost what a channel holds where the key of the largest p has
+//                 a zero; they took 182 us where four take 185.)
 // So nothing is widened, and an SM's shared memory moves about 90 KB a tile (144 KB in bsf8_attend.cu)
 // while HBM moves 33.
 //
 // Warps: a producer of keys (codes, both kinds of exponents), one of values (codes, and a segment's Q,
-// which so comes tiles ahead); one for each product; sets of four for the softmax, three up to 8 rows,
-// two past that, tile about, thread = key.  The rows' references m and the value exponent E are common
+// which so comes tiles ahead); one for each product; three sets of four for the softmax, tile about,
+// thread = key.  The rows' references m and the value exponent E are common
 // to a tile's keys.  A set's warps exchange their largest exponents and whether any x passes the m that
 // the set knows by more than 2.8; then the set takes the tile before's number of changes of m and E, and
 // only where that is new, or an x did pass (a segment's first tiles, as a rule), forms new maxima and
@@ -40,27 +42,26 @@ namespace bsf8 {
 
 namespace {
 
+constexpr int ROWS = kFewRows;
 constexpr int kFewK = 0, kFewV = 1, kFewS = 2, kFewO = 3;  // then the sets
 // Tiles whose value exponents and flags are kept: the keys' producer fills an entry again eight tiles
 // later, once the S of the tile four later is done, which takes the place of this tile's or a later one's
 // S, thus after the softmax has read that.
 constexpr int kRing = 8;
-constexpr float kFewBias = 6.0f;      // p = 2^(x - m + kFewBias)
-constexpr float kFewSlack = 2.8f;     // m lags the maximum by at most this: p <= 2^8.8 < 448, e4m3's largest
+constexpr float kFewBias = 13.0f;     // p = 2^(x - m + kFewBias); P holds p / 2^7
+constexpr float kFewSlack = 2.8f;     // m lags the maximum by at most this: p / 2^7 <= 2^8.8 < 448, e4m3's largest
 constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing: any x passes it
 
-template <int ROWS>
 struct FewShape {
     static constexpr int DIM = 128, RT = ROWS, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
-    // three sets' registers do not suffice for 16 rows, nor does shared memory for their P
-    static constexpr int SETS = ROWS == 8 ? 3 : 2, THREADS = (4 + 4 * SETS) * 32;
+    static constexpr int SETS = 3, THREADS = (4 + 4 * SETS) * 32;
     // tiles' worth of time that a segment takes besides its own (64 requests of 70 to 16384 tokens: 218 us
     // with 2, 197 with 3, 187 with 4 and 5, 189 with 6)
     static constexpr int START = 4;
-    static constexpr int NS = ROWS == 8 ? 4 : 2;          // buffers of S
-    static constexpr int NQ = 2 * ROWS, NP = 12 * ROWS;   // columns of S, of O
-    static constexpr int PCOLS = (NP + 127) / 128;        // 128-byte columns of P
-    static constexpr int PBUF = PCOLS * TN * 128;
+    static constexpr int NS = 4;                          // buffers of S
+    static constexpr int NQ = 2 * ROWS, NP = 16 * ROWS;   // columns of S, of O
+    static constexpr int PBUF = TN * NP;                  // a key's row of P: 128 bytes
+    static_assert(NP == 128);
     // tensor memory columns: two O, S, scales of two tiles' keys and of two segments' rows
     static constexpr int CO = 0, CS = 2 * NP, CB = CS + NS * NQ, CA = CB + 8;
     static_assert(CA + 8 <= 512);
@@ -70,7 +71,6 @@ struct FewShape {
     static constexpr int oExp = oQs + 2 * 512, oVex = oExp + NSLOT * 1024, oPrefix = oVex + kRing * 512;
 };
 
-template <int ROWS>
 struct FewShared : BlockShared {
     uint64_t k_full[4], k_free[4];    // ring slots of keys: codes and exponents landed; multiplied
     uint64_t c_full[4], c_free[4];    // of values
@@ -137,7 +137,6 @@ struct Batch {
 // A segment's rows of Q, by a warp, eight lanes a row.  Each row scaled by a power of two 2^-eq so that
 // its largest lies in [2^7, 2^8), as the sum of two e4m3 parts, the lower one times 2^4.  Exact for
 // bf16 values within 2^14 of the row's largest, else off by at most 2^-22 of that.
-template <int ROWS>
 __device__ __forceinline__ void put_q(const AttendParams &p, const Segment &g, uint8_t *qb, uint32_t *sc, int lane) {
 #pragma unroll 1
     for (int r0 = 0; r0 < ROWS; r0 += 4) {
@@ -185,24 +184,34 @@ __device__ __forceinline__ float warp_max(float x) {
     return y;
 }
 
-// A pair of rows' p times the scale pair sc as three e4m3 pairs: y = h + m / 16 + l / 256.
-__device__ __forceinline__ void split3(uint32_t p2, uint32_t sc, uint32_t &h, uint32_t &m, uint32_t &l) {
-    const uint32_t y = f16x2_mul(p2, sc);
-    h = f16_to_e4m3(y);
-    const uint32_t r = f16x2_mul(f16x2_sub(y, e4m3_to_f16((uint16_t)h)), 0x4C004C00u);  // * 16
-    m = f16_to_e4m3(r);
-    l = f16_to_e4m3(f16x2_mul(f16x2_sub(r, e4m3_to_f16((uint16_t)m)), 0x4C004C00u));
+__device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// A pair of rows' p times the scale pair sc, 2^7 y, as four e4m3 pairs: y = a + b / 2^4 + c / 2^8 + d / 2^19.
+// What a part leaves is exact in f16, and up to 2^8.8 at most 16 (half of its last place) of the next
+// one's units, so nothing overflows; d saturates where y is large and takes what is left of a small one.
+__device__ __forceinline__ void split4(uint32_t p2, uint32_t sc, uint32_t (&w)[4]) {
+    uint32_t r = f16x2_mul(p2, sc);
+    constexpr uint32_t down[4] = {0x20002000u, 0x30003000u, 0x40004000u, 0x6C006C00u};  // 2^-7, 2^-3, 2^1, 2^12
+    constexpr uint32_t up[3] = {0xD800D800u, 0xC800C800u, 0xB800B800u};                 // -2^7, -2^3, -2^-1
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[k] = f16_to_e4m3(f16x2_mul(r, down[k]));
+        if (k < 3) r = f16x2_fma(e4m3_to_f16((uint16_t)w[k]), up[k], r);
+    }
 }
 
 }  // namespace
 
-template <int ROWS>
-__global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(const __grid_constant__ AttendParams p) {
-    using S = FewShape<ROWS>;
+__global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const __grid_constant__ AttendParams p) {
+    using S = FewShape;
     constexpr int TN = S::TN, SETS = S::SETS;
     extern __shared__ uint8_t dyn_smem[];
     uint8_t *const base = dyn_smem + ((1024u - (smem_u32(dyn_smem) & 1023u)) & 1023u);
-    __shared__ FewShared<ROWS> s;
+    __shared__ FewShared s;
     int *const prefix = reinterpret_cast<int *>(base + S::oPrefix);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -260,7 +269,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
             if (value) {
                 ok = seg < 2 || wait(&s.q_free[par], (uint32_t)((seg >> 1) & 1) ^ 1u);
                 if (!ok) break;
-                put_q<ROWS>(p, g, base + S::oQ + par * S::QBUF, reinterpret_cast<uint32_t *>(base + S::oQs + par * 512), lane);
+                put_q(p, g, base + S::oQ + par * S::QBUF, reinterpret_cast<uint32_t *>(base + S::oQs + par * 512), lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.q_full[par]);
             }
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     fence_after();
                     const float fv = pow2i(max(-rise, -149));
 #pragma unroll 1
-                    for (int k = 0; k < 3; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         const uint32_t at = tl + S::CO + par * S::NP + (4 * k + quad) * ROWS;
                         uint32_t o[ROWS];
                         ld_cols(at, o);
@@ -556,25 +565,24 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 // ---- P
                 uint8_t *const pb = base + S::oP + set * S::PBUF + key * 128;
                 // column 4 ROWS part + ROWS block + row of the key's 128-byte rows, swizzled
-                constexpr int U = ROWS == 8 ? 2 : 4;  // 16-byte units a part
+                constexpr int U = ROWS / 4;  // 16-byte units a part
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    uint32_t w[3][4];
+                    uint32_t w[4][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {  // four rows of a block a word
-                        const int blk = ROWS == 8 ? 2 * u + (j >> 1) : u, r = ROWS == 8 ? 4 * (j & 1) : 4 * j;
+                        const int blk = 2 * u + (j >> 1), r = 4 * (j & 1);
                         const int e = (int)((ex >> (8 * blk)) & 0xFFu);
                         const uint32_t sc = f16_pow2(e - E);
-                        uint32_t a[3], b[3];
-                        split3(p2[r / 2], sc, a[0], a[1], a[2]);
-                        split3(p2[r / 2 + 1], sc, b[0], b[1], b[2]);
+                        uint32_t a[4], b[4];
+                        split4(p2[r / 2], sc, a);
+                        split4(p2[r / 2 + 1], sc, b);
 #pragma unroll
-                        for (int k = 0; k < 3; ++k) w[k][j] = a[k] | (b[k] << 16);
+                        for (int k = 0; k < 4; ++k) w[k][j] = a[k] | (b[k] << 16);
                     }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const int un = k * U + u;
-                        *reinterpret_cast<uint4 *>(pb + (un >> 3) * (TN * 128) + (((un & 7) ^ (key & 7)) << 4)) =
+                    for (int k = 0; k < 4; ++k) {
+                        *reinterpret_cast<uint4 *>(pb + (((k * U + u) ^ (key & 7)) << 4)) =
                             make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                     }
                 }
@@ -627,12 +635,12 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                     const float q = s.soff[par][w >> 2][rl], a = s.sum[par][w][rl];
                     L += a == 0.0f ? 0.0f : a * (q == end ? 1.0f : ex2(end - q));
                 }
-                const float inv = L == 0.0f ? 0.0f : fv / L;
+                const float inv = L == 0.0f ? 0.0f : fv * 128.0f / L;
                 const bool bad = s.nan[seg & 3][quad][rl];
                 __syncwarp();
                 if (lane < ROWS) s.nan[seg & 3][quad][lane] = 0;
                 if (quad == 0 && lane < ROWS && lane < rows) {
-                    const float Lt = L * (1.0f / 64.0f);  // bias 6
+                    const float Lt = L * 0x1p-13f;  // without the bias
                     const float M = end == kUnseen ? -INFINITY : kFewBias - end;
                     const int t = lane / p.g, hq = g.h * p.g + lane - t * p.g;
                     if (!whole)
@@ -643,12 +651,12 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
                 }
                 float y[ROWS];
 #pragma unroll
-                for (int k = 2; k >= 0; --k) {
+                for (int k = 3; k >= 0; --k) {
                     uint32_t o[ROWS];
                     ld_cols(tl + S::CO + par * S::NP + (4 * k + quad) * ROWS, o);
                     wait_ld();
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) y[r] = (k == 2 ? 0.0f : y[r] * 0.0625f) + __uint_as_float(o[r]);
+                    for (int r = 0; r < ROWS; ++r) y[r] = (k == 3 ? 0.0f : y[r] * (k == 2 ? 0x1p-11f : 0x1p-4f)) + __uint_as_float(o[r]);
                 }
                 fence_before();
                 __syncwarp();
@@ -676,9 +684,8 @@ __global__ void __launch_bounds__(FewShape<ROWS>::THREADS, 1) attend_few_kernel(
     free_tmem(tmem, warp == kFewS);
 }
 
-cudaError_t launch_attend_few(const AttendParams &prm, int rows, cudaStream_t stream) {
-    return rows <= 8 ? launch_attend_shape<FewShape<8>>(attend_few_kernel<8>, prm, stream)
-                     : launch_attend_shape<FewShape<16>>(attend_few_kernel<16>, prm, stream);
+cudaError_t launch_attend_few(const AttendParams &prm, cudaStream_t stream) {
+    return launch_attend_shape<FewShape>(attend_few_kernel, prm, stream);
 }
 
 }  // namespace bsf8

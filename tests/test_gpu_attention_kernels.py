@@ -1,8 +1,7 @@
-"""GPU: what the attention kernels' own structure can get wrong: up to 16 rows of a request and head (keys
-and channels fill the matrix instruction there), many short requests in one block's share, the
-same call again and again with no pause, waits that run out.  Formula and tolerances are those of
-the other attention tests; up to 16 rows at dim 128 a p below 2^-12 of the largest is kept to 2^-24 of
-it, rounded to nearest, which those tolerances' 2^-9 of the sum of p |v| cover for the lengths here."""
+"""GPU: what the attention kernels' own structure can get wrong: few rows of a request and head, many
+short requests in one block's share, the same call again and again with no pause, waits that run out.
+Formula and tolerances are those of the other attention tests; the kernel for up to 8 rows at dim 128
+rounds p to 11 bits as well, above 2^-31 of its reference."""
 import numpy as np
 import pytest
 import torch
@@ -93,6 +92,98 @@ def test_timeout_is_reported_without_hanging(bsf8_lib, T, D):
     bound; it returns and the status says so.  The next call is right again."""
     p = Problem(T + D, 2, T, 4, 1, D, 16, [300, 40])
     assert bsf8.device_status() == 0
+    old = bsf8.get_option(bsf8.OPT_WAIT_TIMEOUT_NS)
+    try:
+        bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 2_000_000)     # 2 ms
+        bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 1)
+        p.run()
+        assert bsf8.device_status() == 7
+    finally:
+        bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 0)
+        bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, old)
+    p.check(*p.run())
+    assert bsf8.device_status() == 0
+
+
+# ---- up to 8 rows where requests may be longer than 2048 tokens (`extra`: room in the table): keys and
+# channels fill the matrix instruction there, at dim 128
+
+@pytest.mark.parametrize("page", [16, 48, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 3, 3), (2, 8, 2), (8, 1, 1), (4, 2, 1), (3, 4, 2), (1, 8, 1), (7, 1, 1)])
+def test_few_rows_in_a_long_table(bsf8_lib, T, Hq, Hkv, page):
+    """Contexts from none to many tiles, trees and masks that leave rows empty, requests without nodes."""
+    ctx = [0, 1, 15, 16, 127, 128, 129, 255, 700, 3100]
+    nodes = [max(0, T - i % 3) for i in range(len(ctx))]
+    for mask in ("tree", "random", None):
+        p = Problem(11 * T + page, len(ctx), T, Hq, Hkv, 128, page, ctx, nodes=nodes, mask=mask, spread=5)
+        if mask == "random":
+            p.see[:, 0] = False
+            p.mask = ref.mask_words(p.see)
+        p.check(*p.run())
+    assert bsf8.device_status() == 0
+
+
+def test_few_rows_nan_and_bad_pages_in_a_long_table(bsf8_lib):
+    p = Problem(4, 3, 2, 4, 2, 128, 32, [1000, 300, 5], extra=70)
+    good, _ = p.run()
+    pg, off = p.table[0, 500 // 32], 500 % 32
+    p.data[2][pg, 1, off, 64:96], p.data[3][pg, 1, off, 2] = 0x7F, 255     # a value block
+    node = int(p.ctx[1]) + 1
+    pk, ok = p.table[1, node // 32], node % 32
+    p.data[0][pk, 0, ok, 0:32], p.data[1][pk, 0, ok, 0] = 0x7F, 255        # a node's key block
+    out, lse = p.run()
+    p.check(out, lse)
+    assert torch.isnan(out[0, :, 2:, 64:96]).all() and torch.equal(out[0, :, :2], good[0, :, :2])
+    assert torch.equal(out[0, :, 2:, :64], good[0, :, 2:, :64]) and torch.equal(out[2], good[2])
+    assert torch.equal(out[1, 0, :2].isnan().any(), torch.tensor(bool(p.see[1, 0, 1]), device="cuda"))
+    assert torch.isnan(out[1, 1, :2]).all() and not torch.isnan(out[1, :, 2:]).any()
+    assert bsf8.device_status() == 0
+    p.table[0, 500 // 32] = 1 << 29
+    out, _ = p.run()
+    assert bsf8.device_status() == 10
+    assert torch.isfinite(out[0]).all() and torch.equal(out[2], good[2])
+
+
+def test_few_rows_wide_ranges_in_a_long_table(bsf8_lib):
+    for seed, kw, scale in ((1, dict(spread=14), None), (2, dict(qscale=40.0), 1.0), (3, dict(qscale=1e-3), 1e-3),
+                            (4, dict(qscale=0.0), None)):
+        p = Problem(seed, 3, 2, 8, 2, 128, 32, [500, 33, 0], extra=70, **kw)
+        p.check(*p.run(scale=scale), scale=scale)
+    assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 4, 4), (4, 2, 1), (1, 8, 1)])
+def test_many_requests_in_a_long_table(bsf8_lib, T, Hq, Hkv):
+    """More requests than blocks, a few long ones among them, calls back to back: shares of many segments,
+    some of one tile; every call the same bits."""
+    r = np.random.default_rng(Hq)
+    B = 400
+    ctx = r.integers(0, 200, size=B)
+    ctx[[5, 250]] = 5000
+    nodes = r.integers(0, T + 1, size=B)
+    p = Problem(3 * T + Hq, B, T, Hq, Hkv, 128, 16, ctx, nodes=nodes)
+    cache, table, c, n = p.cache(), i32(p.table), i32(p.ctx), i32(p.nodes)
+    q, mask = p.q.cuda(), torch.from_numpy(p.mask).cuda()
+    out = torch.empty(12, *q.shape, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(12, *q.shape[:3], device="cuda")
+    call = lambda i: bsf8.tree_attention(q, cache, table, c, nodes=n, mask=mask, out=out[i], lse=lse[i])  # noqa: E731
+    call(0)
+    torch.cuda.synchronize()
+    p.check(out[0], lse[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(1, 12):
+            call(i)
+    for _ in range(5):
+        out[1:] = 0
+        graph.replay()
+        torch.cuda.synchronize()
+        assert bsf8.device_status() == 0
+        assert torch.equal(out[1:].view(torch.int16), out[:1].expand(11, -1, -1, -1, -1).contiguous().view(torch.int16))
+
+
+def test_few_rows_timeout_in_a_long_table(bsf8_lib):
+    p = Problem(9, 2, 1, 4, 1, 128, 16, [3000, 40])
     old = bsf8.get_option(bsf8.OPT_WAIT_TIMEOUT_NS)
     try:
         bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 2_000_000)     # 2 ms
