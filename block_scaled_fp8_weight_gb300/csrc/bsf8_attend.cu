@@ -76,6 +76,7 @@ struct Shape {
     static constexpr int CS = 0, CO = 2 * TN, CA = CO + D, CB = CA + 4,
                          CQ = D == 256 ? 0 : CA + 32;
     static constexpr bool QS = D == 256;             // Q in shared memory
+    static_assert(CQ + (QS ? 0 : D / 2) <= 512);
     static constexpr int oV = 0, oK = 2 * F16, oRing = oK + NSLOT * SLOT, oQ = oRing + NSLOT * SLOT;
     static constexpr int oExp = oQ + (QS ? 2 * 128 * D : 0), oStage = oExp + NSLOT * 1024;
     static constexpr int oPrefix = oStage + 2 * 128 * 17 * 4;
@@ -131,9 +132,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
     const Segment first = segment_at<S>(p, prefix, w0, w1);
 
     if (warp == kProducerWarp) {
-        ok = produce<S>(p, s, base, first, w1, warp, lane);
+        ok = produce<S>(p, s, base, first, w1, lane);
     } else if (warp == kScoutWarp) {
-        ok = scout<S>(p, s, base, first, w1, warp, lane);
+        ok = scout<S>(p, s, base, first, w1, lane);
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------------------ MMA issue: a thread a product
         // One thread issues an MMA about every 100 cycles whatever its size (to N = 128); two with

@@ -592,11 +592,8 @@ struct Pages {
 // The producer warp: codes.  Keys by TMA boxes (swizzled, for the MMA), values as they are.
 template <class S>
 __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
-                                   int warp, int lane) {
+                                        int lane) {
     constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
-    (void)warp;
-    (void)BT;
-    (void)NSB;
     bool ok = true;  // no wait ran out
     const int gpb = p.box_rows / 16;  // groups a box: boxes never cross a page's end
     const bool lead = lane < NSB && lane % gpb == 0;
@@ -649,11 +646,8 @@ __device__ __forceinline__ bool produce(const AttendParams &p, AttendPipes &s, u
 // The scout warp: exponents and flags.
 template <class S>
 __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
-                                   int warp, int lane) {
+                                      int lane) {
     constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
-    (void)warp;
-    (void)BT;
-    (void)NSB;
     bool ok = true;  // no wait ran out
     constexpr int KPL = 16 / S::EB;  // keys of a lane's 16 exponent bytes
     const int key0 = lane * KPL;
@@ -757,12 +751,9 @@ __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uin
 
 // The dequant warps: values to f16.
 template <class S>
-__device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first, int w1,
-                                   int warp, int lane) {
-    constexpr int TN = S::TN, D = S::DIM, NSB = TN / 16, BT = 32 / NSB;
-    (void)warp;
-    (void)BT;
-    (void)NSB;
+__device__ __forceinline__ bool widen_values(const AttendParams &p, AttendPipes &s, uint8_t *base, const Segment &first,
+                                             int w1, int warp, int lane) {
+    constexpr int TN = S::TN, D = S::DIM;
     bool ok = true;  // no wait ran out
     const int dw = warp - kSoftWarps;
     // A lane takes 32-channel blocks: two 16-byte loads of codes, one scale, four 16-byte stores.
