@@ -79,15 +79,15 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&y)[8]) {
 // A block takes up to kTokens consecutive tokens and, by blockIdx.y, 256 / LPR rows of each: a lane
 // group has one row number throughout, so that from token to token only addresses move on.  The
 // tokens' places and positions are looked up once, by a thread a token, while the first rows are on
-// their way; kAhead rows a lane group stay in flight (three and four: no faster).  (Looking them up in
-// every lane group cost more instructions than the norm, the rotation and the rounding together.)
-// 8191 tokens of 32 + 8 + 8 heads of 128: 45 us, 4.1 TB/s of the 185 MB that it must move (0.60 of the
-// measured HBM rate; half of the issue slots are taken, some 150 instructions for two rows a warp);
-// 63 tokens: 3 us.
-constexpr int kTokens = 64, kAhead = 2;
+// their way; kAhead rows a lane group stay in flight.  (Looking them up in every lane group cost more
+// instructions than the norm, the rotation and the rounding together.)  What hides latency best is warps:
+// five blocks an SM with a row ahead 41 us, four with one 45, with two 45, six with one 43.
+// 8191 tokens of 32 + 8 + 8 heads of 128: 41 us, 4.5 TB/s of the 185 MB that it must move (0.66 of the
+// measured HBM rate; some 150 instructions for two rows a warp); 63 tokens: 3 us.
+constexpr int kTokens = 64, kAhead = 1, kAppendBlocks = 5;
 
 template <int D>
-__global__ void __launch_bounds__(256, 4) append_kernel(const CacheView c, const AppendArgs a, int tokens, int *status) {
+__global__ void __launch_bounds__(256, kAppendBlocks) append_kernel(const CacheView c, const AppendArgs a, int tokens, int *status) {
     __shared__ long long s_row[kTokens];  // cache row of head 0; -1: not kept
     __shared__ int s_pos[kTokens];        // -1: the token is left out
     pdl_trigger();
@@ -219,9 +219,9 @@ template <int D>
 cudaError_t append_dim(const CacheView &c, const AppendArgs &a, cudaStream_t stream, int *status) {
     constexpr int G = 256 / (D / 8);
     const int chunks = (a.Hq + 2 * c.heads + G - 1) / G;
-    // tokens a block: the work in whole waves of resident blocks (four an SM), as few as kTokens allow
-    // (8191 tokens in three waves of 16: 50 us, in one of 41: 45 us; in a full one and a quarter: 64 us)
-    const long long resident = 152 * 4, work = (long long)a.N * chunks;
+    // tokens a block: the work in whole waves of resident blocks, as few as kTokens allow (with four blocks
+    // an SM, 8191 tokens in three waves of 16: 50 us, in one of 41: 45 us; in a full one and a quarter: 64 us)
+    const long long resident = 152 * kAppendBlocks, work = (long long)a.N * chunks;
     const long long waves = (work + resident * kTokens - 1) / (resident * kTokens);
     const int tokens = (int)((work + resident * waves - 1) / (resident * waves));
     cudaLaunchConfig_t cfg = {};
