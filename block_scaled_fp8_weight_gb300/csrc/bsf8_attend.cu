@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             st_cols(tl + S::CA, f);  // both sets write the same
             wait_st();
         }
-        // Per turn: the next segment's Q (once the last S of the one before is there), then the output
-        // of the one before, then the segment's tiles.
+        // Per turn, once the last S of the segment before is there: the next segment's Q, then the output of
+        // the one before, then the segment's tiles.
         Segment g = first;
         int r = 0, t = 0, hq = 0;          // row of the request and head; its node and query head
         bool real = false;
@@ -329,18 +329,21 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             if (it > 0) next_segment<S>(p, next, w1);
             const bool more = live(next);
             int eq = 0;
-            if (more) {
-                uint4 held[HELD] = {};
-                if constexpr (D <= 128) {
-                    bool there;
-                    const uint4 *const qr = q_row(next, there);
-                    if (there)
+            uint4 held[HELD] = {};
+            if (D <= 128 && more) {
+                bool there;
+                const uint4 *const qr = q_row(next, there);
+                if (there)
 #pragma unroll
-                        for (int j = 0; j < HELD; ++j) held[j] = qr[j];
-                }
-                if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
-                if (!ok) break;
-                fence_after();
+                    for (int j = 0; j < HELD; ++j) held[j] = qr[j];
+            }
+            // The last S is there, so its tile's value exponent is known and O has the product of two tiles before.  (Else
+            // the set of the tile before it could take that product's phase, of the same parity, for the last one's
+            // below, and read the exponent before it is written.)
+            if (it > 0) ok = wait(&s.s_full[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1));
+            if (!ok) break;
+            fence_after();
+            if (more) {
                 ok = put_q(next, held, eq);
                 if (!ok) break;
             }

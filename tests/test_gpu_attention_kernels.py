@@ -195,3 +195,25 @@ def test_few_rows_timeout_in_a_long_table(bsf8_lib):
         bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, old)
     p.check(*p.run())
     assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hq,D", [(3, 4, 128), (16, 4, 128), (30, 4, 128), (9, 4, 64), (33, 4, 64), (9, 4, 256), (40, 4, 256)])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4])
+def test_the_last_tiles_value_exponent(bsf8_lib, T, Hq, D, tiles):
+    """Shares of 1 to 4 tiles a block, each tile with a value exponent of its own, so that a block's last tile
+    has another largest exponent than those before it: the outputs are scaled by the last one's.  The same
+    call again and again gives the same bits."""
+    keys = 64 if D == 256 else 128
+    p = Problem(tiles + T + D, 1, T, Hq, 1, D, 128, [152 * tiles * keys - T - 5], spread=0)
+    s = np.arange(int(p.ctx[0]) + T)
+    steps = np.arange(len(s) // keys + 1) * 5 % 16
+    p.data[3][p.table[0, s // 128], 0, s % 128] = (106 + steps[s // keys])[:, None]
+    cache, args = p.cache(), (i32(p.table), i32(p.ctx))
+    q, mask = p.q.cuda(), torch.from_numpy(p.mask).cuda()
+    p.check(*p.run(cache=cache))
+    out = torch.empty(10, *q.shape, dtype=torch.bfloat16, device="cuda")
+    for i in range(10):
+        bsf8.tree_attention(q, cache, *args, mask=mask, out=out[i])
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), out[:1].expand_as(out).contiguous().view(torch.int16))
+    assert bsf8.device_status() == 0
