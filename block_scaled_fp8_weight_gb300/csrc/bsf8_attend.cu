@@ -63,9 +63,7 @@ namespace {
 template <int D, int ROWS>
 struct Shape {
     static constexpr int DIM = D, RT = ROWS, THREADS = kThreadsA;
-    // tiles' worth of time that a segment takes besides its own (trees of 23 nodes over up to 8192 tokens:
-    // 58 us with 2, 53 with 3, 51 with 4 and 6)
-    static constexpr int START = 5;
+    static constexpr int START = kStart;
     static constexpr int TN = D == 256 ? 64 : 128;   // keys a tile
     static constexpr int EB = D / 32;                // exponent bytes a key
     static constexpr int SLOT = TN * D;              // bytes of a tile's codes
@@ -712,10 +710,11 @@ size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim) {
     return 16 + rows * dim * 4 + rows * 8 + round16(((size_t)B + 1) * 4);
 }
 
-// Items of the largest call these arguments allow; they are counted in 31 bits.
+// Places of the largest call these arguments allow (work_of's sums); they are counted in 31 bits.
 bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
     const int g = Hq / c.heads, rt = row_tile(T, g), tn = c.dim == 256 ? 64 : 128;
-    return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn + 4) < 2147483648.0;
+    const int start = few_rows(T, g, c.dim, max_len) ? kFewStart : kStart;
+    return (double)B * c.heads * (((long long)T * g + rt - 1) / rt) * (((long long)max_len + tn - 1) / tn + start) < 2147483648.0;
 }
 
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream) {

@@ -55,9 +55,7 @@ constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing
 struct FewShape {
     static constexpr int DIM = 128, RT = ROWS, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
     static constexpr int SETS = 3, THREADS = (4 + 4 * SETS) * 32;
-    // tiles' worth of time that a segment takes besides its own (64 requests of 70 to 16384 tokens: 218 us
-    // with 2, 197 with 3, 187 with 4 and 5, 189 with 6)
-    static constexpr int START = 4;
+    static constexpr int START = kFewStart;
     static constexpr int NS = 4;                          // buffers of S
     static constexpr int NQ = 2 * ROWS, NP = 16 * ROWS;   // columns of S, of O
     static constexpr int PBUF = TN * NP;                  // a key's row of P: 128 bytes

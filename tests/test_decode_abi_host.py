@@ -96,6 +96,21 @@ def test_attention_refusals(lib):
         assert lib.bsf8_tree_attention_workspace_bytes(*bad) == 0
 
 
+def test_attention_refuses_more_work_than_it_can_count(lib):
+    """Key tiles with a segment's start and end, over all requests, heads and row tiles, are counted in 31 bits.  (A
+    scale of 0, refused after that, shows that the last call inside the bound is not.)"""
+    def f(tiles, dim, heads, T, page=16, scale=0.0):
+        keys = 64 if dim == 256 else 128
+        return attention(lib, cache(dim=dim, heads=heads, page_size=page), B=1024, T=T, Hq=heads, ldq=heads * dim,
+                         max_len=tiles * keys, table_pages=tiles * keys // page, scale=scale)
+    assert f(26, 64, 65536, 1) == VALUE                                      # 2^26 segments of 26 + 5 places
+    assert f(27, 64, 65536, 1) == SHAPE == f(27, 64, 65536, 1, scale=0.1)    # of 27 + 5: 2^31
+    assert f(122, 256, 16384, 1) == VALUE and f(123, 256, 16384, 1) == SHAPE
+    assert f(58, 64, 16384, 256) == VALUE and f(59, 64, 16384, 256) == SHAPE  # two row tiles
+    # up to 8 rows at dim 128 and more than 2048 tokens: 4 a segment
+    assert f(59, 128, 32768, 1) == VALUE and f(60, 128, 32768, 1) == SHAPE
+
+
 def test_verify_refusals(lib):
     def f(**kw):
         d = dict(p=A, q=A, ld=100, tokens=A, parent=A, u=A, nodes=A, path=A, count=A, token=A, B=2, T=3, V=100)
