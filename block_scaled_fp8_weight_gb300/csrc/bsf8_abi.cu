@@ -550,7 +550,8 @@ int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
     if (!q || !ctx || !out) return BSF8_ERR_NULL;
     if (B > 1024 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
         return BSF8_ERR_SHAPE;
-    if (max_len < 1 || (long long)max_len > (long long)table_pages * cache->page_size) return BSF8_ERR_SHAPE;
+    if (max_len < 1 || max_len > BSF8_MAX_LEN || (long long)max_len > (long long)table_pages * cache->page_size)
+        return BSF8_ERR_SHAPE;
     if (!attend_fits(cache_view(cache, table, B, table_pages), B, T, Hq, max_len)) return BSF8_ERR_SHAPE;
     if (!(scale > 0.0f) || scale > 2.0e38f) return BSF8_ERR_VALUE;
     if (ldq < (int64_t)Hq * cache->dim) return BSF8_ERR_STRIDE;

@@ -15,6 +15,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -303,7 +304,7 @@ PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         }
         long max_len = 0;
         if (a[10] == Py_None) {
-            max_len = (long)t.pages * s.page_size;
+            max_len = std::min((long)t.pages * s.page_size, (long)BSF8_MAX_LEN);
         } else {
             max_len = PyLong_AsLong(a[10]);
             if (max_len == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};

@@ -109,7 +109,7 @@ def tree_attention(q, cache: KVCache, table, ctx, *, nodes=None, mask=None, scal
     slot ctx[b] + t; the batch stride must be T row strides), ctx and nodes int32 [B] (nodes None: all
     T), mask int32 [B, T, ceil(T / 32)] with bit j of row t set where node t sees node j (None: a
     chain, j <= t).  scale defaults to 1 / sqrt(D); max_len bounds a request's cached tokens with its
-    nodes (default: the table's capacity).  Returns bf16 [B, T, Hq, D]; lse, where given (fp32
+    nodes (at most 2^30; default: the table's capacity).  Returns bf16 [B, T, Hq, D]; lse, where given (fp32
     [B, T, Hq]), receives the log of the softmax sums."""
     r = _ext.tree_attention(cache.k8, cache.kexp, cache.v8, cache.vexp, q, table, ctx, nodes, mask, scale, max_len,
                             out, lse, workspace)

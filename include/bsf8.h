@@ -319,8 +319,10 @@ typedef struct {
     int pages, page_size, heads, dim;
 } bsf8_kv_cache;
 
-/* Most nodes of a token tree (its root, the last kept token, counts). */
+/* Most nodes of a token tree (its root, the last kept token, counts), and most cached tokens of a
+ * request that attention reaches (slots and 16-token groups are counted in 31 and 26 bits there). */
 #define BSF8_MAX_NODES 256
+#define BSF8_MAX_LEN (1 << 30)
 
 /* Norms, rotates and appends the projections of N tokens in one pass.  Per head row x of
  * dim channels, in fp32:
@@ -374,8 +376,8 @@ int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests,
  *   ctx    device, int32 [B];  nodes  device, int32 [B], or NULL (all T)
  *   mask   device, int32 [B][T][ceil(T / 32)], bit j % 32 of word j / 32, or NULL
  *   max_len  host: no request has more than max_len cached tokens, its nodes included
- *          (1 .. table_pages * page_size); it sizes the launch, and longer requests count as
- *          BSF8_ERR_INDEX and are cut there
+ *          (1 .. table_pages * page_size, at most BSF8_MAX_LEN); it sizes the launch, and
+ *          longer requests count as BSF8_ERR_INDEX and are cut there
  *   out    device, out, bf16 [B][T][Hq][dim], 16-byte aligned
  *   lse    device, out, fp32 [B][T][Hq]: log of the sum of p_l, or NULL
  *   workspace  device, 16-byte aligned, of at least bsf8_tree_attention_workspace_bytes(...);

@@ -111,6 +111,15 @@ def test_attention_refuses_more_work_than_it_can_count(lib):
     assert f(59, 128, 32768, 1) == VALUE and f(60, 128, 32768, 1) == SHAPE
 
 
+def test_attention_refuses_contexts_past_2_30_tokens(lib):
+    """Past that the kernels' 31-bit slots and their division of 16-token groups by pages would leave the
+    block table."""
+    f = lambda n, scale: attention(lib, cache(page_size=1024), max_len=n, table_pages=(1 << 20) + 64, scale=scale)  # noqa: E731
+    assert f(1 << 30, 0.0) == VALUE  # inside: the scale is what is wrong
+    for n in ((1 << 30) + 1, (1 << 30) + 65536):
+        assert f(n, 0.0) == SHAPE == f(n, 0.1)
+
+
 def test_verify_refusals(lib):
     def f(**kw):
         d = dict(p=A, q=A, ld=100, tokens=A, parent=A, u=A, nodes=A, path=A, count=A, token=A, B=2, T=3, V=100)

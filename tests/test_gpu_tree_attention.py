@@ -252,3 +252,11 @@ def test_in_a_graph_with_a_given_workspace(bsf8_lib):
         else:
             p.check(out, lse)
     assert bsf8.device_status() == 0
+
+
+def test_a_table_with_room_for_more_than_2_30_tokens(bsf8_lib):
+    """The default max_len is then 2^30; the requests' own lengths are what counts."""
+    p = Problem(51, 1, 3, 4, 2, 64, 1024, [2500], extra=(1 << 20) + 61)
+    assert p.table.shape[1] * 1024 > 1 << 30
+    p.check(*p.run())
+    assert bsf8.device_status() == 0
