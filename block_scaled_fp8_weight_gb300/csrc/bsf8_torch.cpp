@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -49,15 +50,20 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     return THPVariable_Unpack(o);
 }
 
-// One call's device: that of its first tensor.
+// One call's device: that of its first tensor, current until the call returns (the library launches on
+// the current device and reads its status word there).
 struct Call {
     int dev = -1;
+    c10::cuda::OptionalCUDAGuard guard;
 
     void cuda(const at::Tensor &t, const char *name) {
         if (!t.is_cuda())
             throw Refused{PyExc_ValueError, std::string(name) + " must be a CUDA tensor (libbsf8 has no CPU path)"};
         const int d = t.get_device();
-        if (dev < 0) dev = d;
+        if (dev < 0) {
+            dev = d;
+            guard.set_index((c10::DeviceIndex)d);
+        }
         if (d != dev)
             throw Refused{PyExc_ValueError, std::string(name) + " is on cuda:" + std::to_string(d) + ", the call on cuda:" +
                                                 std::to_string(dev)};

@@ -270,3 +270,31 @@ def test_empty_calls_and_side_stream(bsf8_lib):
     c, e = ref.quantise(x.float().cpu().numpy().astype(np.float64))
     assert torch.equal(k.cpu().double(), torch.from_numpy(ref.decode(c, e)))
     assert not np.array_equal(before[0], arrays(cache)[0])
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two devices")
+def test_calls_run_where_the_tensors_are(bsf8_lib):
+    """Tensors on a device that is not the current one: the calls run there, on its current stream, and the
+    current device is as before."""
+    from test_gpu_tree_attention import Problem
+    p = Problem(1, 2, 3, 4, 2, 128, 16, [100, 7])
+    want = p.run()
+    other = torch.device("cuda", 1)
+    move = lambda *t: [x.to(other) for x in t]  # noqa: E731
+    c = p.cache()
+    cache = bsf8.KVCache(*move(c.k8, c.kexp, c.v8, c.vexp))
+    table, ctx, nodes, q, mask = move(i32(p.table), i32(p.ctx), i32(p.nodes), p.q.cuda(), torch.from_numpy(p.mask).cuda())
+    assert torch.cuda.current_device() == 0
+    out = bsf8.tree_attention(q, cache, table, ctx, nodes=nodes, mask=mask)
+    assert torch.cuda.current_device() == 0 and out.device == other
+    assert torch.equal(out.cpu().view(torch.int16), want[0].cpu().view(torch.int16))
+    req, slot = torch.zeros(5, dtype=torch.int32, device=other), torch.arange(5, dtype=torch.int32, device=other)
+    x = torch.randn(5, 2, 128, device=other).to(torch.bfloat16)
+    bsf8.qkv_append(None, x, x, cache, table, req, slot)
+    k, v = bsf8.kv_read(cache, table, req, slot)
+    path = torch.tensor([[0, 2, -1]] * 2, dtype=torch.int32, device=other)
+    bsf8.kv_commit(cache, table, ctx, path, torch.tensor([2, 2], dtype=torch.int32, device=other))
+    prob = torch.full((2, 3, 5), 0.2, device=other)
+    tree = torch.tensor([[-1, 0, 0]] * 2, dtype=torch.int32, device=other)
+    count = bsf8.verify_tree(prob, tree.clamp(min=0), tree, torch.zeros(2, 3, device=other), q=prob)[1]
+    assert torch.equal(k, v) and count.device == other and torch.cuda.current_device() == 0
