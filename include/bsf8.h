@@ -426,7 +426,8 @@ int bsf8_verify_tree(const float *p, const float *q, int64_t ld, const int32_t *
 /* Moves the kept nodes of each request's tree together: for i < count[b], slot
  * ctx[b] + path[b][i] -> ctx[b] + i, keys and values, codes and exponents, bit for bit.
  * path[b] is strictly increasing over the first count[b] (as bsf8_verify_tree gives it); the
- * slots behind keep what they held.
+ * slots behind keep what they held.  An entry below 0 or its own place, or not above the one
+ * before it, is left out, and a count outside 0 .. T is cut to that (BSF8_ERR_INDEX).
  *   ctx, count  device, int32 [B];  path  device, int32 [B][T];  T  1 .. BSF8_MAX_NODES
  * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_CUDA. */
 int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_pages,

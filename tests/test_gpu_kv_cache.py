@@ -298,3 +298,52 @@ def test_calls_run_where_the_tensors_are(bsf8_lib):
     tree = torch.tensor([[-1, 0, 0]] * 2, dtype=torch.int32, device=other)
     count = bsf8.verify_tree(prob, tree.clamp(min=0), tree, torch.zeros(2, 3, device=other), q=prob)[1]
     assert torch.equal(k, v) and count.device == other and torch.cuda.current_device() == 0
+
+
+@pytest.mark.parametrize("D,Hkv,page", [(64, 1, 16), (128, 8, 16), (256, 3, 48)])
+def test_commit_of_paths_that_leave_node_0_out(bsf8_lib, D, Hkv, page):
+    """Every entry moves, the first one too: paths that start past node 0, that keep all nodes, none, one."""
+    r = np.random.default_rng(D)
+    paths = [[1, 2], [3], [5, 6, 20], [0, 1, 2, 3], [0, 7, 8], [], list(range(1, 21)), [20]]
+    B, T = len(paths), 21
+    ctx = r.integers(0, 70, size=B)
+    tp = -(-(70 + T) // page)
+    cache = make_cache(r, B * tp, Hkv, D, page)
+    table = i32(r.permutation(B * tp).reshape(B, tp))
+    want = arrays(cache)
+    old = [t.copy() for t in want]
+    for b, way in enumerate(paths):
+        for i, node in enumerate(way):
+            a, z = ctx[b] + node, ctx[b] + i
+            for o, w in zip(old, want):
+                w[int(table[b, z // page]), :, z % page] = o[int(table[b, a // page]), :, a % page]
+    bsf8.kv_commit(cache, table, i32(ctx), i32([way + [-1] * (T - len(way)) for way in paths]), i32([len(w) for w in paths]))
+    for a, b in zip(want, arrays(cache)):
+        assert np.array_equal(a, b)
+    assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("path,count,moved", [
+    ([1, 2, 4], 4, [(1, 0), (2, 1), (4, 2)]),     # a count above T: cut to it
+    ([1, 2, 4], -1, []),                          # below 0
+    ([0, 3, 3], 3, [(3, 1)]),                     # the same node twice
+    ([0, 4, 2], 3, [(4, 1)]),                     # backwards
+    ([-1, 1, 4], 3, [(4, 2)]),                    # no node, and the one after it in its place already
+    ([0, 0, 2], 3, [])])
+def test_commit_reports_bad_counts_and_paths(bsf8_lib, path, count, moved):
+    """What is wrong is left out and reported; the rest moves, and so do other requests' nodes."""
+    r = np.random.default_rng(3)
+    D, page = 64, 16
+    cache = make_cache(r, 4, 2, D, page)
+    want = arrays(cache)
+    old = [t.copy() for t in want]
+    table, ctx = np.array([[0, 2], [3, 1]]), [13, 2]
+    for b, steps in ((0, moved), (1, [(2, 1)])):
+        for node, i in steps:
+            a, z = ctx[b] + node, ctx[b] + i
+            for o, w in zip(old, want):
+                w[table[b, z // page], :, z % page] = o[table[b, a // page], :, a % page]
+    bsf8.kv_commit(cache, i32(table), i32(ctx), i32([path, [0, 2, -1]]), i32([count, 2]))
+    assert bsf8.device_status() == 10
+    for a, b in zip(want, arrays(cache)):
+        assert np.array_equal(a, b)
