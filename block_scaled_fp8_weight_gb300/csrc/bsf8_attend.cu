@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             if (!soft_sync()) return false;
             am = max(am, s.amax[warp ^ 4][lane]);
             eq = max((int)(am >> 7) - 127 - 7, -100);
-            const float qs = pow2i(-eq);  // eq <= 121
+            // A row with an infinity or a NaN becomes NaN as a whole, as its scores are (the conversion to
+            // e4m3 would make an infinity its largest value).
+            const float qs = am >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(-eq);  // eq <= 121
             constexpr int CHUNK = 32;
 #pragma unroll(D <= 128 ? D / 64 : 1)
             for (int c0 = 0; c0 < D / 2; c0 += CHUNK) {

@@ -154,7 +154,9 @@ __device__ __forceinline__ void put_q(const AttendParams &p, const Segment &g, u
 #pragma unroll
         for (int k = 1; k < 8; k <<= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, k));
         const int eq = max((int)(am >> 7) - 127 - 7, -100);  // at most 121
-        const float qs = pow2i(-eq);
+        // A row with an infinity or a NaN becomes NaN as a whole, as its scores are (the conversion to
+        // e4m3 would make an infinity its largest value).
+        const float qs = am >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(-eq);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {

@@ -370,7 +370,8 @@ int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests,
  * j <= t, a chain; T = 1 is the single-token step).  Query head h reads cache head
  * h / (Hq / heads).  Sums and softmax statistics are fp32; see bsf8_attend.cu for how the
  * products are formed.  A row that sees nothing, and rows t >= nodes[b], give zeros and an
- * lse of -inf.  A key or a value block that holds NaN reaches exactly the rows that see it.
+ * lse of -inf.  A key or a value block that holds NaN reaches exactly the rows that see it; a query
+ * head with an infinity or a NaN gives NaN (its lse too) where it sees anything, and no other does.
  *   q      device, bf16, 16-byte aligned; node t of request b at q + (b * T + t) * ldq, its
  *          heads one after another; ldq >= Hq * dim, a multiple of 8
  *   ctx    device, int32 [B];  nodes  device, int32 [B], or NULL (all T)

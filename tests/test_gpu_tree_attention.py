@@ -260,3 +260,33 @@ def test_a_table_with_room_for_more_than_2_30_tokens(bsf8_lib):
     assert p.table.shape[1] * 1024 > 1 << 30
     p.check(*p.run())
     assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("extra", [0, 300])  # with room for more than 2048 tokens: the kernel for few rows at dim 128
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 2, 128), (3, 4, 2, 128), (5, 2, 2, 64), (4, 8, 1, 256), (40, 8, 2, 128),
+                                        (20, 12, 3, 64), (70, 2, 1, 256)])
+def test_infinite_and_nan_queries(bsf8_lib, T, Hq, Hkv, D, extra):
+    """q . k of such a head is an infinity or NaN for every key, so its softmax is NaN: output and lse, where it sees
+    anything.  Every other head's are the same bits as without."""
+    p = Problem(D + T, 3, T, Hq, Hkv, D, 16, [700, 0, 130], extra=extra, mask="random")
+    p.see[1, T // 2] = False                                # sees nothing: no context, no node
+    p.mask = ref.mask_words(p.see)
+    good, lse0 = p.run()
+    q, bad = p.q.clone(), torch.zeros(3, T, Hq, dtype=torch.bool)
+    for b, t, h, c, x in ((0, 0, 0, 5, math.inf), (0, T - 1, Hq - 1, D - 1, -math.inf), (1, T // 2, 0, 0, math.inf),
+                          (2, T // 2, 1, 17, math.nan), (2, 0, Hq - 1, D // 2, math.inf)):
+        q[b, t, h, c] = x
+        bad[b, t, h] = True
+    sees = torch.tensor(p.ctx > 0)[:, None] | torch.from_numpy(p.see.any(2))
+    out, lse = p.run(q=q.cuda())
+    out, lse, good, lse0 = out.cpu(), lse.cpu(), good.cpu(), lse0.cpu()
+    want = bad & sees[..., None]
+    assert torch.isnan(out[want]).all() and torch.isnan(lse[want]).all()
+    assert torch.equal(out[~want].view(torch.int16), good[~want].view(torch.int16)) and torch.equal(lse[~want], lse0[~want])
+    assert not out[1, T // 2].any() and torch.all(lse[1, T // 2] == -math.inf)
+    # keys that all point away from the infinite channel
+    p.data[0][:, :, :, 5] |= 0x80
+    p.data[0][:, :, :, 5] &= 0xFE
+    out, lse = p.run(q=q.cuda())
+    assert torch.isnan(out[0, 0, 0]).all() and torch.isnan(lse[0, 0, 0])
+    assert bsf8.device_status() == 0
