@@ -261,10 +261,11 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             s.amax[warp][lane] = am;
             if (!soft_sync()) return false;
             am = max(am, s.amax[warp ^ 4][lane]);
-            eq = max((int)(am >> 7) - 127 - 7, -100);
             // A row with an infinity or a NaN becomes NaN as a whole, as its scores are (the conversion to
             // e4m3 would make an infinity its largest value).
-            const float qs = am >= 0x7F80u ? __uint_as_float(0x7FC00000u) : pow2i(-eq);  // eq <= 121
+            const bool nan = am >= 0x7F80u;
+            eq = nan ? -100 : max((int)(am >> 7) - 127 - 7, -100);  // at most 120
+            const float qs = nan ? __uint_as_float(0x7FC00000u) : pow2i(-eq);
             constexpr int CHUNK = 32;
 #pragma unroll(D <= 128 ? D / 64 : 1)
             for (int c0 = 0; c0 < D / 2; c0 += CHUNK) {
@@ -452,6 +453,10 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
             t = real ? r / p.g : 0;
             hq = g.h * p.g + (real ? r - t * p.g : 0);
             const float c = p.scale_log2 * pow2i(eq);  // S -> x
+            // The largest key exponent byte e for which no |x| of the warp's rows can reach 2^kLarge:
+            // |S| <= D 2^8 2^9 2^(e - 127), and S c = x with c < 2^above.
+            const int above = (int)(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(c)) >> 23) - 126;
+            const int narrow = kLarge - 17 - (D == 64 ? 6 : D == 128 ? 7 : 8) + 127 - above;
 
             m = -INFINITY;
             l = 0.0f;
@@ -489,16 +494,19 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     w &= ((gb & 1u) ? 0x0000FFFFu : 0u) | ((gb & 2u) ? 0xFFFF0000u : 0u);
                     return w;
                 };
-                if (masked) {  // S of what a row does not see becomes -inf, in place
+                // Scores that may be large become x, rounded, in place, and then have their maximum exactly.
+                const bool wide = inf.flags >> 8 > narrow;
+                const float ct = wide ? 1.0f : c, cm = wide ? c : 1.0f;
+                if (masked || wide) {  // S of what a row does not see becomes -inf, in place
                     constexpr int MC = CPT < 32 ? CPT : 32;
 #pragma unroll 1
                     for (int k = 0; k < CPT; k += MC) {
-                        const uint32_t w = seen(k);
+                        const uint32_t w = masked ? seen(k) : 0xFFFFFFFFu;
                         uint32_t y[MC];
                         ld_cols(ts + k, y);
                         wait_ld();
 #pragma unroll
-                        for (int j = 0; j < MC; ++j) y[j] = (w >> j) & 1u ? y[j] : 0xFF800000u;
+                        for (int j = 0; j < MC; ++j) y[j] = (w >> j) & 1u ? __float_as_uint(__uint_as_float(y[j]) * cm) : 0xFF800000u;
                         st_cols(ts + k, y);
                     }
                     wait_st();
@@ -513,11 +521,15 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                 };
                 // from the thread's largest S: the rows' m at this tile, handed on to the other set
                 auto settle = [&](float mt) {
-                    const float me = mt == -INFINITY ? mt : mt * c;
-                    m = me > mp + kSlack ? me : mp;  // also out of -inf
+                    const float me = mt == -INFINITY ? mt : mt * ct;
+                    m = me - mp > kSlack ? me : mp;  // also out of -inf
                     s.mrow[set][32 * quad + lane] = m;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.m_full[set][quad]);
+                };
+                // bias - m; of a large m less than that by up to its last place, so that p stays in range
+                auto offset = [](float m) -> float {
+                    return m == -INFINITY ? 0.0f : fabsf(m) < (float)(1 << kLarge) ? kBias - m : __fadd_rd(kBias, -m);
                 };
                 uint64_t sum;
                 // p = 2^(x - m + bias) of a chunk, its sum and its f16 pairs
@@ -548,8 +560,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                     bool again = false;
 #pragma unroll 1
                     while (true) {
-                        const float off = m == -INFINITY ? 0.0f : kBias - m;
-                        const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                        const float off = offset(m);
+                        const uint64_t c2 = pair(ct, ct), off2 = pair(off, off);
                         sum = pair(0.0f, 0.0f);
                         uint32_t x[CPT > CH ? 2 : 1][CH];
                         ld_cols(ts, x[0]);
@@ -592,8 +604,8 @@ __global__ void __launch_bounds__(kThreadsA, 1) attend_kernel(const __grid_const
                         largest(x[(k / CH) & 1], m0, m1);
                     }
                     settle(fmaxf(m0, m1));
-                    const float off = m == -INFINITY ? 0.0f : kBias - m;
-                    const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+                    const float off = offset(m);
+                    const uint64_t c2 = pair(ct, ct), off2 = pair(off, off);
                     sum = pair(0.0f, 0.0f);
                     static_assert(CPT / CH % 2 == 0 || CPT <= 64);
 #pragma unroll

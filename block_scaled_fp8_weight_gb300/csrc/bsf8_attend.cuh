@@ -24,6 +24,7 @@ constexpr int kThreadsA = (kMmaWarp + 2) * 32;
 constexpr int kInfo = 8;             // tiles whose exponents and flags are kept
 constexpr float kBias = 9.0f;        // p = 2^(x - m + kBias)
 constexpr float kSlack = 6.0f;       // m lags the maximum by at most this
+constexpr int kLarge = 21;           // |x| from 2^21 on: its last place is no longer small against the slack
 constexpr int kShift = 6;            // f16 values are code * 2^(e - E + kShift)
 
 }  // namespace
@@ -481,7 +482,7 @@ struct __align__(16) TileInfo {
     int valid;   // the 16-key groups that exist (bit i)
     int ev;      // the segment's largest value exponent up to this tile,
     int rise;    // and by how much it passes the one up to the tile before
-    int flags;   // 1: the values need care (missing keys, NaN); 2: a value block holds NaN
+    int flags;   // 1: the values need care (missing keys, NaN); 2: a value block holds NaN; above 8 bits: the keys' largest exponent
 };
 
 __device__ __forceinline__ TileInfo load_info(const TileInfo *i) {
@@ -730,6 +731,9 @@ __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uin
                 mx = __vmaxu4(__vmaxu4(drop(v.x), drop(v.y)), __vmaxu4(drop(v.z), drop(v.w)));
             }
             mx = __vmaxu4(mx, mx >> 16);
+            uint32_t mk = __vmaxu4(__vmaxu4(kx.x, kx.y), __vmaxu4(kx.z, kx.w));
+            mk = __vmaxu4(mk, mk >> 16);
+            const int kmax = (int)__reduce_max_sync(0xFFFFFFFFu, max(mk & 0xFFu, (mk >> 8) & 0xFFu));
             const int before = E;
             E = max(E, (int)__reduce_max_sync(0xFFFFFFFFu, max(mx & 0xFFu, (mx >> 8) & 0xFFu)));
             __syncwarp();
@@ -741,7 +745,7 @@ __device__ __forceinline__ bool scout(const AttendParams &p, AttendPipes &s, uin
                 }
             if (lane == 0)
                 *reinterpret_cast<int4 *>(&s.info[info]) =
-                    make_int4((int)vb, E, i > 0 ? E - before : 0, (nan ? 2 : 0) | (nan || part ? 1 : 0));
+                    make_int4((int)vb, E, i > 0 ? E - before : 0, (nan ? 2 : 0) | (nan || part ? 1 : 0) | kmax << 8);
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&s.k_full[slot]);

@@ -50,7 +50,7 @@ constexpr int kFewK = 0, kFewV = 1, kFewS = 2, kFewO = 3;  // then the sets
 constexpr int kRing = 8;
 constexpr float kFewBias = 13.0f;     // p = 2^(x - m + kFewBias); P holds p / 2^7
 constexpr float kFewSlack = 2.8f;     // m lags the maximum by at most this: p / 2^7 <= 2^8.8 < 448, e4m3's largest
-constexpr float kUnseen = 1e30f;      // bias - m of a row that has seen nothing: any x passes it
+constexpr float kUnseen = 3.4028235e38f;  // bias - m of a row that has seen nothing: any x passes it
 
 struct FewShape {
     static constexpr int DIM = 128, RT = ROWS, TN = 128, EB = 4, SLOT = TN * DIM, NSLOT = 4;
@@ -182,6 +182,13 @@ __device__ __forceinline__ float warp_max(float x) {
     float y;
     asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The smaller one, NaN if either is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
 }
 
 __device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
@@ -502,7 +509,9 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const 
                     for (int r = 0; r < ROWS; ++r) {
                         const float mt = fmaxf(fmaxf(s.most[set][0][r], s.most[set][1][r]),
                                                fmaxf(s.most[set][2][r], s.most[set][3][r]));
-                        const float next = fmaf(mt, c, off[r]) > kFewBias + kFewSlack ? kFewBias - mt * c : off[r];
+                        // m rounded down, and never falling: where its last place is no longer small against the slack an x
+                        // below it may seem to pass it
+                        const float next = fmaf(mt, c, off[r]) > kFewBias + kFewSlack ? fminf(off[r], __fmaf_ru(-mt, c, kFewBias)) : off[r];
                         f[r] = next == off[r] ? 1.0f : ex2(next - off[r]);
                         grow |= next != off[r];
                         off[r] = next;
@@ -533,7 +542,9 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const 
                 uint32_t p2[ROWS / 2];
 #pragma unroll
                 for (int r = 0; r < ROWS; r += 2) {
-                    const float a = ex2(fmaf(sv[r], c, off[r])), b = ex2(fmaf(sv[r + 1], c, off[r + 1]));
+                    // (cut off for such an m only: else no x passes it by more)
+                    const float a = ex2(min_nan(fmaf(sv[r], c, off[r]), kFewBias + kFewSlack));
+                    const float b = ex2(min_nan(fmaf(sv[r + 1], c, off[r + 1]), kFewBias + kFewSlack));
                     l[r] += a;
                     l[r + 1] += b;
                     p2[r / 2] = pack_f16(a, b);

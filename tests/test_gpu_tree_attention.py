@@ -290,3 +290,42 @@ def test_infinite_and_nan_queries(bsf8_lib, T, Hq, Hkv, D, extra):
     out, lse = p.run(q=q.cuda())
     assert torch.isnan(out[0, 0, 0]).all() and torch.isnan(lse[0, 0, 0])
     assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("extra", [0, 300])
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 2, 128), (3, 2, 1, 128), (5, 2, 2, 64), (4, 8, 1, 256), (40, 8, 2, 128),
+                                        (33, 4, 1, 64), (70, 2, 1, 256)])
+@pytest.mark.parametrize("scale", [3e4, 1e7, 1e9, 1e18, 1e30])
+@pytest.mark.parametrize("away", [False, True])
+def test_huge_scores(bsf8_lib, T, Hq, Hkv, D, scale, extra, away):
+    """Scores of up to 1e31, of either sign: one key takes all where no other is within what fp32 sums tell apart
+    (D 2^-24 of sum |q k| scale, for each of the two, and that again), and the lse is its score.  The output is the
+    key's value, off by p's rounding to 11 bits and its own to bf16."""
+    p = Problem(7 * D + T, 3, T, Hq, Hkv, D, 16, [2300, 40, 129], extra=extra)
+    if away:  # every key points away from every query
+        p.q = p.q.abs()
+        p.data[0] |= 0x80
+        p.data[0][p.data[0] == 0xFF] = 0xFE
+    out, lse = p.run(scale=scale)
+    out, lse, g, clear = out.double().cpu(), lse.double().cpu(), Hq // Hkv, 0
+    for b in range(3):
+        c = int(p.ctx[b])
+        s = np.arange(c + T)
+        pg, off = p.table[b, s // 16], s % 16
+        see = torch.from_numpy(np.concatenate([np.ones((T, c), bool), p.see[b]], 1))
+        for h in range(Hq):
+            k, v = (torch.from_numpy(ref.decode(p.data[j][pg, h // g, off], p.data[j + 1][pg, h // g, off])) for j in (0, 2))
+            q = p.q[b, :, h].double()
+            x = (q @ k.T * scale).masked_fill(~see, -math.inf)
+            grain = 4 * D * 2.0 ** -24 * (q.abs() @ k.abs().T * scale).amax(1)
+            top, at = x.topk(2, 1)
+            one = top[:, 0] - top[:, 1] > grain + 200
+            clear += int(one.sum())
+            want = v[at[:, 0]]
+            assert torch.all((out[b, :, h] - want).abs()[one] <= (want.abs() * (2.0 ** -8 + 2.0 ** -10))[one]), (b, h)
+            assert torch.all((lse[b, :, h] - top[:, 0]).abs()[one] <= (grain + 2.0 ** -22 * top[:, 0].abs())[one]), (b, h)
+            # the others: between the values, at the score
+            assert torch.isfinite(out[b, :, h]).all() and torch.all((lse[b, :, h] - top[:, 0]).abs() <= grain + 8 + 2.0 ** -22 * top[:, 0].abs())
+            assert torch.all(out[b, :, h].abs() <= v.abs().amax() * (1 + 2.0 ** -7))
+    assert clear > 3 * T * Hq // 2
+    assert bsf8.device_status() == 0
