@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(256, kAppendBlocks) append_kernel(const CacheV
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float o = __shfl_sync(gmask, y[4 * k + i], from);
-                                y[4 * k + i] = fmaf(y[4 * k + i], cs[i], c0 < half ? -o * sn[i] : o * sn[i]);
+                                const float u = fmaf(y[4 * k + i], cs[i], c0 < half ? -o * sn[i] : o * sn[i]);
+                                if (turned) y[4 * k + i] = u;  // else as it is: an infinity times 0 is none
                             }
                         }
                     }

@@ -347,3 +347,30 @@ def test_commit_reports_bad_counts_and_paths(bsf8_lib, path, count, moved):
     assert bsf8.device_status() == 10
     for a, b in zip(want, arrays(cache)):
         assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("D,rot", [(64, 32), (128, 64), (256, 64), (128, 0)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_infinities_outside_the_rotation_stay(bsf8_lib, D, rot, inter):
+    """Channels past `rot` are not rotated: infinities there come out of the queries as they went in; inside, a pair
+    with one is what the formula gives."""
+    r = np.random.default_rng(rot + D)
+    N = 40
+    q, k = bf16(r, N, 3, D), bf16(r, N, 1, D)
+    for n in range(N):
+        q[n, n % 3, rot + n % (D - rot)] = float("inf") if n % 2 else -float("inf")
+    if rot:
+        q[7, 0, 3] = float("inf")
+    cache = make_cache(r, 4, 1, D, 16)
+    pos = r.integers(1, 50, size=N)
+    ang = np.arange(50)[:, None] * 10000.0 ** (-np.arange(max(rot, 2) // 2) / (max(rot, 2) // 2))
+    cs = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    out = bsf8.qkv_append(q.cuda(), k.cuda(), k.cuda(), cache, i32([[0, 1, 2]]), i32([0] * N), i32(range(N)),
+                          pos=i32(pos) if rot else None, cos_sin=torch.from_numpy(cs).cuda() if rot else None, interleaved=inter)
+    with np.errstate(invalid="ignore"):
+        want = ref.norm_rotate(q.float().numpy(), None, cs if rot else None, pos, inter, 0.0)
+    got = out.float().cpu().numpy()
+    assert np.array_equal(got[..., rot:], want[..., rot:])
+    big = ~np.isfinite(want[..., :rot])
+    assert np.array_equal(np.isnan(want[..., :rot]), np.isnan(got[..., :rot])) and np.array_equal(big, ~np.isfinite(got[..., :rot]))
+    assert bsf8.device_status() == 0
