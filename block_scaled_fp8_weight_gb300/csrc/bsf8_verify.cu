@@ -98,7 +98,8 @@ __device__ __forceinline__ u64 times20(u64 q, uint32_t zh, uint32_t zl) {
 __device__ __noinline__ u64 left_of(u64 P, u64 Q, int x, const VerifyShared &s, bool drawn) {
     if (drawn) {
         u64 off = s.rej > 0 ? Q : 0;  // the first rejection's mass is 2^40
-        for (int j = 1; j < s.rej; ++j)
+        // (as soon as it reaches P nothing is left: the sum of all need not fit 64 bits)
+        for (int j = 1; j < s.rej && off < P; ++j)
             off += s.small ? times20(Q, (uint32_t)(s.Z[j] >> 20), (uint32_t)s.Z[j] & 0xFFFFFu) : times(Q, s.Z[j]);
         return P > off ? P - off : 0;
     }

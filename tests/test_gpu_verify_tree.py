@@ -150,3 +150,23 @@ def test_bad_nodes_are_never_kept(bsf8_lib):
     par2[0, 2], par2[1, 1], par2[2, 4] = -9, -9, -9
     tok2[1, 1] = 0
     compare(p, q, tok2, par2, u, got=got)
+
+
+@pytest.mark.parametrize("rejections,V", [(18, 986896), (64, 266306)])
+def test_rows_far_from_a_distribution(bsf8_lib, rejections, V):
+    """Elements of 1 each: the mass left is nearly V 2^40 after every rejection, and what the one drafted token has
+    given up, 2^40 (1 + (rejections - 1)(V - 1)) = 2^64, is more than 64 bits hold.  Nothing is left of it."""
+    assert (rejections - 1) * (V - 1) + 1 == 1 << 24
+    T = rejections + 1
+    p, q = (torch.ones(1, T, V, device="cuda") for _ in range(2))
+    p[..., 0] = 0.5
+    q[..., 1:] = 0
+    u = torch.full((1, T), 0.75, device="cuda")
+    zeros = torch.zeros(1, T, dtype=torch.int32, device="cuda")
+    for u0 in (0.0, 0.5):
+        u[0, 0] = u0
+        path, count, token = bsf8.verify_tree(p, zeros, zeros, u, q=q)
+        assert path.tolist() == [[0] + [-1] * (T - 1)] and count.tolist() == [1]
+        # the lowest x whose x elements of 1 pass u0 (V - 1)
+        assert token.tolist() == [int(u0 * (V - 1)) + 1]
+    assert bsf8.device_status() == 0
