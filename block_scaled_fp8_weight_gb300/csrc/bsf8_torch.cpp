@@ -189,6 +189,12 @@ double number(PyObject *o) {
     return v;
 }
 
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Refused{nullptr, ""};
+    return v != 0;
+}
+
 template <typename F>
 PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F f) {
     if (got != want) {
@@ -240,7 +246,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const void *qn = c.maybe(a[12], at::kBFloat16, dim, "q_norm"), *kn = c.maybe(a[13], at::kBFloat16, dim, "k_norm");
         const int status = bsf8_qkv_append(q.at, k.at, v.at, q.ld, k.ld, v.ld, out.defined() ? out.data_ptr() : nullptr, &s,
                                            t.at, t.requests, t.pages, req, slot, pos, cs, positions, rot,
-                                           PyObject_IsTrue(a[15]), qn, kn, (float)number(a[14]), small(k.n, "the tokens"),
+                                           truth(a[15]), qn, kn, (float)number(a[14]), small(k.n, "the tokens"),
                                            small(q.heads, "Hq"), c.stream());
         if (status) return PyLong_FromLong(status);
         if (!out.defined()) Py_RETURN_NONE;

@@ -374,3 +374,22 @@ def test_infinities_outside_the_rotation_stay(bsf8_lib, D, rot, inter):
     big = ~np.isfinite(want[..., :rot])
     assert np.array_equal(np.isnan(want[..., :rot]), np.isnan(got[..., :rot])) and np.array_equal(big, ~np.isfinite(got[..., :rot]))
     assert bsf8.device_status() == 0
+
+
+def test_arguments_that_have_no_value_are_refused(bsf8_lib):
+    """What Python cannot read as a truth value or a number raises its own error, and nothing is written."""
+    r = np.random.default_rng(6)
+    cache = make_cache(r, 1, 1, 64, 16)
+    before = arrays(cache)
+    x, table, at = bf16(r, 3, 1, 64).cuda(), i32([[0]]), (i32([0] * 3), i32(range(3)))
+    with pytest.raises(RuntimeError, match="more than one value"):
+        bsf8.qkv_append(x, x, x, cache, table, *at, interleaved=torch.zeros(2))
+    with pytest.raises(TypeError, match="real number"):
+        bsf8.qkv_append(x, x, x, cache, table, *at, eps="1e-6")
+    with pytest.raises(TypeError):
+        bsf8.tree_attention(x.view(1, 3, 1, 64), cache, table, i32([0]), max_len=1.5)
+    with pytest.raises(TypeError, match="real number"):
+        bsf8.tree_attention(x.view(1, 3, 1, 64), cache, table, i32([0]), scale="0.1")
+    torch.cuda.synchronize()
+    for a, b in zip(before, arrays(cache)):
+        assert np.array_equal(a, b)
