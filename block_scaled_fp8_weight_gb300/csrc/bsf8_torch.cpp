@@ -14,10 +14,12 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <cmath>
+#include <exception>
 #include <string>
 
 #include "bsf8.h"
@@ -205,8 +207,8 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, F f) {
         return f();
     } catch (const Refused &r) {
         if (r.type) PyErr_SetString(r.type, r.what.c_str());
-    } catch (const std::exception &e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own (out of memory and the like) as its Python errors
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -393,3 +393,15 @@ def test_arguments_that_have_no_value_are_refused(bsf8_lib):
     torch.cuda.synchronize()
     for a, b in zip(before, arrays(cache)):
         assert np.array_equal(a, b)
+
+
+def test_outputs_that_do_not_fit_raise_torchs_own_error(bsf8_lib):
+    r = np.random.default_rng(7)
+    cache = make_cache(r, 1, 8, 256, 16)
+    n = torch.cuda.get_device_properties(0).total_memory // (8 * 256 * 2) + 1  # tokens: keys alone are more than the card
+    at = torch.zeros(n, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.cuda.OutOfMemoryError):
+        bsf8.kv_read(cache, i32([[0]]), at, at)
+    del at
+    k, v = bsf8.kv_read(cache, i32([[0]]), i32([0]), i32([3]))
+    assert k.shape == (1, 8, 256) and bsf8.device_status() == 0
