@@ -637,6 +637,7 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const 
                 const bool whole = g.kv0 == 0 && g.kv1 == g.nt;
                 const int slotw = 2 * blockIdx.x + (g.kv0 > 0 ? 0 : 1);
                 const float fv = pow2i(E - 127);
+                const bool tiny = E < 64;  // fv / L may be too small for fp32
                 // lane r: row r's sum, in units of the last reference
                 const int rl = lane % ROWS;
                 const float end = s.soff[par][set][rl];
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const 
                     const float q = s.soff[par][w >> 2][rl], a = s.sum[par][w][rl];
                     L += a == 0.0f ? 0.0f : a * (q == end ? 1.0f : ex2(end - q));
                 }
-                const float inv = L == 0.0f ? 0.0f : fv * 128.0f / L;
+                const float inv = L == 0.0f ? 0.0f : (tiny ? 1.0f : fv) * 128.0f / L;
                 const bool bad = s.nan[seg & 3][quad][rl];
                 __syncwarp();
                 if (lane < ROWS) s.nan[seg & 3][quad][lane] = 0;
@@ -669,6 +670,9 @@ __global__ void __launch_bounds__(FewShape::THREADS, 1) attend_few_kernel(const 
 #pragma unroll
                     for (int r = 0; r < ROWS; ++r) y[r] = (k == 3 ? 0.0f : y[r] * (k == 2 ? 0x1p-11f : 0x1p-4f)) + __uint_as_float(o[r]);
                 }
+                if (tiny)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) y[r] *= fv;
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.o_free[par]);

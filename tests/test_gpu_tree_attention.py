@@ -329,3 +329,50 @@ def test_huge_scores(bsf8_lib, T, Hq, Hkv, D, scale, extra, away):
             assert torch.all(out[b, :, h].abs() <= v.abs().amax() * (1 + 2.0 ** -7))
     assert clear > 3 * T * Hq // 2
     assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("extra", [0, 300])
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, 4, 2, 128), (3, 2, 1, 128), (5, 2, 2, 64), (4, 8, 1, 256), (40, 8, 2, 128)])
+@pytest.mark.parametrize("byte", [3, 12, 30, 236])
+def test_the_smallest_and_largest_values(bsf8_lib, T, Hq, Hkv, D, extra, byte):
+    """Values about 2^-116 up to 2^117, over a short context, a long one and one that no block holds alone.  The
+    tolerance is check's, with half a step of bf16's subnormal numbers (2^-134), as many channels hold next to nothing."""
+    p = Problem(byte + D + T, 4, T, Hq, Hkv, D, 32, [4, 300, 2000, 4500], extra=extra)
+    for b in range(4):
+        s = np.arange(int(p.ctx[b]) + T)
+        pg, off = p.table[b, s // 32], s % 32
+        p.data[3][pg, :, off] = p.data[3][pg, :, off] - 121 + byte
+    out = p.run()[0].double().cpu()
+    for b in range(4):
+        c = int(p.ctx[b])
+        s = np.arange(c + T)
+        pg, off = p.table[b, s // 32], s % 32
+        see = np.concatenate([np.ones((T, c), bool), p.see[b]], 1)
+        for h in range(Hq):
+            k, v = (ref.decode(p.data[j][pg, h * Hkv // Hq, off], p.data[j + 1][pg, h * Hkv // Hq, off]) for j in (0, 2))
+            want, _, mass, reach = ref.attention(p.q[b, :, h].double(), k, v, see, D ** -0.5)
+            tol = want.abs() * 2.0 ** -8 + mass * (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -15 * reach[:, None])
+            tol = tol + (c + T) * 2.0 ** -40 * np.abs(v).max() + 2.0 ** -134
+            assert torch.all((out[b, :, h] - want).abs() <= tol), (b, h, float(((out[b, :, h] - want).abs() / tol).max()))
+    assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("byte", [0, 3, 121])
+@pytest.mark.parametrize("Hq,D", [(4, 128), (40, 128), (4, 64)])
+def test_long_segments_in_one_block(bsf8_lib, Hq, D, byte):
+    """More requests than blocks, each of 131072 tokens (the table names two pages over and over, so that every key counts
+    512 times): a softmax's sum of 2^17 and values down to 2^-127 of a code, in one block's registers."""
+    B, page, ctx = 200, 128, 131072
+    p = Problem(byte + Hq + D, 1, 1, Hq, 1, D, page, [2 * page - 1], mask=None, spread=0)
+    p.data[3][:] = byte
+    table = np.tile(p.table[0, :2], ctx // page // 2 + 1)[None].repeat(B, 0)
+    q = p.q.cuda().expand(B, 1, Hq, D).contiguous()
+    out = bsf8.tree_attention(q, p.cache(), i32(table), i32([ctx - 1] * B)).double().cpu()
+    s = np.arange(2 * page)
+    pg, off = p.table[0, s // page], s % page
+    k, v = (ref.decode(p.data[j][pg, 0, off], p.data[j + 1][pg, 0, off]) for j in (0, 2))
+    want, _, mass, reach = ref.attention(p.q[0, 0].double(), k, v, np.ones((Hq, 2 * page), bool), D ** -0.5)
+    # 2^12 steps of 32 keys, each sum off by at most 2^-23 of itself
+    tol = want.abs() * 2.0 ** -8 + mass * (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -15 * reach[:, None]) + 2.0 ** -134
+    assert torch.all((out[:, 0] - want).abs() <= tol), float(((out[:, 0] - want).abs() / tol).max())
+    assert bsf8.device_status() == 0
