@@ -62,7 +62,7 @@ def load(build_if_missing: bool = True):
         if _lib is not None:
             return _lib
         path = _build.LIB
-        if not os.path.exists(path) or not os.path.exists(_build.EXT):
+        if not os.path.exists(path):
             if not build_if_missing:
                 raise RuntimeError(f"libbsf8 is not built ({path}); run build.build()")
             _build.build()
@@ -427,15 +427,5 @@ def get_option(option: int) -> int:
 
 # ----------------------------------------------------------------------- decode operators
 
-# decode.py imports torch, which the rest of this module only does when a call needs it.
-_DECODE = ("KVCache", "qkv_append", "kv_read", "tree_attention", "tree_attention_workspace_bytes", "verify_tree",
-           "kv_commit", "MAX_NODES")
-
-
-def __getattr__(name):
-    if name in _DECODE:
-        from . import decode
-        for n in _DECODE:
-            globals()[n] = getattr(decode, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+from .decode import (MAX_NODES, KVCache, kv_commit, kv_read, qkv_append, tree_attention,  # noqa: E402
+                     tree_attention_workspace_bytes, verify_tree)

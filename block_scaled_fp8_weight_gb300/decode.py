@@ -20,12 +20,21 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
+from . import _check, _torch, load
+from . import build as _build
 
-from . import _check, load
 
-load()  # builds what is missing
-from . import _bsf8_torch as _ext  # noqa: E402
+class _Unloaded:
+    """Stands for the extension until a call needs it: torch is imported and what is missing built then."""
+
+    def __getattr__(self, name):
+        global _ext
+        load()
+        _ext = _build.load_extension()
+        return getattr(_ext, name)
+
+
+_ext = _Unloaded()
 
 MAX_NODES = 256
 
@@ -50,6 +59,7 @@ class KVCache:
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page_size: int = 64, device="cuda"):
         """A new cache; its contents are undefined until tokens are appended."""
+        torch = _torch()
         code = lambda: torch.empty((pages, heads, page_size, dim), dtype=torch.uint8, device=device)  # noqa: E731
         byte = lambda: torch.empty((pages, heads, page_size, dim // 32), dtype=torch.uint8, device=device)  # noqa: E731
         return cls(code(), byte(), code(), byte())
