@@ -22,8 +22,8 @@
 //   scout     exponents and flags: the keys' exponents laid out for tensor memory, the largest value
 //             exponent E of the segment so far, which groups of keys exist;
 //   8 dequant a tile's values -> f16 in shared memory (128-byte swizzle), as code * 2^(e - E + 6): exact for
-//             exponents within 2^21 of E, else off by at most 2^-31 of 2^E; e4m3 times a power of
-//             two needs no more than f16's 11 bits;
+//             exponents within 2^21 of E, else off by at most 2^-31 of 448 * 2^E (from 2^31 below E on
+//             they count as 0); e4m3 times a power of two needs no more than f16's 11 bits;
 //   S         S = Q K^T on the cached codes (block-scaled MMA): the exponents go along as its scales.  Q is the
 //             sum of two e4m3 parts (A, in tensor memory; at dim 256 in shared memory): 8 MMAs a tile;
 //   O         O += P V (P in tensor memory as A, V as an N-major B): 8 MMAs of 16 keys;

@@ -9,8 +9,9 @@
 //                 two columns with scales 2^eq and 2^(eq - 4); softmax adds them (fp32).
 //   O^T += V^T P  A: the tile's codes again, 128 channels x 128 keys.  A value's exponent belongs to
 //                 a key and 32 channels, so it goes into P: for each of the four channel blocks c a
-//                 copy p 2^(e(key, c) - E), E the segment's largest exponent so far.  Lane quarter c
-//                 of O^T is right in the columns of copy c only, and only those are read.  Each copy
+//                 copy p 2^(e(key, c) - E), E the segment's largest exponent so far (0 where that power is
+//                 below 2^-24, f16's smallest).  Lane quarter c of O^T is right in the columns of copy c
+//                 only, and only those are read.  Each copy
 //                 is the sum of four e4m3 parts (p = 2^(x - m), rounded to f16's 11 bits first, whole
 //                 where it is above 2^-12, to 2^-35 below that), in columns of their own: 16 columns a row.
 //                 (Three parts, to 2^-24 of p, lost what a channel holds where the key of the largest p has

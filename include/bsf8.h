@@ -368,10 +368,17 @@ int bsf8_kv_read(const bsf8_kv_cache *cache, const int32_t *table, int requests,
  *   out[b][t][h] = sum_l p_l v_l / sum_l p_l,   p_l = exp(scale * q[b][t][h] . k_l),
  * over the ctx[b] tokens and the nodes j < nodes[b] with bit j of mask[b][t] set (mask NULL:
  * j <= t, a chain; T = 1 is the single-token step).  Query head h reads cache head
- * h / (Hq / heads).  Sums and softmax statistics are fp32; see bsf8_attend.cu for how the
- * products are formed.  A row that sees nothing, and rows t >= nodes[b], give zeros and an
- * lse of -inf.  A key or a value block that holds NaN reaches exactly the rows that see it; a query
- * head with an infinity or a NaN gives NaN (its lse too) where it sees anything, and no other does.
+ * h / (Hq / heads).  A row that sees nothing, and rows t >= nodes[b], give zeros and an lse of
+ * -inf.  A key or a value block that holds NaN (exponent byte 255, as bsf8_qkv_append marks it; the
+ * code 0x7F under another byte is not looked for) reaches exactly the rows that see it; a query head
+ * with an infinity or a NaN gives NaN (its lse too) where it sees anything, and no other does.
+ * Scores, sums and softmax statistics are fp32.  What goes into the products has fewer bits:
+ *   - a query head: exact for channels within 2^14 of its largest, else off by at most 2^-22 of that;
+ *   - p: rounded to 11 bits, and to 2^-33 of the row's largest below 2^-23 of it;
+ *   - a value: exact within 2^20 of the largest one cached for its request and cache head (seen by
+ *     the row or not), else off by at most 2^-24 of that; with up to 8 rows a head at dim 128 its
+ *     product with p is held to 2^-35 of it.
+ * The output's own rounding to bf16 (2^-9) is what shows unless values differ by more than these.
  *   q      device, bf16, 16-byte aligned; node t of request b at q + (b * T + t) * ldq, its
  *          heads one after another; ldq >= Hq * dim, a multiple of 8
  *   ctx    device, int32 [B];  nodes  device, int32 [B], or NULL (all T)

@@ -376,3 +376,34 @@ def test_long_segments_in_one_block(bsf8_lib, Hq, D, byte):
     tol = want.abs() * 2.0 ** -8 + mass * (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -15 * reach[:, None]) + 2.0 ** -134
     assert torch.all((out[:, 0] - want).abs() <= tol), float(((out[:, 0] - want).abs() / tol).max())
     assert bsf8.device_status() == 0
+
+
+@pytest.mark.parametrize("extra", [0, 300])
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(4, 4, 2, 128), (8, 1, 1, 128), (5, 2, 2, 64), (4, 8, 1, 256), (40, 8, 2, 128)])
+def test_values_of_any_range(bsf8_lib, T, Hq, Hkv, D, extra):
+    """Value exponents spread over 2^34, and one node's 2^12 above all others: each value is held to 2^-24 of the largest
+    one of its request and head, whether a row sees that or not, and its product with p to 2^-35 of it a key."""
+    p = Problem(3 * D + T, 3, T, Hq, Hkv, D, 16, [500, 33, 0], extra=extra)
+    p.see[:, T - 1, :] = False
+    p.see[:, T - 1, T - 1] = True   # one row sees that node alone, no other row sees it
+    p.see[:, :T - 1, T - 1] = False
+    p.mask = ref.mask_words(p.see)
+    for b in range(3):
+        c = int(p.ctx[b])
+        s = np.arange(c + T)
+        pg, off = p.table[b, s // 16], s % 16
+        p.data[3][pg, :, off] = p.r.integers(80, 115, size=(c + T, Hkv, D // 32))
+        p.data[3][pg[-1], :, off[-1]] = 126
+    out = p.run()[0].double().cpu()
+    for b in range(3):
+        c = int(p.ctx[b])
+        s = np.arange(c + T)
+        pg, off = p.table[b, s // 16], s % 16
+        see = np.concatenate([np.ones((T, c), bool), p.see[b]], 1)
+        for h in range(Hq):
+            k, v = (ref.decode(p.data[j][pg, h * Hkv // Hq, off], p.data[j + 1][pg, h * Hkv // Hq, off]) for j in (0, 2))
+            want, _, mass, reach = ref.attention(p.q[b, :, h].double(), k, v, see, D ** -0.5)
+            tol = want.abs() * 2.0 ** -8 + mass * (2.0 ** -9 + 2.0 ** -11 + 2.0 ** -14 + 2.0 ** -15 * reach[:, None])
+            tol = tol + np.abs(v).max() * (2.0 ** -24 + (c + T) * 2.0 ** -35)
+            assert torch.all((out[b, :, h] - want).abs() <= tol), (b, h, float(((out[b, :, h] - want).abs() / tol).max()))
+    assert bsf8.device_status() == 0
