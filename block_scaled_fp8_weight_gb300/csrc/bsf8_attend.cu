@@ -30,7 +30,9 @@
 //   8 softmax two sets of four, a set every other tile, thread = row: p = 2^(x - m + 9) (fp32, summed in
 //             fp32), rounded to f16 for the second product: 11 bits of p at any p above 2^-23 of 2^m,
 //             half of 2^-33 of it below.  (bf16 would round p to 8 bits: 1.4 times the error of the
-//             output's own rounding.)  m, handed from set to set, only moves when the maximum has
+//             output's own rounding.)  Where the keys' exponents allow |x| >= 2^21, x itself, rounded, takes
+//             S's place first: x - m by one fma, with an m whose last place is large, would give the largest
+//             p any value.  m, handed from set to set, only moves when the maximum has
 //             grown by more than 2^6 over it: p stays below f16's largest, and rescaling O (a round
 //             trip through registers) becomes rare; with 2^2 it took 4 us of 50 at 4096 tokens.
 // RT rows of Q fill the MMA's 128 rows 128 / RT times; each copy handles its own part of the
@@ -49,9 +51,9 @@
 // fit), so the latencies of softmax (2300 cycles) and of the products with their handoffs (1900) add
 // up over two tiles.  P in columns of its own with Q in shared memory ran 20 percent slower, each tile
 // halved between the sets 13 percent slower.
-// Measured: 6 row tiles x 131072 keys x 4 heads at dim 128: 189 us (1.09 PFLOP/s, 0.56 of the measured
-// bf16 rate); 84 to 161 rows, 16 requests of 8192 tokens at most, 4 heads: 44 us, of which a third is
-// segments' starts and ends.
+// Measured (in a graph): 2 requests of 131072 keys, 288 and 320 rows, thus 6 row tiles, x 4 heads at dim 128: 190 us
+// (1.08 PFLOP/s of the tiles' products, 0.55 of the measured bf16 rate); 77 to 161 rows, 16 requests of 8192
+// tokens at most, 4 heads: 45 us, of which a third is segments' starts and ends.
 #include "bsf8_attend.cuh"
 
 #include <mutex>

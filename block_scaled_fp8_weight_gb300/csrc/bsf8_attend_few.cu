@@ -33,8 +33,8 @@
 //
 // Bound: HBM at long contexts.  A tile of 128 keys takes an SM 1440 cycles at its share of the measured
 // HBM rate, which is what it takes here; three sets (of the softmax's 3600 cycles a tile, latencies
-// mostly) keep up with that, two did not.  64 requests of 70 to 16384 tokens, 4 rows, 8 heads: 184 us with
-// the join; this kernel 182, 6.5 TB/s, 0.96 of the measured HBM rate.  At short contexts latency
+// mostly) keep up with that, two did not.  64 requests of 70 to 16384 tokens (559097 keys), 4 rows, 8 heads: 183
+// us in a graph with the join, 6.45 TB/s, 0.95 of the measured HBM rate.  At short contexts latency
 // bounds: one request of 1000 tokens, a tile a block, takes 13 us -- prefix sums 2, table, codes and Q
 // 2.5, products and softmax 2, output 1.5, the join 3, launches 2.
 #include "bsf8_attend.cuh"

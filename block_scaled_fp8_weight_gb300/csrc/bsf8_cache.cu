@@ -82,7 +82,7 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&y)[8]) {
 // their way; kAhead rows a lane group stay in flight.  (Looking them up in every lane group cost more
 // instructions than the norm, the rotation and the rounding together.)  What hides latency best is warps:
 // five blocks an SM with a row ahead 41 us, four with one 45, with two 45, six with one 43.
-// 8191 tokens of 32 + 8 + 8 heads of 128: 41 us, 4.5 TB/s of the 185 MB that it must move (0.66 of the
+// In a graph, 8191 tokens of 32 + 8 + 8 heads of 128: 41 us, 4.5 TB/s of the 185 MB that it must move (0.66 of the
 // measured HBM rate; some 150 instructions for two rows a warp); 63 tokens: 3 us.
 constexpr int kTokens = 64, kAhead = 1, kAppendBlocks = 5;
 
@@ -252,7 +252,7 @@ cudaError_t launch_append(const CacheView &c, const AppendArgs &a, cudaStream_t 
 // A token's pieces are its rows' runs of 16 codes (one 16-byte load, two 16-byte stores), keys then
 // values; a thread takes kReadPieces of a token's, equally far apart, all of their loads in flight:
 // the chain slot, page, codes is walked once for them.  The rebuild is bsf8_dequant's.
-// 65536 tokens of 8 heads of 128: 70 us, 5.8 TB/s (0.86 of the measured HBM rate; one piece a thread:
+// In a graph, 65536 tokens of 8 heads of 128: 70 us, 5.8 TB/s (0.86 of the measured HBM rate; one piece a thread:
 // 88 us); 257 tokens: 3 us.
 constexpr int kReadPieces = 4;
 

@@ -17,8 +17,8 @@
 // which its block reads again (from L2).
 // HBM bound at large batches (a row of p and q a rejection, and one for the last draw), latency bound at
 // small ones: the chain nodes, their probabilities, a pass, the cluster's barrier, the draw.  64 requests
-// of 16 nodes over 131072 tokens: 48 us (110 with each node tested on the way and 64-bit products for every
-// element); one of 6 nodes over 50257: 8.5 us.
+// of 16 nodes over 131072 tokens: 43 to 48 us in a graph, by the walks (110 with each node tested on the way and
+// 64-bit products for every element); one of 6 nodes over 50257: 8.6 to 10.3 us.
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
