@@ -26,6 +26,8 @@ __all__ = [
     "MAX_M", "STATUS",
     "KVCache", "qkv_append", "kv_read", "tree_attention", "tree_attention_workspace_bytes", "verify_tree",
     "kv_commit", "MAX_NODES",
+    "PageBook", "kv_plan", "PageBounds", "kv_bounds", "select_pages", "sparse_attention", "sample_tokens", "token_probs",
+    "residual_norm",
 ]
 
 MAX_M = 16384
@@ -97,6 +99,14 @@ def load(build_if_missing: bool = True):
             "bsf8_tree_attention": (I, [P, I64, P, P, I, P, P, P, ctypes.c_float, I, P, P, I, I, I, P, SZ, P]),
             "bsf8_verify_tree": (I, [P, P, I64, P, P, P, P, P, P, P, I, I, I, P]),
             "bsf8_kv_commit": (I, [P, P, I, P, P, P, I, I, P]),
+            "bsf8_kv_plan": (I, [P, I, I, P, P, P, I, P, P, P, P, P, P, P, I, I, P]),
+            "bsf8_kv_bounds": (I, [P, P, P, I, P, P, I, P]),
+            "bsf8_select_pages": (I, [P, I64, P, P, I, P, P, I, I, I, I, P, P, I, I, I, P]),
+            "bsf8_select_width": (I, [I, I, I]),
+            "bsf8_sparse_attention": (I, [P, I64, P, P, I, P, P, P, ctypes.c_float, I, P, P, I, I, I, P, SZ, P]),
+            "bsf8_sample_tokens": (I, [P, I, I64, P, P, P, P, P, P, P, I, I, P]),
+            "bsf8_token_probs": (I, [P, I, I64, P, P, P, P, P, I, I, P]),
+            "bsf8_residual_norm": (I, [P, I64, P, I64, I, P, P, I, I64, ctypes.c_float, P, ctypes.c_float, P, P, I, I, P]),
             "bsf8_device_status": (I, [P, P]),
             "bsf8_set_option": (I, [I, I64]),
             "bsf8_get_option": (I64, [I]),
@@ -427,5 +437,6 @@ def get_option(option: int) -> int:
 
 # ----------------------------------------------------------------------- decode operators
 
-from .decode import (MAX_NODES, KVCache, kv_commit, kv_read, qkv_append, tree_attention,  # noqa: E402
-                     tree_attention_workspace_bytes, verify_tree)
+from .decode import (MAX_NODES, KVCache, PageBook, PageBounds, kv_bounds, kv_commit, kv_plan, kv_read,  # noqa: E402
+                     qkv_append, residual_norm, sample_tokens, select_pages, sparse_attention, token_probs,
+                     tree_attention, tree_attention_workspace_bytes, verify_tree)

@@ -286,6 +286,72 @@ inline CacheView cache_view(const bsf8_kv_cache *c, const int32_t *table, int re
 
 inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+inline int check_bounds(const bsf8_page_bounds *v) {
+    if (!v || !v->codes || !v->exps) return BSF8_ERR_NULL;
+    if (v->pages < 1 || v->heads < 1 || v->page_size < 16 || v->page_size > 1024 || v->page_size % 16 != 0 ||
+        (v->dim != 64 && v->dim != 128 && v->dim != 256) || (long long)v->pages * v->heads >= (1LL << 31))
+        return BSF8_ERR_SHAPE;
+    if (!aligned16(v->codes)) return BSF8_ERR_ALIGN;
+    return BSF8_OK;
+}
+
+inline BoundsView bounds_view(const bsf8_page_bounds *v, const int32_t *table, int table_pages) {
+    return BoundsView{v->codes, v->exps, table, v->pages, v->page_size, v->heads, v->dim, table_pages};
+}
+
+inline int check_sample(const void *logits, int64_t ld, int bf16, const void *temperature, const void *top_k,
+                        const void *top_p, const void *min_p, const void *p, int N, int V) {
+    if (N == 0) return BSF8_OK;  // nothing to do; empty tensors may have no address
+    if (!logits || !p) return BSF8_ERR_NULL;
+    if (N < 0 || N > (1 << 20) || V < 1 || V > (1 << 20)) return BSF8_ERR_SHAPE;
+    if (ld < V) return BSF8_ERR_STRIDE;
+    (void)bf16;
+    if (!aligned16(logits) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) || !aligned4(p))
+        return BSF8_ERR_ALIGN;
+    return BSF8_OK;
+}
+
+// bsf8_tree_attention, and bsf8_sparse_attention where the table has a row for each head.
+int attention_call(const void *q, int64_t ldq, const bsf8_kv_cache *cache, const int32_t *table, int table_pages, bool per_head,
+                   const int32_t *ctx, const int32_t *nodes, const int32_t *mask, float scale, int max_len, void *out, float *lse,
+                   int B, int T, int Hq, void *workspace, size_t workspace_bytes, bsf8_stream_t stream) {
+    int st = check_cache(cache, table, B, table_pages);
+    if (st) return st;
+    if (!q || !ctx || !out) return BSF8_ERR_NULL;
+    if (B > 1024 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
+        return BSF8_ERR_SHAPE;
+    if (max_len < 1 || max_len > BSF8_MAX_LEN || (long long)max_len > (long long)table_pages * cache->page_size)
+        return BSF8_ERR_SHAPE;
+    CacheView view = cache_view(cache, table, B, table_pages);
+    if (per_head) view.head_pages = table_pages;
+    if (!attend_fits(view, B, T, Hq, max_len)) return BSF8_ERR_SHAPE;
+    if (!(scale > 0.0f) || scale > 2.0e38f) return BSF8_ERR_VALUE;
+    if (ldq < (int64_t)Hq * cache->dim) return BSF8_ERR_STRIDE;
+    if (!aligned16(q) || !aligned16(out) || ldq % 8 != 0) return BSF8_ERR_ALIGN;
+    if (!aligned4(ctx) || !aligned4(nodes) || !aligned4(mask) || !aligned4(lse) || !aligned4(table))
+        return BSF8_ERR_ALIGN;
+    const size_t need = attend_workspace_bytes(B, T, Hq, cache->heads, cache->dim);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return BSF8_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return BSF8_ERR_ALIGN;
+    }
+    AttendArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.ldq = ldq;
+    a.ctx = ctx;
+    a.nodes = nodes;
+    a.mask = mask;
+    a.scale = scale;
+    a.max_len = max_len;
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.workspace = workspace;
+    return from_cuda(launch_attend(view, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -545,40 +611,16 @@ int bsf8_tree_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache,
                         const int32_t *nodes, const int32_t *mask, float scale, int max_len,
                         void *out, float *lse, int B, int T, int Hq, void *workspace,
                         size_t workspace_bytes, bsf8_stream_t stream) {
-    int st = check_cache(cache, table, B, table_pages);
-    if (st) return st;
-    if (!q || !ctx || !out) return BSF8_ERR_NULL;
-    if (B > 1024 || T < 1 || T > BSF8_MAX_NODES || Hq < 1 || Hq % cache->heads != 0 || Hq > 65536)
-        return BSF8_ERR_SHAPE;
-    if (max_len < 1 || max_len > BSF8_MAX_LEN || (long long)max_len > (long long)table_pages * cache->page_size)
-        return BSF8_ERR_SHAPE;
-    if (!attend_fits(cache_view(cache, table, B, table_pages), B, T, Hq, max_len)) return BSF8_ERR_SHAPE;
-    if (!(scale > 0.0f) || scale > 2.0e38f) return BSF8_ERR_VALUE;
-    if (ldq < (int64_t)Hq * cache->dim) return BSF8_ERR_STRIDE;
-    if (!aligned16(q) || !aligned16(out) || ldq % 8 != 0) return BSF8_ERR_ALIGN;
-    if (!aligned4(ctx) || !aligned4(nodes) || !aligned4(mask) || !aligned4(lse) || !aligned4(table))
-        return BSF8_ERR_ALIGN;
-    const size_t need = attend_workspace_bytes(B, T, Hq, cache->heads, cache->dim);
-    if (need > 0) {
-        if (!workspace || workspace_bytes < need) return BSF8_ERR_WORKSPACE;
-        if (!aligned16(workspace)) return BSF8_ERR_ALIGN;
-    }
-    AttendArgs a{};
-    a.q = static_cast<const uint16_t *>(q);
-    a.ldq = ldq;
-    a.ctx = ctx;
-    a.nodes = nodes;
-    a.mask = mask;
-    a.scale = scale;
-    a.max_len = max_len;
-    a.out = static_cast<uint16_t *>(out);
-    a.lse = lse;
-    a.B = B;
-    a.T = T;
-    a.Hq = Hq;
-    a.workspace = workspace;
-    return from_cuda(launch_attend(cache_view(cache, table, B, table_pages), a,
-                                   reinterpret_cast<cudaStream_t>(stream)));
+    return attention_call(q, ldq, cache, table, table_pages, false, ctx, nodes, mask, scale, max_len, out, lse, B, T, Hq,
+                          workspace, workspace_bytes, stream);
+}
+
+int bsf8_sparse_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache, const int32_t *pages, int width,
+                          const int32_t *kept, const int32_t *nodes, const int32_t *mask, float scale, int max_len,
+                          void *out, float *lse, int B, int T, int Hq, void *workspace, size_t workspace_bytes,
+                          bsf8_stream_t stream) {
+    return attention_call(q, ldq, cache, pages, width, true, kept, nodes, mask, scale, max_len, out, lse, B, T, Hq, workspace,
+                          workspace_bytes, stream);
 }
 
 int bsf8_verify_tree(const float *p, const float *q, int64_t ld, const int32_t *tokens,
@@ -605,6 +647,134 @@ int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_p
     if (!aligned4(ctx) || !aligned4(path) || !aligned4(count) || !aligned4(table)) return BSF8_ERR_ALIGN;
     return from_cuda(launch_kv_commit(cache_view(cache, table, B, table_pages), ctx, path, count, B, T,
                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_kv_plan(int32_t *table, int table_pages, int page_size, int32_t *held, int32_t *free_pages, int32_t *free_count,
+                 int pool, const int32_t *lens, const int32_t *add, const int32_t *done, int32_t *req, int32_t *slot,
+                 int32_t *start, int32_t *granted, int B, int N, bsf8_stream_t stream) {
+    if (!table || !held || !free_pages || !free_count || !lens || !add || !start || !granted || (N > 0 && (!req || !slot)))
+        return BSF8_ERR_NULL;
+    if (B < 1 || B > 1024 || N < 0 || N > (1 << 30) || pool < 1 || pool > (1 << 30) || table_pages < 1) return BSF8_ERR_SHAPE;
+    if (page_size < 16 || page_size > 1024 || page_size % 16 != 0) return BSF8_ERR_SHAPE;
+    if ((long long)table_pages * page_size >= (1LL << 31) || (long long)table_pages * B >= (1LL << 31)) return BSF8_ERR_SHAPE;
+    if (!aligned4(table) || !aligned4(held) || !aligned4(free_pages) || !aligned4(free_count) || !aligned4(lens) ||
+        !aligned4(add) || !aligned4(done) || !aligned4(req) || !aligned4(slot) || !aligned4(start) || !aligned4(granted))
+        return BSF8_ERR_ALIGN;
+    PlanArgs a{table, held, free_pages, free_count, lens, add, done, req, slot, start, granted, B, table_pages, page_size, pool, N};
+    return from_cuda(launch_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_kv_bounds(const bsf8_kv_cache *cache, const bsf8_page_bounds *bounds, const int32_t *table, int table_pages,
+                   const int32_t *start, const int32_t *end, int B, bsf8_stream_t stream) {
+    int st = check_cache(cache, table, B, table_pages);
+    if (!st) st = check_bounds(bounds);
+    if (st) return st;
+    if (!end) return BSF8_ERR_NULL;
+    if (B > 1024 || bounds->pages != cache->pages || bounds->page_size != cache->page_size || bounds->heads != cache->heads ||
+        bounds->dim != cache->dim || (long long)B * table_pages >= (1LL << 31))
+        return BSF8_ERR_SHAPE;
+    if (!aligned4(table) || !aligned4(start) || !aligned4(end)) return BSF8_ERR_ALIGN;
+    return from_cuda(launch_bounds(cache_view(cache, table, B, table_pages), bounds_view(bounds, table, table_pages), start, end,
+                                   B, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_select_width(int T, int page_size, int keep) {
+    if (T < 1 || T > BSF8_MAX_NODES || page_size < 16 || page_size > 1024 || page_size % 16 != 0 || keep < 1 ||
+        keep > BSF8_MAX_SELECT_PAGES)
+        return 0;
+    return keep + (2 * page_size - 2 + T) / page_size;
+}
+
+int bsf8_select_pages(const void *q, int64_t ldq, const bsf8_page_bounds *bounds, const int32_t *table, int table_pages,
+                      const int32_t *ctx, const int32_t *nodes, int max_len, int keep, int sink, int recent, int32_t *pages,
+                      int32_t *kept, int B, int T, int Hq, bsf8_stream_t stream) {
+    const int st = check_bounds(bounds);
+    if (st) return st;
+    if (!q || !table || !ctx || !pages || !kept) return BSF8_ERR_NULL;
+    const int P = bounds->page_size, width = bsf8_select_width(T, P, keep);
+    if (B < 1 || B > 1024 || width < 1 || table_pages < 1 || Hq < 1 || Hq % bounds->heads != 0 || Hq > 65536 ||
+        (long long)T * (Hq / bounds->heads) > 4096)
+        return BSF8_ERR_SHAPE;
+    if (max_len < 1 || max_len > BSF8_MAX_LEN || (long long)max_len > (long long)table_pages * P ||
+        max_len / P > BSF8_MAX_SELECT_PAGES)
+        return BSF8_ERR_SHAPE;
+    if (sink < 0 || recent < 0 || sink > keep || recent > keep - sink) return BSF8_ERR_VALUE;
+    if (ldq < (int64_t)Hq * bounds->dim) return BSF8_ERR_STRIDE;
+    if (!aligned16(q) || ldq % 8 != 0 || !aligned4(table) || !aligned4(ctx) || !aligned4(nodes) || !aligned4(pages) ||
+        !aligned4(kept))
+        return BSF8_ERR_ALIGN;
+    SelectArgs a{};
+    a.q = static_cast<const uint16_t *>(q);
+    a.ldq = ldq;
+    a.ctx = ctx;
+    a.nodes = nodes;
+    a.max_len = max_len;
+    a.keep = keep;
+    a.sink = sink;
+    a.recent = recent;
+    a.width = width;
+    a.pages = pages;
+    a.kept = kept;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    return from_cuda(launch_select(bounds_view(bounds, table, table_pages), a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_sample_tokens(const void *logits, int bf16, int64_t ld, const float *u, const float *temperature,
+                       const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *p, int N, int V,
+                       bsf8_stream_t stream) {
+    const int st = check_sample(logits, ld, bf16, temperature, top_k, top_p, min_p, p, N, V);
+    if (st || N == 0) return st;
+    if (!u || !token) return BSF8_ERR_NULL;
+    if (!aligned4(u) || !aligned4(token)) return BSF8_ERR_ALIGN;
+    SampleArgs a{logits, ld, bf16 ? 1 : 0, temperature, top_p, min_p, u, top_k, token, p, N, V};
+    return from_cuda(launch_sample(a, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_token_probs(const void *logits, int bf16, int64_t ld, const float *temperature, const int32_t *top_k,
+                     const float *top_p, const float *min_p, float *p, int N, int V, bsf8_stream_t stream) {
+    const int st = check_sample(logits, ld, bf16, temperature, top_k, top_p, min_p, p, N, V);
+    if (st || N == 0) return st;
+    if (!aligned16(p)) return BSF8_ERR_ALIGN;
+    SampleArgs a{logits, ld, bf16 ? 1 : 0, temperature, top_p, min_p, nullptr, top_k, nullptr, p, N, V};
+    return from_cuda(launch_sample(a, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int bsf8_residual_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, int fp32, const void *post_weight,
+                       const void *gate, int gate_kind, int64_t ldg, float scale, const void *weight, float eps, void *r_out,
+                       void *h_out, int M, int H, bsf8_stream_t stream) {
+    if (M == 0) return BSF8_OK;
+    if (!x || (!r_out && !h_out) || (h_out && !weight) || (gate_kind != BSF8_GATE_NONE && !gate)) return BSF8_ERR_NULL;
+    if (M < 0 || H < 8 || H % 8 != 0 || H > BSF8_MAX_HIDDEN) return BSF8_ERR_SHAPE;
+    if (gate_kind < BSF8_GATE_NONE || gate_kind > BSF8_GATE_FULL) return BSF8_ERR_VALUE;
+    if (!(eps >= 0.0f) || eps > 3.0e38f || !(scale >= -3.0e38f && scale <= 3.0e38f)) return BSF8_ERR_VALUE;
+    if (ldx < H || (residual && ldr < H) || (gate_kind == BSF8_GATE_FULL && ldg < H) || (gate_kind == BSF8_GATE_TOKEN && ldg < 1))
+        return BSF8_ERR_STRIDE;
+    if (!aligned16(x) || ldx % 8 != 0 || !aligned16(residual) || (residual && ldr % (fp32 ? 4 : 8) != 0) ||
+        !aligned16(post_weight) || !aligned16(weight) || !aligned16(r_out) || !aligned16(h_out))
+        return BSF8_ERR_ALIGN;
+    if ((gate_kind == BSF8_GATE_CHANNEL || gate_kind == BSF8_GATE_FULL) && !aligned16(gate)) return BSF8_ERR_ALIGN;
+    if (gate_kind == BSF8_GATE_FULL && ldg % 8 != 0) return BSF8_ERR_ALIGN;
+    if (gate_kind == BSF8_GATE_TOKEN && (reinterpret_cast<uintptr_t>(gate) & 1u)) return BSF8_ERR_ALIGN;
+    NormArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.residual = residual;
+    a.post = static_cast<const uint16_t *>(post_weight);
+    a.gate = static_cast<const uint16_t *>(gate);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.ldg = ldg;
+    a.fp32 = fp32 ? 1 : 0;
+    a.gate_kind = gate_kind;
+    a.scale = scale;
+    a.eps = eps;
+    a.r_out = r_out;
+    a.h = static_cast<uint16_t *>(h_out);
+    a.M = M;
+    a.H = H;
+    return from_cuda(launch_norm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int bsf8_device_status(int *status, bsf8_stream_t stream) {

@@ -736,6 +736,7 @@ bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len) {
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream) {
     AttendParams prm{};
     prm.c = c;
+    prm.req_pages = c.head_pages ? c.head_pages * c.heads : c.table_pages;
     const int tn = c.dim == 256 ? 64 : 128;
     prm.box_rows = 16;  // the largest power of two that divides a page, up to a tile
     while (prm.box_rows < tn && c.page_size % (2 * prm.box_rows) == 0) prm.box_rows *= 2;

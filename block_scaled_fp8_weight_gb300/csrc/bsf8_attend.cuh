@@ -35,6 +35,7 @@ struct AttendParams {
     CUtensorMap vmap;  // the value codes likewise
     int box_rows;
     CacheView c;
+    long long req_pages;  // table entries from a request's to the next's
     const uint16_t *q;
     long long ldq;
     const int32_t *ctx, *nodes, *mask;
@@ -94,6 +95,11 @@ struct Segment {
 };
 
 __device__ __forceinline__ bool live(const Segment &s) { return s.kv1 > s.kv0; }
+
+// Where the block table of a segment's request (or of its request and head) begins.
+__device__ __forceinline__ size_t table_row(const AttendParams &p, const Segment &s) {
+    return (size_t)(s.b * p.req_pages + s.h * p.c.head_pages);
+}
 
 // The segment at place pos of a block whose share ends at end; not live if none of its tiles are the
 // block's (then none of a later segment's are).
@@ -582,7 +588,7 @@ struct Pages {
     }
     static __device__ __forceinline__ int page_of(const AttendParams &p, const Segment &g, int tile, int lane) {
         const int grp = (tile + lane / NSB) * NSB + lane % NSB;
-        return 16 * grp < g.ctx + g.nodes ? p.c.table[(size_t)g.b * p.c.table_pages + in_page(p, grp)] : -1;
+        return 16 * grp < g.ctx + g.nodes ? p.c.table[table_row(p, g) + in_page(p, grp)] : -1;
     }
     static __device__ __forceinline__ int row_of(const AttendParams &p, const Segment &g, int tile, int page, int lane) {
         const int grp = (tile + lane / NSB) * NSB + lane % NSB;

@@ -115,7 +115,7 @@ struct Batch {
         int *const at = ring + 32 * phase + lane;
         if (16 * grp < g.ctx + g.nodes)
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at)),
-                         "l"(p.c.table + (size_t)g.b * p.c.table_pages + in_page(p, grp))
+                         "l"(p.c.table + table_row(p, g) + in_page(p, grp))
                          : "memory");
         asm volatile("cp.async.commit_group;" ::: "memory");  // exponents asked for later are not waited for in rows()
         phase ^= 1;

@@ -129,6 +129,7 @@ struct CacheView {
     const int32_t *table;
     int pages, page_size, heads, dim;
     int requests, table_pages;
+    long long head_pages;  // table entries from a head's to the next's: 0 where all heads share a row
 };
 
 // bsf8_cache.cu
@@ -176,5 +177,63 @@ struct AttendArgs {
 size_t attend_workspace_bytes(int B, int T, int Hq, int heads, int dim);
 bool attend_fits(const CacheView &c, int B, int T, int Hq, int max_len);
 cudaError_t launch_attend(const CacheView &c, const AttendArgs &a, cudaStream_t stream);
+
+// bsf8_plan.cu
+struct PlanArgs {
+    int32_t *table, *held, *free, *count;
+    const int32_t *lens, *add, *done;
+    int32_t *req, *slot, *start, *granted;
+    int B, table_pages, page_size, pool, N;
+};
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream);
+
+// bsf8_select.cu
+struct BoundsView {
+    int8_t *codes;
+    uint8_t *exps;
+    const int32_t *table;
+    int pages, page_size, heads, dim;
+    int table_pages;
+};
+cudaError_t launch_bounds(const CacheView &c, const BoundsView &v, const int32_t *start, const int32_t *end, int B,
+                          cudaStream_t stream);
+struct SelectArgs {
+    const uint16_t *q;
+    long long ldq;
+    const int32_t *ctx, *nodes;
+    int max_len, keep, sink, recent, width;
+    int32_t *pages, *kept;
+    int B, T, Hq;
+};
+constexpr int kMaxSelectPages = 49152;  // their keys lie in a block's shared memory
+cudaError_t launch_select(const BoundsView &v, const SelectArgs &a, cudaStream_t stream);
+
+// bsf8_sample.cu
+struct SampleArgs {
+    const void *logits;
+    long long ld;
+    int bf16;
+    const float *temperature, *top_p, *min_p, *u;
+    const int32_t *top_k;
+    int32_t *token;
+    float *p;      // of the token, [N], or of all, [N][V]
+    int N, V;
+};
+cudaError_t launch_sample(const SampleArgs &a, bool probs, cudaStream_t stream);
+
+// bsf8_norm.cu
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+struct NormArgs {
+    const uint16_t *x;
+    const void *residual;
+    const uint16_t *post, *gate, *weight;
+    long long ldx, ldr, ldg;
+    int fp32, gate_kind;
+    float scale, eps;
+    void *r_out;
+    uint16_t *h;
+    int M, H;
+};
+cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream);
 
 }  // namespace bsf8

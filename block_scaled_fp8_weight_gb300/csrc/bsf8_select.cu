@@ -1,0 +1,575 @@
+// bsf8_select.cu -- bounds of the cached pages' keys, and the pages of each request and cache head that
+// a query's products with those bounds put first.
+//
+// A page's bounds are its keys' largest and smallest value in each channel, as 8-bit integers under a
+// power of two per 32 channels, so that for any query q
+//     q . k  <=  sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d     for every key k of the page.
+// The score is that sum over all rows that share the cache head (heads of the group, nodes of the
+// tree): with the rows' positive and negative parts added up first, one product of 2 dim terms a page
+// whatever the rows.  Queries and bounds are integers in it and only a page's few block sums are added
+// in fp32, in a fixed order: which pages come first depends on no order of threads.
+#include "bsf8_device.cuh"
+#include "bsf8_internal.h"
+
+#include <algorithm>
+
+namespace bsf8 {
+
+namespace {
+
+constexpr int kBThreads = 256;
+constexpr int kBMax = 1024;  // requests
+
+__device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t bmin2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// 2^(byte - 127), byte 0 .. 254.
+__device__ __forceinline__ float pow2_byte(uint32_t byte) { return __uint_as_float(byte ? byte << 23 : 0x400000u); }
+
+// Requests' page sums: items[b] pages before request b.
+__device__ __forceinline__ int sum_pages(int v, int *wsum, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int up = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, up, m);
+        if (lane >= m) up += o;
+    }
+    if (lane == 31) wsum[warp] = up;
+    __syncthreads();
+    int before = up - v;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kBThreads / 32; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    return before;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------------------------ bounds
+// A warp takes a page of a head: D / 16 lanes a key, 16 channels a lane (one 16-byte load), the keys'
+// values rebuilt to bf16 -- exactly, they have four bits -- and their maxima and minima kept in pairs.
+template <int D>
+__global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, const BoundsView v, const int32_t *start,
+                                                           const int32_t *end, int B, int *status) {
+    __shared__ int s_first[kBMax], s_sum[kBMax + 1], s_w[kBThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int PER = kBMax / kBThreads;
+    {
+        int n[PER], sum = 0;
+        const long long capacity = (long long)v.table_pages * c.page_size;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int b = tid * PER + j;
+            n[j] = 0;
+            if (b < B) {
+                const int from = start ? start[b] : 0, to = end[b];
+                if (from < 0 || to < from || to > capacity) {
+                    if (blockIdx.x == 0) report_index(status);
+                } else {
+                    s_first[b] = from / c.page_size;
+                    n[j] = to / c.page_size - from / c.page_size;
+                }
+            }
+            sum += n[j];
+        }
+        int total;
+        int at = sum_pages(sum, s_w, total);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int b = tid * PER + j;
+            if (b < B) s_sum[b] = at;
+            at += n[j];
+        }
+        if (tid == 0) s_sum[B] = total;
+    }
+    __syncthreads();
+    constexpr int LPR = D / 16, RP = 32 / LPR, EB = D / 32;  // lanes a key, keys a pass
+    const int r = lane / LPR, u = lane % LPR;
+    const int items = s_sum[B];
+    const long long warps = (long long)gridDim.x * (kBThreads / 32), all = (long long)items * c.heads;
+    for (long long it = (long long)blockIdx.x * (kBThreads / 32) + (tid >> 5); it < all; it += warps) {
+        const int pi = (int)(it / c.heads), h = (int)(it - (long long)pi * c.heads);
+        int lo = 0, hi = B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_sum[mid] <= pi) lo = mid;
+            else hi = mid;
+        }
+        const int page = v.table[(size_t)lo * v.table_pages + s_first[lo] + (pi - s_sum[lo])];
+        if ((unsigned)page >= (unsigned)c.pages) {
+            if (lane == 0) report_index(status);
+            continue;
+        }
+        const size_t row0 = ((size_t)page * c.heads + h) * c.page_size;
+        const uint8_t *const codes = c.k8 + (row0 + r) * D + 16 * u;
+        const uint8_t *const exps = c.kexp + (row0 + r) * EB + u / 2;
+        uint32_t mx[8], mn[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = 0xFF80FF80u, mn[i] = 0x7F807F80u;  // -inf, +inf
+        bool nan = false;
+#pragma unroll 4
+        for (int k = 0; k < c.page_size; k += RP) {  // page_size is a multiple of 16, RP of it
+            const uint4 w = *reinterpret_cast<const uint4 *>(codes + (size_t)k * D);
+            const uint32_t e = exps[(size_t)k * EB];
+            nan |= e == 255;
+            const Scale sc = make_scale(e);
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a, b;
+                rebuild4(ws[i], sc, a, b);
+                mx[2 * i] = bmax2(mx[2 * i], a);
+                mn[2 * i] = bmin2(mn[2 * i], a);
+                mx[2 * i + 1] = bmax2(mx[2 * i + 1], b);
+                mn[2 * i + 1] = bmin2(mn[2 * i + 1], b);
+            }
+        }
+#pragma unroll
+        for (int m = LPR; m < 32; m <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mx[i] = bmax2(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], m));
+                mn[i] = bmin2(mn[i], __shfl_xor_sync(0xFFFFFFFFu, mn[i], m));
+            }
+        }
+        // the largest magnitude of the block's 32 channels: this lane's and its neighbour's
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            am = max(am, max((mx[i] << 16) & 0x7FFFFFFFu, mx[i] & 0x7FFF0000u));
+            am = max(am, max((mn[i] << 16) & 0x7FFFFFFFu, mn[i] & 0x7FFF0000u));
+        }
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+        // any of the block's keys marked NaN: lanes of the same block
+        uint32_t marked = __ballot_sync(0xFFFFFFFFu, nan);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < RP; ++k) mine |= marked >> (k * LPR + (u & ~1)) & 3u;
+        // 127 = 1.984375 * 2^6: adding 0x1FFFF carries into the exponent past that mantissa
+        uint32_t e = (uint32_t)max(0, (int)((am + 0x1FFFFu) >> 23) - 6);
+        const bool none = mine != 0 || am >= 0x7F800000u;
+        if (none) e = 255;
+        if (r < 2) {  // the first key's lanes write the maxima, the second's the minima
+            const float inv = none ? 0.0f : __uint_as_float((254u - e) << 23);  // 2^(127 - e)
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t w = r == 0 ? mx[2 * i + j / 2] : mn[2 * i + j / 2];
+                    const float y = (j & 1 ? hi16(w) : lo16(w)) * inv;
+                    const int q = none ? 0 : (int)(r == 0 ? ceilf(y) : floorf(y));
+                    o[i] |= (uint32_t)(q & 255) << (8 * j);
+                }
+            }
+            const size_t at = (size_t)page * v.heads + h;
+            *reinterpret_cast<uint4 *>(v.codes + (at * 2 + r) * D + 16 * u) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (r == 0 && (u & 1) == 0) v.exps[at * EB + u / 2] = (uint8_t)e;
+        }
+    }
+}
+
+cudaError_t launch_bounds(const CacheView &c, const BoundsView &v, const int32_t *start, const int32_t *end, int B,
+                          cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    cudaLaunchConfig_t cfg = {};
+    const long long most = (long long)B * v.table_pages * v.heads;
+    cfg.gridDim = dim3((unsigned)std::min<long long>((most + 7) / 8, 152 * 4), 1, 1);
+    cfg.blockDim = dim3(kBThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = options().pdl ? 1 : 0;
+    switch (c.dim) {
+        case 64: return cudaLaunchKernelEx(&cfg, bounds_kernel<64>, c, v, start, end, B, status);
+        case 128: return cudaLaunchKernelEx(&cfg, bounds_kernel<128>, c, v, start, end, B, status);
+        case 256: return cudaLaunchKernelEx(&cfg, bounds_kernel<256>, c, v, start, end, B, status);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// ------------------------------------------------------------------------------------ selection
+// A cluster of blocks a request and cache head.  Every block adds up the rows' queries (integers: any
+// order), scores its share of the pages and puts their keys -- the scores' bits, ordered as integers --
+// into the first block's shared memory, which then finds the key of rank `keep` by digits of what the
+// keys differ in, and writes the pages before it, ties by their index, in ascending order.
+namespace {
+
+constexpr int kSThreads = 256, kSWarps = kSThreads / 32;
+constexpr int kMaxSCluster = 8;
+constexpr uint32_t kTopKey = 0xFF800000u;  // of +inf
+
+struct SelectShared {
+    int q[2][256];              // sums of the rows' positive and negative parts, then the scaled ones
+    int red[kSWarps];
+    int hist[256];
+    int wsum[2][kSWarps];
+    uint32_t lo, hi;            // smallest and largest key below the top one
+    int top;                    // keys that are the top one
+    uint32_t prefix;
+    int want, digit;
+};
+
+__device__ __forceinline__ int dp4a_ss(uint32_t a, uint32_t b, int c) {
+    int d;
+    asm("dp4a.s32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ int dp4a_su(uint32_t a, uint32_t b, int c) {
+    int d;
+    asm("dp4a.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Larger keys for larger scores; equal ones for 0 and -0.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t b = __float_as_uint(f + 0.0f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, const SelectArgs a, int cluster, int *status) {
+    __shared__ SelectShared s;
+    extern __shared__ uint32_t keys[];
+    pdl_trigger();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % cluster, pair = blockIdx.x / cluster;
+    const int b = pair / v.heads, h = pair - b * v.heads, g = a.Hq / v.heads;
+    const int P = v.page_size;
+    int ctx = a.ctx[b], nodes = a.nodes ? a.nodes[b] : a.T;
+    if (ctx < 0 || nodes < 0 || nodes > a.T || (long long)ctx + nodes > a.max_len) {
+        if (tid == 0 && rank == 0) report_index(status);
+        ctx = max(0, min(ctx, a.max_len));
+        nodes = max(0, min(nodes, min(a.T, a.max_len - ctx)));
+    }
+    const int full = ctx / P, n = min(a.keep, full);
+    const int32_t *const table = v.table + (size_t)b * v.table_pages;
+    int32_t *const out = a.pages + (size_t)pair * a.width;
+    const bool choose = full > a.keep;  // else all of them stay
+    if (cluster > 1) cluster_arrive();  // the first block's memory may be written once it runs
+
+    if (choose) {
+        // ---------------------------------------------------------- the rows' queries
+        constexpr int LPQ = D / 8;  // 16-byte pieces a row
+        const int rows = nodes * g, u = tid % LPQ;
+        auto piece = [&](int r) {
+            const int t = r / g;
+            return *reinterpret_cast<const uint4 *>(a.q + ((size_t)b * a.T + t) * a.ldq + (size_t)(h * g + r - t * g) * D + 8 * u);
+        };
+        for (int i = tid; i < 2 * D; i += kSThreads) s.q[i / D][i % D] = 0;
+        uint32_t am = 0;
+        for (int r = tid / LPQ; r < rows; r += kSThreads / LPQ) {
+            const uint4 w = piece(r);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = x[i] & 0x7FFFu, hi = (x[i] >> 16) & 0x7FFFu;
+                am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+            }
+        }
+        am = __reduce_max_sync(0xFFFFFFFFu, am);
+        if (lane == 0) s.red[warp] = (int)am;
+        __syncthreads();
+        am = 0;
+#pragma unroll
+        for (int w = 0; w < kSWarps; ++w) am = max(am, (uint32_t)s.red[w]);
+        // the largest to [2^17, 2^18); it counts as 2^-100 at least
+        const int k = max((int)(am >> 7) - 127, -100);
+        const float scale = __uint_as_float((uint32_t)(127 + 17 - k) << 23);
+        int up[8] = {}, dn[8] = {};
+        for (int r = tid / LPQ; r < rows; r += kSThreads / LPQ) {
+            const uint4 w = piece(r);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16;
+                const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
+                const int z = finite ? __float2int_rn(__uint_as_float(bits) * scale) : 0;
+                up[i] += max(z, 0);
+                dn[i] += min(z, 0);
+            }
+        }
+#pragma unroll
+        for (int m = LPQ; m < 32; m <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                up[i] += __shfl_xor_sync(0xFFFFFFFFu, up[i], m);
+                dn[i] += __shfl_xor_sync(0xFFFFFFFFu, dn[i], m);
+            }
+        }
+        if (lane < LPQ) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (up[i]) atomicAdd(&s.q[0][8 * u + i], up[i]);
+                if (dn[i]) atomicAdd(&s.q[1][8 * u + i], dn[i]);
+            }
+        }
+        __syncthreads();
+        uint32_t big = 0;
+        for (int i = tid; i < 2 * D; i += kSThreads) big = max(big, (uint32_t)abs(s.q[i / D][i % D]));
+        big = __reduce_max_sync(0xFFFFFFFFu, big);
+        if (lane == 0) s.wsum[0][warp] = (int)big;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSWarps; ++w) big = max(big, (uint32_t)s.wsum[0][w]);
+        const int sh = max(0, 32 - __clz(big) - 14), half = (1 << sh) >> 1;
+        // ---------------------------------------------------------- scores
+        // 2 D codes a page, 16 a lane: the maxima's lanes, then the minima's
+        constexpr int LPP = D / 8, PPW = 32 / LPP, EB = D / 32, HALF = D / 16;
+        const int l = lane % LPP, part = l / HALF, ch = 16 * (l % HALF), blk = ch / 32;
+        uint32_t qh[4], ql[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            qh[i] = ql[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int z = (s.q[part][ch + 4 * i + j] + half) >> sh;  // |z| <= 2^14
+                qh[i] |= (uint32_t)((z >> 8) & 255) << (8 * j);
+                ql[i] |= (uint32_t)(z & 255) << (8 * j);
+            }
+        }
+        if (cluster > 1) cluster_wait();
+        const uint32_t keys0 = cluster > 1 ? map_to_rank(keys, 0) : 0;
+        constexpr int U = 4;  // passes in flight
+        const int chunk = PPW * U;
+        for (int p0 = (rank * kSWarps + warp) * chunk; p0 < full; p0 += cluster * kSWarps * chunk) {
+            uint4 w[U];
+            uint32_t e[U];
+            bool good[U];
+            int page = -1;
+            if (lane < chunk && p0 + lane < full) page = table[p0 + lane];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int at = __shfl_sync(0xFFFFFFFFu, page, PPW * j + lane / LPP);
+                good[j] = (unsigned)at < (unsigned)v.pages;
+                w[j] = make_uint4(0, 0, 0, 0);
+                e[j] = 0;
+                if (good[j]) {
+                    const size_t row = (size_t)at * v.heads + h;
+                    w[j] = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
+                    e[j] = v.exps[row * EB + blk];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int p = p0 + PPW * j + lane / LPP;
+                int sh_ = 0, sl = 0;
+                sh_ = dp4a_ss(w[j].x, qh[0], sh_), sl = dp4a_su(w[j].x, ql[0], sl);
+                sh_ = dp4a_ss(w[j].y, qh[1], sh_), sl = dp4a_su(w[j].y, ql[1], sl);
+                sh_ = dp4a_ss(w[j].z, qh[2], sh_), sl = dp4a_su(w[j].z, ql[2], sl);
+                sh_ = dp4a_ss(w[j].w, qh[3], sh_), sl = dp4a_su(w[j].w, ql[3], sl);
+                int S = sh_ * 256 + sl;
+                S += __shfl_xor_sync(0xFFFFFFFFu, S, 1);
+                S += __shfl_xor_sync(0xFFFFFFFFu, S, HALF);  // |S| < 2^27
+                float f = e[j] == 255 ? INFINITY : __fmul_rn(__fmul_rn((float)S, 7.450580596923828e-9f), pow2_byte(e[j]));
+#pragma unroll
+                for (int m = 2; m < HALF; m <<= 1) f = __fadd_rn(f, __shfl_xor_sync(0xFFFFFFFFu, f, m));
+                if (p < full && l == 0) {
+                    uint32_t key = good[j] ? key_of(f) : 0;
+                    if (p < a.sink || p >= full - a.recent) key = kTopKey;
+                    if (!good[j]) report_index(status);
+                    if (cluster > 1) st_cluster_u32(keys0 + 4 * p, key);
+                    else keys[p] = key;
+                }
+            }
+        }
+    } else if (cluster > 1) {
+        cluster_wait();
+    }
+    if (cluster > 1) cluster_barrier();
+    else __syncthreads();
+    if (rank != 0) return;
+
+    // -------------------------------------------------------------- the pages
+    if (!choose) {
+        for (int p = tid; p < n; p += kSThreads) out[p] = table[p];
+    } else {
+        uint32_t lo = 0xFFFFFFFFu, hi = 0;
+        int top = 0;
+        for (int p = tid; p < full; p += kSThreads) {
+            const uint32_t x = keys[p];
+            if (x >= kTopKey) {
+                ++top;
+            } else {
+                lo = min(lo, x);
+                hi = max(hi, x);
+            }
+        }
+        if (tid == 0) s.lo = 0xFFFFFFFFu, s.hi = 0, s.top = 0;
+        __syncthreads();
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+        top = __reduce_add_sync(0xFFFFFFFFu, top);
+        if (lane == 0) {
+            atomicMin(&s.lo, lo);
+            atomicMax(&s.hi, hi);
+            atomicAdd(&s.top, top);
+        }
+        __syncthreads();
+        // the key of rank n: `equal` of those that have it stay, the first ones
+        uint32_t key;
+        int equal;
+        if (s.top >= n) {
+            key = kTopKey;
+            equal = n;
+        } else {
+            lo = s.lo;
+            const uint32_t range = s.hi - lo;
+            int shift = max(0, 32 - __clz(range) - 8), want = n - s.top;
+            uint32_t base = 0, most = range;  // keys - lo of [base, base + most] are in question
+            while (true) {
+                for (int i = tid; i < 256; i += kSThreads) s.hist[i] = 0;
+                __syncthreads();
+                for (int p = tid; p < full; p += kSThreads) {
+                    const uint32_t x = keys[p];
+                    if (x < kTopKey && x - lo >= base && x - lo - base <= most) atomicAdd(&s.hist[(x - lo - base) >> shift], 1);
+                }
+                __syncthreads();
+                if (warp == 0) {  // bins from the top: a lane takes eight
+                    int c[8], sum = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum += c[i] = s.hist[255 - (8 * lane + i)];
+                    int upto = sum;
+#pragma unroll
+                    for (int m = 1; m < 32; m <<= 1) {
+                        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+                        if (lane >= m) upto += o;
+                    }
+                    int before = upto - sum;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (before < want && before + c[i] >= want) {
+                            s.digit = 255 - (8 * lane + i);
+                            s.want = want - before;
+                        }
+                        before += c[i];
+                    }
+                }
+                __syncthreads();
+                base += (uint32_t)s.digit << shift;
+                want = s.want;
+                if (shift == 0) break;
+                most = (1u << shift) - 1u;
+                shift = max(0, shift - 8);
+            }
+            key = lo + base;
+            equal = want;
+        }
+        // in ascending order: a thread takes a run of pages
+        const int run = ((full + kSThreads - 1) / kSThreads) | 1;  // odd: no two lanes on a bank
+        const int p0 = min(full, tid * run), p1 = min(full, p0 + run);
+        uint32_t c = 0;  // above, equal: 16 bits each
+        for (int p = p0; p < p1; ++p) c += keys[p] > key ? 0x10000u : keys[p] == key ? 1u : 0u;
+        uint32_t upto = c;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+            if (lane >= m) upto += o;
+        }
+        if (lane == 31) s.wsum[1][warp] = (int)upto;
+        __syncthreads();
+        upto -= c;
+        for (int w = 0; w < warp; ++w) upto += (uint32_t)s.wsum[1][w];
+        int above = (int)(upto >> 16), same = (int)(upto & 0xFFFFu);
+        for (int p = p0; p < p1; ++p) {
+            if (keys[p] > key) {
+                out[above++ + min(same, equal)] = table[p];
+            } else if (keys[p] == key) {
+                if (same < equal) out[above + same] = table[p];
+                ++same;
+            }
+        }
+    }
+    // the pages of the tail and of the nodes, then none
+    const int last = (int)(((long long)ctx + nodes + P - 1) / P);
+    for (int i = n + tid; i < a.width; i += kSThreads) {
+        const int p = full + (i - n);
+        out[i] = p < last && p < v.table_pages ? table[p] : -1;
+    }
+    if (h == 0 && tid == 0) a.kept[b] = n * P + (ctx - full * P);
+}
+
+template <int D>
+cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t stream, int *status) {
+    const int most = std::min(v.table_pages, a.max_len / v.page_size);
+    const size_t smem = (size_t)most * 4;
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectPages * 4);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    }
+    // blocks a pair: as many as there are SMs for, each with 128 pages at least
+    const long long pairs = (long long)a.B * v.heads;
+    int cluster = 1;
+    while (cluster < kMaxSCluster && 2 * cluster * pairs <= 304 && most > 128 * cluster) cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pairs * cluster), 1, 1);
+    cfg.blockDim = dim3(kSThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attrs[2];
+    int na = 0;
+    if (options().pdl) {
+        attrs[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attrs[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    if (cluster > 1) {
+        attrs[na].id = cudaLaunchAttributeClusterDimension;
+        attrs[na].val.clusterDim.x = (unsigned)cluster;
+        attrs[na].val.clusterDim.y = 1;
+        attrs[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    cfg.attrs = attrs;
+    cfg.numAttrs = na;
+    return cudaLaunchKernelEx(&cfg, select_kernel<D>, v, a, cluster, status);
+}
+
+cudaError_t launch_select(const BoundsView &v, const SelectArgs &a, cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    switch (v.dim) {
+        case 64: return select_dim<64>(v, a, stream, status);
+        case 128: return select_dim<128>(v, a, stream, status);
+        case 256: return select_dim<256>(v, a, stream, status);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace bsf8

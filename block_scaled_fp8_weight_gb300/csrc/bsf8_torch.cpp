@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cmath>
 #include <exception>
+#include <initializer_list>
 #include <string>
 
 #include "bsf8.h"
@@ -40,6 +41,7 @@ std::string shape_text(const int64_t *s, int n) {
 const char *type_text(at::ScalarType t) {
     switch (t) {
         case at::kByte: return "torch.uint8";
+        case at::kChar: return "torch.int8";
         case at::kInt: return "torch.int32";
         case at::kFloat: return "torch.float32";
         case at::kBFloat16: return "torch.bfloat16";
@@ -280,24 +282,49 @@ PyObject *py_read(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// k8 kexp v8 vexp | q table ctx nodes mask scale max_len out lse workspace
+// q as [B, T, Hq, dim] with rows ld apart.
+int64_t query_rows(Call &c, const at::Tensor &q, int64_t dim) {
+    c.cuda(q, "q");
+    c.type(q, at::kBFloat16, "q");
+    if (q.dim() != 4 || q.size(3) != dim)
+        throw Refused{PyExc_ValueError, "q must be [B, T, Hq, " + std::to_string(dim) + "]"};
+    const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2);
+    const int64_t ldq = T > 1 ? q.stride(1) : B > 1 ? q.stride(0) : Hq * dim;
+    if (q.stride(3) != 1 || (Hq > 1 && q.stride(2) != dim) || (B > 1 && q.stride(0) != T * ldq))
+        throw Refused{PyExc_ValueError, "q must have strides (T * ld, ld, " + std::to_string(dim) + ", 1)"};
+    return ldq;
+}
+
+// An integer argument, `none` for None; what does not fit 31 bits is refused here.
+int whole_number(PyObject *o, long none, const char *name) {
+    long v = none;
+    if (o != Py_None) {
+        v = PyLong_AsLong(o);
+        if (v == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};
+    }
+    if (v > 0x7FFFFFFF || v < -0x7FFFFFFF) throw Refused{PyExc_ValueError, std::string(name) + " must fit 31 bits"};
+    return (int)v;
+}
+
+// k8 kexp v8 vexp | q table ctx nodes mask scale max_len out lse workspace; `sparse`: a table for each head
+template <bool sparse>
 PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 14, [&]() -> PyObject * {
         Call c;
         const bsf8_kv_cache s = cache_of(c, a);
         const at::Tensor &q = tensor(a[4], "q");
-        c.cuda(q, "q");
-        c.type(q, at::kBFloat16, "q");
-        if (q.dim() != 4 || q.size(3) != s.dim)
-            throw Refused{PyExc_ValueError, "q must be [B, T, Hq, " + std::to_string(s.dim) + "]"};
-        const int64_t B = q.size(0), T = q.size(1), Hq = q.size(2);
-        const int64_t ldq = T > 1 ? q.stride(1) : B > 1 ? q.stride(0) : Hq * s.dim;
-        if (q.stride(3) != 1 || (Hq > 1 && q.stride(2) != s.dim) || (B > 1 && q.stride(0) != T * ldq))
-            throw Refused{PyExc_ValueError, "q must have strides (T * ld, ld, " + std::to_string(s.dim) + ", 1)"};
-        const Table t = table_of(c, a[5]);
+        const int64_t ldq = query_rows(c, q, s.dim), B = q.size(0), T = q.size(1), Hq = q.size(2);
+        Table t;
+        if (sparse) {
+            const at::Tensor &x = tensor(a[5], "pages");
+            const int64_t shape[3] = {B, s.heads, x.dim() == 3 ? x.size(2) : -1};
+            t = Table{static_cast<const int32_t *>(c.whole(x, at::kInt, shape, "pages")), (int)B, small(shape[2], "pages")};
+        } else {
+            t = table_of(c, a[5]);
+        }
         if (t.requests != B) throw Refused{PyExc_ValueError, "table must have a row for each request"};
         const int64_t per[1] = {B}, words[3] = {B, T, (T + 31) / 32}, rows[3] = {B, T, Hq}, shape[4] = {B, T, Hq, s.dim};
-        const auto *ctx = static_cast<const int32_t *>(c.whole(a[6], at::kInt, per, "ctx"));
+        const auto *ctx = static_cast<const int32_t *>(c.whole(a[6], at::kInt, per, sparse ? "kept" : "ctx"));
         const auto *nodes = static_cast<const int32_t *>(c.maybe(a[7], at::kInt, per, "nodes"));
         const auto *mask = static_cast<const int32_t *>(c.maybe(a[8], at::kInt, words, "mask"));
         auto *lse = static_cast<float *>(c.maybe(a[12], at::kFloat, rows, "lse"));
@@ -316,18 +343,12 @@ PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
             }
             have = (size_t)ws.numel();
         }
-        long max_len = 0;
-        if (a[10] == Py_None) {
-            max_len = std::min((long)t.pages * s.page_size, (long)BSF8_MAX_LEN);
-        } else {
-            max_len = PyLong_AsLong(a[10]);
-            if (max_len == -1 && PyErr_Occurred()) throw Refused{nullptr, ""};
-        }
-        if (max_len > 0x7FFFFFFF || max_len < -1) throw Refused{PyExc_ValueError, "max_len must fit 31 bits"};
+        const int max_len = whole_number(a[10], std::min((long)t.pages * s.page_size, (long)BSF8_MAX_LEN), "max_len");
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)s.dim) : number(a[9]);
         const int status =
-            bsf8_tree_attention(q.data_ptr(), ldq, &s, t.at, t.pages, ctx, nodes, mask, (float)scale, (int)max_len,
-                                out.data_ptr(), lse, b, tt, hq, need ? ws.data_ptr() : nullptr, have, c.stream());
+            (sparse ? bsf8_sparse_attention : bsf8_tree_attention)(q.data_ptr(), ldq, &s, t.at, t.pages, ctx, nodes, mask,
+                                                                   (float)scale, max_len, out.data_ptr(), lse, b, tt, hq,
+                                                                   need ? ws.data_ptr() : nullptr, have, c.stream());
         if (status) return PyLong_FromLong(status);
         return a[11] != Py_None ? Py_NewRef(a[11]) : THPVariable_Wrap(std::move(out));
     });
@@ -390,14 +411,221 @@ PyObject *py_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// New references to the tensors as a tuple.
+PyObject *tuple_of(std::initializer_list<at::Tensor> tensors) {
+    PyObject *r = PyTuple_New((Py_ssize_t)tensors.size());
+    Py_ssize_t i = 0;
+    for (const at::Tensor &t : tensors) {
+        PyObject *o = r ? THPVariable_Wrap(t) : nullptr;
+        if (!o) {
+            Py_XDECREF(r);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(r, i++, o);
+    }
+    return r;
+}
+
+// table held free count | lens add done page_size tokens
+PyObject *py_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject * {
+        Call c;
+        const Table t = table_of(c, a[0]);
+        const int64_t per[1] = {t.requests}, one[1] = {1}, edges[1] = {t.requests + 1LL};
+        auto *held = static_cast<int32_t *>(c.whole(a[1], at::kInt, per, "held"));
+        const at::Tensor &stack = tensor(a[2], "free");
+        const int64_t pool[1] = {stack.dim() == 1 ? stack.size(0) : -1};
+        auto *free_pages = static_cast<int32_t *>(c.whole(stack, at::kInt, pool, "free"));
+        auto *count = static_cast<int32_t *>(c.whole(a[3], at::kInt, one, "count"));
+        const auto *lens = static_cast<const int32_t *>(c.whole(a[4], at::kInt, per, "lens"));
+        const auto *add = static_cast<const int32_t *>(c.whole(a[5], at::kInt, per, "add"));
+        const auto *done = static_cast<const int32_t *>(c.maybe(a[6], at::kInt, per, "done"));
+        const int page_size = whole_number(a[7], 0, "page_size"), tokens = whole_number(a[8], 0, "tokens");
+        if (tokens < 0) throw Refused{PyExc_ValueError, "tokens must not be negative"};
+        const int64_t rows[1] = {tokens};
+        at::Tensor req = c.fresh(at::kInt, rows), slot = c.fresh(at::kInt, rows), start = c.fresh(at::kInt, edges),
+                   granted = c.fresh(at::kInt, per);
+        auto at32 = [](at::Tensor &x) { return static_cast<int32_t *>(x.data_ptr()); };
+        const int status = bsf8_kv_plan(const_cast<int32_t *>(t.at), t.pages, page_size, held, free_pages, count,
+                                        small(pool[0], "free"), lens, add, done, at32(req), at32(slot), at32(start),
+                                        at32(granted), t.requests, tokens, c.stream());
+        if (status) return PyLong_FromLong(status);
+        return tuple_of({req, slot, start, granted});
+    });
+}
+
+// The bounds' tensors and page size.
+bsf8_page_bounds bounds_of(Call &c, PyObject *codes, PyObject *exps, PyObject *page_size) {
+    const at::Tensor &x = tensor(codes, "codes");
+    if (x.dim() != 4 || x.size(2) != 2) throw Refused{PyExc_ValueError, "codes must be [pages, heads, 2, dim]"};
+    const int64_t shape[4] = {x.size(0), x.size(1), 2, x.size(3)}, bytes[3] = {shape[0], shape[1], shape[3] / 32};
+    bsf8_page_bounds v;
+    v.codes = static_cast<int8_t *>(c.whole(x, at::kChar, shape, "codes"));
+    v.exps = static_cast<uint8_t *>(c.whole(exps, at::kByte, bytes, "exps"));
+    v.pages = small(shape[0], "the bounds' sizes");
+    v.heads = small(shape[1], "the bounds' sizes");
+    v.dim = small(shape[3], "the bounds' sizes");
+    v.page_size = whole_number(page_size, 0, "page_size");
+    return v;
+}
+
+// k8 kexp v8 vexp | codes exps page_size table end start
+PyObject *py_bounds(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 10, [&]() -> PyObject * {
+        Call c;
+        const bsf8_kv_cache s = cache_of(c, a);
+        const bsf8_page_bounds v = bounds_of(c, a[4], a[5], a[6]);
+        const Table t = table_of(c, a[7]);
+        const int64_t per[1] = {t.requests};
+        const auto *end = static_cast<const int32_t *>(c.whole(a[8], at::kInt, per, "end"));
+        const auto *start = static_cast<const int32_t *>(c.maybe(a[9], at::kInt, per, "start"));
+        const int status = bsf8_kv_bounds(&s, &v, t.at, t.pages, start, end, t.requests, c.stream());
+        if (status) return PyLong_FromLong(status);
+        Py_RETURN_NONE;
+    });
+}
+
+// codes exps page_size | q table ctx nodes keep sink recent max_len
+PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 11, [&]() -> PyObject * {
+        Call c;
+        const bsf8_page_bounds v = bounds_of(c, a[0], a[1], a[2]);
+        const at::Tensor &q = tensor(a[3], "q");
+        const int64_t ldq = query_rows(c, q, v.dim), B = q.size(0), T = q.size(1), Hq = q.size(2);
+        const Table t = table_of(c, a[4]);
+        if (t.requests != B) throw Refused{PyExc_ValueError, "table must have a row for each request"};
+        const int64_t per[1] = {B};
+        const auto *ctx = static_cast<const int32_t *>(c.whole(a[5], at::kInt, per, "ctx"));
+        const auto *nodes = static_cast<const int32_t *>(c.maybe(a[6], at::kInt, per, "nodes"));
+        const int keep = whole_number(a[7], 0, "keep"), sink = whole_number(a[8], 0, "sink"),
+                  recent = whole_number(a[9], 0, "recent");
+        const int max_len = whole_number(a[10], std::min((long)t.pages * v.page_size, (long)BSF8_MAX_LEN), "max_len");
+        // (a width of 0 is refused by the library)
+        const int64_t shape[3] = {B, v.heads, bsf8_select_width(small(T, "T"), v.page_size, keep)};
+        at::Tensor pages = c.fresh(at::kInt, shape), kept = c.fresh(at::kInt, per);
+        int32_t none;  // an address for outputs without elements
+        const int status = bsf8_select_pages(q.data_ptr(), ldq, &v, t.at, t.pages, ctx, nodes, max_len, keep, sink, recent,
+                                             shape[2] ? static_cast<int32_t *>(pages.data_ptr()) : &none,
+                                             static_cast<int32_t *>(kept.data_ptr()), small(B, "B"), small(T, "T"),
+                                             small(Hq, "Hq"), c.stream());
+        if (status) return PyLong_FromLong(status);
+        return tuple_of({pages, kept});
+    });
+}
+
+// logits u temperature top_k top_p min_p out; `probs`: no u
+template <bool probs>
+PyObject *py_sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject * {
+        Call c;
+        const at::Tensor &x = tensor(a[0], "logits");
+        c.cuda(x, "logits");
+        if (x.scalar_type() != at::kFloat && x.scalar_type() != at::kBFloat16)
+            throw Refused{PyExc_TypeError, std::string("logits must be torch.float32 or torch.bfloat16, got ") +
+                                               type_text(x.scalar_type())};
+        if (x.dim() != 2 || (x.numel() && x.size(1) > 1 && x.stride(1) != 1))
+            throw Refused{PyExc_ValueError, "logits must be [N, V] with strides (ld, 1)"};
+        const int64_t N = x.size(0), V = x.size(1), ld = N > 1 ? x.stride(0) : V;
+        const int64_t per[1] = {N}, all[2] = {N, V};
+        const auto *t = static_cast<const float *>(c.maybe(a[2], at::kFloat, per, "temperature"));
+        const auto *k = static_cast<const int32_t *>(c.maybe(a[3], at::kInt, per, "top_k"));
+        const auto *tp = static_cast<const float *>(c.maybe(a[4], at::kFloat, per, "top_p"));
+        const auto *mp = static_cast<const float *>(c.maybe(a[5], at::kFloat, per, "min_p"));
+        const int bf16 = x.scalar_type() == at::kBFloat16;
+        if (probs) {
+            at::Tensor p = c.output(a[6], at::kFloat, all, "out");
+            const int status = bsf8_token_probs(x.data_ptr(), bf16, ld, t, k, tp, mp, static_cast<float *>(p.data_ptr()),
+                                                small(N, "N"), small(V, "V"), c.stream());
+            if (status) return PyLong_FromLong(status);
+            return a[6] != Py_None ? Py_NewRef(a[6]) : THPVariable_Wrap(std::move(p));
+        }
+        const auto *u = static_cast<const float *>(c.whole(a[1], at::kFloat, per, "u"));
+        at::Tensor token = c.fresh(at::kInt, per), p = c.fresh(at::kFloat, per);
+        const int status = bsf8_sample_tokens(x.data_ptr(), bf16, ld, u, t, k, tp, mp, static_cast<int32_t *>(token.data_ptr()),
+                                              static_cast<float *>(p.data_ptr()), small(N, "N"), small(V, "V"), c.stream());
+        if (status) return PyLong_FromLong(status);
+        return tuple_of({token, p});
+    });
+}
+
+// x residual weight post_weight gate scale eps out residual_out
+PyObject *py_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 9, [&]() -> PyObject * {
+        Call c;
+        auto rows = [&](const at::Tensor &t, const char *name, int64_t M, int64_t H) -> int64_t {
+            if (t.dim() != 2 || (M >= 0 && (t.size(0) != M || t.size(1) != H)) || (t.numel() && t.size(1) > 1 && t.stride(1) != 1))
+                throw Refused{PyExc_ValueError, std::string(name) + " must be [M, H] with strides (ld, 1)" +
+                                                    (M >= 0 ? ", of x's size" : "")};
+            return t.size(0) > 1 ? t.stride(0) : t.size(1);
+        };
+        const at::Tensor &x = tensor(a[0], "x");
+        c.cuda(x, "x");
+        c.type(x, at::kBFloat16, "x");
+        const int64_t ldx = rows(x, "x", -1, -1), M = x.size(0), H = x.size(1);
+        const int64_t vec[1] = {H}, shape[2] = {M, H};
+        at::ScalarType type = at::kBFloat16;
+        const void *res = nullptr;
+        int64_t ldr = H;
+        if (a[1] != Py_None) {
+            const at::Tensor &r = tensor(a[1], "residual");
+            c.cuda(r, "residual");
+            type = r.scalar_type();
+            if (type != at::kFloat && type != at::kBFloat16)
+                throw Refused{PyExc_TypeError, std::string("residual must be torch.float32 or torch.bfloat16, got ") + type_text(type)};
+            ldr = rows(r, "residual", M, H);
+            res = r.data_ptr();
+        } else if (a[8] != Py_None) {
+            type = tensor(a[8], "residual_out").scalar_type() == at::kFloat ? at::kFloat : at::kBFloat16;
+        }
+        const void *w = c.maybe(a[2], at::kBFloat16, vec, "weight"), *post = c.maybe(a[3], at::kBFloat16, vec, "post_weight");
+        const void *gate = nullptr;
+        int kind = BSF8_GATE_NONE;
+        int64_t ldg = 0;
+        if (a[4] != Py_None) {
+            const at::Tensor &g = tensor(a[4], "gate");
+            c.cuda(g, "gate");
+            c.type(g, at::kBFloat16, "gate");
+            if (g.dim() == 1 && g.size(0) == H) {
+                kind = BSF8_GATE_CHANNEL;
+                if (H > 1 && g.stride(0) != 1) throw Refused{PyExc_ValueError, "gate must be contiguous"};
+            } else if (g.dim() == 2 && g.size(0) == M && g.size(1) == 1) {
+                kind = BSF8_GATE_TOKEN;
+                ldg = M > 1 ? g.stride(0) : 1;
+            } else if (g.dim() == 2) {
+                kind = BSF8_GATE_FULL;
+                ldg = rows(g, "gate", M, H);
+            } else {
+                throw Refused{PyExc_ValueError, "gate must be [H], [M, 1] or [M, H]"};
+            }
+            gate = g.data_ptr();
+        }
+        at::Tensor h, r;
+        if (a[2] != Py_None) h = c.output(a[7], at::kBFloat16, shape, "out");
+        if (a[1] != Py_None || a[8] != Py_None) r = c.output(a[8], type, shape, "residual_out");
+        const int status = bsf8_residual_norm(x.data_ptr(), ldx, res, ldr, type == at::kFloat, post, gate, kind, ldg,
+                                              (float)number(a[5]), w, (float)number(a[6]), r.defined() ? r.data_ptr() : nullptr,
+                                              h.defined() ? h.data_ptr() : nullptr, small(M, "M"), small(H, "H"), c.stream());
+        if (status) return PyLong_FromLong(status);
+        PyObject *ho = !h.defined() ? Py_NewRef(Py_None) : a[7] != Py_None ? Py_NewRef(a[7]) : THPVariable_Wrap(std::move(h));
+        PyObject *ro = !r.defined() ? Py_NewRef(Py_None) : a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(std::move(r));
+        PyObject *both = ho && ro ? PyTuple_Pack(2, ho, ro) : nullptr;
+        Py_XDECREF(ho);
+        Py_XDECREF(ro);
+        return both;
+    });
+}
+
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 
 PyMethodDef methods[] = {method<py_append>("qkv_append"), method<py_read>("kv_read"),
-                         method<py_attention>("tree_attention"), method<py_verify>("verify_tree"),
-                         method<py_commit>("kv_commit"), {nullptr, nullptr, 0, nullptr}};
+                         method<py_attention<false>>("tree_attention"), method<py_verify>("verify_tree"),
+                         method<py_commit>("kv_commit"), method<py_plan>("kv_plan"), method<py_bounds>("kv_bounds"),
+                         method<py_select>("select_pages"), method<py_attention<true>>("sparse_attention"),
+                         method<py_sample<false>>("sample_tokens"), method<py_sample<true>>("token_probs"),
+                         method<py_norm>("residual_norm"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bsf8_torch", "Calls of libbsf8's decode operators from torch tensors.", -1,
                       methods, nullptr, nullptr, nullptr, nullptr};

@@ -182,11 +182,6 @@ __device__ __forceinline__ void step(VerifyShared &s, Walk &w, int n, bool drawn
     }
 }
 
-// Cluster barrier whose lanes need not arrive together.
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
 __global__ void __launch_bounds__(kVThreads, 4) verify_kernel(const VerifyArgs a, int cluster, int *status) {
     __shared__ VerifyShared s;
     pdl_trigger();

@@ -145,3 +145,112 @@ def kv_commit(cache: KVCache, table, ctx, path, count):
     r = _ext.kv_commit(cache.k8, cache.kexp, cache.v8, cache.vexp, table, ctx, path, count)
     if r is not None:
         _check(r, "bsf8_kv_commit")
+
+
+class PageBook:
+    """Which pages each request holds, and which are free: table int32 [B, table_pages], held int32 [B] (a row's
+    first held entries are its pages), free int32 [pages] (a stack) and count int32 [1] (how many lie on
+    it), contiguous CUDA tensors that kv_plan keeps (PageBook.empty allocates them)."""
+
+    __slots__ = ("table", "held", "free", "count")
+
+    def __init__(self, table, held, free, count):
+        self.table, self.held, self.free, self.count = table, held, free, count
+
+    @classmethod
+    def empty(cls, requests: int, table_pages: int, pages: int, device="cuda"):
+        """Books in which all of a cache's pages are free."""
+        torch = _torch()
+        z = lambda *s: torch.zeros(s, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(z(requests, table_pages), z(requests), torch.arange(pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), pages, dtype=torch.int32, device=device))
+
+
+def kv_plan(book: PageBook, lens, add, *, page_size: int, tokens: int, done=None):
+    """Pages and slots of a step: rows of book with done != 0 (int32 [B]) give their pages back, then request b,
+    lens[b] tokens long, gets pages for add[b] more (int32 [B] each) while they last, at most `tokens` in all.
+    Returns (req, slot, start, granted): int32 [tokens], [tokens], [B + 1], [B] -- each granted token's request and
+    slot (behind them 0 and -1, which qkv_append does not keep), where each request's begin, how many it got."""
+    r = _ext.kv_plan(book.table, book.held, book.free, book.count, lens, add, done, page_size, tokens)
+    if type(r) is int:
+        _check(r, "bsf8_kv_plan")
+    return r
+
+
+class PageBounds:
+    """Bounds of a layer's keys, page by page: codes int8 [pages, heads, 2, dim] (largest, smallest) and exponent
+    bytes exps uint8 [pages, heads, dim / 32], contiguous CUDA tensors that the caller owns."""
+
+    __slots__ = ("codes", "exps", "page_size")
+
+    def __init__(self, codes, exps, page_size: int):
+        self.codes, self.exps, self.page_size = codes, exps, page_size
+
+    @classmethod
+    def empty(cls, cache: KVCache):
+        """Bounds for a cache; undefined until kv_bounds writes a page's."""
+        torch = _torch()
+        pages, heads, size, dim = cache.k8.shape
+        return cls(torch.empty((pages, heads, 2, dim), dtype=torch.int8, device=cache.k8.device),
+                   torch.empty((pages, heads, dim // 32), dtype=torch.uint8, device=cache.k8.device), size)
+
+
+def kv_bounds(cache: KVCache, bounds: PageBounds, table, end, *, start=None):
+    """Writes the bounds of the pages that became full while request b grew from start[b] (None: 0) to end[b]
+    tokens (int32 [B]): after a prompt, and after each commit."""
+    r = _ext.kv_bounds(cache.k8, cache.kexp, cache.v8, cache.vexp, bounds.codes, bounds.exps, bounds.page_size, table, end,
+                       start)
+    if r is not None:
+        _check(r, "bsf8_kv_bounds")
+
+
+def select_pages(q, bounds: PageBounds, table, ctx, keep: int, *, nodes=None, sink: int = 0, recent: int = 0, max_len=None):
+    """The pages of each request and cache head that attention reads: of the full ones the `keep` whose bounds
+    promise most for q (bf16 [B, T, Hq, D], as tree_attention takes it), the first `sink` and the last `recent` always
+    among them, then the pages of the context's rest and of the nodes.  Returns (pages int32 [B, heads, width],
+    kept int32 [B]: the context's tokens in them), for sparse_attention."""
+    r = _ext.select_pages(bounds.codes, bounds.exps, bounds.page_size, q, table, ctx, nodes, keep, sink, recent, max_len)
+    if type(r) is int:
+        _check(r, "bsf8_select_pages")
+    return r
+
+
+def sparse_attention(q, cache: KVCache, pages, kept, *, nodes=None, mask=None, scale=None, max_len=None, out=None, lse=None,
+                     workspace=None):
+    """tree_attention over the pages that select_pages chose: pages int32 [B, heads, width] and kept int32 [B] in
+    the place of table and ctx."""
+    r = _ext.sparse_attention(cache.k8, cache.kexp, cache.v8, cache.vexp, q, pages, kept, nodes, mask, scale, max_len,
+                              out, lse, workspace)
+    if type(r) is int:
+        _check(r, "bsf8_sparse_attention")
+    return r
+
+
+def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None):
+    """A token of each row of logits (fp32 or bf16 [N, V]) by u (fp32 [N], uniform): temperature, top_p and min_p
+    fp32 [N], top_k int32 [N], None for no such limit (temperature 0: the best one).  Returns (token int32 [N],
+    p fp32 [N]: its probability among those that stay); -1 and 0 for a row without a finite or +inf logit."""
+    r = _ext.sample_tokens(logits, u, temperature, top_k, top_p, min_p, None)
+    if type(r) is int:
+        _check(r, "bsf8_sample_tokens")
+    return r
+
+
+def token_probs(logits, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+    """The distributions that sample_tokens draws from, fp32 [N, V]: what verify_tree takes as p and q."""
+    r = _ext.token_probs(logits, None, temperature, top_k, top_p, min_p, out)
+    if type(r) is int:
+        _check(r, "bsf8_token_probs")
+    return r
+
+
+def residual_norm(x, residual, weight, *, post_weight=None, gate=None, scale: float = 1.0, eps: float = 1e-6, out=None,
+                  residual_out=None):
+    """From one block to the next: x (bf16 [M, H]) normed by post_weight (bf16 [H]; None: as it is), times scale and
+    gate (bf16 [H], [M, 1] or [M, H]), is added to residual (bf16 or fp32 [M, H]; None: 0), and the sum normed by
+    weight (bf16 [H]; None: not).  Returns (h bf16 [M, H] or None, the sum in the residual's type, or None without a
+    residual and residual_out).  residual_out may be residual, out may be x."""
+    r = _ext.residual_norm(x, residual, weight, post_weight, gate, scale, eps, out, residual_out)
+    if type(r) is int:
+        _check(r, "bsf8_residual_norm")
+    return r

@@ -442,6 +442,145 @@ int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_p
                    const int32_t *ctx, const int32_t *path, const int32_t *count, int B, int T,
                    bsf8_stream_t stream);
 
+/* Plans a step: whose pages come back, which pages the new tokens get, where each token goes.  The books
+ * of the pages live on the device, and the call keeps them:
+ *   table       int32 [B][table_pages]: row b's first held[b] entries are its pages
+ *   held        int32 [B]
+ *   free_pages  int32 [pool]: a stack of free pages, the first *free_count of them
+ *   free_count  int32 [1]
+ * In this order, the requests from the first to the last each time:
+ *   - where done[b] is not 0 (done NULL: nowhere) the row's pages go back onto the stack, entry by entry, and
+ *     held[b] becomes 0;
+ *   - a request with lens[b] tokens and add[b] > 0 new ones needs max(0, ceil((lens + add) / page_size) - held)
+ *     pages.  It is granted its tokens where that is 0 or where the pages needed by it and all requests
+ *     before it are on the stack, and where the tokens asked for by it and those before it are at most N.
+ *     What is granted pages takes them from the top of the stack, one after another.
+ * Then the granted tokens lie one after another, request by request:
+ *   req, slot   int32 [N], out: token i's request and its slot, lens[b] onwards; behind the last one 0 and -1
+ *               (rows that bsf8_qkv_append does not keep)
+ *   start       int32 [B + 1], out: where each request's tokens begin; start[B] is how many there are
+ *   granted     int32 [B], out: add[b] or 0
+ * lens, add and done are int32 [B] and stay as they are (lens grows by what is kept of the step: the
+ * caller's).  Table entries past a row's pages and the stack above its count keep what they held.
+ * A row with lens or add below 0, or past table_pages * page_size together, counts as add 0; held outside
+ * 0 .. table_pages, a count outside 0 .. pool and pages that the stack has no room for are cut off
+ * (BSF8_ERR_INDEX in the device status, each).
+ *   B  1 .. 1024;  N  0 .. 2^30;  pool  1 .. 2^30;  page_size as in the cache;  table_pages * page_size and
+ *   table_pages * B below 2^31;  none of the arrays may overlap.
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_CUDA. */
+int bsf8_kv_plan(int32_t *table, int table_pages, int page_size, int32_t *held, int32_t *free_pages,
+                 int32_t *free_count, int pool, const int32_t *lens, const int32_t *add, const int32_t *done,
+                 int32_t *req, int32_t *slot, int32_t *start, int32_t *granted, int B, int N,
+                 bsf8_stream_t stream);
+
+/* Bounds of the pages' keys, for bsf8_select_pages: per page, head and channel the largest (hi) and
+ * smallest (lo) key as 8-bit integers under one power of two per 32 channels, byte e + 127:
+ * the smallest e >= -127 with 127 * 2^e >= every |hi|, |lo| of the 32, codes ceil(hi / 2^e) and
+ * floor(lo / 2^e).  Byte 255 and codes 0 where a key's 32 channels are marked NaN (byte 255) or infinite.
+ *   codes  device, int8 [pages][heads][2][dim] (hi, lo), 16-byte aligned
+ *   exps   device, uint8 [pages][heads][dim / 32]
+ * The sizes are the cache's. */
+typedef struct {
+    int8_t *codes;
+    uint8_t *exps;
+    int pages, page_size, heads, dim;
+} bsf8_page_bounds;
+
+/* Writes the bounds of the pages that became full: of request b the pages with their last slot in
+ * [start[b], end[b]), that is pages start / page_size .. end / page_size - 1 (int32 [B], start NULL: 0).  After a
+ * prompt or a commit: its requests' lengths before and after.  Values are taken as bf16, which they are
+ * exactly (below 2^-126 rounded to its grid).  A start below 0, an end below it or past the table: none of that
+ * request's; a bad page: not that one (BSF8_ERR_INDEX).  The same page may be given twice.
+ *   table  device, int32 [B][table_pages];  B  1 .. 1024;  B * table_pages below 2^31
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE (bounds of other sizes than the cache's among it), BSF8_ERR_ALIGN,
+ *         BSF8_ERR_CUDA. */
+int bsf8_kv_bounds(const bsf8_kv_cache *cache, const bsf8_page_bounds *bounds, const int32_t *table,
+                   int table_pages, const int32_t *start, const int32_t *end, int B, bsf8_stream_t stream);
+
+/* The pages that attention of a step reads, for each request and cache head: of the request's
+ * ctx / page_size full pages the `keep` with the highest scores (all where there are fewer), equal ones by
+ * their index, in ascending order; then the pages that hold the rest of the context and the nodes.
+ * The score is an upper bound of the sum of q . k over the query rows that share the cache head (its
+ * nodes[b] nodes, Hq / heads heads each), but for the roundings of q:
+ *   a    = the rows' largest |q| (elements that are infinite or NaN count as 0), 2^k <= a < 2^(k+1), k >= -100
+ *   Q+_d = sum over the rows of max(n, 0),  Q-_d = sum of min(n, 0),  n = rint(q_d * 2^(17 - k))
+ *   both (Q + 2^(s-1)) >> s, s >= 0 the smallest that leaves the largest |Q| 14 bits (s = 0: as they are)
+ *   score = sum over 32-channel blocks, added in pairs (fp32), of fp32(sum_d Q+_d hi_d + Q-_d lo_d) 2^(e - 27)
+ * and +inf for a page with a byte 255, for the first `sink` pages and the last `recent` full ones.
+ *   q       as in bsf8_tree_attention;  ctx, nodes, max_len too
+ *   bounds  of every full page of the requests
+ *   pages   device, out, int32 [B][heads][width], width = bsf8_select_width(T, page_size, keep): page numbers
+ *           (the table's entries), -1 behind the last one
+ *   kept    device, out, int32 [B]: tokens of the context in them, keep * page_size + ctx % page_size at most
+ * With these, bsf8_sparse_attention finds context and nodes as bsf8_tree_attention does.
+ *   keep  1 .. BSF8_MAX_SELECT_PAGES;  sink, recent >= 0, together at most keep;  max_len / page_size at most
+ *   BSF8_MAX_SELECT_PAGES;  T * Hq / heads at most 4096;  B  1 .. 1024
+ * A page number outside the bounds scores lowest of all (BSF8_ERR_INDEX); lengths as in bsf8_tree_attention.
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_VALUE, BSF8_ERR_CUDA. */
+#define BSF8_MAX_SELECT_PAGES 49152
+int bsf8_select_pages(const void *q, int64_t ldq, const bsf8_page_bounds *bounds, const int32_t *table,
+                      int table_pages, const int32_t *ctx, const int32_t *nodes, int max_len, int keep,
+                      int sink, int recent, int32_t *pages, int32_t *kept, int B, int T, int Hq,
+                      bsf8_stream_t stream);
+
+/* keep plus the most pages that the rest of a context and T nodes take; 0 for invalid arguments. */
+int bsf8_select_width(int T, int page_size, int keep);
+
+/* bsf8_tree_attention over a block table for each request and cache head, as bsf8_select_pages gives it:
+ * pages int32 [B][heads][width] in table's place, kept [B] in ctx's, the rest as there (its workspace
+ * too; max_len at most width * page_size, at least kept + nodes of every request).
+ * Errors: as bsf8_tree_attention. */
+int bsf8_sparse_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache, const int32_t *pages,
+                          int width, const int32_t *kept, const int32_t *nodes, const int32_t *mask,
+                          float scale, int max_len, void *out, float *lse, int B, int T, int Hq,
+                          void *workspace, size_t workspace_bytes, bsf8_stream_t stream);
+
+/* A token from each row of logits.  With m the row's largest logit and t its temperature, a logit x weighs
+ *   w = 2^40 for x = m, else floor(2^40 * 2^-y) for y = (m - x) * (log2(e) / t) <= 40, 0 beyond
+ * (fp32 steps, each rounded; 2^-y by a polynomial to 2^-22 of itself; -inf and NaN weigh 0).  t <= 0 or NaN:
+ * only the lowest index of x = m weighs.  Of these stay, in this order,
+ *   top_k   the first k by (larger x, then lower index);  k <= 0 or >= V: all
+ *   min_p   those with w >= ceil(min_p * 2^40);  NaN counts as 0, above 1 as 1
+ *   top_p   in the same order, those before which less than max(1, floor(floor(p * 2^24) * W / 2^24)) has been
+ *           given, W the sum of w by then;  p >= 1 or NaN: all;  p < 0 counts as 0
+ * and the token is the lowest x with  w(0) + .. + w(x) > floor(floor(u * 2^24) * W / 2^24) over those that
+ * stay, W their sum.  All sums are of integers: the result depends on no order.
+ *   logits  device, bf16 (bf16 != 0) or fp32, row n at element n * ld, 16-byte aligned, ld >= V
+ *   u       device, fp32 [N], uniform in [0, 1)
+ *   temperature, top_p, min_p  device, fp32 [N], top_k int32 [N]; NULL: 1, all, none, all
+ *   token   device, out, int32 [N]; -1 for a row of nothing but -inf and NaN
+ *   p       device, out, fp32 [N]: the token's share w / W (0 for token -1), off by at most 2^-22 of itself
+ *   N  0 .. 2^20;  V  1 .. 2^20
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_CUDA. */
+int bsf8_sample_tokens(const void *logits, int bf16, int64_t ld, const float *u, const float *temperature,
+                       const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *p,
+                       int N, int V, bsf8_stream_t stream);
+
+/* The distributions that bsf8_sample_tokens draws from: p[n][x] = w / W of those that stay, 0 of the others
+ * (as bsf8_verify_tree takes p and q).  p device, out, fp32 [N][V], 16-byte aligned.  Else as there. */
+int bsf8_token_probs(const void *logits, int bf16, int64_t ld, const float *temperature, const int32_t *top_k,
+                     const float *top_p, const float *min_p, float *p, int N, int V, bsf8_stream_t stream);
+
+/* From one block to the next: per row of H channels, in fp32,
+ *   z = x * rsqrt(mean(x^2) + eps) * post_weight     (post_weight NULL: z = x)
+ *   r = residual + scale * gate * z                  (residual NULL: 0;  no gate: 1)
+ *   h = r * rsqrt(mean(r^2) + eps) * weight          (of r before its rounding)
+ *   x            device, bf16 [M][ldx];  post_weight, weight  device, bf16 [H]
+ *   residual     device, [M][ldr], fp32 where fp32 != 0, else bf16
+ *   gate         device, bf16: BSF8_GATE_CHANNEL [H], BSF8_GATE_TOKEN one of each row at gate[m * ldg],
+ *                BSF8_GATE_FULL [M][ldg]
+ *   r_out        device, out, [M][H] of the residual's type, or NULL; may be the residual itself (ldr = H)
+ *   h_out        device, out, bf16 [M][H], or NULL (then weight is not read); may be x itself (ldx = H)
+ * Pointers 16-byte aligned (a token gate's: 2), ldx, ldg (full) and ldr multiples of 16 bytes.
+ *   H  8 .. BSF8_MAX_HIDDEN, a multiple of 8;  eps >= 0, scale finite
+ * Errors: BSF8_ERR_NULL, BSF8_ERR_SHAPE, BSF8_ERR_ALIGN, BSF8_ERR_STRIDE, BSF8_ERR_VALUE, BSF8_ERR_CUDA. */
+#define BSF8_MAX_HIDDEN 32768
+enum { BSF8_GATE_NONE = 0, BSF8_GATE_CHANNEL = 1, BSF8_GATE_TOKEN = 2, BSF8_GATE_FULL = 3 };
+int bsf8_residual_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, int fp32,
+                       const void *post_weight, const void *gate, int gate_kind, int64_t ldg, float scale,
+                       const void *weight, float eps, void *r_out, void *h_out, int M, int H,
+                       bsf8_stream_t stream);
+
 /* ------------------------------------------------------------------ diagnostics
  * Not part of the method: a measurement aid.  Launches 2*nsm one-warp blocks on `stream`;
  * the block on SM i writes out[2i] = the global nanosecond timer and out[2i+1] = SM i's
