@@ -176,7 +176,9 @@ __global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, co
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t w = r == 0 ? mx[2 * i + j / 2] : mn[2 * i + j / 2];
-                    const float y = (j & 1 ? hi16(w) : lo16(w)) * inv;
+                    const float x = j & 1 ? hi16(w) : lo16(w);
+                    float y = x * inv;
+                    if (y == 0.0f) y = x;  // too small a part for fp32: as far from 0 as its sign says
                     const int q = none ? 0 : (int)(r == 0 ? ceilf(y) : floorf(y));
                     o[i] |= (uint32_t)(q & 255) << (8 * j);
                 }
