@@ -5,9 +5,18 @@
 // log2(e) / t, and every sum is of these: which tokens stay and which one is drawn depends on no order of
 // threads and on no split of the row.
 //
-// A cluster of blocks a row; a block takes a contiguous slice of it, a warp a contiguous part of that.
-// The order that top-k and top-p go by (larger logits first, then the lower index) is that of the bits of
-// d = max - x >= 0, whose digits a histogram at a time narrows down: counts for top-k, weights for top-p.
+// A cluster of blocks a row; a block takes a contiguous slice of it, a warp a contiguous part of that.  The
+// slice is read once, for the row's largest logit, and kept in shared memory for what follows (rows too
+// long for that are read again, from L2).  Then, by what the row asks for:
+//   - the best one: the lowest index that has the largest logit;
+//   - top-k: the k-th largest of the threads' own largest logits is at most the k-th largest of all, so that
+//     little more than k elements reach it; the first block sorts those, and all that follows (min-p,
+//     top-p, the draw) is done on them;
+//   - top-p alone: the weights go into a histogram by y in sixteenths of an octave, the bin in which the sum
+//     reaches the share is sorted, the elements before it stay;
+//   - neither: the weights are added up as they lie.
+// Where more elements than the sort takes are alike (or k is larger than that), the digits of
+// d = max - x >= 0 are narrowed down by one histogram after another instead.
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
@@ -20,31 +29,44 @@ namespace {
 typedef unsigned long long u64;
 constexpr int kTThreads = 512, kTWarps = kTThreads / 32;
 constexpr int kMaxTCluster = 8;
-constexpr u64 kWhole = 1ull << 40;
-constexpr int kBins = 1024;
+constexpr int kBins = 1024;      // of the digits' histograms
+constexpr int kOctaves = 16 * 41;  // of the histogram by y: y <= 40 in sixteenths
+constexpr int kList = 2048;      // elements that the first block sorts
+constexpr int kStage = 72 * 1024;  // bytes of a slice that are kept: two blocks an SM
 constexpr uint32_t kInfBits = 0x7F800000u;
-static_assert(kBins == 2 * kTThreads, "two bins a thread");
+static_assert(kBins == 2 * kTThreads && kList == 4 * kTThreads, "bins and elements a thread");
 
 struct TokenShared {
-    float wmax[kTWarps], bmax;      // bmax, bsum, bmin: read by the cluster
-    int wmin[kTWarps], bmin;
+    float tmax[kTThreads];          // the threads' largest logits
+    float wmax[kTWarps], bmax;      // bmax, bsum, bmin ..: read by the cluster
+    int bmin;
     u64 wsum[kTWarps], bsum;
     int wcount[kTWarps], bcount;
-    uint32_t count[kBins];          // a histogram: elements, their weights' low 12 bits and the rest
-    uint32_t low[kBins];
-    u64 high[kBins];
     u64 tsum[kTWarps];
     int tcount[kTWarps];
+    int tally[32];                  // counts of the search for the k-th
     int bin;                        // the bin in which the wanted rank or weight lies,
     int before;                     // and what is before it
     u64 mass;
-    u64 at;                         // the draw, inside a warp's part
-    int warp;
+    u64 all;
     int cut;
+    int listed;                     // elements in list
+    u64 cut_key, total;             // of the first block: what stays, its sum
+    u64 list[kList];                // this block's elements: bits of d, index
+    union {
+        u64 sort[kList];
+        struct {
+            uint32_t low[kOctaves], high[kOctaves];  // the weights' (as integers of 24 bits) low 12 bits and the rest
+        } y;
+        struct {
+            uint32_t count[kBins], low[kBins];
+            u64 high[kBins];
+        };
+    };
 };
 
 // 2^-f on [0, 1): a polynomial fitted to it (least squares, weighted towards the largest relative error,
-// 2^-22), every step rounded by itself so that any machine gets the same bits.
+// 2^-22), every step rounded by itself so that any machine gets the same bits.  It stays in [1/2, 1].
 __device__ __forceinline__ float exp2_of(float f) {
     float p = -0.0009449035860598087f;
     p = __fadd_rn(__fmul_rn(p, f), 0.00920579768717289f);
@@ -54,13 +76,72 @@ __device__ __forceinline__ float exp2_of(float f) {
     return __fadd_rn(__fmul_rn(p, f), 1.0f);
 }
 
-// The weight at distance d = max - x >= 0; `rate` is log2(e) / t, infinite for the largest alone.
+// The weight at distance d = max - x >= 0; `rate` is log2(e) / t.
 __device__ __forceinline__ u64 weight(float d, float rate) {
-    const float y = d == 0.0f ? 0.0f : __fmul_rn(d, rate);
+    const float y = __fmul_rn(d, rate);
     if (!(y <= 40.0f)) return 0;
     const float n = floorf(y);
     const uint32_t m = (uint32_t)(exp2_of(__fsub_rn(y, n)) * 16777216.0f);  // 2^23 .. 2^24
     return ((u64)m << 16) >> (int)n;
+}
+
+// The same for two elements at a time, without conversions: adding 2^23 towards zero leaves floor(y) in the
+// low bits, and a p in [1/2, 1] is its own bits less those of 1/4 (in units of 2^-24).
+struct Two {
+    float y[2];
+    uint32_t n[2], m[2];  // w = (m << 16) >> n where y <= 40
+};
+
+__device__ __forceinline__ u64 two(float a, float b) {
+    u64 x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    return x;
+}
+__device__ __forceinline__ void apart(u64 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+// a * b; `zero` is a pair of -0 that comes to the kernel as an argument: the assembler turns a product and
+// a sum of pairs into one fma, .rn or not, unless it cannot know that this is a product.
+__device__ __forceinline__ u64 mul2(u64 a, u64 b, u64 zero) {
+    u64 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(zero));
+    return d;
+}
+__device__ __forceinline__ u64 sum2(u64 a, u64 b) {
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 sum2_rz(u64 a, u64 b) {
+    u64 d;
+    asm("add.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 less2(u64 a, u64 b) {  // a - b, rounded once
+    u64 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(b), "l"(two(-1.0f, -1.0f)), "l"(a));
+    return d;
+}
+
+__device__ __forceinline__ Two weights2(float a, float b, u64 top, u64 rate, u64 zero) {
+    Two r;
+    const u64 y = mul2(less2(top, two(a, b)), rate, zero);
+    const u64 big = two(8388608.0f, 8388608.0f);
+    const u64 t = sum2_rz(y, big);
+    const u64 f = less2(y, sum2(t, two(-8388608.0f, -8388608.0f)));
+    u64 p = two(-0.0009449035860598087f, -0.0009449035860598087f);
+    p = sum2(mul2(p, f, zero), two(0.00920579768717289f, 0.00920579768717289f));
+    p = sum2(mul2(p, f, zero), two(-0.0552973598241806f, -0.0552973598241806f));
+    p = sum2(mul2(p, f, zero), two(0.2401801496744156f, 0.2401801496744156f));
+    p = sum2(mul2(p, f, zero), two(-0.6931437253952026f, -0.6931437253952026f));
+    p = sum2(mul2(p, f, zero), two(1.0f, 1.0f));
+    float p0, p1, t0, t1;
+    apart(y, r.y[0], r.y[1]);
+    apart(p, p0, p1);
+    apart(t, t0, t1);
+    r.n[0] = __float_as_uint(t0) & 63u;
+    r.n[1] = __float_as_uint(t1) & 63u;
+    r.m[0] = __float_as_uint(p0) - 0x3E800000u;
+    r.m[1] = __float_as_uint(p1) - 0x3E800000u;
+    return r;
 }
 
 __device__ __forceinline__ u64 part_of(u64 u, u64 z) {  // floor(u z / 2^24)
@@ -79,19 +160,32 @@ __device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr) {
     return v;
 }
 
+// Larger for larger values.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t b = __float_as_uint(f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// A group of 16 bytes: its elements, NaN as -inf.
 template <typename T>
 struct Logit;
 template <>
 struct Logit<float> {
     static constexpr int N = 4;
+    static constexpr uint32_t kNone = 0xFF800000u;  // -inf, as a word of elements
     static __device__ __forceinline__ void unpack(const uint4 &w, float (&y)[4]) {
         y[0] = __uint_as_float(w.x), y[1] = __uint_as_float(w.y), y[2] = __uint_as_float(w.z), y[3] = __uint_as_float(w.w);
     }
-    static __device__ __forceinline__ float one(const float *p) { return *p; }
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) { return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY)); }
+    static __device__ __forceinline__ void set(uint4 &w, int i, const float *p) {
+        (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w) = __float_as_uint(*p);
+    }
 };
 template <>
 struct Logit<uint16_t> {
     static constexpr int N = 8;
+    static constexpr uint32_t kNone = 0xFF80FF80u;
     static __device__ __forceinline__ void unpack(const uint4 &w, float (&y)[8]) {
         const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -100,14 +194,75 @@ struct Logit<uint16_t> {
             y[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
         }
     }
-    static __device__ __forceinline__ float one(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
+    static __device__ __forceinline__ uint32_t clean(uint32_t w) {
+        uint32_t d;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(kNone));
+        return d;
+    }
+    static __device__ __forceinline__ void set(uint4 &w, int i, const uint16_t *p) {
+        uint32_t &a = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+        a = i & 1 ? (a & 0xFFFFu) | (uint32_t)*p << 16 : (a & 0xFFFF0000u) | *p;
+    }
 };
+
+// The sums over the threads before this one, and over all; a barrier inside (and one before the next call).
+__device__ __forceinline__ u64 sum_before(u64 v, TokenShared &s, u64 &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 up = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const u64 o = __shfl_up_sync(0xFFFFFFFFu, up, m);
+        if (lane >= m) up += o;
+    }
+    if (lane == 31) s.tsum[warp] = up;
+    __syncthreads();
+    u64 before = up - v;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kTWarps; ++w) {
+        if (w < warp) before += s.tsum[w];
+        all += s.tsum[w];
+    }
+    return before;
+}
+
+// Sorts s.sort[0 .. n), all different, by the whole block: by counting how many are smaller up to 256 of them (several
+// threads each), else in a bitonic network.  Ends with a barrier; what lies behind is undefined.
+__device__ __forceinline__ void sort_list(TokenShared &s, int n) {
+    const int tid = threadIdx.x;
+    int size = 32;
+    while (size < n) size *= 2;
+    if (size <= 256) {
+        const int each = kTThreads / size, i = tid / each, part = tid % each;  // threads an element: 2 .. 16
+        const u64 mine = i < n ? s.sort[i] : ~0ull;
+        int rank = 0;
+        for (int j = part; j < n; j += each) rank += s.sort[j] < mine ? 1 : 0;
+        for (int m = 1; m < each; m <<= 1) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, m);
+        __syncthreads();
+        if (i < n && part == 0) s.sort[rank] = mine;
+        __syncthreads();
+        return;
+    }
+    for (int i = n + tid; i < size; i += kTThreads) s.sort[i] = ~0ull;
+    __syncthreads();
+    for (int block = 2; block <= size; block *= 2)
+        for (int step = block / 2; step > 0; step /= 2) {
+            for (int i = tid; i < size / 2; i += kTThreads) {
+                const int a = (i / step) * 2 * step + i % step, b = a + step;
+                const u64 x = s.sort[a], y = s.sort[b];
+                if ((x > y) == ((a & block) == 0)) s.sort[a] = y, s.sort[b] = x;
+            }
+            __syncthreads();
+        }
+}
 
 }  // namespace
 
 template <typename T, bool PROBS>
-__global__ void __launch_bounds__(kTThreads) sample_kernel(const SampleArgs a, int cluster) {
-    __shared__ TokenShared s;
+__global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
+    extern __shared__ __align__(16) uint8_t memory[];
+    TokenShared &s = *reinterpret_cast<TokenShared *>(memory);
+    uint4 *const stage = reinterpret_cast<uint4 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16);
     pdl_trigger();
     pdl_wait();
     using L = Logit<T>;
@@ -118,67 +273,407 @@ __global__ void __launch_bounds__(kTThreads) sample_kernel(const SampleArgs a, i
     // groups of VEC elements that start on 16 bytes; the first and last may be partly outside the row
     const int mis = (int)(((size_t)row * a.ld) % VEC), groups = (V + mis + VEC - 1) / VEC;
     const int per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 31) / 32 * 32;
-    const int g0 = min(groups, (rank * kTWarps + warp) * per_warp), g1 = min(groups, g0 + per_warp);
+    const int b0 = rank * kTWarps * per_warp;  // the block's first group
+    const int g0 = min(groups, b0 + warp * per_warp), g1 = min(groups, g0 + per_warp);
     const float tp = a.temperature ? a.temperature[row] : 1.0f;
-    const bool greedy = !(tp > 0.0f);
-    const float rate = greedy ? INFINITY : __fdiv_rn(1.4426950408889634f, tp);
+    const bool greedy = !(tp >= 1.17549435e-38f);  // a temperature below fp32's normal numbers counts as 0
+    const float rate = greedy ? 1.0f : __fdiv_rn(1.4426950408889634f, tp);
     int k = a.top_k ? a.top_k[row] : 0;
     if (k <= 0 || k > V) k = V;
-    if (greedy) k = 1;
     const float mp = a.min_p ? fminf(fmaxf(a.min_p[row], 0.0f), 1.0f) : 0.0f;
     const u64 least = max((u64)1, (u64)ceilf(mp * 1099511627776.0f));
     const float pp = a.top_p ? a.top_p[row] : 1.0f;
     const bool nucleus = pp < 1.0f;
     const u64 pfix = nucleus ? (u64)(fmaxf(pp, 0.0f) * 16777216.0f) : 0;
+    const float u = PROBS ? 0.0f : a.u[row];
+    float *const out = PROBS ? a.p + (size_t)row * V : nullptr;
 
-    // elements of group g: outside the row, and NaN, as -inf
-    auto load = [&](int g, float (&y)[VEC]) {
+    // group g from the caller's memory: elements outside the row, and NaN, as -inf
+    auto fetch = [&](int g) -> uint4 {
         const int e = g * VEC - mis;
+        uint4 w;
         if (e >= 0 && e + VEC <= V) {
-            L::unpack(*reinterpret_cast<const uint4 *>(x + e), y);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) y[i] = fmaxf(y[i], -INFINITY);  // NaN becomes -inf
+            w = *reinterpret_cast<const uint4 *>(x + e);
         } else {
+            w = make_uint4(L::kNone, L::kNone, L::kNone, L::kNone);
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                y[i] = (unsigned)(e + i) < (unsigned)V ? fmaxf(L::one(x + e + i), -INFINITY) : -INFINITY;
+                if ((unsigned)(e + i) < (unsigned)V) L::set(w, i, x + e + i);
         }
+        return make_uint4(L::clean(w.x), L::clean(w.y), L::clean(w.z), L::clean(w.w));
     };
+    auto load = [&](int g, float (&y)[VEC]) { L::unpack(staged ? stage[g - b0] : fetch(g), y); };
     auto barrier = [&]() {
         if (cluster > 1) cluster_barrier();
         else __syncthreads();
     };
+    auto of32 = [&](const void *p, int c) { return cluster > 1 ? ld_cluster32(map_to_rank(p, c)) : *static_cast<const uint32_t *>(p); };
+    auto of64 = [&](const void *p, int c) { return cluster > 1 ? ld_cluster64(map_to_rank(p, c)) : *static_cast<const u64 *>(p); };
 
     // ---------------------------------------------------------------- the largest
     float top = -INFINITY;
-    for (int g = g0 + lane; g < g1; g += 32) {
-        float y[VEC];
-        load(g, y);
+    {
+        constexpr int U = 4;  // loads in flight
+        int g = g0 + lane;
+        for (; g + 32 * (U - 1) < g1; g += 32 * U) {
+            uint4 w[U];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) top = fmaxf(top, y[i]);
+            for (int j = 0; j < U; ++j) w[j] = fetch(g + 32 * j);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (staged) stage[g + 32 * j - b0] = w[j];
+                float y[VEC];
+                L::unpack(w[j], y);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) top = fmaxf(top, y[i]);
+            }
+        }
+        for (; g < g1; g += 32) {
+            const uint4 w = fetch(g);
+            if (staged) stage[g - b0] = w;
+            float y[VEC];
+            L::unpack(w, y);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) top = fmaxf(top, y[i]);
+        }
     }
+    s.tmax[tid] = top;
+    float wtop = top;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    if (lane == 0) s.wmax[warp] = top;
+    for (int m = 16; m > 0; m >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
+    if (lane == 0) s.wmax[warp] = wtop;
+    if (tid == 0) s.listed = 0, s.bmin = 0x7FFFFFFF;
+    if (tid < 32) s.tally[tid] = 0;
     __syncthreads();
-    if (tid == 0) {
-        float v = -INFINITY;
-        for (int w = 0; w < kTWarps; ++w) v = fmaxf(v, s.wmax[w]);
-        s.bmax = v;
+    if (warp == 0) {
+        wtop = lane < kTWarps ? s.wmax[lane] : -INFINITY;
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
+        if (lane == 0) s.bmax = wtop;
     }
     barrier();
-    top = -INFINITY;
-    for (int c = 0; c < cluster; ++c)
-        top = fmaxf(top, cluster > 1 ? __uint_as_float(ld_cluster32(map_to_rank(&s.bmax, c))) : s.bmax);
-
+    const float mine = top;  // this thread's own
+    top = lane < cluster ? __uint_as_float(of32(&s.bmax, lane)) : -INFINITY;
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     const bool none = top == -INFINITY;
+
+    // p of the row's elements from their weights; 0 where nothing stays
+    float inv = 0.0f;
+    auto share = [&](u64 w) { return fmaf((float)(uint32_t)(w >> 20), 1048576.0f, (float)(uint32_t)(w & 0xFFFFFu)) * inv; };
+    auto zeros = [&]() {  // of this block's slice of the distribution
+        const int from = max(0, b0 * VEC - mis), to = min(V, (b0 + kTWarps * per_warp) * VEC - mis);
+        float *const o = out + from;
+        const int n = to - from, head = min(max(n, 0), (int)((16 - (reinterpret_cast<uintptr_t>(o) & 15)) & 15) / 4);
+        if (tid < head) o[tid] = 0.0f;
+        for (int i = head + 4 * tid; i + 4 <= n; i += 4 * kTThreads) *reinterpret_cast<float4 *>(o + i) = make_float4(0, 0, 0, 0);
+        const int tail = head + max(n - head, 0) / 4 * 4;
+        if (tail + tid < n) o[tail + tid] = 0.0f;
+    };
+
+    if (none || greedy) {
+        // ------------------------------------------------------------ the best one, or none
+        if (!none && mine == top) {
+            int at = 0x7FFFFFFF;
+            for (int g = g0 + lane; g < g1 && at == 0x7FFFFFFF; g += 32) {
+                float y[VEC];
+                load(g, y);
+#pragma unroll
+                for (int i = VEC - 1; i >= 0; --i)
+                    if (y[i] == top) at = g * VEC - mis + i;
+            }
+            atomicMin(&s.bmin, at);
+        }
+        if (PROBS) zeros();
+        barrier();
+        if (rank == 0 && warp == 0) {
+            int at = lane < cluster ? (int)of32(&s.bmin, lane) : 0x7FFFFFFF;
+            at = __reduce_min_sync(0xFFFFFFFFu, at);
+            if (lane == 0) {
+                if (PROBS) {
+                    if (!none) out[at] = 1.0f;
+                } else {
+                    a.token[row] = none ? -1 : at;
+                    a.p[row] = none ? 0.0f : 1.0f;
+                }
+            }
+        }
+        if (cluster > 1) cluster_barrier();  // no block leaves while another may read its memory
+        return;
+    }
+
     // the distance of an element, as bits that order as it does; infinite where it has no part
-    auto distance = [&](float v) { return v == top ? (none ? INFINITY : 0.0f) : __fsub_rn(top, v); };
+    auto distance = [&](float v) { return v == top ? 0.0f : __fsub_rn(top, v); };
+    auto key_at = [&](float v, int index) { return (u64)__float_as_uint(distance(v)) << 20 | (u64)index; };
+    auto keep_in_list = [&](float v, int index) {
+        const u64 key = key_at(v, index);
+        if (key >> 20 >= kInfBits) return;
+        const int at = atomicAdd(&s.listed, 1);
+        if (at < kList) s.list[at] = key;
+    };
+    // the blocks' lists, in the first one's `sort`: how many; barriers on the way (none where they are too long)
+    auto collect = [&]() {
+        int n = 0, from = 0, count = 0;
+        for (int c = 0; c < cluster; ++c) {
+            const int m = (int)of32(&s.listed, c);
+            n += m;
+        }
+        if (n > kList || rank > 0) return n;
+        for (int c = 0; c < cluster; ++c) {
+            count = (int)of32(&s.listed, c);
+            for (int i = tid; i < count; i += kTThreads) s.sort[from + i] = of64(&s.list[i], c);
+            from += count;
+        }
+        __syncthreads();
+        return n;
+    };
+    const u64 top2 = two(top, top), rate2 = two(rate, rate), zero2 = two(minus_zero, minus_zero);
+    // what the sort finds to stay: elements up to cut_key in the order of (bits of d, index)
+    u64 cut_key = ~0ull;
+    bool by_list = false;   // all that stays is in the first block's sorted list
+    int bin_cut = kOctaves;  // of the histogram by y: the elements of lower bins stay, of this one those up to cut_key
+    bool done = false;      // the cut is found
 
-    // What stays: elements below `cut` in the order of (bits of d, index), with weight `least` at least.
-    uint32_t cut_bits = kInfBits;    // those below it,
+    // ---------------------------------------------------------------- top-k by a few candidates
+    const bool few = V <= kList && (k < V || nucleus);
+    const int g8 = 64 * cluster, gt = kTThreads * cluster;  // maxima of eight threads, of one
+    if (top < INFINITY && (few || 3 * k <= gt)) {
+        float least_value = -INFINITY;
+        if (!few) {
+            // the k-th largest of them, to 20 bits of their order; at most eight a thread
+            uint32_t v[kMaxTCluster];
+            int nv = 1;
+            if (3 * k <= g8) {
+                float m8 = -INFINITY;
+                if (tid < g8) {
+                    const float *const from = s.tmax + 8 * (tid % 64);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) m8 = fmaxf(m8, __uint_as_float(of32(from + i, tid / 64)));
+                }
+                v[0] = order_of(m8);
+            } else {
+                nv = cluster;
+#pragma unroll
+                for (int c = 0; c < kMaxTCluster; ++c) v[c] = c < cluster ? order_of(__uint_as_float(of32(&s.tmax[tid], c))) : 0u;
+            }
+            uint32_t t = 0;
+            int turn = 0;
+            for (int bit = 31; bit >= 12; --bit, ++turn) {
+                const uint32_t want = t | 1u << bit;
+                int n;
+                if (nv == 1) {
+                    n = __syncthreads_count(v[0] >= want);
+                } else {
+                    int c = 0;
+#pragma unroll
+                    for (int i = 0; i < kMaxTCluster; ++i) c += v[i] >= want ? 1 : 0;
+                    c = __reduce_add_sync(0xFFFFFFFFu, c);
+                    if (lane == 0) atomicAdd(&s.tally[turn], c);
+                    __syncthreads();
+                    n = s.tally[turn];
+                }
+                if (n >= k) t = want;
+            }
+            least_value = value_of(t);
+            if (!(least_value >= -INFINITY)) least_value = -INFINITY;  // (no such number)
+        }
+        for (int g = g0 + lane; g < g1; g += 32) {
+            float y[VEC];
+            load(g, y);
+            float m = y[0];
+#pragma unroll
+            for (int i = 1; i < VEC; ++i) m = fmaxf(m, y[i]);
+            if (m >= least_value) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (y[i] >= least_value) keep_in_list(y[i], g * VEC - mis + i);
+            }
+        }
+        if (PROBS) zeros();
+        barrier();
+        const int n = collect();
+        if (n <= kList) {
+            by_list = done = true;
+            if (rank == 0) {
+                sort_list(s, n);
+                // four a thread, in order: weights, what min-p and top-p leave of the first k
+                u64 w[4], key[4], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * tid + i;
+                    key[i] = at < min(n, k) ? s.sort[at] : ~0ull;
+                    w[i] = at < min(n, k) ? weight(__uint_as_float((uint32_t)(key[i] >> 20)), rate) : 0;
+                    if (w[i] < least) w[i] = 0;
+                    sum += w[i];
+                }
+                u64 all, before = sum_before(sum, s, all);
+                const u64 cut = max((u64)1, part_of(pfix, all));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const u64 mine_ = w[i];
+                    if (nucleus && before >= cut) w[i] = 0;
+                    before += mine_;
+                }
+                __syncthreads();
+                // their sum, and how many they are
+                u64 total, stay;
+                (void)sum_before(w[0] + w[1] + w[2] + w[3], s, total);
+                __syncthreads();
+                const int ones = (w[0] ? 1 : 0) + (w[1] ? 1 : 0) + (w[2] ? 1 : 0) + (w[3] ? 1 : 0);
+                u64 place = sum_before((u64)ones, s, stay);
+                inv = total ? 1.0f / (float)total : 0.0f;
+                if (PROBS) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (w[i]) out[(int)(key[i] & 0xFFFFFu)] = share(w[i]);
+                } else {
+                    // the draw goes by their index
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (w[i]) s.sort[place++] = (key[i] & 0xFFFFFu) << 41 | w[i];
+                    __syncthreads();
+                    sort_list(s, (int)stay);
+                    u64 q[4];
+                    sum = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        q[i] = 4 * tid + i < (int)stay ? s.sort[4 * tid + i] : 0;
+                        sum += q[i] & ((1ull << 41) - 1);
+                    }
+                    before = sum_before(sum, s, all);
+                    const u64 at = part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), total);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const u64 wi = q[i] & ((1ull << 41) - 1);
+                        if (at >= before && at < before + wi) {
+                            a.token[row] = (int)(q[i] >> 41);
+                            a.p[row] = share(wi);
+                        }
+                        before += wi;
+                    }
+                }
+            }
+            if (cluster > 1) cluster_barrier();  // no block leaves while another may read its memory
+            return;
+        }
+        barrier();  // the lists are begun again
+        if (tid == 0) s.listed = 0;
+        __syncthreads();
+    }
+
+    // ---------------------------------------------------------------- top-p by the histogram of y
+    if (!done && nucleus && k == V && top < INFINITY) {
+        for (int i = tid; i < kOctaves; i += kTThreads) s.y.low[i] = s.y.high[i] = 0;
+        __syncthreads();
+        for (int g = g0 + lane; g < g1; g += 32) {
+            float y[VEC];
+            load(g, y);
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) {
+                const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!(w.y[j] <= 40.0f) || ((u64)w.m[j] << 16) >> w.n[j] < least) continue;
+                    const int bin = (int)(__float_as_uint(__fadd_rz(w.y[j] * 16.0f, 8388608.0f)) & 1023u);
+                    const uint32_t v = w.n[j] > 16 ? w.m[j] >> (w.n[j] - 16) : w.m[j];
+                    atomicAdd(&s.y.low[bin], v & 0xFFFu);
+                    atomicAdd(&s.y.high[bin], v >> 12);
+                }
+            }
+        }
+        barrier();
+        u64 mass[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int bin = 2 * tid + j;
+            u64 lo = 0, hi = 0;
+            if (bin < kOctaves)
+                for (int c = 0; c < cluster; ++c) {
+                    lo += of32(&s.y.low[bin], c);
+                    hi += of32(&s.y.high[bin], c);
+                }
+            mass[j] = (lo + (hi << 12)) << (bin < 256 ? 16 - (bin >> 4) : 0);
+        }
+        u64 all, before = sum_before(mass[0] + mass[1], s, all);
+        const u64 cut = max((u64)1, part_of(pfix, all));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (before < cut && before + mass[j] >= cut) {
+                s.bin = 2 * tid + j;
+                s.mass = before;
+            }
+            before += mass[j];
+        }
+        barrier();  // (the histograms are read)
+        bin_cut = s.bin;
+        const u64 below = s.mass;
+        // that bin's elements; the others' sums, a warp's part each
+        u64 sum = 0;
+        const float from = (float)bin_cut * 0.0625f, to = (float)(bin_cut + 1) * 0.0625f;
+        for (int g = g0 + lane; g < g1; g += 32) {
+            float y[VEC];
+            load(g, y);
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) {
+                const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!(w.y[j] < to) || !(w.y[j] <= 40.0f)) continue;
+                    const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
+                    if (wj < least) continue;
+                    if (w.y[j] < from) sum += wj;
+                    else keep_in_list(y[i + j], g * VEC - mis + i + j);
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+        if (lane == 0) s.wsum[warp] = sum;
+        barrier();
+        const int n = collect();
+        if (n <= kList) {
+            done = true;
+            if (rank == 0) {
+                sort_list(s, n);
+                u64 w[4], here = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = 4 * tid + i;
+                    w[i] = at < n ? weight(__uint_as_float((uint32_t)(s.sort[at] >> 20)), rate) : 0;
+                    here += w[i];
+                }
+                u64 total, run = below + sum_before(here, s, total);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (run < cut && run + w[i] >= cut) {
+                        s.cut_key = s.sort[4 * tid + i];
+                        s.total = run + w[i];
+                    }
+                    run += w[i];
+                }
+            }
+            barrier();
+            cut_key = of64(&s.cut_key, 0);
+            inv = 1.0f / (float)of64(&s.total, 0);
+            if (!PROBS) {
+                // this block's share of them, into the sums of the warps whose part they lie in
+                for (int i = tid; i < s.listed; i += kTThreads) {
+                    const u64 key = s.list[i];
+                    if (key > cut_key) continue;
+                    const int g = ((int)(key & 0xFFFFFu) + mis) / VEC;
+                    atomicAdd(&s.wsum[(g - b0) / per_warp], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
+                }
+                __syncthreads();
+            }
+        } else {
+            bin_cut = kOctaves;
+            barrier();
+        }
+    }
+
+    // ---------------------------------------------------------------- by digits, where there are too many alike
+    uint32_t cut_bits = kInfBits;    // elements with bits of d below it stay,
     int cut_index = -1;              // and of those that equal it the ones up to this index
-
     // Narrows the cut down to the element in which the running count (or weight) reaches `want`: of those inside
     // the present cut.  Returns how many stay of those that equal the new cut's bits.
     auto narrow = [&](bool by_weight, u64 want_in, bool fraction) {
@@ -352,94 +847,132 @@ __global__ void __launch_bounds__(kTThreads) sample_kernel(const SampleArgs a, i
         barrier();  // s.cut is written again
     };
 
-    if (!none) {
+    if (!done) {
         if (k < V) narrow(false, (u64)k, false);
-        if (nucleus && !greedy) narrow(true, pfix, true);
+        if (nucleus) narrow(true, pfix, true);
+        if (k < V || nucleus) cut_key = ((u64)cut_bits << 20) + (u64)(long long)cut_index;
     }
 
     // ---------------------------------------------------------------- what stays, in order of index
     auto kept = [&](float v, int index) -> u64 {
         const float d = distance(v);
         const uint32_t bits = __float_as_uint(d);
-        if (bits >= kInfBits || bits > cut_bits || (bits == cut_bits && index > cut_index)) return 0;
+        if (bits >= kInfBits) return 0;
+        if (cut_key != ~0ull) {
+            const u64 key = (u64)bits << 20 | (u64)index;
+            if (key > cut_key) return 0;
+        }
         const u64 w = weight(d, rate);
         return w >= least ? w : 0;
     };
-    u64 sum = 0;
-    for (int g = g0 + lane; g < g1; g += 32) {
-        float y[VEC];
-        load(g, y);
+    const bool summed = bin_cut < kOctaves;  // the warps' sums are there
+    if (!summed) {
+        u64 sum = 0;
+        if (cut_key == ~0ull && top < INFINITY) {  // nothing is cut off
+            for (int g = g0 + lane; g < g1; g += 32) {
+                float y[VEC];
+                load(g, y);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum += kept(y[i], g * VEC - mis + i);
-    }
+                for (int i = 0; i < VEC; i += 2) {
+                    const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-    if (lane == 0) s.wsum[warp] = sum;
-    __syncthreads();
-    if (tid == 0) {
-        u64 v = 0;
-        for (int w = 0; w < kTWarps; ++w) v += s.wsum[w];
-        s.bsum = v;
-    }
-    barrier();
-    u64 total = 0, first = 0;
-    for (int c = 0; c < cluster; ++c) {
-        const u64 v = cluster > 1 ? ld_cluster64(map_to_rank(&s.bsum, c)) : s.bsum;
-        if (c < rank) first += v;
-        total += v;
-    }
-    const float inv = total ? 1.0f / (float)total : 0.0f;
-    auto share = [&](u64 w) { return fmaf((float)(uint32_t)(w >> 20), 1048576.0f, (float)(uint32_t)(w & 0xFFFFFu)) * inv; };
-
-    if constexpr (PROBS) {
-        float *const out = a.p + (size_t)row * V;
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC];
-            load(g, y);
-            const int e = g * VEC - mis;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if ((unsigned)(e + i) < (unsigned)V) out[e + i] = share(kept(y[i], e + i));
-        }
-    } else {
-        if (total == 0) {
-            if (rank == 0 && tid == 0) {
-                a.token[row] = -1;
-                a.p[row] = 0.0f;
+                    for (int j = 0; j < 2; ++j) {
+                        const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
+                        if (w.y[j] <= 40.0f && wj >= least) sum += wj;
+                    }
+                }
             }
         } else {
-            const float u = a.u[row];
-            const u64 at = part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), total);
-            u64 before = first;
-            for (int w = 0; w < warp; ++w) before += s.wsum[w];
-            if (at >= before && at < before + sum) {  // this warp's part has it
-                for (int gb = g0; gb < g1; gb += 32) {
-                    const int g = gb + lane;
-                    float y[VEC];
+            for (int g = g0 + lane; g < g1; g += 32) {
+                float y[VEC];
+                load(g, y);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) y[i] = -INFINITY;
-                    if (g < g1) load(g, y);
-                    u64 w[VEC], mine = 0;
+                for (int i = 0; i < VEC; ++i) sum += kept(y[i], g * VEC - mis + i);
+            }
+        }
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) mine += w[i] = kept(y[i], g * VEC - mis + i);
-                    u64 upto = mine;
+        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+        if (lane == 0) s.wsum[warp] = sum;
+        __syncthreads();
+    }
+    u64 total = 0, first = 0;
+    if (!(PROBS && summed)) {
+        if (warp == 0) {
+            u64 v = lane < kTWarps ? s.wsum[lane] : 0;
 #pragma unroll
-                    for (int m = 1; m < 32; m <<= 1) {
-                        const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
-                        if (lane >= m) upto += o;
+            for (int m = 8; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+            if (lane == 0) s.bsum = v;
+        }
+        barrier();
+        for (int c = 0; c < cluster; ++c) {
+            const u64 v = of64(&s.bsum, c);
+            if (c < rank) first += v;
+            total += v;
+        }
+        inv = 1.0f / (float)total;
+    }
+
+    if constexpr (PROBS) {
+        for (int g = g0 + lane; g < g1; g += 32) {
+            float y[VEC], p[VEC];
+            load(g, y);
+            const int e = g * VEC - mis;
+            if (top < INFINITY && (cut_key == ~0ull || summed)) {
+#pragma unroll
+                for (int i = 0; i < VEC; i += 2) {
+                    const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
+                        const bool in = w.y[j] <= 40.0f && wj >= least && (!summed || key_at(y[i + j], e + i + j) <= cut_key);
+                        p[i + j] = in ? share(wj) : 0.0f;
                     }
-                    u64 r = before + upto - mine;
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        if (at >= r && at < r + w[i]) {
-                            a.token[row] = g * VEC - mis + i;
-                            a.p[row] = share(w[i]);
-                        }
-                        r += w[i];
-                    }
-                    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-                    if (before > at) break;
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) p[i] = share(kept(y[i], e + i));
+            }
+            if (e >= 0 && e + VEC <= V && (reinterpret_cast<uintptr_t>(out + e) & 15) == 0) {
+#pragma unroll
+                for (int i = 0; i < VEC; i += 4)
+                    *reinterpret_cast<float4 *>(out + e + i) = make_float4(p[i], p[i + 1], p[i + 2], p[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if ((unsigned)(e + i) < (unsigned)V) out[e + i] = p[i];
+            }
+        }
+    } else {
+        const u64 at = part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), total);
+        u64 before = first;
+        for (int w = 0; w < warp; ++w) before += s.wsum[w];
+        if (at >= before && at < before + s.wsum[warp]) {  // this warp's part has it
+            for (int gb = g0; gb < g1; gb += 32) {
+                const int g = gb + lane;
+                float y[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) y[i] = -INFINITY;
+                if (g < g1) load(g, y);
+                u64 w[VEC], own = 0;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) own += w[i] = kept(y[i], g * VEC - mis + i);
+                u64 upto = own;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+                    if (lane >= m) upto += o;
+                }
+                u64 r = before + upto - own;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    if (at >= r && at < r + w[i]) {
+                        a.token[row] = g * VEC - mis + i;
+                        a.p[row] = share(w[i]);
+                    }
+                    r += w[i];
+                }
+                before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+                if (before > at) break;
             }
         }
     }
@@ -450,9 +983,27 @@ template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     int cluster = 1;
     while (cluster < kMaxTCluster && a.V > 4096 * cluster) cluster *= 2;
+    // a block's slice, as the kernel cuts it (one group more where rows do not start on 16 bytes)
+    const long long groups = a.V / (16 / sizeof(T)) + 2;
+    const long long per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 31) / 32 * 32;
+    const int slice = (int)std::min<long long>(per_warp * kTWarps * 16, kStage + 1);
+    const int staged = slice <= kStage;
+    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0);
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(sample_kernel<T, PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(TokenShared) + 16 + kStage);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * cluster), 1, 1);
     cfg.blockDim = dim3(kTThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     int na = 0;
@@ -470,7 +1021,7 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     }
     cfg.attrs = attrs;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, sample_kernel<T, PROBS>, a, cluster);
+    return cudaLaunchKernelEx(&cfg, sample_kernel<T, PROBS>, a, cluster, staged, -0.0f);
 }
 
 cudaError_t launch_sample(const SampleArgs &a, bool probs, cudaStream_t stream) {

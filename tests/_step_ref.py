@@ -141,7 +141,7 @@ def kept(x, t=1.0, k=0, tp=1.0, mp=0.0):
     v = w[order]
     if k <= 0 or k > len(x):
         k = len(x)
-    if not t > 0:
+    if not t >= 2.0 ** -126:
         k = 1
     v[k:] = 0
     least = max(1, math.ceil((min(max(float(F(mp)), 0.0), 1.0) if mp == mp else 0.0) * ONE))
