@@ -38,13 +38,14 @@ static_assert(kBins == 2 * kTThreads && kList == 4 * kTThreads, "bins and elemen
 
 struct TokenShared {
     float tmax[kTThreads];          // the threads' largest logits
-    float wmax[kTWarps], bmax;      // bmax, bsum, bmin ..: read by the cluster
+    float wmax[kTWarps], wlow[kTWarps], bmax;      // bmax, bsum, bmin ..: read by the cluster
     int bmin;
     u64 wsum[kTWarps], bsum;
     int wcount[kTWarps], bcount;
     u64 tsum[kTWarps];
     int tcount[kTWarps];
-    int tally[32];                  // counts of the search for the k-th
+    float max8[kTThreads / 8];      // largest logits of eight threads
+    float blow;                     // the smallest of the threads' largest ones, -inf left out
     int bin;                        // the bin in which the wanted rank or weight lies,
     int before;                     // and what is before it
     u64 mass;
@@ -55,6 +56,7 @@ struct TokenShared {
     u64 list[kList];                // this block's elements: bits of d, index
     union {
         u64 sort[kList];
+        int tally[kList];           // counts of the search for the k-th
         struct {
             uint32_t low[kOctaves], high[kOctaves];  // the weights' (as integers of 24 bits) low 12 bits and the rest
         } y;
@@ -177,6 +179,7 @@ struct Logit<float> {
     static __device__ __forceinline__ void unpack(const uint4 &w, float (&y)[4]) {
         y[0] = __uint_as_float(w.x), y[1] = __uint_as_float(w.y), y[2] = __uint_as_float(w.z), y[3] = __uint_as_float(w.w);
     }
+    static __device__ __forceinline__ float one(const float *p) { return *p; }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) { return __float_as_uint(fmaxf(__uint_as_float(w), -INFINITY)); }
     static __device__ __forceinline__ void set(uint4 &w, int i, const float *p) {
         (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w) = __float_as_uint(*p);
@@ -194,6 +197,7 @@ struct Logit<uint16_t> {
             y[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
         }
     }
+    static __device__ __forceinline__ float one(const uint16_t *p) { return __uint_as_float((uint32_t)*p << 16); }
     static __device__ __forceinline__ uint32_t clean(uint32_t w) {
         uint32_t d;
         asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(kNone));
@@ -243,17 +247,50 @@ __device__ __forceinline__ void sort_list(TokenShared &s, int n) {
         __syncthreads();
         return;
     }
-    for (int i = n + tid; i < size; i += kTThreads) s.sort[i] = ~0ull;
-    __syncthreads();
+    // Places tid, tid + 512, ..: partners up to 16 apart are lanes of a warp, from 512 apart a thread's own.
+    constexpr int R = kList / kTThreads;
+    u64 v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = tid + r * kTThreads < n ? s.sort[tid + r * kTThreads] : ~0ull;
     for (int block = 2; block <= size; block *= 2)
         for (int step = block / 2; step > 0; step /= 2) {
-            for (int i = tid; i < size / 2; i += kTThreads) {
-                const int a = (i / step) * 2 * step + i % step, b = a + step;
-                const u64 x = s.sort[a], y = s.sort[b];
-                if ((x > y) == ((a & block) == 0)) s.sort[a] = y, s.sort[b] = x;
+            if (step >= kTThreads) {
+                auto swap = [&](u64 &x, u64 &y, int at) {
+                    const bool turn = (x > y) == ((at & block) == 0);
+                    const u64 z = turn ? y : x;
+                    y = turn ? x : y;
+                    x = z;
+                };
+                if (step == kTThreads) {
+                    swap(v[0], v[1], tid);
+                    swap(v[2], v[3], tid + 2 * kTThreads);
+                } else {
+                    swap(v[0], v[2], tid);
+                    swap(v[1], v[3], tid + kTThreads);
+                }
+                continue;
             }
-            __syncthreads();
+            if (step >= 32) {
+                __syncthreads();
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (r * kTThreads < size) s.sort[tid + r * kTThreads] = v[r];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (r * kTThreads >= size) break;
+                const int at = tid + r * kTThreads;
+                const u64 y = step >= 32 ? s.sort[at ^ step] : __shfl_xor_sync(0xFFFFFFFFu, v[r], step);
+                const bool smaller = ((at & block) == 0) == ((at & step) == 0);  // this place takes the smaller one
+                v[r] = (y < v[r]) == smaller ? y : v[r];
+            }
         }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (r * kTThreads < size) s.sort[tid + r * kTThreads] = v[r];
+    __syncthreads();
 }
 
 }  // namespace
@@ -338,29 +375,42 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         }
     }
     s.tmax[tid] = top;
-    float wtop = top;
+    float wtop = top, wlow = top > -INFINITY ? top : INFINITY;  // of those that have any
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
-    if (lane == 0) s.wmax[warp] = wtop;
+    for (int m = 1; m < 32; m <<= 1) {
+        wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
+        wlow = fminf(wlow, __shfl_xor_sync(0xFFFFFFFFu, wlow, m));
+        if (m == 4 && (lane & 7) == 0) s.max8[tid >> 3] = wtop;
+    }
+    if (lane == 0) s.wmax[warp] = wtop, s.wlow[warp] = wlow;
     if (tid == 0) s.listed = 0, s.bmin = 0x7FFFFFFF;
-    if (tid < 32) s.tally[tid] = 0;
+    for (int i = tid; i < kList; i += kTThreads) s.tally[i] = 0;
     __syncthreads();
     if (warp == 0) {
-        wtop = lane < kTWarps ? s.wmax[lane] : -INFINITY;
+        wtop = s.wmax[lane & (kTWarps - 1)];
+        wlow = s.wlow[lane & (kTWarps - 1)];
 #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
-        if (lane == 0) s.bmax = wtop;
+        for (int m = 8; m > 0; m >>= 1) {
+            wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
+            wlow = fminf(wlow, __shfl_xor_sync(0xFFFFFFFFu, wlow, m));
+        }
+        if (lane == 0) s.bmax = wtop, s.blow = wlow;
     }
     barrier();
     const float mine = top;  // this thread's own
     top = lane < cluster ? __uint_as_float(of32(&s.bmax, lane)) : -INFINITY;
+    float low = lane < cluster ? __uint_as_float(of32(&s.blow, lane)) : INFINITY;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    for (int m = 16; m > 0; m >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, m));
+    }
     const bool none = top == -INFINITY;
 
     // p of the row's elements from their weights; 0 where nothing stays
     float inv = 0.0f;
     auto share = [&](u64 w) { return fmaf((float)(uint32_t)(w >> 20), 1048576.0f, (float)(uint32_t)(w & 0xFFFFFu)) * inv; };
+    auto draw_at = [&](u64 sum) { return part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), sum); };
     auto zeros = [&]() {  // of this block's slice of the distribution
         const int from = max(0, b0 * VEC - mis), to = min(V, (b0 + kTWarps * per_warp) * VEC - mis);
         float *const o = out + from;
@@ -411,70 +461,89 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         const int at = atomicAdd(&s.listed, 1);
         if (at < kList) s.list[at] = key;
     };
-    // the blocks' lists, in the first one's `sort`: how many; barriers on the way (none where they are too long)
+    // the blocks' lists, in the first one's `sort`; how many elements (none are moved where they are too many)
     auto collect = [&]() {
-        int n = 0, from = 0, count = 0;
-        for (int c = 0; c < cluster; ++c) {
-            const int m = (int)of32(&s.listed, c);
-            n += m;
+        int upto = lane < cluster ? (int)of32(&s.listed, lane) : 0;
+#pragma unroll
+        for (int m = 1; m < kMaxTCluster; m <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+            if (lane >= m) upto += o;
         }
+        const int n = __shfl_sync(0xFFFFFFFFu, upto, kMaxTCluster - 1);
         if (n > kList || rank > 0) return n;
-        for (int c = 0; c < cluster; ++c) {
-            count = (int)of32(&s.listed, c);
-            for (int i = tid; i < count; i += kTThreads) s.sort[from + i] = of64(&s.list[i], c);
-            from += count;
+        int end[kMaxTCluster];
+#pragma unroll
+        for (int c = 0; c < kMaxTCluster; ++c) end[c] = __shfl_sync(0xFFFFFFFFu, upto, c);
+        for (int i = tid; i < n; i += kTThreads) {
+            int c = 0, from = 0;
+#pragma unroll
+            for (int j = 0; j < kMaxTCluster - 1; ++j)
+                if (i >= end[j]) c = j + 1, from = end[j];
+            s.sort[i] = of64(&s.list[i - from], c);
         }
-        __syncthreads();
         return n;
     };
     const u64 top2 = two(top, top), rate2 = two(rate, rate), zero2 = two(minus_zero, minus_zero);
     // what the sort finds to stay: elements up to cut_key in the order of (bits of d, index)
     u64 cut_key = ~0ull;
-    bool by_list = false;   // all that stays is in the first block's sorted list
     int bin_cut = kOctaves;  // of the histogram by y: the elements of lower bins stay, of this one those up to cut_key
     bool done = false;      // the cut is found
 
     // ---------------------------------------------------------------- top-k by a few candidates
     const bool few = V <= kList && (k < V || nucleus);
     const int g8 = 64 * cluster, gt = kTThreads * cluster;  // maxima of eight threads, of one
-    if (top < INFINITY && (few || 3 * k <= gt)) {
+    if (top < INFINITY && (few || (k < V && 3 * k <= gt))) {
         float least_value = -INFINITY;
         if (!few) {
-            // the k-th largest of them, to 20 bits of their order; at most eight a thread
+            // (a little below) the k-th largest of the maxima; at most eight a thread
             uint32_t v[kMaxTCluster];
-            int nv = 1;
-            if (3 * k <= g8) {
-                float m8 = -INFINITY;
-                if (tid < g8) {
-                    const float *const from = s.tmax + 8 * (tid % 64);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) m8 = fmaxf(m8, __uint_as_float(of32(from + i, tid / 64)));
-                }
-                v[0] = order_of(m8);
+            const int nv = 3 * k <= g8 ? 1 : cluster;
+            if (nv == 1) {
+                v[0] = tid < g8 ? order_of(__uint_as_float(of32(&s.max8[tid & 63], tid >> 6))) : 0u;
             } else {
-                nv = cluster;
 #pragma unroll
                 for (int c = 0; c < kMaxTCluster; ++c) v[c] = c < cluster ? order_of(__uint_as_float(of32(&s.tmax[tid], c))) : 0u;
             }
-            uint32_t t = 0;
-            int turn = 0;
-            for (int bit = 31; bit >= 12; --bit, ++turn) {
-                const uint32_t want = t | 1u << bit;
-                int n;
-                if (nv == 1) {
-                    n = __syncthreads_count(v[0] >= want);
-                } else {
-                    int c = 0;
-#pragma unroll
-                    for (int i = 0; i < kMaxTCluster; ++i) c += v[i] >= want ? 1 : 0;
-                    c = __reduce_add_sync(0xFFFFFFFFu, c);
-                    if (lane == 0) atomicAdd(&s.tally[turn], c);
+            // a histogram between the least and the largest of them, finer again where those are far apart; what
+            // lies above the bins counts in the first one
+            uint32_t from = order_of(low), range = order_of(top) - from;
+            for (int turn = 0; turn < 3 && (turn == 0 || range >= 65536); ++turn) {
+                const int shift = max(0, 32 - __clz(range) - 11);
+                if (turn > 0) {
                     __syncthreads();
-                    n = s.tally[turn];
+                    for (int i = tid; i < kList; i += kTThreads) s.tally[i] = 0;
+                    __syncthreads();
                 }
-                if (n >= k) t = want;
+                auto add = [&](uint32_t x) {
+                    if (x >= from) atomicAdd(&s.tally[kList - 1 - min((x - from) >> shift, (uint32_t)(kList - 1))], 1);
+                };
+                add(v[0]);
+                if (nv > 1) {
+#pragma unroll
+                    for (int c = 1; c < kMaxTCluster; ++c)
+                        if (c < nv) add(v[c]);
+                }
+                if (tid == 0) s.bin = -1;
+                __syncthreads();
+                int n[4], sum = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum += n[i] = s.tally[4 * tid + i];
+                u64 all;
+                int before = (int)sum_before((u64)sum, s, all);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (before < k && before + n[i] >= k) s.bin = kList - 1 - (4 * tid + i);
+                    before += n[i];
+                }
+                __syncthreads();
+                if (s.bin < 0) {  // fewer than k threads have any
+                    from = 0;
+                    break;
+                }
+                from += (uint32_t)s.bin << shift;
+                range = (1u << shift) - 1;
             }
-            least_value = value_of(t);
+            least_value = value_of(from);
             if (!(least_value >= -INFINITY)) least_value = -INFINITY;  // (no such number)
         }
         for (int g = g0 + lane; g < g1; g += 32) {
@@ -493,7 +562,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         barrier();
         const int n = collect();
         if (n <= kList) {
-            by_list = done = true;
+            barrier();  // the lists are read: the other blocks leave
             if (rank == 0) {
                 sort_list(s, n);
                 // four a thread, in order: weights, what min-p and top-p leave of the first k
@@ -506,54 +575,64 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                     if (w[i] < least) w[i] = 0;
                     sum += w[i];
                 }
-                u64 all, before = sum_before(sum, s, all);
-                const u64 cut = max((u64)1, part_of(pfix, all));
+                u64 all, before;
+                if (nucleus) {
+                    before = sum_before(sum, s, all);
+                    const u64 cut = max((u64)1, part_of(pfix, all));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u64 mine_ = w[i];
-                    if (nucleus && before >= cut) w[i] = 0;
-                    before += mine_;
+                    for (int i = 0; i < 4; ++i) {
+                        const u64 wi = w[i];
+                        if (before >= cut) w[i] = 0;
+                        before += wi;
+                    }
                 }
                 __syncthreads();
-                // their sum, and how many they are
-                u64 total, stay;
-                (void)sum_before(w[0] + w[1] + w[2] + w[3], s, total);
-                __syncthreads();
-                const int ones = (w[0] ? 1 : 0) + (w[1] ? 1 : 0) + (w[2] ? 1 : 0) + (w[3] ? 1 : 0);
-                u64 place = sum_before((u64)ones, s, stay);
-                inv = total ? 1.0f / (float)total : 0.0f;
                 if (PROBS) {
+                    (void)sum_before(w[0] + w[1] + w[2] + w[3], s, all);
+                    inv = 1.0f / (float)all;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (w[i]) out[(int)(key[i] & 0xFFFFFu)] = share(w[i]);
                 } else {
-                    // the draw goes by their index
+                    // the draw goes by index: sums over 2048 equal parts of the row, then inside one of them
+                    for (int i = tid; i < kList; i += kTThreads) s.sort[i] = 0;
+                    if (tid == 0) s.listed = 0;
+                    __syncthreads();
+                    const int shift = max(0, 32 - __clz(V - 1) - 11);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (w[i]) s.sort[place++] = (key[i] & 0xFFFFFu) << 41 | w[i];
+                        if (w[i]) atomicAdd(&s.sort[(uint32_t)(key[i] & 0xFFFFFu) >> shift], w[i]);
                     __syncthreads();
-                    sort_list(s, (int)stay);
-                    u64 q[4];
-                    sum = 0;
+                    u64 part[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part[i] = s.sort[4 * tid + i];
+                    before = sum_before(part[0] + part[1] + part[2] + part[3], s, all);
+                    inv = 1.0f / (float)all;
+                    const u64 at = draw_at(all);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        q[i] = 4 * tid + i < (int)stay ? s.sort[4 * tid + i] : 0;
-                        sum += q[i] & ((1ull << 41) - 1);
+                        if (at >= before && at < before + part[i]) s.bin = 4 * tid + i, s.mass = before;
+                        before += part[i];
                     }
-                    before = sum_before(sum, s, all);
-                    const u64 at = part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), total);
+                    __syncthreads();
+                    const int bin = s.bin;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const u64 wi = q[i] & ((1ull << 41) - 1);
-                        if (at >= before && at < before + wi) {
-                            a.token[row] = (int)(q[i] >> 41);
-                            a.p[row] = share(wi);
+                    for (int i = 0; i < 4; ++i)
+                        if (w[i] && (int)((uint32_t)(key[i] & 0xFFFFFu) >> shift) == bin)
+                            s.list[atomicAdd(&s.listed, 1)] = (key[i] & 0xFFFFFu) << 41 | w[i];
+                    __syncthreads();
+                    if (tid < s.listed) {  // at most 512 indices a part
+                        const u64 me = s.list[tid], one = (1ull << 41) - 1;
+                        before = s.mass;
+                        for (int j = 0; j < s.listed; ++j)
+                            if (s.list[j] < me) before += s.list[j] & one;
+                        if (at >= before && at < before + (me & one)) {
+                            a.token[row] = (int)(me >> 41);
+                            a.p[row] = share(me & one);
                         }
-                        before += wi;
                     }
                 }
             }
-            if (cluster > 1) cluster_barrier();  // no block leaves while another may read its memory
             return;
         }
         barrier();  // the lists are begun again
@@ -587,11 +666,14 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         for (int j = 0; j < 2; ++j) {
             const int bin = 2 * tid + j;
             u64 lo = 0, hi = 0;
-            if (bin < kOctaves)
-                for (int c = 0; c < cluster; ++c) {
-                    lo += of32(&s.y.low[bin], c);
-                    hi += of32(&s.y.high[bin], c);
-                }
+            if (bin < kOctaves) {
+#pragma unroll
+                for (int c = 0; c < kMaxTCluster; ++c)  // all on their way at once
+                    if (c < cluster) {
+                        lo += of32(&s.y.low[bin], c);
+                        hi += of32(&s.y.high[bin], c);
+                    }
+            }
             mass[j] = (lo + (hi << 12)) << (bin < 256 ? 16 - (bin >> 4) : 0);
         }
         u64 all, before = sum_before(mass[0] + mass[1], s, all);
@@ -634,6 +716,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         if (n <= kList) {
             done = true;
             if (rank == 0) {
+                __syncthreads();
                 sort_list(s, n);
                 u64 w[4], here = 0;
 #pragma unroll
@@ -904,11 +987,16 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             if (lane == 0) s.bsum = v;
         }
         barrier();
-        for (int c = 0; c < cluster; ++c) {
-            const u64 v = of64(&s.bsum, c);
-            if (c < rank) first += v;
-            total += v;
+        const u64 v = lane < cluster ? of64(&s.bsum, lane) : 0;
+        first = lane < rank ? v : 0;
+        total = v;
+#pragma unroll
+        for (int m = kMaxTCluster / 2; m > 0; m >>= 1) {
+            first += __shfl_xor_sync(0xFFFFFFFFu, first, m);
+            total += __shfl_xor_sync(0xFFFFFFFFu, total, m);
         }
+        first = __shfl_sync(0xFFFFFFFFu, first, 0);
+        total = __shfl_sync(0xFFFFFFFFu, total, 0);
         inv = 1.0f / (float)total;
     }
 
@@ -943,36 +1031,34 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             }
         }
     } else {
-        const u64 at = part_of((u64)(fminf(fmaxf(u, 0.0f), 0.99999994f) * 16777216.0f), total);
-        u64 before = first;
-        for (int w = 0; w < warp; ++w) before += s.wsum[w];
-        if (at >= before && at < before + s.wsum[warp]) {  // this warp's part has it
-            for (int gb = g0; gb < g1; gb += 32) {
-                const int g = gb + lane;
-                float y[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) y[i] = -INFINITY;
-                if (g < g1) load(g, y);
-                u64 w[VEC], own = 0;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) own += w[i] = kept(y[i], g * VEC - mis + i);
-                u64 upto = own;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const u64 o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
-                    if (lane >= m) upto += o;
-                }
-                u64 r = before + upto - own;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    if (at >= r && at < r + w[i]) {
-                        a.token[row] = g * VEC - mis + i;
-                        a.p[row] = share(w[i]);
+        const u64 at = draw_at(total);
+        if (at >= first && at < first + s.bsum) {  // this block's slice has it: which warp's part
+            u64 before = first;
+            int w = 0;
+            while (at >= before + s.wsum[w]) before += s.wsum[w++];
+            // the whole block over that part, a thread some elements one after another
+            const int from = (b0 + w * per_warp) * VEC, parts = (per_warp * VEC + kTThreads - 1) / kTThreads;
+            auto element = [&](int e) -> float {  // counted from the first group's first
+                if (staged) return L::one(reinterpret_cast<const T *>(stage) + (e - b0 * VEC));
+                e -= mis;
+                return (unsigned)e < (unsigned)V ? fmaxf(L::one(x + e), -INFINITY) : -INFINITY;
+            };
+            const int mine0 = from + tid * parts;
+            const int end = min(from + per_warp * VEC, groups * VEC);
+            u64 own = 0, all;
+            for (int i = 0; i < parts; ++i)
+                if (mine0 + i < end) own += kept(element(mine0 + i), mine0 + i - mis);
+            before += sum_before(own, s, all);
+            if (at >= before && at < before + own) {
+                for (int i = 0; i < parts; ++i) {
+                    if (mine0 + i >= end) break;
+                    const u64 wi = kept(element(mine0 + i), mine0 + i - mis);
+                    if (at >= before && at < before + wi) {
+                        a.token[row] = mine0 + i - mis;
+                        a.p[row] = share(wi);
                     }
-                    r += w[i];
+                    before += wi;
                 }
-                before += __shfl_sync(0xFFFFFFFFu, upto, 31);
-                if (before > at) break;
             }
         }
     }
