@@ -231,8 +231,8 @@ __device__ __forceinline__ u64 sum_before(u64 v, TokenShared &s, u64 &all) {
 }
 
 // Sorts s.sort[0 .. n), all different, by the whole block: by counting how many are smaller up to 256 of them (several
-// threads each), else in a bitonic network.  Ends with a barrier; what lies behind is undefined.
-__device__ __forceinline__ void sort_list(TokenShared &s, int n) {
+// threads each), else into bins of even width in d first.  s.list is written too.  Ends with a barrier.
+__device__ __noinline__ void sort_list(TokenShared &s, int n) {
     const int tid = threadIdx.x;
     int size = 32;
     while (size < n) size *= 2;
@@ -247,49 +247,61 @@ __device__ __forceinline__ void sort_list(TokenShared &s, int n) {
         __syncthreads();
         return;
     }
-    // Places tid, tid + 512, ..: partners up to 16 apart are lanes of a warp, from 512 apart a thread's own.
     constexpr int R = kList / kTThreads;
     u64 v[R];
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = tid + r * kTThreads < n ? s.sort[tid + r * kTThreads] : ~0ull;
-    for (int block = 2; block <= size; block *= 2)
-        for (int step = block / 2; step > 0; step /= 2) {
-            if (step >= kTThreads) {
-                auto swap = [&](u64 &x, u64 &y, int at) {
-                    const bool turn = (x > y) == ((at & block) == 0);
-                    const u64 z = turn ? y : x;
-                    y = turn ? x : y;
-                    x = z;
-                };
-                if (step == kTThreads) {
-                    swap(v[0], v[1], tid);
-                    swap(v[2], v[3], tid + 2 * kTThreads);
-                } else {
-                    swap(v[0], v[2], tid);
-                    swap(v[1], v[3], tid + kTThreads);
-                }
-                continue;
-            }
-            if (step >= 32) {
-                __syncthreads();
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (r * kTThreads < size) s.sort[tid + r * kTThreads] = v[r];
-                __syncthreads();
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (r * kTThreads >= size) break;
-                const int at = tid + r * kTThreads;
-                const u64 y = step >= 32 ? s.sort[at ^ step] : __shfl_xor_sync(0xFFFFFFFFu, v[r], step);
-                const bool smaller = ((at & block) == 0) == ((at & step) == 0);  // this place takes the smaller one
-                v[r] = (y < v[r]) == smaller ? y : v[r];
-            }
+    for (int r = 0; r < R; ++r) {
+        v[r] = tid + r * kTThreads < n ? s.sort[tid + r * kTThreads] : ~0ull;
+        if (tid + r * kTThreads < n) {
+            lo = min(lo, (uint32_t)(v[r] >> 20));
+            hi = max(hi, (uint32_t)(v[r] >> 20));
         }
+    }
+    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+    if ((tid & 31) == 0) s.tcount[tid >> 5] = (int)lo, s.wcount[tid >> 5] = (int)hi;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTWarps; ++w) lo = min(lo, (uint32_t)s.tcount[w]), hi = max(hi, (uint32_t)s.wcount[w]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) s.tally[tid + r * kTThreads] = 0;  // (where sort was)
+    __syncthreads();
+    const float least = __uint_as_float(lo), per = fminf((float)(kList - 1) / (__uint_as_float(hi) - least), 1e38f);
+    auto bin_of = [&](u64 key) { return min((int)((__uint_as_float((uint32_t)(key >> 20)) - least) * per), kList - 1); };
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (tid + r * kTThreads < n) atomicAdd(&s.tally[bin_of(v[r])], 1);
+    __syncthreads();
+    int c[R], sum = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) sum += c[r] = s.tally[R * tid + r];
+    u64 all;
+    int at = (int)sum_before((u64)sum, s, all);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        s.tally[R * tid + r] = at;
+        at += c[r];
+    }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r)
-        if (r * kTThreads < size) s.sort[tid + r * kTThreads] = v[r];
+        if (tid + r * kTThreads < n) s.list[atomicAdd(&s.tally[bin_of(v[r])], 1)] = v[r];
+    __syncthreads();
+    int rank[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rank[r] = 0;
+        if (tid + r * kTThreads >= n) continue;
+        v[r] = s.list[tid + r * kTThreads];
+        const int bin = bin_of(v[r]), from = bin > 0 ? s.tally[bin - 1] : 0, to = s.tally[bin];
+        rank[r] = from;
+        for (int j = from; j < to; ++j) rank[r] += s.list[j] < v[r] ? 1 : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (tid + r * kTThreads < n) s.sort[rank[r]] = v[r];
     __syncthreads();
 }
 
@@ -739,12 +751,13 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             cut_key = of64(&s.cut_key, 0);
             inv = 1.0f / (float)of64(&s.total, 0);
             if (!PROBS) {
-                // this block's share of them, into the sums of the warps whose part they lie in
-                for (int i = tid; i < s.listed; i += kTThreads) {
-                    const u64 key = s.list[i];
-                    if (key > cut_key) continue;
-                    const int g = ((int)(key & 0xFFFFFu) + mis) / VEC;
-                    atomicAdd(&s.wsum[(g - b0) / per_warp], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
+                // this block's share of them, into the sums of the warps whose part they lie in (the first block has
+                // all of them sorted, and its own list no longer)
+                const u64 *const from_list = rank == 0 ? s.sort : s.list;
+                for (int i = tid; i < (rank == 0 ? n : s.listed); i += kTThreads) {
+                    const u64 key = from_list[i];
+                    const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
+                    if (key <= cut_key && part < kTWarps) atomicAdd(&s.wsum[part], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
                 }
                 __syncthreads();
             }
