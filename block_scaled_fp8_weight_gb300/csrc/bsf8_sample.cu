@@ -27,14 +27,18 @@ namespace bsf8 {
 namespace {
 
 typedef unsigned long long u64;
-constexpr int kTThreads = 512, kTWarps = kTThreads / 32;
+constexpr int kTThreads = 256, kTWarps = kTThreads / 32;
 constexpr int kMaxTCluster = 8;
-constexpr int kBins = 1024;      // of the digits' histograms
-constexpr int kOctaves = 16 * 41;  // of the histogram by y: y <= 40 in sixteenths
-constexpr int kList = 2048;      // elements that the first block sorts
-constexpr int kStage = 72 * 1024;  // bytes of a slice that are kept: two blocks an SM
+constexpr int kBins = 1024;      // of the digits' histograms, and of the sort
+constexpr int kOctaves = 41, kParts = 16;  // the histogram by y: y <= 40 in sixteenths
+constexpr int kSteps = kOctaves * kParts;
+constexpr int kList = 2048;      // elements that the first block sorts,
+constexpr int kOwn = 704;        // and that a block of a cluster finds
+// Bytes of a slice that are kept: four blocks an SM, whose latencies hide each other, are worth more than slices
+// of twice that (192 rows of 131072 bf16, k = 50: 53 us with two blocks of 512 threads).
+constexpr int kStage = 34 * 1024;
 constexpr uint32_t kInfBits = 0x7F800000u;
-static_assert(kBins == 2 * kTThreads && kList == 4 * kTThreads, "bins and elements a thread");
+constexpr int kEach = kList / kTThreads, kBinsEach = kBins / kTThreads;
 
 struct TokenShared {
     float tmax[kTThreads];          // the threads' largest logits
@@ -49,16 +53,17 @@ struct TokenShared {
     int bin;                        // the bin in which the wanted rank or weight lies,
     int before;                     // and what is before it
     u64 mass;
-    u64 all;
+    u64 wstep[kParts];              // weights by step of an octave
     int cut;
     int listed;                     // elements in list
     u64 cut_key, total;             // of the first block: what stays, its sum
-    u64 list[kList];                // this block's elements: bits of d, index
+    u64 octave[kOctaves];           // weights of this block by octave
+    u64 list[kOwn];                 // this block's elements: bits of d, index
     union {
         u64 sort[kList];
         int tally[kList];           // counts of the search for the k-th
         struct {
-            uint32_t low[kOctaves], high[kOctaves];  // the weights' (as integers of 24 bits) low 12 bits and the rest
+            uint32_t low[kSteps], high[kSteps];  // the weights' (as integers of 24 bits) low 12 bits and the rest
         } y;
         struct {
             uint32_t count[kBins], low[kBins];
@@ -162,6 +167,13 @@ __device__ __forceinline__ uint32_t ld_cluster32(uint32_t addr) {
     return v;
 }
 
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
 // Larger for larger values.
 __device__ __forceinline__ uint32_t order_of(float f) {
     const uint32_t b = __float_as_uint(f);
@@ -230,14 +242,15 @@ __device__ __forceinline__ u64 sum_before(u64 v, TokenShared &s, u64 &all) {
     return before;
 }
 
-// Sorts s.sort[0 .. n), all different, by the whole block: by counting how many are smaller up to 256 of them (several
-// threads each), else into bins of even width in d first.  s.list is written too.  Ends with a barrier.
-__device__ __noinline__ void sort_list(TokenShared &s, int n) {
+// Sorts s.sort[0 .. n), all different, by the whole block: by counting how many are smaller up to 256 of them (a
+// thread or more each), else into bins of even width in d first.  `bins`: kBins words of scratch.  Ends with a
+// barrier.
+__device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
     const int tid = threadIdx.x;
     int size = 32;
     while (size < n) size *= 2;
-    if (size <= 256) {
-        const int each = kTThreads / size, i = tid / each, part = tid % each;  // threads an element: 2 .. 16
+    if (size <= kTThreads) {
+        const int each = kTThreads / size, i = tid / each, part = tid % each;  // threads an element: 1 .. 8
         const u64 mine = i < n ? s.sort[i] : ~0ull;
         int rank = 0;
         for (int j = part; j < n; j += each) rank += s.sort[j] < mine ? 1 : 0;
@@ -247,11 +260,10 @@ __device__ __noinline__ void sort_list(TokenShared &s, int n) {
         __syncthreads();
         return;
     }
-    constexpr int R = kList / kTThreads;
-    u64 v[R];
+    u64 v[kEach];
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < kEach; ++r) {
         v[r] = tid + r * kTThreads < n ? s.sort[tid + r * kTThreads] : ~0ull;
         if (tid + r * kTThreads < n) {
             lo = min(lo, (uint32_t)(v[r] >> 20));
@@ -261,46 +273,44 @@ __device__ __noinline__ void sort_list(TokenShared &s, int n) {
     lo = __reduce_min_sync(0xFFFFFFFFu, lo);
     hi = __reduce_max_sync(0xFFFFFFFFu, hi);
     if ((tid & 31) == 0) s.tcount[tid >> 5] = (int)lo, s.wcount[tid >> 5] = (int)hi;
+    for (int i = tid; i < kBins; i += kTThreads) bins[i] = 0;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kTWarps; ++w) lo = min(lo, (uint32_t)s.tcount[w]), hi = max(hi, (uint32_t)s.wcount[w]);
+    const float least = __uint_as_float(lo), per = fminf((float)(kBins - 1) / (__uint_as_float(hi) - least), 1e38f);
+    auto bin_of = [&](u64 key) { return min((int)((__uint_as_float((uint32_t)(key >> 20)) - least) * per), kBins - 1); };
 #pragma unroll
-    for (int r = 0; r < R; ++r) s.tally[tid + r * kTThreads] = 0;  // (where sort was)
+    for (int r = 0; r < kEach; ++r)
+        if (tid + r * kTThreads < n) atomicAdd(&bins[bin_of(v[r])], 1);
     __syncthreads();
-    const float least = __uint_as_float(lo), per = fminf((float)(kList - 1) / (__uint_as_float(hi) - least), 1e38f);
-    auto bin_of = [&](u64 key) { return min((int)((__uint_as_float((uint32_t)(key >> 20)) - least) * per), kList - 1); };
+    int c[kBinsEach], sum = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (tid + r * kTThreads < n) atomicAdd(&s.tally[bin_of(v[r])], 1);
-    __syncthreads();
-    int c[R], sum = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) sum += c[r] = s.tally[R * tid + r];
+    for (int r = 0; r < kBinsEach; ++r) sum += c[r] = bins[kBinsEach * tid + r];
     u64 all;
     int at = (int)sum_before((u64)sum, s, all);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        s.tally[R * tid + r] = at;
+    for (int r = 0; r < kBinsEach; ++r) {
+        bins[kBinsEach * tid + r] = at;
         at += c[r];
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (tid + r * kTThreads < n) s.list[atomicAdd(&s.tally[bin_of(v[r])], 1)] = v[r];
+    for (int r = 0; r < kEach; ++r)
+        if (tid + r * kTThreads < n) s.sort[atomicAdd(&bins[bin_of(v[r])], 1)] = v[r];
     __syncthreads();
-    int rank[R];
+    int rank[kEach];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < kEach; ++r) {
         rank[r] = 0;
         if (tid + r * kTThreads >= n) continue;
-        v[r] = s.list[tid + r * kTThreads];
-        const int bin = bin_of(v[r]), from = bin > 0 ? s.tally[bin - 1] : 0, to = s.tally[bin];
+        v[r] = s.sort[tid + r * kTThreads];
+        const int bin = bin_of(v[r]), from = bin > 0 ? bins[bin - 1] : 0, to = bins[bin];
         rank[r] = from;
-        for (int j = from; j < to; ++j) rank[r] += s.list[j] < v[r] ? 1 : 0;
+        for (int j = from; j < to; ++j) rank[r] += s.sort[j] < v[r] ? 1 : 0;
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kEach; ++r)
         if (tid + r * kTThreads < n) s.sort[rank[r]] = v[r];
     __syncthreads();
 }
@@ -308,10 +318,13 @@ __device__ __noinline__ void sort_list(TokenShared &s, int n) {
 }  // namespace
 
 template <typename T, bool PROBS>
-__global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
+__global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
     extern __shared__ __align__(16) uint8_t memory[];
     TokenShared &s = *reinterpret_cast<TokenShared *>(memory);
-    uint4 *const stage = reinterpret_cast<uint4 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16);
+    // a block by itself may find as many elements as are sorted: its list lies behind the slice
+    u64 *const list = cluster > 1 ? s.list : reinterpret_cast<u64 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16);
+    const int own = cluster > 1 ? kOwn : kList;
+    uint4 *const stage = reinterpret_cast<uint4 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16 + (cluster > 1 ? 0 : kList * 8));
     pdl_trigger();
     pdl_wait();
     using L = Logit<T>;
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
     const T *const x = static_cast<const T *>(a.logits) + (size_t)row * a.ld;
     // groups of VEC elements that start on 16 bytes; the first and last may be partly outside the row
     const int mis = (int)(((size_t)row * a.ld) % VEC), groups = (V + mis + VEC - 1) / VEC;
-    const int per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 31) / 32 * 32;
+    const int per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 7) / 8 * 8;
     const int b0 = rank * kTWarps * per_warp;  // the block's first group
     const int g0 = min(groups, b0 + warp * per_warp), g1 = min(groups, g0 + per_warp);
     const float tp = a.temperature ? a.temperature[row] : 1.0f;
@@ -352,6 +365,26 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         return make_uint4(L::clean(w.x), L::clean(w.y), L::clean(w.z), L::clean(w.w));
     };
     auto load = [&](int g, float (&y)[VEC]) { L::unpack(staged ? stage[g - b0] : fetch(g), y); };
+    // f(elements, first one's index) of the warp's part, a lane's groups 32 apart, four on their way
+    auto each = [&](auto f) {
+        int g = g0 + lane;
+        for (; g + 96 < g1; g += 128) {
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = staged ? stage[g + 32 * j - b0] : fetch(g + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float y[VEC];
+                L::unpack(w[j], y);
+                f(y, (g + 32 * j) * VEC - mis);
+            }
+        }
+        for (; g < g1; g += 32) {
+            float y[VEC];
+            load(g, y);
+            f(y, g * VEC - mis);
+        }
+    };
     auto barrier = [&]() {
         if (cluster > 1) cluster_barrier();
         else __syncthreads();
@@ -471,7 +504,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         const u64 key = key_at(v, index);
         if (key >> 20 >= kInfBits) return;
         const int at = atomicAdd(&s.listed, 1);
-        if (at < kList) s.list[at] = key;
+        if (at < own) list[at] = key;
     };
     // the blocks' lists, in the first one's `sort`; how many elements (none are moved where they are too many)
     auto collect = [&]() {
@@ -482,6 +515,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             if (lane >= m) upto += o;
         }
         const int n = __shfl_sync(0xFFFFFFFFu, upto, kMaxTCluster - 1);
+        if (__any_sync(0xFFFFFFFFu, lane < cluster && (int)of32(&s.listed, lane) > own)) return kList + 1;
         if (n > kList || rank > 0) return n;
         int end[kMaxTCluster];
 #pragma unroll
@@ -491,27 +525,28 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
 #pragma unroll
             for (int j = 0; j < kMaxTCluster - 1; ++j)
                 if (i >= end[j]) c = j + 1, from = end[j];
-            s.sort[i] = of64(&s.list[i - from], c);
+            s.sort[i] = of64(&list[i - from], c);
         }
         return n;
     };
     const u64 top2 = two(top, top), rate2 = two(rate, rate), zero2 = two(minus_zero, minus_zero);
     // what the sort finds to stay: elements up to cut_key in the order of (bits of d, index)
     u64 cut_key = ~0ull;
-    int bin_cut = kOctaves;  // of the histogram by y: the elements of lower bins stay, of this one those up to cut_key
+    int bin_cut = kSteps;    // of the histogram by y: the elements of lower bins stay, of this one those up to cut_key
     bool done = false;      // the cut is found
 
     // ---------------------------------------------------------------- top-k by a few candidates
     const bool few = V <= kList && (k < V || nucleus);
-    const int g8 = 64 * cluster, gt = kTThreads * cluster;  // maxima of eight threads, of one
-    if (top < INFINITY && (few || (k < V && 3 * k <= gt))) {
+    constexpr int kMax8 = kTThreads / 8;
+    const int g8 = kMax8 * cluster, gt = kTThreads * cluster;  // maxima of eight threads, of one
+    if (top < INFINITY && (few || (k < V && 2 * k <= gt))) {
         float least_value = -INFINITY;
         if (!few) {
             // (a little below) the k-th largest of the maxima; at most eight a thread
             uint32_t v[kMaxTCluster];
-            const int nv = 3 * k <= g8 ? 1 : cluster;
+            const int nv = 2 * k <= g8 ? 1 : cluster;
             if (nv == 1) {
-                v[0] = tid < g8 ? order_of(__uint_as_float(of32(&s.max8[tid & 63], tid >> 6))) : 0u;
+                v[0] = tid < g8 ? order_of(__uint_as_float(of32(&s.max8[tid % kMax8], tid / kMax8))) : 0u;
             } else {
 #pragma unroll
                 for (int c = 0; c < kMaxTCluster; ++c) v[c] = c < cluster ? order_of(__uint_as_float(of32(&s.tmax[tid], c))) : 0u;
@@ -537,14 +572,14 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                 }
                 if (tid == 0) s.bin = -1;
                 __syncthreads();
-                int n[4], sum = 0;
+                int n[kEach], sum = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sum += n[i] = s.tally[4 * tid + i];
+                for (int i = 0; i < kEach; ++i) sum += n[i] = s.tally[kEach * tid + i];
                 u64 all;
                 int before = (int)sum_before((u64)sum, s, all);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (before < k && before + n[i] >= k) s.bin = kList - 1 - (4 * tid + i);
+                for (int i = 0; i < kEach; ++i) {
+                    if (before < k && before + n[i] >= k) s.bin = kList - 1 - (kEach * tid + i);
                     before += n[i];
                 }
                 __syncthreads();
@@ -558,30 +593,28 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             least_value = value_of(from);
             if (!(least_value >= -INFINITY)) least_value = -INFINITY;  // (no such number)
         }
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC];
-            load(g, y);
+        each([&](const float (&y)[VEC], int at) {
             float m = y[0];
 #pragma unroll
             for (int i = 1; i < VEC; ++i) m = fmaxf(m, y[i]);
             if (m >= least_value) {
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
-                    if (y[i] >= least_value) keep_in_list(y[i], g * VEC - mis + i);
+                    if (y[i] >= least_value) keep_in_list(y[i], at + i);
             }
-        }
+        });
         if (PROBS) zeros();
         barrier();
         const int n = collect();
         if (n <= kList) {
             barrier();  // the lists are read: the other blocks leave
             if (rank == 0) {
-                sort_list(s, n);
-                // four a thread, in order: weights, what min-p and top-p leave of the first k
-                u64 w[4], key[4], sum = 0;
+                sort_list(s, reinterpret_cast<int *>(list), n);
+                // some a thread, in order: weights, what min-p and top-p leave of the first k
+                u64 w[kEach], key[kEach], sum = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 4 * tid + i;
+                for (int i = 0; i < kEach; ++i) {
+                    const int at = kEach * tid + i;
                     key[i] = at < min(n, k) ? s.sort[at] : ~0ull;
                     w[i] = at < min(n, k) ? weight(__uint_as_float((uint32_t)(key[i] >> 20)), rate) : 0;
                     if (w[i] < least) w[i] = 0;
@@ -592,7 +625,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                     before = sum_before(sum, s, all);
                     const u64 cut = max((u64)1, part_of(pfix, all));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < kEach; ++i) {
                         const u64 wi = w[i];
                         if (before >= cut) w[i] = 0;
                         before += wi;
@@ -600,10 +633,13 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                 }
                 __syncthreads();
                 if (PROBS) {
-                    (void)sum_before(w[0] + w[1] + w[2] + w[3], s, all);
+                    sum = 0;
+#pragma unroll
+                    for (int i = 0; i < kEach; ++i) sum += w[i];
+                    (void)sum_before(sum, s, all);
                     inv = 1.0f / (float)all;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kEach; ++i)
                         if (w[i]) out[(int)(key[i] & 0xFFFFFu)] = share(w[i]);
                 } else {
                     // the draw goes by index: sums over 2048 equal parts of the row, then inside one of them
@@ -612,32 +648,34 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                     __syncthreads();
                     const int shift = max(0, 32 - __clz(V - 1) - 11);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kEach; ++i)
                         if (w[i]) atomicAdd(&s.sort[(uint32_t)(key[i] & 0xFFFFFu) >> shift], w[i]);
                     __syncthreads();
-                    u64 part[4];
+                    u64 part[kEach];
+                    sum = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) part[i] = s.sort[4 * tid + i];
-                    before = sum_before(part[0] + part[1] + part[2] + part[3], s, all);
+                    for (int i = 0; i < kEach; ++i) sum += part[i] = s.sort[kEach * tid + i];
+                    before = sum_before(sum, s, all);
                     inv = 1.0f / (float)all;
                     const u64 at = draw_at(all);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (at >= before && at < before + part[i]) s.bin = 4 * tid + i, s.mass = before;
+                    for (int i = 0; i < kEach; ++i) {
+                        if (at >= before && at < before + part[i]) s.bin = kEach * tid + i, s.mass = before;
                         before += part[i];
                     }
                     __syncthreads();
                     const int bin = s.bin;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kEach; ++i)
                         if (w[i] && (int)((uint32_t)(key[i] & 0xFFFFFu) >> shift) == bin)
-                            s.list[atomicAdd(&s.listed, 1)] = (key[i] & 0xFFFFFu) << 41 | w[i];
+                            list[atomicAdd(&s.listed, 1)] = (key[i] & 0xFFFFFu) << 41 | w[i];
                     __syncthreads();
-                    if (tid < s.listed) {  // at most 512 indices a part
-                        const u64 me = s.list[tid], one = (1ull << 41) - 1;
+                    const int listed = s.listed;  // at most 512 indices a part
+                    for (int i = tid; i < listed; i += kTThreads) {
+                        const u64 me = list[i], one = (1ull << 41) - 1;
                         before = s.mass;
-                        for (int j = 0; j < s.listed; ++j)
-                            if (s.list[j] < me) before += s.list[j] & one;
+                        for (int j = 0; j < listed; ++j)
+                            if (list[j] < me) before += list[j] & one;
                         if (at >= before && at < before + (me & one)) {
                             a.token[row] = (int)(me >> 41);
                             a.p[row] = share(me & one);
@@ -654,94 +692,121 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
 
     // ---------------------------------------------------------------- top-p by the histogram of y
     if (!done && nucleus && k == V && top < INFINITY) {
-        for (int i = tid; i < kOctaves; i += kTThreads) s.y.low[i] = s.y.high[i] = 0;
+        for (int i = tid; i < kSteps; i += kTThreads) s.y.low[i] = s.y.high[i] = 0;
         __syncthreads();
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC];
-            load(g, y);
+        each([&](const float (&y)[VEC], int) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
                 const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     if (!(w.y[j] <= 40.0f) || ((u64)w.m[j] << 16) >> w.n[j] < least) continue;
-                    const int bin = (int)(__float_as_uint(__fadd_rz(w.y[j] * 16.0f, 8388608.0f)) & 1023u);
+                    const int bin = (int)(__float_as_uint(__fadd_rz(w.y[j] * (float)kParts, 8388608.0f)) & 1023u);
                     const uint32_t v = w.n[j] > 16 ? w.m[j] >> (w.n[j] - 16) : w.m[j];
                     atomicAdd(&s.y.low[bin], v & 0xFFFu);
                     atomicAdd(&s.y.high[bin], v >> 12);
                 }
             }
-        }
-        barrier();
-        u64 mass[2];
+        });
+        __syncthreads();
+        // a step's weights are integers of 24 bits that are (m << 16) >> n shifted down by what n leaves
+        auto unit = [](int octave) { return octave < 16 ? 16 - octave : 0; };
+        const int o = tid / 4, c0 = tid % 4;  // four threads an octave
+        static_assert(kTThreads / 4 >= kOctaves && kTThreads / 2 == 8 * kParts, "threads an octave, and a step and block");
+        {
+            u64 v = 0;
+            if (o < kOctaves) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int bin = 2 * tid + j;
-            u64 lo = 0, hi = 0;
-            if (bin < kOctaves) {
-#pragma unroll
-                for (int c = 0; c < kMaxTCluster; ++c)  // all on their way at once
-                    if (c < cluster) {
-                        lo += of32(&s.y.low[bin], c);
-                        hi += of32(&s.y.high[bin], c);
-                    }
-            }
-            mass[j] = (lo + (hi << 12)) << (bin < 256 ? 16 - (bin >> 4) : 0);
-        }
-        u64 all, before = sum_before(mass[0] + mass[1], s, all);
-        const u64 cut = max((u64)1, part_of(pfix, all));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (before < cut && before + mass[j] >= cut) {
-                s.bin = 2 * tid + j;
-                s.mass = before;
-            }
-            before += mass[j];
-        }
-        barrier();  // (the histograms are read)
-        bin_cut = s.bin;
-        const u64 below = s.mass;
-        // that bin's elements; the others' sums, a warp's part each
-        u64 sum = 0;
-        const float from = (float)bin_cut * 0.0625f, to = (float)(bin_cut + 1) * 0.0625f;
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC];
-            load(g, y);
-#pragma unroll
-            for (int i = 0; i < VEC; i += 2) {
-                const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!(w.y[j] < to) || !(w.y[j] <= 40.0f)) continue;
-                    const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
-                    if (wj < least) continue;
-                    if (w.y[j] < from) sum += wj;
-                    else keep_in_list(y[i + j], g * VEC - mis + i + j);
+                for (int j = 0; j < kParts / 4; ++j) {
+                    const int bin = o * kParts + c0 * (kParts / 4) + j;
+                    v += s.y.low[bin] + ((u64)s.y.high[bin] << 12);
                 }
             }
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+            if (c0 == 0 && o < kOctaves) s.octave[o] = v << unit(o);
         }
+        barrier();
+        // the octave in which the sum reaches the share of all; then the step inside it
+        u64 cut, below;
+        {
+            u64 mass = 0;
+            if (o < kOctaves) {  // two blocks' sums a thread
+                if (c0 < cluster) mass = of64(&s.octave[o], c0);
+                if (c0 + 4 < cluster) mass += of64(&s.octave[o], c0 + 4);
+            }
+            // what an octave's threads hold is added up by the sum over them
+            u64 all, before = sum_before(mass, s, all);
+            cut = max((u64)1, part_of(pfix, all));
+            u64 whole = mass + __shfl_xor_sync(0xFFFFFFFFu, mass, 1);
+            whole += __shfl_xor_sync(0xFFFFFFFFu, whole, 2);
+            if (c0 == 0 && before < cut && before + whole >= cut) s.bin = o, s.mass = before;
+            __syncthreads();
+            const int octave = s.bin;
+            if (warp < 4) {  // 16 steps, eight blocks: a thread each
+                const int step = tid / 8, c = tid % 8;
+                u64 v = 0;
+                if (c < cluster)
+                    v = of32(&s.y.low[octave * kParts + step], c) + ((u64)of32(&s.y.high[octave * kParts + step], c) << 12);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-        if (lane == 0) s.wsum[warp] = sum;
+                for (int m = 1; m < 8; m <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+                if (c == 0) s.wstep[step] = v << unit(octave);
+            }
+            __syncthreads();
+            below = s.mass;
+            int step = 0;
+            while (below + s.wstep[step] < cut) below += s.wstep[step++];
+            bin_cut = octave * kParts + step;
+        }
+        barrier();  // (the histograms are read)
+        // that step's elements; the others' sums, a warp's part each, for the draw
+        u64 sum = 0;
+        const float from = (float)bin_cut * (1.0f / kParts), to = (float)(bin_cut + 1) * (1.0f / kParts);
+        each([&](const float (&y)[VEC], int at) {
+#pragma unroll
+            for (int i = 0; i < VEC; i += 2) {
+                Two w;
+                if (PROBS) {
+                    apart(mul2(less2(top2, two(y[i], y[i + 1])), rate2, zero2), w.y[0], w.y[1]);
+                } else {
+                    w = weights2(y[i], y[i + 1], top2, rate2, zero2);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!PROBS && w.y[j] < from) {
+                        const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
+                        sum += wj >= least ? wj : 0;
+                    }
+                    if (w.y[j] >= from && w.y[j] < to && w.y[j] <= 40.0f &&
+                        (least <= 1 || weight(distance(y[i + j]), rate) >= least))
+                        keep_in_list(y[i + j], at + i + j);
+                }
+            }
+        });
+        if (!PROBS) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+            if (lane == 0) s.wsum[warp] = sum;
+        }
         barrier();
         const int n = collect();
         if (n <= kList) {
             done = true;
             if (rank == 0) {
                 __syncthreads();
-                sort_list(s, n);
-                u64 w[4], here = 0;
+                sort_list(s, reinterpret_cast<int *>(list), n);
+                u64 w[kEach], here = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = 4 * tid + i;
+                for (int i = 0; i < kEach; ++i) {
+                    const int at = kEach * tid + i;
                     w[i] = at < n ? weight(__uint_as_float((uint32_t)(s.sort[at] >> 20)), rate) : 0;
                     here += w[i];
                 }
                 u64 total, run = below + sum_before(here, s, total);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < kEach; ++i) {
                     if (run < cut && run + w[i] >= cut) {
-                        s.cut_key = s.sort[4 * tid + i];
+                        s.cut_key = s.sort[kEach * tid + i];
                         s.total = run + w[i];
                     }
                     run += w[i];
@@ -753,7 +818,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             if (!PROBS) {
                 // this block's share of them, into the sums of the warps whose part they lie in (the first block has
                 // all of them sorted, and its own list no longer)
-                const u64 *const from_list = rank == 0 ? s.sort : s.list;
+                const u64 *const from_list = rank == 0 ? s.sort : list;
                 for (int i = tid; i < (rank == 0 ? n : s.listed); i += kTThreads) {
                     const u64 key = from_list[i];
                     const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
@@ -762,7 +827,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                 __syncthreads();
             }
         } else {
-            bin_cut = kOctaves;
+            bin_cut = kSteps;
             barrier();
         }
     }
@@ -807,25 +872,19 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                 }
             }
             barrier();
-            // the cluster's histogram, two bins a thread, and the sums before each
-            u64 w2[2] = {0, 0};
-            int c2[2] = {0, 0};
+            // the cluster's histogram, some bins a thread, and the sums before each
+            u64 w2[kBinsEach] = {}, upw = 0;
+            int c2[kBinsEach] = {}, upc = 0;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int bin = 2 * tid + j;
+            for (int j = 0; j < kBinsEach; ++j) {
+                const int bin = kBinsEach * tid + j;
                 for (int c = 0; c < cluster; ++c) {
-                    if (cluster > 1) {
-                        c2[j] += (int)ld_cluster32(map_to_rank(&s.count[bin], c));
-                        if (by_weight)
-                            w2[j] += (u64)ld_cluster32(map_to_rank(&s.low[bin], c)) + (ld_cluster64(map_to_rank(&s.high[bin], c)) << 12);
-                    } else {
-                        c2[j] += (int)s.count[bin];
-                        if (by_weight) w2[j] += (u64)s.low[bin] + (s.high[bin] << 12);
-                    }
+                    c2[j] += (int)of32(&s.count[bin], c);
+                    if (by_weight) w2[j] += (u64)of32(&s.low[bin], c) + (of64(&s.high[bin], c) << 12);
                 }
+                upw += w2[j];
+                upc += c2[j];
             }
-            u64 upw = w2[0] + w2[1];
-            int upc = c2[0] + c2[1];
             const u64 myw = upw;
             const int myc = upc;
 #pragma unroll
@@ -847,10 +906,10 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
             if (level == 0 && fraction) want = max((u64)1, part_of(want, all));
             // the bin in which the running sum reaches it
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < kBinsEach; ++j) {
                 const u64 before = by_weight ? upw : (u64)upc, mine = by_weight ? w2[j] : (u64)c2[j];
                 if (before < want && before + mine >= want) {
-                    s.bin = 2 * tid + j;
+                    s.bin = kBinsEach * tid + j;
                     s.mass = before;
                     s.before = upc;
                 }
@@ -961,30 +1020,30 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
         const u64 w = weight(d, rate);
         return w >= least ? w : 0;
     };
-    const bool summed = bin_cut < kOctaves;  // the warps' sums are there
+    const bool summed = bin_cut < kSteps;  // the warps' sums are there
     if (!summed) {
         u64 sum = 0;
         if (cut_key == ~0ull && top < INFINITY) {  // nothing is cut off
-            for (int g = g0 + lane; g < g1; g += 32) {
-                float y[VEC];
-                load(g, y);
+            auto add = [&](auto all) {  // all: no weight is too small to stay
+                each([&](const float (&y)[VEC], int) {
 #pragma unroll
-                for (int i = 0; i < VEC; i += 2) {
-                    const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
+                    for (int i = 0; i < VEC; i += 2) {
+                        const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
-                        if (w.y[j] <= 40.0f && wj >= least) sum += wj;
+                        for (int j = 0; j < 2; ++j) {
+                            const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
+                            if (w.y[j] <= 40.0f && (decltype(all)::value || wj >= least)) sum += wj;
+                        }
                     }
-                }
-            }
+                });
+            };
+            if (least <= 1) add(Yes{});
+            else add(No{});
         } else {
-            for (int g = g0 + lane; g < g1; g += 32) {
-                float y[VEC];
-                load(g, y);
+            each([&](const float (&y)[VEC], int at) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum += kept(y[i], g * VEC - mis + i);
-            }
+                for (int i = 0; i < VEC; ++i) sum += kept(y[i], at + i);
+            });
         }
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
@@ -1014,10 +1073,8 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
     }
 
     if constexpr (PROBS) {
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC], p[VEC];
-            load(g, y);
-            const int e = g * VEC - mis;
+        each([&](const float (&y)[VEC], int e) {
+            float p[VEC];
             if (top < INFINITY && (cut_key == ~0ull || summed)) {
 #pragma unroll
                 for (int i = 0; i < VEC; i += 2) {
@@ -1042,7 +1099,7 @@ __global__ void __launch_bounds__(kTThreads, 2) sample_kernel(const SampleArgs a
                 for (int i = 0; i < VEC; ++i)
                     if ((unsigned)(e + i) < (unsigned)V) out[e + i] = p[i];
             }
-        }
+        });
     } else {
         const u64 at = draw_at(total);
         if (at >= first && at < first + s.bsum) {  // this block's slice has it: which warp's part
@@ -1082,12 +1139,13 @@ template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     int cluster = 1;
     while (cluster < kMaxTCluster && a.V > 4096 * cluster) cluster *= 2;
-    // a block's slice, as the kernel cuts it (one group more where rows do not start on 16 bytes)
-    const long long groups = a.V / (16 / sizeof(T)) + 2;
-    const long long per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 31) / 32 * 32;
+    // a block's slice, as the kernel cuts it (rows that do not start on 16 bytes may take a group more)
+    constexpr int VEC = 16 / sizeof(T);
+    const long long groups = (a.V + (a.ld % VEC ? VEC - 1 : 0) + VEC - 1) / VEC;
+    const long long per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 7) / 8 * 8;
     const int slice = (int)std::min<long long>(per_warp * kTWarps * 16, kStage + 1);
     const int staged = slice <= kStage;
-    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0);
+    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster > 1 ? 0 : kList * 8);
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1095,7 +1153,7 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(sample_kernel<T, PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(TokenShared) + 16 + kStage);
+                                 (int)sizeof(TokenShared) + 16 + kStage + kList * 8);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
