@@ -12,8 +12,8 @@
 //   - top-k: the k-th largest of the threads' own largest logits is at most the k-th largest of all, so that
 //     little more than k elements reach it; the first block sorts those, and all that follows (min-p,
 //     top-p, the draw) is done on them;
-//   - top-p alone: the weights go into a histogram by y in sixteenths of an octave, the bin in which the sum
-//     reaches the share is sorted, the elements before it stay;
+//   - top-p alone: a histogram of y tells about where the weights reach the share; the elements there are
+//     sorted, those before them added up;
 //   - neither: the weights are added up as they lie.
 // Where more elements than the sort takes are alike (or k is larger than that), the digits of
 // d = max - x >= 0 are narrowed down by one histogram after another instead.
@@ -30,7 +30,7 @@ typedef unsigned long long u64;
 constexpr int kTThreads = 256, kTWarps = kTThreads / 32;
 constexpr int kMaxTCluster = 8;
 constexpr int kBins = 1024;      // of the digits' histograms, and of the sort
-constexpr int kOctaves = 41, kParts = 16;  // the histogram by y: y <= 40 in sixteenths
+constexpr int kOctaves = 41, kParts = 64;  // the histogram by y: y <= 40 in 64ths
 constexpr int kSteps = kOctaves * kParts;
 constexpr int kList = 2048;      // elements that the first block sorts,
 constexpr int kOwn = 704;        // and that a block of a cluster finds
@@ -41,10 +41,9 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr int kEach = kList / kTThreads, kBinsEach = kBins / kTThreads;
 
 struct TokenShared {
-    float tmax[kTThreads];          // the threads' largest logits
     float wmax[kTWarps], wlow[kTWarps], bmax;      // bmax, bsum, bmin ..: read by the cluster
     int bmin;
-    u64 wsum[kTWarps], bsum;
+    u64 wsum[kTWarps], bsum, wevery[kTWarps], bevery;
     int wcount[kTWarps], bcount;
     u64 tsum[kTWarps];
     int tcount[kTWarps];
@@ -53,18 +52,16 @@ struct TokenShared {
     int bin;                        // the bin in which the wanted rank or weight lies,
     int before;                     // and what is before it
     u64 mass;
-    u64 wstep[kParts];              // weights by step of an octave
+    float wstep[2][kParts];         // about the weights by step of two octaves
     int cut;
     int listed;                     // elements in list
     u64 cut_key, total;             // of the first block: what stays, its sum
-    u64 octave[kOctaves];           // weights of this block by octave
+    float octave[kOctaves], all8[kOctaves];  // about the weights of this block by octave, and of all
     u64 list[kOwn];                 // this block's elements: bits of d, index
     union {
         u64 sort[kList];
         int tally[kList];           // counts of the search for the k-th
-        struct {
-            uint32_t low[kSteps], high[kSteps];  // the weights' (as integers of 24 bits) low 12 bits and the rest
-        } y;
+        uint32_t steps[kSteps];     // elements by y
         struct {
             uint32_t count[kBins], low[kBins];
             u64 high[kBins];
@@ -87,13 +84,14 @@ __device__ __forceinline__ float exp2_of(float f) {
 __device__ __forceinline__ u64 weight(float d, float rate) {
     const float y = __fmul_rn(d, rate);
     if (!(y <= 40.0f)) return 0;
-    const float n = floorf(y);
-    const uint32_t m = (uint32_t)(exp2_of(__fsub_rn(y, n)) * 16777216.0f);  // 2^23 .. 2^24
-    return ((u64)m << 16) >> (int)n;
+    // without conversions: adding 2^23 towards zero leaves floor(y) in the low bits, and a p in [1/2, 1] is its own
+    // bits less those of 1/4 (in units of 2^-24)
+    const float t = __fadd_rz(y, 8388608.0f);
+    const uint32_t m = __float_as_uint(exp2_of(__fsub_rn(y, __fsub_rn(t, 8388608.0f)))) - 0x3E800000u;  // 2^23 .. 2^24
+    return ((u64)m << 16) >> (__float_as_uint(t) & 63u);
 }
 
-// The same for two elements at a time, without conversions: adding 2^23 towards zero leaves floor(y) in the
-// low bits, and a p in [1/2, 1] is its own bits less those of 1/4 (in units of 2^-24).
+// The same for two elements at a time.
 struct Two {
     float y[2];
     uint32_t n[2], m[2];  // w = (m << 16) >> n where y <= 40
@@ -324,7 +322,10 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
     // a block by itself may find as many elements as are sorted: its list lies behind the slice
     u64 *const list = cluster > 1 ? s.list : reinterpret_cast<u64 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16);
     const int own = cluster > 1 ? kOwn : kList;
-    uint4 *const stage = reinterpret_cast<uint4 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16 + (cluster > 1 ? 0 : kList * 8));
+    // the threads' largest logits, kept apart by fourths of their groups (halves of four blocks, none of eight)
+    const int subs = cluster >= 8 ? 1 : cluster == 4 ? 2 : 4;
+    float *const tmax = reinterpret_cast<float *>(memory + (sizeof(TokenShared) + 15) / 16 * 16 + (cluster > 1 ? 0 : kList * 8));
+    uint4 *const stage = reinterpret_cast<uint4 *>(tmax + subs * kTThreads);
     pdl_trigger();
     pdl_wait();
     using L = Logit<T>;
@@ -393,9 +394,10 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
     auto of64 = [&](const void *p, int c) { return cluster > 1 ? ld_cluster64(map_to_rank(p, c)) : *static_cast<const u64 *>(p); };
 
     // ---------------------------------------------------------------- the largest
-    float top = -INFINITY;
+    float top;
     {
         constexpr int U = 4;  // loads in flight
+        float m[U] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         int g = g0 + lane;
         for (; g + 32 * (U - 1) < g1; g += 32 * U) {
             uint4 w[U];
@@ -407,20 +409,30 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
                 float y[VEC];
                 L::unpack(w[j], y);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) top = fmaxf(top, y[i]);
+                for (int i = 0; i < VEC; ++i) m[j] = fmaxf(m[j], y[i]);
             }
         }
-        for (; g < g1; g += 32) {
+#pragma unroll
+        for (int j = 0; j < U - 1; ++j, g += 32) {
+            if (g >= g1) break;
             const uint4 w = fetch(g);
             if (staged) stage[g - b0] = w;
             float y[VEC];
             L::unpack(w, y);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) top = fmaxf(top, y[i]);
+            for (int i = 0; i < VEC; ++i) m[j] = fmaxf(m[j], y[i]);
         }
+        if (subs == 4) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) tmax[j * kTThreads + tid] = m[j];
+        }
+        m[0] = fmaxf(m[0], m[2]);
+        m[1] = fmaxf(m[1], m[3]);
+        if (subs == 2) tmax[tid] = m[0], tmax[kTThreads + tid] = m[1];
+        top = fmaxf(m[0], m[1]);
+        if (subs == 1) tmax[tid] = top;
     }
-    s.tmax[tid] = top;
-    float wtop = top, wlow = top > -INFINITY ? top : INFINITY;  // of those that have any
+    float wtop = top, wlow = top > -INFINITY ? top : INFINITY;  // (of the threads that have any)
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         wtop = fmaxf(wtop, __shfl_xor_sync(0xFFFFFFFFu, wtop, m));
@@ -532,24 +544,25 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
     const u64 top2 = two(top, top), rate2 = two(rate, rate), zero2 = two(minus_zero, minus_zero);
     // what the sort finds to stay: elements up to cut_key in the order of (bits of d, index)
     u64 cut_key = ~0ull;
-    int bin_cut = kSteps;    // of the histogram by y: the elements of lower bins stay, of this one those up to cut_key
-    bool done = false;      // the cut is found
+    bool done = false;      // the cut is found,
+    bool summed = false;    // and the sums of what stays in each warp's part
 
     // ---------------------------------------------------------------- top-k by a few candidates
     const bool few = V <= kList && (k < V || nucleus);
     constexpr int kMax8 = kTThreads / 8;
-    const int g8 = kMax8 * cluster, gt = kTThreads * cluster;  // maxima of eight threads, of one
+    const int g8 = kMax8 * cluster, gt = kTThreads * cluster * subs;  // maxima of eight threads, of (a part of) one
     if (top < INFINITY && (few || (k < V && 2 * k <= gt))) {
         float least_value = -INFINITY;
         if (!few) {
-            // (a little below) the k-th largest of the maxima; at most eight a thread
+            // (a little below) the k-th largest of the maxima
             uint32_t v[kMaxTCluster];
-            const int nv = 2 * k <= g8 ? 1 : cluster;
+            const int nv = 2 * k <= g8 ? 1 : cluster * subs;  // at most eight
             if (nv == 1) {
                 v[0] = tid < g8 ? order_of(__uint_as_float(of32(&s.max8[tid % kMax8], tid / kMax8))) : 0u;
             } else {
 #pragma unroll
-                for (int c = 0; c < kMaxTCluster; ++c) v[c] = c < cluster ? order_of(__uint_as_float(of32(&s.tmax[tid], c))) : 0u;
+                for (int c = 0; c < kMaxTCluster; ++c)
+                    v[c] = c < nv ? order_of(__uint_as_float(of32(&tmax[c / cluster * kTThreads + tid], c % cluster))) : 0u;
             }
             // a histogram between the least and the largest of them, finer again where those are far apart; what
             // lies above the bins counts in the first one
@@ -690,109 +703,167 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
         __syncthreads();
     }
 
-    // ---------------------------------------------------------------- top-p by the histogram of y
+    // ---------------------------------------------------------------- top-p by a histogram of y
+    // Weights of 11 bits in each 64th of an octave tell to a thousandth (of the smaller side) where they reach the
+    // share.  The elements there are sorted, everything else is added up
+    // exactly, and if the cut is not among them after all the digits below find it.
     if (!done && nucleus && k == V && top < INFINITY) {
-        for (int i = tid; i < kSteps; i += kTThreads) s.y.low[i] = s.y.high[i] = 0;
+        for (int i = tid; i < kSteps; i += kTThreads) s.steps[i] = 0;
         __syncthreads();
+        const float farthest = least > 1 ? fminf(40.0f, 40.001f - log2f((float)least)) : 40.0f;
+        const u64 eighths = two(8.0f * kParts, 8.0f * kParts), big = two(8388608.0f, 8388608.0f);
         each([&](const float (&y)[VEC], int) {
 #pragma unroll
             for (int i = 0; i < VEC; i += 2) {
-                const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!(w.y[j] <= 40.0f) || ((u64)w.m[j] << 16) >> w.n[j] < least) continue;
-                    const int bin = (int)(__float_as_uint(__fadd_rz(w.y[j] * (float)kParts, 8388608.0f)) & 1023u);
-                    const uint32_t v = w.n[j] > 16 ? w.m[j] >> (w.n[j] - 16) : w.m[j];
-                    atomicAdd(&s.y.low[bin], v & 0xFFFu);
-                    atomicAdd(&s.y.high[bin], v >> 12);
-                }
+                const u64 z = mul2(less2(top2, two(y[i], y[i + 1])), rate2, zero2);
+                u64 t;
+                asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(z), "l"(eighths), "l"(big));
+                float y0, y1, t0, t1;
+                apart(z, y0, y1);
+                apart(t, t0, t1);
+                const uint32_t q0 = __float_as_uint(t0) & 0x7FFFu, q1 = __float_as_uint(t1) & 0x7FFFu;
+                // 2048 less what an eighth of a step takes off: at most 2^20 elements
+                if (y0 <= farthest) atomicAdd(&s.steps[q0 >> 3], (16373u - 22u * (q0 & 7)) >> 3);
+                if (y1 <= farthest) atomicAdd(&s.steps[q1 >> 3], (16373u - 22u * (q1 & 7)) >> 3);
             }
         });
         __syncthreads();
-        // a step's weights are integers of 24 bits that are (m << 16) >> n shifted down by what n leaves
-        auto unit = [](int octave) { return octave < 16 ? 16 - octave : 0; };
+        // the weight of a step, in units of its octave's largest
+        auto step_mass = [&](uint32_t v, int step) { return (float)v * exp2f(-11.0f - (float)step / kParts); };
         const int o = tid / 4, c0 = tid % 4;  // four threads an octave
-        static_assert(kTThreads / 4 >= kOctaves && kTThreads / 2 == 8 * kParts, "threads an octave, and a step and block");
+        static_assert(kTThreads / 4 >= kOctaves && kTThreads == 4 * kParts, "threads an octave, and a step");
         {
-            u64 v = 0;
+            float v = 0.0f;
+            if (o < kOctaves)
+#pragma unroll 4
+                for (int j = c0; j < kParts; j += 4) v += step_mass(s.steps[o * kParts + j], j);
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
+            v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
+            if (c0 == 0 && o < kOctaves) s.octave[o] = v * exp2f(-(float)o);
+        }
+        barrier();
+        // two octaves, then the steps in them: where the share less and more a thousandth lies (every block for itself)
+        int edge[2];
+        {
+            float v = 0.0f;
             if (o < kOctaves) {
-#pragma unroll
-                for (int j = 0; j < kParts / 4; ++j) {
-                    const int bin = o * kParts + c0 * (kParts / 4) + j;
-                    v += s.y.low[bin] + ((u64)s.y.high[bin] << 12);
-                }
+                if (c0 < cluster) v = __uint_as_float(of32(&s.octave[o], c0));
+                if (c0 + 4 < cluster) v += __uint_as_float(of32(&s.octave[o], c0 + 4));
             }
             v += __shfl_xor_sync(0xFFFFFFFFu, v, 1);
             v += __shfl_xor_sync(0xFFFFFFFFu, v, 2);
-            if (c0 == 0 && o < kOctaves) s.octave[o] = v << unit(o);
-        }
-        barrier();
-        // the octave in which the sum reaches the share of all; then the step inside it
-        u64 cut, below;
-        {
-            u64 mass = 0;
-            if (o < kOctaves) {  // two blocks' sums a thread
-                if (c0 < cluster) mass = of64(&s.octave[o], c0);
-                if (c0 + 4 < cluster) mass += of64(&s.octave[o], c0 + 4);
-            }
-            // what an octave's threads hold is added up by the sum over them
-            u64 all, before = sum_before(mass, s, all);
-            cut = max((u64)1, part_of(pfix, all));
-            u64 whole = mass + __shfl_xor_sync(0xFFFFFFFFu, mass, 1);
-            whole += __shfl_xor_sync(0xFFFFFFFFu, whole, 2);
-            if (c0 == 0 && before < cut && before + whole >= cut) s.bin = o, s.mass = before;
+            if (c0 == 0 && o < kOctaves) s.all8[o] = v;
             __syncthreads();
-            const int octave = s.bin;
-            if (warp < 4) {  // 16 steps, eight blocks: a thread each
-                const int step = tid / 8, c = tid % 8;
-                u64 v = 0;
-                if (c < cluster)
-                    v = of32(&s.y.low[octave * kParts + step], c) + ((u64)of32(&s.y.high[octave * kParts + step], c) << 12);
+            // two of them a lane, in every warp: the sums before each
+            auto sums = [&](const float *m, int n, float &m0, float &m1, float &all_) {
+                m0 = 2 * lane < n ? m[2 * lane] : 0.0f;
+                m1 = 2 * lane + 1 < n ? m[2 * lane + 1] : 0.0f;
+                float up = m0 + m1;
 #pragma unroll
-                for (int m = 1; m < 8; m <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-                if (c == 0) s.wstep[step] = v << unit(octave);
+                for (int i = 1; i < 32; i <<= 1) {
+                    const float x = __shfl_up_sync(0xFFFFFFFFu, up, i);
+                    if (lane >= i) up += x;
+                }
+                all_ = __shfl_sync(0xFFFFFFFFu, up, 31);
+                m1 = up;        // up to the second,
+                m0 = up - (2 * lane + 1 < n ? m[2 * lane + 1] : 0.0f);  // and up to the first
+            };
+            // the first that passes `want` (the last of n if none does)
+            auto first = [&](float m0, float m1, float want, int n) {
+                const uint32_t f = __ballot_sync(0xFFFFFFFFu, m0 > want), g = __ballot_sync(0xFFFFFFFFu, m1 > want);
+                const int i = f ? 2 * (__ffs(f) - 1) : 64, j = g ? 2 * (__ffs(g) - 1) + 1 : 64;
+                return min(min(i, j), n - 1);
+            };
+            const float p0 = fmaxf(pp, 0.0f), slack = 0.003f * p0 * (1.0f - p0) + 1e-6f;
+            float m0, m1, whole, before[2];
+            sums(s.all8, kOctaves, m0, m1, whole);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float want = (e ? p0 + slack : p0 - slack) * whole;
+                edge[e] = first(m0, m1, want, kOctaves);
+                // what the octaves before it hold
+                const int at = edge[e] - 1;
+                const float a0 = __shfl_sync(0xFFFFFFFFu, m0, max(at, 0) / 2), a1 = __shfl_sync(0xFFFFFFFFu, m1, max(at, 0) / 2);
+                before[e] = want - (at < 0 ? 0.0f : at & 1 ? a1 : a0);
+            }
+            // four threads a step, two blocks' counts each
+            const int step = tid / 4;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float m = 0.0f;
+                if (c0 < cluster) m = step_mass(of32(&s.steps[edge[e] * kParts + step], c0), step);
+                if (c0 + 4 < cluster) m += step_mass(of32(&s.steps[edge[e] * kParts + step], c0 + 4), step);
+                m += __shfl_xor_sync(0xFFFFFFFFu, m, 1);
+                m += __shfl_xor_sync(0xFFFFFFFFu, m, 2);
+                if (c0 == 0) s.wstep[e][step] = m * exp2f(-(float)edge[e]);
             }
             __syncthreads();
-            below = s.mass;
-            int step = 0;
-            while (below + s.wstep[step] < cut) below += s.wstep[step++];
-            bin_cut = octave * kParts + step;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                sums(s.wstep[e], kParts, m0, m1, whole);
+                edge[e] = edge[e] * kParts + first(m0, m1, before[e], kParts);
+            }
         }
         barrier();  // (the histograms are read)
-        // that step's elements; the others' sums, a warp's part each, for the draw
-        u64 sum = 0;
-        const float from = (float)bin_cut * (1.0f / kParts), to = (float)(bin_cut + 1) * (1.0f / kParts);
-        each([&](const float (&y)[VEC], int at) {
+        u64 sum = 0, every = 0;
+        const float from = (float)edge[0] * (1.0f / kParts), to = (float)(edge[1] + 1) * (1.0f / kParts);
+        auto part_by = [&](auto all_stay) {  // all_stay: no weight is too small to stay
+            each([&](const float (&y)[VEC], int at) {
+                uint32_t here = 0;  // those of the steps in question
 #pragma unroll
-            for (int i = 0; i < VEC; i += 2) {
-                Two w;
-                if (PROBS) {
-                    apart(mul2(less2(top2, two(y[i], y[i + 1])), rate2, zero2), w.y[0], w.y[1]);
-                } else {
-                    w = weights2(y[i], y[i + 1], top2, rate2, zero2);
-                }
+                for (int i = 0; i < VEC; i += 2) {
+                    const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (!PROBS && w.y[j] < from) {
+                    for (int j = 0; j < 2; ++j) {
                         const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
-                        sum += wj >= least ? wj : 0;
+                        const bool real = w.y[j] <= 40.0f && (decltype(all_stay)::value || wj >= least);
+                        if (real) every += wj;
+                        if (real && w.y[j] < from) sum += wj;
+                        here |= real && w.y[j] >= from && w.y[j] < to ? 1u << (i + j) : 0u;
                     }
-                    if (w.y[j] >= from && w.y[j] < to && w.y[j] <= 40.0f &&
-                        (least <= 1 || weight(distance(y[i + j]), rate) >= least))
-                        keep_in_list(y[i + j], at + i + j);
                 }
-            }
-        });
-        if (!PROBS) {
+                while (here) {
+                    const int i = __ffs(here) - 1;
+                    here &= here - 1;
+                    float v = y[0];
 #pragma unroll
-            for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-            if (lane == 0) s.wsum[warp] = sum;
+                    for (int j = 1; j < VEC; ++j) v = i == j ? y[j] : v;
+                    keep_in_list(v, at + i);
+                }
+            });
+        };
+        if (least <= 1) part_by(Yes{});
+        else part_by(No{});
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+            every += __shfl_xor_sync(0xFFFFFFFFu, every, m);
+        }
+        if (lane == 0) s.wsum[warp] = sum, s.wevery[warp] = every;
+        __syncthreads();
+        if (warp == 0) {
+            u64 v = s.wsum[lane % kTWarps], w = s.wevery[lane % kTWarps];
+#pragma unroll
+            for (int m = kTWarps / 2; m > 0; m >>= 1) {
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+                w += __shfl_xor_sync(0xFFFFFFFFu, w, m);
+            }
+            if (lane == 0) s.bsum = v, s.bevery = w;
         }
         barrier();
         const int n = collect();
-        if (n <= kList) {
-            done = true;
+        bool found = n <= kList;
+        if (found) {
             if (rank == 0) {
+                u64 below = lane < cluster ? of64(&s.bsum, lane) : 0, all = lane < cluster ? of64(&s.bevery, lane) : 0;
+#pragma unroll
+                for (int m = kMaxTCluster / 2; m > 0; m >>= 1) {
+                    below += __shfl_xor_sync(0xFFFFFFFFu, below, m);
+                    all += __shfl_xor_sync(0xFFFFFFFFu, all, m);
+                }
+                below = __shfl_sync(0xFFFFFFFFu, below, 0);
+                const u64 cut = max((u64)1, part_of(pfix, __shfl_sync(0xFFFFFFFFu, all, 0)));
+                if (tid == 0) s.total = 0;
                 __syncthreads();
                 sort_list(s, reinterpret_cast<int *>(list), n);
                 u64 w[kEach], here = 0;
@@ -802,7 +873,7 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
                     w[i] = at < n ? weight(__uint_as_float((uint32_t)(s.sort[at] >> 20)), rate) : 0;
                     here += w[i];
                 }
-                u64 total, run = below + sum_before(here, s, total);
+                u64 run = below + sum_before(here, s, all);
 #pragma unroll
                 for (int i = 0; i < kEach; ++i) {
                     if (run < cut && run + w[i] >= cut) {
@@ -813,22 +884,26 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
                 }
             }
             barrier();
-            cut_key = of64(&s.cut_key, 0);
-            inv = 1.0f / (float)of64(&s.total, 0);
-            if (!PROBS) {
-                // this block's share of them, into the sums of the warps whose part they lie in (the first block has
-                // all of them sorted, and its own list no longer)
-                const u64 *const from_list = rank == 0 ? s.sort : list;
-                for (int i = tid; i < (rank == 0 ? n : s.listed); i += kTThreads) {
-                    const u64 key = from_list[i];
-                    const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
-                    if (key <= cut_key && part < kTWarps) atomicAdd(&s.wsum[part], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
-                }
-                __syncthreads();
+            const u64 kept_all = of64(&s.total, 0);
+            found = kept_all != 0;  // else the cut is elsewhere
+            if (found) {
+                done = summed = true;
+                cut_key = of64(&s.cut_key, 0);
+                inv = 1.0f / (float)kept_all;
             }
-        } else {
-            bin_cut = kSteps;
-            barrier();
+        }
+        if (!found) {
+            barrier();  // the sorted list is read
+        } else if (!PROBS) {
+            // this block's share of them, into the sums of the warps whose part they lie in (the first block has
+            // all of them sorted, and its own list no longer)
+            const u64 *const from_list = rank == 0 ? s.sort : list;
+            for (int i = tid; i < (rank == 0 ? n : s.listed); i += kTThreads) {
+                const u64 key = from_list[i];
+                const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
+                if (key <= cut_key && part < kTWarps) atomicAdd(&s.wsum[part], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
+            }
+            __syncthreads();
         }
     }
 
@@ -1020,7 +1095,6 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
         const u64 w = weight(d, rate);
         return w >= least ? w : 0;
     };
-    const bool summed = bin_cut < kSteps;  // the warps' sums are there
     if (!summed) {
         u64 sum = 0;
         if (cut_key == ~0ull && top < INFINITY) {  // nothing is cut off
@@ -1106,28 +1180,41 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
             u64 before = first;
             int w = 0;
             while (at >= before + s.wsum[w]) before += s.wsum[w++];
-            // the whole block over that part, a thread some elements one after another
-            const int from = (b0 + w * per_warp) * VEC, parts = (per_warp * VEC + kTThreads - 1) / kTThreads;
-            auto element = [&](int e) -> float {  // counted from the first group's first
-                if (staged) return L::one(reinterpret_cast<const T *>(stage) + (e - b0 * VEC));
-                e -= mis;
-                return (unsigned)e < (unsigned)V ? fmaxf(L::one(x + e), -INFINITY) : -INFINITY;
-            };
-            const int mine0 = from + tid * parts;
-            const int end = min(from + per_warp * VEC, groups * VEC);
+            // the whole block over that part, a thread some groups one after another; then a warp over those of one
+            const int p0 = b0 + w * per_warp, p1 = min(groups, p0 + per_warp), some = (per_warp + kTThreads - 1) / kTThreads;
+            const int mine0 = p0 + tid * some;
             u64 own = 0, all;
-            for (int i = 0; i < parts; ++i)
-                if (mine0 + i < end) own += kept(element(mine0 + i), mine0 + i - mis);
+            for (int g = mine0; g < min(p1, mine0 + some); ++g) {
+                float y[VEC];
+                load(g, y);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) own += kept(y[i], g * VEC - mis + i);
+            }
             before += sum_before(own, s, all);
-            if (at >= before && at < before + own) {
-                for (int i = 0; i < parts; ++i) {
-                    if (mine0 + i >= end) break;
-                    const u64 wi = kept(element(mine0 + i), mine0 + i - mis);
-                    if (at >= before && at < before + wi) {
-                        a.token[row] = mine0 + i - mis;
+            if (at >= before && at < before + own) s.bin = mine0, s.mass = before;
+            __syncthreads();
+            if (warp == 0) {
+                before = s.mass;
+                const int e0 = s.bin * VEC, e1 = min(e0 + some * VEC, p1 * VEC);
+                for (int e = e0; e < e1 && before <= at; e += 32) {
+                    float v = -INFINITY;
+                    const int index = e + lane - mis;
+                    if (e + lane < e1)
+                        v = staged ? L::one(reinterpret_cast<const T *>(stage) + (e + lane - b0 * VEC))
+                                   : (unsigned)index < (unsigned)V ? fmaxf(L::one(x + index), -INFINITY) : -INFINITY;
+                    const u64 wi = kept(v, index);
+                    u64 upto = wi;
+#pragma unroll
+                    for (int m = 1; m < 32; m <<= 1) {
+                        const u64 q = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+                        if (lane >= m) upto += q;
+                    }
+                    const u64 r = before + upto - wi;
+                    if (at >= r && at < r + wi) {
+                        a.token[row] = index;
                         a.p[row] = share(wi);
                     }
-                    before += wi;
+                    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
                 }
             }
         }
@@ -1137,15 +1224,20 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
 
 template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
+    // Blocks a row: eight unless fewer give each at most 4096 elements, or unless there are more rows than then run at
+    // once, four blocks an SM (192 rows of 131072: 67 us by eight blocks, %% by two).
     int cluster = 1;
     while (cluster < kMaxTCluster && a.V > 4096 * cluster) cluster *= 2;
+    while (cluster > 2 && (long long)a.N * cluster > 608) cluster /= 2;
     // a block's slice, as the kernel cuts it (rows that do not start on 16 bytes may take a group more)
     constexpr int VEC = 16 / sizeof(T);
     const long long groups = (a.V + (a.ld % VEC ? VEC - 1 : 0) + VEC - 1) / VEC;
     const long long per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 7) / 8 * 8;
     const int slice = (int)std::min<long long>(per_warp * kTWarps * 16, kStage + 1);
     const int staged = slice <= kStage;
-    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster > 1 ? 0 : kList * 8);
+    const int subs = cluster >= 8 ? 1 : cluster == 4 ? 2 : 4;
+    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster > 1 ? 0 : kList * 8) +
+                        subs * kTThreads * sizeof(float);
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1153,7 +1245,7 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(sample_kernel<T, PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(TokenShared) + 16 + kStage + kList * 8);
+                                 (int)sizeof(TokenShared) + 16 + kStage + kList * 8 + 4 * kTThreads * 4);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
