@@ -38,6 +38,7 @@ constexpr int kOwn = 704;        // and that a block of a cluster finds
 // of twice that (192 rows of 131072 bf16, k = 50: 53 us with two blocks of 512 threads).
 constexpr int kStage = 34 * 1024;
 constexpr uint32_t kInfBits = 0x7F800000u;
+constexpr int kMaxShared = 228 * 1024;  // an SM's, of which each block takes 1 KB more than it asks for
 constexpr int kEach = kList / kTThreads, kBinsEach = kBins / kTThreads;
 
 struct TokenShared {
@@ -319,12 +320,13 @@ template <typename T, bool PROBS>
 __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
     extern __shared__ __align__(16) uint8_t memory[];
     TokenShared &s = *reinterpret_cast<TokenShared *>(memory);
-    // a block by itself may find as many elements as are sorted: its list lies behind the slice
-    u64 *const list = cluster > 1 ? s.list : reinterpret_cast<u64 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16);
-    const int own = cluster > 1 ? kOwn : kList;
+    // one of a few blocks may find as many elements as are sorted: its list lies behind
+    const bool long_list = cluster < 8;
+    u64 *const list = long_list ? reinterpret_cast<u64 *>(memory + (sizeof(TokenShared) + 15) / 16 * 16) : s.list;
+    const int own = long_list ? kList : kOwn;
     // the threads' largest logits, kept apart by fourths of their groups (halves of four blocks, none of eight)
     const int subs = cluster >= 8 ? 1 : cluster == 4 ? 2 : 4;
-    float *const tmax = reinterpret_cast<float *>(memory + (sizeof(TokenShared) + 15) / 16 * 16 + (cluster > 1 ? 0 : kList * 8));
+    float *const tmax = reinterpret_cast<float *>(memory + (sizeof(TokenShared) + 15) / 16 * 16 + (long_list ? kList * 8 : 0));
     uint4 *const stage = reinterpret_cast<uint4 *>(tmax + subs * kTThreads);
     pdl_trigger();
     pdl_wait();
@@ -1224,11 +1226,12 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
 
 template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
-    // Blocks a row: eight unless fewer give each at most 4096 elements, or unless there are more rows than then run at
-    // once, four blocks an SM (192 rows of 131072: 67 us by eight blocks, %% by two).
+    // Blocks a row: eight unless fewer give each at most 4096 elements, or unless that is more than eight blocks an SM
+    // in all, two turns of four (192 rows of 131072 that ask for different things: 62 us by eight blocks, 61 by four,
+    // 71 by two; for top-k alone 37, 30, 25; 48 rows 41, 58, 89).
     int cluster = 1;
     while (cluster < kMaxTCluster && a.V > 4096 * cluster) cluster *= 2;
-    while (cluster > 2 && (long long)a.N * cluster > 608) cluster /= 2;
+    while (cluster > 2 && (long long)a.N * cluster > 1216) cluster /= 2;
     // a block's slice, as the kernel cuts it (rows that do not start on 16 bytes may take a group more)
     constexpr int VEC = 16 / sizeof(T);
     const long long groups = (a.V + (a.ld % VEC ? VEC - 1 : 0) + VEC - 1) / VEC;
@@ -1236,8 +1239,13 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     const int slice = (int)std::min<long long>(per_warp * kTWarps * 16, kStage + 1);
     const int staged = slice <= kStage;
     const int subs = cluster >= 8 ? 1 : cluster == 4 ? 2 : 4;
-    const size_t smem = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster > 1 ? 0 : kList * 8) +
+    const size_t need = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster < 8 ? kList * 8 : 0) +
                         subs * kTThreads * sizeof(float);
+    // No more blocks an SM than an even share of them (the call's first blocks are placed while the kernel before
+    // still holds some of the SMs: four on one and one on the next took twice as long): what the shares leave free
+    // is asked for too.
+    const int share = (int)std::max(1LL, std::min(4LL, ((long long)a.N * cluster + 151) / 152));
+    const size_t smem = std::max(need, (size_t)(kMaxShared / share - 1024 - 512));
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1245,7 +1253,7 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
         e = cudaFuncSetAttribute(sample_kernel<T, PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(TokenShared) + 16 + kStage + kList * 8 + 4 * kTThreads * 4);
+                                 kMaxShared - 1024);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
