@@ -16,6 +16,7 @@ namespace bsf8 {
 namespace {
 
 constexpr int kMaxWarps = 32;
+constexpr int kMaxRow = 4 * 3 * 1024 * 16;  // bytes of the longest row's pieces: 192 KB
 
 __device__ __forceinline__ void widen8(const uint4 &w, float (&y)[8]) {
     const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -36,165 +37,168 @@ __device__ __forceinline__ uint4 narrow8(const float (&y)[8]) {
     return make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7]));
 }
 
-// Eight channels of a row of x, and of the residual.
-template <bool F32>
-struct Piece {
-    uint4 x, r, r2;
+__device__ __forceinline__ void async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
-    __device__ __forceinline__ void load(const NormArgs &a, long long row, int c) {
-        x = *reinterpret_cast<const uint4 *>(a.x + row * a.ldx + c);
-        if (!a.residual) return;
-        if constexpr (F32) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(a.residual) + row * a.ldr + c);
-            r = p[0];
-            r2 = p[1];
-        } else {
-            r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.residual) + row * a.ldr + c);
-        }
+// Eight channels of the residual.
+template <bool F32>
+__device__ __forceinline__ const uint4 *residual_at(const NormArgs &a, long long row, int c) {
+    return reinterpret_cast<const uint4 *>(static_cast<const char *>(a.residual) + (row * a.ldr + c) * (F32 ? 4 : 2));
+}
+
+template <bool F32>
+__device__ __forceinline__ void residual_of(const uint4 &r, const uint4 &r2, float (&y)[8]) {
+    if constexpr (F32) {
+        y[0] = __uint_as_float(r.x), y[1] = __uint_as_float(r.y), y[2] = __uint_as_float(r.z), y[3] = __uint_as_float(r.w);
+        y[4] = __uint_as_float(r2.x), y[5] = __uint_as_float(r2.y), y[6] = __uint_as_float(r2.z), y[7] = __uint_as_float(r2.w);
+    } else {
+        widen8(r, y);
     }
-    __device__ __forceinline__ void residual(float (&y)[8]) const {
-        if constexpr (F32) {
-            y[0] = __uint_as_float(r.x), y[1] = __uint_as_float(r.y), y[2] = __uint_as_float(r.z), y[3] = __uint_as_float(r.w);
-            y[4] = __uint_as_float(r2.x), y[5] = __uint_as_float(r2.y), y[6] = __uint_as_float(r2.z), y[7] = __uint_as_float(r2.w);
-        } else {
-            widen8(r, y);
-        }
-    }
-};
+}
 
 }  // namespace
 
-// P pieces of 8 channels a thread; `warps` warps a row, blockDim / (32 warps) rows a block at a time.
+// P pieces of 8 channels a thread; `warps` warps a row, blockDim / (32 warps) rows a block.  Few rows: one piece a
+// thread, its loads straight to registers (P = 1).  Many: four pieces a thread, which go to shared memory by the
+// thread's own asynchronous copies (nothing is handed from thread to thread there) and wait there for the row's first
+// sum; with few threads a row six blocks and more share an SM, so that the loads, sums and stores of one run under
+// those of the others.  (8191 rows of 5120: 122 us with 640 threads a row and the next row's loads in registers, 168
+// with 320 threads and two rows ahead in shared memory, %% so.)
 template <int P, bool F32>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps) {
+    constexpr int WORDS = F32 ? 3 : 2;  // of 16 bytes a piece: x, the residual
     __shared__ float s_sum[2][kMaxWarps];
+    extern __shared__ uint4 ring[];
     pdl_trigger();
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = warp / warps, w0 = sub * warps;             // the block's row, its first warp
     const int t = (int)threadIdx.x - 32 * w0, threads = 32 * warps;
     const int rows = (int)(blockDim.x >> 5) / warps;
-    const int pieces = a.H / 8;
+    const int step = (int)blockDim.x;
     const float inv = 1.0f / (float)a.H;
-    uint4 wv[P], pv[P], gv[P];
+    const long long row = (long long)blockIdx.x * rows + sub;
+    const bool real = row < a.M, full = a.gate_kind == kGateFull;
+    auto slot = [&](int p) { return ring + (size_t)p * WORDS * step + threadIdx.x; };
+    uint4 x0, r0, r1;  // P = 1
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int c = 8 * (t + p * threads);
-        wv[p] = pv[p] = gv[p] = make_uint4(0, 0, 0, 0);
-        if (c < a.H) {
-            if (a.weight) wv[p] = *reinterpret_cast<const uint4 *>(a.weight + c);
-            if (a.post) pv[p] = *reinterpret_cast<const uint4 *>(a.post + c);
-            if (a.gate_kind == kGateChannel) gv[p] = *reinterpret_cast<const uint4 *>(a.gate + c);
+        if (!real || c >= a.H) continue;
+        if constexpr (P == 1) {
+            x0 = *reinterpret_cast<const uint4 *>(a.x + row * a.ldx + c);
+            if (a.residual) {
+                r0 = residual_at<F32>(a, row, c)[0];
+                if (F32) r1 = residual_at<F32>(a, row, c)[1];
+            }
+        } else {
+            async16(slot(p), a.x + row * a.ldx + c);
+            if (a.residual) {
+                async16(slot(p) + step, residual_at<F32>(a, row, c));
+                if (F32) async16(slot(p) + 2 * step, residual_at<F32>(a, row, c) + 1);
+            }
         }
     }
+    if constexpr (P > 1) asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    auto vec = [&](const uint16_t *v, int p) { return *reinterpret_cast<const uint4 *>(v + 8 * (t + p * threads)); };
     // the sum of v over the row's threads
-    uint32_t sums = 0;  // two sets of slots in turn: one is written again after the barrier of the other
-    auto row_sum = [&](float v) {
+    auto row_sum = [&](float v, int which) {
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
         if (warps == 1) return v;
-        float *const at = s_sum[sums++ & 1];
-        if (lane == 0) at[warp] = v;
+        if (lane == 0) s_sum[which][warp] = v;
         __syncthreads();
-        v = 0.0f;
-        for (int w = 0; w < warps; ++w) v += at[w0 + w];
+        v = lane < warps ? s_sum[which][w0 + lane] : 0.0f;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
         return v;
     };
-    const long long step = (long long)gridDim.x * rows;
-    Piece<F32> next[P];
-    const long long first = (long long)blockIdx.x * rows;
-    auto load = [&](long long row) {
-        if (row >= a.M) return;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-            if (t + p * threads < pieces) next[p].load(a, row, 8 * (t + p * threads));
-    };
-    load(first + sub);
-    for (long long base = first; base < a.M; base += step) {  // the same turns for every thread: barriers
-        const long long row = base + sub;
-        const bool real = row < a.M;
-        float z[P][8];
-        float ss = 0.0f;
+    float f = a.scale;
+    if (a.gate_kind == kGateToken && real) f *= __uint_as_float((uint32_t)a.gate[row * a.ldg] << 16);
+    float z[P][8];
+    float ss = 0.0f;
+    if (a.post) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            if (!real || t + p * threads >= pieces) {
+            if (!real || 8 * (t + p * threads) >= a.H) continue;
+            widen8(P == 1 ? x0 : *slot(p), z[p]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[p][i] = 0.0f;
-                continue;
-            }
-            widen8(next[p].x, z[p]);
-            if (a.post) {
+            for (int i = 0; i < 8; ++i) ss = fmaf(z[p][i], z[p][i], ss);
+        }
+    }
+    const float n = a.post ? rsqrtf(fmaf(row_sum(ss, 0), inv, a.eps)) : 1.0f;
+    ss = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(z[p][i], z[p][i], ss);
+    for (int p = 0; p < P; ++p) {
+        const int c = 8 * (t + p * threads);
+        if (!real || c >= a.H) continue;
+        const uint4 *const at = slot(p);
+        float g[8];
+        widen8(P == 1 ? x0 : at[0], z[p]);
+        if (a.post) {
+            widen8(vec(a.post, p), g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[p][i] = z[p][i] * n * g[i];
+        }
+        if (full || a.gate_kind == kGateChannel) {
+            widen8(vec(full ? a.gate + row * a.ldg : a.gate, p), g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[p][i] *= g[i];
+        }
+        float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (a.residual) residual_of<F32>(P == 1 ? r0 : at[step], P == 1 ? r1 : at[F32 ? 2 * step : 0], r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            z[p][i] = fmaf(f, z[p][i], r[i]);
+            ss = fmaf(z[p][i], z[p][i], ss);
+        }
+        if (a.r_out) {
+            if constexpr (F32) {
+                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.r_out) + row * a.H + c);
+                o[0] = make_float4(z[p][0], z[p][1], z[p][2], z[p][3]);
+                o[1] = make_float4(z[p][4], z[p][5], z[p][6], z[p][7]);
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.r_out) + row * a.H + c) = narrow8(z[p]);
             }
         }
-        float f = a.scale;
-        if (a.gate_kind == kGateToken && real) f *= __uint_as_float((uint32_t)a.gate[row * a.ldg] << 16);
-        const float n = a.post ? rsqrtf(fmaf(row_sum(ss), inv, a.eps)) : 1.0f;
-        ss = 0.0f;
+    }
+    if (!a.h) return;
+    const float k = rsqrtf(fmaf(row_sum(ss, 1), inv, a.eps));
+    if (!real) return;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int c = 8 * (t + p * threads);
-            if (!real || c >= a.H) continue;
-            float g[8];
-            if (a.post) {
-                widen8(pv[p], g);
+    for (int p = 0; p < P; ++p) {
+        const int c = 8 * (t + p * threads);
+        if (c >= a.H) continue;
+        float g[8];
+        widen8(vec(a.weight, p), g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[p][i] = z[p][i] * n * g[i];
-            }
-            if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) {
-                if (a.gate_kind == kGateFull) gv[p] = *reinterpret_cast<const uint4 *>(a.gate + row * a.ldg + c);
-                widen8(gv[p], g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) z[p][i] *= g[i];
-            }
-            float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (a.residual) next[p].residual(r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                z[p][i] = fmaf(f, z[p][i], r[i]);
-                ss = fmaf(z[p][i], z[p][i], ss);
-            }
-        }
-        load(row + step);  // the next row's, while this one's sum goes round
-        if (a.r_out && real) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                const int c = 8 * (t + p * threads);
-                if (c >= a.H) continue;
-                if constexpr (F32) {
-                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.r_out) + row * a.H + c);
-                    o[0] = make_float4(z[p][0], z[p][1], z[p][2], z[p][3]);
-                    o[1] = make_float4(z[p][4], z[p][5], z[p][6], z[p][7]);
-                } else {
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.r_out) + row * a.H + c) = narrow8(z[p]);
-                }
-            }
-        }
-        if (!a.h) continue;
-        const float k = rsqrtf(fmaf(row_sum(ss), inv, a.eps));
-        if (!real) continue;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int c = 8 * (t + p * threads);
-            if (c >= a.H) continue;
-            float g[8];
-            widen8(wv[p], g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= z[p][i] * k;
-            *reinterpret_cast<uint4 *>(a.h + row * a.H + c) = narrow8(g);
-        }
+        for (int i = 0; i < 8; ++i) g[i] *= z[p][i] * k;
+        *reinterpret_cast<uint4 *>(a.h + row * a.H + c) = narrow8(g);
     }
 }
 
 template <int P, bool F32>
 cudaError_t norm_pieces(const NormArgs &a, cudaStream_t stream) {
     const int warps = (a.H / 8 + 32 * P - 1) / (32 * P);
-    const int rows = warps >= 8 ? 1 : 8 / warps;
+    const int rows = warps >= 5 ? 1 : 8 / warps, threads = rows * warps * 32;
+    const size_t smem = P == 1 ? 0 : (size_t)P * (F32 ? 3 : 2) * threads * sizeof(uint4);
+    if (P > 1) {
+        static int configured[64] = {0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+            e = cudaFuncSetAttribute(norm_kernel<P, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRow);
+            if (e != cudaSuccess) return e;
+            __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    const int per_sm = std::max(1, 2048 / (rows * warps * 32));
-    cfg.gridDim = dim3((unsigned)std::min<long long>(((long long)a.M + rows - 1) / rows, 152LL * per_sm), 1, 1);
-    cfg.blockDim = dim3((unsigned)(rows * warps * 32), 1, 1);
+    cfg.gridDim = dim3((unsigned)(((long long)a.M + rows - 1) / rows), 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -204,10 +208,14 @@ cudaError_t norm_pieces(const NormArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, norm_kernel<P, F32>, a, warps);
 }
 
+template <bool F32>
+cudaError_t norm_typed(const NormArgs &a, cudaStream_t stream) {
+    // one piece a thread while no more than one block of them comes to an SM
+    return a.H <= 8192 && (long long)a.M * a.H <= 152LL * 8192 ? norm_pieces<1, F32>(a, stream) : norm_pieces<4, F32>(a, stream);
+}
+
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {
-    if (a.H <= 8192) return a.fp32 ? norm_pieces<1, true>(a, stream) : norm_pieces<1, false>(a, stream);
-    if (a.H <= 16384) return a.fp32 ? norm_pieces<2, true>(a, stream) : norm_pieces<2, false>(a, stream);
-    return a.fp32 ? norm_pieces<4, true>(a, stream) : norm_pieces<4, false>(a, stream);
+    return a.fp32 ? norm_typed<true>(a, stream) : norm_typed<false>(a, stream);
 }
 
 }  // namespace bsf8
