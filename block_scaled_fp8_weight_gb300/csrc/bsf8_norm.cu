@@ -16,6 +16,8 @@ namespace bsf8 {
 namespace {
 
 constexpr int kMaxWarps = 32;
+constexpr int kRowsWarps = 20;  // a block of the kernel for many rows: 96 registers a thread (at 64 it spilled, to L2: no L1 is left)
+constexpr int kMaxRows = 225 * 1024;
 constexpr int kMaxRow = 4 * 3 * 1024 * 16;  // bytes of the longest row's pieces: 192 KB
 
 __device__ __forceinline__ void widen8(const uint4 &w, float (&y)[8]) {
@@ -63,8 +65,7 @@ __device__ __forceinline__ void residual_of(const uint4 &r, const uint4 &r2, flo
 // thread, its loads straight to registers (P = 1).  Many: four pieces a thread, which go to shared memory by the
 // thread's own asynchronous copies (nothing is handed from thread to thread there) and wait there for the row's first
 // sum; with few threads a row six blocks and more share an SM, so that the loads, sums and stores of one run under
-// those of the others.  (8191 rows of 5120: 122 us with 640 threads a row and the next row's loads in registers, 168
-// with 320 threads and two rows ahead in shared memory, %% so.)
+// those of the others.
 template <int P, bool F32>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps) {
     constexpr int WORDS = F32 ? 3 : 2;  // of 16 bytes a piece: x, the residual
@@ -178,6 +179,214 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps)
     }
 }
 
+// Channels that a thread takes at a time in the kernel for many rows: a residual of 16 bytes, next to its
+// neighbours' (eight channels a thread were two of 16 bytes, each half a sector from the next lane's).
+template <bool F32>
+struct Unit;
+template <>
+struct Unit<false> {
+    static constexpr int N = 8;
+    typedef uint4 Half;  // bf16 values
+    static __device__ __forceinline__ void widen(const uint4 &w, float (&y)[8]) { widen8(w, y); }
+    static __device__ __forceinline__ uint4 narrow(const float (&y)[8]) { return narrow8(y); }
+    static __device__ __forceinline__ void residual(const uint4 &w, float (&y)[8]) { widen8(w, y); }
+    static __device__ __forceinline__ uint4 store(const float (&y)[8]) { return narrow8(y); }
+};
+template <>
+struct Unit<true> {
+    static constexpr int N = 4;
+    typedef uint2 Half;
+    static __device__ __forceinline__ void widen(const uint2 &w, float (&y)[4]) {
+        y[0] = __uint_as_float(w.x << 16), y[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        y[2] = __uint_as_float(w.y << 16), y[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ uint2 narrow(const float (&y)[4]) { return make_uint2(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])); }
+    static __device__ __forceinline__ void residual(const uint4 &w, float (&y)[4]) {
+        y[0] = __uint_as_float(w.x), y[1] = __uint_as_float(w.y), y[2] = __uint_as_float(w.z), y[3] = __uint_as_float(w.w);
+    }
+    static __device__ __forceinline__ uint4 store(const float (&y)[4]) {
+        return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+    }
+};
+
+// Many rows: one block an SM in groups of `warps` warps, a group a row at a time, 32 channels a thread.  The weights
+// lie in shared memory for good; a row comes there by bulk copies of one thread, the next row's asked for as soon as
+// this one's are used up, under its last stores.
+// 8191 rows of 5120 (fp32 residual, both norms, channel gate): 87 us, 5.8 TB/s of what must move (0.86 of the measured
+// rate); waits for the loads are two thirds of a row's time in its group.  Six groups at 64 registers: 135 us, their
+// spills go to L2; a block a row (the kernel below): 110; the same with 640 threads a row: 122.
+template <bool F32>
+__global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const NormArgs a, int warps, int groups, unsigned long long timeout_ns,
+                                                            int skip_loads, int *status) {
+    using U = Unit<F32>;
+    using Half = typename U::Half;
+    constexpr int N = U::N, J = 32 / N;
+    __shared__ float s_sum[2][kMaxWarps];
+    __shared__ uint64_t s_full[kMaxWarps];
+    extern __shared__ uint4 memory[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / warps, w0 = group * warps;
+    const int t = (int)threadIdx.x - 32 * w0, threads = 32 * warps, step = (int)blockDim.x, units = a.H / N;
+    if (t == 0) mbar_init(&s_full[group], 1);
+    fence_mbar_init();
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    const float inv = 1.0f / (float)a.H;
+    const bool full = a.gate_kind == kGateFull, channel = a.gate_kind == kGateChannel;
+    // each group's row of the residual, of x and of a full gate; then weight, post_weight and a channel gate
+    uint4 *const r_at = memory + group * units;
+    Half *const x_at = reinterpret_cast<Half *>(memory + groups * units) + group * units;
+    Half *const g_at = reinterpret_cast<Half *>(memory + groups * units) + (groups + group) * units;
+    Half *const vec = reinterpret_cast<Half *>(memory + groups * units) + (full ? 2 : 1) * groups * units;
+    const uint32_t row_bytes = (uint32_t)a.H * 2;
+    auto ask = [&](long long row) {
+        if (t != 0 || row >= a.M) return;
+        mbar_arrive_expect_tx(&s_full[group], row_bytes * (full ? 2u : 1u) + (a.residual ? row_bytes * (F32 ? 2u : 1u) : 0u));
+        if (skip_loads) return;
+        bulk_g2s(x_at, a.x + row * a.ldx, row_bytes, &s_full[group]);
+        if (full) bulk_g2s(g_at, a.gate + row * a.ldg, row_bytes, &s_full[group]);
+        if (a.residual)
+            bulk_g2s(r_at, static_cast<const char *>(a.residual) + row * a.ldr * (F32 ? 4 : 2), row_bytes * (F32 ? 2 : 1), &s_full[group]);
+    };
+    const long long stride = (long long)gridDim.x * groups;
+    long long row = (long long)blockIdx.x * groups + group;
+    ask(row);
+    for (int i = threadIdx.x; i < units; i += step) {
+        if (a.h) vec[i] = reinterpret_cast<const Half *>(a.weight)[i];
+        if (a.post) vec[units + i] = reinterpret_cast<const Half *>(a.post)[i];
+        if (channel) vec[2 * units + i] = reinterpret_cast<const Half *>(a.gate)[i];
+    }
+    __syncthreads();
+    // the sum of v over the group
+    uint32_t sums = 0;  // two sets of slots in turn: one is written again after the barrier of the other
+    auto group_sum = [&](float v) {
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        if (warps == 1) return v;
+        float *const at = s_sum[sums++ & 1];
+        if (lane == 0) at[warp] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
+        v = lane < warps ? at[w0 + lane] : 0.0f;
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        return v;
+    };
+    // whether v holds for the whole group, which so goes on or leaves as one
+    auto group_all = [&](bool v) {
+        if (warps == 1) return __all_sync(0xFFFFFFFFu, v) != 0;
+        uint32_t all;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                     : "=r"(all)
+                     : "r"((uint32_t)v), "r"(group + 1), "r"(threads)
+                     : "memory");
+        return all != 0;
+    };
+    uint32_t phase = 0;
+    for (; row < a.M; row += stride) {
+        float f = a.scale;
+        if (a.gate_kind == kGateToken) f *= __uint_as_float((uint32_t)a.gate[row * a.ldg] << 16);
+        if (!group_all(mbar_wait_bounded(&s_full[group], phase, timeout_ns))) {
+            // the wait ran out: what was asked for may still land, and the block's memory is not left before
+            report_timeout(status);
+            if (!skip_loads) (void)mbar_wait_bounded(&s_full[group], phase, timeout_ns);
+            return;
+        }
+        phase ^= 1;
+        float z[J][N];
+        float ss = 0.0f, n = 1.0f;
+        if (a.post) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (t + j * threads >= units) continue;
+                U::widen(x_at[t + j * threads], z[j]);
+#pragma unroll
+                for (int i = 0; i < N; ++i) ss = fmaf(z[j][i], z[j][i], ss);
+            }
+            n = rsqrtf(fmaf(group_sum(ss), inv, a.eps));
+            ss = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + j * threads;
+            if (u >= units) continue;
+            float g[N];
+            U::widen(x_at[t + j * threads], z[j]);
+            if (a.post) {
+                U::widen(vec[units + u], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) z[j][i] = z[j][i] * n * g[i];
+            }
+            if (channel || full) {
+                U::widen(full ? g_at[u] : vec[2 * units + u], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) z[j][i] *= g[i];
+            }
+            float r[N] = {};
+            if (a.residual) U::residual(r_at[u], r);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                z[j][i] = fmaf(f, z[j][i], r[i]);
+                ss = fmaf(z[j][i], z[j][i], ss);
+            }
+            if (a.r_out) static_cast<uint4 *>(a.r_out)[row * units + u] = U::store(z[j]);
+        }
+        const float k = rsqrtf(fmaf(group_sum(ss), inv, a.eps));
+        if (warps == 1) __syncwarp();
+        ask(row + stride);  // the whole group has read this row
+        if (!a.h) continue;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int u = t + j * threads;
+            if (u >= units) continue;
+            float g[N];
+            U::widen(vec[u], g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) g[i] *= z[j][i] * k;
+            reinterpret_cast<Half *>(a.h)[row * units + u] = U::narrow(g);
+        }
+    }
+}
+
+// Groups of a block: as many as its threads, named barriers (15) and shared memory allow.
+template <bool F32>
+int row_groups(int H, bool full, size_t *bytes) {
+    const int warps = (H / 8 + 127) / 128;
+    const size_t row = (size_t)H * (2 + (F32 ? 4 : 2) + (full ? 2 : 0)), weights = (size_t)3 * H * 2;
+    int g = std::min(warps == 1 ? kRowsWarps : 15, kRowsWarps / warps);
+    while (g > 0 && weights + g * row > (size_t)kMaxRows) --g;
+    *bytes = weights + g * row;
+    return g;
+}
+
+template <bool F32>
+cudaError_t launch_rows(const NormArgs &a, int groups, size_t smem, cudaStream_t stream) {
+    static int configured[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(norm_rows_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxRows);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
+    }
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    const int warps = (a.H / 8 + 127) / 128;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<long long>(((long long)a.M + groups - 1) / groups, 152), 1, 1);
+    cfg.blockDim = dim3((unsigned)(groups * warps * 32), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = options().pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, norm_rows_kernel<F32>, a, warps, groups, options().timeout_ns, options().skip_loads, status);
+}
+
 template <int P, bool F32>
 cudaError_t norm_pieces(const NormArgs &a, cudaStream_t stream) {
     const int warps = (a.H / 8 + 32 * P - 1) / (32 * P);
@@ -210,6 +419,10 @@ cudaError_t norm_pieces(const NormArgs &a, cudaStream_t stream) {
 
 template <bool F32>
 cudaError_t norm_typed(const NormArgs &a, cudaStream_t stream) {
+    // work for several turns of every group: a block an SM
+    size_t smem;
+    const int groups = row_groups<F32>(a.H, a.gate_kind == kGateFull, &smem);
+    if (groups >= 2 && (long long)a.M >= 152LL * 2 * groups) return launch_rows<F32>(a, groups, smem, stream);
     // one piece a thread while no more than one block of them comes to an SM
     return a.H <= 8192 && (long long)a.M * a.H <= 152LL * 8192 ? norm_pieces<1, F32>(a, stream) : norm_pieces<4, F32>(a, stream);
 }

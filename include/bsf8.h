@@ -605,8 +605,9 @@ enum {
                                    /* mbarriers (decode-ahead, decode-ahead tensor-    */
                                    /* core, tensor-core, wide-weight) issue no weight  */
                                    /* loads, the attention kernels none of the cache,  */
-                                   /* so their bounded waits run out and the call      */
-                                   /* ends with BSF8_ERR_TIMEOUT in the status         */
+                                   /* the norms of many rows none at all, so their     */
+                                   /* bounded waits run out and the call ends with     */
+                                   /* BSF8_ERR_TIMEOUT in the status                   */
     BSF8_OPT_GEMM_PATH = 4         /* 0 (default): the kernel chosen by shape:         */
                                    /*  - up to 8 token rows: the decode-ahead kernel   */
                                    /*    when its grid fits two blocks an SM, else the */

@@ -33,7 +33,8 @@ def compare(h, r, x, res, w, post, gate, scale):
 
 
 @pytest.mark.parametrize("M,H", [(1, 8), (3, 64), (6, 5120), (17, 248), (65, 2056), (130, 1024), (1, 8192), (5, 8200), (40, 16384),
-                                 (3, 16392), (2, 32768), (1300, 256), (2500, 5120)])
+                                 (3, 16392), (2, 32768), (1300, 256), (2500, 5120),
+                                 (7000, 264), (1300, 8192), (700, 12296)])
 @pytest.mark.parametrize("fp32,post,gate", [(False, False, None), (True, True, "channel"), (False, True, "token"), (True, False, "full")])
 def test_norm(bsf8_lib, M, H, fp32, post, gate):
     r = np.random.default_rng(M + H)
@@ -121,3 +122,20 @@ def test_refused_tensors(bsf8_lib):
         f(x, None, None)  # nothing to write
     with pytest.raises(bsf8.Bsf8Error):
         f(x[:, 1:57], x[:, 8:], w[:56])  # not 16-byte aligned
+
+
+def test_a_wait_that_runs_out_is_reported(bsf8_lib):
+    """No loads are issued (a test-only option): the kernel for many rows gives up its waits and says so."""
+    x = torch.ones(3000, 5120, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(5120, device="cuda", dtype=torch.bfloat16)
+    h = torch.full_like(x, 7.0)
+    try:
+        bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 1)
+        bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 1000000)
+        bsf8.residual_norm(x, x, w, post_weight=w, out=h)
+        assert bsf8.device_status() == 7 and (h == 7).all()
+    finally:
+        bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 0)
+        bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 2000000000)
+    bsf8.residual_norm(x, x, w, post_weight=w, out=h)
+    assert bsf8.device_status() == 0 and (h == 1).all()
