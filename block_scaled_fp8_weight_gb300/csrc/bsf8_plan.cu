@@ -1,11 +1,12 @@
 // bsf8_plan.cu -- the pages and slots of a step: pages of requests that are done go back to the free
 // stack, the others get what their new tokens need, and each new token its request and slot.
 //
-// One cluster does it all: its blocks each take the same sums over the requests (at most 1024, two
-// integers a request), so that nothing but the pages themselves goes from one to the other -- what the
-// first half gives back the second may hand out, with the cluster's barrier between them -- and share
-// the pages and tokens evenly.  Bound by latency: the requests' words, three sums over a block, the
-// barrier, a page, its entry.
+// One cluster does it all: its blocks each take the same sums over the requests (a thread a request, two
+// scans), so that nothing but the pages themselves goes from one to the other -- what the first half gives
+// back the second may hand out, with the cluster's barrier between them -- and share the pages and tokens
+// evenly.  Few requests and tokens take one small block: what it costs is the chain of loads, scans and
+// barriers.  (1024 requests, half of them leaving, 198000 tokens: 9.6 us in a graph, 13.7 with eight blocks, 30 with
+// those of 512 threads, three scans and a search a token; seven requests of a few tokens 2.9.)
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
@@ -15,36 +16,54 @@ namespace bsf8 {
 
 namespace {
 
-constexpr int kPThreads = 512, kPWarps = kPThreads / 32, kPer = 2;  // 1024 requests
-constexpr int kMaxRequests = kPThreads * kPer;
-constexpr int kPlanCluster = 8;
+constexpr int kPlanCluster = 16;  // 8 where the device does not schedule those
 
+template <int NT>
 struct PlanShared {
     // sums over the requests before each, and over all: pages that come back, pages handed out, tokens
-    int back[kMaxRequests + 1], need[kMaxRequests + 1], start[kMaxRequests + 1];
-    int lens[kMaxRequests], held[kMaxRequests];  // held: after what comes back
-    long long wsum[2][kPWarps];
+    int back[NT + 1], need[NT + 1], start[NT + 1];
+    int lens[NT], held[NT];  // held: after what comes back
+    int wsum[2][3][NT / 32];
 };
 
-// The sums over the threads before this one, and over all in `total`; barriers inside.
-__device__ __forceinline__ long long before_me(long long v, long long *wsum, long long &total) {
+// The sums of K numbers over the threads before this one (v), and over all (all); one barrier.  The last number's sums
+// stop at `most`, below 2^31 with one more (a sum that is cut off there is still one: in any order).  `set`: slots in turn.
+template <int NT, int K>
+__device__ __forceinline__ void before_me(PlanShared<NT> &s, int set, int (&v)[K], int (&all)[K], int most) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long up = v;
+    auto add = [&](int k, int a, int b) { return k == K - 1 ? min(a + b, most) : a + b; };
+    int up[K], w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) up[k] = v[k];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xFFFFFFFFu, up, m);
-        if (lane >= m) up += o;
-    }
-    if (lane == 31) wsum[warp] = up;
-    __syncthreads();
-    long long before = up - v;
-    total = 0;
 #pragma unroll
-    for (int w = 0; w < kPWarps; ++w) {
-        if (w < warp) before += wsum[w];
-        total += wsum[w];
+        for (int k = 0; k < K; ++k) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, up[k], m);
+            if (lane >= m) up[k] = add(k, up[k], o);
+        }
     }
-    return before;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (lane == 31) s.wsum[set][k][warp] = up[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) w[k] = lane < NT / 32 ? s.wsum[set][k][lane] : 0;
+#pragma unroll
+    for (int m = 1; m < NT / 32; m <<= 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, w[k], m);
+            if (lane >= m) w[k] = add(k, w[k], o);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        all[k] = __shfl_sync(0xFFFFFFFFu, w[k], NT / 32 - 1);
+        const int p = __shfl_sync(0xFFFFFFFFu, w[k], max(warp - 1, 0));
+        const int o = __shfl_up_sync(0xFFFFFFFFu, up[k], 1);
+        v[k] = add(k, lane > 0 ? o : 0, warp > 0 ? p : 0);
+    }
 }
 
 // The request of item i: sum[b] <= i < sum[b + 1].
@@ -58,141 +77,139 @@ __device__ __forceinline__ int owner(const int *sum, int B, int i) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kPThreads) plan_kernel(const PlanArgs a, int cluster, int *status) {
-    __shared__ PlanShared s;
+template <int NT>
+__global__ void __launch_bounds__(NT) plan_kernel(const PlanArgs a, int cluster, int *status) {
+    __shared__ PlanShared<NT> s;
     pdl_trigger();
     pdl_wait();
-    const int tid = threadIdx.x, rank = blockIdx.x;
+    const int tid = threadIdx.x, rank = blockIdx.x, B = a.B;
     const int P = a.page_size;
     const long long capacity = (long long)a.table_pages * P;
     bool bad = false;
     int count = *a.count;
+    // a thread's request
+    int held = 0, len = 0, add = 0, back = 0, need = 0;
+    if (tid < B) {
+        held = a.held[tid], len = a.lens[tid], add = a.add[tid];
+        const bool done = a.done && a.done[tid] != 0;
+        if (held < 0 || held > a.table_pages) {
+            bad = true;
+            held = max(0, min(held, a.table_pages));
+        }
+        if (len < 0 || add < 0 || (long long)len + add > capacity) {
+            bad = true;
+            len = add = 0;
+        }
+        if (done) {
+            back = held;
+            held = 0;
+        }
+        if (add > 0) need = max(0, (len + add - 1) / P + 1 - held);
+        s.lens[tid] = len;
+        s.held[tid] = held;
+    }
     if (count < 0 || count > a.pool) {
         bad = true;
         count = max(0, min(count, a.pool));
     }
-    // a thread's requests
-    long long back = 0, need = 0, ask = 0;
-    int nb[kPer], nn[kPer], na[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int b = tid * kPer + j;
-        nb[j] = nn[j] = na[j] = 0;
-        if (b < a.B) {
-            int held = a.held[b], len = a.lens[b], add = a.add[b];
-            const bool done = a.done && a.done[b] != 0;
-            if (held < 0 || held > a.table_pages) {
-                bad = true;
-                held = max(0, min(held, a.table_pages));
-            }
-            if (len < 0 || add < 0 || (long long)len + add > capacity) {
-                bad = true;
-                len = add = 0;
-            }
-            if (done) {
-                nb[j] = held;
-                held = 0;
-            }
-            if (add > 0) nn[j] = max(0, (len + add - 1) / P + 1 - held);
-            na[j] = add;
-            s.lens[b] = len;
-            s.held[b] = held;
-        }
-        back += nb[j];
-        need += nn[j];
-        ask += na[j];
-    }
-    long long total, tokens;
-    long long back0 = before_me(back, s.wsum[0], total);  // at most B table_pages: fits 31 bits
-    if (count + total > a.pool) {
+    // pages that come back and pages asked for (each below 2^31 in all), and tokens asked for, as far as they count
+    int v[3] = {back, need, min(add, a.N + 1)}, all[3];
+    before_me(s, 0, v, all, a.N + 1);
+    int returned = all[0];
+    if (returned > a.pool - count) {
         bad = true;  // more than the stack can hold: the rest is lost
-        total = a.pool - count;
+        returned = a.pool - count;
     }
-    const int top = count + (int)total;
-    // pages and tokens asked for by a request and those before it: what does not fit gets nothing
-    const long long need0 = before_me(need, s.wsum[1], total);
-    __syncthreads();
-    const long long ask0 = before_me(ask, s.wsum[0], tokens);
-    need = ask = 0;
-    long long upn = need0, upa = ask0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int b = tid * kPer + j;
-        upn += nn[j];
-        upa += na[j];
-        if ((nn[j] > 0 && upn > top) || upa > a.N) nn[j] = na[j] = 0;
-        need += nn[j];
-        ask += na[j];
-        if (b < a.B) s.back[b] = (int)back0;
-        back0 += nb[j];
-    }
-    __syncthreads();
-    // both sums of what is granted, in one: pages and tokens are below 2^31
-    long long both;
-    long long at = before_me(need << 32 | ask, s.wsum[1], both);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const int b = tid * kPer + j;
-        if (b < a.B) {
-            s.need[b] = (int)(at >> 32);
-            s.start[b] = (int)(at & 0x7FFFFFFF);
-        }
-        at += (long long)nn[j] << 32 | na[j];
-    }
-    if (tid * kPer < a.B && (tid + 1) * kPer >= a.B) s.back[a.B] = (int)back0;  // the last request's thread
-    if (tid == 0) {
-        s.need[a.B] = (int)(both >> 32);
-        s.start[a.B] = (int)(both & 0x7FFFFFFF);
-    }
+    const int top = count + returned;
+    if (tid < B) s.back[tid] = v[0];
+    // what does not fit, pages or tokens, by a request and those before it, gets nothing
+    if ((need > 0 && need > top - v[1]) || add > a.N - v[2]) need = add = 0;
+    int at[2] = {need, add}, granted[2];
+    before_me(s, 1, at, granted, a.N);
+    if (tid < B) s.need[tid] = at[0], s.start[tid] = at[1];
+    if (tid == 0) s.back[B] = all[0], s.need[B] = granted[0], s.start[B] = granted[1];
     if (bad && rank == 0) report_index(status);
     __syncthreads();
 
-    // the pages that come back, onto the stack
-    const int threads = cluster * kPThreads, me = rank * kPThreads + tid;
-    for (int i = me; i < top - count; i += threads) {
-        const int b = owner(s.back, a.B, i);
-        a.free[count + i] = a.table[(size_t)b * a.table_pages + (i - s.back[b])];
-    }
-    // (every block has read the books by then)
-    if (cluster > 1) cluster_barrier();
-    else __syncthreads();
-    // the pages handed out, from its top
-    const int used = s.need[a.B];
-    for (int i = me; i < used; i += threads) {
-        const int b = owner(s.need, a.B, i);
-        a.table[(size_t)b * a.table_pages + s.held[b] + (i - s.need[b])] = __ldcg(a.free + (top - 1 - i));
-    }
-    const int last = s.start[a.B];
-    for (int i = me; i < a.N; i += threads) {
-        int b = 0, slot = -1;
-        if (i < last) {
-            b = owner(s.start, a.B, i);
-            slot = s.lens[b] + (i - s.start[b]);
-        }
-        a.req[i] = b;
-        a.slot[i] = slot;
-    }
-    if (rank == 0) {
-        for (int b = tid; b <= a.B; b += kPThreads) {
-            a.start[b] = s.start[b];
-            if (b < a.B) {
-                a.granted[b] = s.start[b + 1] - s.start[b];
-                a.held[b] = s.held[b] + s.need[b + 1] - s.need[b];
+    const int threads = cluster * NT, me = rank * NT + tid;
+    // the pages that come back, onto the stack, four a thread on their way
+    for (int i0 = me; i0 < returned; i0 += 4 * threads) {
+        int page[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * threads;
+            if (i < returned) {
+                const int b = owner(s.back, B, i);
+                page[j] = a.table[(size_t)b * a.table_pages + (i - s.back[b])];
             }
         }
-        if (tid == 0) *a.count = top - used;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + j * threads < returned) a.free[count + i0 + j * threads] = page[j];
+    }
+    if (cluster > 1) cluster_arrive();
+    // the tokens, four a thread one after another
+    const int last = s.start[B];
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.req) | reinterpret_cast<uintptr_t>(a.slot)) & 15) == 0;
+    for (long long r0 = 4LL * me; r0 < a.N; r0 += 4LL * threads) {
+        const int i0 = (int)r0;
+        int req[4], slot[4], b = i0 < last ? owner(s.start, B, i0) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j;
+            req[j] = 0, slot[j] = -1;
+            if (i < last) {
+                while (s.start[b + 1] <= i) ++b;
+                req[j] = b;
+                slot[j] = s.lens[b] + (i - s.start[b]);
+            }
+        }
+        if (aligned && i0 + 4 <= a.N) {
+            *reinterpret_cast<int4 *>(a.req + i0) = make_int4(req[0], req[1], req[2], req[3]);
+            *reinterpret_cast<int4 *>(a.slot + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (i0 + j < a.N) a.req[i0 + j] = req[j], a.slot[i0 + j] = slot[j];
+        }
+    }
+    // (every block has read the books by then, and its pages are back)
+    if (cluster > 1) cluster_wait();
+    else __syncthreads();
+    // the pages handed out, from its top
+    const int used = s.need[B];
+    for (int i0 = me; i0 < used; i0 += 4 * threads) {
+        int page[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (i0 + j * threads < used) page[j] = __ldcg(a.free + (top - 1 - (i0 + j * threads)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * threads;
+            if (i < used) {
+                const int b = owner(s.need, B, i);
+                a.table[(size_t)b * a.table_pages + s.held[b] + (i - s.need[b])] = page[j];
+            }
+        }
+    }
+    if (rank == 0) {
+        if (tid < B) {
+            a.start[tid] = s.start[tid];
+            a.granted[tid] = add;
+            a.held[tid] = held + need;
+        }
+        if (tid == 0) {
+            a.start[B] = last;
+            *a.count = top - used;
+        }
     }
 }
 
-}  // namespace
-
-cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
-    int *status = status_word();
-    if (!status) return cudaErrorInvalidSymbol;
-    const int cluster = a.B > 64 || a.N > 2048 ? kPlanCluster : 1;
+template <int NT>
+cudaError_t plan_threads(const PlanArgs &a, int cluster, cudaStream_t stream, int *status) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster, 1, 1);
-    cfg.blockDim = dim3(kPThreads, 1, 1);
+    cfg.blockDim = dim3(NT, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     int na = 0;
@@ -210,7 +227,40 @@ cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
     }
     cfg.attrs = attrs;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, plan_kernel, a, cluster, status);
+    return cudaLaunchKernelEx(&cfg, plan_kernel<NT>, a, cluster, status);
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
+    int *status = status_word();
+    if (!status) return cudaErrorInvalidSymbol;
+    if (a.B <= 128 && a.N <= 4096) return plan_threads<128>(a, 1, stream, status);
+    // clusters of 16 blocks: asked for once per device
+    static int known[64] = {0};  // 0 unknown, else the cluster
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int cluster = __atomic_load_n(&known[dev], __ATOMIC_ACQUIRE);
+    if (cluster == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kPlanCluster, 1, 1);
+        cfg.blockDim = dim3(1024, 1, 1);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kPlanCluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        const bool fits = cudaFuncSetAttribute(plan_kernel<1024>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                          cudaOccupancyMaxActiveClusters(&n, plan_kernel<1024>, &cfg) == cudaSuccess && n > 0;
+        if (!fits) (void)cudaGetLastError();
+        cluster = fits ? kPlanCluster : kPlanCluster / 2;
+        __atomic_store_n(&known[dev], cluster, __ATOMIC_RELEASE);
+    }
+    return plan_threads<1024>(a, cluster, stream, status);
 }
 
 }  // namespace bsf8
