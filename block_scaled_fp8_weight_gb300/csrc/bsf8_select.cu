@@ -221,17 +221,16 @@ namespace {
 
 constexpr int kSThreads = 256, kSWarps = kSThreads / 32;
 constexpr int kMaxSCluster = 8;
+constexpr int kSBins = 2048, kSBinsEach = kSBins / kSThreads;
 constexpr uint32_t kTopKey = 0xFF800000u;  // of +inf
 
 struct SelectShared {
-    int q[2][256];              // sums of the rows' positive and negative parts, then the scaled ones
-    int red[kSWarps];
-    int hist[256];
-    int wsum[2][kSWarps];
+    int q[2][256];              // sums of the rows' positive and negative parts
+    int red[kSWarps], wsum[kSWarps];
+    int hist[kSBins];           // counts of the keys; then the chosen pages, where that many suffice
     uint32_t lo, hi;            // smallest and largest key below the top one
     int top;                    // keys that are the top one
-    uint32_t prefix;
-    int want, digit;
+    int want, digit, count;
 };
 
 __device__ __forceinline__ int dp4a_ss(uint32_t a, uint32_t b, int c) {
@@ -289,16 +288,36 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
             return *reinterpret_cast<const uint4 *>(a.q + ((size_t)b * a.T + t) * a.ldq + (size_t)(h * g + r - t * g) * D + 8 * u);
         };
         for (int i = tid; i < 2 * D; i += kSThreads) s.q[i / D][i % D] = 0;
+        // f(piece) of this thread's rows, four on their way; the first four stay for the second turn
+        constexpr int RPP = kSThreads / LPQ;  // rows at a time
+        const int r0 = tid / LPQ;
+        uint4 kept[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r0 + j * RPP < rows) kept[j] = piece(r0 + j * RPP);
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r0 + j * RPP < rows) f(kept[j]);
+            for (int r = r0 + 4 * RPP; r < rows; r += 4 * RPP) {
+                uint4 w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r + j * RPP < rows) w[j] = piece(r + j * RPP);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (r + j * RPP < rows) f(w[j]);
+            }
+        };
         uint32_t am = 0;
-        for (int r = tid / LPQ; r < rows; r += kSThreads / LPQ) {
-            const uint4 w = piece(r);
+        each([&](const uint4 &w) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t lo = x[i] & 0x7FFFu, hi = (x[i] >> 16) & 0x7FFFu;
                 am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
             }
-        }
+        });
         am = __reduce_max_sync(0xFFFFFFFFu, am);
         if (lane == 0) s.red[warp] = (int)am;
         __syncthreads();
@@ -309,8 +328,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
         const int k = max((int)(am >> 7) - 127, -100);
         const float scale = __uint_as_float((uint32_t)(127 + 17 - k) << 23);
         int up[8] = {}, dn[8] = {};
-        for (int r = tid / LPQ; r < rows; r += kSThreads / LPQ) {
-            const uint4 w = piece(r);
+        each([&](const uint4 &w) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
                 up[i] += max(z, 0);
                 dn[i] += min(z, 0);
             }
-        }
+        });
 #pragma unroll
         for (int m = LPQ; m < 32; m <<= 1) {
 #pragma unroll
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
                 dn[i] += __shfl_xor_sync(0xFFFFFFFFu, dn[i], m);
             }
         }
-        if (lane < LPQ) {
+        if (lane < LPQ && warp * 32 / LPQ < rows) {  // warps that had rows
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (up[i]) atomicAdd(&s.q[0][8 * u + i], up[i]);
@@ -337,13 +355,10 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
             }
         }
         __syncthreads();
-        uint32_t big = 0;
-        for (int i = tid; i < 2 * D; i += kSThreads) big = max(big, (uint32_t)abs(s.q[i / D][i % D]));
-        big = __reduce_max_sync(0xFFFFFFFFu, big);
-        if (lane == 0) s.wsum[0][warp] = (int)big;
-        __syncthreads();
+        uint32_t big = 0;  // (every warp for itself)
 #pragma unroll
-        for (int w = 0; w < kSWarps; ++w) big = max(big, (uint32_t)s.wsum[0][w]);
+        for (int i = 0; i < 2 * D; i += 32) big = max(big, (uint32_t)abs(s.q[(i + lane) / D][(i + lane) % D]));
+        big = __reduce_max_sync(0xFFFFFFFFu, big);
         const int sh = max(0, 32 - __clz(big) - 14), half = (1 << sh) >> 1;
         // ---------------------------------------------------------- scores
         // 2 D codes a page, 16 a lane: the maxima's lanes, then the minima's
@@ -362,44 +377,68 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
         }
         if (cluster > 1) cluster_wait();
         const uint32_t keys0 = cluster > 1 ? map_to_rank(keys, 0) : 0;
-        constexpr int U = 4;  // passes in flight
-        const int chunk = PPW * U;
-        for (int p0 = (rank * kSWarps + warp) * chunk; p0 < full; p0 += cluster * kSWarps * chunk) {
+        // a warp takes 32 pages: a lane each asks for their entries, then their bounds come, a batch of passes on their
+        // way while the one before is multiplied
+        constexpr int PASSES = 32 / PPW, U = PASSES < 8 ? PASSES : 8;
+        const int first = (rank * kSWarps + warp) * 32, stride = cluster * kSWarps * 32;
+        int next = first + lane < full ? table[first + lane] : -1;
+        for (int p0 = first; p0 < full; p0 += stride) {
+            const int page = next;
+            next = p0 + stride + lane < full ? table[p0 + stride + lane] : -1;
+            const int passes = (min(32, full - p0) + PPW - 1) / PPW;
             uint4 w[U];
             uint32_t e[U];
-            bool good[U];
-            int page = -1;
-            if (lane < chunk && p0 + lane < full) page = table[p0 + lane];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int at = __shfl_sync(0xFFFFFFFFu, page, PPW * j + lane / LPP);
-                good[j] = (unsigned)at < (unsigned)v.pages;
-                w[j] = make_uint4(0, 0, 0, 0);
-                e[j] = 0;
-                if (good[j]) {
+            auto ask = [&](int i, uint4 &w_, uint32_t &e_) {
+                const int at = __shfl_sync(0xFFFFFFFFu, page, (PPW * i + lane / LPP) & 31);
+                w_ = make_uint4(0, 0, 0, 0);
+                e_ = 256;  // no such page
+                if ((unsigned)at < (unsigned)v.pages) {
                     const size_t row = (size_t)at * v.heads + h;
-                    w[j] = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
-                    e[j] = v.exps[row * EB + blk];
+                    w_ = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
+                    e_ = v.exps[row * EB + blk];
                 }
-            }
+            };
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const int p = p0 + PPW * j + lane / LPP;
-                int sh_ = 0, sl = 0;
-                sh_ = dp4a_ss(w[j].x, qh[0], sh_), sl = dp4a_su(w[j].x, ql[0], sl);
-                sh_ = dp4a_ss(w[j].y, qh[1], sh_), sl = dp4a_su(w[j].y, ql[1], sl);
-                sh_ = dp4a_ss(w[j].z, qh[2], sh_), sl = dp4a_su(w[j].z, ql[2], sl);
-                sh_ = dp4a_ss(w[j].w, qh[3], sh_), sl = dp4a_su(w[j].w, ql[3], sl);
-                int S = sh_ * 256 + sl;
-                S += __shfl_xor_sync(0xFFFFFFFFu, S, 1);
-                S += __shfl_xor_sync(0xFFFFFFFFu, S, HALF);  // |S| < 2^27
-                float f = e[j] == 255 ? INFINITY : __fmul_rn(__fmul_rn((float)S, 7.450580596923828e-9f), pow2_byte(e[j]));
+            for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
+            for (int i0 = 0; i0 < passes; i0 += U) {
+                // step by step over the whole batch: its chains of shuffles run side by side
+                int S[U];
+                float f[U];
+                uint32_t byte[U];
 #pragma unroll
-                for (int m = 2; m < HALF; m <<= 1) f = __fadd_rn(f, __shfl_xor_sync(0xFFFFFFFFu, f, m));
-                if (p < full && l == 0) {
-                    uint32_t key = good[j] ? key_of(f) : 0;
+                for (int j = 0; j < U; ++j) {
+                    int sh_ = 0, sl = 0;
+                    sh_ = dp4a_ss(w[j].x, qh[0], sh_), sl = dp4a_su(w[j].x, ql[0], sl);
+                    sh_ = dp4a_ss(w[j].y, qh[1], sh_), sl = dp4a_su(w[j].y, ql[1], sl);
+                    sh_ = dp4a_ss(w[j].z, qh[2], sh_), sl = dp4a_su(w[j].z, ql[2], sl);
+                    sh_ = dp4a_ss(w[j].w, qh[3], sh_), sl = dp4a_su(w[j].w, ql[3], sl);
+                    S[j] = sh_ * 256 + sl;
+                    byte[j] = e[j];
+                }
+                if (i0 + U < passes)
+#pragma unroll
+                    for (int j = 0; j < U; ++j) ask(i0 + U + j, w[j], e[j]);
+#pragma unroll
+                for (int j = 0; j < U; ++j) S[j] += __shfl_xor_sync(0xFFFFFFFFu, S[j], 1);
+#pragma unroll
+                for (int j = 0; j < U; ++j) S[j] += __shfl_xor_sync(0xFFFFFFFFu, S[j], HALF);  // |S| < 2^27
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    f[j] = byte[j] == 255 ? INFINITY : __fmul_rn(__fmul_rn((float)S[j], 7.450580596923828e-9f), pow2_byte(byte[j] & 255u));
+#pragma unroll
+                for (int m = 2; m < HALF; m <<= 1) {
+#pragma unroll
+                    for (int j = 0; j < U; ++j) f[j] = __fadd_rn(f[j], __shfl_xor_sync(0xFFFFFFFFu, f[j], m));
+                }
+                // pass l's by its lane l
+                uint32_t key = 0;
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+                    if (l == j) key = byte[j] < 256 ? key_of(f[j]) : 0;
+                const int p = p0 + PPW * (i0 + l) + lane / LPP;
+                if (l < U && p < min(full, p0 + 32)) {
+                    if (key == 0) report_index(status);  // no such page
                     if (p < a.sink || p >= full - a.recent) key = kTopKey;
-                    if (!good[j]) report_index(status);
                     if (cluster > 1) st_cluster_u32(keys0 + 4 * p, key);
                     else keys[p] = key;
                 }
@@ -428,6 +467,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
             }
         }
         if (tid == 0) s.lo = 0xFFFFFFFFu, s.hi = 0, s.top = 0;
+        for (int i = tid; i < kSBins; i += kSThreads) s.hist[i] = 0;
         __syncthreads();
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
         hi = __reduce_max_sync(0xFFFFFFFFu, hi);
@@ -435,10 +475,10 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
         if (lane == 0) {
             atomicMin(&s.lo, lo);
             atomicMax(&s.hi, hi);
-            atomicAdd(&s.top, top);
+            if (top) atomicAdd(&s.top, top);
         }
         __syncthreads();
-        // the key of rank n: `equal` of those that have it stay, the first ones
+        // keys above `key` stay, and the first `equal` of those that have it
         uint32_t key;
         int equal;
         if (s.top >= n) {
@@ -446,46 +486,51 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
             equal = n;
         } else {
             lo = s.lo;
-            const uint32_t range = s.hi - lo;
-            int shift = max(0, 32 - __clz(range) - 8), want = n - s.top;
-            uint32_t base = 0, most = range;  // keys - lo of [base, base + most] are in question
-            while (true) {
-                for (int i = tid; i < 256; i += kSThreads) s.hist[i] = 0;
-                __syncthreads();
+            uint32_t base = 0, most = s.hi - lo;  // keys - lo of [base, base + most] are in question
+            int want = n - s.top;
+            while (true) {  // 11 bits of them a turn, until a bin's keys are all wanted
+                const int shift = max(0, 32 - __clz(most) - 11);
                 for (int p = tid; p < full; p += kSThreads) {
                     const uint32_t x = keys[p];
-                    if (x < kTopKey && x - lo >= base && x - lo - base <= most) atomicAdd(&s.hist[(x - lo - base) >> shift], 1);
+                    if (x < kTopKey && x - lo >= base && x - lo - base <= most) atomicAdd(&s.hist[kSBins - 1 - ((x - lo - base) >> shift)], 1);
                 }
                 __syncthreads();
-                if (warp == 0) {  // bins from the top: a lane takes eight
-                    int c[8], sum = 0;
+                // bins from the top, some a thread
+                int c[kSBinsEach], sum = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum += c[i] = s.hist[255 - (8 * lane + i)];
-                    int upto = sum;
+                for (int i = 0; i < kSBinsEach; ++i) sum += c[i] = s.hist[kSBinsEach * tid + i];
+                int upto = sum;
 #pragma unroll
-                    for (int m = 1; m < 32; m <<= 1) {
-                        const int o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
-                        if (lane >= m) upto += o;
+                for (int m = 1; m < 32; m <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
+                    if (lane >= m) upto += o;
+                }
+                if (lane == 31) s.wsum[warp] = upto;
+                __syncthreads();
+                int before = upto - sum;
+#pragma unroll
+                for (int w = 0; w < kSWarps; ++w) before += w < warp ? s.wsum[w] : 0;
+#pragma unroll
+                for (int i = 0; i < kSBinsEach; ++i) {
+                    if (before < want && before + c[i] >= want) {
+                        s.digit = kSBins - 1 - (kSBinsEach * tid + i);
+                        s.want = want - before;
+                        s.count = c[i];
                     }
-                    int before = upto - sum;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (before < want && before + c[i] >= want) {
-                            s.digit = 255 - (8 * lane + i);
-                            s.want = want - before;
-                        }
-                        before += c[i];
-                    }
+                    before += c[i];
+                    s.hist[kSBinsEach * tid + i] = 0;  // for the next turn
                 }
                 __syncthreads();
                 base += (uint32_t)s.digit << shift;
                 want = s.want;
-                if (shift == 0) break;
+                if (shift == 0 || want == s.count) break;
                 most = (1u << shift) - 1u;
-                shift = max(0, shift - 8);
+                __syncthreads();
             }
-            key = lo + base;
-            equal = want;
+            // all of the bin's keys: those from its start on (which is not 0: then all pages would stay)
+            const bool all = want == s.count;
+            key = all ? lo + base - 1 : lo + base;
+            equal = all ? 0 : want;
         }
         // in ascending order: a thread takes a run of pages
         const int run = ((full + kSThreads - 1) / kSThreads) | 1;  // odd: no two lanes on a bank
@@ -498,18 +543,29 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, m);
             if (lane >= m) upto += o;
         }
-        if (lane == 31) s.wsum[1][warp] = (int)upto;
+        if (lane == 31) s.red[warp] = (int)upto;
         __syncthreads();
         upto -= c;
-        for (int w = 0; w < warp; ++w) upto += (uint32_t)s.wsum[1][w];
+#pragma unroll
+        for (int w = 0; w < kSWarps; ++w) upto += w < warp ? (uint32_t)s.red[w] : 0u;
         int above = (int)(upto >> 16), same = (int)(upto & 0xFFFFu);
-        for (int p = p0; p < p1; ++p) {
-            if (keys[p] > key) {
-                out[above++ + min(same, equal)] = table[p];
-            } else if (keys[p] == key) {
-                if (same < equal) out[above + same] = table[p];
-                ++same;
+        const bool listed = n <= kSBins;  // then their entries are asked for at once
+        auto put = [&](int at, int p) {
+            if (listed) s.hist[at] = p;
+            else out[at] = table[p];
+        };
+        if (c)
+            for (int p = p0; p < p1; ++p) {
+                if (keys[p] > key) {
+                    put(above++ + min(same, equal), p);
+                } else if (keys[p] == key) {
+                    if (same < equal) put(above + same, p);
+                    ++same;
+                }
             }
+        if (listed) {
+            __syncthreads();
+            for (int i = tid; i < n; i += kSThreads) out[i] = table[s.hist[i]];
         }
     }
     // the pages of the tail and of the nodes, then none
@@ -535,10 +591,10 @@ cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t st
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
-    // blocks a pair: as many as there are SMs for, each with 128 pages at least
+    // blocks a pair: as many as run at once (four an SM), with 128 pages each at least where the request is longest
     const long long pairs = (long long)a.B * v.heads;
     int cluster = 1;
-    while (cluster < kMaxSCluster && 2 * cluster * pairs <= 304 && most > 128 * cluster) cluster *= 2;
+    while (cluster < kMaxSCluster && 2 * cluster * pairs <= 1216 && most > 128 * cluster) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * cluster), 1, 1);
     cfg.blockDim = dim3(kSThreads, 1, 1);
