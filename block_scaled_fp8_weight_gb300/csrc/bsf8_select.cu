@@ -257,8 +257,9 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 
 }  // namespace
 
-template <int D>
-__global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, const SelectArgs a, int cluster, int *status) {
+// MANY: for many pairs of a request and a head, fewer loads ahead for four blocks an SM, whose phases hide each other.
+template <int D, bool MANY>
+__global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const BoundsView v, const SelectArgs a, int cluster, int *status) {
     __shared__ SelectShared s;
     extern __shared__ uint32_t keys[];
     pdl_trigger();
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
         const uint32_t keys0 = cluster > 1 ? map_to_rank(keys, 0) : 0;
         // a warp takes 32 pages: a lane each asks for their entries, then their bounds come, a batch of passes on their
         // way while the one before is multiplied
-        constexpr int PASSES = 32 / PPW, U = PASSES < 8 ? PASSES : 8;
+        constexpr int PASSES = 32 / PPW, U = MANY ? 4 : 8;
         const int first = (rank * kSWarps + warp) * 32, stride = cluster * kSWarps * 32;
         int next = first + lane < full ? table[first + lane] : -1;
         for (int p0 = first; p0 < full; p0 += stride) {
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kSThreads) select_kernel(const BoundsView v, c
     if (h == 0 && tid == 0) a.kept[b] = n * P + (ctx - full * P);
 }
 
-template <int D>
+template <int D, bool MANY>
 cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t stream, int *status) {
     const int most = std::min(v.table_pages, a.max_len / v.page_size);
     const size_t smem = (size_t)most * 4;
@@ -587,14 +588,14 @@ cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t st
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectPages * 4);
+        e = cudaFuncSetAttribute(select_kernel<D, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectPages * 4);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
-    // blocks a pair: as many as run at once (four an SM), with 128 pages each at least where the request is longest
+    // blocks a pair: as many as run at once, with 128 pages each at least where the request is longest
     const long long pairs = (long long)a.B * v.heads;
     int cluster = 1;
-    while (cluster < kMaxSCluster && 2 * cluster * pairs <= 1216 && most > 128 * cluster) cluster *= 2;
+    while (cluster < kMaxSCluster && 2 * cluster * pairs <= (MANY ? 608 : 304) && most > 128 * cluster) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * cluster), 1, 1);
     cfg.blockDim = dim3(kSThreads, 1, 1);
@@ -616,16 +617,18 @@ cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t st
     }
     cfg.attrs = attrs;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D>, v, a, cluster, status);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D, MANY>, v, a, cluster, status);
 }
 
 cudaError_t launch_select(const BoundsView &v, const SelectArgs &a, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
+    // (32 requests of up to 65536 tokens, 8 heads, then the attention: 88 us as few, 84 as many; one of 131072: 28, 33)
+    const bool many = (long long)a.B * v.heads > 152;
     switch (v.dim) {
-        case 64: return select_dim<64>(v, a, stream, status);
-        case 128: return select_dim<128>(v, a, stream, status);
-        case 256: return select_dim<256>(v, a, stream, status);
+        case 64: return many ? select_dim<64, true>(v, a, stream, status) : select_dim<64, false>(v, a, stream, status);
+        case 128: return many ? select_dim<128, true>(v, a, stream, status) : select_dim<128, false>(v, a, stream, status);
+        case 256: return many ? select_dim<256, true>(v, a, stream, status) : select_dim<256, false>(v, a, stream, status);
         default: return cudaErrorInvalidValue;
     }
 }
