@@ -553,7 +553,9 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
     const bool few = V <= kList && (k < V || nucleus);
     constexpr int kMax8 = kTThreads / 8;
     const int g8 = kMax8 * cluster, gt = kTThreads * cluster * subs;  // maxima of eight threads, of (a part of) one
-    if (top < INFINITY && (few || (k < V && 2 * k <= gt))) {
+    // with k of gt maxima to reach, some -gt ln(1 - k / gt) elements do
+    const int most_k = (int)((float)gt * fminf(0.95f, 1.0f - expf(-1800.0f / (float)gt)));
+    if (top < INFINITY && (few || (k < V && k <= most_k))) {
         float least_value = -INFINITY;
         if (!few) {
             // (a little below) the k-th largest of the maxima

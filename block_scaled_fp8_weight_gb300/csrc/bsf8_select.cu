@@ -281,6 +281,25 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
     if (cluster > 1) cluster_arrive();  // the first block's memory may be written once it runs
 
     if (choose) {
+        // a warp takes 32 pages: a lane each asks for their entries, then their bounds come, a batch of passes on their
+        // way while the one before is multiplied; the first batch before the queries are looked at
+        constexpr int LPP = D / 8, PPW = 32 / LPP, EB = D / 32, HALF = D / 16;
+        const int l = lane % LPP, part = l / HALF, ch = 16 * (l % HALF), blk = ch / 32;
+        constexpr int PASSES = 32 / PPW, U = MANY ? 4 : 8;
+        const int first = (rank * kSWarps + warp) * 32, stride = cluster * kSWarps * 32;
+        int page = !MANY && first + lane < full ? table[first + lane] : -1;
+        uint4 w[U];
+        uint32_t e[U];
+        auto ask = [&](int i, uint4 &w_, uint32_t &e_) {
+            const int at = __shfl_sync(0xFFFFFFFFu, page, (PPW * i + lane / LPP) & 31);
+            w_ = make_uint4(0, 0, 0, 0);
+            e_ = 256;  // no such page
+            if ((unsigned)at < (unsigned)v.pages) {
+                const size_t row = (size_t)at * v.heads + h;
+                w_ = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
+                e_ = v.exps[row * EB + blk];
+            }
+        };
         // ---------------------------------------------------------- the rows' queries
         constexpr int LPQ = D / 8;  // 16-byte pieces a row
         const int rows = nodes * g, u = tid % LPQ;
@@ -289,18 +308,23 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
             return *reinterpret_cast<const uint4 *>(a.q + ((size_t)b * a.T + t) * a.ldq + (size_t)(h * g + r - t * g) * D + 8 * u);
         };
         for (int i = tid; i < 2 * D; i += kSThreads) s.q[i / D][i % D] = 0;
-        // f(piece) of this thread's rows, four on their way; the first four stay for the second turn
+        // f(piece) of this thread's rows, four on their way; the first ones stay for the second turn
         constexpr int RPP = kSThreads / LPQ;  // rows at a time
         const int r0 = tid / LPQ;
-        uint4 kept[4];
+        constexpr int KEPT = MANY ? 1 : 4;
+        uint4 kept[KEPT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < KEPT; ++j)
             if (r0 + j * RPP < rows) kept[j] = piece(r0 + j * RPP);
+        if (!MANY) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
+        }
         auto each = [&](auto f) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < KEPT; ++j)
                 if (r0 + j * RPP < rows) f(kept[j]);
-            for (int r = r0 + 4 * RPP; r < rows; r += 4 * RPP) {
+            for (int r = r0 + KEPT * RPP; r < rows; r += 4 * RPP) {
                 uint4 w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -363,8 +387,6 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
         const int sh = max(0, 32 - __clz(big) - 14), half = (1 << sh) >> 1;
         // ---------------------------------------------------------- scores
         // 2 D codes a page, 16 a lane: the maxima's lanes, then the minima's
-        constexpr int LPP = D / 8, PPW = 32 / LPP, EB = D / 32, HALF = D / 16;
-        const int l = lane % LPP, part = l / HALF, ch = 16 * (l % HALF), blk = ch / 32;
         uint32_t qh[4], ql[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -378,29 +400,14 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
         }
         if (cluster > 1) cluster_wait();
         const uint32_t keys0 = cluster > 1 ? map_to_rank(keys, 0) : 0;
-        // a warp takes 32 pages: a lane each asks for their entries, then their bounds come, a batch of passes on their
-        // way while the one before is multiplied
-        constexpr int PASSES = 32 / PPW, U = MANY ? 4 : 8;
-        const int first = (rank * kSWarps + warp) * 32, stride = cluster * kSWarps * 32;
-        int next = first + lane < full ? table[first + lane] : -1;
+        if (MANY && first + lane < full) page = table[first + lane];
         for (int p0 = first; p0 < full; p0 += stride) {
-            const int page = next;
-            next = p0 + stride + lane < full ? table[p0 + stride + lane] : -1;
             const int passes = (min(32, full - p0) + PPW - 1) / PPW;
-            uint4 w[U];
-            uint32_t e[U];
-            auto ask = [&](int i, uint4 &w_, uint32_t &e_) {
-                const int at = __shfl_sync(0xFFFFFFFFu, page, (PPW * i + lane / LPP) & 31);
-                w_ = make_uint4(0, 0, 0, 0);
-                e_ = 256;  // no such page
-                if ((unsigned)at < (unsigned)v.pages) {
-                    const size_t row = (size_t)at * v.heads + h;
-                    w_ = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
-                    e_ = v.exps[row * EB + blk];
-                }
-            };
+            if (p0 > first || MANY) {
 #pragma unroll
-            for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
+                for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
+            }
+            int next = p0 + stride + lane < full ? table[p0 + stride + lane] : -1;
             for (int i0 = 0; i0 < passes; i0 += U) {
                 // step by step over the whole batch: its chains of shuffles run side by side
                 int S[U];
@@ -444,6 +451,7 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
                     else keys[p] = key;
                 }
             }
+            page = next;
         }
     } else if (cluster > 1) {
         cluster_wait();
