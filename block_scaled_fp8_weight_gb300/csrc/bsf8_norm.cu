@@ -59,6 +59,51 @@ __device__ __forceinline__ void residual_of(const uint4 &r, const uint4 &r2, flo
     }
 }
 
+// A row's squares are added up in one order whatever the kernel, so that a row's bits do not depend on how many come with
+// it: channels in fours, one after another; the fours of 256 channels (64) by a tree, neighbours first; then those sums,
+// c, c + 32, .. one after another and the 32 of them by a tree, far ones first.
+template <int N>
+__device__ __forceinline__ float squares(const float (&z)[N]) {
+    float sum[N / 4];
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) {
+        sum[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[k] = fmaf(z[4 * k + i], z[4 * k + i], sum[k]);
+    }
+    return N == 4 ? sum[0] : sum[0] + sum[N / 4 - 1];
+}
+
+// J trees over a warp's lanes side by side: lane l gets the sum of all lanes' v[l % J], every shuffle carrying what
+// the other lane needs.
+template <int J>
+__device__ __forceinline__ float lane_sums(float (&v)[J]) {
+    const uint32_t lane = threadIdx.x & 31;
+    int n = J;
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+        if (n == 1) {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], m);
+            continue;
+        }
+        n /= 2;
+#pragma unroll
+        for (int q = 0; q < J / 2; ++q) {
+            if (q >= n) continue;
+            const bool odd = lane & m;
+            const float keep = odd ? v[2 * q + 1] : v[2 * q], send = odd ? v[2 * q] : v[2 * q + 1];
+            v[q] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, m);
+        }
+    }
+    return v[0];
+}
+
+__device__ __forceinline__ float far_first(float v) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+    return v;
+}
+
 }  // namespace
 
 // P pieces of 8 channels a thread; `warps` warps a row, blockDim / (32 warps) rows a block.  Few rows: one piece a
@@ -69,7 +114,7 @@ __device__ __forceinline__ void residual_of(const uint4 &r, const uint4 &r2, flo
 template <int P, bool F32>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps) {
     constexpr int WORDS = F32 ? 3 : 2;  // of 16 bytes a piece: x, the residual
-    __shared__ float s_sum[2][kMaxWarps];
+    __shared__ float s_sum[2][P * kMaxWarps];
     extern __shared__ uint4 ring[];
     pdl_trigger();
     pdl_wait();
@@ -103,36 +148,43 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps)
     }
     if constexpr (P > 1) asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     auto vec = [&](const uint16_t *v, int p) { return *reinterpret_cast<const uint4 *>(v + 8 * (t + p * threads)); };
-    // the sum of v over the row's threads
-    auto row_sum = [&](float v, int which) {
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-        if (warps == 1) return v;
-        if (lane == 0) s_sum[which][warp] = v;
+    // the sum over the row of the pieces' sums
+    auto row_sum = [&](float (&v)[P], int which) {
+        float sum = lane_sums(v);
+        if (warps == 1) {
+            if (P > 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2), sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            return sum;
+        }
+        float *const at = s_sum[which] + P * w0;  // by 256 channels
+        if (lane < P) at[lane * warps + warp - w0] = sum;
         __syncthreads();
-        v = lane < warps ? s_sum[which][w0 + lane] : 0.0f;
+        sum = lane < P * warps ? at[lane] : 0.0f;
+        if (P > 1 && P * warps > 32) {
+            float more[P];
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-        return v;
+            for (int k = 1; k < P; ++k) more[k] = lane + 32 * k < P * warps ? at[lane + 32 * k] : 0.0f;
+#pragma unroll
+            for (int k = 1; k < P; ++k) sum += more[k];
+        }
+        return far_first(sum);
     };
     float f = a.scale;
     if (a.gate_kind == kGateToken && real) f *= __uint_as_float((uint32_t)a.gate[row * a.ldg] << 16);
-    float z[P][8];
-    float ss = 0.0f;
+    float z[P][8], ss[P];
     if (a.post) {
 #pragma unroll
         for (int p = 0; p < P; ++p) {
+            ss[p] = 0.0f;
             if (!real || 8 * (t + p * threads) >= a.H) continue;
             widen8(P == 1 ? x0 : *slot(p), z[p]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(z[p][i], z[p][i], ss);
+            ss[p] = squares(z[p]);
         }
     }
     const float n = a.post ? rsqrtf(fmaf(row_sum(ss, 0), inv, a.eps)) : 1.0f;
-    ss = 0.0f;
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int c = 8 * (t + p * threads);
+        ss[p] = 0.0f;
         if (!real || c >= a.H) continue;
         const uint4 *const at = slot(p);
         float g[8];
@@ -150,10 +202,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps)
         float r[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (a.residual) residual_of<F32>(P == 1 ? r0 : at[step], P == 1 ? r1 : at[F32 ? 2 * step : 0], r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            z[p][i] = fmaf(f, z[p][i], r[i]);
-            ss = fmaf(z[p][i], z[p][i], ss);
-        }
+        for (int i = 0; i < 8; ++i) z[p][i] = fmaf(f, z[p][i], r[i]);
+        ss[p] = squares(z[p]);
         if (a.r_out) {
             if constexpr (F32) {
                 float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.r_out) + row * a.H + c);
@@ -210,67 +260,80 @@ struct Unit<true> {
 };
 
 // Many rows: one block an SM in groups of `warps` warps, a group a row at a time, 32 channels a thread.  The weights
-// lie in shared memory for good; a row comes there by bulk copies of one thread, the next row's asked for as soon as
-// this one's are used up, under its last stores.
-// 8191 rows of 5120 (fp32 residual, both norms, channel gate): 87 us, 5.8 TB/s of what must move (0.86 of the measured
+// lie in shared memory for good; a row comes there by bulk copies of one thread, the next row's (or the one after) asked
+// for as soon as this one's are used up, under its last stores.
+// 8191 rows of 5120 (fp32 residual, both norms, channel gate): 85 us, 5.9 TB/s of what must move (0.87 of the measured
 // rate); waits for the loads are two thirds of a row's time in its group.  Six groups at 64 registers: 135 us, their
-// spills go to L2; a block a row (the kernel below): 110; the same with 640 threads a row: 122.
+// spills go to L2; a block a row (the kernel above): 110; the same with 640 threads a row: 97.
 template <bool F32>
-__global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const NormArgs a, int warps, int groups, unsigned long long timeout_ns,
-                                                            int skip_loads, int *status) {
+__global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const NormArgs a, int warps, int groups, int depth,
+                                                                       unsigned long long timeout_ns, int skip_loads, int *status) {
     using U = Unit<F32>;
     using Half = typename U::Half;
     constexpr int N = U::N, J = 32 / N;
-    __shared__ float s_sum[2][kMaxWarps];
-    __shared__ uint64_t s_full[kMaxWarps];
+    static_assert(4 * kRowsWarps <= 96, "three sums of 256 channels a lane");
+    __shared__ __align__(8) float s_sum[2][J * kRowsWarps];
+    __shared__ uint64_t s_full[2 * kRowsWarps];
     extern __shared__ uint4 memory[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = warp / warps, w0 = group * warps;
     const int t = (int)threadIdx.x - 32 * w0, threads = 32 * warps, step = (int)blockDim.x, units = a.H / N;
-    if (t == 0) mbar_init(&s_full[group], 1);
+    const int first = group * depth, buffers = groups * depth;  // its first buffer
+    if (t == 0) {
+        for (int d = 0; d < depth; ++d) mbar_init(&s_full[first + d], 1);
+    }
     fence_mbar_init();
     __syncthreads();
     pdl_trigger();
     pdl_wait();
     const float inv = 1.0f / (float)a.H;
     const bool full = a.gate_kind == kGateFull, channel = a.gate_kind == kGateChannel;
-    // each group's row of the residual, of x and of a full gate; then weight, post_weight and a channel gate
-    uint4 *const r_at = memory + group * units;
-    Half *const x_at = reinterpret_cast<Half *>(memory + groups * units) + group * units;
-    Half *const g_at = reinterpret_cast<Half *>(memory + groups * units) + (groups + group) * units;
-    Half *const vec = reinterpret_cast<Half *>(memory + groups * units) + (full ? 2 : 1) * groups * units;
+    // the buffers' rows of the residual, of x and of a full gate; then weight, post_weight and a channel gate
+    Half *const x_rows = reinterpret_cast<Half *>(memory + buffers * units);
+    Half *const vec = x_rows + (full ? 2 : 1) * buffers * units;
     const uint32_t row_bytes = (uint32_t)a.H * 2;
-    auto ask = [&](long long row) {
+    auto ask = [&](long long row, int b) {
         if (t != 0 || row >= a.M) return;
-        mbar_arrive_expect_tx(&s_full[group], row_bytes * (full ? 2u : 1u) + (a.residual ? row_bytes * (F32 ? 2u : 1u) : 0u));
+        mbar_arrive_expect_tx(&s_full[b], row_bytes * (full ? 2u : 1u) + (a.residual ? row_bytes * (F32 ? 2u : 1u) : 0u));
         if (skip_loads) return;
-        bulk_g2s(x_at, a.x + row * a.ldx, row_bytes, &s_full[group]);
-        if (full) bulk_g2s(g_at, a.gate + row * a.ldg, row_bytes, &s_full[group]);
+        bulk_g2s(x_rows + b * units, a.x + row * a.ldx, row_bytes, &s_full[b]);
+        if (full) bulk_g2s(x_rows + (buffers + b) * units, a.gate + row * a.ldg, row_bytes, &s_full[b]);
         if (a.residual)
-            bulk_g2s(r_at, static_cast<const char *>(a.residual) + row * a.ldr * (F32 ? 4 : 2), row_bytes * (F32 ? 2 : 1), &s_full[group]);
+            bulk_g2s(memory + b * units, static_cast<const char *>(a.residual) + row * a.ldr * (F32 ? 4 : 2), row_bytes * (F32 ? 2 : 1), &s_full[b]);
     };
     const long long stride = (long long)gridDim.x * groups;
     long long row = (long long)blockIdx.x * groups + group;
-    ask(row);
+    for (int d = 0; d < depth; ++d) ask(row + d * stride, first + d);
     for (int i = threadIdx.x; i < units; i += step) {
         if (a.h) vec[i] = reinterpret_cast<const Half *>(a.weight)[i];
         if (a.post) vec[units + i] = reinterpret_cast<const Half *>(a.post)[i];
         if (channel) vec[2 * units + i] = reinterpret_cast<const Half *>(a.gate)[i];
     }
     __syncthreads();
-    // the sum of v over the group
+    // the sum over the row of the units' sums
     uint32_t sums = 0;  // two sets of slots in turn: one is written again after the barrier of the other
-    auto group_sum = [&](float v) {
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-        if (warps == 1) return v;
-        float *const at = s_sum[sums++ & 1];
-        if (lane == 0) at[warp] = v;
+    auto group_sum = [&](float (&v)[J]) {
+        float sum = lane_sums(v);
+        if (warps == 1) {
+            if (J == 8) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, J / 2);
+            return sum + __shfl_xor_sync(0xFFFFFFFFu, sum, J / 4);
+        }
+        float *const at = s_sum[sums++ & 1] + J * w0;  // by 32 N channels
+        if (lane < J) at[lane * warps + warp - w0] = sum;
         asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-        v = lane < warps ? at[w0 + lane] : 0.0f;
-#pragma unroll
-        for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-        return v;
+        auto piece = [&](int c) {
+            if (c >= 4 * warps) return 0.0f;
+            if constexpr (J == 4) return at[c];
+            const float2 two = reinterpret_cast<const float2 *>(at)[c];
+            return two.x + two.y;
+        };
+        sum = piece(lane);
+        if (4 * warps > 32) {
+            const float more = piece(lane + 32), last = piece(lane + 64);
+            sum = sum + more + last;
+        }
+        return far_first(sum);
     };
     // whether v holds for the whole group, which so goes on or leaves as one
     auto group_all = [&](bool v) {
@@ -283,32 +346,38 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const Nor
         return all != 0;
     };
     uint32_t phase = 0;
+    int d = 0;
     for (; row < a.M; row += stride) {
+        const int b = first + d;
         float f = a.scale;
         if (a.gate_kind == kGateToken) f *= __uint_as_float((uint32_t)a.gate[row * a.ldg] << 16);
-        if (!group_all(mbar_wait_bounded(&s_full[group], phase, timeout_ns))) {
+        if (!group_all(mbar_wait_bounded(&s_full[b], phase, timeout_ns))) {
             // the wait ran out: what was asked for may still land, and the block's memory is not left before
             report_timeout(status);
-            if (!skip_loads) (void)mbar_wait_bounded(&s_full[group], phase, timeout_ns);
+            if (!skip_loads) {
+                (void)mbar_wait_bounded(&s_full[b], phase, timeout_ns);
+                if (depth > 1 && row + stride < a.M) (void)mbar_wait_bounded(&s_full[first + (d ^ 1)], phase ^ d, timeout_ns);
+            }
             return;
         }
-        phase ^= 1;
-        float z[J][N];
-        float ss = 0.0f, n = 1.0f;
+        if (++d == depth) d = 0, phase ^= 1;
+        const uint4 *const r_at = memory + b * units;
+        const Half *const x_at = x_rows + b * units, *const g_at = x_rows + (buffers + b) * units;
+        float z[J][N], ss[J], n = 1.0f;
         if (a.post) {
 #pragma unroll
             for (int j = 0; j < J; ++j) {
+                ss[j] = 0.0f;
                 if (t + j * threads >= units) continue;
                 U::widen(x_at[t + j * threads], z[j]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) ss = fmaf(z[j][i], z[j][i], ss);
+                ss[j] = squares(z[j]);
             }
             n = rsqrtf(fmaf(group_sum(ss), inv, a.eps));
-            ss = 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int u = t + j * threads;
+            ss[j] = 0.0f;
             if (u >= units) continue;
             float g[N];
             U::widen(x_at[t + j * threads], z[j]);
@@ -325,15 +394,13 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const Nor
             float r[N] = {};
             if (a.residual) U::residual(r_at[u], r);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                z[j][i] = fmaf(f, z[j][i], r[i]);
-                ss = fmaf(z[j][i], z[j][i], ss);
-            }
+            for (int i = 0; i < N; ++i) z[j][i] = fmaf(f, z[j][i], r[i]);
+            ss[j] = squares(z[j]);
             if (a.r_out) static_cast<uint4 *>(a.r_out)[row * units + u] = U::store(z[j]);
         }
         const float k = rsqrtf(fmaf(group_sum(ss), inv, a.eps));
         if (warps == 1) __syncwarp();
-        ask(row + stride);  // the whole group has read this row
+        ask(row + depth * stride, b);  // the whole group has read this row
         if (!a.h) continue;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
@@ -348,19 +415,23 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 1) norm_rows_kernel(const Nor
     }
 }
 
-// Groups of a block: as many as its threads, named barriers (15) and shared memory allow.
+// Groups of a block: as many as its threads, named barriers (15) and shared memory allow; with two rows each where that
+// takes no group away (8191 rows, fp32 residual, both norms, channel gate: of 7168 two groups 127 -> 119 us, of 12288 one
+// group 257 -> 195; of 5120 three groups for four 87 -> 90).
 template <bool F32>
-int row_groups(int H, bool full, size_t *bytes) {
+int row_groups(int H, bool full, int *depth, size_t *bytes) {
     const int warps = (H / 8 + 127) / 128;
     const size_t row = (size_t)H * (2 + (F32 ? 4 : 2) + (full ? 2 : 0)), weights = (size_t)3 * H * 2;
-    int g = std::min(warps == 1 ? kRowsWarps : 15, kRowsWarps / warps);
-    while (g > 0 && weights + g * row > (size_t)kMaxRows) --g;
-    *bytes = weights + g * row;
-    return g;
+    const int most = std::min(warps == 1 ? kRowsWarps : 15, kRowsWarps / warps);
+    if (weights + row > (size_t)kMaxRows) return 0;
+    const int one = std::min(most, (int)((kMaxRows - weights) / row)), two = std::min(most, (int)((kMaxRows - weights) / (2 * row)));
+    *depth = two == one ? 2 : 1;
+    *bytes = weights + one * *depth * row;
+    return one;
 }
 
 template <bool F32>
-cudaError_t launch_rows(const NormArgs &a, int groups, size_t smem, cudaStream_t stream) {
+cudaError_t launch_rows(const NormArgs &a, int groups, int depth, size_t smem, cudaStream_t stream) {
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -384,7 +455,7 @@ cudaError_t launch_rows(const NormArgs &a, int groups, size_t smem, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = options().pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, norm_rows_kernel<F32>, a, warps, groups, options().timeout_ns, options().skip_loads, status);
+    return cudaLaunchKernelEx(&cfg, norm_rows_kernel<F32>, a, warps, groups, depth, options().timeout_ns, options().skip_loads, status);
 }
 
 template <int P, bool F32>
@@ -419,12 +490,20 @@ cudaError_t norm_pieces(const NormArgs &a, cudaStream_t stream) {
 
 template <bool F32>
 cudaError_t norm_typed(const NormArgs &a, cudaStream_t stream) {
-    // work for several turns of every group: a block an SM
+    // One piece a thread while the SMs hold all rows in a turn or two, and for an fp32 residual without a first norm where
+    // rows are short.  Else the rows' kernel if more than two bytes a channel come beside x (its copies make whole sectors
+    // of them), four pieces a thread if not.  One piece / four / the rows' kernel, us (gate: a post norm and an fp32
+    // residual too): 304 rows of 5120 bf16 3.0 / 3.7 / 4.0, gate 4.5 / 6.9 / 6.0; 500 of 4096 bf16 4.2 / 5.3 / 4.4, gate
+    // 6.8 / 11 / 6.4; 304 of 7168 bf16 4.5 / 4.0 / 3.9; 8191 of 5120 bf16 65 / 50 / 54, with a full gate 96 / 78 / 69, gate
+    // 97 / 110 / 85, fp32 without a first norm 78 / 95 / 86; of 7168 bf16 122 / 69 / 82, fp32 135 / 130 / 117; six rows of
+    // 12288, gate - / 7.1 / 6.1.
+    const bool full = a.gate_kind == kGateFull;
+    const long long few = 152LL * (F32 || full || a.H > 5120 ? 10240 : 16384);  // channels
+    if (a.H <= 8192 && (a.M * (long long)a.H <= few || (F32 && !a.post && !full && a.H <= 5120))) return norm_pieces<1, F32>(a, stream);
+    int depth;
     size_t smem;
-    const int groups = row_groups<F32>(a.H, a.gate_kind == kGateFull, &smem);
-    if (groups >= 2 && (long long)a.M >= 152LL * 2 * groups) return launch_rows<F32>(a, groups, smem, stream);
-    // one piece a thread while no more than one block of them comes to an SM
-    return a.H <= 8192 && (long long)a.M * a.H <= 152LL * 8192 ? norm_pieces<1, F32>(a, stream) : norm_pieces<4, F32>(a, stream);
+    const int groups = F32 || full ? row_groups<F32>(a.H, full, &depth, &smem) : 0;
+    return groups > 0 ? launch_rows<F32>(a, groups, depth, smem, stream) : norm_pieces<4, F32>(a, stream);
 }
 
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t stream) {

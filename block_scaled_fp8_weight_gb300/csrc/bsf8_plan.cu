@@ -5,8 +5,8 @@
 // scans), so that nothing but the pages themselves goes from one to the other -- what the first half gives
 // back the second may hand out, with the cluster's barrier between them -- and share the pages and tokens
 // evenly.  Few requests and tokens take one small block: what it costs is the chain of loads, scans and
-// barriers.  (1024 requests, half of them leaving, 198000 tokens: 9.6 us in a graph, 13.7 with eight blocks, 30 with
-// those of 512 threads, three scans and a search a token; seven requests of a few tokens 2.9.)
+// barriers.  (1024 requests, half of them leaving, 198000 tokens: 9.2 us in a graph, 13.7 with eight blocks, 30 with
+// those of 512 threads, three scans and a search a token; seven requests of a few tokens 2.6.)
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
@@ -235,7 +235,8 @@ cudaError_t plan_threads(const PlanArgs &a, int cluster, cudaStream_t stream, in
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
-    if (a.B <= 128 && a.N <= 4096) return plan_threads<128>(a, 1, stream, status);
+    // (one block / the cluster: 64 requests, 576 tokens 3.7 us / 4.9; 128, 1152 tokens 4.7 / 5.05; 64, 4096 tokens 5.95 / 5.0)
+    if (a.B <= 128 && a.N <= 1536) return plan_threads<128>(a, 1, stream, status);
     // clusters of 16 blocks: asked for once per device
     static int known[64] = {0};  // 0 unknown, else the cluster
     int dev = 0;

@@ -565,6 +565,7 @@ int bsf8_token_probs(const void *logits, int bf16, int64_t ld, const float *temp
  *   z = x * rsqrt(mean(x^2) + eps) * post_weight     (post_weight NULL: z = x)
  *   r = residual + scale * gate * z                  (residual NULL: 0;  no gate: 1)
  *   h = r * rsqrt(mean(r^2) + eps) * weight          (of r before its rounding)
+ * A row's bits depend on the row, H, fp32 and what is applied alone, not on how many rows come with it.
  *   x            device, bf16 [M][ldx];  post_weight, weight  device, bf16 [H]
  *   residual     device, [M][ldr], fp32 where fp32 != 0, else bf16
  *   gate         device, bf16: BSF8_GATE_CHANNEL [H], BSF8_GATE_TOKEN one of each row at gate[m * ldg],

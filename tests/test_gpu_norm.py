@@ -107,6 +107,23 @@ def test_same_bits_whatever_else_is_in_the_call(bsf8_lib):
         assert torch.equal(a[0], h[i]) and torch.equal(b[0], o[i])
 
 
+@pytest.mark.parametrize("H", [200, 1000, 2056, 5120, 7168, 8192, 12288, 16392])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_same_bits_in_calls_of_every_size(bsf8_lib, H, fp32):
+    """The kernels for few and for many rows add up a row's squares in one order."""
+    r = np.random.default_rng(H)
+    M = 2600 if H < 8000 else 700
+    x, res, w, g = bf16(r, M, H, scale=3.0), bf16(r, M, H), bf16(r, H), bf16(r, M, H)
+    if fp32:
+        res = res.float() * 1.001
+    for post in (None, w):
+        for gate in (None, g):
+            h, o = bsf8.residual_norm(x, res, w, post_weight=post, gate=gate)
+            for n in (1, 9, 150, 450, 1300):
+                a, b = bsf8.residual_norm(x[-n:], res[-n:], w, post_weight=post, gate=None if gate is None else g[-n:])
+                assert torch.equal(a, h[-n:]) and torch.equal(b, o[-n:])
+
+
 def test_refused_tensors(bsf8_lib):
     x = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)
     w = torch.ones(64, device="cuda", dtype=torch.bfloat16)
@@ -124,18 +141,20 @@ def test_refused_tensors(bsf8_lib):
         f(x[:, 1:57], x[:, 8:], w[:56])  # not 16-byte aligned
 
 
-def test_a_wait_that_runs_out_is_reported(bsf8_lib):
+@pytest.mark.parametrize("M,H", [(3000, 5120), (1500, 7168)])  # one row ahead, and two
+def test_a_wait_that_runs_out_is_reported(bsf8_lib, M, H):
     """No loads are issued (a test-only option): the kernel for many rows gives up its waits and says so."""
-    x = torch.ones(3000, 5120, device="cuda", dtype=torch.bfloat16)
-    w = torch.ones(5120, device="cuda", dtype=torch.bfloat16)
+    x = torch.ones(M, H, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    res = x.float()
     h = torch.full_like(x, 7.0)
     try:
         bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 1)
         bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 1000000)
-        bsf8.residual_norm(x, x, w, post_weight=w, out=h)
+        bsf8.residual_norm(x, res, w, post_weight=w, out=h)
         assert bsf8.device_status() == 7 and (h == 7).all()
     finally:
         bsf8.set_option(bsf8.OPT_DEBUG_SKIP_LOADS, 0)
         bsf8.set_option(bsf8.OPT_WAIT_TIMEOUT_NS, 2000000000)
-    bsf8.residual_norm(x, x, w, post_weight=w, out=h)
+    bsf8.residual_norm(x, res, w, post_weight=w, out=h)
     assert bsf8.device_status() == 0 and (h == 1).all()
