@@ -12,6 +12,7 @@
 #include "bsf8_internal.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace bsf8 {
 
@@ -217,6 +218,10 @@ cudaError_t launch_bounds(const CacheView &c, const BoundsView &v, const int32_t
 // order), scores its share of the pages and puts their keys -- the scores' bits, ordered as integers --
 // into the first block's shared memory, which then finds the key of rank `keep` by digits of what the
 // keys differ in, and writes the pages before it, ties by their index, in ascending order.
+// Bounds come by asynchronous copies, 8 KB a warp on their way: two blocks an SM at 128 registers keep what a lane's
+// two chains of products need (three at 80 spilled: 32 requests 21.7 us for 16).  32 requests of up to 65536 tokens, 8
+// heads: 16 us with the bounds (34 MB) in L2, 23 without, of which DRAM is 5; one of 131072: 10, the chain of loads (lengths,
+// table, bounds), the queries' four barriers, a turn of products (1.5), the cluster's barrier, the digits (2) and the list (1.5).
 namespace {
 
 constexpr int kSThreads = 256, kSWarps = kSThreads / 32;
@@ -225,9 +230,8 @@ constexpr int kSBins = 2048, kSBinsEach = kSBins / kSThreads;
 constexpr uint32_t kTopKey = 0xFF800000u;  // of +inf
 
 struct SelectShared {
-    int q[2][256];              // sums of the rows' positive and negative parts
+    alignas(16) int q[2][256];  // sums of the rows' positive and negative parts; then their bytes
     int red[kSWarps], wsum[kSWarps];
-    int hist[kSBins];           // counts of the keys; then the chosen pages, where that many suffice
     uint32_t lo, hi;            // smallest and largest key below the top one
     int top;                    // keys that are the top one
     int want, digit, count;
@@ -249,6 +253,26 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+// 16 bytes, or zeros where `bytes` is 0 (then nothing is read).
+__device__ __forceinline__ void async16(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// A page's exponent bytes of a head, held by one lane; byte(word, lane, i): byte i of what `lane` holds.
+template <int EB>
+struct ExpWord {
+    typedef typename std::conditional<EB == 2, uint16_t, uint32_t>::type T;
+    static __device__ __forceinline__ uint32_t byte(T w, int lane, int i) { return __shfl_sync(0xFFFFFFFFu, (uint32_t)w, lane) >> 8 * i & 255u; }
+};
+template <>
+struct ExpWord<8> {
+    typedef uint2 T;
+    static __device__ __forceinline__ uint32_t byte(uint2 w, int lane, int i) {
+        const uint32_t x = __shfl_sync(0xFFFFFFFFu, w.x, lane), y = __shfl_sync(0xFFFFFFFFu, w.y, lane);
+        return (i < 4 ? x : y) >> 8 * (i & 3) & 255u;
+    }
+};
+
 // Larger keys for larger scores; equal ones for 0 and -0.
 __device__ __forceinline__ uint32_t key_of(float f) {
     const uint32_t b = __float_as_uint(f + 0.0f);
@@ -257,11 +281,30 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 
 }  // namespace
 
-// MANY: for many pairs of a request and a head, fewer loads ahead for four blocks an SM, whose phases hide each other.
-template <int D, bool MANY>
-__global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const BoundsView v, const SelectArgs a, int cluster, int *status) {
+// How a warp goes through its pages: PAGES a turn, in BATCHES of 2 KB.  Four copies of 16 bytes a lane bring a batch to
+// shared memory, whole sectors at a time; there a lane takes all of 32 channels, LPP lanes a page.
+template <int D>
+struct Turn {
+    static constexpr int LPP = D / 32, PPB = 32 / LPP;  // lanes a page, pages a batch
+    static constexpr int PAGES = D == 256 ? 16 : 32, BATCHES = PAGES / PPB;
+    static constexpr int CHUNKS = D / 8;                // of 16 bytes a page
+    static constexpr int BLOCK = kSWarps * 2048;
+    // where chunk c of a batch's page lies: eight lanes that read theirs at once touch all banks
+    static __device__ __forceinline__ int at(int page, int c) {
+        return page * CHUNKS + (D == 64 ? c ^ ((page & 1) | (page & 2) << 1) : D == 128 ? c ^ (page & 1) : c ^ (c >> 3 & 1));
+    }
+};
+
+// `depth` batches of a warp (2 or 4, no more than a turn's) are on their way at a time.
+template <int D>
+__global__ void __launch_bounds__(kSThreads, 2) select_kernel(const BoundsView v, const SelectArgs a, int cluster, int depth, int *status) {
+    using W = Turn<D>;
     __shared__ SelectShared s;
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint8_t select_memory[];
+    static_assert(W::BLOCK >= kSBins * 4, "the histogram lies there after the scores");
+    uint8_t *const batches = select_memory;
+    int *const hist = reinterpret_cast<int *>(select_memory);  // counts of the keys; then the chosen pages, where that many suffice
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(select_memory + depth * W::BLOCK);
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -281,25 +324,28 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
     if (cluster > 1) cluster_arrive();  // the first block's memory may be written once it runs
 
     if (choose) {
-        // a warp takes 32 pages: a lane each asks for their entries, then their bounds come, a batch of passes on their
-        // way while the one before is multiplied; the first batch before the queries are looked at
-        constexpr int LPP = D / 8, PPW = 32 / LPP, EB = D / 32, HALF = D / 16;
-        const int l = lane % LPP, part = l / HALF, ch = 16 * (l % HALF), blk = ch / 32;
-        constexpr int PASSES = 32 / PPW, U = MANY ? 4 : 8;
-        const int first = (rank * kSWarps + warp) * 32, stride = cluster * kSWarps * 32;
-        int page = !MANY && first + lane < full ? table[first + lane] : -1;
-        uint4 w[U];
-        uint32_t e[U];
-        auto ask = [&](int i, uint4 &w_, uint32_t &e_) {
-            const int at = __shfl_sync(0xFFFFFFFFu, page, (PPW * i + lane / LPP) & 31);
-            w_ = make_uint4(0, 0, 0, 0);
-            e_ = 256;  // no such page
-            if ((unsigned)at < (unsigned)v.pages) {
-                const size_t row = (size_t)at * v.heads + h;
-                w_ = *reinterpret_cast<const uint4 *>(v.codes + row * 2 * D + 16 * l);
-                e_ = v.exps[row * EB + blk];
+        // a lane each asks for a page's entry and exponents, then its bounds come, batches on their way while earlier ones are
+        // multiplied; the first before the queries are looked at
+        constexpr int LPP = W::LPP, PPB = W::PPB, PAGES = W::PAGES, EB = D / 32;
+        using Word = typename ExpWord<EB>::T;
+        const int blk = lane % LPP;
+        const int first = (rank * kSWarps + warp) * PAGES, stride = cluster * kSWarps * PAGES;
+        uint8_t *const mine = batches + warp * depth * 2048;
+        auto entry = [&](int p) { return lane < PAGES && p + lane < full ? table[p + lane] : -1; };
+        auto row_of = [&](int page) { return (unsigned)page < (unsigned)v.pages ? page * v.heads + h : -1; };
+        auto word_of = [&](int row) { return row >= 0 ? reinterpret_cast<const Word *>(v.exps)[row] : Word{}; };
+        // two batches of a turn's rows, `sub` the first
+        auto ask = [&](int row, int sub) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int in = (lane + 32 * (j & 3)) / W::CHUNKS, c = (lane + 32 * (j & 3)) % W::CHUNKS;
+                const int from = __shfl_sync(0xFFFFFFFFu, row, PPB * (sub + j / 4) + in);
+                async16(mine + ((sub + j / 4) & (depth - 1)) * 2048 + 16 * W::at(in, c), v.codes + (size_t)max(from, 0) * 2 * D + 16 * c,
+                        from >= 0 ? 16u : 0u);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        int row = row_of(entry(first));
         // ---------------------------------------------------------- the rows' queries
         constexpr int LPQ = D / 8;  // 16-byte pieces a row
         const int rows = nodes * g, u = tid % LPQ;
@@ -311,15 +357,14 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
         // f(piece) of this thread's rows, four on their way; the first ones stay for the second turn
         constexpr int RPP = kSThreads / LPQ;  // rows at a time
         const int r0 = tid / LPQ;
-        constexpr int KEPT = MANY ? 1 : 4;
+        constexpr int KEPT = 4;
         uint4 kept[KEPT];
 #pragma unroll
         for (int j = 0; j < KEPT; ++j)
             if (r0 + j * RPP < rows) kept[j] = piece(r0 + j * RPP);
-        if (!MANY) {
-#pragma unroll
-            for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
-        }
+        Word word = word_of(row);
+        for (int i = 0; i < depth; i += 2) ask(row, i);
+        int next = entry(first + stride);
         auto each = [&](auto f) {
 #pragma unroll
             for (int j = 0; j < KEPT; ++j)
@@ -386,72 +431,83 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
         big = __reduce_max_sync(0xFFFFFFFFu, big);
         const int sh = max(0, 32 - __clz(big) - 14), half = (1 << sh) >> 1;
         // ---------------------------------------------------------- scores
-        // 2 D codes a page, 16 a lane: the maxima's lanes, then the minima's
-        uint32_t qh[4], ql[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            qh[i] = ql[i] = 0;
+        // the sums in two bytes, high and low, four channels a word, where the sums were
+        uint32_t high = 0, low = 0;
+        if (tid < 2 * D / 4) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int z = (s.q[part][ch + 4 * i + j] + half) >> sh;  // |z| <= 2^14
-                qh[i] |= (uint32_t)((z >> 8) & 255) << (8 * j);
-                ql[i] |= (uint32_t)(z & 255) << (8 * j);
+                const int z = (s.q[4 * tid / D][4 * tid % D + j] + half) >> sh;  // |z| <= 2^14
+                high |= (uint32_t)((z >> 8) & 255) << (8 * j);
+                low |= (uint32_t)(z & 255) << (8 * j);
             }
+        }
+        __syncthreads();
+        if (tid < 2 * D / 4) {
+            s.q[0][tid] = (int)high;
+            s.q[1][tid] = (int)low;
+        }
+        __syncthreads();
+        uint4 qh[4], ql[4];  // of this lane's 32 channels: against the maxima, then against the minima
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = (i / 2 * D + 32 * blk + 16 * (i & 1)) / 4;
+            qh[i] = *reinterpret_cast<const uint4 *>(&s.q[0][at]);
+            ql[i] = *reinterpret_cast<const uint4 *>(&s.q[1][at]);
         }
         if (cluster > 1) cluster_wait();
         const uint32_t keys0 = cluster > 1 ? map_to_rank(keys, 0) : 0;
-        if (MANY && first + lane < full) page = table[first + lane];
         for (int p0 = first; p0 < full; p0 += stride) {
-            const int passes = (min(32, full - p0) + PPW - 1) / PPW;
-            if (p0 > first || MANY) {
+            const int ahead = row_of(next), after = entry(p0 + 2 * stride);
+            const Word later = word_of(ahead);
+            if (row < 0 && lane < PAGES && p0 + lane < full) report_index(status);  // no such page
+#pragma unroll 1
+            for (int sub = 0; sub < W::BATCHES; sub += 2) {
+                if (depth == 4) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncwarp();
+                // two batches side by side: what their chains take adds up otherwise
+                int S[2];
 #pragma unroll
-                for (int j = 0; j < U; ++j) ask(j, w[j], e[j]);
-            }
-            int next = p0 + stride + lane < full ? table[p0 + stride + lane] : -1;
-            for (int i0 = 0; i0 < passes; i0 += U) {
-                // step by step over the whole batch: its chains of shuffles run side by side
-                int S[U];
-                float f[U];
-                uint32_t byte[U];
+                for (int k = 0; k < 2; ++k) {
+                    const uint8_t *const batch = mine + ((sub + k) & (depth - 1)) * 2048;
+                    int high[2] = {}, low[2] = {};
 #pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    int sh_ = 0, sl = 0;
-                    sh_ = dp4a_ss(w[j].x, qh[0], sh_), sl = dp4a_su(w[j].x, ql[0], sl);
-                    sh_ = dp4a_ss(w[j].y, qh[1], sh_), sl = dp4a_su(w[j].y, ql[1], sl);
-                    sh_ = dp4a_ss(w[j].z, qh[2], sh_), sl = dp4a_su(w[j].z, ql[2], sl);
-                    sh_ = dp4a_ss(w[j].w, qh[3], sh_), sl = dp4a_su(w[j].w, ql[3], sl);
-                    S[j] = sh_ * 256 + sl;
-                    byte[j] = e[j];
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(batch + 16 * W::at(lane / LPP, i / 2 * (D / 16) + 2 * blk + (i & 1)));
+                        int &H = high[i & 1], &L = low[i & 1];
+                        H = dp4a_ss(w.x, qh[i].x, H), L = dp4a_su(w.x, ql[i].x, L);
+                        H = dp4a_ss(w.y, qh[i].y, H), L = dp4a_su(w.y, ql[i].y, L);
+                        H = dp4a_ss(w.z, qh[i].z, H), L = dp4a_su(w.z, ql[i].z, L);
+                        H = dp4a_ss(w.w, qh[i].w, H), L = dp4a_su(w.w, ql[i].w, L);
+                    }
+                    S[k] = (high[0] + high[1]) * 256 + low[0] + low[1];  // |S| < 2^27
                 }
-                if (i0 + U < passes)
+                __syncwarp();
+                ask(sub + depth < W::BATCHES ? row : ahead, (sub + depth) & (W::BATCHES - 1));
+                float f[2];
 #pragma unroll
-                    for (int j = 0; j < U; ++j) ask(i0 + U + j, w[j], e[j]);
-#pragma unroll
-                for (int j = 0; j < U; ++j) S[j] += __shfl_xor_sync(0xFFFFFFFFu, S[j], 1);
-#pragma unroll
-                for (int j = 0; j < U; ++j) S[j] += __shfl_xor_sync(0xFFFFFFFFu, S[j], HALF);  // |S| < 2^27
-#pragma unroll
-                for (int j = 0; j < U; ++j)
-                    f[j] = byte[j] == 255 ? INFINITY : __fmul_rn(__fmul_rn((float)S[j], 7.450580596923828e-9f), pow2_byte(byte[j] & 255u));
-#pragma unroll
-                for (int m = 2; m < HALF; m <<= 1) {
-#pragma unroll
-                    for (int j = 0; j < U; ++j) f[j] = __fadd_rn(f[j], __shfl_xor_sync(0xFFFFFFFFu, f[j], m));
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t byte = ExpWord<EB>::byte(word, PPB * (sub + k) + lane / LPP, blk);
+                    f[k] = byte == 255 ? INFINITY : __fmul_rn(__fmul_rn((float)S[k], 7.450580596923828e-9f), pow2_byte(byte));
                 }
-                // pass l's by its lane l
-                uint32_t key = 0;
 #pragma unroll
-                for (int j = 0; j < U; ++j)
-                    if (l == j) key = byte[j] < 256 ? key_of(f[j]) : 0;
-                const int p = p0 + PPW * (i0 + l) + lane / LPP;
-                if (l < U && p < min(full, p0 + 32)) {
-                    if (key == 0) report_index(status);  // no such page
+                for (int m = 1; m < LPP; m <<= 1) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) f[k] = __fadd_rn(f[k], __shfl_xor_sync(0xFFFFFFFFu, f[k], m));
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = PPB * (sub + k) + lane / LPP, p = p0 + i;
+                    uint32_t key = __shfl_sync(0xFFFFFFFFu, row, i) < 0 ? 0 : key_of(f[k]);
                     if (p < a.sink || p >= full - a.recent) key = kTopKey;
+                    if (blk != 0 || p >= full) continue;
                     if (cluster > 1) st_cluster_u32(keys0 + 4 * p, key);
                     else keys[p] = key;
                 }
             }
-            page = next;
+            row = ahead;
+            next = after;
+            word = later;
         }
     } else if (cluster > 1) {
         cluster_wait();
@@ -476,7 +532,7 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
             }
         }
         if (tid == 0) s.lo = 0xFFFFFFFFu, s.hi = 0, s.top = 0;
-        for (int i = tid; i < kSBins; i += kSThreads) s.hist[i] = 0;
+        for (int i = tid; i < kSBins; i += kSThreads) hist[i] = 0;
         __syncthreads();
         lo = __reduce_min_sync(0xFFFFFFFFu, lo);
         hi = __reduce_max_sync(0xFFFFFFFFu, hi);
@@ -501,13 +557,13 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
                 const int shift = max(0, 32 - __clz(most) - 11);
                 for (int p = tid; p < full; p += kSThreads) {
                     const uint32_t x = keys[p];
-                    if (x < kTopKey && x - lo >= base && x - lo - base <= most) atomicAdd(&s.hist[kSBins - 1 - ((x - lo - base) >> shift)], 1);
+                    if (x < kTopKey && x - lo >= base && x - lo - base <= most) atomicAdd(&hist[kSBins - 1 - ((x - lo - base) >> shift)], 1);
                 }
                 __syncthreads();
                 // bins from the top, some a thread
                 int c[kSBinsEach], sum = 0;
 #pragma unroll
-                for (int i = 0; i < kSBinsEach; ++i) sum += c[i] = s.hist[kSBinsEach * tid + i];
+                for (int i = 0; i < kSBinsEach; ++i) sum += c[i] = hist[kSBinsEach * tid + i];
                 int upto = sum;
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
@@ -527,7 +583,7 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
                         s.count = c[i];
                     }
                     before += c[i];
-                    s.hist[kSBinsEach * tid + i] = 0;  // for the next turn
+                    hist[kSBinsEach * tid + i] = 0;  // for the next turn
                 }
                 __syncthreads();
                 base += (uint32_t)s.digit << shift;
@@ -560,7 +616,7 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
         int above = (int)(upto >> 16), same = (int)(upto & 0xFFFFu);
         const bool listed = n <= kSBins;  // then their entries are asked for at once
         auto put = [&](int at, int p) {
-            if (listed) s.hist[at] = p;
+            if (listed) hist[at] = p;
             else out[at] = table[p];
         };
         if (c)
@@ -574,7 +630,7 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
             }
         if (listed) {
             __syncthreads();
-            for (int i = tid; i < n; i += kSThreads) out[i] = table[s.hist[i]];
+            for (int i = tid; i < n; i += kSThreads) out[i] = table[hist[i]];
         }
     }
     // the pages of the tail and of the nodes, then none
@@ -586,24 +642,29 @@ __global__ void __launch_bounds__(kSThreads, MANY ? 4 : 1) select_kernel(const B
     if (h == 0 && tid == 0) a.kept[b] = n * P + (ctx - full * P);
 }
 
-template <int D, bool MANY>
+template <int D>
 cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t stream, int *status) {
+    constexpr int kMost = 224 * 1024;  // dynamic shared memory
+    static_assert(kMaxSelectPages * 4 + 2 * Turn<D>::BLOCK <= kMost && kMost + sizeof(SelectShared) <= 227 * 1024, "two batches fit with the most keys");
     const int most = std::min(v.table_pages, a.max_len / v.page_size);
-    const size_t smem = (size_t)most * 4;
+    int depth = Turn<D>::BATCHES;
+    while (depth > 2 && most * 4 + depth * Turn<D>::BLOCK > kMost) depth /= 2;
+    const size_t smem = (size_t)most * 4 + depth * Turn<D>::BLOCK;
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!__atomic_load_n(&configured[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(select_kernel<D, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectPages * 4);
+        e = cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
         __atomic_store_n(&configured[dev], 1, __ATOMIC_RELEASE);
     }
     // blocks a pair: as many as run at once, with 128 pages each at least where the request is longest
     const long long pairs = (long long)a.B * v.heads;
+    const long long resident = 152LL * std::max<size_t>(1, std::min<size_t>(2, 228 * 1024 / (smem + sizeof(SelectShared) + 1024)));
     int cluster = 1;
-    while (cluster < kMaxSCluster && 2 * cluster * pairs <= (MANY ? 608 : 304) && most > 128 * cluster) cluster *= 2;
+    while (cluster < kMaxSCluster && 2 * cluster * pairs <= resident && most > 128 * cluster) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * cluster), 1, 1);
     cfg.blockDim = dim3(kSThreads, 1, 1);
@@ -625,18 +686,16 @@ cudaError_t select_dim(const BoundsView &v, const SelectArgs &a, cudaStream_t st
     }
     cfg.attrs = attrs;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, select_kernel<D, MANY>, v, a, cluster, status);
+    return cudaLaunchKernelEx(&cfg, select_kernel<D>, v, a, cluster, depth, status);
 }
 
 cudaError_t launch_select(const BoundsView &v, const SelectArgs &a, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
-    // (32 requests of up to 65536 tokens, 8 heads, then the attention: 88 us as few, 84 as many; one of 131072: 28, 33)
-    const bool many = (long long)a.B * v.heads > 152;
     switch (v.dim) {
-        case 64: return many ? select_dim<64, true>(v, a, stream, status) : select_dim<64, false>(v, a, stream, status);
-        case 128: return many ? select_dim<128, true>(v, a, stream, status) : select_dim<128, false>(v, a, stream, status);
-        case 256: return many ? select_dim<256, true>(v, a, stream, status) : select_dim<256, false>(v, a, stream, status);
+        case 64: return select_dim<64>(v, a, stream, status);
+        case 128: return select_dim<128>(v, a, stream, status);
+        case 256: return select_dim<256>(v, a, stream, status);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -145,6 +145,11 @@ def test_selection_of_many_pages(bsf8_lib, n, keep, H):
     Choice(n + H, [n * 16 + 5], 1, 2 * H, H, 64, 16, keep, 1, 2).check(max_len=n * 16 + 6)
 
 
+@pytest.mark.parametrize("D,n,keep", [(128, 45000, 300), (256, 42000, 41000), (128, 40950, 5)])
+def test_selection_of_many_pages_of_larger_heads(bsf8_lib, D, n, keep):
+    Choice(n, [n * 16 + 5, 40], 2, 3, 1, D, 16, keep, 1, 2).check(max_len=n * 16 + 8)
+
+
 def test_selection_for_many_requests(bsf8_lib):
     r = np.random.default_rng(2)
     Choice(5, [int(c) for c in r.integers(0, 5000, size=300)], 1, 8, 4, 128, 16, 20, 1, 1).check()
