@@ -34,9 +34,8 @@ constexpr int kOctaves = 41, kParts = 64;  // the histogram by y: y <= 40 in 64t
 constexpr int kSteps = kOctaves * kParts;
 constexpr int kList = 2048;      // elements that the first block sorts,
 constexpr int kOwn = 704;        // and that a block of a cluster finds
-// Bytes of a slice that are kept: four blocks an SM, whose latencies hide each other, are worth more than slices
-// of twice that (192 rows of 131072 bf16, k = 50: 53 us with two blocks of 512 threads).
-constexpr int kStage = 34 * 1024;
+// Blocks an SM: their latencies hide each other (192 rows of 131072 bf16, k = 50: 30 us, 53 by two of 512 threads).
+constexpr int kTBlocks = 4;
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr int kMaxShared = 228 * 1024;  // an SM's, of which each block takes 1 KB more than it asks for
 constexpr int kEach = kList / kTThreads, kBinsEach = kBins / kTThreads;
@@ -317,7 +316,7 @@ __device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
 }  // namespace
 
 template <typename T, bool PROBS>
-__global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
+__global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const SampleArgs a, int cluster, int staged, float minus_zero) {
     extern __shared__ __align__(16) uint8_t memory[];
     TokenShared &s = *reinterpret_cast<TokenShared *>(memory);
     // one of a few blocks may find as many elements as are sorted: its list lies behind
@@ -1226,6 +1225,27 @@ __global__ void __launch_bounds__(kTThreads, 4) sample_kernel(const SampleArgs a
     if (cluster > 1) cluster_barrier();  // no block leaves while another may read its sums
 }
 
+// Clusters that run at once with so many blocks an SM: fewer than the SMs in all would take, as a cluster stays within
+// one part of them (by an even share of the SMs 16 rows of 131072 bf16 took a block an SM, two turns and 18 us; now 12;
+// 38 rows 19, now 15).  Not for more than that: 48 fp32 rows by four blocks an SM where three do 19 us, 16 by three.
+template <typename T, bool PROBS>
+cudaError_t clusters_at_once(const cudaLaunchConfig_t &cfg, int dev, int cluster, int blocks, int *n) {
+    static int known[64][kMaxTCluster + 1][kTBlocks];  // and one more; 0: not asked yet
+    int *const at = &known[dev][cluster][blocks];
+    int v = __atomic_load_n(at, __ATOMIC_RELAXED);
+    if (v == 0) {
+        if (cluster == 1) {
+            v = 152 * blocks;
+        } else {
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&v, sample_kernel<T, PROBS>, &cfg);
+            if (e != cudaSuccess) return e;
+        }
+        __atomic_store_n(at, ++v, __ATOMIC_RELAXED);
+    }
+    *n = v - 1;
+    return cudaSuccess;
+}
+
 template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     // Blocks a row: eight unless fewer give each at most 4096 elements, or unless that is more than eight blocks an SM
@@ -1238,16 +1258,9 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     constexpr int VEC = 16 / sizeof(T);
     const long long groups = (a.V + (a.ld % VEC ? VEC - 1 : 0) + VEC - 1) / VEC;
     const long long per_warp = ((groups + cluster * kTWarps - 1) / (cluster * kTWarps) + 7) / 8 * 8;
-    const int slice = (int)std::min<long long>(per_warp * kTWarps * 16, kStage + 1);
-    const int staged = slice <= kStage;
+    const long long slice = per_warp * kTWarps * 16;
     const int subs = cluster >= 8 ? 1 : cluster == 4 ? 2 : 4;
-    const size_t need = (sizeof(TokenShared) + 15) / 16 * 16 + (staged ? slice : 0) + (cluster < 8 ? kList * 8 : 0) +
-                        subs * kTThreads * sizeof(float);
-    // No more blocks an SM than an even share of them (the call's first blocks are placed while the kernel before
-    // still holds some of the SMs: four on one and one on the next took twice as long): what the shares leave free
-    // is asked for too.
-    const int share = (int)std::max(1LL, std::min(4LL, ((long long)a.N * cluster + 151) / 152));
-    const size_t smem = std::max(need, (size_t)(kMaxShared / share - 1024 - 512));
+    const size_t fixed = (sizeof(TokenShared) + 15) / 16 * 16 + (cluster < 8 ? kList * 8 : 0) + subs * kTThreads * sizeof(float);
     static int configured[64] = {0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1262,7 +1275,6 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * cluster), 1, 1);
     cfg.blockDim = dim3(kTThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
     int na = 0;
@@ -1280,6 +1292,20 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     }
     cfg.attrs = attrs;
     cfg.numAttrs = na;
+    // No more blocks an SM than the call needs to run at once (the first are placed while the kernel before still holds
+    // some of the SMs: four on one and one on the next took twice as long): all that these leave free is asked for,
+    // and slices are kept that fit in it (one row of 131072 fp32 10.8 -> 9.5 us, by top-p 25 -> 23).
+    auto room = [](int blocks) { return (size_t)(kMaxShared / blocks / 128 * 128 - 1024); };
+    int blocks = 1;
+    for (; blocks < kTBlocks; ++blocks) {
+        int n = 0;
+        cfg.dynamicSmemBytes = room(blocks);
+        e = clusters_at_once<T, PROBS>(cfg, dev, cluster, blocks, &n);
+        if (e != cudaSuccess) return e;
+        if (n >= a.N) break;
+    }
+    cfg.dynamicSmemBytes = room(blocks);
+    const int staged = slice <= (long long)(room(blocks) - fixed);
     return cudaLaunchKernelEx(&cfg, sample_kernel<T, PROBS>, a, cluster, staged, -0.0f);
 }
 
