@@ -291,7 +291,7 @@ inline int check_bounds(const bsf8_page_bounds *v) {
     if (v->pages < 1 || v->heads < 1 || v->page_size < 16 || v->page_size > 1024 || v->page_size % 16 != 0 ||
         (v->dim != 64 && v->dim != 128 && v->dim != 256) || (long long)v->pages * v->heads >= (1LL << 31))
         return BSF8_ERR_SHAPE;
-    if (!aligned16(v->codes) || (reinterpret_cast<uintptr_t>(v->exps) & 7u) != 0) return BSF8_ERR_ALIGN;
+    if (!aligned16(v->codes) || (reinterpret_cast<uintptr_t>(v->exps) & (uintptr_t)(v->dim / 32 - 1)) != 0) return BSF8_ERR_ALIGN;
     return BSF8_OK;
 }
 

@@ -1,9 +1,10 @@
 """Binding of the decode operators (include/bsf8.h, "decode operators"): the paged block-scaled
-fp8 cache of keys and values, attention of a drafted token tree over it, and the verification
-of the drafts.  Like the rest of the binding it only checks and marshals arguments -- here through
-the extension _bsf8_torch (csrc/bsf8_torch.cpp), as a decode step's operators take the GPU less
-time than a ctypes call of this many arguments takes the host; every computation runs in the
-library's kernels on the current stream of the tensors' device.
+fp8 cache of keys and values, attention of a drafted token tree over it (or over the pages that a
+score selects), the verification of the drafts, and what a step needs around them: plans of pages
+and slots, sampling, the residual and its norms.  Like the rest of the binding it only checks and
+marshals arguments -- here through the extension _bsf8_torch (csrc/bsf8_torch.cpp), as a decode
+step's operators take the GPU less time than a ctypes call of this many arguments takes the host;
+every computation runs in the library's kernels on the current stream of the tensors' device.
 
 One step of speculative decoding, per layer and then once:
 

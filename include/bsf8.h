@@ -478,7 +478,7 @@ int bsf8_kv_plan(int32_t *table, int table_pages, int page_size, int32_t *held, 
  * the smallest e >= -127 with 127 * 2^e >= every |hi|, |lo| of the 32, codes ceil(hi / 2^e) and
  * floor(lo / 2^e).  Byte 255 and codes 0 where a key's 32 channels are marked NaN (byte 255) or infinite.
  *   codes  device, int8 [pages][heads][2][dim] (hi, lo), 16-byte aligned
- *   exps   device, uint8 [pages][heads][dim / 32], 8-byte aligned
+ *   exps   device, uint8 [pages][heads][dim / 32], on dim / 32 bytes
  * The sizes are the cache's. */
 typedef struct {
     int8_t *codes;

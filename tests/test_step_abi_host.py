@@ -38,7 +38,7 @@ def bounds(**kw):
 
 BAD_BOUNDS = [(dict(codes=0), NULL), (dict(exps=0), NULL), (dict(pages=0), SHAPE), (dict(page_size=8), SHAPE),
               (dict(page_size=40), SHAPE), (dict(page_size=2048), SHAPE), (dict(heads=0), SHAPE), (dict(dim=96), SHAPE),
-              (dict(codes=A + 8), ALIGN), (dict(exps=A + 4), ALIGN), (dict(pages=1 << 30, heads=2), SHAPE)]
+              (dict(codes=A + 8), ALIGN), (dict(exps=A + 2), ALIGN), (dict(exps=A + 4, dim=256), ALIGN), (dict(pages=1 << 30, heads=2), SHAPE)]
 
 
 def test_plan_refusals(lib):
