@@ -65,6 +65,8 @@ __device__ __forceinline__ int sum_pages(int v, int *wsum, int &total) {
 // ------------------------------------------------------------------------------------ bounds
 // A warp takes a page of a head: D / 16 lanes a key, 16 channels a lane (one 16-byte load), the keys'
 // values rebuilt to bf16 -- exactly, they have four bits -- and their maxima and minima kept in pairs.
+// Three requests of 21843 tokens in all, 8 heads, 36 MB: 11.2 us, 3.2 TB/s, by the ALU pipe (54 %) and 2 us of prefix sums
+// before the first load; a request's single token that fills a page 2.3.
 template <int D>
 __global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, const BoundsView v, const int32_t *start,
                                                            const int32_t *end, int B, int *status) {
