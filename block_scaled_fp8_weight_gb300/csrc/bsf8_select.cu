@@ -20,6 +20,8 @@ namespace {
 
 constexpr int kBThreads = 256;
 constexpr int kBMax = 1024;  // requests
+constexpr int kBBlocks = 4;  // an SM
+constexpr int kBAhead = 4;   // a lane's keys on their way (8 and 16 need registers that a fourth block has more of)
 
 __device__ __forceinline__ uint32_t bmax2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -63,12 +65,14 @@ __device__ __forceinline__ int sum_pages(int v, int *wsum, int &total) {
 }  // namespace
 
 // ------------------------------------------------------------------------------------ bounds
-// A warp takes a page of a head: D / 16 lanes a key, 16 channels a lane (one 16-byte load), the keys'
-// values rebuilt to bf16 -- exactly, they have four bits -- and their maxima and minima kept in pairs.
-// Three requests of 21843 tokens in all, 8 heads, 36 MB: 11.2 us, 3.2 TB/s, by the ALU pipe (54 %) and 2 us of prefix sums
-// before the first load; a request's single token that fills a page 2.3.
+// D / 16 lanes a key, 16 channels a lane (one 16-byte load), the keys' values rebuilt to bf16 -- exactly, they have four
+// bits -- and their maxima and minima kept in pairs.  A warp's groups of lanes share the keys of one page where pages are
+// few, and take a page each where all warps have enough of them and pages are short: then nothing goes from lane to lane.
+// Bound by the ALU pipe: 13 instructions rebuild and compare four codes.  Three requests of 21843 tokens in all, 8 heads, dim
+// 128, 36 MB: 11.1 us, 3.3 TB/s, 2 us of them prefix sums before the first load; 64 requests of 5000 tokens in pages of 16:
+// 51 us, 3.7 TB/s (95 by a warp a page), of 4000 at dim 64 22 (67); 16 of 60000 in pages of 128: 90, 5.7 TB/s.
 template <int D>
-__global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, const BoundsView v, const int32_t *start,
+__global__ void __launch_bounds__(kBThreads, kBBlocks) bounds_kernel(const CacheView c, const BoundsView v, const int32_t *start,
                                                            const int32_t *end, int B, int *status) {
     __shared__ int s_first[kBMax], s_sum[kBMax + 1], s_w[kBThreads / 32];
     pdl_trigger();
@@ -105,55 +109,77 @@ __global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, co
     }
     __syncthreads();
     constexpr int LPR = D / 16, RP = 32 / LPR, EB = D / 32;  // lanes a key, keys a pass
-    const int r = lane / LPR, u = lane % LPR;
     const int items = s_sum[B];
     const long long warps = (long long)gridDim.x * (kBThreads / 32), all = (long long)items * c.heads;
-    for (long long it = (long long)blockIdx.x * (kBThreads / 32) + (tid >> 5); it < all; it += warps) {
-        const int pi = (int)(it / c.heads), h = (int)(it - (long long)pi * c.heads);
-        int lo = 0, hi = B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_sum[mid] <= pi) lo = mid;
-            else hi = mid;
+    int split = RP;  // groups of lanes that share a page's keys
+    while (split > 1 && c.page_size < 16 * split && all * (split / 2) >= warps * RP) split /= 2;
+    const int u = lane % LPR, part = lane / LPR % split, together = RP / split;
+    for (long long it0 = ((long long)blockIdx.x * (kBThreads / 32) + (tid >> 5)) * together; it0 < all; it0 += warps * together) {
+        const long long it = it0 + lane / LPR / split;
+        const int pi = all < (1LL << 31) ? (int)it / c.heads : (int)(it / c.heads), h = (int)(it - (long long)pi * c.heads);
+        int page = -1;
+        if (it < all) {
+            int lo = 0, hi = B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_sum[mid] <= pi) lo = mid;
+                else hi = mid;
+            }
+            page = v.table[(size_t)lo * v.table_pages + s_first[lo] + (pi - s_sum[lo])];
+            if ((unsigned)page >= (unsigned)c.pages) {
+                if (u == 0 && part == 0) report_index(status);
+                page = -1;
+            }
         }
-        const int page = v.table[(size_t)lo * v.table_pages + s_first[lo] + (pi - s_sum[lo])];
-        if ((unsigned)page >= (unsigned)c.pages) {
-            if (lane == 0) report_index(status);
-            continue;
-        }
-        const size_t row0 = ((size_t)page * c.heads + h) * c.page_size;
-        const uint8_t *const codes = c.k8 + (row0 + r) * D + 16 * u;
-        const uint8_t *const exps = c.kexp + (row0 + r) * EB + u / 2;
+        const size_t row0 = ((size_t)max(page, 0) * c.heads + h) * c.page_size;
+        const uint8_t *const codes = c.k8 + row0 * D + 16 * u;
+        const uint8_t *const exps = c.kexp + row0 * EB + u / 2;
         uint32_t mx[8], mn[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) mx[i] = 0xFF80FF80u, mn[i] = 0x7F807F80u;  // -inf, +inf
-        bool nan = false;
-#pragma unroll 4
-        for (int k = 0; k < c.page_size; k += RP) {  // page_size is a multiple of 16, RP of it
-            const uint4 w = *reinterpret_cast<const uint4 *>(codes + (size_t)k * D);
-            const uint32_t e = exps[(size_t)k * EB];
-            nan |= e == 255;
-            const Scale sc = make_scale(e);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        uint32_t nan = 0;
+        // keys k, k + split, ..: their loads together on their way
+        auto keys = [&](int k, auto count) {
+            constexpr int K = decltype(count)::value;
+            uint4 w[K];
+            uint32_t e[K];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a, b;
-                rebuild4(ws[i], sc, a, b);
-                mx[2 * i] = bmax2(mx[2 * i], a);
-                mn[2 * i] = bmin2(mn[2 * i], a);
-                mx[2 * i + 1] = bmax2(mx[2 * i + 1], b);
-                mn[2 * i + 1] = bmin2(mn[2 * i + 1], b);
+            for (int j = 0; j < K; ++j) {
+                w[j] = *reinterpret_cast<const uint4 *>(codes + (size_t)(k + j * split) * D);
+                e[j] = exps[(size_t)(k + j * split) * EB];
             }
-        }
 #pragma unroll
-        for (int m = LPR; m < 32; m <<= 1) {
+            for (int j = 0; j < K; ++j) {
+                nan |= e[j] == 255 ? 1u : 0u;
+                const Scale sc = make_scale(e[j]);
+                const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t a, b;
+                    rebuild4(ws[i], sc, a, b);
+                    mx[2 * i] = bmax2(mx[2 * i], a);
+                    mn[2 * i] = bmin2(mn[2 * i], a);
+                    mx[2 * i + 1] = bmax2(mx[2 * i + 1], b);
+                    mn[2 * i + 1] = bmin2(mn[2 * i + 1], b);
+                }
+            }
+        };
+        if (page >= 0) {
+            int k = part, left = c.page_size / split;  // even: a page is a multiple of 16 keys, split at most 8
+            for (; left >= kBAhead; left -= kBAhead, k += kBAhead * split) keys(k, std::integral_constant<int, kBAhead>());
+            if (left & 2) keys(k, std::integral_constant<int, 2>());
+        }
+        __syncwarp();
+        for (int m = LPR; m < LPR * split; m <<= 1) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 mx[i] = bmax2(mx[i], __shfl_xor_sync(0xFFFFFFFFu, mx[i], m));
                 mn[i] = bmin2(mn[i], __shfl_xor_sync(0xFFFFFFFFu, mn[i], m));
             }
+            nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, m);
         }
-        // the largest magnitude of the block's 32 channels: this lane's and its neighbour's
+        // the largest magnitude of the block's 32 channels, and whether any of its keys is marked NaN: this lane's and
+        // its neighbour's
         uint32_t am = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -161,34 +187,33 @@ __global__ void __launch_bounds__(kBThreads) bounds_kernel(const CacheView c, co
             am = max(am, max((mn[i] << 16) & 0x7FFFFFFFu, mn[i] & 0x7FFF0000u));
         }
         am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-        // any of the block's keys marked NaN: lanes of the same block
-        uint32_t marked = __ballot_sync(0xFFFFFFFFu, nan);
-        uint32_t mine = 0;
-#pragma unroll
-        for (int k = 0; k < RP; ++k) mine |= marked >> (k * LPR + (u & ~1)) & 3u;
+        nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, 1);
+        if (page < 0) continue;
         // 127 = 1.984375 * 2^6: adding 0x1FFFF carries into the exponent past that mantissa
         uint32_t e = (uint32_t)max(0, (int)((am + 0x1FFFFu) >> 23) - 6);
-        const bool none = mine != 0 || am >= 0x7F800000u;
+        const bool none = nan != 0 || am >= 0x7F800000u;
         if (none) e = 255;
-        if (r < 2) {  // the first key's lanes write the maxima, the second's the minima
-            const float inv = none ? 0.0f : __uint_as_float((254u - e) << 23);  // 2^(127 - e)
+        const float inv = none ? 0.0f : __uint_as_float((254u - e) << 23);  // 2^(127 - e)
+        const size_t at = (size_t)page * v.heads + h;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {  // maxima, minima: by the page's first two groups of lanes, or its one
+            if (split > 1 && part != which) continue;
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 o[i] = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t w = r == 0 ? mx[2 * i + j / 2] : mn[2 * i + j / 2];
+                    const uint32_t w = which == 0 ? mx[2 * i + j / 2] : mn[2 * i + j / 2];
                     const float x = j & 1 ? hi16(w) : lo16(w);
                     float y = x * inv;
                     if (y == 0.0f) y = x;  // too small a part for fp32: as far from 0 as its sign says
-                    const int q = none ? 0 : (int)(r == 0 ? ceilf(y) : floorf(y));
+                    const int q = none ? 0 : (int)(which == 0 ? ceilf(y) : floorf(y));
                     o[i] |= (uint32_t)(q & 255) << (8 * j);
                 }
             }
-            const size_t at = (size_t)page * v.heads + h;
-            *reinterpret_cast<uint4 *>(v.codes + (at * 2 + r) * D + 16 * u) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (r == 0 && (u & 1) == 0) v.exps[at * EB + u / 2] = (uint8_t)e;
+            *reinterpret_cast<uint4 *>(v.codes + (at * 2 + which) * D + 16 * u) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (which == 0 && (u & 1) == 0) v.exps[at * EB + u / 2] = (uint8_t)e;
         }
     }
 }
@@ -199,7 +224,7 @@ cudaError_t launch_bounds(const CacheView &c, const BoundsView &v, const int32_t
     if (!status) return cudaErrorInvalidSymbol;
     cudaLaunchConfig_t cfg = {};
     const long long most = (long long)B * v.table_pages * v.heads;
-    cfg.gridDim = dim3((unsigned)std::min<long long>((most + 7) / 8, 152 * 4), 1, 1);
+    cfg.gridDim = dim3((unsigned)std::min<long long>((most + 7) / 8, 152 * kBBlocks), 1, 1);
     cfg.blockDim = dim3(kBThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

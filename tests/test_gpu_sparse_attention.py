@@ -62,6 +62,28 @@ def test_bounds(bsf8_lib, D, H, page, B, most):
     assert bsf8.device_status() == 0
 
 
+@pytest.mark.parametrize("D,H,page,B,most", [(64, 10, 16, 100, 40), (64, 5, 48, 60, 70), (128, 8, 16, 64, 40), (256, 8, 16, 33, 41),
+                                             (64, 3, 16, 100, 41)])
+def test_bounds_of_many_short_pages(bsf8_lib, D, H, page, B, most):
+    """More pages than warps: some to a warp at once, the last ones fewer, bad entries and marked blocks among them."""
+    r = np.random.default_rng(D + B + page)
+    pages = B * most + 1
+    data = random_cache(r, pages, H, page, D, 110, 130)
+    data[1][r.integers(0, pages, 50), r.integers(0, H, 50), r.integers(0, page, 50), r.integers(0, D // 32, 50)] = 255
+    table = r.permutation(pages)[:B * most].reshape(B, most)
+    given = table.copy()
+    wrong = r.integers(0, B * most, 40)
+    given.reshape(-1)[wrong] = np.where(wrong % 2, -1 - wrong, pages + wrong)
+    cache = bsf8.KVCache(*(torch.from_numpy(t).cuda() for t in data))
+    b = fresh_bounds(r, pages, H, page, D)
+    want, byte = b.codes.cpu().numpy().copy(), b.exps.cpu().numpy().copy()
+    touched = np.delete(table.reshape(-1), wrong)
+    want[touched], byte[touched] = ref.bounds(data[0][touched], data[1][touched])
+    bsf8.kv_bounds(cache, b, i32(given), i32([most * page] * B))
+    assert np.array_equal(b.exps.cpu().numpy(), byte) and np.array_equal(b.codes.cpu().numpy(), want)
+    assert bsf8.device_status() == INDEX
+
+
 def test_bounds_bound_the_keys(bsf8_lib):
     """q . k of every key is below the page's sum."""
     r = np.random.default_rng(3)
