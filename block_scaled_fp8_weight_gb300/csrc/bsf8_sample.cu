@@ -21,6 +21,7 @@
 #include "bsf8_internal.h"
 
 #include <algorithm>
+#include <cfloat>
 
 namespace bsf8 {
 
@@ -552,15 +553,20 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     const bool few = V <= kList && (k < V || nucleus);
     constexpr int kMax8 = kTThreads / 8;
     const int g8 = kMax8 * cluster, gt = kTThreads * cluster * subs;  // maxima of eight threads, of (a part of) one
-    // with k of gt maxima to reach, some -gt ln(1 - k / gt) elements do
-    const int most_k = (int)((float)gt * fminf(0.95f, 1.0f - expf(-1800.0f / (float)gt)));
+    // with k of so many maxima to reach, some -real ln(1 - k / real) elements do; where that is far above k and the block has
+    // the whole row, all elements take the maxima's place (18 rows of 4435, k = 1000 and top-p: 46 us by the digits below, 19)
+    const int real = min(gt, groups);
+    const bool one = cluster == 1 && 2 * k > real;
+    const int most_k = one ? kList - 96 : (int)((float)real * fminf(0.95f, 1.0f - expf(-1800.0f / (float)real)));
     if (top < INFINITY && (few || (k < V && k <= most_k))) {
         float least_value = -INFINITY;
         if (!few) {
             // (a little below) the k-th largest of the maxima
             uint32_t v[kMaxTCluster];
             const int nv = 2 * k <= g8 ? 1 : cluster * subs;  // at most eight
-            if (nv == 1) {
+            if (one) {
+                v[0] = 0;
+            } else if (nv == 1) {
                 v[0] = tid < g8 ? order_of(__uint_as_float(of32(&s.max8[tid % kMax8], tid / kMax8))) : 0u;
             } else {
 #pragma unroll
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             }
             // a histogram between the least and the largest of them, finer again where those are far apart; what
             // lies above the bins counts in the first one
-            uint32_t from = order_of(low), range = order_of(top) - from;
+            uint32_t from = order_of(one ? -FLT_MAX : low), range = order_of(top) - from;
             for (int turn = 0; turn < 3 && (turn == 0 || range >= 65536); ++turn) {
                 const int shift = max(0, 32 - __clz(range) - 11);
                 if (turn > 0) {
@@ -580,8 +586,15 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 auto add = [&](uint32_t x) {
                     if (x >= from) atomicAdd(&s.tally[kList - 1 - min((x - from) >> shift, (uint32_t)(kList - 1))], 1);
                 };
-                add(v[0]);
-                if (nv > 1) {
+                if (one) {
+                    each([&](const float (&y)[VEC], int) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) add(order_of(y[i]));
+                    });
+                } else {
+                    add(v[0]);
+                }
+                if (!one && nv > 1) {
 #pragma unroll
                     for (int c = 1; c < kMaxTCluster; ++c)
                         if (c < nv) add(v[c]);
@@ -599,7 +612,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                     before += n[i];
                 }
                 __syncthreads();
-                if (s.bin < 0) {  // fewer than k threads have any
+                if (s.bin < 0) {  // fewer than k threads (or elements) have any
                     from = 0;
                     break;
                 }
@@ -1248,11 +1261,11 @@ cudaError_t clusters_at_once(const cudaLaunchConfig_t &cfg, int dev, int cluster
 
 template <typename T, bool PROBS>
 cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
-    // Blocks a row: eight unless fewer give each at most 4096 elements, or unless that is more than eight blocks an SM
-    // in all, two turns of four (192 rows of 131072 that ask for different things: 62 us by eight blocks, 61 by four,
-    // 71 by two; for top-k alone 37, 30, 25; 48 rows 41, 58, 89).
+    // Blocks a row: eight unless fewer give each at most 4096 elements (one alone 8192: 190 rows of that 7.9 us, by two 8.7), or
+    // unless that is more than eight blocks an SM in all, two turns of four (192 rows of 131072 that ask for different
+    // things: 62 us by eight blocks, 61 by four, 71 by two; for top-k alone 37, 30, 25; 48 rows 41, 58, 89).
     int cluster = 1;
-    while (cluster < kMaxTCluster && a.V > 4096 * cluster) cluster *= 2;
+    while (cluster < kMaxTCluster && a.V > (cluster == 1 ? 8192 : 4096 * cluster)) cluster *= 2;
     while (cluster > 2 && (long long)a.N * cluster > 1216) cluster /= 2;
     // a block's slice, as the kernel cuts it (rows that do not start on 16 bytes may take a group more)
     constexpr int VEC = 16 / sizeof(T);

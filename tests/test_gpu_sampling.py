@@ -58,6 +58,25 @@ def test_sampling(bsf8_lib, N, V, ld, bf16, how):
     check(x[:, :V], u, **{a: [v] * N for a, v in HOW[how].items()})
 
 
+@pytest.mark.parametrize("V", [2049, 2113, 4435, 8192, 8193, 9000])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_of_a_short_row(bsf8_lib, V, bf16):
+    """k about the maxima that a row has, the elements that are sorted, and the row's finite elements."""
+    r = np.random.default_rng(V)
+    ks = [60, 250, 257, 500, 530, 700, 840, 900, 1100, 1300, 1800, 1952, 1953, 2047, 2048]
+    N = len(ks)
+    x = torch.from_numpy((r.standard_normal((N, V)) * 2.5).astype(np.float32)).cuda()
+    x[3, 400:] = float("-inf")  # 500 of 400
+    x[7] = x[7].mul(2).round()  # few values
+    x[9] *= 1e-30
+    x[11, 5] = 1e30
+    if bf16:
+        x = x.to(torch.bfloat16)
+    u = r.random(N).astype(np.float32)
+    check(x, u, k=ks)
+    check(x, u, k=ks, tp=[0.9] * N, mp=[1e-4] * N)
+
+
 def test_rows_ask_for_different_things(bsf8_lib):
     r = np.random.default_rng(1)
     N, V = 64, 3001
