@@ -249,6 +249,7 @@ cudaError_t launch_bounds(const CacheView &c, const BoundsView &v, const int32_t
 // two chains of products need (three at 80 spilled: 32 requests 21.7 us for 16).  32 requests of up to 65536 tokens, 8
 // heads: 16 us with the bounds (34 MB) in L2, 23 without, of which DRAM is 5; one of 131072: 10, the chain of loads (lengths,
 // table, bounds), the queries' four barriers, a turn of products (1.5), the cluster's barrier, the digits (2) and the list (1.5).
+// Rows of queries cost each block of the cluster the same: 512 of them at dim 128 9 us (16 by conversions and a division a row).
 namespace {
 
 constexpr int kSThreads = 256, kSWarps = kSThreads / 32;
@@ -376,8 +377,9 @@ __global__ void __launch_bounds__(kSThreads, 2) select_kernel(const BoundsView v
         // ---------------------------------------------------------- the rows' queries
         constexpr int LPQ = D / 8;  // 16-byte pieces a row
         const int rows = nodes * g, u = tid % LPQ;
+        const float inv_g = 1.0f / (float)g;
         auto piece = [&](int r) {
-            const int t = r / g;
+            const int t = (int)(((float)r + 0.5f) * inv_g);  // r / g: both below 2^13
             return *reinterpret_cast<const uint4 *>(a.q + ((size_t)b * a.T + t) * a.ldq + (size_t)(h * g + r - t * g) * D + 8 * u);
         };
         for (int i = tid; i < 2 * D; i += kSThreads) s.q[i / D][i % D] = 0;
@@ -406,36 +408,59 @@ __global__ void __launch_bounds__(kSThreads, 2) select_kernel(const BoundsView v
                     if (r + j * RPP < rows) f(w[j]);
             }
         };
-        uint32_t am = 0;
+        auto block_max = [&](uint32_t v) {
+            v = __reduce_max_sync(0xFFFFFFFFu, v);
+            if (lane == 0) s.red[warp] = (int)v;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kSWarps; ++w) v = max(v, (uint32_t)s.red[w]);
+            return v;
+        };
+        uint32_t am = 0;  // two magnitudes at a time
         each([&](const uint4 &w) {
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t lo = x[i] & 0x7FFFu, hi = (x[i] >> 16) & 0x7FFFu;
-                am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-            }
+            am = __vmaxu2(__vmaxu2(am, w.x & 0x7FFF7FFFu), w.y & 0x7FFF7FFFu);
+            am = __vmaxu2(__vmaxu2(am, w.z & 0x7FFF7FFFu), w.w & 0x7FFF7FFFu);
         });
-        am = __reduce_max_sync(0xFFFFFFFFu, am);
-        if (lane == 0) s.red[warp] = (int)am;
-        __syncthreads();
-        am = 0;
+        am = block_max(max(am & 0xFFFFu, am >> 16));
+        const bool finite = am < 0x7F80u;
+        if (!finite) {  // again without what is infinite or NaN
+            am = 0;
+            each([&](const uint4 &w) {
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int w = 0; w < kSWarps; ++w) am = max(am, (uint32_t)s.red[w]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = x[i] & 0x7FFFu, hi = (x[i] >> 16) & 0x7FFFu;
+                    am = max(am, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                }
+            });
+            __syncthreads();
+            am = block_max(am);
+        }
         // the largest to [2^17, 2^18); it counts as 2^-100 at least
         const int k = max((int)(am >> 7) - 127, -100);
         const float scale = __uint_as_float((uint32_t)(127 + 17 - k) << 23);
-        int up[8] = {}, dn[8] = {};
+        // The integers by adding 1.5 * 2^23, which rounds as rint does and leaves them in the low bits; what that adds to
+        // the sums (modulo 2^32) goes off at the end.  up: of the positive ones, dn: of all, then of the rest.
+        constexpr float kRound = 12582912.0f;
+        const uint32_t zero = __float_as_uint(kRound);
+        uint32_t up[8] = {}, dn[8] = {}, count = 0;
         each([&](const uint4 &w) {
             const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            ++count;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t bits = i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16;
-                const bool finite = (bits & 0x7F800000u) != 0x7F800000u;
-                const int z = finite ? __float2int_rn(__uint_as_float(bits) * scale) : 0;
-                up[i] += max(z, 0);
-                dn[i] += min(z, 0);
+                uint32_t bits = i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16;
+                if (!finite && (bits & 0x7F800000u) == 0x7F800000u) bits = 0;
+                const uint32_t z = __float_as_uint(__fmaf_rn(__uint_as_float(bits), scale, kRound));
+                up[i] += max(z, zero);
+                dn[i] += z;
             }
         });
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            up[i] -= count * zero;
+            dn[i] -= count * zero + up[i];
+        }
 #pragma unroll
         for (int m = LPQ; m < 32; m <<= 1) {
 #pragma unroll
@@ -447,8 +472,8 @@ __global__ void __launch_bounds__(kSThreads, 2) select_kernel(const BoundsView v
         if (lane < LPQ && warp * 32 / LPQ < rows) {  // warps that had rows
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (up[i]) atomicAdd(&s.q[0][8 * u + i], up[i]);
-                if (dn[i]) atomicAdd(&s.q[1][8 * u + i], dn[i]);
+                if (up[i]) atomicAdd(&s.q[0][8 * u + i], (int)up[i]);
+                if (dn[i]) atomicAdd(&s.q[1][8 * u + i], (int)dn[i]);
             }
         }
         __syncthreads();
