@@ -314,6 +314,93 @@ __device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
     __syncthreads();
 }
 
+// Of s.sort[0 .. n) in order, all different, the element in which the weights, from `run` on, reach `cut`: its key and the
+// sum up to it in s.cut_key and s.total, which stay if there is none.  By bins over the distances in question, or
+// over the indices of those at one distance, whose weights are added up; the few of the last bin are compared.  Loses s.sort.
+__device__ __noinline__ void find_cut(TokenShared &s, int n, float rate, u64 run, u64 cut, int V) {
+    constexpr int kFew = 32;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    // how many a bin has, and their weights by 20 bits (2048 of at most 2^40): atomics of 64 bits try again and again
+    uint32_t *const counts = reinterpret_cast<uint32_t *>(s.sort), *const low = counts + kBins, *const high = low + kBins;
+    u64 *const few = s.sort + 3 * kBins / 2;
+    u64 v[kEach];
+    uint32_t in = 0;  // elements in question
+#pragma unroll
+    for (int r = 0; r < kEach; ++r) {
+        const int at = tid + r * kTThreads;
+        v[r] = at < n ? s.sort[at] : 0;
+        in |= at < n ? 1u << r : 0u;
+    }
+    auto weight_of = [&](u64 key) { return weight(__uint_as_float((uint32_t)(key >> 20)), rate); };
+    int count = n, index0 = 0, bits = 32 - __clz(V - 1);  // the indices in question, 2^bits of them
+    while (count > kFew) {
+        uint32_t lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+        for (int r = 0; r < kEach; ++r) {
+            if (!(in >> r & 1)) continue;
+            lo = min(lo, (uint32_t)(v[r] >> 20));
+            hi = max(hi, (uint32_t)(v[r] >> 20));
+        }
+        lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+        hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+        if ((tid & 31) == 0) s.tcount[warp] = (int)lo, s.wcount[warp] = (int)hi;
+        __syncthreads();
+        for (int i = tid; i < 3 * kBins; i += kTThreads) counts[i] = 0;
+        if (tid == 0) s.bin = -1;
+#pragma unroll
+        for (int i = 0; i < kTWarps; ++i) lo = min(lo, (uint32_t)s.tcount[i]), hi = max(hi, (uint32_t)s.wcount[i]);
+        const bool by_index = lo == hi;
+        const int shift = max(0, (by_index ? bits : 32 - __clz(hi - lo)) - 10);
+        auto bin_of = [&](u64 key) {
+            return (by_index ? (uint32_t)(key & 0xFFFFFu) - (uint32_t)index0 : (uint32_t)(key >> 20) - lo) >> shift;
+        };
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kEach; ++r) {
+            if (!(in >> r & 1)) continue;
+            const uint32_t bin = bin_of(v[r]);
+            const u64 w = weight_of(v[r]);
+            atomicAdd(&counts[bin], 1u);
+            atomicAdd(&low[bin], (uint32_t)w & 0xFFFFFu);
+            atomicAdd(&high[bin], (uint32_t)(w >> 20));
+        }
+        __syncthreads();
+        u64 m[kBinsEach], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < kBinsEach; ++i) sum += m[i] = ((u64)high[kBinsEach * tid + i] << 20) + low[kBinsEach * tid + i];
+        u64 before = run + sum_before(sum, s, all);
+#pragma unroll
+        for (int i = 0; i < kBinsEach; ++i) {
+            if (before < cut && before + m[i] >= cut) s.bin = kBinsEach * tid + i, s.mass = before;
+            before += m[i];
+        }
+        __syncthreads();
+        const int bin = s.bin;
+        if (bin < 0) return;
+        run = s.mass;
+        count = (int)counts[bin];  // (one index has one element)
+#pragma unroll
+        for (int r = 0; r < kEach; ++r)
+            if ((in >> r & 1) && bin_of(v[r]) != (uint32_t)bin) in &= ~(1u << r);
+        if (by_index) index0 += bin << shift, bits = shift;
+    }
+    if (tid == 0) s.cut = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kEach; ++r) {
+        if (!(in >> r & 1)) continue;
+        const int at = 2 * atomicAdd(&s.cut, 1);
+        few[at] = v[r], few[at + 1] = weight_of(v[r]);
+    }
+    __syncthreads();
+    if (tid < count) {
+        const u64 me = few[2 * tid], mine = few[2 * tid + 1];
+        for (int j = 0; j < count; ++j)
+            if (few[2 * j] < me) run += few[2 * j + 1];
+        if (run < cut && run + mine >= cut) s.cut_key = me, s.total = run + mine;
+    }
+}
+
 }  // namespace
 
 template <typename T, bool PROBS>
@@ -672,18 +759,23 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                         if (w[i]) out[(int)(key[i] & 0xFFFFFu)] = share(w[i]);
                 } else {
                     // the draw goes by index: sums over 2048 equal parts of the row, then inside one of them
+                    uint32_t *const low = reinterpret_cast<uint32_t *>(s.sort), *const high = low + kList;  // by 20 bits
                     for (int i = tid; i < kList; i += kTThreads) s.sort[i] = 0;
                     if (tid == 0) s.listed = 0;
                     __syncthreads();
                     const int shift = max(0, 32 - __clz(V - 1) - 11);
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i)
-                        if (w[i]) atomicAdd(&s.sort[(uint32_t)(key[i] & 0xFFFFFu) >> shift], w[i]);
+                    for (int i = 0; i < kEach; ++i) {
+                        if (w[i] == 0) continue;
+                        const uint32_t at = (uint32_t)(key[i] & 0xFFFFFu) >> shift;
+                        atomicAdd(&low[at], (uint32_t)w[i] & 0xFFFFFu);
+                        atomicAdd(&high[at], (uint32_t)(w[i] >> 20));
+                    }
                     __syncthreads();
                     u64 part[kEach];
                     sum = 0;
 #pragma unroll
-                    for (int i = 0; i < kEach; ++i) sum += part[i] = s.sort[kEach * tid + i];
+                    for (int i = 0; i < kEach; ++i) sum += part[i] = ((u64)high[kEach * tid + i] << 20) + low[kEach * tid + i];
                     before = sum_before(sum, s, all);
                     inv = 1.0f / (float)all;
                     const u64 at = draw_at(all);
@@ -881,23 +973,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 const u64 cut = max((u64)1, part_of(pfix, __shfl_sync(0xFFFFFFFFu, all, 0)));
                 if (tid == 0) s.total = 0;
                 __syncthreads();
-                sort_list(s, reinterpret_cast<int *>(list), n);
-                u64 w[kEach], here = 0;
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    const int at = kEach * tid + i;
-                    w[i] = at < n ? weight(__uint_as_float((uint32_t)(s.sort[at] >> 20)), rate) : 0;
-                    here += w[i];
-                }
-                u64 run = below + sum_before(here, s, all);
-#pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    if (run < cut && run + w[i] >= cut) {
-                        s.cut_key = s.sort[kEach * tid + i];
-                        s.total = run + w[i];
-                    }
-                    run += w[i];
-                }
+                find_cut(s, n, rate, below, cut, V);
             }
             barrier();
             const u64 kept_all = of64(&s.total, 0);
@@ -909,16 +985,21 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             }
         }
         if (!found) {
-            barrier();  // the sorted list is read
+            barrier();  // the lists are read
         } else if (!PROBS) {
-            // this block's share of them, into the sums of the warps whose part they lie in (the first block has
-            // all of them sorted, and its own list no longer)
-            const u64 *const from_list = rank == 0 ? s.sort : list;
-            for (int i = tid; i < (rank == 0 ? n : s.listed); i += kTThreads) {
-                const u64 key = from_list[i];
+            // this block's share of them, into the sums of the warps whose part they lie in (by 20 bits)
+            if (tid < kTWarps) s.tcount[tid] = s.wcount[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < s.listed; i += kTThreads) {
+                const u64 key = list[i];
                 const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
-                if (key <= cut_key && part < kTWarps) atomicAdd(&s.wsum[part], weight(__uint_as_float((uint32_t)(key >> 20)), rate));
+                if (key > cut_key || part >= kTWarps) continue;
+                const u64 w = weight(__uint_as_float((uint32_t)(key >> 20)), rate);
+                atomicAdd(&s.tcount[part], (int)((uint32_t)w & 0xFFFFFu));
+                atomicAdd(&s.wcount[part], (int)(w >> 20));
             }
+            __syncthreads();
+            if (tid < kTWarps) s.wsum[tid] += ((u64)(uint32_t)s.wcount[tid] << 20) + (uint32_t)s.tcount[tid];
             __syncthreads();
         }
     }
