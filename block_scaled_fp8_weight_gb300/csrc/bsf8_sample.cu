@@ -12,8 +12,8 @@
 //   - top-k: the k-th largest of the threads' own largest logits is at most the k-th largest of all, so that
 //     little more than k elements reach it; the first block sorts those, and all that follows (min-p,
 //     top-p, the draw) is done on them;
-//   - top-p alone: a histogram of y tells about where the weights reach the share; the elements there are
-//     sorted, those before them added up;
+//   - top-p alone: a histogram of y tells about where the weights reach the share; the few elements there are
+//     narrowed down to the one by bins of their exact weights, those before them added up;
 //   - neither: the weights are added up as they lie.
 // Where more elements than the sort takes are alike (or k is larger than that), the digits of
 // d = max - x >= 0 are narrowed down by one histogram after another instead.
@@ -33,7 +33,7 @@ constexpr int kMaxTCluster = 8;
 constexpr int kBins = 1024;      // of the digits' histograms, and of the sort
 constexpr int kOctaves = 41, kParts = 64;  // the histogram by y: y <= 40 in 64ths
 constexpr int kSteps = kOctaves * kParts;
-constexpr int kList = 2048;      // elements that the first block sorts,
+constexpr int kList = 2048;      // elements that the first block takes up,
 constexpr int kOwn = 704;        // and that a block of a cluster finds
 // Blocks an SM: their latencies hide each other (192 rows of 131072 bf16, k = 50: 30 us, 53 by two of 512 threads).
 constexpr int kTBlocks = 4;
@@ -813,8 +813,9 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
 
     // ---------------------------------------------------------------- top-p by a histogram of y
     // Weights of 11 bits in each 64th of an octave tell to a thousandth (of the smaller side) where they reach the
-    // share.  The elements there are sorted, everything else is added up
-    // exactly, and if the cut is not among them after all the digits below find it.
+    // share.  Of the elements there the one is looked for, everything else is added up exactly, and if the cut is not among
+    // them after all the digits below find it.  (192 rows of 131072 bf16, p = 0.9: 91 us in two turns; of a row's 53 in
+    // its turn the largest takes 6, the histogram 10, its edges 4.5, the exact weights 17, the cut 8, the draw 6.)
     if (!done && nucleus && k == V && top < INFINITY) {
         for (int i = tid; i < kSteps; i += kTThreads) s.steps[i] = 0;
         __syncthreads();
