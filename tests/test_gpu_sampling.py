@@ -77,6 +77,27 @@ def test_many_of_a_short_row(bsf8_lib, V, bf16):
     check(x, u, k=ks, tp=[0.9] * N, mp=[1e-4] * N)
 
 
+@pytest.mark.parametrize("V", [2500, 20000, 70001])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_the_cut_among_many_alike(bsf8_lib, V, bf16):
+    """top-p that ends among hundreds or thousands of one logit, of two next to each other, and of a few."""
+    r = np.random.default_rng(V)
+    ps = [0.02, 0.2, 0.35, 0.5, 0.51, 0.7, 0.8, 0.9, 0.97, 0.999, 0.9999, 1e-7]
+    alike = [1, 20, 31, 33, 300, 700, 1500, 2040, 2049, 2300, 900, 64]
+    x = np.full((len(ps), V), -9.0, np.float32)
+    for i, n in enumerate(alike):
+        at = r.permutation(V)
+        x[i, at[:n]] = 2.0
+        x[i, at[n:n + n // 2]] = 2.0 - 2.0 ** -7  # the bf16 value below it
+        x[i, at[:5]] += r.random(5).astype(np.float32) * 3
+    x = torch.from_numpy(x).cuda()
+    if bf16:
+        x = x.to(torch.bfloat16)
+    u = r.random(len(ps)).astype(np.float32)
+    check(x, u, tp=ps)
+    check(x, u, tp=ps[::-1], mp=[1e-3] * len(ps), t=[0.8] * len(ps))
+
+
 def test_rows_ask_for_different_things(bsf8_lib):
     r = np.random.default_rng(1)
     N, V = 64, 3001
