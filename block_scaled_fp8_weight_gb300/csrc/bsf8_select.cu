@@ -561,6 +561,8 @@ __global__ void __launch_bounds__(kSThreads, 2) select_kernel(const BoundsView v
             next = after;
             word = later;
         }
+        // what was asked for past the last page writes zeros, and that memory is the histogram's next
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (cluster > 1) {
         cluster_wait();
     }

@@ -177,6 +177,21 @@ def test_selection_for_many_requests(bsf8_lib):
     Choice(5, [int(c) for c in r.integers(0, 5000, size=300)], 1, 8, 4, 128, 16, 20, 1, 1).check()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("full,keep", [(33, 32), (40, 3), (257, 31), (2049, 2000)])
+def test_selection_of_a_few_pages_again_and_again(bsf8_lib, D, full, keep):
+    """Warps whose pages end early, or that have none, ask for copies that write zeros where the keys are counted and listed
+    next: hundreds of calls give the same pages."""
+    c = Choice(D + full, [full * 16 + 3] * 40, 1, 4, 2, D, 16, keep)
+    want = c.check()[0]
+    bounds = bsf8.PageBounds(torch.from_numpy(c.codes).cuda(), torch.from_numpy(c.exps).cuda(), 16)
+    table, ctx = i32(c.table), i32(c.ctx)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        differ += (bsf8.select_pages(c.q, bounds, table, ctx, keep)[0] != want).sum()
+    assert int(differ) == 0 and bsf8.device_status() == 0
+
+
 def test_equal_scores_go_to_the_lowest_index(bsf8_lib):
     c = Choice(6, [16 * 700, 16 * 33], 1, 2, 2, 64, 16, 31)
     c.codes[:] = c.codes[:1]
