@@ -301,8 +301,10 @@ struct ExpWord<8> {
     }
 };
 
-// Larger keys for larger scores; equal ones for 0 and -0.
+// Larger keys for larger scores; equal ones for 0 and -0.  None above kTopKey: a NaN (infinities of both signs added up,
+// which exponents that kv_bounds does not write can give) has that of +inf, or more pages than `keep` would be listed.
 __device__ __forceinline__ uint32_t key_of(float f) {
+    if (!(f < INFINITY)) return kTopKey;
     const uint32_t b = __float_as_uint(f + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }

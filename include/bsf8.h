@@ -506,7 +506,8 @@ int bsf8_kv_bounds(const bsf8_kv_cache *cache, const bsf8_page_bounds *bounds, c
  *   Q+_d = sum over the rows of max(n, 0),  Q-_d = sum of min(n, 0),  n = rint(q_d * 2^(17 - k))
  *   both (Q + 2^(s-1)) >> s, s >= 0 the smallest that leaves the largest |Q| 14 bits (s = 0: as they are)
  *   score = sum over 32-channel blocks, added in pairs (fp32), of fp32(sum_d Q+_d hi_d + Q-_d lo_d) 2^(e - 27)
- * and +inf for a page with a byte 255, for the first `sink` pages and the last `recent` full ones.
+ * and +inf for a page with a byte 255, for the first `sink` pages and the last `recent` full ones, and where the sum
+ * is NaN (bytes above 249, which bsf8_kv_bounds does not write, can add up to infinities of both signs).
  *   q       as in bsf8_tree_attention;  ctx, nodes, max_len too
  *   bounds  of every full page of the requests
  *   pages   device, out, int32 [B][heads][width], width = bsf8_select_width(T, page_size, keep): page numbers

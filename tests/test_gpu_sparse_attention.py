@@ -225,6 +225,29 @@ def test_queries_and_bounds_at_their_ends(bsf8_lib):
     c.check()
 
 
+@pytest.mark.parametrize("full,keep", [(90, 20), (3000, 2500), (300, 1)])
+def test_scores_that_are_nan_count_as_infinite(bsf8_lib, monkeypatch, full, keep):
+    """Bounds that kv_bounds does not write: sums of exponent 2^127 that overflow downwards beside blocks of byte 255.  Their
+    pages come first, `keep` of them at most, and nothing is written behind a row of the list."""
+    c = Choice(15, [16 * full + 2], 2, 4, 2, 256, 16, keep)
+    c.q[:, 1] = -c.q[:, 0]  # sums of both signs, of almost 2^14, in all channels
+    c.q[:] = torch.where(c.q < 0, -255 / 128, 255 / 128).to(c.q.dtype)
+    r = np.random.default_rng(15)
+    down = r.random(len(c.codes)) < 0.6
+    c.codes[down, :, 0], c.codes[down, :, 1] = -128, 127
+    c.exps[down] = 254
+    c.exps[down, :, 7] = 255
+    plain = ref.scores
+
+    def scores(*a):
+        with np.errstate(all="ignore"):
+            f = plain(*a)
+        assert np.isnan(f).sum() > full // 3
+        return np.where(np.isnan(f), np.inf, f)
+    monkeypatch.setattr(ref, "scores", scores)
+    c.check()
+
+
 def test_query_rows_with_a_stride(bsf8_lib):
     Choice(9, [16 * 50, 16 * 80 + 7], 4, 6, 3, 64, 16, 12, ld=40).check()
 
