@@ -16,7 +16,8 @@
 //     narrowed down to the one by bins of their exact weights, those before them added up;
 //   - neither: the weights are added up as they lie.
 // Where more elements than the sort takes are alike (or k is larger than that), the digits of
-// d = max - x >= 0 are narrowed down by one histogram after another instead.
+// d = max - x >= 0 are narrowed down by one histogram after another instead, then those of x among elements whose rounded d
+// is one.
 #include "bsf8_device.cuh"
 #include "bsf8_internal.h"
 
@@ -46,6 +47,7 @@ struct TokenShared {
     int bmin;
     u64 wsum[kTWarps], bsum, wevery[kTWarps], bevery;
     int wcount[kTWarps], bcount;
+    uint32_t wfirst[kTWarps], wlast[kTWarps], bfirst, blast;
     u64 tsum[kTWarps];
     int tcount[kTWarps];
     float max8[kTThreads / 8];      // largest logits of eight threads
@@ -58,7 +60,7 @@ struct TokenShared {
     int listed;                     // elements in list
     u64 cut_key, total;             // of the first block: what stays, its sum
     float octave[kOctaves], all8[kOctaves];  // about the weights of this block by octave, and of all
-    u64 list[kOwn];                 // this block's elements: bits of d, index
+    u64 list[kOwn];                 // this block's elements, as keys
     union {
         u64 sort[kList];
         int tally[kList];           // counts of the search for the k-th
@@ -180,6 +182,14 @@ __device__ __forceinline__ uint32_t order_of(float f) {
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
+// An element's place in the order that top-k and top-p go by, smaller for larger logits, then for lower indices; 0 and -0
+// are one.  Of the logit itself: max - x is rounded, and many x far below a large maximum have one distance.
+__device__ __forceinline__ u64 key_at(float v, int index) { return (u64)~order_of(v + 0.0f) << 20 | (u64)index; }
+__device__ __forceinline__ float logit_of(u64 key) { return value_of(~(uint32_t)(key >> 20)); }
+
+// max - x, 0 for the largest itself (inf - inf)
+__device__ __forceinline__ float distance_to(float top, float v) { return v == top ? 0.0f : __fsub_rn(top, v); }
+
 // A group of 16 bytes: its elements, NaN as -inf.
 template <typename T>
 struct Logit;
@@ -242,7 +252,7 @@ __device__ __forceinline__ u64 sum_before(u64 v, TokenShared &s, u64 &all) {
 }
 
 // Sorts s.sort[0 .. n), all different, by the whole block: by counting how many are smaller up to 256 of them (a
-// thread or more each), else into bins of even width in d first.  `bins`: kBins words of scratch.  Ends with a
+// thread or more each), else into bins of even width in the logits first.  `bins`: kBins words of scratch.  Ends with a
 // barrier.
 __device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
     const int tid = threadIdx.x;
@@ -276,8 +286,8 @@ __device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kTWarps; ++w) lo = min(lo, (uint32_t)s.tcount[w]), hi = max(hi, (uint32_t)s.wcount[w]);
-    const float least = __uint_as_float(lo), per = fminf((float)(kBins - 1) / (__uint_as_float(hi) - least), 1e38f);
-    auto bin_of = [&](u64 key) { return min((int)((__uint_as_float((uint32_t)(key >> 20)) - least) * per), kBins - 1); };
+    const float first = value_of(~lo), per = fminf((float)(kBins - 1) / (first - value_of(~hi)), 1e38f);
+    auto bin_of = [&](u64 key) { return min((int)((first - logit_of(key)) * per), kBins - 1); };
 #pragma unroll
     for (int r = 0; r < kEach; ++r)
         if (tid + r * kTThreads < n) atomicAdd(&bins[bin_of(v[r])], 1);
@@ -315,9 +325,9 @@ __device__ __noinline__ void sort_list(TokenShared &s, int *bins, int n) {
 }
 
 // Of s.sort[0 .. n) in order, all different, the element in which the weights, from `run` on, reach `cut`: its key and the
-// sum up to it in s.cut_key and s.total, which stay if there is none.  By bins over the distances in question, or
-// over the indices of those at one distance, whose weights are added up; the few of the last bin are compared.  Loses s.sort.
-__device__ __noinline__ void find_cut(TokenShared &s, int n, float rate, u64 run, u64 cut, int V) {
+// sum up to it in s.cut_key and s.total, which stay if there is none.  By bins over the logits in question, or
+// over the indices of those of one logit, whose weights are added up; the few of the last bin are compared.  Loses s.sort.
+__device__ __noinline__ void find_cut(TokenShared &s, int n, float top, float rate, u64 run, u64 cut, int V) {
     constexpr int kFew = 32;
     const int tid = threadIdx.x, warp = tid >> 5;
     // how many a bin has, and their weights by 20 bits (2048 of at most 2^40): atomics of 64 bits try again and again
@@ -331,7 +341,7 @@ __device__ __noinline__ void find_cut(TokenShared &s, int n, float rate, u64 run
         v[r] = at < n ? s.sort[at] : 0;
         in |= at < n ? 1u << r : 0u;
     }
-    auto weight_of = [&](u64 key) { return weight(__uint_as_float((uint32_t)(key >> 20)), rate); };
+    auto weight_of = [&](u64 key) { return weight(distance_to(top, logit_of(key)), rate); };
     int count = n, index0 = 0, bits = 32 - __clz(V - 1);  // the indices in question, 2^bits of them
     while (count > kFew) {
         uint32_t lo = 0xFFFFFFFFu, hi = 0;
@@ -598,14 +608,13 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
         return;
     }
 
-    // the distance of an element, as bits that order as it does; infinite where it has no part
-    auto distance = [&](float v) { return v == top ? 0.0f : __fsub_rn(top, v); };
-    auto key_at = [&](float v, int index) { return (u64)__float_as_uint(distance(v)) << 20 | (u64)index; };
+    // the distance of an element, infinite where it has no part
+    auto distance = [&](float v) { return distance_to(top, v); };
+    auto weight_of = [&](u64 key) { return weight(distance(logit_of(key)), rate); };
     auto keep_in_list = [&](float v, int index) {
-        const u64 key = key_at(v, index);
-        if (key >> 20 >= kInfBits) return;
+        if (distance(v) == INFINITY) return;
         const int at = atomicAdd(&s.listed, 1);
-        if (at < own) list[at] = key;
+        if (at < own) list[at] = key_at(v, index);
     };
     // the blocks' lists, in the first one's `sort`; how many elements (none are moved where they are too many)
     auto collect = [&]() {
@@ -631,8 +640,10 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
         return n;
     };
     const u64 top2 = two(top, top), rate2 = two(rate, rate), zero2 = two(minus_zero, minus_zero);
-    // what the sort finds to stay: elements up to cut_key in the order of (bits of d, index)
-    u64 cut_key = ~0ull;
+    // what is found to stay: elements of logits above cut_x, and of those that equal it the ones up to cut_index (all: -inf)
+    float cut_x = -INFINITY;
+    int cut_index = 0x7FFFFFFF;
+    auto stays = [&](float v, int index) { return v > cut_x || (v == cut_x && index <= cut_index); };
     bool done = false;      // the cut is found,
     bool summed = false;    // and the sums of what stays in each warp's part
 
@@ -732,7 +743,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 for (int i = 0; i < kEach; ++i) {
                     const int at = kEach * tid + i;
                     key[i] = at < min(n, k) ? s.sort[at] : ~0ull;
-                    w[i] = at < min(n, k) ? weight(__uint_as_float((uint32_t)(key[i] >> 20)), rate) : 0;
+                    w[i] = at < min(n, k) ? weight_of(key[i]) : 0;
                     if (w[i] < least) w[i] = 0;
                     sum += w[i];
                 }
@@ -974,14 +985,16 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 const u64 cut = max((u64)1, part_of(pfix, __shfl_sync(0xFFFFFFFFu, all, 0)));
                 if (tid == 0) s.total = 0;
                 __syncthreads();
-                find_cut(s, n, rate, below, cut, V);
+                find_cut(s, n, top, rate, below, cut, V);
             }
             barrier();
             const u64 kept_all = of64(&s.total, 0);
             found = kept_all != 0;  // else the cut is elsewhere
             if (found) {
                 done = summed = true;
-                cut_key = of64(&s.cut_key, 0);
+                const u64 key = of64(&s.cut_key, 0);
+                cut_x = logit_of(key);
+                cut_index = (int)(key & 0xFFFFFu);
                 inv = 1.0f / (float)kept_all;
             }
         }
@@ -994,8 +1007,8 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             for (int i = tid; i < s.listed; i += kTThreads) {
                 const u64 key = list[i];
                 const int part = (((int)(key & 0xFFFFFu) + mis) / VEC - b0) / per_warp;
-                if (key > cut_key || part >= kTWarps) continue;
-                const u64 w = weight(__uint_as_float((uint32_t)(key >> 20)), rate);
+                if (part >= kTWarps || !stays(logit_of(key), (int)(key & 0xFFFFFu))) continue;
+                const u64 w = weight_of(key);
                 atomicAdd(&s.tcount[part], (int)((uint32_t)w & 0xFFFFFu));
                 atomicAdd(&s.wcount[part], (int)(w >> 20));
             }
@@ -1006,13 +1019,9 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     }
 
     // ---------------------------------------------------------------- by digits, where there are too many alike
-    uint32_t cut_bits = kInfBits;    // elements with bits of d below it stay,
-    int cut_index = -1;              // and of those that equal it the ones up to this index
     // Narrows the cut down to the element in which the running count (or weight) reaches `want`: of those inside
-    // the present cut.  Returns how many stay of those that equal the new cut's bits.
+    // the present cut.
     auto narrow = [&](bool by_weight, u64 want_in, bool fraction) {
-        const uint32_t limit = cut_bits;
-        const int limit_index = cut_index;
         uint32_t base = 0, most = kInfBits;
         u64 want = want_in;
         int level = 0, shift = 18;
@@ -1026,8 +1035,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 for (int i = 0; i < VEC; ++i) {
                     const float d = distance(y[i]);
                     const uint32_t bits = __float_as_uint(d);
-                    if (bits - base > most || bits >= kInfBits) continue;
-                    if (bits > limit || (bits == limit && g * VEC - mis + i > limit_index)) continue;
+                    if (bits - base > most || bits >= kInfBits || !stays(y[i], g * VEC - mis + i)) continue;
                     int bin;
                     if (level == 0) {  // 16 octaves of 32 bins, what is below and above them in one each
                         const int b = (int)(bits >> 18) - (119 << 5);
@@ -1114,30 +1122,85 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             }
             ++level;
         }
-        // elements of these bits have one weight: as many of them, by index, as it takes
+        // elements at this distance have one weight: as many of them as it takes, by their logits where those differ (far below
+        // a large maximum), then by index
         const u64 each = by_weight ? weight(__uint_as_float(base), rate) : 1;
-        const u64 keep = (want + each - 1) / each;
-        // the index of the keep-th of them
-        int mine = 0;
-        for (int g = g0 + lane; g < g1; g += 32) {
-            float y[VEC];
-            load(g, y);
+        u64 keep = (want + each - 1) / each;
+        float least_x = -INFINITY, most_x = INFINITY;  // the logits in question
+        auto is_one = [&](float v, int index) {
+            return __float_as_uint(distance(v)) == base && v >= least_x && v <= most_x && stays(v, index);
+        };
+        int mine;
+        while (true) {
+            mine = 0;
+            float least_of = INFINITY, most_of = -INFINITY;
+            for (int g = g0 + lane; g < g1; g += 32) {
+                float y[VEC];
+                load(g, y);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                mine += __float_as_uint(distance(y[i])) == base && (base != limit || g * VEC - mis + i <= limit_index) ? 1 : 0;
+                for (int i = 0; i < VEC; ++i) {
+                    const bool in = is_one(y[i], g * VEC - mis + i);
+                    mine += in ? 1 : 0;
+                    least_of = in ? fminf(least_of, y[i]) : least_of;
+                    most_of = in ? fmaxf(most_of, y[i]) : most_of;
+                }
+            }
+            mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+            uint32_t lo = __reduce_min_sync(0xFFFFFFFFu, order_of(least_of + 0.0f)), hi = __reduce_max_sync(0xFFFFFFFFu, order_of(most_of + 0.0f));
+            if (lane == 0) s.wcount[warp] = mine, s.wfirst[warp] = lo, s.wlast[warp] = hi;
+            __syncthreads();
+            if (tid == 0) {
+                int v = 0;
+#pragma unroll
+                for (int w = 0; w < kTWarps; ++w) {
+                    v += s.wcount[w];
+                    lo = min(lo, s.wfirst[w]);
+                    hi = max(hi, s.wlast[w]);
+                }
+                s.bcount = v, s.bfirst = lo, s.blast = hi;
+                s.cut = -1;
+            }
+            barrier();
+            lo = __reduce_min_sync(0xFFFFFFFFu, lane < cluster ? of32(&s.bfirst, lane) : ~0u);
+            hi = __reduce_max_sync(0xFFFFFFFFu, lane < cluster ? of32(&s.blast, lane) : 0u);
+            least_x = value_of(lo);
+            most_x = value_of(hi);
+            if (lo == hi) break;
+            // which of the logits, from the largest: 10 bits of them a turn
+            for (int i = tid; i < kBins; i += kTThreads) s.count[i] = 0;
+            __syncthreads();
+            const int narrower = max(0, 32 - __clz(hi - lo) - 10);
+            for (int g = g0 + lane; g < g1; g += 32) {
+                float y[VEC];
+                load(g, y);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    if (is_one(y[i], g * VEC - mis + i)) atomicAdd(&s.count[(hi - order_of(y[i] + 0.0f)) >> narrower], 1u);
+            }
+            barrier();
+            int n[kBinsEach], sum = 0;
+#pragma unroll
+            for (int j = 0; j < kBinsEach; ++j) {
+                n[j] = 0;
+                for (int c = 0; c < cluster; ++c) n[j] += (int)of32(&s.count[kBinsEach * tid + j], c);
+                sum += n[j];
+            }
+            u64 all;
+            u64 before = sum_before((u64)sum, s, all);
+#pragma unroll
+            for (int j = 0; j < kBinsEach; ++j) {
+                if (before < keep && before + n[j] >= keep) s.bin = kBinsEach * tid + j, s.mass = before;
+                before += n[j];
+            }
+            barrier();
+            keep -= s.mass;
+            hi -= (uint32_t)s.bin << narrower;
+            lo = max(lo, hi - min(hi, (1u << narrower) - 1u));
+            least_x = value_of(lo);
+            most_x = value_of(hi);
         }
-        mine = __reduce_add_sync(0xFFFFFFFFu, mine);
-        if (lane == 0) s.wcount[warp] = mine;
-        __syncthreads();
-        if (tid == 0) {
-            int v = 0;
-            for (int w = 0; w < kTWarps; ++w) v += s.wcount[w];
-            s.bcount = v;
-            s.cut = -1;
-        }
-        barrier();
-        u64 before = 0;
-        for (int c = 0; c < rank; ++c) before += ld_cluster32(map_to_rank(&s.bcount, c));
+        // the index of the keep-th of them
+        u64 before = __reduce_add_sync(0xFFFFFFFFu, lane < rank ? of32(&s.bcount, lane) : 0u);
         for (int w = 0; w < warp; ++w) before += s.wcount[w];
         if (before < keep && before + mine >= keep) {  // this warp's part has it
             for (int gb = g0; gb < g1; gb += 32) {
@@ -1150,7 +1213,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
                 bool is[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) {
-                    is[i] = __float_as_uint(distance(y[i])) == base && (base != limit || g * VEC - mis + i <= limit_index);
+                    is[i] = y[i] == most_x && stays(y[i], g * VEC - mis + i);
                     n += is[i] ? 1 : 0;
                 }
                 int upto = n;
@@ -1168,34 +1231,26 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             }
         }
         barrier();
-        int found = -1;
-        for (int c = 0; c < cluster; ++c) found = max(found, cluster > 1 ? (int)ld_cluster32(map_to_rank(&s.cut, c)) : s.cut);
-        cut_bits = base;
-        cut_index = found;
+        cut_index = __reduce_max_sync(0xFFFFFFFFu, lane < cluster ? (int)of32(&s.cut, lane) : -1);
+        cut_x = most_x;
         barrier();  // s.cut is written again
     };
 
     if (!done) {
         if (k < V) narrow(false, (u64)k, false);
         if (nucleus) narrow(true, pfix, true);
-        if (k < V || nucleus) cut_key = ((u64)cut_bits << 20) + (u64)(long long)cut_index;
     }
 
     // ---------------------------------------------------------------- what stays, in order of index
     auto kept = [&](float v, int index) -> u64 {
         const float d = distance(v);
-        const uint32_t bits = __float_as_uint(d);
-        if (bits >= kInfBits) return 0;
-        if (cut_key != ~0ull) {
-            const u64 key = (u64)bits << 20 | (u64)index;
-            if (key > cut_key) return 0;
-        }
+        if (d == INFINITY || !stays(v, index)) return 0;
         const u64 w = weight(d, rate);
         return w >= least ? w : 0;
     };
     if (!summed) {
         u64 sum = 0;
-        if (cut_key == ~0ull && top < INFINITY) {  // nothing is cut off
+        if (cut_x == -INFINITY && top < INFINITY) {  // nothing is cut off
             auto add = [&](auto all) {  // all: no weight is too small to stay
                 each([&](const float (&y)[VEC], int) {
 #pragma unroll
@@ -1247,14 +1302,14 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     if constexpr (PROBS) {
         each([&](const float (&y)[VEC], int e) {
             float p[VEC];
-            if (top < INFINITY && (cut_key == ~0ull || summed)) {
+            if (top < INFINITY && (cut_x == -INFINITY || summed)) {
 #pragma unroll
                 for (int i = 0; i < VEC; i += 2) {
                     const Two w = weights2(y[i], y[i + 1], top2, rate2, zero2);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const u64 wj = ((u64)w.m[j] << 16) >> w.n[j];
-                        const bool in = w.y[j] <= 40.0f && wj >= least && (!summed || key_at(y[i + j], e + i + j) <= cut_key);
+                        const bool in = w.y[j] <= 40.0f && wj >= least && (!summed || stays(y[i + j], e + i + j));
                         p[i + j] = in ? share(wj) : 0.0f;
                     }
                 }

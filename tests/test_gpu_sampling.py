@@ -142,6 +142,53 @@ def test_the_draw_at_its_ends(bsf8_lib):
     check(x, [0.0, 1 - 2.0 ** -24, 1.0, 2.0, -1.0, NAN, INF, 2.0 ** -24], tp=[0.9] * 8)
 
 
+def close_logits(r, N, V, n, top, far, few_values=False):
+    """Rows whose largest logit is `top`, with n logits about 0 that it is one rounded distance away from, of either sign, the
+    rest at `far`."""
+    x = np.full((N, V), far, np.float32)
+    for i in range(N):
+        at = r.permutation(V)
+        small = r.integers(-40, 41, size=n) if few_values else r.permutation(2 * n) - n
+        x[i, at[:n]] = small[:n] * np.float32(2.0 ** -50)
+        x[i, at[n]] = top
+    return torch.from_numpy(x).cuda()
+
+
+def test_a_larger_logit_at_the_same_rounded_distance_comes_first(bsf8_lib):
+    """10 - 2^-31 and 10 - 2^-30 are one number in fp32: the order is the logits'."""
+    for bf16 in (False, True):
+        for V in (64, 3000, 9000):
+            x = torch.full((2, V), -5.0, device="cuda")
+            x[:, 0], x[:, 1], x[:, 2], x[:, 3], x[:, 4] = 10.0, 2.0 ** -31, 2.0 ** -30, -0.0, 0.0
+            if bf16:
+                x = x.to(torch.bfloat16)
+            for k in (2, 3, 4, 5):
+                check(x, [0.99999994, 0.3], k=[k] * 2)
+                check(x, [0.99999994, 0.3], k=[k] * 2, t=[30.0] * 2, tp=[0.9] * 2)
+
+
+@pytest.mark.parametrize("V,n", [(100, 60), (2048, 1500), (2500, 700), (8000, 4000), (5000, 3000), (40000, 900), (40000, 30000),
+                                 (131072, 100000)])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("few_values", [False, True])
+def test_the_cut_among_logits_at_one_rounded_distance(bsf8_lib, V, n, bf16, few_values):
+    """By k: in the sort, among all of a short row, by digits; by top-p; by one after the other."""
+    r = np.random.default_rng(V + n)
+    ks = sorted({2, 5, n // 7 + 2, n // 3, n // 2, n - 1, n, min(n, 1900)})
+    N = len(ks)
+    x = close_logits(r, N, V, n, 10.0, -900.0, few_values)
+    if bf16:
+        x = x.to(torch.bfloat16)
+    u = r.random(N).astype(np.float32)
+    u[::2] = 0.99999994
+    t = [20.0] * N  # the logits about 0 weigh 0.6 of the largest, those at -900 nothing
+    check(x, u, t=t, k=ks)
+    ps = np.linspace(0.01, 0.99, N)
+    check(x, u, t=t, tp=ps)
+    check(x, u, t=t, tp=ps, mp=[0.5] * N)
+    check(x, u, t=t, k=ks, tp=ps[::-1])
+
+
 @pytest.mark.parametrize("value", [0.0, -5.5])
 def test_ties_go_to_the_lowest_index(bsf8_lib, value):
     """A row of equal logits over many blocks: top-k and top-p cut inside it."""
