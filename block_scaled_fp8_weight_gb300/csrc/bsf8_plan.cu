@@ -27,11 +27,12 @@ struct PlanShared {
 };
 
 // The sums of K numbers over the threads before this one (v), and over all (all); one barrier.  The last number's sums
-// stop at `most`, below 2^31 with one more (a sum that is cut off there is still one: in any order).  `set`: slots in turn.
+// stop at `most`, at most 2^30 + 1 (a sum that is cut off there is still one: in any order; two of them fit 32 bits without a
+// sign).  `set`: slots in turn.
 template <int NT, int K>
 __device__ __forceinline__ void before_me(PlanShared<NT> &s, int set, int (&v)[K], int (&all)[K], int most) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto add = [&](int k, int a, int b) { return k == K - 1 ? min(a + b, most) : a + b; };
+    auto add = [&](int k, int a, int b) { return k == K - 1 ? (int)min((uint32_t)a + (uint32_t)b, (uint32_t)most) : a + b; };
     int up[K], w[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) up[k] = v[k];

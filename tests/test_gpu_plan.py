@@ -107,6 +107,24 @@ def test_bad_books_and_lengths_are_cut_off_and_reported(bsf8_lib):
     assert bsf8.device_status() == INDEX
 
 
+@pytest.mark.parametrize("N", [(1 << 30) - 2, (1 << 30) - 1, 1 << 30])
+@pytest.mark.parametrize("B,large", [(4, (0, 1)), (7, (0, 1, 2)), (40, (0, 5, 35)), (200, (3, 7, 40, 190)), (200, (0, 1, 2, 3, 4))])
+def test_requests_past_the_largest_budget_leave_nothing_behind_them(bsf8_lib, N, B, large):
+    """Requests that each ask for more tokens than any call has: what comes after them does not fit either, though it needs no
+    page."""
+    pages = (1 << 30) // 1024 + 1
+    add, held = [0] * B, [0] * B
+    for b in large:
+        add[b] = N + 1
+        if b + 1 not in large:
+            add[b + 1], held[b + 1] = 5, 1
+    add[B - 1], held[B - 1] = 3, 1
+    book = bsf8.PageBook(torch.zeros((B, pages), dtype=torch.int32, device="cuda"), i32(held), i32([2, 1, 0]), i32([3]))
+    req, slot, start, granted = bsf8.kv_plan(book, i32([0] * B), i32(add), page_size=1024, tokens=N)
+    assert not granted.any() and not start.any() and not req.any() and (slot == -1).all()
+    assert int(book.count) == 3 and book.held.tolist() == held and bsf8.device_status() == 0
+
+
 def test_fresh_books_serve_a_few_steps(bsf8_lib):
     """Steps one after another from PageBook.empty: no page is held twice, none is lost."""
     r = np.random.default_rng(4)
