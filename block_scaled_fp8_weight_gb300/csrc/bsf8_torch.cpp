@@ -600,6 +600,7 @@ PyObject *py_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             gate = g.data_ptr();
         }
         at::Tensor h, r;
+        if (a[2] == Py_None && a[7] != Py_None) throw Refused{PyExc_ValueError, "out needs weight: without it only the sum is written"};
         if (a[2] != Py_None) h = c.output(a[7], at::kBFloat16, shape, "out");
         if (a[1] != Py_None || a[8] != Py_None) r = c.output(a[8], type, shape, "residual_out");
         const int status = bsf8_residual_norm(x.data_ptr(), ldx, res, ldr, type == at::kFloat, post, gate, kind, ldg,

@@ -249,7 +249,7 @@ def residual_norm(x, residual, weight, *, post_weight=None, gate=None, scale: fl
                   residual_out=None):
     """From one block to the next: x (bf16 [M, H]) normed by post_weight (bf16 [H]; None: as it is), times scale and
     gate (bf16 [H], [M, 1] or [M, H]), is added to residual (bf16 or fp32 [M, H]; None: 0), and the sum normed by
-    weight (bf16 [H]; None: not).  Returns (h bf16 [M, H] or None, the sum in the residual's type, or None without a
+    weight (bf16 [H]; None: not, and no out).  Returns (h bf16 [M, H] or None, the sum in the residual's type, or None without a
     residual and residual_out).  residual_out may be residual, out may be x."""
     r = _ext.residual_norm(x, residual, weight, post_weight, gate, scale, eps, out, residual_out)
     if type(r) is int:

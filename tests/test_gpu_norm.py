@@ -141,6 +141,15 @@ def test_refused_tensors(bsf8_lib):
         f(x[:, 1:57], x[:, 8:], w[:56])  # not 16-byte aligned
 
 
+def test_an_output_that_nothing_writes_is_refused(bsf8_lib):
+    x = torch.zeros(4, 64, device="cuda", dtype=torch.bfloat16)
+    out = torch.full_like(x, 3.0)
+    for residual, residual_out in ((x, None), (None, torch.empty_like(x)), (None, None)):
+        with pytest.raises(ValueError, match="out needs weight"):
+            bsf8.residual_norm(x, residual, None, out=out, residual_out=residual_out)
+    assert (out == 3).all()
+
+
 @pytest.mark.parametrize("M,H", [(3000, 5120), (1500, 7168)])  # one row ahead, and two
 def test_a_wait_that_runs_out_is_reported(bsf8_lib, M, H):
     """No loads are issued (a test-only option): the kernel for many rows gives up its waits and says so."""
