@@ -306,6 +306,13 @@ int whole_number(PyObject *o, long none, const char *name) {
     return (int)v;
 }
 
+// max_len, the table's capacity for None; what is far below any length is refused here.
+int max_len_of(PyObject *o, int pages, int page_size) {
+    const int v = whole_number(o, std::min((long)pages * page_size, (long)BSF8_MAX_LEN), "max_len");
+    if (v < -1) throw Refused{PyExc_ValueError, "max_len must fit 31 bits"};
+    return v;
+}
+
 // k8 kexp v8 vexp | q table ctx nodes mask scale max_len out lse workspace; `sparse`: a table for each head
 template <bool sparse>
 PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -343,7 +350,7 @@ PyObject *py_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
             }
             have = (size_t)ws.numel();
         }
-        const int max_len = whole_number(a[10], std::min((long)t.pages * s.page_size, (long)BSF8_MAX_LEN), "max_len");
+        const int max_len = max_len_of(a[10], t.pages, s.page_size);
         const double scale = a[9] == Py_None ? 1.0 / std::sqrt((double)s.dim) : number(a[9]);
         const int status =
             (sparse ? bsf8_sparse_attention : bsf8_tree_attention)(q.data_ptr(), ldq, &s, t.at, t.pages, ctx, nodes, mask,
@@ -499,7 +506,7 @@ PyObject *py_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const auto *nodes = static_cast<const int32_t *>(c.maybe(a[6], at::kInt, per, "nodes"));
         const int keep = whole_number(a[7], 0, "keep"), sink = whole_number(a[8], 0, "sink"),
                   recent = whole_number(a[9], 0, "recent");
-        const int max_len = whole_number(a[10], std::min((long)t.pages * v.page_size, (long)BSF8_MAX_LEN), "max_len");
+        const int max_len = max_len_of(a[10], t.pages, v.page_size);
         // (a width of 0 is refused by the library)
         const int64_t shape[3] = {B, v.heads, bsf8_select_width(small(T, "T"), v.page_size, keep)};
         at::Tensor pages = c.fresh(at::kInt, shape), kept = c.fresh(at::kInt, per);

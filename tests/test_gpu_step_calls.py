@@ -152,6 +152,29 @@ def test_past_two_to_the_31_elements(bsf8_lib):
     assert torch.equal(p[-1:], bsf8.token_probs(x[-1:].clone())) and (p[:-1, 7] == 1).all() and not p[:-1, 8:].any()
 
 
+def test_lengths_that_no_call_takes(bsf8_lib):
+    """max_len outside 31 bits and below -1 is a ValueError, as it always was for tree_attention; what only the library refuses
+    is a Bsf8Error."""
+    cache = bsf8.KVCache.empty(4, 1, 64, 16)
+    b = bsf8.PageBounds.empty(cache)
+    q = torch.zeros(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    table, ctx = torch.zeros((1, 4), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = (lambda n: bsf8.tree_attention(q, cache, table, ctx, max_len=n),
+             lambda n: bsf8.sparse_attention(q, cache, table[:, None], ctx, max_len=n),
+             lambda n: bsf8.select_pages(q, b, table, ctx, 2, max_len=n))
+    for f in calls:
+        for n in (-2, -2 ** 31 + 1, -2 ** 31, 2 ** 31, -2 ** 40, 2 ** 40):
+            with pytest.raises(ValueError):
+                f(n)
+        for n in (-1, 0, 65):
+            with pytest.raises(bsf8.Bsf8Error):
+                f(n)
+        with pytest.raises(OverflowError):
+            f(2 ** 70)
+        with pytest.raises(TypeError):
+            f(3.5)
+
+
 def test_a_plan_of_many_tokens(bsf8_lib):
     N = (1 << 27) + 3
     book = bsf8.PageBook.empty(3, 1 << 15, 1 << 15)
