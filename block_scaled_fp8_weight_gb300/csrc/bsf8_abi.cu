@@ -299,13 +299,12 @@ inline BoundsView bounds_view(const bsf8_page_bounds *v, const int32_t *table, i
     return BoundsView{v->codes, v->exps, table, v->pages, v->page_size, v->heads, v->dim, table_pages};
 }
 
-inline int check_sample(const void *logits, int64_t ld, int bf16, const void *temperature, const void *top_k,
+inline int check_sample(const void *logits, int64_t ld, const void *temperature, const void *top_k,
                         const void *top_p, const void *min_p, const void *p, int N, int V) {
     if (N == 0) return BSF8_OK;  // nothing to do; empty tensors may have no address
     if (!logits || !p) return BSF8_ERR_NULL;
     if (N < 0 || N > (1 << 20) || V < 1 || V > (1 << 20)) return BSF8_ERR_SHAPE;
     if (ld < V) return BSF8_ERR_STRIDE;
-    (void)bf16;
     if (!aligned16(logits) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) || !aligned4(p))
         return BSF8_ERR_ALIGN;
     return BSF8_OK;
@@ -724,7 +723,7 @@ int bsf8_select_pages(const void *q, int64_t ldq, const bsf8_page_bounds *bounds
 int bsf8_sample_tokens(const void *logits, int bf16, int64_t ld, const float *u, const float *temperature,
                        const int32_t *top_k, const float *top_p, const float *min_p, int32_t *token, float *p, int N, int V,
                        bsf8_stream_t stream) {
-    const int st = check_sample(logits, ld, bf16, temperature, top_k, top_p, min_p, p, N, V);
+    const int st = check_sample(logits, ld, temperature, top_k, top_p, min_p, p, N, V);
     if (st || N == 0) return st;
     if (!u || !token) return BSF8_ERR_NULL;
     if (!aligned4(u) || !aligned4(token)) return BSF8_ERR_ALIGN;
@@ -734,7 +733,7 @@ int bsf8_sample_tokens(const void *logits, int bf16, int64_t ld, const float *u,
 
 int bsf8_token_probs(const void *logits, int bf16, int64_t ld, const float *temperature, const int32_t *top_k,
                      const float *top_p, const float *min_p, float *p, int N, int V, bsf8_stream_t stream) {
-    const int st = check_sample(logits, ld, bf16, temperature, top_k, top_p, min_p, p, N, V);
+    const int st = check_sample(logits, ld, temperature, top_k, top_p, min_p, p, N, V);
     if (st || N == 0) return st;
     if (!aligned16(p)) return BSF8_ERR_ALIGN;
     SampleArgs a{logits, ld, bf16 ? 1 : 0, temperature, top_p, min_p, nullptr, top_k, nullptr, p, N, V};

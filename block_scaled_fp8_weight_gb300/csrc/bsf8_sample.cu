@@ -644,8 +644,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     float cut_x = -INFINITY;
     int cut_index = 0x7FFFFFFF;
     auto stays = [&](float v, int index) { return v > cut_x || (v == cut_x && index <= cut_index); };
-    bool done = false;      // the cut is found,
-    bool summed = false;    // and the sums of what stays in each warp's part
+    bool summed = false;  // the cut is found, and the sums of what stays in each warp's part
 
     // ---------------------------------------------------------------- top-k by a few candidates
     const bool few = V <= kList && (k < V || nucleus);
@@ -827,7 +826,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     // share.  Of the elements there the one is looked for, everything else is added up exactly, and if the cut is not among
     // them after all the digits below find it.  (192 rows of 131072 bf16, p = 0.9: 91 us in two turns; of a row's 53 in
     // its turn the largest takes 6, the histogram 10, its edges 4.5, the exact weights 17, the cut 8, the draw 6.)
-    if (!done && nucleus && k == V && top < INFINITY) {
+    if (nucleus && k == V && top < INFINITY) {
         for (int i = tid; i < kSteps; i += kTThreads) s.steps[i] = 0;
         __syncthreads();
         const float farthest = least > 1 ? fminf(40.0f, 40.001f - log2f((float)least)) : 40.0f;
@@ -991,7 +990,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
             const u64 kept_all = of64(&s.total, 0);
             found = kept_all != 0;  // else the cut is elsewhere
             if (found) {
-                done = summed = true;
+                summed = true;
                 const u64 key = of64(&s.cut_key, 0);
                 cut_x = logit_of(key);
                 cut_index = (int)(key & 0xFFFFFu);
@@ -1236,7 +1235,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
         barrier();  // s.cut is written again
     };
 
-    if (!done) {
+    if (!summed) {
         if (k < V) narrow(false, (u64)k, false);
         if (nucleus) narrow(true, pfix, true);
     }
