@@ -4,7 +4,7 @@
 // One cluster does it all: its blocks each take the same sums over the requests (a thread a request, two
 // scans), so that nothing but the pages themselves goes from one to the other -- what the first half gives
 // back the second may hand out, with the cluster's barrier between them -- and share the pages and tokens
-// evenly.  Few requests and tokens take one small block: what it costs is the chain of loads, scans and
+// evenly.  Few requests, tokens and pages take one small block: what it costs is the chain of loads, scans and
 // barriers.  (1024 requests, half of them leaving, 198000 tokens: 9.2 us in a graph, 13.7 with eight blocks, 30 with
 // those of 512 threads, three scans and a search a token; seven requests of a few tokens 2.6.)
 #include "bsf8_device.cuh"
@@ -236,8 +236,11 @@ cudaError_t plan_threads(const PlanArgs &a, int cluster, cudaStream_t stream, in
 cudaError_t launch_plan(const PlanArgs &a, cudaStream_t stream) {
     int *status = status_word();
     if (!status) return cudaErrorInvalidSymbol;
-    // (one block / the cluster: 64 requests, 576 tokens 3.7 us / 4.9; 128, 1152 tokens 4.7 / 5.05; 64, 4096 tokens 5.95 / 5.0)
-    if (a.B <= 128 && a.N <= 1536) return plan_threads<128>(a, 1, stream, status);
+    // One block where tokens are few, and pages that may come back (those handed out are no more than tokens and requests).
+    // One block / the cluster: 64 requests, 576 tokens 3.7 us / 4.9; 128, 1152 tokens 4.7 / 5.05; 64, 4096 tokens 5.95 / 5.0.
+    // 64 requests of one token, tables of 64 pages, none leaves 2.7 / 4.1, one 3.9 / 4.9, all 14.7 / 5.2; of 512 pages 3.0 /
+    // 3.8, 4.4 / 4.9, 88 / 5.9; of 2048 2.3 / 3.6, 8.4 / 5.4, 340 / 8.5: how many leave only the device knows.
+    if (a.B <= 128 && a.N <= 1536 && (!a.done || (long long)a.B * a.table_pages <= 4096)) return plan_threads<128>(a, 1, stream, status);
     // clusters of 16 blocks: asked for once per device
     static int known[64] = {0};  // 0 unknown, else the cluster
     int dev = 0;

@@ -107,6 +107,21 @@ def test_bad_books_and_lengths_are_cut_off_and_reported(bsf8_lib):
     assert bsf8.device_status() == INDEX
 
 
+@pytest.mark.parametrize("B,pages", [(64, 64), (64, 65), (128, 32), (128, 33), (1, 4096), (1, 4097), (3, 8191), (64, 2048), (128, 700)])
+@pytest.mark.parametrize("leave", [None, 0.0, 0.3, 1.0])
+def test_long_requests_leave_in_a_call_of_few_tokens(bsf8_lib, B, pages, leave):
+    """Few new tokens, tables on both sides of where the kernel for many pages takes over."""
+    r = np.random.default_rng(B + pages)
+    held = np.maximum(1, pages - r.integers(0, 3, size=B))
+    done = None if leave is None else (r.random(B) < leave).astype(int)
+    lens = held * 16 - r.integers(0, 16, size=B)
+    if done is not None:
+        lens = np.where(done, 0, lens)
+    add = np.minimum(r.integers(0, 9, size=B), pages * 16 - lens)
+    w = check(books(r, B, pages, int(held.sum()) + 2 * B, held), lens, add, done, 16, int(add.sum()) + 1)
+    assert (w["granted"] == add).all()
+
+
 @pytest.mark.parametrize("N", [(1 << 30) - 2, (1 << 30) - 1, 1 << 30])
 @pytest.mark.parametrize("B,large", [(4, (0, 1)), (7, (0, 1, 2)), (40, (0, 5, 35)), (200, (3, 7, 40, 190)), (200, (0, 1, 2, 3, 4))])
 def test_requests_past_the_largest_budget_leave_nothing_behind_them(bsf8_lib, N, B, large):
