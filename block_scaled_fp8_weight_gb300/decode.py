@@ -151,7 +151,8 @@ def kv_commit(cache: KVCache, table, ctx, path, count):
 class PageBook:
     """Which pages each request holds, and which are free: table int32 [B, table_pages], held int32 [B] (a row's
     first held entries are its pages), free int32 [pages] (a stack) and count int32 [1] (how many lie on
-    it), contiguous CUDA tensors that kv_plan keeps (PageBook.empty allocates them)."""
+    it), contiguous CUDA tensors that kv_plan keeps (PageBook.empty allocates them).  A page is one row's alone or lies on
+    the stack once: rows that share pages are not for kv_plan, which would hand them out again when the first one leaves."""
 
     __slots__ = ("table", "held", "free", "count")
 

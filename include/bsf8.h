@@ -448,6 +448,9 @@ int bsf8_kv_commit(const bsf8_kv_cache *cache, const int32_t *table, int table_p
  *   held        int32 [B]
  *   free_pages  int32 [pool]: a stack of free pages, the first *free_count of them
  *   free_count  int32 [1]
+ * A page is one row's alone, or lies on the stack once: a row that leaves gives all of its pages back, so that one which
+ * another row holds too would be handed out while it is read, and twice (nothing here looks for that).  Requests that share
+ * pages need tables and counts of users of the caller's own; the calls that read a table take such rows.
  * In this order, the requests from the first to the last each time:
  *   - where done[b] is not 0 (done NULL: nowhere) the row's pages go back onto the stack, entry by entry, and
  *     held[b] becomes 0;
