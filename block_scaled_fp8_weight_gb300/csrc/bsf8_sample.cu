@@ -72,8 +72,9 @@ struct TokenShared {
     };
 };
 
-// 2^-f on [0, 1): a polynomial fitted to it (least squares, weighted towards the largest relative error,
-// 2^-22), every step rounded by itself so that any machine gets the same bits.  It stays in [1/2, 1].
+// 2^-f on [0, 1): a polynomial fitted to it (least squares, weighted towards the largest relative error, 2^-21.92 with its
+// roundings over all multiples of 2^-24), every step rounded by itself so that any machine gets the same bits.  It stays
+// in [1/2, 1].
 __device__ __forceinline__ float exp2_of(float f) {
     float p = -0.0009449035860598087f;
     p = __fadd_rn(__fmul_rn(p, f), 0.00920579768717289f);

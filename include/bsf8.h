@@ -541,7 +541,7 @@ int bsf8_sparse_attention(const void *q, int64_t ldq, const bsf8_kv_cache *cache
 
 /* A token from each row of logits.  With m the row's largest logit and t its temperature, a logit x weighs
  *   w = 2^40 for x = m, else floor(2^40 * 2^-y) for y = (m - x) * (log2(e) / t) <= 40, 0 beyond
- * (fp32 steps, each rounded; 2^-y by a polynomial to 2^-22 of itself; -inf and NaN weigh 0).  t below 2^-126 or
+ * (fp32 steps, each rounded; 2^-y by a polynomial to 2^-21.9 of itself; -inf and NaN weigh 0).  t below 2^-126 or
  * NaN counts as 0: only the lowest index of x = m weighs.  Of these stay, in this order,
  *   top_k   the first k by (larger x, then lower index);  k <= 0 or >= V: all
  *   min_p   those with w >= ceil(min_p * 2^40);  NaN counts as 0, above 1 as 1
