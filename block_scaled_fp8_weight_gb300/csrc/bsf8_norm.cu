@@ -110,7 +110,7 @@ __device__ __forceinline__ float far_first(float v) {
 // thread, its loads straight to registers (P = 1).  Many: four pieces a thread, which go to shared memory by the
 // thread's own asynchronous copies (nothing is handed from thread to thread there) and wait there for the row's first
 // sum; with few threads a row six blocks and more share an SM, so that the loads, sums and stores of one run under
-// those of the others.
+// those of the others.  (Four pieces at 64 registers spill 4 or 12 bytes a thread.)
 template <int P, bool F32>
 __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a, int warps) {
     constexpr int WORDS = F32 ? 3 : 2;  // of 16 bytes a piece: x, the residual
@@ -493,10 +493,14 @@ cudaError_t norm_typed(const NormArgs &a, cudaStream_t stream) {
     // One piece a thread while the SMs hold all rows in a turn or two, and for an fp32 residual without a first norm where
     // rows are short.  Else the rows' kernel if more than two bytes a channel come beside x (its copies make whole sectors
     // of them), four pieces a thread if not.  One piece / four / the rows' kernel, us (gate: a post norm and an fp32
-    // residual too): 304 rows of 5120 bf16 3.0 / 3.7 / 4.0, gate 4.5 / 6.9 / 6.0; 500 of 4096 bf16 4.2 / 5.3 / 4.4, gate
-    // 6.8 / 11 / 6.4; 304 of 7168 bf16 4.5 / 4.0 / 3.9; 8191 of 5120 bf16 65 / 50 / 54, with a full gate 96 / 78 / 69, gate
-    // 97 / 110 / 85, fp32 without a first norm 78 / 95 / 86; of 7168 bf16 122 / 69 / 82, fp32 135 / 130 / 117; six rows of
-    // 12288, gate - / 7.1 / 6.1.
+    // residual too): 304 rows of 5120 bf16 3.3 / 3.9 / 4.8, gate 4.8 / 7.4 / 6.9; 500 of 4096 bf16 4.6 / 5.6 / 5.2, gate
+    // 7.2 / 11.7 / 7.4; 304 of 7168 bf16 4.7 / 4.3 / 4.6; 8191 of 5120 bf16 66 / 51 / 57, with a full gate 89 / 76 / 69, gate
+    // 100 / 120 / 85, fp32 without a first norm 80 / 98 / 88; of 5632 (one piece a thread takes more than 20 warps a row, and
+    // an SM holds fewer rows) bf16 111 / 55 / 65, full gate 144 / 87 / 74, gate 165 / 129 / 97, fp32 121 / 108 / 90; of 6144,
+    // 6656 and 7168 the same order (7168: bf16 124 / 70 / 83, fp32 138 / 135 / 119).  From 300 to 1000 rows it is within 5 %
+    // of the best at most of these sizes, but 304 rows of 5632 and 6144 are 15 % faster by one piece (5.0 for 4.3), and 500
+    // rows with a full gate from 5632 on, 1000 at 4096, 10 to 25 % by four pieces (8.1 for 6.1).  Six rows of 12288, gate
+    // - / 7.1 / 6.1.
     const bool full = a.gate_kind == kGateFull;
     const long long few = 152LL * (F32 || full || a.H > 5120 ? 10240 : 16384);  // channels
     if (a.H <= 8192 && (a.M * (long long)a.H <= few || (F32 && !a.post && !full && a.H <= 5120))) return norm_pieces<1, F32>(a, stream);

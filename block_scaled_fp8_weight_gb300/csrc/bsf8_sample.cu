@@ -36,7 +36,8 @@ constexpr int kOctaves = 41, kParts = 64;  // the histogram by y: y <= 40 in 64t
 constexpr int kSteps = kOctaves * kParts;
 constexpr int kList = 2048;      // elements that the first block takes up,
 constexpr int kOwn = 704;        // and that a block of a cluster finds
-// Blocks an SM: their latencies hide each other (192 rows of 131072 bf16, k = 50: 30 us, 53 by two of 512 threads).
+// Blocks an SM: their latencies hide each other (192 rows of 131072 bf16, k = 50: 30 us, 53 by two of 512 threads).  At the
+// 64 registers that leaves, each of the four kernels spills 12 to 68 bytes a thread, the functions out of line 32 to 56.
 constexpr int kTBlocks = 4;
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr int kMaxShared = 228 * 1024;  // an SM's, of which each block takes 1 KB more than it asks for
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     constexpr int kMax8 = kTThreads / 8;
     const int g8 = kMax8 * cluster, gt = kTThreads * cluster * subs;  // maxima of eight threads, of (a part of) one
     // with k of so many maxima to reach, some -real ln(1 - k / real) elements do; where that is far above k and the block has
-    // the whole row, all elements take the maxima's place (18 rows of 4435, k = 1000 and top-p: 46 us by the digits below, 19)
+    // the whole row, all elements take the maxima's place (18 rows of 4435, k = 1000 and top-p: 41 us by the digits below, 21)
     const int real = min(gt, groups);
     const bool one = cluster == 1 && 2 * k > real;
     const int most_k = one ? kList - 96 : (int)((float)real * fminf(0.95f, 1.0f - expf(-1800.0f / (float)real)));
@@ -825,8 +826,9 @@ __global__ void __launch_bounds__(kTThreads, kTBlocks) sample_kernel(const Sampl
     // ---------------------------------------------------------------- top-p by a histogram of y
     // Weights of 11 bits in each 64th of an octave tell to a thousandth (of the smaller side) where they reach the
     // share.  Of the elements there the one is looked for, everything else is added up exactly, and if the cut is not among
-    // them after all the digits below find it.  (192 rows of 131072 bf16, p = 0.9: 91 us in two turns; of a row's 53 in
-    // its turn the largest takes 6, the histogram 10, its edges 4.5, the exact weights 17, the cut 8, the draw 6.)
+    // them after all the digits below find it.  (p = 0.9, rows of 131072 bf16: 38 rows 34 us, 76 55, 114 68, 152 87, 192 93:
+    // blocks that share an SM slow each other.  Of the 53 us of a row among as many as run at once the largest takes 6, the
+    // histogram 10, its edges 4.5, the exact weights 17, the cut 8, the draw 6.)
     if (nucleus && k == V && top < INFINITY) {
         for (int i = tid; i < kSteps; i += kTThreads) s.steps[i] = 0;
         __syncthreads();
@@ -1444,7 +1446,7 @@ cudaError_t sample_typed(const SampleArgs &a, cudaStream_t stream) {
     cfg.numAttrs = na;
     // No more blocks an SM than the call needs to run at once (the first are placed while the kernel before still holds
     // some of the SMs: four on one and one on the next took twice as long): all that these leave free is asked for,
-    // and slices are kept that fit in it (one row of 131072 fp32 10.8 -> 9.5 us, by top-p 25 -> 23).
+    // and slices are kept that fit in it (one row of 131072 fp32 10.8 -> 9.5 us).
     auto room = [](int blocks) { return (size_t)(kMaxShared / blocks / 128 * 128 - 1024); };
     int blocks = 1;
     for (; blocks < kTBlocks; ++blocks) {

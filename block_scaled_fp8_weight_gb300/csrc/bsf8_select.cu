@@ -2,7 +2,7 @@
 // a query's products with those bounds put first.
 //
 // A page's bounds are its keys' largest and smallest value in each channel, as 8-bit integers under a
-// power of two per 32 channels, so that for any query q
+// power of two per 32 channels (scoring a page by such bounds is a published idea), so that for any query q
 //     q . k  <=  sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d     for every key k of the page.
 // The score is that sum over all rows that share the cache head (heads of the group, nodes of the
 // tree): with the rows' positive and negative parts added up first, one product of 2 dim terms a page
